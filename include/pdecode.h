@@ -87,6 +87,7 @@ typedef enum {
 #define PD_DEVERR_TIMEOUT 4u  /* a pipeline wait ran past its limit; the call gave up */
 #define PD_DEVERR_SLOT 8u     /* write_kv_cache: a slot at or beyond num_blocks*block_size */
 #define PD_DEVERR_QUERY_START 16u /* decode_paged_varlen: a sequence's query range is malformed */
+#define PD_DEVERR_FREE_LIST 32u /* the free list has too few blocks, would overflow, or its count is bad */
 
 /* Shapes of one call.
  *   B                  number of sequences (rows of block_table / seq_lens)
@@ -214,6 +215,131 @@ PD_API pd_status decode_paged_combine(const float* part_m, const float* part_l, 
 PD_API pd_status write_kv_cache(const void* k_new, const void* v_new, const int64_t* slot_mapping,
                                 int num_tokens, void* k_cache, void* v_cache, const pd_dims* dims,
                                 uint32_t* error_flag, void* stream);
+
+/* Differential decode over the paged caches: decode_paged with two softmax
+ * maps per head and their difference weighted by a learned factor. The head
+ * size D of dims (128 or 256) is that of the cache rows and of V; each q row
+ * and each K row is two halves of D / 2, one per map:
+ *   out[h] = softmax(scale * q[h][:D/2] . K[:][:D/2]) V
+ *          - lambda[h] * softmax(scale * q[h][D/2:] . K[:][D/2:]) V
+ * over the keys that decode_paged's masks leave (causal, window), followed,
+ * where norm_weight is given, by the head's own root-mean-square norm:
+ *   out[h] = out[h] * rsqrt(mean(out[h]^2) + norm_eps) * norm_weight * norm_gain.
+ * The caches, their writer (write_kv_cache), block_table, seq_lens, the
+ * splits, the workspace rules and the errors are decode_paged's. Both maps of
+ * a head are computed from one reading of its K and V.
+ *   lambda          device fp32 [Hq]
+ *   query_start_loc NULL: qlen query tokens for each sequence (num_query_tokens
+ *                   is then ignored); else int32 [B+1] as in
+ *                   decode_paged_varlen, and qlen is the bound of every count
+ *   norm_weight     [D] of q's type (norm_weight_f32 = 0) or fp32 (1), or NULL
+ *   norm_eps        >= 0; norm_gain multiplies the result (ignored without a
+ *                   norm_weight)
+ *   workspace       pd_diff_workspace_bytes(dims, qlen, num_splits, 0) bytes
+ * Rows without a visible key are zeros. Hq/Hkv*qlen must be <= 32. */
+PD_API size_t pd_diff_workspace_bytes(const pd_dims* dims, int qlen, int num_splits, int sm_count);
+PD_API pd_status decode_paged_diff(const void* q, const void* k_cache, const void* v_cache,
+                                   const int32_t* block_table, const int32_t* seq_lens,
+                                   const int32_t* query_start_loc, int num_query_tokens,
+                                   const float* lambda, float scale, int window, int qlen,
+                                   int num_splits, const void* norm_weight, int norm_weight_f32,
+                                   float norm_eps, float norm_gain, void* out, const pd_dims* dims,
+                                   void* workspace, size_t workspace_bytes, uint32_t* error_flag,
+                                   void* stream);
+
+/* Block tables and slot maps of one serving step, built on the GPU from the
+ * requests' lengths, for write_kv_cache and decode_paged_varlen. Sequence b
+ * has context_lens[b] keys in the cache and brings query_lens[b] new tokens;
+ * it holds the first ceil(context_lens[b] / block_size) entries of its
+ * block_table row and is given what it lacks from the top of the free list.
+ *   context_lens    int32 [B]
+ *   query_lens      int32 [B]; 0 for a sequence that rests (or a padding row)
+ *   num_tokens      entries of slot_mapping and positions: at least the sum of
+ *                   query_lens, more for a padded batch
+ *   block_table     int32 [B, max_blocks_per_seq], new entries written
+ *   free_blocks     int32 [num_blocks], of which the first free_count[0] are
+ *                   the free blocks' ids; the last of them is taken first,
+ *                   sequences in order
+ *   free_count      int32 [1]; free_count_out [1] gets what is left (may be
+ *                   free_count itself)
+ *   seq_lens        int32 [B]: context + query (may be context_lens itself)
+ *   query_start_loc int32 [B+1]: exclusive prefix sums of query_lens
+ *   slot_mapping    int64 [num_tokens]: the tokens' slots, -1 behind the last
+ *   positions       int32 [num_tokens] or NULL: the tokens' positions in their
+ *                   sequences, 0 behind the last
+ *   dims            B (at most 16384), block_size, num_blocks and
+ *                   max_blocks_per_seq are read
+ * A sequence is served whole or not at all: one with a bad length
+ * (PD_DEVERR_SEQ_LEN), whose tokens pass num_tokens (PD_DEVERR_QUERY_START) or
+ * for which the free list has too few blocks (PD_DEVERR_FREE_LIST; every later
+ * sequence that needs a block is refused too) takes no block, its seq_lens
+ * entry is 0 and its slots are -1. An id outside [0, num_blocks) among those
+ * used sets PD_DEVERR_BLOCK_ID and gives slot -1. One launch on `stream`. */
+PD_API pd_status build_block_tables(const int32_t* context_lens, const int32_t* query_lens,
+                                    int num_tokens, int32_t* block_table,
+                                    const int32_t* free_blocks, const int32_t* free_count,
+                                    int32_t* free_count_out, int32_t* seq_lens,
+                                    int32_t* query_start_loc, int64_t* slot_mapping,
+                                    int32_t* positions, const pd_dims* dims,
+                                    uint32_t* error_flag, void* stream);
+
+/* Returns the blocks of finished sequences to the free list: for every b with
+ * released[b] != 0 (one byte each), in order, the first
+ * ceil(seq_lens[b] / block_size) entries of its block_table row are appended.
+ *   free_count      int32 [1]; free_count_out [1] gets the new count (may be
+ *                   free_count itself)
+ *   seq_lens_out    int32 [B]: seq_lens, 0 for a released sequence (may be
+ *                   seq_lens itself)
+ * The table's entries stay. A marked sequence with a bad length
+ * (PD_DEVERR_SEQ_LEN), or whose blocks would make the list longer than
+ * num_blocks (PD_DEVERR_FREE_LIST), is not released. An entry outside
+ * [0, num_blocks) sets PD_DEVERR_BLOCK_ID and is appended as -1. One launch on
+ * `stream`. */
+PD_API pd_status release_blocks(const int32_t* block_table, const int32_t* seq_lens,
+                                const uint8_t* released, int32_t* free_blocks,
+                                const int32_t* free_count, int32_t* free_count_out,
+                                int32_t* seq_lens_out, const pd_dims* dims,
+                                uint32_t* error_flag, void* stream);
+
+typedef enum {
+  PD_NORM_SAME = 0, /* x's type */
+  PD_NORM_E4M3 = 1, /* OCP e4m3fn codes; value = decode(code) * scale */
+  PD_NORM_INT8 = 2  /* int8 codes in [-127, 127]; value = code * scale */
+} pd_norm_out;
+
+/* Shapes of one rms_norm call.
+ *   rows, N     x is [rows, N]; N is at most 32768
+ *   norm_size   values normalised together, a divisor of N (N: the whole row;
+ *               D: every head of a decode's output on its own)
+ *   scale_size  8-bit outputs: values that share a scale, a divisor of N
+ *   x_bf16      x, residual (and out, for PD_NORM_SAME) are bfloat16, else fp16
+ *   weight_f32  weight is fp32, else of x's type
+ *   out_kind    pd_norm_out */
+typedef struct {
+  int64_t rows;
+  int32_t N, norm_size, scale_size;
+  int32_t x_bf16, weight_f32, out_kind;
+} pd_norm_dims;
+
+/* Root-mean-square norm of rows with the residual's addition and an 8-bit
+ * output: in fp32, h = x + residual; y = h * rsqrt(mean(h^2) + eps) * weight *
+ * gain, the mean over each norm_size values.
+ *   x            [rows, N]
+ *   residual     [rows, N] of x's type, or NULL (h = x)
+ *   weight       [norm_size]
+ *   residual_out [rows, N] of x's type or NULL: gets h rounded (may be
+ *                residual or x)
+ *   out          [rows, N]: y in x's type (may be x or, without a
+ *                residual_out, residual), or one byte codes of y / s rounded
+ *                to the nearest, ties to even, NaN as write_kv_cache's
+ *   out_scale    8-bit outputs: fp32 [rows, N / scale_size], s = max(max |y| / Q,
+ *                2^-100), Q = 448 (e4m3fn) or 127 (int8), NaN left out of the
+ *                maximum
+ * Otherwise no output may overlap an input or another output. One launch on
+ * `stream`. */
+PD_API pd_status rms_norm(const void* x, const void* residual, const void* weight, float eps,
+                          float gain, void* residual_out, void* out, float* out_scale,
+                          const pd_norm_dims* dims, void* stream);
 
 /* Failure-detection controls (process-wide, read at each launch; for tests of
  * the error path, not for production use).

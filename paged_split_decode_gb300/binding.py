@@ -7,6 +7,7 @@ there is no CPU or PyTorch fallback, and a missing library is an error.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -29,9 +30,11 @@ DEVERR_SEQ_LEN = 2
 DEVERR_TIMEOUT = 4
 DEVERR_SLOT = 8
 DEVERR_QUERY_START = 16
+DEVERR_FREE_LIST = 32
 
 EXPORTS = ("decode_paged", "decode_paged_varlen", "decode_paged_combine", "decode_paged_static_scratch",
-           "write_kv_cache", "pd_workspace_bytes", "pd_grid_ctas", "pd_status_str", "pd_set_wait_limit_ns",
+           "write_kv_cache", "decode_paged_diff", "build_block_tables", "release_blocks", "rms_norm",
+           "pd_workspace_bytes", "pd_diff_workspace_bytes", "pd_grid_ctas", "pd_status_str", "pd_set_wait_limit_ns",
            "pd_set_fault_injection")
 
 
@@ -41,6 +44,12 @@ class PdDims(ctypes.Structure):
                 ("num_blocks", ctypes.c_int32), ("max_blocks_per_seq", ctypes.c_int32),
                 ("kv_dtype", ctypes.c_int32), ("k_scale", ctypes.c_float),
                 ("v_scale", ctypes.c_float)]
+
+
+class PdNormDims(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("N", ctypes.c_int32), ("norm_size", ctypes.c_int32),
+                ("scale_size", ctypes.c_int32), ("x_bf16", ctypes.c_int32),
+                ("weight_f32", ctypes.c_int32), ("out_kind", ctypes.c_int32)]
 
 
 class DecodeError(RuntimeError):
@@ -82,6 +91,16 @@ def load():
             lib.decode_paged_combine.restype = ctypes.c_int
             lib.write_kv_cache.argtypes = [P, P, P, ctypes.c_int, P, P, ctypes.POINTER(PdDims), P, P]
             lib.write_kv_cache.restype = ctypes.c_int
+            dims_p, i, f = ctypes.POINTER(PdDims), ctypes.c_int, ctypes.c_float
+            lib.pd_diff_workspace_bytes.argtypes = [dims_p, i, i, i]
+            lib.pd_diff_workspace_bytes.restype = ctypes.c_size_t
+            lib.decode_paged_diff.argtypes = [P, P, P, P, P, P, i, P, f, i, i, i, P, i, f, f, P, dims_p, P,
+                                              ctypes.c_size_t, P, P]
+            lib.build_block_tables.argtypes = [P, P, i, P, P, P, P, P, P, P, P, dims_p, P, P]
+            lib.release_blocks.argtypes = [P, P, P, P, P, P, P, dims_p, P, P]
+            lib.rms_norm.argtypes = [P, P, P, f, f, P, P, P, ctypes.POINTER(PdNormDims), P]
+            for fn in (lib.decode_paged_diff, lib.build_block_tables, lib.release_blocks, lib.rms_norm):
+                fn.restype = i
             lib.pd_set_wait_limit_ns.argtypes = [ctypes.c_ulonglong]
             lib.pd_set_wait_limit_ns.restype = None
             lib.pd_set_fault_injection.argtypes = [ctypes.c_int]
@@ -168,6 +187,12 @@ def workspace_bytes(dims: PdDims, qlen: int, num_splits: int, sm_count: int = 0)
 
 def grid_ctas(dims: PdDims, qlen: int, num_splits: int, sm_count: int = 0) -> int:
     return int(load().pd_grid_ctas(ctypes.byref(dims), int(qlen), int(num_splits), int(sm_count)))
+
+
+def diff_workspace_bytes(dims: PdDims, qlen: int, num_splits: int, sm_count: int = 0) -> int:
+    """Workspace of decode_paged_diff (two maps' partials)."""
+    return int(load().pd_diff_workspace_bytes(ctypes.byref(dims), int(qlen), int(num_splits),
+                                              int(sm_count)))
 
 
 _workspaces: dict = {}
@@ -332,3 +357,260 @@ def write_kv_cache(k_new, v_new, slot_mapping, k_cache, v_cache, *, k_scale=1.0,
                             _dev_ptr(k_cache, "k_cache", kv_dt), _dev_ptr(v_cache, "v_cache", kv_dt),
                             ctypes.byref(dims), flag_ptr, stream)
     _check(rc, "write_kv_cache")
+
+
+# ---- differential decode, block tables, root-mean-square norm ----------------
+_FLAG_TYPES = (torch.int32, torch.uint32)
+_CODE_KINDS = {torch.float8_e4m3fn: 1, torch.int8: 2}
+
+
+def _same_device(dev: torch.device, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, expected {dev}")
+
+
+def _opt_ptr(t, name, dtype):
+    return None if t is None else _dev_ptr(t, name, dtype)
+
+
+def _launch(dev: torch.device, stream, call):
+    """Run ``call(stream handle)`` with ``dev`` current."""
+    if torch.cuda.current_device() == dev.index:
+        return call(torch.cuda.current_stream(dev).cuda_stream if stream is None else int(stream))
+    with torch.cuda.device(dev):
+        return call(torch.cuda.current_stream(dev).cuda_stream if stream is None else int(stream))
+
+
+def _on_stream(dev: torch.device, stream):
+    """Allocations under this context are ordered by the stream of the launch."""
+    if stream is None or int(stream) == torch.cuda.current_stream(dev).cuda_stream:
+        return contextlib.nullcontext()
+    return torch.cuda.stream(torch.cuda.ExternalStream(int(stream), device=dev))
+
+
+def decode_paged_diff(q, k_cache, v_cache, block_table, seq_lens, lam, scale, window=0, qlen=1,
+                      num_splits=0, out=None, *, query_start_loc=None, norm_weight=None,
+                      norm_eps=1e-5, norm_gain=1.0, k_scale=1.0, v_scale=1.0, workspace=None,
+                      error_flag=None, stream=None):
+    """Differential paged decode; returns ``out`` (q's type, [T, Hq, D]).
+
+    Each head's q and K rows are two halves of D / 2, one per softmax map:
+    ``softmax(scale q1 K1^T) V - lam[h] softmax(scale q2 K2^T) V``, with
+    ``norm_weight`` ([D], q's type or float32) followed by the head's own
+    root-mean-square norm times ``norm_gain``. ``lam``: float32 [Hq]. Caches,
+    tables, masks and splits as in ``decode_paged``; with ``query_start_loc``
+    (int32 [B+1]) sequence b has its own count of query tokens, at most
+    ``qlen``, as in ``decode_paged_varlen`` (rows outside every range are left
+    as they were; a new ``out`` is zeroed there).
+    """
+    lib = load()
+    kind = kv_kind_of(k_cache, q.dtype)
+    kv_dt, q_dt = _dtypes(kind)
+    B = block_table.shape[0]
+    if v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype:
+        raise ValueError("v_cache must match k_cache in shape and dtype")
+    if q.dim() != 3 or q.shape[2] != k_cache.shape[3] or seq_lens.numel() != B:
+        raise ValueError("q must be [T, Hq, D] with the caches' D; seq_lens [B]")
+    if query_start_loc is None:
+        if q.shape[0] != B * qlen:
+            raise ValueError("q must be [B*qlen, Hq, D] with B = rows of block_table")
+    elif query_start_loc.numel() != B + 1:
+        raise ValueError("query_start_loc must be [B+1]")
+    if lam.numel() != q.shape[1]:
+        raise ValueError("lam must be [Hq]")
+    if norm_weight is not None and norm_weight.numel() != q.shape[2]:
+        raise ValueError("norm_weight must be [D]")
+    if out is not None and out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    dims = dims_of(q, k_cache, block_table, qlen, None, k_scale, v_scale)
+    dev = q.device
+    _same_device(dev, k_cache=k_cache, v_cache=v_cache, block_table=block_table, seq_lens=seq_lens, lam=lam,
+                 out=out, query_start_loc=query_start_loc, norm_weight=norm_weight, workspace=workspace,
+                 error_flag=error_flag)
+
+    def call(s):
+        nonlocal out, workspace
+        with _on_stream(dev, stream):
+            if out is None:
+                out = torch.empty_like(q) if query_start_loc is None else torch.zeros_like(q)
+            if workspace is None:
+                need = diff_workspace_bytes(dims, qlen, num_splits)
+                # a captured call keeps a workspace of its own in the graph's
+                # pool: graphs may be replayed at the same time
+                if need and torch.cuda.is_current_stream_capturing():
+                    workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+                else:
+                    workspace = get_workspace(dev, need, s)
+        return lib.decode_paged_diff(
+            _dev_ptr(q, "q", q_dt), _dev_ptr(k_cache, "k_cache", kv_dt), _dev_ptr(v_cache, "v_cache", kv_dt),
+            _dev_ptr(block_table, "block_table", torch.int32), _dev_ptr(seq_lens, "seq_lens", torch.int32),
+            _opt_ptr(query_start_loc, "query_start_loc", torch.int32), int(q.shape[0]),
+            _dev_ptr(lam, "lam", torch.float32), float(scale), int(window), int(qlen), int(num_splits),
+            _opt_ptr(norm_weight, "norm_weight", (q_dt, torch.float32)),
+            int(norm_weight is not None and norm_weight.dtype == torch.float32), float(norm_eps),
+            float(norm_gain), _dev_ptr(out, "out", q_dt), ctypes.byref(dims),
+            None if workspace is None else _dev_ptr(workspace, "workspace"),
+            0 if workspace is None else workspace.numel() * workspace.element_size(),
+            _opt_ptr(error_flag, "error_flag", _FLAG_TYPES), s)
+
+    _check(_launch(dev, stream, call), "decode_paged_diff")
+    return out
+
+
+def _table_dims(block_table, free_blocks, block_size) -> PdDims:
+    return PdDims(block_table.shape[0], 1, 1, 1, int(block_size), free_blocks.numel(), block_table.shape[1], 0,
+                  1.0, 1.0)
+
+
+def build_block_tables(context_lens, query_lens, block_table, free_blocks, free_count, block_size,
+                       num_tokens=None, *, seq_lens=None, query_start_loc=None, slot_mapping=None,
+                       positions=None, free_count_out=None, error_flag=None, stream=None):
+    """Block tables and slot maps of one serving step, built on the GPU.
+
+    Sequence b has ``context_lens[b]`` keys cached and brings
+    ``query_lens[b]`` tokens (int32 [B]); the blocks it lacks are taken from
+    the top of ``free_blocks[:free_count]`` and written to its ``block_table``
+    row. Returns ``(seq_lens, query_start_loc, slot_mapping, positions)`` for
+    ``write_kv_cache`` and ``decode_paged_varlen``; the maps have
+    ``num_tokens`` entries (or those of the given ``slot_mapping``), -1 / 0
+    behind the last token. ``seq_lens`` may be ``context_lens`` itself;
+    ``free_count`` is updated in place unless ``free_count_out`` is given.
+    """
+    lib = load()
+    if block_table.dim() != 2 or context_lens.numel() != block_table.shape[0] \
+            or query_lens.numel() != block_table.shape[0]:
+        raise ValueError("block_table must be [B, max_blocks]; context_lens and query_lens [B]")
+    B, dev = block_table.shape[0], block_table.device
+    if slot_mapping is None and num_tokens is None:
+        raise ValueError("give num_tokens or a slot_mapping")
+    T = slot_mapping.numel() if num_tokens is None else int(num_tokens)
+    if slot_mapping is not None and slot_mapping.numel() != T:
+        raise ValueError("slot_mapping must be [num_tokens]")
+    if positions is not None and positions.numel() != T:
+        raise ValueError("positions must be [num_tokens]")
+    if free_count.numel() != 1 or (free_count_out is not None and free_count_out.numel() != 1):
+        raise ValueError("free_count must be [1]")
+    if seq_lens is not None and seq_lens.numel() != B:
+        raise ValueError("seq_lens must be [B]")
+    if query_start_loc is not None and query_start_loc.numel() != B + 1:
+        raise ValueError("query_start_loc must be [B+1]")
+    _same_device(dev, context_lens=context_lens, query_lens=query_lens, free_blocks=free_blocks, free_count=free_count,
+                 seq_lens=seq_lens, query_start_loc=query_start_loc, slot_mapping=slot_mapping, positions=positions,
+                 free_count_out=free_count_out, error_flag=error_flag)
+    dims = _table_dims(block_table, free_blocks, block_size)
+    i32 = torch.int32
+
+    def call(s):
+        nonlocal seq_lens, query_start_loc, slot_mapping, positions
+        with _on_stream(dev, stream):
+            if seq_lens is None:
+                seq_lens = torch.empty(B, dtype=i32, device=dev)
+            if query_start_loc is None:
+                query_start_loc = torch.empty(B + 1, dtype=i32, device=dev)
+            if slot_mapping is None:
+                slot_mapping = torch.empty(T, dtype=torch.int64, device=dev)
+            if positions is None:
+                positions = torch.empty(T, dtype=i32, device=dev)
+        return lib.build_block_tables(
+            _dev_ptr(context_lens, "context_lens", i32), _dev_ptr(query_lens, "query_lens", i32), T,
+            _dev_ptr(block_table, "block_table", i32), _dev_ptr(free_blocks, "free_blocks", i32),
+            _dev_ptr(free_count, "free_count", i32),
+            _dev_ptr(free_count if free_count_out is None else free_count_out, "free_count_out", i32),
+            _dev_ptr(seq_lens, "seq_lens", i32), _dev_ptr(query_start_loc, "query_start_loc", i32),
+            _dev_ptr(slot_mapping, "slot_mapping", torch.int64), _dev_ptr(positions, "positions", i32),
+            ctypes.byref(dims), _opt_ptr(error_flag, "error_flag", _FLAG_TYPES), s)
+
+    _check(_launch(dev, stream, call), "build_block_tables")
+    return seq_lens, query_start_loc, slot_mapping, positions
+
+
+def release_blocks(block_table, seq_lens, released, free_blocks, free_count, block_size, *,
+                   seq_lens_out=None, free_count_out=None, error_flag=None, stream=None):
+    """Push the blocks of the sequences marked in ``released`` (bool or uint8
+    [B]) back onto ``free_blocks``, in order, and set their ``seq_lens`` to 0;
+    ``seq_lens`` and ``free_count`` are updated in place unless
+    ``seq_lens_out`` / ``free_count_out`` are given. Returns the lengths."""
+    lib = load()
+    if block_table.dim() != 2 or seq_lens.numel() != block_table.shape[0] or released.numel() != block_table.shape[0]:
+        raise ValueError("block_table must be [B, max_blocks]; seq_lens and released [B]")
+    if free_count.numel() != 1 or (free_count_out is not None and free_count_out.numel() != 1):
+        raise ValueError("free_count must be [1]")
+    if seq_lens_out is None:
+        seq_lens_out = seq_lens
+    elif seq_lens_out.numel() != seq_lens.numel():
+        raise ValueError("seq_lens_out must be [B]")
+    dev = block_table.device
+    _same_device(dev, seq_lens=seq_lens, released=released, free_blocks=free_blocks, free_count=free_count,
+                 seq_lens_out=seq_lens_out, free_count_out=free_count_out, error_flag=error_flag)
+    dims = _table_dims(block_table, free_blocks, block_size)
+    i32 = torch.int32
+    _check(_launch(dev, stream, lambda s: lib.release_blocks(
+        _dev_ptr(block_table, "block_table", i32), _dev_ptr(seq_lens, "seq_lens", i32),
+        _dev_ptr(released, "released", (torch.bool, torch.uint8)), _dev_ptr(free_blocks, "free_blocks", i32),
+        _dev_ptr(free_count, "free_count", i32),
+        _dev_ptr(free_count if free_count_out is None else free_count_out, "free_count_out", i32),
+        _dev_ptr(seq_lens_out, "seq_lens_out", i32), ctypes.byref(dims),
+        _opt_ptr(error_flag, "error_flag", _FLAG_TYPES), s)), "release_blocks")
+    return seq_lens_out
+
+
+def rms_norm(x, weight, eps=1e-5, *, residual=None, residual_out=None, gain=1.0, norm_size=None,
+             out_dtype=None, scale_size=None, out=None, out_scale=None, stream=None):
+    """Root-mean-square norm of ``x`` ([..., N], fp16 or bfloat16) with the
+    residual's addition and an 8-bit output.
+
+    ``h = x + residual``; every ``norm_size`` values (default: all N) are
+    normalised together, times ``weight`` ([norm_size], x's type or float32)
+    and ``gain``. ``residual`` is replaced by h in place unless
+    ``residual_out`` is given. ``out_dtype`` (or ``out``'s) is x's type,
+    float8_e4m3fn or int8; the 8-bit types come with a float32 scale for every
+    ``scale_size`` values (default: N). Returns ``out``, or ``(out,
+    out_scale)`` for the 8-bit types."""
+    lib = load()
+    if x.dtype not in (torch.float16, torch.bfloat16):
+        raise TypeError(f"x has dtype {x.dtype}, expected float16 or bfloat16")
+    if x.dim() < 1 or x.shape[-1] < 1:
+        raise ValueError("x must be [..., N] with N >= 1")
+    N = x.shape[-1]
+    rows = x.numel() // N
+    norm_size = N if norm_size is None else int(norm_size)
+    dt = out_dtype if out_dtype is not None else x.dtype if out is None else out.dtype
+    kind = 0 if dt == x.dtype else _CODE_KINDS.get(dt)
+    if kind is None:
+        raise TypeError(f"unsupported output dtype {dt}")
+    scale_size = N if scale_size is None else int(scale_size)
+    if norm_size < 1 or scale_size < 1 or N % norm_size or N % scale_size:
+        raise ValueError("norm_size and scale_size must divide N")
+    if weight.numel() != norm_size:
+        raise ValueError("weight must be [norm_size]")
+    if residual is not None:
+        if residual.shape != x.shape:
+            raise ValueError("residual must have x's shape")
+        if residual_out is None:
+            residual_out = residual
+    if residual_out is not None and residual_out.shape != x.shape:
+        raise ValueError("residual_out must have x's shape")
+    if out is not None and (out.shape != x.shape or out.dtype != dt):
+        raise ValueError("out must have x's shape and the output dtype")
+    if out_scale is not None and (kind == 0 or out_scale.numel() != rows * (N // scale_size)):
+        raise ValueError("out_scale is [..., N / scale_size], for 8-bit outputs only")
+    dev = x.device
+    _same_device(dev, weight=weight, residual=residual, residual_out=residual_out, out=out, out_scale=out_scale)
+    dims = PdNormDims(rows, N, norm_size, scale_size, int(x.dtype == torch.bfloat16),
+                      int(weight.dtype == torch.float32), kind)
+
+    def call(s):
+        nonlocal out, out_scale
+        with _on_stream(dev, stream):
+            if out is None:
+                out = torch.empty(x.shape, dtype=dt, device=dev)
+            if kind and out_scale is None:
+                out_scale = torch.empty(x.shape[:-1] + (N // scale_size,), dtype=torch.float32, device=dev)
+        return lib.rms_norm(_dev_ptr(x, "x"), _opt_ptr(residual, "residual", x.dtype),
+                            _dev_ptr(weight, "weight", (x.dtype, torch.float32)), float(eps), float(gain),
+                            _opt_ptr(residual_out, "residual_out", x.dtype), _dev_ptr(out, "out", dt),
+                            _opt_ptr(out_scale, "out_scale", torch.float32), ctypes.byref(dims), s)
+
+    _check(_launch(dev, stream, call), "rms_norm")
+    return (out, out_scale) if kind else out

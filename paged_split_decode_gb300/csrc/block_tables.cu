@@ -1,0 +1,363 @@
+// block_tables.cu -- block tables, slot maps and the free list, built on the
+// GPU from the requests' lengths (build_block_tables, release_blocks): what a
+// serving step needs before write_kv_cache and decode_paged_varlen, without a
+// copy to the host.
+//
+// Mathematics, with bs keys per block (sequence b holds held_b blocks before
+// the step and wants want_b after it):
+//   held_b = ceil(context_b / bs), want_b = ceil((context_b + query_b) / bs),
+//   start_b = sum_{a<b} query_a, off_b = sum_{a<b} (want_a - held_a);
+//   block_table[b][held_b + i] = free[count - 1 - (off_b + i)]  (a stack: the
+//   k-th block taken is the k-th from the top), count -= sum (want - held);
+//   token t of sequence b (start_b <= t < start_b + query_b) has position
+//   p = context_b + t - start_b and slot block_table[b][p / bs] * bs + p % bs.
+// A release pushes the blocks of the marked sequences in sequence order.
+//
+// Latency-bound: a few bytes per sequence and 12 per token. One launch of one
+// thread-block cluster: every CTA reads all lengths and scans them (each
+// thread a run of consecutive sequences, then one block scan), which costs
+// less than a second launch; the cluster barrier then makes the in-place
+// forms safe (seq_lens over context_lens, the count over itself), since no
+// CTA writes before all have read. Tokens and new blocks are dealt to all
+// threads of the cluster, each finding its sequence by a binary search in the
+// prefix held in shared memory.
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "launch.h"
+#include "pdecode.h"
+
+namespace pd {
+namespace {
+
+constexpr int kTabThreads = 1024;
+constexpr int kTabWarps = kTabThreads / 32;
+constexpr int kMaxTableB = 16384;  // three ints per sequence in shared memory
+constexpr uint32_t kSatMax = 0x7fffffffu;
+
+// Saturating sums of non-negative 31-bit values: associative, so a scan of
+// them is well defined however the lengths overflow.
+__device__ __forceinline__ uint32_t sat_add(uint32_t a, uint32_t b) { return min(a + b, kSatMax); }
+
+// Exclusive scan over the block of one value per thread; `total` gets the sum.
+__device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t (&s_warp)[kTabWarps], uint32_t& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint32_t x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x = sat_add(x, y);
+  }
+  const uint32_t prev = __shfl_up_sync(0xffffffffu, x, 1);
+  if (lane == 31) s_warp[warp] = x;
+  __syncthreads();
+  if (warp == 0) {
+    uint32_t w = s_warp[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t y = __shfl_up_sync(0xffffffffu, w, o);
+      if (lane >= o) w = sat_add(w, y);
+    }
+    s_warp[lane] = w;
+  }
+  __syncthreads();
+  total = s_warp[kTabWarps - 1];
+  const uint32_t base = warp > 0 ? s_warp[warp - 1] : 0u;
+  const uint32_t r = sat_add(base, lane > 0 ? prev : 0u);
+  __syncthreads();  // s_warp free again
+  return r;
+}
+
+// The sequence whose range holds x: the largest b with pre[b] <= x, given
+// pre[0] = 0 <= x < pre[n] (empty ranges before it are passed over).
+__device__ __forceinline__ int find_seq(const int* pre, int n, int x) {
+  int lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (pre[mid] <= x) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void raise_bits(uint32_t* flag, uint32_t bits) {
+  if (flag && bits) atomicOr(flag, bits);
+}
+
+struct TableArgs {
+  const int32_t *context, *query;
+  int32_t* table;
+  const int32_t* free_blocks;
+  const int32_t* count_in;
+  int32_t* count_out;
+  int32_t *seq_lens, *q_start;
+  int64_t* slots;
+  int32_t* positions;
+  uint32_t* flag;
+  int B, T, bs, num_blocks, max_blocks;
+};
+
+// Shared: s_start[B + 1], s_off[B + 1], s_ctx[B] (-1: the sequence is refused).
+__global__ void __launch_bounds__(kTabThreads, 1) build_tables_kernel(const TableArgs a) {
+  extern __shared__ int s_dyn[];
+  int* s_start = s_dyn;
+  int* s_off = s_start + a.B + 1;
+  int* s_ctx = s_off + a.B + 1;
+  __shared__ uint32_t s_warp[kTabWarps];
+  __shared__ int s_taken;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int t = threadIdx.x, rank = blockIdx.x, ranks = gridDim.x;
+  const long long cap = static_cast<long long>(a.max_blocks) * a.bs;
+  const int per = (a.B + kTabThreads - 1) / kTabThreads;
+  const int b0 = min(a.B, t * per), b1 = min(a.B, b0 + per);
+  uint32_t bits = 0;
+  int count = *a.count_in;
+  if (count < 0 || count > a.num_blocks) {
+    bits |= PD_DEVERR_FREE_LIST;
+    count = count < 0 ? 0 : a.num_blocks;
+  }
+  if (t == 0) s_taken = 0;
+  // lengths -> start and off
+  uint32_t qs = 0, ns = 0;
+  for (int b = b0; b < b1; ++b) {
+    const int c = a.context[b], q = a.query[b];
+    const bool ok = c >= 0 && q >= 0 && static_cast<long long>(c) + q <= cap;
+    if (!ok) bits |= PD_DEVERR_SEQ_LEN;
+    const int need = ok ? (c + q + a.bs - 1) / a.bs - (c + a.bs - 1) / a.bs : 0;
+    s_ctx[b] = ok ? c : -1;
+    s_start[b] = q > 0 ? q : 0;
+    s_off[b] = need;
+    qs = sat_add(qs, q > 0 ? q : 0);
+    ns = sat_add(ns, need);
+  }
+  uint32_t q_total, n_total;
+  uint32_t q_run = block_scan(qs, s_warp, q_total);
+  uint32_t n_run = block_scan(ns, s_warp, n_total);
+  int taken = 0;
+  for (int b = b0; b < b1; ++b) {
+    const uint32_t q = s_start[b], need = s_off[b];
+    s_start[b] = static_cast<int>(q_run);
+    s_off[b] = static_cast<int>(n_run);
+    const uint32_t qe = sat_add(q_run, q), ne = sat_add(n_run, need);
+    // a sequence is served whole or not at all; those that need blocks fail
+    // from the first that does not fit, so the blocks taken are the list's top
+    if (q > 0 && qe > static_cast<uint32_t>(a.T)) {
+      bits |= PD_DEVERR_QUERY_START;
+      s_ctx[b] = -1;
+    }
+    if (need > 0 && ne > static_cast<uint32_t>(count)) {
+      bits |= PD_DEVERR_FREE_LIST;
+      s_ctx[b] = -1;
+    }
+    if (need > 0 && s_ctx[b] >= 0) taken = static_cast<int>(ne);
+    q_run = qe;
+    n_run = ne;
+  }
+  if (t == 0) {
+    s_start[a.B] = static_cast<int>(q_total);
+    s_off[a.B] = static_cast<int>(n_total);
+  }
+  if (taken) atomicMax(&s_taken, taken);
+  cluster_sync();  // (and a block barrier) every CTA has read its inputs
+  taken = s_taken;
+
+  const int nt = ranks * kTabThreads, me = rank * kTabThreads + t;
+  for (int b = me; b <= a.B; b += nt) {
+    a.q_start[b] = s_start[b];
+    if (b < a.B) {
+      const int c = s_ctx[b];
+      // query_b = start_{b+1} - start_b (exact while the sums do not saturate,
+      // and a sequence behind a saturated sum is refused)
+      a.seq_lens[b] = c >= 0 ? c + (s_start[b + 1] - s_start[b]) : 0;
+    }
+  }
+  if (me == 0) *a.count_out = count - taken;
+  for (int k = me; k < taken; k += nt) {
+    const int b = find_seq(s_off, a.B, k);
+    const int blk = a.free_blocks[count - 1 - k];
+    if (blk < 0 || blk >= a.num_blocks) bits |= PD_DEVERR_BLOCK_ID;
+    const int held = (s_ctx[b] + a.bs - 1) / a.bs;
+    a.table[static_cast<long long>(b) * a.max_blocks + held + (k - s_off[b])] = blk;
+  }
+  const int live = min(s_start[a.B], a.T);
+  for (int k = me; k < a.T; k += nt) {
+    long long slot = -1;
+    int pos = 0;
+    if (k < live) {
+      const int b = find_seq(s_start, a.B, k);
+      const int c = s_ctx[b];
+      if (c >= 0) {
+        pos = c + (k - s_start[b]);
+        const int n = pos / a.bs, held = (c + a.bs - 1) / a.bs;
+        const int blk = n < held ? a.table[static_cast<long long>(b) * a.max_blocks + n]
+                                 : a.free_blocks[count - 1 - (s_off[b] + n - held)];
+        if (blk < 0 || blk >= a.num_blocks) bits |= PD_DEVERR_BLOCK_ID;
+        else slot = static_cast<long long>(blk) * a.bs + (pos - n * a.bs);
+      }
+    }
+    a.slots[k] = slot;
+    if (a.positions) a.positions[k] = pos;
+  }
+  raise_bits(a.flag, bits);
+}
+
+struct ReleaseArgs {
+  const int32_t* table;
+  const int32_t* lens;
+  const uint8_t* released;
+  int32_t* free_blocks;
+  const int32_t* count_in;
+  int32_t* count_out;
+  int32_t* lens_out;
+  uint32_t* flag;
+  int B, bs, num_blocks, max_blocks;
+};
+
+// Shared: s_off[B + 1], s_len[B] (the length to write).
+__global__ void __launch_bounds__(kTabThreads, 1) release_kernel(const ReleaseArgs a) {
+  extern __shared__ int s_dyn[];
+  int* s_off = s_dyn;
+  int* s_len = s_off + a.B + 1;
+  __shared__ uint32_t s_warp[kTabWarps];
+  __shared__ int s_given;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int t = threadIdx.x, rank = blockIdx.x, ranks = gridDim.x;
+  const long long cap = static_cast<long long>(a.max_blocks) * a.bs;
+  const int per = (a.B + kTabThreads - 1) / kTabThreads;
+  const int b0 = min(a.B, t * per), b1 = min(a.B, b0 + per);
+  uint32_t bits = 0;
+  int count = *a.count_in;
+  if (count < 0 || count > a.num_blocks) {
+    bits |= PD_DEVERR_FREE_LIST;
+    count = count < 0 ? 0 : a.num_blocks;
+  }
+  if (t == 0) s_given = 0;
+  uint32_t ns = 0;
+  for (int b = b0; b < b1; ++b) {
+    const int len = a.lens[b];
+    int n = 0;
+    if (a.released[b]) {
+      if (len < 0 || len > cap) bits |= PD_DEVERR_SEQ_LEN;
+      else n = (len + a.bs - 1) / a.bs;
+    }
+    s_len[b] = len;
+    s_off[b] = n;
+    ns = sat_add(ns, n);
+  }
+  uint32_t n_total;
+  uint32_t n_run = block_scan(ns, s_warp, n_total);
+  int given = 0;
+  for (int b = b0; b < b1; ++b) {
+    const uint32_t n = s_off[b], ne = sat_add(n_run, n);
+    s_off[b] = static_cast<int>(n_run);
+    if (n > 0) {
+      if (ne > static_cast<uint32_t>(a.num_blocks - count)) bits |= PD_DEVERR_FREE_LIST;
+      else {
+        s_len[b] = 0;
+        given = static_cast<int>(ne);
+      }
+    }
+    n_run = ne;
+  }
+  if (t == 0) s_off[a.B] = static_cast<int>(n_total);
+  if (given) atomicMax(&s_given, given);
+  cluster_sync();
+  given = s_given;
+  const int nt = ranks * kTabThreads, me = rank * kTabThreads + t;
+  for (int b = me; b < a.B; b += nt) a.lens_out[b] = s_len[b];
+  if (me == 0) *a.count_out = count + given;
+  for (int k = me; k < given; k += nt) {
+    const int b = find_seq(s_off, a.B, k);
+    int blk = a.table[static_cast<long long>(b) * a.max_blocks + (k - s_off[b])];
+    if (blk < 0 || blk >= a.num_blocks) {
+      bits |= PD_DEVERR_BLOCK_ID;
+      blk = -1;
+    }
+    a.free_blocks[count + k] = blk;
+  }
+  raise_bits(a.flag, bits);
+}
+
+pd_status check_table_dims(const pd_dims* d) {
+  if (!d) return PD_ERR_NULL;
+  if (d->B < 0 || d->block_size < 1 || d->num_blocks < 0 || d->max_blocks_per_seq < 0) return PD_ERR_SHAPE;
+  // lengths and slots of one sequence fit 31 bits
+  if (static_cast<long long>(d->max_blocks_per_seq) * d->block_size > (1ll << 30)) return PD_ERR_UNSUPPORTED;
+  if (d->B > kMaxTableB) return PD_ERR_UNSUPPORTED;
+  return PD_OK;
+}
+
+bool misaligned(const void* p, uintptr_t mask) { return (reinterpret_cast<uintptr_t>(p) & mask) != 0; }
+
+// One cluster of `ctas` CTAs (1 to 8, the portable size).
+template <class Kern, class Args>
+pd_status launch_cluster(Kern kernel, unsigned long long (&done)[64], int ctas, size_t smem, cudaStream_t s,
+                         const Args& args) {
+  const int most = (3 * kMaxTableB + 2) * 4;
+  if (once_per_context(done, [&] { return set_kernel_attributes(kernel, most); }) != cudaSuccess) return PD_ERR_CUDA;
+  return launch_pdl(kernel, ctas, kTabThreads, static_cast<int>(smem), s, ctas, args) == cudaSuccess ? PD_OK
+                                                                                                    : PD_ERR_CUDA;
+}
+
+// CTAs for `items` dealt out to the threads.
+int table_ctas(long long items) { return items > kTabThreads ? 8 : 1; }
+
+}  // namespace
+}  // namespace pd
+
+using namespace pd;
+
+extern "C" pd_status build_block_tables(const int32_t* context_lens, const int32_t* query_lens, int num_tokens,
+                                        int32_t* block_table, const int32_t* free_blocks, const int32_t* free_count,
+                                        int32_t* free_count_out, int32_t* seq_lens, int32_t* query_start_loc,
+                                        int64_t* slot_mapping, int32_t* positions, const pd_dims* dims,
+                                        uint32_t* error_flag, void* stream) {
+  const pd_status st = check_table_dims(dims);
+  if (st != PD_OK) return st;
+  if (num_tokens < 0) return PD_ERR_SHAPE;
+  const pd_dims& d = *dims;
+  if (!free_count || !free_count_out || !query_start_loc) return PD_ERR_NULL;
+  if (d.B > 0 && (!context_lens || !query_lens || !seq_lens)) return PD_ERR_NULL;
+  if (d.B > 0 && d.max_blocks_per_seq > 0 && !block_table) return PD_ERR_NULL;
+  if (d.num_blocks > 0 && !free_blocks) return PD_ERR_NULL;
+  if (num_tokens > 0 && !slot_mapping) return PD_ERR_NULL;
+  if (misaligned(context_lens, 3) || misaligned(query_lens, 3) || misaligned(block_table, 3) ||
+      misaligned(free_blocks, 3) || misaligned(free_count, 3) || misaligned(free_count_out, 3) ||
+      misaligned(seq_lens, 3) || misaligned(query_start_loc, 3) || misaligned(slot_mapping, 7) ||
+      misaligned(positions, 3) || misaligned(error_flag, 3))
+    return PD_ERR_ALIGN;
+  TableArgs a{context_lens, query_lens, block_table, free_blocks, free_count, free_count_out, seq_lens,
+              query_start_loc, slot_mapping, positions, error_flag, d.B, num_tokens, d.block_size, d.num_blocks,
+              d.max_blocks_per_seq};
+  static unsigned long long done[64] = {};
+  return launch_cluster(build_tables_kernel, done, table_ctas(num_tokens), (3 * static_cast<size_t>(d.B) + 2) * 4,
+                        static_cast<cudaStream_t>(stream), a);
+}
+
+extern "C" pd_status release_blocks(const int32_t* block_table, const int32_t* seq_lens, const uint8_t* released,
+                                    int32_t* free_blocks, const int32_t* free_count, int32_t* free_count_out,
+                                    int32_t* seq_lens_out, const pd_dims* dims, uint32_t* error_flag, void* stream) {
+  const pd_status st = check_table_dims(dims);
+  if (st != PD_OK) return st;
+  const pd_dims& d = *dims;
+  if (!free_count || !free_count_out) return PD_ERR_NULL;
+  if (d.B > 0 && (!seq_lens || !released || !seq_lens_out)) return PD_ERR_NULL;
+  if (d.B > 0 && d.max_blocks_per_seq > 0 && !block_table) return PD_ERR_NULL;
+  if (d.num_blocks > 0 && !free_blocks) return PD_ERR_NULL;
+  if (misaligned(block_table, 3) || misaligned(seq_lens, 3) || misaligned(free_blocks, 3) ||
+      misaligned(free_count, 3) || misaligned(free_count_out, 3) || misaligned(seq_lens_out, 3) ||
+      misaligned(error_flag, 3))
+    return PD_ERR_ALIGN;
+  ReleaseArgs a{block_table, seq_lens, released, free_blocks, free_count, free_count_out, seq_lens_out, error_flag,
+                d.B, d.block_size, d.num_blocks, d.max_blocks_per_seq};
+  static unsigned long long done[64] = {};
+  const long long blocks = static_cast<long long>(d.B) * d.max_blocks_per_seq;
+  return launch_cluster(release_kernel, done, table_ctas(blocks), (2 * static_cast<size_t>(d.B) + 1) * 4,
+                        static_cast<cudaStream_t>(stream), a);
+}

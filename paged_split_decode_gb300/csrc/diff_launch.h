@@ -1,0 +1,100 @@
+// diff_launch.h -- internal interface between the host layer and the
+// differential decode's instantiation units (one per cache element kind).
+#pragma once
+#include "decode_diff.cuh"
+#include "launch.h"
+
+namespace pd {
+
+// Shape of the instantiation for (D, cache element kind, ntm row tiles of 8
+// query rows per map, grouped); false when there is none.
+bool diff_kernel_shape(int D, int kv, int ntm, int grouped, KernelShape* out);
+cudaError_t launch_diff(int D, int kv, int ntm, int grouped, const CUtensorMap& tk, const CUtensorMap& tv,
+                        const DiffParams& p, int grid, cudaStream_t stream);
+cudaError_t launch_diff_combine(int D, const DiffParams& p, int n_units, int row_chunks, int rows_at_once,
+                                cudaStream_t stream);
+
+bool diff_shape_f16(int D, int ntm, int grouped, KernelShape* out);
+bool diff_shape_bf16(int D, int ntm, int grouped, KernelShape* out);
+bool diff_shape_fp8(int D, int ntm, int grouped, KernelShape* out);
+bool diff_shape_i8(int D, int ntm, int grouped, KernelShape* out);
+cudaError_t diff_launch_f16(int D, int ntm, int grouped, const CUtensorMap&, const CUtensorMap&, const DiffParams&,
+                            int, cudaStream_t);
+cudaError_t diff_launch_bf16(int D, int ntm, int grouped, const CUtensorMap&, const CUtensorMap&, const DiffParams&,
+                             int, cudaStream_t);
+cudaError_t diff_launch_fp8(int D, int ntm, int grouped, const CUtensorMap&, const CUtensorMap&, const DiffParams&,
+                            int, cudaStream_t);
+cudaError_t diff_launch_i8(int D, int ntm, int grouped, const CUtensorMap&, const CUtensorMap&, const DiffParams&,
+                           int, cudaStream_t);
+
+// The deepest ring (at most 32 stages) that lets MINB CTAs share an SM.
+template <int D, int KV, int NTM, int RG, int MINB, int HG, int NS = 32>
+constexpr int diff_stages() {
+  if constexpr (NS <= 2)
+    return 2;
+  else if constexpr (DiffCfg<D, KV, NTM, RG, NS, MINB, HG>::kSmemBytes <= smem_limit(MINB))
+    return NS;
+  else
+    return diff_stages<D, KV, NTM, RG, MINB, HG, NS - 1>();
+}
+template <int D, int KV, int NTM, int RG, int MINB, int HG>
+using DiffCfgFor = DiffCfg<D, KV, NTM, RG, diff_stages<D, KV, NTM, RG, MINB, HG>(), MINB, HG>;
+
+template <class Cfg>
+bool diff_shape_of(KernelShape* out) {
+  out->threads = Cfg::kThreads;
+  out->smem_bytes = Cfg::kSmemBytes;
+  out->rows_padded = Cfg::RP;
+  out->ctas_per_sm = Cfg::kMinBlocks;
+  out->heads = Cfg::HG;
+  out->unit_cost = 4;
+  out->fixed_pieces = 0;
+  for (int& c : out->max_clusters) c = 0;  // split units go through the combine
+  return true;
+}
+
+template <class Cfg>
+cudaError_t diff_launch_cfg(const CUtensorMap& tk, const CUtensorMap& tv, const DiffParams& p, int grid,
+                            cudaStream_t stream) {
+  static unsigned long long attr_ctx[64] = {};
+  const cudaError_t e =
+      once_per_context(attr_ctx, [] { return set_kernel_attributes(decode_diff_kernel<Cfg>, Cfg::kSmemBytes); });
+  if (e != cudaSuccess) return e;
+  return launch_pdl(decode_diff_kernel<Cfg>, grid, Cfg::kThreads, Cfg::kSmemBytes, stream, 1, tk, tv, p);
+}
+
+// The shapes of one cache kind: C1H, tiles of HG consecutive KV heads (one
+// row tile per map, Hkv a multiple of four) on one CTA per SM; else per-head
+// tiles on two CTAs per SM, with a warp pair for every row tile.
+template <int D, int KV, int HG>
+struct DiffShapes {
+  using C1H = DiffCfgFor<D, KV, 1, 1, 1, HG>;
+  using C1 = DiffCfgFor<D, KV, 1, 1, 2, 1>;
+  using C2 = DiffCfgFor<D, KV, 2, 2, 2, 1>;
+  using C3 = DiffCfgFor<D, KV, 3, 3, 2, 1>;
+  using C4 = DiffCfgFor<D, KV, 4, 4, 2, 1>;
+
+  static bool shape(int ntm, int grouped, KernelShape* out) {
+    if (grouped) return ntm == 1 && diff_shape_of<C1H>(out);
+    switch (ntm) {
+      case 1: return diff_shape_of<C1>(out);
+      case 2: return diff_shape_of<C2>(out);
+      case 3: return diff_shape_of<C3>(out);
+      case 4: return diff_shape_of<C4>(out);
+      default: return false;
+    }
+  }
+  static cudaError_t launch(int ntm, int grouped, const CUtensorMap& tk, const CUtensorMap& tv, const DiffParams& p,
+                            int grid, cudaStream_t s) {
+    if (grouped) return ntm == 1 ? diff_launch_cfg<C1H>(tk, tv, p, grid, s) : cudaErrorInvalidValue;
+    switch (ntm) {
+      case 1: return diff_launch_cfg<C1>(tk, tv, p, grid, s);
+      case 2: return diff_launch_cfg<C2>(tk, tv, p, grid, s);
+      case 3: return diff_launch_cfg<C3>(tk, tv, p, grid, s);
+      case 4: return diff_launch_cfg<C4>(tk, tv, p, grid, s);
+      default: return cudaErrorInvalidValue;
+    }
+  }
+};
+
+}  // namespace pd

@@ -11,6 +11,7 @@
 #include <atomic>
 #include <mutex>
 
+#include "diff_launch.h"
 #include "launch.h"
 #include "pdecode.h"
 
@@ -133,7 +134,9 @@ int device_sm_count(int sm_count) {
 // within ~2 % or the fixed one loses (B=16: +1.0 us, 2 x 2048 tiles: +0.5). The
 // workspace is sized for the balanced split in either case (the fixed split
 // needs fewer slots), so pd_workspace_bytes does not depend on the window.
-pd_status make_plan(const pd_dims* d, int qlen, int num_splits, int sm_count, Plan* pl, int window = 0) {
+// `diff` plans the differential decode, whose kernels hold two maps' rows.
+pd_status make_plan(const pd_dims* d, int qlen, int num_splits, int sm_count, Plan* pl, int window = 0,
+                    bool diff = false) {
   pd_status st = check_dims(d, qlen);
   if (st != PD_OK) return st;
   if (num_splits < 0) return PD_ERR_SHAPE;
@@ -147,8 +150,8 @@ pd_status make_plan(const pd_dims* d, int qlen, int num_splits, int sm_count, Pl
   // single-row-tile shapes whose head count is a multiple of four (the
   // instantiation chooses how many heads a tile holds: 2 or 4)
   const bool grouped = pl->nt == 1 && d->Hkv % 4 == 0;
-  if (!(grouped && kernel_shape(d->D, d->kv_dtype, pl->nt, 1, &ks)) &&
-      !kernel_shape(d->D, d->kv_dtype, pl->nt, 0, &ks))
+  const auto shape = diff ? diff_kernel_shape : kernel_shape;
+  if (!(grouped && shape(d->D, d->kv_dtype, pl->nt, 1, &ks)) && !shape(d->D, d->kv_dtype, pl->nt, 0, &ks))
     return PD_ERR_UNSUPPORTED;
   pl->hg = ks.heads;
   pl->rows_padded = ks.rows_padded;
@@ -303,6 +306,12 @@ size_t pd_workspace_bytes(const pd_dims* dims, int qlen, int num_splits, int sm_
   return pl.bytes;
 }
 
+size_t pd_diff_workspace_bytes(const pd_dims* dims, int qlen, int num_splits, int sm_count) {
+  Plan pl;
+  if (make_plan(dims, qlen, num_splits, sm_count, &pl, 0, true) != PD_OK) return 0;
+  return pl.bytes;
+}
+
 int pd_grid_ctas(const pd_dims* dims, int qlen, int num_splits, int sm_count) {
   Plan pl;
   if (make_plan(dims, qlen, num_splits, sm_count, &pl) != PD_OK) return 0;
@@ -313,14 +322,18 @@ int pd_grid_ctas(const pd_dims* dims, int qlen, int num_splits, int sm_count) {
 
 namespace {
 
-// decode_paged and decode_paged_varlen: q_start null means B sequences of qlen
+// What every decode call checks and fills in: the plan, the caches' maps and
+// the kernel's parameters (`diff`: of the differential decode). `ready` is
+// false when there is nothing to launch. q_start null means B sequences of qlen
 // query tokens each (total_q = B * qlen); otherwise sequence b owns rows
 // [q_start[b], q_start[b+1]) of q and out, at most qlen of them.
-pd_status decode_impl(const void* q, const void* k_cache, const void* v_cache,
-                      const int32_t* block_table, const int32_t* seq_lens, const int32_t* q_start,
-                      int total_q, float scale, int window, int qlen, int num_splits, void* out,
-                      const pd_dims* dims, void* workspace, size_t workspace_bytes,
-                      uint32_t* error_flag, void* stream) {
+pd_status prepare_decode(const void* q, const void* k_cache, const void* v_cache,
+                         const int32_t* block_table, const int32_t* seq_lens, const int32_t* q_start,
+                         int total_q, float scale, int window, int qlen, int num_splits, void* out,
+                         const pd_dims* dims, void* workspace, size_t workspace_bytes,
+                         uint32_t* error_flag, bool diff, Plan& pl, CUtensorMap& tk, CUtensorMap& tv,
+                         DecodeParams& p, bool& ready) {
+  ready = false;
   pd_status st = check_dims(dims, qlen);
   if (st != PD_OK) return st;
   if (num_splits < 0 || !std::isfinite(scale)) return PD_ERR_SHAPE;
@@ -333,20 +346,17 @@ pd_status decode_impl(const void* q, const void* k_cache, const void* v_cache,
       (reinterpret_cast<uintptr_t>(q_start) & 3u) || (reinterpret_cast<uintptr_t>(error_flag) & 3u))
     return PD_ERR_ALIGN;
   if (dims->num_blocks == 0) return PD_ERR_SHAPE;
-  Plan pl;
-  st = make_plan(dims, qlen, num_splits, 0, &pl, window);
+  st = make_plan(dims, qlen, num_splits, 0, &pl, window, diff);
   if (st != PD_OK) return st;
   if (pl.bytes > 0) {
     if (!workspace || workspace_bytes < pl.bytes) return PD_ERR_WORKSPACE;
     if (reinterpret_cast<uintptr_t>(workspace) & 255u) return PD_ERR_ALIGN;
   }
 
-  CUtensorMap tk, tv;
   if (!encode_cache_map(&tk, k_cache, dims, pl.hg) || !encode_cache_map(&tv, v_cache, dims, pl.hg))
     return PD_ERR_CUDA;
 
   const bool fp8 = byte_kind(dims->kv_dtype);  // scaled codes
-  DecodeParams p;
   p.q = static_cast<const __half*>(q);
   p.out = static_cast<__half*>(out);
   p.block_table = block_table;
@@ -384,6 +394,23 @@ pd_status decode_impl(const void* q, const void* k_cache, const void* v_cache,
   p.inject = g_inject.load(std::memory_order_relaxed);
   p.cluster = pl.cluster;
 
+  ready = true;
+  return PD_OK;
+}
+
+pd_status decode_impl(const void* q, const void* k_cache, const void* v_cache,
+                      const int32_t* block_table, const int32_t* seq_lens, const int32_t* q_start,
+                      int total_q, float scale, int window, int qlen, int num_splits, void* out,
+                      const pd_dims* dims, void* workspace, size_t workspace_bytes,
+                      uint32_t* error_flag, void* stream) {
+  Plan pl;
+  CUtensorMap tk, tv;
+  DecodeParams p;
+  bool ready;
+  const pd_status st = prepare_decode(q, k_cache, v_cache, block_table, seq_lens, q_start, total_q, scale, window, qlen,
+                                      num_splits, out, dims, workspace, workspace_bytes, error_flag, false, pl, tk, tv,
+                                      p, ready);
+  if (st != PD_OK || !ready) return st;
   cudaError_t e = launch_decode(dims->D, dims->kv_dtype, pl.nt, pl.hg > 1 ? 1 : 0, tk, tv, p, pl.grid,
                                 static_cast<cudaStream_t>(stream));
   if (e == cudaSuccess && pl.n_merge > 0) {
@@ -443,6 +470,55 @@ pd_status decode_paged_varlen(const void* q, const void* k_cache, const void* v_
   return decode_impl(q, k_cache, v_cache, block_table, seq_lens, query_start_loc,
                      num_query_tokens, scale, window, max_qlen, num_splits, out, dims, workspace,
                      workspace_bytes, error_flag, stream);
+}
+
+pd_status decode_paged_diff(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_table,
+                            const int32_t* seq_lens, const int32_t* query_start_loc, int num_query_tokens,
+                            const float* lambda, float scale, int window, int qlen, int num_splits,
+                            const void* norm_weight, int norm_weight_f32, float norm_eps, float norm_gain, void* out,
+                            const pd_dims* dims, void* workspace, size_t workspace_bytes, uint32_t* error_flag,
+                            void* stream) {
+  if (!dims) return PD_ERR_NULL;
+  long long total = num_query_tokens;
+  if (!query_start_loc) {
+    total = static_cast<long long>(dims->B) * (qlen > 0 ? qlen : 0);
+    if (total > (1ll << 31) - 1) return PD_ERR_UNSUPPORTED;
+  }
+  if (norm_weight && (!(norm_eps >= 0.f) || !std::isfinite(norm_eps) || !std::isfinite(norm_gain))) return PD_ERR_SHAPE;
+  if (dims->B > 0 && total > 0) {
+    if (!lambda) return PD_ERR_NULL;
+    if ((reinterpret_cast<uintptr_t>(lambda) & 3u) ||
+        (reinterpret_cast<uintptr_t>(norm_weight) & (norm_weight_f32 ? 3u : 1u)))
+      return PD_ERR_ALIGN;
+  }
+  Plan pl;
+  CUtensorMap tk, tv;
+  DiffParams p;
+  bool ready;
+  const pd_status st = prepare_decode(q, k_cache, v_cache, block_table, seq_lens, query_start_loc,
+                                      static_cast<int>(total), scale, window, qlen, num_splits, out, dims, workspace,
+                                      workspace_bytes, error_flag, true, pl, tk, tv, p.d, ready);
+  if (st != PD_OK || !ready) return st;
+  p.lambda = lambda;
+  p.norm_weight = norm_weight;
+  p.norm_f32 = norm_weight_f32 ? 1 : 0;
+  p.norm_eps = norm_eps;
+  p.norm_gain = norm_gain;
+  auto s = static_cast<cudaStream_t>(stream);
+  cudaError_t e = launch_diff(dims->D, dims->kv_dtype, pl.nt, pl.hg > 1 ? 1 : 0, tk, tv, p, pl.grid, s);
+  if (e == cudaSuccess && pl.n_merge > 0) {
+    // rows of a unit's head spread over CTAs while the grid stays within one
+    // CTA per SM (resident beside the decode grid, as the split combine's);
+    // a CTA takes one row at a time when units have many pieces, so that
+    // more threads share a row's pieces
+    const long long per_unit = pl.splits == 0 ? pl.grid / (pl.units > 0 ? pl.units : 1) + 1 : pl.splits;
+    int chunks = p.d.R;
+    while (chunks > 1 && pl.n_merge * chunks * pl.hg > pl.sms) chunks = (chunks + 1) / 2;
+    const int most = 512 / (2 * dims->D / 4);
+    const int rows = static_cast<int>(std::max<long long>(1, std::min<long long>(most, 2ll * most / per_unit)));
+    e = launch_diff_combine(dims->D, p, static_cast<int>(pl.n_merge), chunks, rows, s);
+  }
+  return e == cudaSuccess ? PD_OK : PD_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -1,0 +1,250 @@
+"""GPU parity of the differential decode (decode_paged_diff) against 64 bits;
+the error bound is derived in ref_diff.py."""
+import numpy as np
+import pytest
+import torch
+
+import ref_diff
+from paged_split_decode_gb300 import inputs
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+KINDS = ("f16", "bf16", "fp8", "int8", "fp8_bf16q", "int8_bf16q")
+
+
+@pytest.fixture(scope="module")
+def pd():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import paged_split_decode_gb300 as pd
+    pd.load()
+    return pd
+
+
+def caches(w):
+    k, v = w.k_cache.to(DEV), w.v_cache.to(DEV)
+    return (k.view(torch.int8), v.view(torch.int8)) if w.kv_int8 else (k, v)
+
+
+def factors(w, seed=0):
+    g = torch.Generator().manual_seed(seed)
+    lam = 0.2 + 0.6 * torch.rand(w.Hq, generator=g)
+    weight = (1 + 0.1 * torch.randn(w.D, generator=g)).to(w.q.dtype)
+    return lam, weight
+
+
+def run(pd, w, lam, S=0, weight=None, out=None, flag=None, **kw):
+    k, v = caches(w)
+    res = pd.decode_paged_diff(w.q.to(DEV), k, v, w.block_table.to(DEV), w.seq_lens.to(DEV), lam.to(DEV), w.scale,
+                               w.window, w.qlen, S, out=out,
+                               query_start_loc=None if w.q_start is None else w.q_start.to(DEV),
+                               norm_weight=None if weight is None else weight.to(DEV), k_scale=w.k_scale,
+                               v_scale=w.v_scale, error_flag=flag, **kw)
+    torch.cuda.synchronize()
+    return res
+
+
+def check(got, ref, bound):
+    g = got.float().cpu().numpy().astype(np.float64)
+    assert np.all(np.isfinite(g))
+    excess = np.abs(g - ref) / bound
+    assert excess.max() <= 1.0, f"error {excess.max():.2f}x the bound"
+    empty = np.all(ref == 0.0, axis=-1)
+    assert np.all(g[empty] == 0.0), "rows without a key are not zero"
+
+
+def parity(pd, w, S=0, norm=False, **kw):
+    lam, weight = factors(w, w.meta.get("seed", 0))
+    weight = weight if norm else None
+    flag = torch.zeros(1, dtype=torch.int32, device=DEV)
+    got = run(pd, w, lam, S, weight, flag=flag, **kw)
+    assert int(flag.item()) == 0
+    ref, bound = ref_diff.reference(w, lam.double().numpy(), None if weight is None else weight.double().numpy(),
+                                    kw.get("norm_eps", 1e-5), kw.get("norm_gain", 1.0))
+    check(got, ref, bound)
+    return got
+
+
+# every cache kind, head size, tile grouping (Hkv % 4) and count of row tiles
+# per map (G * qlen of 1 to 32), with empty, one-key and ragged sequences
+@pytest.mark.parametrize("norm", (False, True))
+@pytest.mark.parametrize("Hq,Hkv,D,qlen", [
+    (4, 4, 256, 1), (24, 4, 256, 1), (32, 8, 128, 1), (12, 2, 256, 1), (3, 3, 128, 1), (12, 2, 256, 2),
+    (28, 4, 128, 2), (24, 4, 256, 3), (12, 2, 128, 3), (8, 1, 256, 4), (32, 8, 128, 8)])
+@pytest.mark.parametrize("kv", KINDS)
+def test_parity(pd, kv, Hq, Hkv, D, qlen, norm):
+    w = inputs.make_workload(B=5, Hq=Hq, Hkv=Hkv, D=D, seq_lens=[300, 0, max(1, qlen - 1), 17, 129], qlen=qlen, kv=kv,
+                             seed=Hq + D + qlen, scale=(D // 2) ** -0.5, stale="nan")
+    parity(pd, w, norm=norm)
+
+
+@pytest.mark.parametrize("S", (0, 1, 2, 3, 8, 40))
+@pytest.mark.parametrize("kv", ("f16", "bf16", "fp8_bf16q", "int8"))
+def test_splits_agree(pd, kv, S):
+    w = inputs.make_workload(B=3, Hq=12, Hkv=4, D=256, seq_lens=[1000, 5, 2049], kv=kv, seed=7, scale=128 ** -0.5)
+    parity(pd, w, S, norm=True, norm_gain=0.4)
+
+
+@pytest.mark.parametrize("window", (1, 15, 16, 100, 5000))
+@pytest.mark.parametrize("S", (0, 1, 5))
+def test_window(pd, window, S):
+    w = inputs.make_workload(B=4, Hq=8, Hkv=2, D=128, seq_lens=[700, 64, 0, 33], qlen=3, window=window, kv="f16",
+                             seed=11, scale=0.125)
+    parity(pd, w, S)
+
+
+@pytest.mark.parametrize("block_size", (16, 48, 128))
+def test_block_sizes(pd, block_size):
+    w = inputs.make_workload(B=3, Hq=8, Hkv=4, D=128, seq_lens=[700, 1, 333], kv="bf16", block_size=block_size, seed=13,
+                             scale=0.125, stale="nan")
+    parity(pd, w, norm=True)
+
+
+@pytest.mark.parametrize("B", (1, 2, 200, 300, 1200))
+def test_batches(pd, B):
+    """One sequence over all SMs, more units than SMs (finished by their own
+    piece), and batches beyond the cached (256) and the balanced (1024) ones."""
+    rng = np.random.RandomState(B)
+    lens = [3000] if B == 1 else [int(x) for x in rng.randint(0, 60, B)]
+    w = inputs.make_workload(B=B, Hq=8, Hkv=4, D=128, seq_lens=lens, kv="f16", seed=17, scale=0.125)
+    parity(pd, w, norm=True)
+
+
+@pytest.mark.parametrize("kv", ("f16", "fp8"))
+@pytest.mark.parametrize("S", (0, 1, 4))
+def test_varlen(pd, kv, S):
+    w = inputs.make_varlen_workload(B=6, qlens=[1, 0, 4, 2, 3, 1], Hq=24, Hkv=4, D=256,
+                                    seq_lens=[500, 40, 1200, 0, 2, 77], kv=kv, seed=19, scale=128 ** -0.5)
+    parity(pd, w, S, norm=True)
+
+
+def test_varlen_leaves_other_rows(pd):
+    w = inputs.make_varlen_workload(B=3, qlens=[2, 1, 1], Hq=8, Hkv=2, D=128, seq_lens=[50, 20, 30], kv="f16", seed=23,
+                                    scale=0.125)
+    lam, _ = factors(w)
+    q = torch.cat([w.q, w.q[:3]])
+    k, v = caches(w)
+    out = torch.full((q.shape[0], 8, 128), 7.0, dtype=torch.float16, device=DEV)
+    pd.decode_paged_diff(q.to(DEV), k, v, w.block_table.to(DEV), w.seq_lens.to(DEV), lam.to(DEV), w.scale, qlen=2,
+                         out=out, query_start_loc=w.q_start.to(DEV))
+    ref, bound = ref_diff.reference(w, lam.double().numpy())
+    check(out[:4], ref, bound)
+    assert torch.all(out[4:] == 7.0)
+
+
+def test_lambda_zero_is_the_first_map_alone(pd):
+    """lambda = 0: the plain decode on q and K whose second halves are zero."""
+    w = inputs.make_workload(B=2, Hq=8, Hkv=4, D=256, seq_lens=[400, 90], kv="f16", seed=29, scale=128 ** -0.5)
+    got = run(pd, w, torch.zeros(8))
+    ref, bound = ref_diff.reference(w, np.zeros(8))
+    check(got, ref, bound)
+    q, k = w.q.clone(), w.k_cache.clone()
+    q[..., 128:] = 0
+    plain = pd.decode_paged(q.to(DEV), k.to(DEV), w.v_cache.to(DEV), w.block_table.to(DEV), w.seq_lens.to(DEV), w.scale)
+    check(plain, ref, bound)
+
+
+def test_norm_weight_in_float32_and_zero_eps(pd):
+    w = inputs.make_workload(B=3, Hq=8, Hkv=4, D=128, seq_lens=[200, 0, 65], kv="f16", seed=31, scale=0.125)
+    lam, weight = factors(w)
+    got = run(pd, w, lam, 0, weight.float(), norm_eps=0.0, norm_gain=2.5)
+    ref, bound = ref_diff.reference(w, lam.double().numpy(), weight.double().numpy(), 1e-300, 2.5)
+    check(got, ref, bound)
+
+
+def test_same_bits_again_and_after_other_calls(pd):
+    w = inputs.make_workload(B=4, Hq=24, Hkv=4, D=256, seq_lens=[900, 31, 2000, 64], kv="bf16", seed=37,
+                             scale=128 ** -0.5)
+    lam, weight = factors(w)
+    a = run(pd, w, lam, 0, weight).clone()
+    other = inputs.make_workload(B=2, Hq=8, Hkv=2, D=128, seq_lens=[3000, 100], kv="f16", seed=38, scale=0.125)
+    run(pd, other, factors(other)[0])
+    assert torch.equal(a, run(pd, w, lam, 0, weight))
+
+
+def test_bad_tables_and_lengths_raise_bits(pd):
+    w = inputs.make_workload(B=3, Hq=8, Hkv=4, D=128, seq_lens=[100, 40, 64], kv="f16", seed=41, scale=0.125)
+    lam, _ = factors(w)
+    flag = torch.zeros(1, dtype=torch.int32, device=DEV)
+    w.block_table[1, 0] = 10_000
+    got = run(pd, w, lam, flag=flag)
+    assert int(flag.item()) == pd.DEVERR_BLOCK_ID
+    w.block_table[1, 0] = 0
+    w.seq_lens[1] = 7000
+    flag.zero_()
+    run(pd, w, lam, flag=flag)
+    assert int(flag.item()) & pd.DEVERR_SEQ_LEN
+    ref, bound = ref_diff.reference(inputs.make_workload(B=3, Hq=8, Hkv=4, D=128, seq_lens=[100, 40, 64], kv="f16",
+                                                         seed=41, scale=0.125), lam.double().numpy())
+    check(got[0:1], ref[0:1], bound[0:1])  # the other sequences are not disturbed
+    check(got[2:3], ref[2:3], bound[2:3])
+
+
+def test_a_wait_that_runs_out_reports(pd):
+    from paged_split_decode_gb300 import binding
+    w = inputs.make_workload(B=2, Hq=8, Hkv=4, D=128, seq_lens=[100, 40], kv="f16", seed=43, scale=0.125)
+    lam, _ = factors(w)
+    flag = torch.zeros(1, dtype=torch.int32, device=DEV)
+    binding.set_wait_limit_ns(2_000_000)
+    binding.set_fault_injection(1)
+    try:
+        run(pd, w, lam, flag=flag)
+    finally:
+        binding.set_fault_injection(0)
+        binding.set_wait_limit_ns(0)
+    assert int(flag.item()) == pd.DEVERR_TIMEOUT
+    parity(pd, w)
+
+
+def test_two_streams_and_two_captured_graphs(pd):
+    """Calls without a workspace on two streams, and two graphs captured on
+    one stream and replayed on two, do not share partials."""
+    ws = [inputs.make_workload(B=2, Hq=24, Hkv=4, D=256, seq_lens=[3000, 2000], kv="f16", seed=s, scale=128 ** -0.5)
+          for s in (47, 48)]
+    lams = [factors(w)[0] for w in ws]
+    want = [run(pd, w, lam).clone() for w, lam in zip(ws, lams)]
+    args = []
+    for w, lam in zip(ws, lams):
+        k, v = caches(w)
+        args.append([w.q.to(DEV), k, v, w.block_table.to(DEV), w.seq_lens.to(DEV), lam.to(DEV), w.scale])
+    outs = [torch.empty_like(a[0]) for a in args]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for s, a, o in zip(streams, args, outs):
+            with torch.cuda.stream(s):
+                pd.decode_paged_diff(*a, out=o)
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, x) for o, x in zip(outs, want))
+    graphs = []
+    for a, o in zip(args, outs):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=streams[0]):
+            pd.decode_paged_diff(*a, out=o)
+        graphs.append(g)
+        o.zero_()
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for s, g in zip(streams, graphs):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, x) for o, x in zip(outs, want))
+
+
+def test_an_explicit_stream_handle(pd):
+    w = inputs.make_workload(B=2, Hq=8, Hkv=4, D=128, seq_lens=[900, 33], kv="f16", seed=53, scale=0.125)
+    lam, weight = factors(w)
+    want = run(pd, w, lam, 0, weight)
+    s = torch.cuda.Stream()
+    got = run(pd, w, lam, 0, weight, stream=s.cuda_stream)
+    assert torch.equal(got, want)
+
+
+def test_a_workspace_too_small_is_refused(pd):
+    w = inputs.make_workload(B=2, Hq=8, Hkv=4, D=128, seq_lens=[900, 33], kv="f16", seed=53, scale=0.125)
+    lam, _ = factors(w)
+    with pytest.raises(pd.DecodeError, match="workspace"):
+        run(pd, w, lam, workspace=torch.empty(256, dtype=torch.uint8, device=DEV))
+    need = pd.diff_workspace_bytes(pd.dims_of(w.q, w.k_cache, w.block_table, 1), 1, 0)
+    parity(pd, w, workspace=torch.empty(need, dtype=torch.uint8, device=DEV))
