@@ -360,33 +360,72 @@ def write_kv_cache(k_new, v_new, slot_mapping, k_cache, v_cache, *, k_scale=1.0,
 
 
 # ---- differential decode, block tables, root-mean-square norm ----------------
+# These run beside kernels of a few microseconds, so their checks are kept to
+# one query each per tensor, and a plan's workspace size is kept by its shapes.
+_INT = (torch.int32,)
+_LONG = (torch.int64,)
+_FLOAT = (torch.float32,)
+_BYTE = (torch.bool, torch.uint8)
+_HALF = (torch.float16,)
+_BF16 = (torch.bfloat16,)
 _FLAG_TYPES = (torch.int32, torch.uint32)
 _CODE_KINDS = {torch.float8_e4m3fn: 1, torch.int8: 2}
+_diff_need: dict = {}
 
 
-def _same_device(dev: torch.device, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, expected {dev}")
+def _arg(t, name, dtypes, index) -> int:
+    """Device pointer of a contiguous tensor on GPU ``index`` (None: 0)."""
+    if t is None:
+        return 0
+    if t.get_device() != index:
+        if not t.is_cuda:
+            raise TypeError(f"{name} must be a CUDA tensor")
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtypes}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
 
 
-def _opt_ptr(t, name, dtype):
-    return None if t is None else _dev_ptr(t, name, dtype)
+def _gpu_of(t, name) -> int:
+    index = t.get_device()
+    if index < 0:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    return index
 
 
-def _launch(dev: torch.device, stream, call):
-    """Run ``call(stream handle)`` with ``dev`` current."""
-    if torch.cuda.current_device() == dev.index:
-        return call(torch.cuda.current_stream(dev).cuda_stream if stream is None else int(stream))
-    with torch.cuda.device(dev):
-        return call(torch.cuda.current_stream(dev).cuda_stream if stream is None else int(stream))
+def _call(fn, what, index, stream, args):
+    """Launch on ``stream`` (None: the current one) with GPU ``index`` current."""
+    s = torch._C._cuda_getCurrentRawStream(index) if stream is None else int(stream)
+    if torch._C._cuda_getDevice() == index:
+        rc = fn(*args, s)
+    else:
+        with torch.cuda.device(index):
+            rc = fn(*args, s)
+    if rc:
+        _check(rc, what)
 
 
-def _on_stream(dev: torch.device, stream):
-    """Allocations under this context are ordered by the stream of the launch."""
-    if stream is None or int(stream) == torch.cuda.current_stream(dev).cuda_stream:
+def _alloc_on(stream, index):
+    """Allocations under this context are ordered by the launch's stream."""
+    if stream is None or int(stream) == torch._C._cuda_getCurrentRawStream(index):
         return contextlib.nullcontext()
-    return torch.cuda.stream(torch.cuda.ExternalStream(int(stream), device=dev))
+    return torch.cuda.stream(torch.cuda.ExternalStream(int(stream), device=index))
+
+
+def _diff_workspace(need, index, stream):
+    """The workspace of a call that brought none. A captured call keeps one of
+    its own in the graph's pool, as graphs may be replayed at the same time."""
+    with _alloc_on(stream, index):
+        if torch._C._cuda_isCurrentStreamCapturing():
+            return torch.empty(need, dtype=torch.uint8, device=torch.device("cuda", index))
+    s = torch._C._cuda_getCurrentRawStream(index) if stream is None else int(stream)
+    ws = _workspaces.get(("cuda", index, s))
+    if ws is None or ws.numel() < need:
+        with torch.cuda.device(index):
+            ws = get_workspace(torch.device("cuda", index), need, s)
+    return ws
 
 
 def decode_paged_diff(q, k_cache, v_cache, block_table, seq_lens, lam, scale, window=0, qlen=1,
@@ -404,63 +443,60 @@ def decode_paged_diff(q, k_cache, v_cache, block_table, seq_lens, lam, scale, wi
     ``qlen``, as in ``decode_paged_varlen`` (rows outside every range are left
     as they were; a new ``out`` is zeroed there).
     """
-    lib = load()
-    kind = kv_kind_of(k_cache, q.dtype)
-    kv_dt, q_dt = _dtypes(kind)
-    B = block_table.shape[0]
-    if v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype:
+    lib = _lib or load()
+    q_dtype = q.dtype
+    kind = kv_kind_of(k_cache, q_dtype)
+    io = _BF16 if kind in _BF16_IO else _HALF
+    kv_dt = (k_cache.dtype,)
+    if q.dim() != 3 or k_cache.dim() != 4 or block_table.dim() != 2:
+        raise ValueError("q must be [T, Hq, D], the caches [num_blocks, block_size, Hkv, D], block_table [B, max_blocks]")
+    T, Hq, D = q.shape
+    num_blocks, bs, Hkv, Dk = k_shape = k_cache.shape
+    B, cols = block_table.shape
+    if v_cache.shape != k_shape or v_cache.dtype != k_cache.dtype:
         raise ValueError("v_cache must match k_cache in shape and dtype")
-    if q.dim() != 3 or q.shape[2] != k_cache.shape[3] or seq_lens.numel() != B:
+    if D != Dk or seq_lens.numel() != B:
         raise ValueError("q must be [T, Hq, D] with the caches' D; seq_lens [B]")
     if query_start_loc is None:
-        if q.shape[0] != B * qlen:
+        if T != B * qlen:
             raise ValueError("q must be [B*qlen, Hq, D] with B = rows of block_table")
     elif query_start_loc.numel() != B + 1:
         raise ValueError("query_start_loc must be [B+1]")
-    if lam.numel() != q.shape[1]:
+    if lam.numel() != Hq:
         raise ValueError("lam must be [Hq]")
-    if norm_weight is not None and norm_weight.numel() != q.shape[2]:
-        raise ValueError("norm_weight must be [D]")
+    weight_f32 = 0
+    if norm_weight is not None:
+        if norm_weight.numel() != D:
+            raise ValueError("norm_weight must be [D]")
+        weight_f32 = int(norm_weight.dtype == torch.float32)
     if out is not None and out.shape != q.shape:
         raise ValueError("out must have q's shape")
-    dims = dims_of(q, k_cache, block_table, qlen, None, k_scale, v_scale)
-    dev = q.device
-    _same_device(dev, k_cache=k_cache, v_cache=v_cache, block_table=block_table, seq_lens=seq_lens, lam=lam,
-                 out=out, query_start_loc=query_start_loc, norm_weight=norm_weight, workspace=workspace,
-                 error_flag=error_flag)
-
-    def call(s):
-        nonlocal out, workspace
-        with _on_stream(dev, stream):
-            if out is None:
-                out = torch.empty_like(q) if query_start_loc is None else torch.zeros_like(q)
-            if workspace is None:
+    index = _gpu_of(q, "q")
+    dims = PdDims(B, Hq, Hkv, D, bs, num_blocks, cols, kind, k_scale, v_scale)
+    if out is None:
+        with _alloc_on(stream, index):
+            out = torch.empty_like(q) if query_start_loc is None else torch.zeros_like(q)
+    if workspace is None:
+        key = (index, B, Hq, Hkv, D, bs, num_blocks, cols, kind, qlen, num_splits)
+        need = _diff_need.get(key)
+        if need is None:
+            with torch.cuda.device(index):
                 need = diff_workspace_bytes(dims, qlen, num_splits)
-                # a captured call keeps a workspace of its own in the graph's
-                # pool: graphs may be replayed at the same time
-                if need and torch.cuda.is_current_stream_capturing():
-                    workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-                else:
-                    workspace = get_workspace(dev, need, s)
-        return lib.decode_paged_diff(
-            _dev_ptr(q, "q", q_dt), _dev_ptr(k_cache, "k_cache", kv_dt), _dev_ptr(v_cache, "v_cache", kv_dt),
-            _dev_ptr(block_table, "block_table", torch.int32), _dev_ptr(seq_lens, "seq_lens", torch.int32),
-            _opt_ptr(query_start_loc, "query_start_loc", torch.int32), int(q.shape[0]),
-            _dev_ptr(lam, "lam", torch.float32), float(scale), int(window), int(qlen), int(num_splits),
-            _opt_ptr(norm_weight, "norm_weight", (q_dt, torch.float32)),
-            int(norm_weight is not None and norm_weight.dtype == torch.float32), float(norm_eps),
-            float(norm_gain), _dev_ptr(out, "out", q_dt), ctypes.byref(dims),
-            None if workspace is None else _dev_ptr(workspace, "workspace"),
-            0 if workspace is None else workspace.numel() * workspace.element_size(),
-            _opt_ptr(error_flag, "error_flag", _FLAG_TYPES), s)
-
-    _check(_launch(dev, stream, call), "decode_paged_diff")
+            if len(_diff_need) >= 4096:
+                _diff_need.clear()
+            _diff_need[key] = need
+        if need:
+            workspace = _diff_workspace(need, index, stream)
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _call(lib.decode_paged_diff, "decode_paged_diff", index, stream, (
+        _arg(q, "q", io, index), _arg(k_cache, "k_cache", kv_dt, index), _arg(v_cache, "v_cache", kv_dt, index),
+        _arg(block_table, "block_table", _INT, index), _arg(seq_lens, "seq_lens", _INT, index),
+        _arg(query_start_loc, "query_start_loc", _INT, index), T, _arg(lam, "lam", _FLOAT, index), scale, window, qlen,
+        num_splits, _arg(norm_weight, "norm_weight", _FLOAT if weight_f32 else io, index), weight_f32, norm_eps,
+        norm_gain, _arg(out, "out", io, index), ctypes.byref(dims),
+        0 if workspace is None else _arg(workspace, "workspace", (workspace.dtype,), index), ws_bytes,
+        _arg(error_flag, "error_flag", _FLAG_TYPES, index)))
     return out
-
-
-def _table_dims(block_table, free_blocks, block_size) -> PdDims:
-    return PdDims(block_table.shape[0], 1, 1, 1, int(block_size), free_blocks.numel(), block_table.shape[1], 0,
-                  1.0, 1.0)
 
 
 def build_block_tables(context_lens, query_lens, block_table, free_blocks, free_count, block_size,
@@ -477,51 +513,52 @@ def build_block_tables(context_lens, query_lens, block_table, free_blocks, free_
     behind the last token. ``seq_lens`` may be ``context_lens`` itself;
     ``free_count`` is updated in place unless ``free_count_out`` is given.
     """
-    lib = load()
-    if block_table.dim() != 2 or context_lens.numel() != block_table.shape[0] \
-            or query_lens.numel() != block_table.shape[0]:
-        raise ValueError("block_table must be [B, max_blocks]; context_lens and query_lens [B]")
-    B, dev = block_table.shape[0], block_table.device
-    if slot_mapping is None and num_tokens is None:
+    lib = _lib or load()
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [B, max_blocks]")
+    B, cols = block_table.shape
+    if context_lens.numel() != B or query_lens.numel() != B:
+        raise ValueError("context_lens and query_lens must be [B]")
+    if slot_mapping is not None:
+        T = slot_mapping.numel()
+        if num_tokens is not None and num_tokens != T:
+            raise ValueError("slot_mapping must be [num_tokens]")
+    elif num_tokens is None:
         raise ValueError("give num_tokens or a slot_mapping")
-    T = slot_mapping.numel() if num_tokens is None else int(num_tokens)
-    if slot_mapping is not None and slot_mapping.numel() != T:
-        raise ValueError("slot_mapping must be [num_tokens]")
+    else:
+        T = int(num_tokens)
+        if T < 0:
+            raise ValueError("num_tokens must not be negative")
     if positions is not None and positions.numel() != T:
         raise ValueError("positions must be [num_tokens]")
-    if free_count.numel() != 1 or (free_count_out is not None and free_count_out.numel() != 1):
+    if free_count_out is None:
+        free_count_out = free_count
+    if free_count.numel() != 1 or free_count_out.numel() != 1:
         raise ValueError("free_count must be [1]")
     if seq_lens is not None and seq_lens.numel() != B:
         raise ValueError("seq_lens must be [B]")
     if query_start_loc is not None and query_start_loc.numel() != B + 1:
         raise ValueError("query_start_loc must be [B+1]")
-    _same_device(dev, context_lens=context_lens, query_lens=query_lens, free_blocks=free_blocks, free_count=free_count,
-                 seq_lens=seq_lens, query_start_loc=query_start_loc, slot_mapping=slot_mapping, positions=positions,
-                 free_count_out=free_count_out, error_flag=error_flag)
-    dims = _table_dims(block_table, free_blocks, block_size)
-    i32 = torch.int32
-
-    def call(s):
-        nonlocal seq_lens, query_start_loc, slot_mapping, positions
-        with _on_stream(dev, stream):
+    index = _gpu_of(block_table, "block_table")
+    if seq_lens is None or query_start_loc is None or slot_mapping is None or positions is None:
+        with _alloc_on(stream, index):
+            dev = block_table.device
             if seq_lens is None:
-                seq_lens = torch.empty(B, dtype=i32, device=dev)
+                seq_lens = torch.empty(B, dtype=torch.int32, device=dev)
             if query_start_loc is None:
-                query_start_loc = torch.empty(B + 1, dtype=i32, device=dev)
+                query_start_loc = torch.empty(B + 1, dtype=torch.int32, device=dev)
             if slot_mapping is None:
                 slot_mapping = torch.empty(T, dtype=torch.int64, device=dev)
             if positions is None:
-                positions = torch.empty(T, dtype=i32, device=dev)
-        return lib.build_block_tables(
-            _dev_ptr(context_lens, "context_lens", i32), _dev_ptr(query_lens, "query_lens", i32), T,
-            _dev_ptr(block_table, "block_table", i32), _dev_ptr(free_blocks, "free_blocks", i32),
-            _dev_ptr(free_count, "free_count", i32),
-            _dev_ptr(free_count if free_count_out is None else free_count_out, "free_count_out", i32),
-            _dev_ptr(seq_lens, "seq_lens", i32), _dev_ptr(query_start_loc, "query_start_loc", i32),
-            _dev_ptr(slot_mapping, "slot_mapping", torch.int64), _dev_ptr(positions, "positions", i32),
-            ctypes.byref(dims), _opt_ptr(error_flag, "error_flag", _FLAG_TYPES), s)
-
-    _check(_launch(dev, stream, call), "build_block_tables")
+                positions = torch.empty(T, dtype=torch.int32, device=dev)
+    dims = PdDims(B, 1, 1, 1, block_size, free_blocks.numel(), cols, 0, 1.0, 1.0)
+    _call(lib.build_block_tables, "build_block_tables", index, stream, (
+        _arg(context_lens, "context_lens", _INT, index), _arg(query_lens, "query_lens", _INT, index), T,
+        _arg(block_table, "block_table", _INT, index), _arg(free_blocks, "free_blocks", _INT, index),
+        _arg(free_count, "free_count", _INT, index), _arg(free_count_out, "free_count_out", _INT, index),
+        _arg(seq_lens, "seq_lens", _INT, index), _arg(query_start_loc, "query_start_loc", _INT, index),
+        _arg(slot_mapping, "slot_mapping", _LONG, index), _arg(positions, "positions", _INT, index),
+        ctypes.byref(dims), _arg(error_flag, "error_flag", _FLAG_TYPES, index)))
     return seq_lens, query_start_loc, slot_mapping, positions
 
 
@@ -531,27 +568,28 @@ def release_blocks(block_table, seq_lens, released, free_blocks, free_count, blo
     [B]) back onto ``free_blocks``, in order, and set their ``seq_lens`` to 0;
     ``seq_lens`` and ``free_count`` are updated in place unless
     ``seq_lens_out`` / ``free_count_out`` are given. Returns the lengths."""
-    lib = load()
-    if block_table.dim() != 2 or seq_lens.numel() != block_table.shape[0] or released.numel() != block_table.shape[0]:
-        raise ValueError("block_table must be [B, max_blocks]; seq_lens and released [B]")
-    if free_count.numel() != 1 or (free_count_out is not None and free_count_out.numel() != 1):
+    lib = _lib or load()
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [B, max_blocks]")
+    B, cols = block_table.shape
+    if seq_lens.numel() != B or released.numel() != B:
+        raise ValueError("seq_lens and released must be [B]")
+    if free_count_out is None:
+        free_count_out = free_count
+    if free_count.numel() != 1 or free_count_out.numel() != 1:
         raise ValueError("free_count must be [1]")
     if seq_lens_out is None:
         seq_lens_out = seq_lens
-    elif seq_lens_out.numel() != seq_lens.numel():
+    elif seq_lens_out.numel() != B:
         raise ValueError("seq_lens_out must be [B]")
-    dev = block_table.device
-    _same_device(dev, seq_lens=seq_lens, released=released, free_blocks=free_blocks, free_count=free_count,
-                 seq_lens_out=seq_lens_out, free_count_out=free_count_out, error_flag=error_flag)
-    dims = _table_dims(block_table, free_blocks, block_size)
-    i32 = torch.int32
-    _check(_launch(dev, stream, lambda s: lib.release_blocks(
-        _dev_ptr(block_table, "block_table", i32), _dev_ptr(seq_lens, "seq_lens", i32),
-        _dev_ptr(released, "released", (torch.bool, torch.uint8)), _dev_ptr(free_blocks, "free_blocks", i32),
-        _dev_ptr(free_count, "free_count", i32),
-        _dev_ptr(free_count if free_count_out is None else free_count_out, "free_count_out", i32),
-        _dev_ptr(seq_lens_out, "seq_lens_out", i32), ctypes.byref(dims),
-        _opt_ptr(error_flag, "error_flag", _FLAG_TYPES), s)), "release_blocks")
+    index = _gpu_of(block_table, "block_table")
+    dims = PdDims(B, 1, 1, 1, block_size, free_blocks.numel(), cols, 0, 1.0, 1.0)
+    _call(lib.release_blocks, "release_blocks", index, stream, (
+        _arg(block_table, "block_table", _INT, index), _arg(seq_lens, "seq_lens", _INT, index),
+        _arg(released, "released", _BYTE, index), _arg(free_blocks, "free_blocks", _INT, index),
+        _arg(free_count, "free_count", _INT, index), _arg(free_count_out, "free_count_out", _INT, index),
+        _arg(seq_lens_out, "seq_lens_out", _INT, index), ctypes.byref(dims),
+        _arg(error_flag, "error_flag", _FLAG_TYPES, index)))
     return seq_lens_out
 
 
@@ -567,16 +605,18 @@ def rms_norm(x, weight, eps=1e-5, *, residual=None, residual_out=None, gain=1.0,
     float8_e4m3fn or int8; the 8-bit types come with a float32 scale for every
     ``scale_size`` values (default: N). Returns ``out``, or ``(out,
     out_scale)`` for the 8-bit types."""
-    lib = load()
-    if x.dtype not in (torch.float16, torch.bfloat16):
-        raise TypeError(f"x has dtype {x.dtype}, expected float16 or bfloat16")
-    if x.dim() < 1 or x.shape[-1] < 1:
+    lib = _lib or load()
+    x_dtype, shape = x.dtype, x.shape
+    bf16 = x_dtype == torch.bfloat16
+    if not bf16 and x_dtype != torch.float16:
+        raise TypeError(f"x has dtype {x_dtype}, expected float16 or bfloat16")
+    if len(shape) < 1 or shape[-1] < 1:
         raise ValueError("x must be [..., N] with N >= 1")
-    N = x.shape[-1]
+    N = shape[-1]
     rows = x.numel() // N
     norm_size = N if norm_size is None else int(norm_size)
-    dt = out_dtype if out_dtype is not None else x.dtype if out is None else out.dtype
-    kind = 0 if dt == x.dtype else _CODE_KINDS.get(dt)
+    dt = out_dtype if out_dtype is not None else x_dtype if out is None else out.dtype
+    kind = 0 if dt == x_dtype else _CODE_KINDS.get(dt)
     if kind is None:
         raise TypeError(f"unsupported output dtype {dt}")
     scale_size = N if scale_size is None else int(scale_size)
@@ -585,32 +625,29 @@ def rms_norm(x, weight, eps=1e-5, *, residual=None, residual_out=None, gain=1.0,
     if weight.numel() != norm_size:
         raise ValueError("weight must be [norm_size]")
     if residual is not None:
-        if residual.shape != x.shape:
+        if residual.shape != shape:
             raise ValueError("residual must have x's shape")
         if residual_out is None:
             residual_out = residual
-    if residual_out is not None and residual_out.shape != x.shape:
+    if residual_out is not None and residual_out.shape != shape:
         raise ValueError("residual_out must have x's shape")
-    if out is not None and (out.shape != x.shape or out.dtype != dt):
+    if out is not None and (out.shape != shape or out.dtype != dt):
         raise ValueError("out must have x's shape and the output dtype")
     if out_scale is not None and (kind == 0 or out_scale.numel() != rows * (N // scale_size)):
         raise ValueError("out_scale is [..., N / scale_size], for 8-bit outputs only")
-    dev = x.device
-    _same_device(dev, weight=weight, residual=residual, residual_out=residual_out, out=out, out_scale=out_scale)
-    dims = PdNormDims(rows, N, norm_size, scale_size, int(x.dtype == torch.bfloat16),
-                      int(weight.dtype == torch.float32), kind)
-
-    def call(s):
-        nonlocal out, out_scale
-        with _on_stream(dev, stream):
+    index = _gpu_of(x, "x")
+    if out is None or (kind and out_scale is None):
+        with _alloc_on(stream, index):
             if out is None:
-                out = torch.empty(x.shape, dtype=dt, device=dev)
+                out = torch.empty(shape, dtype=dt, device=x.device)
             if kind and out_scale is None:
-                out_scale = torch.empty(x.shape[:-1] + (N // scale_size,), dtype=torch.float32, device=dev)
-        return lib.rms_norm(_dev_ptr(x, "x"), _opt_ptr(residual, "residual", x.dtype),
-                            _dev_ptr(weight, "weight", (x.dtype, torch.float32)), float(eps), float(gain),
-                            _opt_ptr(residual_out, "residual_out", x.dtype), _dev_ptr(out, "out", dt),
-                            _opt_ptr(out_scale, "out_scale", torch.float32), ctypes.byref(dims), s)
-
-    _check(_launch(dev, stream, call), "rms_norm")
+                out_scale = torch.empty(shape[:-1] + (N // scale_size,), dtype=torch.float32, device=x.device)
+    weight_f32 = int(weight.dtype == torch.float32)
+    io = _BF16 if bf16 else _HALF
+    dims = PdNormDims(rows, N, norm_size, scale_size, bf16, weight_f32, kind)
+    _call(lib.rms_norm, "rms_norm", index, stream, (
+        _arg(x, "x", io, index), _arg(residual, "residual", io, index),
+        _arg(weight, "weight", _FLOAT if weight_f32 else io, index), eps, gain,
+        _arg(residual_out, "residual_out", io, index), _arg(out, "out", (dt,), index),
+        _arg(out_scale, "out_scale", _FLOAT, index), ctypes.byref(dims)))
     return (out, out_scale) if kind else out

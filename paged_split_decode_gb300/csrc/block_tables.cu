@@ -18,9 +18,10 @@
 // thread a run of consecutive sequences, then one block scan), which costs
 // less than a second launch; the cluster barrier then makes the in-place
 // forms safe (seq_lens over context_lens, the count over itself), since no
-// CTA writes before all have read. Tokens and new blocks are dealt to all
-// threads of the cluster, each finding its sequence by a binary search in the
-// prefix held in shared memory.
+// CTA writes before all have read. Tokens and blocks are dealt to the
+// cluster's warps in contiguous shares: a lane finds its first item's sequence
+// by a binary search in the prefix held in shared memory and the next ones
+// from there, with eight items' loads in flight.
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -86,6 +87,49 @@ __device__ __forceinline__ void cluster_sync() {
 
 __device__ __forceinline__ void raise_bits(uint32_t* flag, uint32_t bits) {
   if (flag && bits) atomicOr(flag, bits);
+}
+
+// The warps of the cluster take equal contiguous shares of n items, a lane
+// every 32nd of its warp's: `item` is called with each k, in increasing order,
+// kBatch of them between two calls of `flush`.
+constexpr int kBatch = 8;
+template <class Item, class Flush>
+__device__ __forceinline__ void deal(int n, int rank, int ranks, Item item, Flush flush) {
+  if (n <= ranks * kTabThreads) {  // one item a thread
+    const int k = rank * kTabThreads + static_cast<int>(threadIdx.x);
+    if (k < n) {
+      item(k, 0);
+      flush(k, 0);
+    }
+    return;
+  }
+  const int warps = ranks * kTabWarps, warp = rank * kTabWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const int share = ((n + warps - 1) / warps + 31) / 32 * 32;
+  const long long first = static_cast<long long>(warp) * share;
+  const int end = static_cast<int>(min(static_cast<long long>(n), first + share));
+  for (long long k0 = first + lane; k0 < end; k0 += 32 * kBatch) {
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const long long k = k0 + 32 * j;
+      if (k < end) item(static_cast<int>(k), j);
+    }
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const long long k = k0 + 32 * j;
+      if (k < end) flush(static_cast<int>(k), j);
+    }
+  }
+}
+
+// find_seq for increasing x: from the last answer (-1: none yet) forwards.
+__device__ __forceinline__ int next_seq(const int* pre, int n, int x, int last) {
+  if (last < 0) return find_seq(pre, n, x);
+  int b = last;
+  for (int step = 0; step < 8; ++step) {
+    if (b + 1 >= n || pre[b + 1] > x) return b;
+    ++b;
+  }
+  return find_seq(pre, n, x);
 }
 
 struct TableArgs {
@@ -177,31 +221,45 @@ __global__ void __launch_bounds__(kTabThreads, 1) build_tables_kernel(const Tabl
     }
   }
   if (me == 0) *a.count_out = count - taken;
-  for (int k = me; k < taken; k += nt) {
-    const int b = find_seq(s_off, a.B, k);
-    const int blk = a.free_blocks[count - 1 - k];
-    if (blk < 0 || blk >= a.num_blocks) bits |= PD_DEVERR_BLOCK_ID;
-    const int held = (s_ctx[b] + a.bs - 1) / a.bs;
-    a.table[static_cast<long long>(b) * a.max_blocks + held + (k - s_off[b])] = blk;
+  {
+    int b = -1, blk[kBatch];
+    long long at[kBatch];
+    deal(taken, rank, ranks,
+         [&](int k, int j) {
+           b = next_seq(s_off, a.B, k, b);
+           blk[j] = a.free_blocks[count - 1 - k];
+           const int held = (s_ctx[b] + a.bs - 1) / a.bs;
+           at[j] = static_cast<long long>(b) * a.max_blocks + held + (k - s_off[b]);
+         },
+         [&](int, int j) {
+           if (blk[j] < 0 || blk[j] >= a.num_blocks) bits |= PD_DEVERR_BLOCK_ID;
+           a.table[at[j]] = blk[j];
+         });
   }
   const int live = min(s_start[a.B], a.T);
-  for (int k = me; k < a.T; k += nt) {
-    long long slot = -1;
-    int pos = 0;
-    if (k < live) {
-      const int b = find_seq(s_start, a.B, k);
-      const int c = s_ctx[b];
-      if (c >= 0) {
-        pos = c + (k - s_start[b]);
-        const int n = pos / a.bs, held = (c + a.bs - 1) / a.bs;
-        const int blk = n < held ? a.table[static_cast<long long>(b) * a.max_blocks + n]
-                                 : a.free_blocks[count - 1 - (s_off[b] + n - held)];
-        if (blk < 0 || blk >= a.num_blocks) bits |= PD_DEVERR_BLOCK_ID;
-        else slot = static_cast<long long>(blk) * a.bs + (pos - n * a.bs);
-      }
-    }
-    a.slots[k] = slot;
-    if (a.positions) a.positions[k] = pos;
+  {
+    int b = -1, blk[kBatch], pos[kBatch];
+    deal(a.T, rank, ranks,
+         [&](int k, int j) {
+           pos[j] = -1;
+           if (k >= live) return;
+           b = next_seq(s_start, a.B, k, b);
+           const int c = s_ctx[b];
+           if (c < 0) return;
+           pos[j] = c + (k - s_start[b]);
+           const int n = pos[j] / a.bs, held = (c + a.bs - 1) / a.bs;
+           blk[j] = n < held ? a.table[static_cast<long long>(b) * a.max_blocks + n]
+                             : a.free_blocks[count - 1 - (s_off[b] + n - held)];
+         },
+         [&](int k, int j) {
+           long long slot = -1;
+           if (pos[j] >= 0) {
+             if (blk[j] < 0 || blk[j] >= a.num_blocks) bits |= PD_DEVERR_BLOCK_ID;
+             else slot = static_cast<long long>(blk[j]) * a.bs + pos[j] % a.bs;
+           }
+           a.slots[k] = slot;
+           if (a.positions) a.positions[k] = max(pos[j], 0);
+         });
   }
   raise_bits(a.flag, bits);
 }
@@ -272,15 +330,19 @@ __global__ void __launch_bounds__(kTabThreads, 1) release_kernel(const ReleaseAr
   const int nt = ranks * kTabThreads, me = rank * kTabThreads + t;
   for (int b = me; b < a.B; b += nt) a.lens_out[b] = s_len[b];
   if (me == 0) *a.count_out = count + given;
-  for (int k = me; k < given; k += nt) {
-    const int b = find_seq(s_off, a.B, k);
-    int blk = a.table[static_cast<long long>(b) * a.max_blocks + (k - s_off[b])];
-    if (blk < 0 || blk >= a.num_blocks) {
-      bits |= PD_DEVERR_BLOCK_ID;
-      blk = -1;
-    }
-    a.free_blocks[count + k] = blk;
-  }
+  int b = -1, blk[kBatch];
+  deal(given, rank, ranks,
+       [&](int k, int j) {
+         b = next_seq(s_off, a.B, k, b);
+         blk[j] = a.table[static_cast<long long>(b) * a.max_blocks + (k - s_off[b])];
+       },
+       [&](int k, int j) {
+         if (blk[j] < 0 || blk[j] >= a.num_blocks) {
+           bits |= PD_DEVERR_BLOCK_ID;
+           blk[j] = -1;
+         }
+         a.free_blocks[count + k] = blk[j];
+       });
   raise_bits(a.flag, bits);
 }
 

@@ -11,21 +11,27 @@
 // The decode's structure is kept (decode_kernel.cuh: persistent CTAs over
 // balanced ranges of 16-key tiles, one TMA producer warp, a ring of
 // 128B-swizzled stages, S^T = K Q^T and O^T = V^T P^T with mma.sync, bounded
-// waits). What differs is what the two maps make possible: the two warps of a
-// head's pair split D in halves, and a half of a K row belongs to one map
-// only. So warp m scores map m over its whole contraction (no partial scores to
-// add) and runs that map's softmax alone; the pair then swaps its packed P
-// fragments and rescale factors through shared memory (16 bytes per lane and
-// row tile, one 64-thread barrier per tile) and each warp accumulates both
-// maps over its own half of V's dims. Every K and V byte is thus read from
+// waits). What differs is what the two maps make possible: a half of a K row
+// belongs to one map only, so the two maps' scores cost one pass over K, and
+// both maps' P meet the same V fragments: every K and V byte is read from
 // shared memory, and a one-byte code widened, once for both maps.
-// Each warp pair holds one to four tiles of 8 query rows per map (G * qlen <=
-// 32), dealt to RG row groups.
+//  * W = 1: a warp serves a head alone (both maps, all of V's dims): no
+//    exchange between warps at all. KT = 2 takes two tiles a step, which halves
+//    the shuffles and gives the tensor pipe independent chains.
+//  * W = 4 (more row tiles than one warp's registers hold): warp (map m, row
+//    group h) scores map m for its row tiles over that map's whole
+//    contraction (no partial scores to add), and the four swap their packed
+//    P fragments (8 bytes per lane, tile and row tile, one
+//    barrier per step); each warp accumulates both maps over a quarter of V's dims.
+//  * KG key groups of such warps take the ring's steps in turn and merge their
+//    (m, l, O) through shared memory at the end of a piece.
+// A tile is one box of a 4-D tensor map that puts keys before heads: a head's
+// 16 keys are 16 adjacent 128-byte rows of a slab and meet all eight swizzle
+// phases whatever the heads per tile.
 //
-// A unit covered by one piece is finished from the accumulators: the pair
-// exchanges row sums, takes the difference in fp32 and, with a norm, the sums
-// of squares. A split unit's pieces write fp32 (m, l, O) partials of both
-// maps, which diff_combine_kernel joins.
+// A unit covered by one piece is finished here, the difference and the norm in
+// fp32; a split unit's pieces write fp32 (m, l, O) partials of both maps, which
+// diff_combine_kernel joins.
 #pragma once
 #include <cuda_bf16.h>
 
@@ -41,39 +47,56 @@ struct DiffParams {
   float norm_eps, norm_gain;
 };
 
-template <int D_, int KV_, int NTM_, int RG_, int NS_, int MINB_, int HG_>
+template <int D_, int KV_, int NTM_, int HG_, int W_, int KG_, int KT_, int NS_, int MINB_>
 struct DiffCfg {
-  static constexpr int D = D_, KV = KV_, NTM = NTM_, RG = RG_, NS = NS_, HG = HG_;
+  static constexpr int D = D_, KV = KV_, NTM = NTM_, HG = HG_, W = W_, KG = KG_, KT = KT_, NS = NS_;
   static constexpr int kMinBlocks = MINB_;
   static constexpr bool BYTE = KV == kKvFp8 || KV == kKvInt8;
   static constexpr bool BF16 = KV == kKvBf16;  // bfloat16 operands; byte kinds use fp16 ones
   static constexpr int kElem = BYTE ? 1 : 2;
   static constexpr int kSlabElems = 128 / kElem;
   static constexpr int kSlabs = D / kSlabElems;
-  static constexpr int kSlabBytes = kTileKeys * HG * 128;  // [key][head][128 B]
+  static constexpr int kHeadBytes = kTileKeys * 128;  // one head's keys of a slab
+  static constexpr int kSlabBytes = HG * kHeadBytes;  // [head][key][128 B]
   static constexpr int kTileBytes = kSlabs * kSlabBytes;
   static constexpr int kStageBytes = 2 * kTileBytes;
-  static_assert(NTM % RG == 0, "row groups take equal shares of the row tiles");
-  static constexpr int NTW = NTM / RG;  // row tiles (per map) of a warp
-  static constexpr int kPairs = HG * RG;
-  static constexpr int kConsumerWarps = 2 * kPairs;
-  static constexpr int kThreads = kConsumerWarps * 32 + 32;
+  static constexpr int MPW = W == 1 ? 2 : 1;             // maps a warp scores
+  static constexpr int RG = W == 4 ? 2 : 1;              // row groups
+  static constexpr int NTR = (NTM + RG - 1) / RG;        // row tiles (per map) a warp scores
+  static constexpr int kGroupWarps = HG * W;             // warps of a key group
+  static constexpr int kConsumerWarps = kGroupWarps * KG;
+  static constexpr int kConsumerThreads = kConsumerWarps * 32;
+  // Eight consumer warps alone on an SM take the registers that the producer's
+  // warpgroup gives up (256 x 216 + 128 x 56 of the launch's 384 x 168).
+  static constexpr bool kSplitRegs = kConsumerWarps == 8 && MINB_ == 1;
+  static constexpr int kThreads = kConsumerThreads + (kSplitRegs ? 128 : 32);
   static constexpr int RM = NTM * 8;      // partial rows per map of a head
   static constexpr int RH = 2 * RM;       // per head
   static constexpr int RP = HG * RH;      // per unit
-  // a pair's exchange: two buffers of (own fragments of each map), and the
-  // epilogue's row sums
-  static constexpr int kXBuf = 32 * NTW * 16;  // one warp's 16 bytes per lane and row tile
-  static constexpr int kXPair = 2 * 2 * kXBuf + 2 * kXBuf;
-  static constexpr int kOffX = NS * kStageBytes;
-  static constexpr int kOffBars = kOffX + kPairs * kXPair;
+  static constexpr bool kMerge = KG > 1;                 // the epilogue goes through shared memory
+  static constexpr int kDP = D + 4;                      // merge row pitch (floats)
+  static constexpr int kMergeO = kMerge ? RP * kDP * 4 : 0;
+  static constexpr int kMergeML = kMerge ? KG * RP * 8 : 0;
+  // a head's exchange, double-buffered: packed P [map][row tile][lane], rescale
+  // factors [map][row tile][row], a flag per warp
+  static constexpr int kXTiles = 2 * RG * NTR;
+  static constexpr int kXP = kXTiles * 32 * 8 * KT;
+  static constexpr int kXOne = kXP + kXTiles * 8 * 4 + 16;
+  static constexpr int kXEnd = kXTiles * 8 * 4 + W * NTM * 8 * 4;  // row sums; sums of squares
+  static constexpr int kXHead = 2 * kXOne + (kMerge ? 0 : kXEnd);
+  static constexpr int kX = W > 1 ? HG * KG * kXHead : 0;
+  static constexpr int kOffMergeML = NS * kStageBytes + kMergeO;
+  static constexpr int kOffX = kOffMergeML + kMergeML;
+  static constexpr int kOffBars = kOffX + kX;
   static constexpr int kOffPre = kOffBars + 2 * NS * 8;
   static constexpr int kSmemBytes = (kOffPre + (kMaxAutoB + 1) * 4 + 15) / 16 * 16 + 1024;
-  static_assert(kPairs <= 14, "named barriers 2..");
+  // a stage always belongs to the same key group (see Cfg), which takes KT
+  // consecutive ring positions a step
+  static_assert(KG == 1 || NS % (KG * KT) == 0, "ring stages must be a multiple of the key groups' steps");
+  static_assert(KT == 1 || KT == 2, "one or two tiles a step");
+  static_assert(W == 1 || W == 4, "one or four warps per head");
+  static_assert(HG * KG <= 14, "named barriers 2.. serve the heads' warps");
 };
-
-// Output value of row sums: the difference of the two maps.
-__device__ __forceinline__ float diff_of(float o1, float o2, float inv1, float inv2l) { return o1 * inv1 - o2 * inv2l; }
 
 __device__ __forceinline__ float norm_weight_at(const DiffParams& p, int d) {
   if (p.norm_f32) return __ldg(static_cast<const float*>(p.norm_weight) + d);
@@ -81,8 +104,23 @@ __device__ __forceinline__ float norm_weight_at(const DiffParams& p, int d) {
   return p.d.out_bf16 ? __uint_as_float(static_cast<uint32_t>(w) << 16) : __half2float(__ushort_as_half(w));
 }
 
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+
 __device__ __forceinline__ uint32_t pack_out(bool bf16, float lo, float hi) {
   return bf16 ? pack_bf162(lo, hi) : pack_half2(lo, hi);
+}
+
+// Four dims d .. d + 3 of an output row, normalised by f where there is a norm.
+// (A zero row with eps = 0: rsqrt is infinite, the row stays zero.)
+__device__ __forceinline__ void store_row4(const DiffParams& p, uint16_t* dst, int d, float4 v, float f) {
+  if (p.norm_weight != nullptr) {
+    v.x = v.x == 0.f ? 0.f : v.x * f * norm_weight_at(p, d);
+    v.y = v.y == 0.f ? 0.f : v.y * f * norm_weight_at(p, d + 1);
+    v.z = v.z == 0.f ? 0.f : v.z * f * norm_weight_at(p, d + 2);
+    v.w = v.w == 0.f ? 0.f : v.w * f * norm_weight_at(p, d + 3);
+  }
+  const bool bf = p.d.out_bf16 != 0;
+  *reinterpret_cast<uint2*>(dst + d) = make_uint2(pack_out(bf, v.x, v.y), pack_out(bf, v.z, v.w));
 }
 
 template <class Cfg>
@@ -90,21 +128,23 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::kMinBlocks)
     decode_diff_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                        const DiffParams dp) {
   const DecodeParams& p = dp.d;
-  constexpr int D = Cfg::D, NS = Cfg::NS, HG = Cfg::HG, NTW = Cfg::NTW, RG = Cfg::RG;
+  constexpr int D = Cfg::D, NS = Cfg::NS, NTM = Cfg::NTM;
   constexpr bool BYTE = Cfg::BYTE, BF16 = Cfg::BF16;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Cfg::kOffBars);  // full[NS], empty[NS]
   int* s_pre = reinterpret_cast<int*>(smem + Cfg::kOffPre);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // (what a warp's branches depend on is broadcast, so that they compile to
+  // uniform ones without reconvergence around the matrix instructions)
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   const bool is_producer = warp == Cfg::kConsumerWarps;
   const uint32_t full0 = smem_u32(bars), empty0 = smem_u32(bars + NS);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < NS; ++s) {
       mbar_init(full0 + 8 * s, 1);
-      mbar_init(empty0 + 8 * s, Cfg::kConsumerWarps);
+      mbar_init(empty0 + 8 * s, Cfg::kGroupWarps);
     }
     fence_mbar_init();
   }
@@ -122,7 +162,19 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::kMinBlocks)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   Piece pc;
 
+  if constexpr (Cfg::kSplitRegs) {
+    if (warp < Cfg::kConsumerWarps) {
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    } else {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+      if (!is_producer) return;  // the rest of the producer's warpgroup
+    }
+  }
   if (is_producer) {
+    // One elected lane issues two copies a tile, K and V, each one box of the 4-D map
+    // (128 bytes, 16 keys, HG heads, all slabs): copies issued by several lanes
+    // are serialised, which at four to eight boxes a tile held the ring back.
+    // Each lane translates its own of the next 32 tiles.
     const uint64_t pol = l2_policy_evict_first();
     uint32_t q = 0, issued = 0;
     bool ok = true;
@@ -136,38 +188,33 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::kMinBlocks)
       };
       int cur = load_group(0);
       for (int t = 0; t < pc.ntiles; t += 32) {
-        const int nxt = (t + 32 < pc.ntiles) ? load_group(t + 32) : -1;
+        const int nxt = (t + 32 < pc.ntiles) ? load_group(t + 32) : 0;
         const int n = min(32, pc.ntiles - t);
+        if (cur < 0 || cur >= p.num_blocks) {
+          raise_error(p.error_flag, kErrBlockId);
+          cur = 0;
+        }
+        const int row0 = cur * p.block_size + ((pc.first_tile + t + lane) % p.tiles_per_block) * kTileKeys;
         for (int i = 0; i < n; ++i, ++q) {
-          int blk = __shfl_sync(0xffffffffu, cur, i);
-          if (blk < 0 || blk >= p.num_blocks) {
-            if (lane == 0) raise_error(p.error_flag, kErrBlockId);
-            blk = 0;
-          }
-          const int stage = q % NS;
-          const uint32_t fb = full0 + 8 * stage;
-          if (lane == 0) {
+          const int z = __shfl_sync(0xffffffffu, row0, i);
+          if (elect_one()) {
+            const int stage = q % NS;
+            const uint32_t fb = full0 + 8 * stage;
             if (ok && q >= NS) ok = mbar_wait(empty0 + 8 * stage, ((q / NS) - 1) & 1, p.timeout_ns);
             if (ok && p.inject == 1) ok = false;
-            if (ok) mbar_arrive_expect_tx(fb, Cfg::kStageBytes);
+            if (ok) {
+              mbar_arrive_expect_tx(fb, Cfg::kStageBytes);
+              const uint32_t dst = smem_u32(smem + stage * Cfg::kStageBytes);
+              tma_load_4d(dst, &tm_k, fb, 0, z, pc.kh, 0, pol);
+              tma_load_4d(dst + Cfg::kTileBytes, &tm_v, fb, 0, z, pc.kh, 0, pol);
+              issued = q + 1;
+            }
           }
-          ok = __shfl_sync(0xffffffffu, ok, 0);
-          if (!ok) continue;
-          if (lane < 2 * Cfg::kSlabs) {
-            const int tile = pc.first_tile + t + i;
-            const int z = blk * p.block_size + (tile % p.tiles_per_block) * kTileKeys;
-            const int sl = lane % Cfg::kSlabs;
-            const bool is_v = lane >= Cfg::kSlabs;
-            const uint32_t dst = smem_u32(smem + stage * Cfg::kStageBytes) + (is_v ? Cfg::kTileBytes : 0) +
-                                 sl * Cfg::kSlabBytes;
-            tma_load_3d(dst, is_v ? &tm_v : &tm_k, fb, sl * Cfg::kSlabElems, pc.kh, z, pol);
-          }
-          issued = q + 1;
         }
         cur = nxt;
       }
     }
-    if (lane == 0) {
+    if (elect_one()) {
       if (!ok) raise_error(p.error_flag, kErrTimeout);
       // every issued load lands before the CTA's shared memory is released
       const uint32_t first = issued > NS ? issued - NS : 0;
@@ -179,53 +226,85 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::kMinBlocks)
   }
 
   // -------------------------------------------------------------- consumers
-  const int map = warp & 1;                  // the map this warp scores; its half of V's dims
-  const int pair = warp >> 1, rg = pair % RG, th = pair / RG;
+  constexpr int W = Cfg::W, KG = Cfg::KG, KT = Cfg::KT, HG = Cfg::HG, MPW = Cfg::MPW, NTR = Cfg::NTR;
+  const int w = warp % W;                    // warp of the head: its 1 / W of V's dims
+  const int kg = (warp / W) % KG;            // key group
+  const int th = warp / (W * KG);            // head of the tile
+  const int map = w & 1, rt0 = (w >> 1) * NTR;  // W > 1: the map and first row tile it scores
   const int g = lane >> 2, t4 = lane & 3;
   constexpr int KSW = D / 32;                // k-steps of one map (D / 2 dims)
-  constexpr int MTW = D / 32;                // m-tiles of 16 output dims of this warp
-  uint8_t* xch = smem + Cfg::kOffX + pair * Cfg::kXPair;
-  float4* xend = reinterpret_cast<float4*>(xch + 4 * Cfg::kXBuf);  // [map][tile][lane] row sums
-  // One-byte tiles at D = 128: a map's half of a slab row is four 16-byte
-  // chunks, and the eight lanes of a shared-memory phase hold two rows of
-  // four; rows whose swizzle phases differ in their high bit use different
-  // halves of the banks, so lane row g stands for key (g & 1) * 4 + (g >> 1).
-  constexpr bool kPermute = BYTE && D == 128;
-  auto key_of = [](int r) { return kPermute ? (r & 1) * 4 + (r >> 1) : r; };
+  constexpr int MTW = D / 16 / W;            // m-tiles of 16 output dims of this warp
+  float* merge_o = reinterpret_cast<float*>(smem + NS * Cfg::kStageBytes);
+  float* merge_ml = reinterpret_cast<float*>(smem + Cfg::kOffMergeML);
+  const uint32_t smem0 = smem_u32(smem);
+  const uint32_t xch = smem0 + Cfg::kOffX + (th * KG + kg) * Cfg::kXHead;
+  // One-byte tiles: 16-byte chunk 4 s + t4 of a 64-dim super-step s. The eight
+  // lanes of a shared-memory phase hold two accumulator rows of four chunks, so
+  // rows 2i and 2i + 1 stand for keys whose swizzle phases differ by 4; and the
+  // four keys that a V read touches (rows 2 t4) differ in their phases' upper
+  // two bits: no bank conflict on either.
+  auto key_of = [](int r) { return BYTE ? static_cast<int>((0x37621540u >> (4 * r)) & 15u) : r; };
   const int kg0 = key_of(g);                 // key of accumulator row g (row g + 8: + 8)
-  uint32_t qf[KSW][NTW][2];
-  float o[2][MTW][NTW][4];                   // [own map, other map]
-  uint32_t q = 0;
+  // Per-lane offsets within a stage. 16-bit: the row that this lane addresses for
+  // ldmatrix (K; V transposed) with the swizzled chunk of k-step (m-tile) 0; that
+  // of step s is 32 s away by exclusive or, since the rows are 128-byte aligned.
+  // One-byte: row key_of(g) with chunk t4 of super-step 0 (64 s away by exclusive
+  // or); V's two keys (and those + 8) with the first chunk of the 32-dim group.
+  uint32_t k_off, v_off[2];
+  if constexpr (!BYTE) {
+    const int kk = lane & 15, kv = (lane & 7) + (lane >> 4) * 8;
+    k_off = th * Cfg::kHeadBytes + kk * 128 + (((lane >> 4) ^ (kk & 7)) << 4);
+    v_off[0] = Cfg::kTileBytes + th * Cfg::kHeadBytes + kv * 128 + ((((lane >> 3) & 1) ^ (kv & 7)) << 4);
+  } else {
+    k_off = th * Cfg::kHeadBytes + kg0 * 128 + ((t4 ^ (kg0 & 7)) << 4);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int kv = key_of(2 * t4 + i);
+      v_off[i] = Cfg::kTileBytes + th * Cfg::kHeadBytes + kv * 128 + (((g >> 2) ^ (kv & 7)) << 4) + ((4 * g) & 15);
+    }
+  }
+  // a negative score factor is taken as a positive one on -q; a factor of zero
+  // as one too small to matter, so that a masked score (-inf) stays -inf
+  const float sl2 = fmaxf(fabsf(p.sl2), 1e-30f);
+  const uint32_t flip = p.sl2 < 0.f ? 0x80008000u : 0u;
+  uint32_t qf[MPW][KSW][NTR][2];
+  float o[2][MTW][NTM][4];
+  uint32_t q = 0;                            // ring position of the piece's first tile
   bool ok = true;
 
-  while (work_next(p, s_pre, it, pc)) {
-    // ---- q fragments of this warp's map
-    float sl2r[NTW][2];
+  while (uniform(work_next(p, s_pre, it, pc))) {
+    const int ntiles = uniform(pc.ntiles), first_tile = uniform(pc.first_tile), seq_len = uniform(pc.L);
+    const int lo_all = uniform(pc.tile_lo_all), hi_all = uniform(pc.tile_hi_all);
+    // ---- q fragments of the rows and maps this warp scores
+    float sl2r[MPW][NTR][2];                 // score factors (log2 units), positive
+    int hi_r[NTR][2];                        // last visible key of a row
+    float m_r[MPW][NTR][2], l_r[MPW][NTR][2];  // reference maxima (scaled) and sums
 #pragma unroll
-    for (int n = 0; n < NTW; ++n) {
-      sl2r[n][0] = sl2r[n][1] = p.sl2;
-      const int r = (rg * NTW + n) * 8 + g;
+    for (int n = 0; n < NTR; ++n) {
+      const int r = (rt0 + n) * 8 + g;
       const __half* qrow = nullptr;
       if (r < pc.R && pc.ntiles > 0) {
         const int i = r / p.G, hl = r % p.G;
-        qrow = p.q + (static_cast<long long>(pc.q0 + i) * p.Hq + (pc.kh + th) * p.G + hl) * D + map * (D / 2);
+        qrow = p.q + (static_cast<long long>(pc.q0 + i) * p.Hq + (pc.kh + th) * p.G + hl) * D;
       }
 #pragma unroll
-      for (int ks = 0; ks < KSW; ++ks) {
-        int d0, d1;  // dims within the half
-        if constexpr (!BYTE) {
-          d0 = ks * 16 + 2 * t4;
-          d1 = d0 + 8;
-        } else if constexpr (D == 256) {
-          // super-step ss = ks / 4 of the half's slab: chunk 2 t4 + ss
-          d0 = 16 * (2 * t4 + (ks >> 2)) + 4 * (ks & 3);
-          d1 = d0 + 2;
-        } else {
-          d0 = 16 * t4 + 4 * ks;
-          d1 = d0 + 2;
+      for (int m = 0; m < MPW; ++m) {
+        sl2r[m][n][0] = sl2r[m][n][1] = sl2;
+        m_r[m][n][0] = m_r[m][n][1] = -INFINITY;
+        l_r[m][n][0] = l_r[m][n][1] = 0.f;
+        const int half = (W == 1 ? m : map) * (D / 2);
+#pragma unroll
+        for (int ks = 0; ks < KSW; ++ks) {
+          const int d0 = half + (BYTE ? 64 * (ks >> 2) + 16 * t4 + 4 * (ks & 3) : ks * 16 + 2 * t4);
+          const int d1 = d0 + (BYTE ? 2 : 8);
+          qf[m][ks][n][0] = qrow ? __ldg(reinterpret_cast<const uint32_t*>(qrow + d0)) ^ flip : 0u;
+          qf[m][ks][n][1] = qrow ? __ldg(reinterpret_cast<const uint32_t*>(qrow + d1)) ^ flip : 0u;
         }
-        qf[ks][n][0] = qrow ? __ldg(reinterpret_cast<const uint32_t*>(qrow + d0)) : 0u;
-        qf[ks][n][1] = qrow ? __ldg(reinterpret_cast<const uint32_t*>(qrow + d1)) : 0u;
+      }
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int rc = (rt0 + n) * 8 + 2 * t4 + c;
+        hi_r[n][c] = pc.L - pc.qlen + rc / p.G;  // (padded rows: q = 0, never written)
       }
     }
     if constexpr (BYTE) {
@@ -233,416 +312,645 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::kMinBlocks)
         // bfloat16 q over byte caches: the half row scaled by 2^e into fp16,
         // exactly; 2^-e joins the row's score factor
 #pragma unroll
-        for (int n = 0; n < NTW; ++n) {
-          float m = 0.f;
+        for (int m = 0; m < MPW; ++m)
 #pragma unroll
-          for (int ks = 0; ks < KSW; ++ks)
+          for (int n = 0; n < NTR; ++n) {
+            float mx = 0.f;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const uint32_t w = qf[ks][n][h];
-              m = fmaxf(m, fmaxf(fabsf(__uint_as_float(w << 16)), fabsf(__uint_as_float(w & 0xffff0000u))));
-            }
-          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-          const int e = q_row_exponent(m);
-          sl2r[n][0] = p.sl2 * pow2f(-__shfl_sync(0xffffffffu, e, 8 * t4));
-          sl2r[n][1] = p.sl2 * pow2f(-__shfl_sync(0xffffffffu, e, 8 * t4 + 4));
-          const float up = pow2f(e);
+            for (int ks = 0; ks < KSW; ++ks)
 #pragma unroll
-          for (int ks = 0; ks < KSW; ++ks)
+              for (int h = 0; h < 2; ++h) {
+                const uint32_t v = qf[m][ks][n][h];
+                mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(v << 16)), fabsf(__uint_as_float(v & 0xffff0000u))));
+              }
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+            const int e = q_row_exponent(mx);
+            sl2r[m][n][0] = fmaxf(sl2 * pow2f(-__shfl_sync(0xffffffffu, e, 8 * t4)), 0x1p-126f);
+            sl2r[m][n][1] = fmaxf(sl2 * pow2f(-__shfl_sync(0xffffffffu, e, 8 * t4 + 4)), 0x1p-126f);
+            const float up = pow2f(e);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const uint32_t w = qf[ks][n][h];
-              qf[ks][n][h] = pack_half2(__uint_as_float(w << 16) * up, __uint_as_float(w & 0xffff0000u) * up);
-            }
-        }
+            for (int ks = 0; ks < KSW; ++ks)
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const uint32_t v = qf[m][ks][n][h];
+                qf[m][ks][n][h] = pack_half2(__uint_as_float(v << 16) * up, __uint_as_float(v & 0xffff0000u) * up);
+              }
+          }
       }
     }
-    int lo_r[NTW][2], hi_r[NTW][2];
-    float m_r[NTW][2], l_r[NTW][2];
 #pragma unroll
-    for (int n = 0; n < NTW; ++n) {
+    for (int m = 0; m < 2; ++m)
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const int r = (rg * NTW + n) * 8 + 2 * t4 + c;
-        if (r < pc.R) {
-          const int pos = pc.L - pc.qlen + r / p.G;
-          hi_r[n][c] = pos;
-          lo_r[n][c] = (p.window > 0) ? max(0, pos - p.window + 1) : 0;
-        } else {
-          hi_r[n][c] = -1;
-          lo_r[n][c] = 0;
-        }
-        m_r[n][c] = -INFINITY;
-        l_r[n][c] = 0.f;
-      }
+      for (int mt = 0; mt < MTW; ++mt)
 #pragma unroll
-      for (int w = 0; w < 2; ++w)
-#pragma unroll
-        for (int mt = 0; mt < MTW; ++mt) o[w][mt][n][0] = o[w][mt][n][1] = o[w][mt][n][2] = o[w][mt][n][3] = 0.f;
-    }
+        for (int n = 0; n < NTM; ++n) o[m][mt][n][0] = o[m][mt][n][1] = o[m][mt][n][2] = o[m][mt][n][3] = 0.f;
 
-    for (int k = 0; k < pc.ntiles; ++k) {
-      const uint32_t qq = q + k;
-      const int stage = qq % NS;
-      if (ok) ok = mbar_wait(full0 + 8 * stage, (qq / NS) & 1, p.timeout_ns);
-      if (!ok) {
-        named_bar_sync(2 + pair, 64);  // keep the pair's barrier sequence
+    // ---- this key group's steps: KT ring positions each, dealt to the groups
+    // by ring position (a piece may start or end inside a step)
+    const int lead = KG > 1 && KT > 1 ? static_cast<int>(q % KT) : 0;
+    const uint32_t step0 = (q - lead) / KT;
+    for (int st = (kg - static_cast<int>(step0 % KG) + KG) % KG; st * KT - lead < ntiles; st += KG) {
+      const int k0 = st * KT - lead;
+      bool have[KT];
+      int tile[KT];  // a step's missing tile is its other one over again, masked: no branch splits the step
+#pragma unroll
+      for (int j = 0; j < KT; ++j) {
+        have[j] = k0 + j >= 0 && k0 + j < ntiles;
+        if (ok && have[j])
+          ok = __all_sync(0xffffffffu, mbar_wait(full0 + 8 * ((q + k0 + j) % NS), ((q + k0 + j) / NS) & 1, p.timeout_ns));
+      }
+#pragma unroll
+      for (int j = 0; j < KT; ++j) tile[j] = have[j] ? k0 + j : k0 + (KT - 1 - j);
+      if (!ok) {  // gave up: keep the head's barrier sequence
+        if constexpr (W > 1) named_bar_sync(2 + th * KG + kg, W * 32);
         continue;
       }
-      const uint32_t kb = smem_u32(smem + stage * Cfg::kStageBytes);
-      const uint32_t vb = kb + Cfg::kTileBytes;
-      const int key0 = (pc.first_tile + k) * kTileKeys;
-
-      // ---- S^T of this warp's map: 16 keys x 8 rows per row tile, over D / 2
-      float sa[NTW][4], sb[NTW][4];
+      uint32_t pf[KT][2][NTM][2];  // P^T fragments of both maps
+      float x[KT][MPW][NTR][4];    // raw scores
 #pragma unroll
-      for (int n = 0; n < NTW; ++n)
+      for (int j = 0; j < KT; ++j) {
+        // ---- S^T: 16 keys x 8 rows per row tile and map
+        const uint32_t ka = smem0 + ((q + tile[j]) % NS) * Cfg::kStageBytes + k_off;
+        float sa[MPW][NTR][4], sb[MPW][NTR][4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) sa[n][e] = sb[n][e] = 0.f;
-      if constexpr (!BYTE) {
-        const int key = (lane & 7) + ((lane >> 3) & 1) * 8;
-        const int srow = key * HG + th;
-        const uint32_t rowb = kb + srow * 128;
+        for (int m = 0; m < MPW; ++m)
 #pragma unroll
-        for (int ksl = 0; ksl < KSW; ++ksl) {
-          const int ks = map * KSW + ksl;
-          const int slab = ks >> 2, chunk = (ks & 3) * 2 + (lane >> 4);
-          uint32_t a[4];
-          ldsm_x4(rowb + slab * Cfg::kSlabBytes + ((chunk ^ (srow & 7)) << 4), a);
+          for (int n = 0; n < NTR; ++n)
 #pragma unroll
-          for (int n = 0; n < NTW; ++n) {
-            if (ksl & 1) mma_op<BF16>(sb[n], a, qf[ksl][n][0], qf[ksl][n][1]);
-            else mma_op<BF16>(sa[n], a, qf[ksl][n][0], qf[ksl][n][1]);
-          }
-        }
-      } else {
-        const int srow = kg0 * HG + th;
-        const uint32_t r0 = kb + srow * 128, r8 = kb + (srow + 8 * HG) * 128;
+            for (int e = 0; e < 4; ++e) sa[m][n][e] = sb[m][n][e] = 0.f;
+        if constexpr (!BYTE) {
+          // (KSW is 4 or 8: a map's k-steps start a slab)
 #pragma unroll
-        for (int sup = 0; sup < KSW / 4; ++sup) {
-          const int slab = D == 256 ? map : 0;
-          const int chunk = (D == 256 ? 2 * t4 + sup : 4 * map + t4) ^ (srow & 7);
-          uint4 w0, w8;
-          asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-                       : "=r"(w0.x), "=r"(w0.y), "=r"(w0.z), "=r"(w0.w)
-                       : "r"(r0 + slab * Cfg::kSlabBytes + (chunk << 4)));
-          asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-                       : "=r"(w8.x), "=r"(w8.y), "=r"(w8.z), "=r"(w8.w)
-                       : "r"(r8 + slab * Cfg::kSlabBytes + (chunk << 4)));
-          const uint32_t wa[4] = {w0.x, w0.y, w0.z, w0.w};
-          const uint32_t wb[4] = {w8.x, w8.y, w8.z, w8.w};
+          for (int m = 0; m < MPW; ++m) {
+            const uint32_t km = ka + (W == 1 ? m : map) * (KSW / 4) * Cfg::kSlabBytes;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int ksl = sup * 4 + j;
-            uint32_t a[4];
-            const uint32_t xa = byte_word_prep<Cfg::KV>(wa[j]), xb = byte_word_prep<Cfg::KV>(wb[j]);
-            a[0] = byte_pair_to_half2<Cfg::KV>(xa, false);
-            a[1] = byte_pair_to_half2<Cfg::KV>(xb, false);
-            a[2] = byte_pair_to_half2<Cfg::KV>(xa, true);
-            a[3] = byte_pair_to_half2<Cfg::KV>(xb, true);
+            for (int ksl = 0; ksl < KSW; ++ksl) {
+              uint32_t a[4];
+              ldsm_x4((km ^ ((ksl & 3) * 32)) + (ksl >> 2) * Cfg::kSlabBytes, a);
 #pragma unroll
-            for (int n = 0; n < NTW; ++n) {
-              if (j & 1) mma_op<BF16>(sb[n], a, qf[ksl][n][0], qf[ksl][n][1]);
-              else mma_op<BF16>(sa[n], a, qf[ksl][n][0], qf[ksl][n][1]);
+              for (int n = 0; n < NTR; ++n) {
+                if (NTM % Cfg::RG != 0 && n == NTR - 1 && rt0 + n >= NTM) continue;
+                if (ksl & 1) mma_op<BF16>(sb[m][n], a, qf[m][ksl][n][0], qf[m][ksl][n][1]);
+                else mma_op<BF16>(sa[m][n], a, qf[m][ksl][n][0], qf[m][ksl][n][1]);
+              }
             }
           }
-        }
-      }
-      // ---- mask and online softmax of this map; P rounded to the operands'
-      // 16-bit type (the sum l is of the unrounded exponentials)
-      uint32_t pf[2][NTW][2];  // [own, other] P^T fragments
-      float al[2][NTW][2];     // [own, other] rescale factors
-      const bool interior = key0 >= pc.tile_lo_all && key0 + kTileKeys - 1 <= pc.tile_hi_all;
-      uint4* buf = reinterpret_cast<uint4*>(xch + (qq & 1) * 2 * Cfg::kXBuf);  // [map][tile][lane]
-#pragma unroll
-      for (int n = 0; n < NTW; ++n) {
-        const int j0 = key0 + kg0, j1 = j0 + 8;
-        float x[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] = (sa[n][e] + sb[n][e]) * sl2r[n][e & 1];
-        if (interior) {
-          if (hi_r[n][0] < 0) x[0] = x[2] = -INFINITY;  // padded rows stay masked
-          if (hi_r[n][1] < 0) x[1] = x[3] = -INFINITY;
         } else {
-          if (!(j0 >= lo_r[n][0] && j0 <= hi_r[n][0])) x[0] = -INFINITY;
-          if (!(j0 >= lo_r[n][1] && j0 <= hi_r[n][1])) x[1] = -INFINITY;
-          if (!(j1 >= lo_r[n][0] && j1 <= hi_r[n][0])) x[2] = -INFINITY;
-          if (!(j1 >= lo_r[n][1] && j1 <= hi_r[n][1])) x[3] = -INFINITY;
-        }
-        float mx0 = fmaxf(x[0], x[2]), mx1 = fmaxf(x[1], x[3]);
 #pragma unroll
-        for (int off = 4; off < 32; off <<= 1) {
-          mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, off));
-          mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, off));
-        }
-        const float mn0 = fmaxf(m_r[n][0], mx0), mn1 = fmaxf(m_r[n][1], mx1);
-        const float base0 = (mn0 == -INFINITY) ? 0.f : mn0;
-        const float base1 = (mn1 == -INFINITY) ? 0.f : mn1;
-        al[0][n][0] = (m_r[n][0] == -INFINITY) ? 1.f : ex2(m_r[n][0] - base0);
-        al[0][n][1] = (m_r[n][1] == -INFINITY) ? 1.f : ex2(m_r[n][1] - base1);
-        const float p00 = ex2(x[0] - base0), p01 = ex2(x[1] - base1);
-        const float p10 = ex2(x[2] - base0), p11 = ex2(x[3] - base1);
-        m_r[n][0] = mn0;
-        m_r[n][1] = mn1;
-        l_r[n][0] = l_r[n][0] * al[0][n][0] + (p00 + p10);
-        l_r[n][1] = l_r[n][1] * al[0][n][1] + (p01 + p11);
-        pf[0][n][0] = movmatrix_trans(pack2<BF16>(p00, p01));
-        pf[0][n][1] = movmatrix_trans(pack2<BF16>(p10, p11));
-        buf[(map * NTW + n) * 32 + lane] = make_uint4(pf[0][n][0], pf[0][n][1], __float_as_uint(al[0][n][0]),
-                                                      __float_as_uint(al[0][n][1]));
-      }
-      named_bar_sync(2 + pair, 64);
-      bool rescale = false;
+          for (int m = 0; m < MPW; ++m)
 #pragma unroll
-      for (int n = 0; n < NTW; ++n) {
-        const uint4 w = buf[((map ^ 1) * NTW + n) * 32 + lane];
-        pf[1][n][0] = w.x;
-        pf[1][n][1] = w.y;
-        al[1][n][0] = __uint_as_float(w.z);
-        al[1][n][1] = __uint_as_float(w.w);
-        rescale |= al[0][n][0] != 1.f || al[0][n][1] != 1.f || al[1][n][0] != 1.f || al[1][n][1] != 1.f;
-      }
-      if (__any_sync(0xffffffffu, rescale)) {
+            for (int sup = 0; sup < KSW / 4; ++sup) {
+              // 64-dim super-steps: two a slab
+              const uint32_t half = static_cast<uint32_t>(W == 1 ? m : map);
+              const uint32_t at = D == 256 ? (ka ^ (sup * 64)) + half * Cfg::kSlabBytes : ka ^ (half * 64);
+              const uint4 w0 = lds_v4_tile(at), w8 = lds_v4_tile(at + 8 * 128);
+              const uint32_t wa[4] = {w0.x, w0.y, w0.z, w0.w};
+              const uint32_t wb[4] = {w8.x, w8.y, w8.z, w8.w};
 #pragma unroll
-        for (int w = 0; w < 2; ++w)
+              for (int i = 0; i < 4; ++i) {
+                const int ksl = sup * 4 + i;
+                uint32_t a[4];
+                const uint32_t xa = byte_word_prep<Cfg::KV>(wa[i]), xb = byte_word_prep<Cfg::KV>(wb[i]);
+                a[0] = byte_pair_to_half2<Cfg::KV>(xa, false);
+                a[1] = byte_pair_to_half2<Cfg::KV>(xb, false);
+                a[2] = byte_pair_to_half2<Cfg::KV>(xa, true);
+                a[3] = byte_pair_to_half2<Cfg::KV>(xb, true);
 #pragma unroll
-          for (int mt = 0; mt < MTW; ++mt)
-#pragma unroll
-            for (int n = 0; n < NTW; ++n) {
-              o[w][mt][n][0] *= al[w][n][0]; o[w][mt][n][1] *= al[w][n][1];
-              o[w][mt][n][2] *= al[w][n][0]; o[w][mt][n][3] *= al[w][n][1];
+                for (int n = 0; n < NTR; ++n) {
+                  if (NTM % Cfg::RG != 0 && n == NTR - 1 && rt0 + n >= NTM) continue;
+                  if (i & 1) mma_op<BF16>(sb[m][n], a, qf[m][ksl][n][0], qf[m][ksl][n][1]);
+                  else mma_op<BF16>(sa[m][n], a, qf[m][ksl][n][0], qf[m][ksl][n][1]);
+                }
+              }
             }
+        }
+        const int key0 = (first_tile + tile[j]) * kTileKeys;
+        const bool interior = have[j] && key0 >= lo_all && key0 + kTileKeys - 1 <= hi_all;
+        const int j0 = key0 + kg0, j1 = j0 + 8;
+#pragma unroll
+        for (int n = 0; n < NTR; ++n) {
+#pragma unroll
+          for (int m = 0; m < MPW; ++m)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[j][m][n][e] = sa[m][n][e] + sb[m][n][e];
+          if (!interior) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              const int hi = have[j] ? hi_r[n][c] : -1, lo = p.window > 0 ? hi - p.window + 1 : 0;
+#pragma unroll
+              for (int m = 0; m < MPW; ++m) {
+                if (j0 < lo || j0 > hi) x[j][m][n][c] = -INFINITY;
+                if (j1 < lo || j1 > hi) x[j][m][n][2 + c] = -INFINITY;
+              }
+            }
+          }
+        }
+      }
+      // ---- online softmax. P = 2^(x sl2 - m) is relative to a reference m that
+      // is raised to the running maximum only when a score passes it by more than
+      // 2^kLazy: P stays within the 16-bit operands' range (at most 2^kLazy), the
+      // result does not depend on m, and the common step needs no shuffle, no
+      // rescaling and, between warps, no factors.
+      constexpr float kLazy = 8.f;
+      bool raise = false;
+#pragma unroll
+      for (int m = 0; m < MPW; ++m)
+#pragma unroll
+        for (int n = 0; n < NTR; ++n)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            float mx = fmaxf(x[0][m][n][c], x[0][m][n][2 + c]);
+            if constexpr (KT > 1) mx = fmaxf(mx, fmaxf(x[KT - 1][m][n][c], x[KT - 1][m][n][2 + c]));
+            raise |= fmaf(mx, sl2r[m][n][c], -m_r[m][n][c]) > kLazy;  // (no key seen: m = -inf)
+          }
+      raise = __any_sync(0xffffffffu, raise);
+      const uint32_t xcur = xch + (static_cast<uint32_t>(st / KG) & 1u) * Cfg::kXOne;
+      const uint32_t xa = xcur + Cfg::kXP, flags = xa + Cfg::kXTiles * 32;
+      if (raise) {
+#pragma unroll
+        for (int m = 0; m < MPW; ++m)
+#pragma unroll
+          for (int n = 0; n < NTR; ++n) {
+            float al[2];
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              float mx = fmaxf(x[0][m][n][c], x[0][m][n][2 + c]);
+              if constexpr (KT > 1) mx = fmaxf(mx, fmaxf(x[KT - 1][m][n][c], x[KT - 1][m][n][2 + c]));
+#pragma unroll
+              for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+              const float old = m_r[m][n][c], mn = fmaxf(old, mx * sl2r[m][n][c]);
+              // nothing accumulated yet: O and l are zero, keep factor 1
+              al[c] = old == -INFINITY ? 1.f : ex2(old - mn);
+              m_r[m][n][c] = mn;
+              l_r[m][n][c] *= al[c];
+            }
+            if constexpr (W == 1) {
+#pragma unroll
+              for (int mt = 0; mt < MTW; ++mt) {
+                o[m][mt][n][0] *= al[0]; o[m][mt][n][1] *= al[1];
+                o[m][mt][n][2] *= al[0]; o[m][mt][n][3] *= al[1];
+              }
+            } else if (g == 0) {
+              sts_f2(xa + (map * Cfg::RG * NTR + rt0 + n) * 32 + 8 * t4, al[0], al[1]);
+            }
+          }
+      }
+      // P rounded to the operands' 16-bit type (tensor-core products), the sum
+      // l of the unrounded exponentials
+#pragma unroll
+      for (int m = 0; m < MPW; ++m)
+#pragma unroll
+        for (int n = 0; n < NTR; ++n) {
+          float nb[2];
+#pragma unroll
+          for (int c = 0; c < 2; ++c) nb[c] = m_r[m][n][c] == -INFINITY ? 0.f : -m_r[m][n][c];
+          uint32_t pk[KT][2];
+#pragma unroll
+          for (int j = 0; j < KT; ++j) {
+            const float p00 = ex2(fmaf(x[j][m][n][0], sl2r[m][n][0], nb[0]));
+            const float p01 = ex2(fmaf(x[j][m][n][1], sl2r[m][n][1], nb[1]));
+            const float p10 = ex2(fmaf(x[j][m][n][2], sl2r[m][n][0], nb[0]));
+            const float p11 = ex2(fmaf(x[j][m][n][3], sl2r[m][n][1], nb[1]));
+            l_r[m][n][0] += p00 + p10;
+            l_r[m][n][1] += p01 + p11;
+            pk[j][0] = movmatrix_trans(pack2<BF16>(p00, p01));
+            pk[j][1] = movmatrix_trans(pack2<BF16>(p10, p11));
+            if constexpr (W == 1) {
+              pf[j][m][n][0] = pk[j][0];
+              pf[j][m][n][1] = pk[j][1];
+            }
+          }
+          if constexpr (W > 1) {
+            const uint32_t at = xcur + ((map * Cfg::RG * NTR + rt0 + n) * 32 + lane) * 8 * KT;
+            if constexpr (KT == 1) sts_v2(at, pk[0][0], pk[0][1]);
+            else sts_v4(at, pk[0][0], pk[0][1], pk[KT - 1][0], pk[KT - 1][1]);
+          }
+        }
+      if constexpr (W > 1) {
+        if (lane == 0) sts_b32(flags + 4 * w, raise ? 1u : 0u);
+        named_bar_sync(2 + th * KG + kg, W * 32);
+        const uint4 fl = lds_v4(flags);
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+          for (int n = 0; n < NTM; ++n) {
+            const uint32_t at = xcur + ((m * Cfg::RG * NTR + n) * 32 + lane) * 8 * KT;
+            if constexpr (KT == 1) {
+              const uint2 v = lds_v2(at);
+              pf[0][m][n][0] = v.x;
+              pf[0][m][n][1] = v.y;
+            } else {
+              const uint4 v = lds_v4(at);
+              pf[0][m][n][0] = v.x;
+              pf[0][m][n][1] = v.y;
+              pf[KT - 1][m][n][0] = v.z;
+              pf[KT - 1][m][n][1] = v.w;
+            }
+          }
+        if (uniform(fl.x | fl.y | fl.z | fl.w)) {
+          const uint32_t of[4] = {fl.x, fl.y, fl.z, fl.w};
+#pragma unroll
+          for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int n = 0; n < NTM; ++n) {
+              if (of[(m + 2 * (n / NTR)) % W] == 0u) continue;
+              const float2 al = lds_f2(xa + (m * Cfg::RG * NTR + n) * 32 + 8 * t4);
+#pragma unroll
+              for (int mt = 0; mt < MTW; ++mt) {
+                o[m][mt][n][0] *= al.x; o[m][mt][n][1] *= al.y;
+                o[m][mt][n][2] *= al.x; o[m][mt][n][3] *= al.y;
+              }
+            }
+        }
       }
 
-      // ---- O^T += V^T P^T of both maps over this warp's half of the dims; V
-      // of keys at or past the sequence end is zeroed (its bits may be NaN)
-      const bool tail = key0 + kTileKeys > pc.L;
-      if constexpr (!BYTE) {
-        const int key = (lane & 7) + (lane >> 4) * 8;
-        const int srow = key * HG + th;
-        const uint32_t rowb = vb + srow * 128;
-        uint32_t vm01 = 0xffffffffu, vm23 = 0xffffffffu;
-        if (tail) {
-          const int k0 = key0 + 2 * t4;
-          vm01 = (k0 < pc.L ? 0x0000ffffu : 0u) | (k0 + 1 < pc.L ? 0xffff0000u : 0u);
-          vm23 = (k0 + 8 < pc.L ? 0x0000ffffu : 0u) | (k0 + 9 < pc.L ? 0xffff0000u : 0u);
-        }
+      // ---- O^T += V^T P^T of both maps over this warp's dims; V of keys at or
+      // past the sequence end is zeroed (its bits may be NaN)
 #pragma unroll
-        for (int mtl = 0; mtl < MTW; ++mtl) {
-          const int mt = map * MTW + mtl;
-          const int slab = mt >> 2, chunk = (mt & 3) * 2 + ((lane >> 3) & 1);
-          uint32_t a[4];
-          ldsm_x4_trans(rowb + slab * Cfg::kSlabBytes + ((chunk ^ (srow & 7)) << 4), a);
+      for (int j = 0; j < KT; ++j) {
+        const uint32_t stage = (q + tile[j]) % NS, sbase = smem0 + stage * Cfg::kStageBytes;
+        const int key0 = (first_tile + tile[j]) * kTileKeys;
+        const bool tail = key0 + kTileKeys > seq_len;
+        if constexpr (!BYTE) {
+          // this warp's m-tiles: a part of a slab's four, or whole slabs
+          const uint32_t va = (sbase + v_off[0] + (MTW >= 4 ? w * (MTW / 4) * Cfg::kSlabBytes : (w * MTW >> 2) * Cfg::kSlabBytes)) ^
+                              (MTW >= 4 ? 0 : (w * MTW & 3) * 32);
+          uint32_t vm01 = 0xffffffffu, vm23 = 0xffffffffu;
           if (tail) {
-            a[0] &= vm01; a[1] &= vm01; a[2] &= vm23; a[3] &= vm23;
+            const int kt = key0 + 2 * t4;
+            vm01 = (kt < seq_len ? 0x0000ffffu : 0u) | (kt + 1 < seq_len ? 0xffff0000u : 0u);
+            vm23 = (kt + 8 < seq_len ? 0x0000ffffu : 0u) | (kt + 9 < seq_len ? 0xffff0000u : 0u);
           }
 #pragma unroll
-          for (int w = 0; w < 2; ++w)
+          for (int mtl = 0; mtl < MTW; ++mtl) {
+            uint32_t a[4];
+            ldsm_x4_trans((va ^ ((mtl & 3) * 32)) + (mtl >> 2) * Cfg::kSlabBytes, a);
+            if (tail) {
+              a[0] &= vm01; a[1] &= vm01; a[2] &= vm23; a[3] &= vm23;
+            }
 #pragma unroll
-            for (int n = 0; n < NTW; ++n) mma_op<BF16>(o[w][mtl][n], a, pf[w][n][0], pf[w][n][1]);
-        }
-      } else {
-        const int kA = key_of(2 * t4), kB = key_of(2 * t4 + 1), kC = kA + 8, kD = kB + 8;
-        const int rA = kA * HG + th, rB = kB * HG + th, rC = kC * HG + th, rD = kD * HG + th;
+            for (int m = 0; m < 2; ++m)
 #pragma unroll
-        for (int pl = 0; pl < MTW / 2; ++pl) {
-          const int P32 = map * (MTW / 2) + pl;
-          const int slab = P32 >> 2;
-          const int chunk = (P32 & 3) * 2 + (g >> 2);
-          const int byte = (4 * g) & 15;
-          const uint32_t sb0 = vb + slab * Cfg::kSlabBytes + byte;
-          uint32_t wA, wB, wC, wD;
-          asm volatile("ld.shared.b32 %0, [%1];" : "=r"(wA) : "r"(sb0 + rA * 128 + ((chunk ^ (rA & 7)) << 4)));
-          asm volatile("ld.shared.b32 %0, [%1];" : "=r"(wB) : "r"(sb0 + rB * 128 + ((chunk ^ (rB & 7)) << 4)));
-          asm volatile("ld.shared.b32 %0, [%1];" : "=r"(wC) : "r"(sb0 + rC * 128 + ((chunk ^ (rC & 7)) << 4)));
-          asm volatile("ld.shared.b32 %0, [%1];" : "=r"(wD) : "r"(sb0 + rD * 128 + ((chunk ^ (rD & 7)) << 4)));
-          if (tail) {  // code 0 is the value 0 in both byte formats
-            if (key0 + kA >= pc.L) wA = 0u;
-            if (key0 + kB >= pc.L) wB = 0u;
-            if (key0 + kC >= pc.L) wC = 0u;
-            if (key0 + kD >= pc.L) wD = 0u;
+              for (int n = 0; n < NTM; ++n) mma_op<BF16>(o[m][mtl][n], a, pf[j][m][n][0], pf[j][m][n][1]);
           }
-          wA = byte_word_prep<Cfg::KV>(wA); wB = byte_word_prep<Cfg::KV>(wB);
-          wC = byte_word_prep<Cfg::KV>(wC); wD = byte_word_prep<Cfg::KV>(wD);
-          const uint32_t ab01 = prmt(wA, wB, 0x5140u), ab23 = prmt(wA, wB, 0x7362u);
-          const uint32_t cd01 = prmt(wC, wD, 0x5140u), cd23 = prmt(wC, wD, 0x7362u);
-          uint32_t a[4];
-          a[0] = byte_pair_to_half2<Cfg::KV>(ab01, false);
-          a[1] = byte_pair_to_half2<Cfg::KV>(ab01, true);
-          a[2] = byte_pair_to_half2<Cfg::KV>(cd01, false);
-          a[3] = byte_pair_to_half2<Cfg::KV>(cd01, true);
+        } else {
+          // 32-dim group P32: lane reads 4 codes at dims 32 P32 + 4 g of keys
+          // key_of(2 t4), key_of(2 t4 + 1) and those + 8; m-tile 2 P32 takes
+          // dims 4 g (row g) and 4 g + 1 (row g + 8), m-tile 2 P32 + 1 the next two
+          const int kA = key_of(2 * t4), kB = key_of(2 * t4 + 1), kC = kA + 8, kD = kB + 8;
 #pragma unroll
-          for (int w = 0; w < 2; ++w)
+          for (int pl = 0; pl < MTW / 2; ++pl) {
+            const int P32 = w * (MTW / 2) + pl;
+            const uint32_t x32 = (P32 & 3) * 32, slab = sbase + (P32 >> 2) * Cfg::kSlabBytes;
+            const uint32_t vA = slab + (v_off[0] ^ x32), vB = slab + (v_off[1] ^ x32);
+            uint32_t wA = lds_b32_tile(vA), wB = lds_b32_tile(vB);
+            uint32_t wC = lds_b32_tile(vA + 8 * 128), wD = lds_b32_tile(vB + 8 * 128);
+            if (tail) {  // code 0 is the value 0 in both byte formats
+              if (key0 + kA >= seq_len) wA = 0u;
+              if (key0 + kB >= seq_len) wB = 0u;
+              if (key0 + kC >= seq_len) wC = 0u;
+              if (key0 + kD >= seq_len) wD = 0u;
+            }
+            wA = byte_word_prep<Cfg::KV>(wA); wB = byte_word_prep<Cfg::KV>(wB);
+            wC = byte_word_prep<Cfg::KV>(wC); wD = byte_word_prep<Cfg::KV>(wD);
+            const uint32_t ab01 = prmt(wA, wB, 0x5140u), ab23 = prmt(wA, wB, 0x7362u);
+            const uint32_t cd01 = prmt(wC, wD, 0x5140u), cd23 = prmt(wC, wD, 0x7362u);
+            uint32_t a[4];
+            a[0] = byte_pair_to_half2<Cfg::KV>(ab01, false);
+            a[1] = byte_pair_to_half2<Cfg::KV>(ab01, true);
+            a[2] = byte_pair_to_half2<Cfg::KV>(cd01, false);
+            a[3] = byte_pair_to_half2<Cfg::KV>(cd01, true);
 #pragma unroll
-            for (int n = 0; n < NTW; ++n) mma_op<BF16>(o[w][2 * pl][n], a, pf[w][n][0], pf[w][n][1]);
-          a[0] = byte_pair_to_half2<Cfg::KV>(ab23, false);
-          a[1] = byte_pair_to_half2<Cfg::KV>(ab23, true);
-          a[2] = byte_pair_to_half2<Cfg::KV>(cd23, false);
-          a[3] = byte_pair_to_half2<Cfg::KV>(cd23, true);
+            for (int m = 0; m < 2; ++m)
 #pragma unroll
-          for (int w = 0; w < 2; ++w)
+              for (int n = 0; n < NTM; ++n) mma_op<BF16>(o[m][2 * pl][n], a, pf[j][m][n][0], pf[j][m][n][1]);
+            a[0] = byte_pair_to_half2<Cfg::KV>(ab23, false);
+            a[1] = byte_pair_to_half2<Cfg::KV>(ab23, true);
+            a[2] = byte_pair_to_half2<Cfg::KV>(cd23, false);
+            a[3] = byte_pair_to_half2<Cfg::KV>(cd23, true);
 #pragma unroll
-            for (int n = 0; n < NTW; ++n) mma_op<BF16>(o[w][2 * pl + 1][n], a, pf[w][n][0], pf[w][n][1]);
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+              for (int n = 0; n < NTM; ++n) mma_op<BF16>(o[m][2 * pl + 1][n], a, pf[j][m][n][0], pf[j][m][n][1]);
+          }
         }
+        __syncwarp();
+        // (a stage taken twice is given back after the second time)
+        if (lane == 0 && (j == KT - 1 || (have[0] && have[KT - 1]))) mbar_arrive(empty0 + 8 * stage);
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(empty0 + 8 * stage);
     }
-    q += pc.ntiles;
+    q += ntiles;
 
     // ---- end of the piece: row sums over the lanes of each row
 #pragma unroll
-    for (int n = 0; n < NTW; ++n)
+    for (int m = 0; m < MPW; ++m)
 #pragma unroll
-      for (int off = 4; off < 32; off <<= 1) {
-        l_r[n][0] += __shfl_xor_sync(0xffffffffu, l_r[n][0], off);
-        l_r[n][1] += __shfl_xor_sync(0xffffffffu, l_r[n][1], off);
-      }
+      for (int n = 0; n < NTR; ++n)
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1) {
+          l_r[m][n][0] += __shfl_xor_sync(0xffffffffu, l_r[m][n][0], off);
+          l_r[m][n][1] += __shfl_xor_sync(0xffffffffu, l_r[m][n][1], off);
+        }
     // output dims of accumulator registers e = 0/1 and 2/3 of m-tile mtl
     auto dim0 = [&](int mtl) {
-      const int mt = map * MTW + mtl;
+      const int mt = w * MTW + mtl;
       return BYTE ? (mt >> 1) * 32 + 4 * g + 2 * (mt & 1) : mt * 16 + g;
     };
     constexpr int kStep = BYTE ? 1 : 8;
-    if (pc.npieces > 1) {
+    const bool direct = pc.npieces == 1;
+
+    if constexpr (!Cfg::kMerge) {
+      // straight from the accumulators
+      if (!direct) {
 #pragma unroll
-      for (int n = 0; n < NTW; ++n)
+        for (int n = 0; n < NTM; ++n)
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const int r = (rg * NTW + n) * 8 + 2 * t4 + c;
-          if (r >= pc.R) continue;
+          for (int c = 0; c < 2; ++c) {
+            const int r = n * 8 + 2 * t4 + c;
+            if (r >= pc.R) continue;
 #pragma unroll
-          for (int w = 0; w < 2; ++w) {
-            const long long prow = static_cast<long long>(pc.slot) * Cfg::RP + th * Cfg::RH + (map ^ w) * Cfg::RM + r;
-            float* dst = p.ws_o + prow * D;
+            for (int m = 0; m < 2; ++m) {
+              const long long prow = static_cast<long long>(pc.slot) * Cfg::RP + th * Cfg::RH + m * Cfg::RM + r;
+              float* dst = p.ws_o + prow * D;
 #pragma unroll
-            for (int mtl = 0; mtl < MTW; ++mtl) {
-              const int d0 = dim0(mtl);
-              if constexpr (BYTE) {
-                __stcg(reinterpret_cast<float2*>(dst + d0), make_float2(o[w][mtl][n][c], o[w][mtl][n][2 + c]));
-              } else {
-                __stcg(dst + d0, o[w][mtl][n][c]);
-                __stcg(dst + d0 + 8, o[w][mtl][n][2 + c]);
+              for (int mtl = 0; mtl < MTW; ++mtl) {
+                const int d0 = dim0(mtl);
+                if constexpr (BYTE) {
+                  __stcg(reinterpret_cast<float2*>(dst + d0), make_float2(o[m][mtl][n][c], o[m][mtl][n][2 + c]));
+                } else {
+                  __stcg(dst + d0, o[m][mtl][n][c]);
+                  __stcg(dst + d0 + 8, o[m][mtl][n][2 + c]);
+                }
               }
             }
-            if (w == 0 && g == 0)
-              __stcg(reinterpret_cast<float2*>(p.ws_ml + prow * 2), make_float2(m_r[n][c], l_r[n][c]));
+          }
+        if (g == 0) {  // the maxima and sums of the rows this warp scored
+#pragma unroll
+          for (int m = 0; m < MPW; ++m)
+#pragma unroll
+            for (int n = 0; n < NTR; ++n)
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
+                const int r = (rt0 + n) * 8 + 2 * t4 + c;
+                const long long prow =
+                    static_cast<long long>(pc.slot) * Cfg::RP + th * Cfg::RH + (W == 1 ? m : map) * Cfg::RM + r;
+                if (r < pc.R)
+                  __stcg(reinterpret_cast<float2*>(p.ws_ml + prow * 2), make_float2(m_r[m][n][c], l_r[m][n][c]));
+              }
+        }
+        continue;
+      }
+      // the whole unit: row sums of both maps, the difference, the norm. The
+      // warps of a head swap sums; the buffers' last readers are a tile's
+      // barrier back, and a piece without tiles (all sums zero) swaps nothing.
+      const uint32_t xl = xch + 2 * Cfg::kXOne, xs = xl + Cfg::kXTiles * 32;
+      float l_map[2][NTM][2];
+      if constexpr (W > 1) {
+        if (g == 0) {
+#pragma unroll
+          for (int n = 0; n < NTR; ++n)
+            sts_f2(xl + (map * Cfg::RG * NTR + rt0 + n) * 32 + 8 * t4, l_r[0][n][0], l_r[0][n][1]);
+        }
+        if (pc.ntiles > 0) named_bar_sync(2 + th * KG + kg, W * 32);
+      }
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int n = 0; n < NTM; ++n) {
+          if constexpr (W == 1) {
+            l_map[m][n][0] = l_r[m % MPW][n % NTR][0];
+            l_map[m][n][1] = l_r[m % MPW][n % NTR][1];
+          } else {
+            float2 v = make_float2(0.f, 0.f);
+            if (ntiles > 0) v = lds_f2(xl + (m * Cfg::RG * NTR + n) * 32 + 8 * t4);
+            l_map[m][n][0] = v.x;
+            l_map[m][n][1] = v.y;
           }
         }
-      continue;
-    }
-    // ---- the whole unit: swap row sums, take the difference, normalise. A
-    // piece with tiles had a barrier per tile after the last use of xend; one
-    // without has all sums zero and swaps nothing.
-    float lo_sum[NTW][2];  // the other map's row sums
+      float ss[NTM][2];
 #pragma unroll
-    for (int n = 0; n < NTW; ++n) lo_sum[n][0] = lo_sum[n][1] = 0.f;
-    if (pc.ntiles > 0) {
-#pragma unroll
-      for (int n = 0; n < NTW; ++n) xend[(map * NTW + n) * 32 + lane] = make_float4(l_r[n][0], l_r[n][1], 0.f, 0.f);
-      named_bar_sync(2 + pair, 64);
-#pragma unroll
-      for (int n = 0; n < NTW; ++n) {
-        const float4 w = xend[((map ^ 1) * NTW + n) * 32 + lane];
-        lo_sum[n][0] = w.x;
-        lo_sum[n][1] = w.y;
-      }
-    }
-    float ss[NTW][2];
-#pragma unroll
-    for (int n = 0; n < NTW; ++n)
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        ss[n][c] = 0.f;
-        const int r = (rg * NTW + n) * 8 + 2 * t4 + c;
-        const float l1 = map == 0 ? l_r[n][c] : lo_sum[n][c], l2 = map == 0 ? lo_sum[n][c] : l_r[n][c];
-        const float lam = r < pc.R ? __ldg(dp.lambda + (pc.kh + th) * p.G + r % p.G) : 0.f;
-        const float inv1 = l1 > 0.f ? p.out_scale / l1 : 0.f;
-        const float inv2 = l2 > 0.f ? p.out_scale / l2 * lam : 0.f;
-#pragma unroll
-        for (int mtl = 0; mtl < MTW; ++mtl)
-#pragma unroll
-          for (int e = c; e < 4; e += 2) {
-            const float own = o[0][mtl][n][e], other = o[1][mtl][n][e];
-            const float v = map == 0 ? diff_of(own, other, inv1, inv2) : diff_of(other, own, inv1, inv2);
-            o[0][mtl][n][e] = v;
-            ss[n][c] += v * v;
-          }
-      }
-    float f[NTW][2];
-#pragma unroll
-    for (int n = 0; n < NTW; ++n) f[n][0] = f[n][1] = 1.f;
-    if (dp.norm_weight != nullptr) {
-#pragma unroll
-      for (int n = 0; n < NTW; ++n)
-#pragma unroll
-        for (int off = 4; off < 32; off <<= 1) {
-          ss[n][0] += __shfl_xor_sync(0xffffffffu, ss[n][0], off);
-          ss[n][1] += __shfl_xor_sync(0xffffffffu, ss[n][1], off);
-        }
-      if (pc.ntiles > 0) {
-        named_bar_sync(2 + pair, 64);  // xend has been read
-#pragma unroll
-        for (int n = 0; n < NTW; ++n) xend[(map * NTW + n) * 32 + lane] = make_float4(ss[n][0], ss[n][1], 0.f, 0.f);
-        named_bar_sync(2 + pair, 64);
-#pragma unroll
-        for (int n = 0; n < NTW; ++n) {
-          const float4 w = xend[((map ^ 1) * NTW + n) * 32 + lane];
-          ss[n][0] += w.x;
-          ss[n][1] += w.y;
-        }
-      }
-#pragma unroll
-      for (int n = 0; n < NTW; ++n)
-#pragma unroll
-        for (int c = 0; c < 2; ++c) f[n][c] = rsqrtf(ss[n][c] / static_cast<float>(D) + dp.norm_eps) * dp.norm_gain;
-    }
-#pragma unroll
-    for (int mtl = 0; mtl < MTW; ++mtl) {
-      const int d0 = dim0(mtl);
-      float w0 = 1.f, w1 = 1.f;
-      if (dp.norm_weight != nullptr) {
-        w0 = norm_weight_at(dp, d0);
-        w1 = norm_weight_at(dp, d0 + kStep);
-      }
-#pragma unroll
-      for (int n = 0; n < NTW; ++n)
+      for (int n = 0; n < NTM; ++n)
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          const int r = (rg * NTW + n) * 8 + 2 * t4 + c;
-          if (r >= pc.R) continue;
-          uint16_t* dst = reinterpret_cast<uint16_t*>(p.out) +
-                          (static_cast<long long>(pc.q0 + r / p.G) * p.Hq + (pc.kh + th) * p.G + r % p.G) * D;
-          // (a zero row with eps = 0: rsqrt is infinite, the row stays zero)
-          const float a = o[0][mtl][n][c], b = o[0][mtl][n][2 + c];
-          const uint32_t v = pack_out(p.out_bf16 != 0, a == 0.f ? 0.f : a * f[n][c] * w0, b == 0.f ? 0.f : b * f[n][c] * w1);
-          if constexpr (BYTE) {
-            *reinterpret_cast<uint32_t*>(dst + d0) = v;
-          } else {
-            dst[d0] = static_cast<uint16_t>(v & 0xffffu);
-            dst[d0 + kStep] = static_cast<uint16_t>(v >> 16);
+          const int r = n * 8 + 2 * t4 + c;
+          const float lam = r < pc.R ? __ldg(dp.lambda + (pc.kh + th) * p.G + r % p.G) : 0.f;
+          const float inv1 = l_map[0][n][c] > 0.f ? p.out_scale / l_map[0][n][c] : 0.f;
+          const float inv2 = l_map[1][n][c] > 0.f ? p.out_scale / l_map[1][n][c] * lam : 0.f;
+          float s = 0.f;
+#pragma unroll
+          for (int mtl = 0; mtl < MTW; ++mtl)
+#pragma unroll
+            for (int e = c; e < 4; e += 2) {
+              const float v = o[0][mtl][n][e] * inv1 - o[1][mtl][n][e] * inv2;
+              o[0][mtl][n][e] = v;
+              s += v * v;
+            }
+          ss[n][c] = s;
+        }
+      if (dp.norm_weight != nullptr) {
+#pragma unroll
+        for (int n = 0; n < NTM; ++n) {
+#pragma unroll
+          for (int off = 4; off < 32; off <<= 1) {
+            ss[n][0] += __shfl_xor_sync(0xffffffffu, ss[n][0], off);
+            ss[n][1] += __shfl_xor_sync(0xffffffffu, ss[n][1], off);
+          }
+          if (W > 1 && g == 0)
+            sts_f2(xs + (w * NTM + n) * 32 + 8 * t4, ss[n][0], ss[n][1]);
+        }
+        if constexpr (W > 1) {
+          if (pc.ntiles > 0) named_bar_sync(2 + th * KG + kg, W * 32);
+#pragma unroll
+          for (int n = 0; n < NTM; ++n) {
+            float2 s = make_float2(0.f, 0.f);
+            if (pc.ntiles > 0) {
+#pragma unroll
+              for (int ww = 0; ww < W; ++ww) {
+                const float2 v = lds_f2(xs + (ww * NTM + n) * 32 + 8 * t4);
+                s.x += v.x;
+                s.y += v.y;
+              }
+            }
+            ss[n][0] = s.x;
+            ss[n][1] = s.y;
           }
         }
+      }
+#pragma unroll
+      for (int n = 0; n < NTM; ++n)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int r = n * 8 + 2 * t4 + c;
+          if (r >= pc.R) continue;
+          const float f = rsqrtf(ss[n][c] / static_cast<float>(D) + dp.norm_eps) * dp.norm_gain;
+          uint16_t* dst = reinterpret_cast<uint16_t*>(p.out) +
+                          (static_cast<long long>(pc.q0 + r / p.G) * p.Hq + (pc.kh + th) * p.G + r % p.G) * D;
+#pragma unroll
+          for (int mtl = 0; mtl < MTW; ++mtl) {
+            const int d0 = dim0(mtl);
+            float a = o[0][mtl][n][c], b = o[0][mtl][n][2 + c];
+            if (dp.norm_weight != nullptr) {
+              // (a zero row with eps = 0: rsqrt is infinite, the row stays zero)
+              a = a == 0.f ? 0.f : a * f * norm_weight_at(dp, d0);
+              b = b == 0.f ? 0.f : b * f * norm_weight_at(dp, d0 + kStep);
+            }
+            const uint32_t v = pack_out(p.out_bf16 != 0, a, b);
+            if constexpr (BYTE) {
+              *reinterpret_cast<uint32_t*>(dst + d0) = v;
+            } else {
+              dst[d0] = static_cast<uint16_t>(v & 0xffffu);
+              dst[d0 + kStep] = static_cast<uint16_t>(v >> 16);
+            }
+          }
+        }
+    } else {
+      // ---- through shared memory: rows [head][map][row], a row's key groups
+      // weighted by 2^(m - max m) and added in group order
+      if (g == 0) {
+#pragma unroll
+        for (int m = 0; m < MPW; ++m)
+#pragma unroll
+          for (int n = 0; n < NTR; ++n) {
+            if (rt0 + n >= NTM) continue;
+            float* ml = merge_ml + (kg * Cfg::RP + th * Cfg::RH + (W == 1 ? m : map) * Cfg::RM + (rt0 + n) * 8 + 2 * t4) * 2;
+            ml[0] = m_r[m][n][0];
+            ml[1] = l_r[m][n][0];
+            ml[2] = m_r[m][n][1];
+            ml[3] = l_r[m][n][1];
+          }
+      }
+      named_bar_sync(1, Cfg::kConsumerThreads);
+#pragma unroll 1
+      for (int k = 0; k < KG; ++k) {
+        if (kg == k) {
+#pragma unroll
+          for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int n = 0; n < NTM; ++n)
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
+                const int row = th * Cfg::RH + m * Cfg::RM + n * 8 + 2 * t4 + c;
+                float M = -INFINITY;
+#pragma unroll
+                for (int kk = 0; kk < KG; ++kk) M = fmaxf(M, merge_ml[(kk * Cfg::RP + row) * 2]);
+                const float mk = merge_ml[(k * Cfg::RP + row) * 2];
+                const float f = mk == -INFINITY ? 0.f : ex2(mk - M);
+                float* mo = merge_o + row * Cfg::kDP;
+#pragma unroll
+                for (int mtl = 0; mtl < MTW; ++mtl) {
+                  const int d0 = dim0(mtl);
+                  const float a = f * o[m][mtl][n][c], b = f * o[m][mtl][n][2 + c];
+                  if (k == 0) {
+                    mo[d0] = a;
+                    mo[d0 + kStep] = b;
+                  } else {
+                    mo[d0] += a;
+                    mo[d0 + kStep] += b;
+                  }
+                }
+              }
+        }
+        named_bar_sync(1, Cfg::kConsumerThreads);
+      }
+      auto row_ml = [&](int row, float& M, float& L) {
+        M = -INFINITY;
+        L = 0.f;
+#pragma unroll
+        for (int k = 0; k < KG; ++k) M = fmaxf(M, merge_ml[(k * Cfg::RP + row) * 2]);
+#pragma unroll
+        for (int k = 0; k < KG; ++k) {
+          const float mk = merge_ml[(k * Cfg::RP + row) * 2];
+          if (mk != -INFINITY) L += ex2(mk - M) * merge_ml[(k * Cfg::RP + row) * 2 + 1];
+        }
+      };
+      constexpr int V4 = D / 128;  // float4 groups per lane of a row
+      // a warp per row: (head, map, row) partials, or (head, row) results
+      const int rows = HG * pc.R * (direct ? 1 : 2);
+      for (int i = warp; i < rows; i += Cfg::kConsumerWarps) {
+        const int r = i % pc.R;
+        if (!direct) {
+          const int row = i / pc.R / 2 * Cfg::RH + (i / pc.R & 1) * Cfg::RM + r;
+          float M, L;
+          row_ml(row, M, L);
+          const long long prow = static_cast<long long>(pc.slot) * Cfg::RP + row;
+#pragma unroll
+          for (int v = 0; v < V4; ++v)
+            __stcg(reinterpret_cast<float4*>(p.ws_o + prow * D) + v * 32 + lane,
+                   *(reinterpret_cast<const float4*>(merge_o + row * Cfg::kDP) + v * 32 + lane));
+          if (lane == 0) __stcg(reinterpret_cast<float2*>(p.ws_ml + prow * 2), make_float2(M, L));
+        } else {
+          const int hh = i / pc.R, row1 = hh * Cfg::RH + r, row2 = row1 + Cfg::RM;
+          float M, l1, l2;
+          row_ml(row1, M, l1);
+          row_ml(row2, M, l2);
+          const int head = (pc.kh + hh) * p.G + r % p.G;
+          const float inv1 = l1 > 0.f ? p.out_scale / l1 : 0.f;
+          const float inv2 = l2 > 0.f ? p.out_scale / l2 * __ldg(dp.lambda + head) : 0.f;
+          float4 y[V4];
+          float ss = 0.f;
+#pragma unroll
+          for (int v = 0; v < V4; ++v) {
+            const float4 a = *(reinterpret_cast<const float4*>(merge_o + row1 * Cfg::kDP) + v * 32 + lane);
+            const float4 b = *(reinterpret_cast<const float4*>(merge_o + row2 * Cfg::kDP) + v * 32 + lane);
+            y[v] = make_float4(a.x * inv1 - b.x * inv2, a.y * inv1 - b.y * inv2, a.z * inv1 - b.z * inv2,
+                               a.w * inv1 - b.w * inv2);
+            ss += y[v].x * y[v].x + y[v].y * y[v].y + y[v].z * y[v].z + y[v].w * y[v].w;
+          }
+          float f = 1.f;
+          if (dp.norm_weight != nullptr) {
+#pragma unroll
+            for (int off = 16; off >= 1; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
+            f = rsqrtf(ss / static_cast<float>(D) + dp.norm_eps) * dp.norm_gain;
+          }
+          uint16_t* dst = reinterpret_cast<uint16_t*>(p.out) + (static_cast<long long>(pc.q0 + r / p.G) * p.Hq + head) * D;
+#pragma unroll
+          for (int v = 0; v < V4; ++v) store_row4(dp, dst, 4 * (v * 32 + lane), y[v], f);
+        }
+      }
+      named_bar_sync(1, Cfg::kConsumerThreads);  // the merge buffers are free again
     }
   }
   if (!ok && lane == 0) raise_error(p.error_flag, kErrTimeout);
 }
 
 // ---------------------------------------------------------------------------
-// Joins the partials of every split unit (unit_layout, merge_pieces), takes the
-// difference of the two maps and, with a norm, normalises the row.
-//   grid (units, row chunks, heads per tile), NT threads. A row's items are its
-//   2 maps x D / 4 groups of four dims; RB rows are taken at a time with PG =
-//   NT / (RB * items) threads per item, which share the item's pieces (pg, pg +
-//   PG, ...) and are joined in pg order, so the result does not depend on
-//   scheduling.
-template <int D, int NB, int NT>
-__global__ void __launch_bounds__(NT) diff_combine_kernel(const DiffParams dp, int RB) {
+// Joins the partials of every split unit, takes the difference of the two maps
+// and, with a norm, normalises the row.
+//   grid (units, row chunks, heads per tile), NT threads. A thread holds four
+//   dims of one row for MPT maps; RB rows are taken at a time with PG = NT /
+//   (RB * (D / 4) * 2 / MPT) threads per item, which share the item's pieces
+//   (pg, pg + PG, ...) and are joined in pg order, so the result does not depend
+//   on scheduling. Few pieces: both maps in a thread, whose difference is then
+//   its own; many: a map each, so that twice the threads share them. What does
+//   not come from the decode kernel (the unit's layout, lambda, the norm's
+//   weights) is read before the wait for it: the CTA is small enough to sit
+//   beside the decode's.
+constexpr int kJoinThreads = 384, kJoinThreadsMany = 1024;
+
+struct JoinState {
+  float m, l;
+  float4 o;
+};
+// Adds a partial (m, l, O) to a state.
+__device__ __forceinline__ void join_add(JoinState& s, float2 ml, float4 o) {
+  if (ml.x == -INFINITY) return;
+  if (ml.x > s.m) {
+    const float f = s.m == -INFINITY ? 0.f : ex2(s.m - ml.x);
+    s.l *= f;
+    s.o.x *= f; s.o.y *= f; s.o.z *= f; s.o.w *= f;
+    s.m = ml.x;
+  }
+  const float w = ex2(ml.x - s.m);
+  s.l += w * ml.y;
+  s.o.x += w * o.x; s.o.y += w * o.y; s.o.z += w * o.z; s.o.w += w * o.w;
+}
+
+template <int D, int NT, int MPT>
+__global__ void __launch_bounds__(NT, NT <= 384 ? 2 : 1) diff_combine_kernel(const DiffParams dp, int RB) {
   const DecodeParams& p = dp.d;
-  constexpr int S4 = D / 4, ITEMS = 2 * S4;
-  __shared__ float s_m[NT], s_l[NT];
-  __shared__ float4 s_o[NT];
+  constexpr int S4 = D / 4, NB = MPT == 2 ? 3 : 4;
+  __shared__ JoinState s_st[MPT][NT];
   __shared__ float s_ss[NT / 32];
   __shared__ long long s_red[2][NT / 32];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -654,77 +962,96 @@ __global__ void __launch_bounds__(NT) diff_combine_kernel(const DiffParams dp, i
   int q0, qn;
   seq_queries(p, b, false, q0, qn);
   const int kh = (u % p.hgn) * p.hg + blockIdx.z;
-  const int rbase = blockIdx.z * p.rows_head, rmap = p.rows_head / 2;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (P <= 1) return;
   const int live = p.G * qn;
   const int chunk = (live + gridDim.y - 1) / gridDim.y;
   const int r_begin = blockIdx.y * chunk, r_end = min(live, r_begin + chunk);
-  const int t = threadIdx.x, width = RB * ITEMS, PG = NT / width;
-  const int item = t % width, pg = t / width;
-  const int j = item / ITEMS, map = (item / S4) & 1, c4 = item % S4;
+  const int rows4 = RB * S4;                   // (row, four dims) items
+  const int t = threadIdx.x, width = rows4 * (2 / MPT), PG = NT / width;
+  const int item = t % rows4, pg = t / width;  // (MPT = 1: the second half of a width is map 2)
+  const int map0 = MPT == 1 ? t % width / rows4 : 0;
+  const int j = item / S4, c4 = item % S4;
+  float4 wt = make_float4(1.f, 1.f, 1.f, 1.f);
+  if (dp.norm_weight != nullptr)
+    wt = make_float4(norm_weight_at(dp, 4 * c4), norm_weight_at(dp, 4 * c4 + 1), norm_weight_at(dp, 4 * c4 + 2),
+                     norm_weight_at(dp, 4 * c4 + 3));
+  float lam = r_begin + j < r_end ? __ldg(dp.lambda + kh * p.G + (r_begin + j) % p.G) : 0.f;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (P <= 1) return;
+  const long long RP = p.rows_padded;
+  const int rbase = blockIdx.z * p.rows_head, rmap = p.rows_head / 2;
   for (int r0 = r_begin; r0 < r_end; r0 += RB) {
     const int r = r0 + j;
-    float m_run = -INFINITY, l_run = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (r < r_end && pg < PG)
-      merge_pieces<D, NB>(p, P, slot0, slot_base, step, rbase, map * rmap + r, 4 * c4, pg, PG, m_run, l_run, acc);
-    s_m[t] = m_run;
-    s_l[t] = l_run;
-    s_o[t] = acc;
-    __syncthreads();
-    // the threads of pg = 0 join the groups and leave out_scale O / l
-    if (t < width && PG > 1) {
-      float M = -INFINITY;
-      for (int k = 0; k < PG; ++k) M = fmaxf(M, s_m[k * width + t]);
-      l_run = 0.f;
-      acc = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int k = 0; k < PG; ++k) {
-        const float mk = s_m[k * width + t];
-        if (mk == -INFINITY) continue;
-        const float w = ex2(mk - M);
-        l_run += w * s_l[k * width + t];
-        const float4 v = s_o[k * width + t];
-        acc.x += w * v.x; acc.y += w * v.y; acc.z += w * v.z; acc.w += w * v.w;
+    if (r0 > r_begin) lam = r < r_end ? __ldg(dp.lambda + kh * p.G + r % p.G) : 0.f;
+    JoinState st[2];
+#pragma unroll
+    for (int m = 0; m < 2; ++m) st[m] = {-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+    if (r < r_end && pg < PG) {
+#pragma unroll 1
+      for (int k0 = pg; k0 < P; k0 += NB * PG) {
+        float2 ml[NB][MPT];
+        float4 v[NB][MPT];
+#pragma unroll
+        for (int i = 0; i < NB; ++i) {
+          const int k = k0 + i * PG;
+#pragma unroll
+          for (int m = 0; m < MPT; ++m) {
+            ml[i][m] = make_float2(-INFINITY, 0.f);
+            if (k < P) {
+              const long long row =
+                  (k == 0 ? slot0 : slot_base + static_cast<long long>(step) * k) * RP + rbase + (map0 + m) * rmap + r;
+              ml[i][m] = __ldcg(reinterpret_cast<const float2*>(p.ws_ml + row * 2));
+              v[i][m] = __ldcg(reinterpret_cast<const float4*>(p.ws_o + row * D) + c4);
+            }
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < NB; ++i)
+#pragma unroll
+          for (int m = 0; m < MPT; ++m) join_add(st[m], ml[i][m], v[i][m]);
       }
     }
-    if (t < width) {
-      const float lam = map == 0 || r >= r_end ? 1.f : __ldg(dp.lambda + kh * p.G + r % p.G);
-      const float inv = l_run > 0.f ? p.out_scale / l_run * lam : 0.f;
-      s_o[t] = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+    if (PG > 1 || MPT == 1) {
+      if (r0 > r_begin) __syncthreads();  // the last rows' states have been read
+#pragma unroll
+      for (int m = 0; m < MPT; ++m) s_st[m][t] = st[m];
+      __syncthreads();
+      if (t < rows4) {
+        st[0] = s_st[0][t];
+        st[1] = MPT == 1 ? s_st[0][rows4 + t] : s_st[MPT - 1][t];
+#pragma unroll 1
+        for (int k = 1; k < PG; ++k)
+#pragma unroll
+          for (int m = 0; m < 2; ++m) {
+            const JoinState o = MPT == 1 ? s_st[0][k * width + m * rows4 + t] : s_st[m % MPT][k * width + t];
+            join_add(st[m], make_float2(o.m, o.l), o.o);
+          }
+      }
     }
-    __syncthreads();
-    // thread (row jj, four dims)
-    const int jj = t / S4, cc = t % S4, rr = r0 + jj;
-    const bool on = jj < RB && rr < r_end;
-    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (on) {
-      const float4 a = s_o[jj * ITEMS + cc], c = s_o[jj * ITEMS + S4 + cc];
-      v = make_float4(a.x - c.x, a.y - c.y, a.z - c.z, a.w - c.w);
-    }
+    const bool on = t < rows4 && r < r_end;
+    const float i1 = st[0].l > 0.f ? p.out_scale / st[0].l : 0.f, i2 = st[1].l > 0.f ? p.out_scale / st[1].l * lam : 0.f;
+    float4 v = make_float4(st[0].o.x * i1 - st[1].o.x * i2, st[0].o.y * i1 - st[1].o.y * i2,
+                           st[0].o.z * i1 - st[1].o.z * i2, st[0].o.w * i1 - st[1].o.w * i2);
     if (dp.norm_weight != nullptr) {
       float ss = v.x * v.x + v.y * v.y + v.z * v.z + v.w * v.w;
 #pragma unroll
       for (int o = 16; o >= 1; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
       if (S4 > 32) {  // a row spans two warps
+        if (r0 > r_begin) __syncthreads();
         if ((t & 31) == 0) s_ss[t >> 5] = ss;
         __syncthreads();
         ss = s_ss[(t >> 5) & ~1] + s_ss[(t >> 5) | 1];
       }
-      if (on) {
-        const float f = rsqrtf(ss / static_cast<float>(D) + dp.norm_eps) * dp.norm_gain;
-        v.x = v.x == 0.f ? 0.f : v.x * f * norm_weight_at(dp, 4 * cc);
-        v.y = v.y == 0.f ? 0.f : v.y * f * norm_weight_at(dp, 4 * cc + 1);
-        v.z = v.z == 0.f ? 0.f : v.z * f * norm_weight_at(dp, 4 * cc + 2);
-        v.w = v.w == 0.f ? 0.f : v.w * f * norm_weight_at(dp, 4 * cc + 3);
-      }
+      const float f = rsqrtf(ss / static_cast<float>(D) + dp.norm_eps) * dp.norm_gain;
+      // (a zero row with eps = 0: rsqrt is infinite, the row stays zero)
+      v.x = v.x == 0.f ? 0.f : v.x * f * wt.x;
+      v.y = v.y == 0.f ? 0.f : v.y * f * wt.y;
+      v.z = v.z == 0.f ? 0.f : v.z * f * wt.z;
+      v.w = v.w == 0.f ? 0.f : v.w * f * wt.w;
     }
-    if (on) {
-      uint16_t* dst = reinterpret_cast<uint16_t*>(p.out) +
-                      (static_cast<long long>(q0 + rr / p.G) * p.Hq + kh * p.G + rr % p.G) * D + 4 * cc;
-      *reinterpret_cast<uint2*>(dst) = make_uint2(pack_out(p.out_bf16 != 0, v.x, v.y), pack_out(p.out_bf16 != 0, v.z, v.w));
-    }
-    __syncthreads();  // s_o free again
+    if (on)
+      *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(p.out) +
+                                (static_cast<long long>(q0 + r / p.G) * p.Hq + kh * p.G + r % p.G) * D + 4 * c4) =
+          make_uint2(pack_out(p.out_bf16 != 0, v.x, v.y), pack_out(p.out_bf16 != 0, v.z, v.w));
   }
 }
 

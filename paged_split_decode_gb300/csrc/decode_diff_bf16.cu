@@ -4,8 +4,8 @@
 
 namespace pd {
 namespace {
-using S128 = DiffShapes<128, kKvBf16, 4>;
-using S256 = DiffShapes<256, kKvBf16, 2>;
+using S128 = DiffShapes<128, kKvBf16>;
+using S256 = DiffShapes<256, kKvBf16>;
 }  // namespace
 
 bool diff_shape_bf16(int D, int ntm, int grouped, KernelShape* out) {

@@ -4,8 +4,8 @@
 
 namespace pd {
 namespace {
-using S128 = DiffShapes<128, kKvF16, 4>;
-using S256 = DiffShapes<256, kKvF16, 2>;
+using S128 = DiffShapes<128, kKvF16>;
+using S256 = DiffShapes<256, kKvF16>;
 }  // namespace
 
 bool diff_shape_f16(int D, int ntm, int grouped, KernelShape* out) {

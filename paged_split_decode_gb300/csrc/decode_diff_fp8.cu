@@ -4,8 +4,8 @@
 
 namespace pd {
 namespace {
-using S128 = DiffShapes<128, kKvFp8, 4>;
-using S256 = DiffShapes<256, kKvFp8, 4>;
+using S128 = DiffShapes<128, kKvFp8>;
+using S256 = DiffShapes<256, kKvFp8>;
 }  // namespace
 
 bool diff_shape_fp8(int D, int ntm, int grouped, KernelShape* out) {

@@ -4,8 +4,8 @@
 
 namespace pd {
 namespace {
-using S128 = DiffShapes<128, kKvInt8, 4>;
-using S256 = DiffShapes<256, kKvInt8, 4>;
+using S128 = DiffShapes<128, kKvInt8>;
+using S256 = DiffShapes<256, kKvInt8>;
 }  // namespace
 
 bool diff_shape_i8(int D, int ntm, int grouped, KernelShape* out) {

@@ -24,20 +24,21 @@ cudaError_t launch_diff(int D, int kv, int ntm, int grouped, const CUtensorMap& 
   }
 }
 
-cudaError_t launch_diff_combine(int D, const DiffParams& p, int n_units, int row_chunks, int rows_at_once,
+cudaError_t launch_diff_combine(int D, const DiffParams& p, int n_units, int row_chunks, int rows_at_once, bool many,
                                 cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(n_units), static_cast<unsigned>(row_chunks),
                      static_cast<unsigned>(p.d.hg));
-  cfg.blockDim = dim3(512, 1, 1);
+  cfg.blockDim = dim3(many ? kJoinThreadsMany : kJoinThreads, 1, 1);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = D == 128 ? cudaLaunchKernelEx(&cfg, diff_combine_kernel<128, 8, 512>, p, rows_at_once)
-                                 : cudaLaunchKernelEx(&cfg, diff_combine_kernel<256, 8, 512>, p, rows_at_once);
+  const auto kernel = D == 128 ? (many ? diff_combine_kernel<128, kJoinThreadsMany, 1> : diff_combine_kernel<128, kJoinThreads, 2>)
+                               : (many ? diff_combine_kernel<256, kJoinThreadsMany, 1> : diff_combine_kernel<256, kJoinThreads, 2>);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p, rows_at_once);
   if (e != cudaSuccess) return e;
   return cudaPeekAtLastError();
 }

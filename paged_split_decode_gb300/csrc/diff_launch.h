@@ -11,7 +11,7 @@ namespace pd {
 bool diff_kernel_shape(int D, int kv, int ntm, int grouped, KernelShape* out);
 cudaError_t launch_diff(int D, int kv, int ntm, int grouped, const CUtensorMap& tk, const CUtensorMap& tv,
                         const DiffParams& p, int grid, cudaStream_t stream);
-cudaError_t launch_diff_combine(int D, const DiffParams& p, int n_units, int row_chunks, int rows_at_once,
+cudaError_t launch_diff_combine(int D, const DiffParams& p, int n_units, int row_chunks, int rows_at_once, bool many,
                                 cudaStream_t stream);
 
 bool diff_shape_f16(int D, int ntm, int grouped, KernelShape* out);
@@ -27,21 +27,26 @@ cudaError_t diff_launch_fp8(int D, int ntm, int grouped, const CUtensorMap&, con
 cudaError_t diff_launch_i8(int D, int ntm, int grouped, const CUtensorMap&, const CUtensorMap&, const DiffParams&,
                            int, cudaStream_t);
 
-// The deepest ring (at most 32 stages) that lets MINB CTAs share an SM.
-template <int D, int KV, int NTM, int RG, int MINB, int HG, int NS = 32>
+// The deepest ring (at most 32 stages, a multiple of the key groups' steps) that
+// lets MINB CTAs share an SM.
+template <int D, int KV, int NTM, int HG, int W, int KG, int KT, int MINB, int NS = 32>
 constexpr int diff_stages() {
-  if constexpr (NS <= 2)
-    return 2;
-  else if constexpr (DiffCfg<D, KV, NTM, RG, NS, MINB, HG>::kSmemBytes <= smem_limit(MINB))
+  constexpr int unit = KG > 1 ? KG * KT : 1;
+  if constexpr (NS <= unit || NS <= 2)
+    return unit > 2 ? unit : 2;
+  else if constexpr (NS % unit != 0)
+    return diff_stages<D, KV, NTM, HG, W, KG, KT, MINB, NS - 1>();
+  else if constexpr (DiffCfg<D, KV, NTM, HG, W, KG, KT, NS, MINB>::kSmemBytes <= smem_limit(MINB))
     return NS;
   else
-    return diff_stages<D, KV, NTM, RG, MINB, HG, NS - 1>();
+    return diff_stages<D, KV, NTM, HG, W, KG, KT, MINB, NS - 1>();
 }
-template <int D, int KV, int NTM, int RG, int MINB, int HG>
-using DiffCfgFor = DiffCfg<D, KV, NTM, RG, diff_stages<D, KV, NTM, RG, MINB, HG>(), MINB, HG>;
+template <int D, int KV, int NTM, int HG, int W, int KG, int KT, int MINB>
+using DiffCfgFor = DiffCfg<D, KV, NTM, HG, W, KG, KT, diff_stages<D, KV, NTM, HG, W, KG, KT, MINB>(), MINB>;
 
 template <class Cfg>
 bool diff_shape_of(KernelShape* out) {
+  static_assert(Cfg::kSmemBytes <= smem_limit(Cfg::kMinBlocks), "the ring fits");
   out->threads = Cfg::kThreads;
   out->smem_bytes = Cfg::kSmemBytes;
   out->rows_padded = Cfg::RP;
@@ -63,16 +68,25 @@ cudaError_t diff_launch_cfg(const CUtensorMap& tk, const CUtensorMap& tv, const 
   return launch_pdl(decode_diff_kernel<Cfg>, grid, Cfg::kThreads, Cfg::kSmemBytes, stream, 1, tk, tv, p);
 }
 
-// The shapes of one cache kind: C1H, tiles of HG consecutive KV heads (one
-// row tile per map, Hkv a multiple of four) on one CTA per SM; else per-head
-// tiles on two CTAs per SM, with a warp pair for every row tile.
-template <int D, int KV, int HG>
+// The shapes of one cache kind, as measured fastest on GB300 (D = 256 GQA 6:1
+// L = 4096 B = 32 unless said):
+//  * C1H, one row tile per map and Hkv a multiple of four: a warp per head, four
+//    heads a tile, one CTA per SM. Two tiles a step at D = 128 (e4m3, 32 x 8
+//    heads, ragged: 108 -> 100 us); at D = 256 two tiles' scores spill (e4m3 54
+//    -> 60 us). Two warps per head that swap P took 66 us at e4m3, four 77.
+//  * C1, other head counts: per-head tiles, three key groups of one warp on two
+//    CTAs per SM (two CTAs' producers: one tile's copies take 0.2 us to issue).
+//  * C2 to C4, two to four row tiles per map: four warps a head, two key groups,
+//    one CTA per SM; two tiles a step while the fragments fit (qlen = 3, e4m3, L
+//    = 8192, B = 8: 69 -> 65 us).
+template <int D, int KV>
 struct DiffShapes {
-  using C1H = DiffCfgFor<D, KV, 1, 1, 1, HG>;
-  using C1 = DiffCfgFor<D, KV, 1, 1, 2, 1>;
-  using C2 = DiffCfgFor<D, KV, 2, 2, 2, 1>;
-  using C3 = DiffCfgFor<D, KV, 3, 3, 2, 1>;
-  using C4 = DiffCfgFor<D, KV, 4, 4, 2, 1>;
+  // row tiles per map, heads per tile, warps per head, key groups, tiles per step, CTAs per SM
+  using C1H = DiffCfgFor<D, KV, 1, 4, 1, 1, (D == 128 ? 2 : 1), 1>;
+  using C1 = DiffCfgFor<D, KV, 1, 1, 1, 3, 1, 2>;
+  using C2 = DiffCfgFor<D, KV, 2, 1, 4, 2, 2, 1>;
+  using C3 = DiffCfgFor<D, KV, 3, 1, 4, 2, 2, 1>;
+  using C4 = DiffCfgFor<D, KV, 4, 1, 4, 2, 1, 1>;
 
   static bool shape(int ntm, int grouped, KernelShape* out) {
     if (grouped) return ntm == 1 && diff_shape_of<C1H>(out);
