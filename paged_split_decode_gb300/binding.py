@@ -1,4 +1,5 @@
-"""Thin ctypes binding over libpdecode (C ABI in include/pdecode.h).
+"""Thin binding over libpdecode (C ABI in include/pdecode.h): ctypes, and for the
+calls beside kernels of a few microseconds a small CPython extension.
 
 Argument marshalling only: tensors become device pointers, the current torch
 stream becomes the launch stream, a status other than PD_OK becomes an
@@ -7,8 +8,8 @@ there is no CPU or PyTorch fallback, and a missing library is an error.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import importlib.util
 import os
 import threading
 
@@ -360,72 +361,46 @@ def write_kv_cache(k_new, v_new, slot_mapping, k_cache, v_cache, *, k_scale=1.0,
 
 
 # ---- differential decode, block tables, root-mean-square norm ----------------
-# These run beside kernels of a few microseconds, so their checks are kept to
-# one query each per tensor, and a plan's workspace size is kept by its shapes.
-_INT = (torch.int32,)
-_LONG = (torch.int64,)
-_FLOAT = (torch.float32,)
-_BYTE = (torch.bool, torch.uint8)
-_HALF = (torch.float16,)
-_BF16 = (torch.bfloat16,)
-_FLAG_TYPES = (torch.int32, torch.uint32)
-_CODE_KINDS = {torch.float8_e4m3fn: 1, torch.int8: 2}
-_diff_need: dict = {}
+# These run beside kernels of a few microseconds: their checks and marshalling
+# are compiled (csrc/bind.cpp).
+_bind = None
 
 
-def _arg(t, name, dtypes, index) -> int:
-    """Device pointer of a contiguous tensor on GPU ``index`` (None: 0)."""
-    if t is None:
-        return 0
-    if t.get_device() != index:
-        if not t.is_cuda:
-            raise TypeError(f"{name} must be a CUDA tensor")
-        raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
-    if t.dtype not in dtypes:
-        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtypes}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
-
-
-def _gpu_of(t, name) -> int:
-    index = t.get_device()
-    if index < 0:
-        raise TypeError(f"{name} must be a CUDA tensor")
-    return index
-
-
-def _call(fn, what, index, stream, args):
-    """Launch on ``stream`` (None: the current one) with GPU ``index`` current."""
-    s = torch._C._cuda_getCurrentRawStream(index) if stream is None else int(stream)
-    if torch._C._cuda_getDevice() == index:
-        rc = fn(*args, s)
-    else:
-        with torch.cuda.device(index):
-            rc = fn(*args, s)
-    if rc:
-        _check(rc, what)
-
-
-def _alloc_on(stream, index):
-    """Allocations under this context are ordered by the launch's stream."""
-    if stream is None or int(stream) == torch._C._cuda_getCurrentRawStream(index):
-        return contextlib.nullcontext()
-    return torch.cuda.stream(torch.cuda.ExternalStream(int(stream), device=index))
+def _fast():
+    """The compiled binding over libpdecode; raises if it has not been built."""
+    global _bind
+    lib = load()
+    with _lock:
+        if _bind is None:
+            path = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_bind.so")
+            if not os.path.exists(path):
+                raise RuntimeError(f"{path} is missing: build it first "
+                                   "(paged_split_decode_gb300.build.build())")
+            spec = importlib.util.spec_from_file_location("paged_split_decode_gb300._bind", path)
+            mod = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(mod)
+            mod.init(*(ctypes.cast(fn, ctypes.c_void_p).value for fn in (
+                lib.decode_paged_diff, lib.pd_diff_workspace_bytes, lib.build_block_tables, lib.release_blocks,
+                lib.rms_norm, lib.pd_status_str)), DecodeError, _diff_workspace)
+            _bind = mod
+    return _bind
 
 
 def _diff_workspace(need, index, stream):
-    """The workspace of a call that brought none. A captured call keeps one of
-    its own in the graph's pool, as graphs may be replayed at the same time."""
-    with _alloc_on(stream, index):
-        if torch._C._cuda_isCurrentStreamCapturing():
-            return torch.empty(need, dtype=torch.uint8, device=torch.device("cuda", index))
+    """The workspace of a differential decode that brought none. A captured
+    call keeps one of its own in the graph's pool, as graphs may be replayed at
+    the same time; else the (device, stream) one of ``get_workspace``."""
     s = torch._C._cuda_getCurrentRawStream(index) if stream is None else int(stream)
-    ws = _workspaces.get(("cuda", index, s))
-    if ws is None or ws.numel() < need:
-        with torch.cuda.device(index):
-            ws = get_workspace(torch.device("cuda", index), need, s)
-    return ws
+    if not torch.cuda.is_current_stream_capturing():
+        ws = _workspaces.get(("cuda", index, s))
+        if ws is not None and ws.numel() >= need:
+            return ws
+    device = torch.device("cuda", index)
+    cur = torch.cuda.current_stream(device)
+    with torch.cuda.stream(cur if s == cur.cuda_stream else torch.cuda.ExternalStream(s, device=device)):
+        if torch.cuda.is_current_stream_capturing():
+            return torch.empty(need, dtype=torch.uint8, device=device)
+        return get_workspace(device, need, s)
 
 
 def decode_paged_diff(q, k_cache, v_cache, block_table, seq_lens, lam, scale, window=0, qlen=1,
@@ -443,60 +418,9 @@ def decode_paged_diff(q, k_cache, v_cache, block_table, seq_lens, lam, scale, wi
     ``qlen``, as in ``decode_paged_varlen`` (rows outside every range are left
     as they were; a new ``out`` is zeroed there).
     """
-    lib = _lib or load()
-    q_dtype = q.dtype
-    kind = kv_kind_of(k_cache, q_dtype)
-    io = _BF16 if kind in _BF16_IO else _HALF
-    kv_dt = (k_cache.dtype,)
-    if q.dim() != 3 or k_cache.dim() != 4 or block_table.dim() != 2:
-        raise ValueError("q must be [T, Hq, D], the caches [num_blocks, block_size, Hkv, D], block_table [B, max_blocks]")
-    T, Hq, D = q.shape
-    num_blocks, bs, Hkv, Dk = k_shape = k_cache.shape
-    B, cols = block_table.shape
-    if v_cache.shape != k_shape or v_cache.dtype != k_cache.dtype:
-        raise ValueError("v_cache must match k_cache in shape and dtype")
-    if D != Dk or seq_lens.numel() != B:
-        raise ValueError("q must be [T, Hq, D] with the caches' D; seq_lens [B]")
-    if query_start_loc is None:
-        if T != B * qlen:
-            raise ValueError("q must be [B*qlen, Hq, D] with B = rows of block_table")
-    elif query_start_loc.numel() != B + 1:
-        raise ValueError("query_start_loc must be [B+1]")
-    if lam.numel() != Hq:
-        raise ValueError("lam must be [Hq]")
-    weight_f32 = 0
-    if norm_weight is not None:
-        if norm_weight.numel() != D:
-            raise ValueError("norm_weight must be [D]")
-        weight_f32 = int(norm_weight.dtype == torch.float32)
-    if out is not None and out.shape != q.shape:
-        raise ValueError("out must have q's shape")
-    index = _gpu_of(q, "q")
-    dims = PdDims(B, Hq, Hkv, D, bs, num_blocks, cols, kind, k_scale, v_scale)
-    if out is None:
-        with _alloc_on(stream, index):
-            out = torch.empty_like(q) if query_start_loc is None else torch.zeros_like(q)
-    if workspace is None:
-        key = (index, B, Hq, Hkv, D, bs, num_blocks, cols, kind, qlen, num_splits)
-        need = _diff_need.get(key)
-        if need is None:
-            with torch.cuda.device(index):
-                need = diff_workspace_bytes(dims, qlen, num_splits)
-            if len(_diff_need) >= 4096:
-                _diff_need.clear()
-            _diff_need[key] = need
-        if need:
-            workspace = _diff_workspace(need, index, stream)
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _call(lib.decode_paged_diff, "decode_paged_diff", index, stream, (
-        _arg(q, "q", io, index), _arg(k_cache, "k_cache", kv_dt, index), _arg(v_cache, "v_cache", kv_dt, index),
-        _arg(block_table, "block_table", _INT, index), _arg(seq_lens, "seq_lens", _INT, index),
-        _arg(query_start_loc, "query_start_loc", _INT, index), T, _arg(lam, "lam", _FLOAT, index), scale, window, qlen,
-        num_splits, _arg(norm_weight, "norm_weight", _FLOAT if weight_f32 else io, index), weight_f32, norm_eps,
-        norm_gain, _arg(out, "out", io, index), ctypes.byref(dims),
-        0 if workspace is None else _arg(workspace, "workspace", (workspace.dtype,), index), ws_bytes,
-        _arg(error_flag, "error_flag", _FLAG_TYPES, index)))
-    return out
+    return (_bind or _fast()).decode_paged_diff(q, k_cache, v_cache, block_table, seq_lens, lam, scale, window, qlen,
+                                                num_splits, out, query_start_loc, norm_weight, norm_eps, norm_gain,
+                                                k_scale, v_scale, workspace, error_flag, stream)
 
 
 def build_block_tables(context_lens, query_lens, block_table, free_blocks, free_count, block_size,
@@ -513,53 +437,9 @@ def build_block_tables(context_lens, query_lens, block_table, free_blocks, free_
     behind the last token. ``seq_lens`` may be ``context_lens`` itself;
     ``free_count`` is updated in place unless ``free_count_out`` is given.
     """
-    lib = _lib or load()
-    if block_table.dim() != 2:
-        raise ValueError("block_table must be [B, max_blocks]")
-    B, cols = block_table.shape
-    if context_lens.numel() != B or query_lens.numel() != B:
-        raise ValueError("context_lens and query_lens must be [B]")
-    if slot_mapping is not None:
-        T = slot_mapping.numel()
-        if num_tokens is not None and num_tokens != T:
-            raise ValueError("slot_mapping must be [num_tokens]")
-    elif num_tokens is None:
-        raise ValueError("give num_tokens or a slot_mapping")
-    else:
-        T = int(num_tokens)
-        if T < 0:
-            raise ValueError("num_tokens must not be negative")
-    if positions is not None and positions.numel() != T:
-        raise ValueError("positions must be [num_tokens]")
-    if free_count_out is None:
-        free_count_out = free_count
-    if free_count.numel() != 1 or free_count_out.numel() != 1:
-        raise ValueError("free_count must be [1]")
-    if seq_lens is not None and seq_lens.numel() != B:
-        raise ValueError("seq_lens must be [B]")
-    if query_start_loc is not None and query_start_loc.numel() != B + 1:
-        raise ValueError("query_start_loc must be [B+1]")
-    index = _gpu_of(block_table, "block_table")
-    if seq_lens is None or query_start_loc is None or slot_mapping is None or positions is None:
-        with _alloc_on(stream, index):
-            dev = block_table.device
-            if seq_lens is None:
-                seq_lens = torch.empty(B, dtype=torch.int32, device=dev)
-            if query_start_loc is None:
-                query_start_loc = torch.empty(B + 1, dtype=torch.int32, device=dev)
-            if slot_mapping is None:
-                slot_mapping = torch.empty(T, dtype=torch.int64, device=dev)
-            if positions is None:
-                positions = torch.empty(T, dtype=torch.int32, device=dev)
-    dims = PdDims(B, 1, 1, 1, block_size, free_blocks.numel(), cols, 0, 1.0, 1.0)
-    _call(lib.build_block_tables, "build_block_tables", index, stream, (
-        _arg(context_lens, "context_lens", _INT, index), _arg(query_lens, "query_lens", _INT, index), T,
-        _arg(block_table, "block_table", _INT, index), _arg(free_blocks, "free_blocks", _INT, index),
-        _arg(free_count, "free_count", _INT, index), _arg(free_count_out, "free_count_out", _INT, index),
-        _arg(seq_lens, "seq_lens", _INT, index), _arg(query_start_loc, "query_start_loc", _INT, index),
-        _arg(slot_mapping, "slot_mapping", _LONG, index), _arg(positions, "positions", _INT, index),
-        ctypes.byref(dims), _arg(error_flag, "error_flag", _FLAG_TYPES, index)))
-    return seq_lens, query_start_loc, slot_mapping, positions
+    return (_bind or _fast()).build_block_tables(context_lens, query_lens, block_table, free_blocks, free_count,
+                                                 block_size, num_tokens, seq_lens, query_start_loc, slot_mapping,
+                                                 positions, free_count_out, error_flag, stream)
 
 
 def release_blocks(block_table, seq_lens, released, free_blocks, free_count, block_size, *,
@@ -568,29 +448,8 @@ def release_blocks(block_table, seq_lens, released, free_blocks, free_count, blo
     [B]) back onto ``free_blocks``, in order, and set their ``seq_lens`` to 0;
     ``seq_lens`` and ``free_count`` are updated in place unless
     ``seq_lens_out`` / ``free_count_out`` are given. Returns the lengths."""
-    lib = _lib or load()
-    if block_table.dim() != 2:
-        raise ValueError("block_table must be [B, max_blocks]")
-    B, cols = block_table.shape
-    if seq_lens.numel() != B or released.numel() != B:
-        raise ValueError("seq_lens and released must be [B]")
-    if free_count_out is None:
-        free_count_out = free_count
-    if free_count.numel() != 1 or free_count_out.numel() != 1:
-        raise ValueError("free_count must be [1]")
-    if seq_lens_out is None:
-        seq_lens_out = seq_lens
-    elif seq_lens_out.numel() != B:
-        raise ValueError("seq_lens_out must be [B]")
-    index = _gpu_of(block_table, "block_table")
-    dims = PdDims(B, 1, 1, 1, block_size, free_blocks.numel(), cols, 0, 1.0, 1.0)
-    _call(lib.release_blocks, "release_blocks", index, stream, (
-        _arg(block_table, "block_table", _INT, index), _arg(seq_lens, "seq_lens", _INT, index),
-        _arg(released, "released", _BYTE, index), _arg(free_blocks, "free_blocks", _INT, index),
-        _arg(free_count, "free_count", _INT, index), _arg(free_count_out, "free_count_out", _INT, index),
-        _arg(seq_lens_out, "seq_lens_out", _INT, index), ctypes.byref(dims),
-        _arg(error_flag, "error_flag", _FLAG_TYPES, index)))
-    return seq_lens_out
+    return (_bind or _fast()).release_blocks(block_table, seq_lens, released, free_blocks, free_count, block_size,
+                                             seq_lens_out, free_count_out, error_flag, stream)
 
 
 def rms_norm(x, weight, eps=1e-5, *, residual=None, residual_out=None, gain=1.0, norm_size=None,
@@ -605,49 +464,5 @@ def rms_norm(x, weight, eps=1e-5, *, residual=None, residual_out=None, gain=1.0,
     float8_e4m3fn or int8; the 8-bit types come with a float32 scale for every
     ``scale_size`` values (default: N). Returns ``out``, or ``(out,
     out_scale)`` for the 8-bit types."""
-    lib = _lib or load()
-    x_dtype, shape = x.dtype, x.shape
-    bf16 = x_dtype == torch.bfloat16
-    if not bf16 and x_dtype != torch.float16:
-        raise TypeError(f"x has dtype {x_dtype}, expected float16 or bfloat16")
-    if len(shape) < 1 or shape[-1] < 1:
-        raise ValueError("x must be [..., N] with N >= 1")
-    N = shape[-1]
-    rows = x.numel() // N
-    norm_size = N if norm_size is None else int(norm_size)
-    dt = out_dtype if out_dtype is not None else x_dtype if out is None else out.dtype
-    kind = 0 if dt == x_dtype else _CODE_KINDS.get(dt)
-    if kind is None:
-        raise TypeError(f"unsupported output dtype {dt}")
-    scale_size = N if scale_size is None else int(scale_size)
-    if norm_size < 1 or scale_size < 1 or N % norm_size or N % scale_size:
-        raise ValueError("norm_size and scale_size must divide N")
-    if weight.numel() != norm_size:
-        raise ValueError("weight must be [norm_size]")
-    if residual is not None:
-        if residual.shape != shape:
-            raise ValueError("residual must have x's shape")
-        if residual_out is None:
-            residual_out = residual
-    if residual_out is not None and residual_out.shape != shape:
-        raise ValueError("residual_out must have x's shape")
-    if out is not None and (out.shape != shape or out.dtype != dt):
-        raise ValueError("out must have x's shape and the output dtype")
-    if out_scale is not None and (kind == 0 or out_scale.numel() != rows * (N // scale_size)):
-        raise ValueError("out_scale is [..., N / scale_size], for 8-bit outputs only")
-    index = _gpu_of(x, "x")
-    if out is None or (kind and out_scale is None):
-        with _alloc_on(stream, index):
-            if out is None:
-                out = torch.empty(shape, dtype=dt, device=x.device)
-            if kind and out_scale is None:
-                out_scale = torch.empty(shape[:-1] + (N // scale_size,), dtype=torch.float32, device=x.device)
-    weight_f32 = int(weight.dtype == torch.float32)
-    io = _BF16 if bf16 else _HALF
-    dims = PdNormDims(rows, N, norm_size, scale_size, bf16, weight_f32, kind)
-    _call(lib.rms_norm, "rms_norm", index, stream, (
-        _arg(x, "x", io, index), _arg(residual, "residual", io, index),
-        _arg(weight, "weight", _FLOAT if weight_f32 else io, index), eps, gain,
-        _arg(residual_out, "residual_out", io, index), _arg(out, "out", (dt,), index),
-        _arg(out_scale, "out_scale", _FLOAT, index), ctypes.byref(dims)))
-    return (out, out_scale) if kind else out
+    return (_bind or _fast()).rms_norm(x, weight, eps, residual, residual_out, gain, norm_size, out_dtype, scale_size,
+                                       out, out_scale, stream)

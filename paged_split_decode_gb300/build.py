@@ -3,16 +3,21 @@
 Each translation unit under csrc/ is compiled in parallel to an object file
 under _build/, then linked into paged_split_decode_gb300/libpdecode.so (the
 CUDA runtime is linked statically; the driver's tensor-map encoder is reached
-through the runtime's entry-point query, so no -lcuda is needed). A rebuild is
-skipped when the library is newer than every source and header.
+through the runtime's entry-point query, so no -lcuda is needed). csrc/bind.cpp
+becomes _bind.so beside it, the compiled part of the Python binding, against
+the headers of the installed PyTorch. A rebuild is skipped when both are newer
+than every source and header and PyTorch is the one they were built for.
 """
 from __future__ import annotations
 
 import glob
+import importlib.metadata
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -20,6 +25,9 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libpdecode.so")
+BIND = os.path.join(PKG, "_bind.so")
+BIND_SRC = os.path.join(CSRC, "bind.cpp")
+BIND_FOR = os.path.join(BUILD, "bind.for")  # the PyTorch and Python that _bind.so was built for
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
          "-I", os.path.join(ROOT, "include"), "-I", CSRC]
@@ -36,11 +44,26 @@ def sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
+def _bind_for() -> str:
+    return f"torch {importlib.metadata.version('torch')} python {sys.version.split()[0]}"
+
+
+def _bind_command(out: str):
+    torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
+    lib = os.path.join(torch_dir, "lib")
+    return [nvcc(), "-O2", "-std=c++17", "-shared", "-Xcompiler", "-fPIC,-fvisibility=hidden,-w",
+            "-I", os.path.join(ROOT, "include"), "-I", sysconfig.get_paths()["include"],
+            "-I", os.path.join(torch_dir, "include"), BIND_SRC, "-o", out, "-L", lib, "-lc10", "-lc10_cuda",
+            "-ltorch_cpu", "-ltorch_python", "-Xlinker", f"-rpath={lib}"]
+
+
 def _stale() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(BIND):
         return True
-    t = os.path.getmtime(LIB)
-    deps = sources() + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh")) \
+    if not os.path.exists(BIND_FOR) or open(BIND_FOR).read() != _bind_for():
+        return True
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BIND))
+    deps = sources() + [BIND_SRC] + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh")) \
         + glob.glob(os.path.join(ROOT, "include", "*.h")) + [__file__]
     return any(os.path.getmtime(p) > t for p in deps)
 
@@ -62,8 +85,19 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
             sys.stderr.write(r.stdout + r.stderr)
         return obj
 
-    with ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 1)) as ex:
+    def compile_bind():
+        tmp = BIND + f".tmp{os.getpid()}"
+        r = subprocess.run(_bind_command(tmp), capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"build of {BIND_SRC} failed:\n{r.stdout}\n{r.stderr}")
+        os.replace(tmp, BIND)
+        with open(BIND_FOR, "w") as f:
+            f.write(_bind_for())
+
+    with ThreadPoolExecutor(max_workers=min(16, os.cpu_count() or 1)) as ex:
+        bind = ex.submit(compile_bind)
         objs = list(ex.map(compile_one, sources()))
+        bind.result()
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [cc, *ARCH, "-shared", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)

@@ -24,10 +24,10 @@ def _dims(**kw):
 
 def test_diff_workspace_holds_two_maps(lib):
     up = lambda x: (x + 255) // 256 * 256
-    # head-group tiles of two KV heads, 8 padded rows per map: 2 x 2 x 8 rows per slot
-    assert binding.diff_workspace_bytes(_dims(), 1, 0, sm_count=152) == up(304 * 32 * 2 * 4) + 304 * 32 * 256 * 4
+    # head-group tiles of four KV heads, 8 padded rows per map: 4 x 2 x 8 rows per slot
+    assert binding.diff_workspace_bytes(_dims(), 1, 0, sm_count=152) == up(304 * 64 * 2 * 4) + 304 * 64 * 256 * 4
     assert binding.diff_workspace_bytes(_dims(), 1, 1, sm_count=152) == 0
-    assert binding.diff_workspace_bytes(_dims(), 1, 3, sm_count=152) == up(192 * 32 * 2 * 4) + 192 * 32 * 256 * 4
+    assert binding.diff_workspace_bytes(_dims(), 1, 3, sm_count=152) == up(96 * 64 * 2 * 4) + 96 * 64 * 256 * 4
 
 
 @pytest.mark.parametrize("kw,qlen", [
