@@ -357,18 +357,25 @@ pd_status check_table_dims(const pd_dims* d) {
 
 bool misaligned(const void* p, uintptr_t mask) { return (reinterpret_cast<uintptr_t>(p) & mask) != 0; }
 
-// One cluster of `ctas` CTAs (1 to 8, the portable size).
+// One cluster of `ctas` CTAs: 1, 8 (the portable size) or, where the device runs
+// such a cluster, 16.
 template <class Kern, class Args>
-pd_status launch_cluster(Kern kernel, unsigned long long (&done)[64], int ctas, size_t smem, cudaStream_t s,
-                         const Args& args) {
+pd_status launch_cluster(Kern kernel, unsigned long long (&done)[64], unsigned long long (&done_occ)[64],
+                         int (&cache)[64][kMaxCluster + 1], int ctas, size_t smem, cudaStream_t s, const Args& args) {
   const int most = (3 * kMaxTableB + 2) * 4;
   if (once_per_context(done, [&] { return set_kernel_attributes(kernel, most); }) != cudaSuccess) return PD_ERR_CUDA;
+  if (ctas > 8) {
+    int counts[kMaxCluster + 1];
+    max_active_clusters(kernel, kTabThreads, most, done_occ, cache, counts);
+    if (counts[ctas] < 1) ctas = 8;
+  }
   return launch_pdl(kernel, ctas, kTabThreads, static_cast<int>(smem), s, ctas, args) == cudaSuccess ? PD_OK
                                                                                                     : PD_ERR_CUDA;
 }
 
-// CTAs for `items` dealt out to the threads.
-int table_ctas(long long items) { return items > kTabThreads ? 8 : 1; }
+// CTAs for `items` dealt out to the threads. More than one costs a cluster launch
+// and barrier, more than eight a place for 16 CTAs at once.
+int table_ctas(long long items) { return items <= kTabThreads ? 1 : items <= 8 * kTabThreads ? 8 : 16; }
 
 }  // namespace
 }  // namespace pd
@@ -397,8 +404,9 @@ extern "C" pd_status build_block_tables(const int32_t* context_lens, const int32
   TableArgs a{context_lens, query_lens, block_table, free_blocks, free_count, free_count_out, seq_lens,
               query_start_loc, slot_mapping, positions, error_flag, d.B, num_tokens, d.block_size, d.num_blocks,
               d.max_blocks_per_seq};
-  static unsigned long long done[64] = {};
-  return launch_cluster(build_tables_kernel, done, table_ctas(num_tokens), (3 * static_cast<size_t>(d.B) + 2) * 4,
+  static unsigned long long done[64] = {}, done_occ[64] = {};
+  static int cache[64][kMaxCluster + 1] = {};
+  return launch_cluster(build_tables_kernel, done, done_occ, cache, table_ctas(num_tokens), (3 * static_cast<size_t>(d.B) + 2) * 4,
                         static_cast<cudaStream_t>(stream), a);
 }
 
@@ -418,8 +426,9 @@ extern "C" pd_status release_blocks(const int32_t* block_table, const int32_t* s
     return PD_ERR_ALIGN;
   ReleaseArgs a{block_table, seq_lens, released, free_blocks, free_count, free_count_out, seq_lens_out, error_flag,
                 d.B, d.block_size, d.num_blocks, d.max_blocks_per_seq};
-  static unsigned long long done[64] = {};
+  static unsigned long long done[64] = {}, done_occ[64] = {};
+  static int cache[64][kMaxCluster + 1] = {};
   const long long blocks = static_cast<long long>(d.B) * d.max_blocks_per_seq;
-  return launch_cluster(release_kernel, done, table_ctas(blocks), (2 * static_cast<size_t>(d.B) + 1) * 4,
+  return launch_cluster(release_kernel, done, done_occ, cache, table_ctas(blocks), (2 * static_cast<size_t>(d.B) + 1) * 4,
                         static_cast<cudaStream_t>(stream), a);
 }

@@ -60,6 +60,10 @@ struct DiffCfg {
   static constexpr int kSlabBytes = HG * kHeadBytes;  // [head][key][128 B]
   static constexpr int kTileBytes = kSlabs * kSlabBytes;
   static constexpr int kStageBytes = 2 * kTileBytes;
+  // 16-bit caches, a warp per head: P is carried as the sum of two operands (the
+  // rounded value and the rounded rest), which makes the output as exact as one
+  // rounding allows
+  static constexpr int PP = W == 1 && !BYTE ? 2 : 1;
   static constexpr int MPW = W == 1 ? 2 : 1;             // maps a warp scores
   static constexpr int RG = W == 4 ? 2 : 1;              // row groups
   static constexpr int NTR = (NTM + RG - 1) / RG;        // row tiles (per map) a warp scores
@@ -102,6 +106,13 @@ __device__ __forceinline__ float norm_weight_at(const DiffParams& p, int d) {
   if (p.norm_f32) return __ldg(static_cast<const float*>(p.norm_weight) + d);
   const uint16_t w = __ldg(static_cast<const uint16_t*>(p.norm_weight) + d);
   return p.d.out_bf16 ? __uint_as_float(static_cast<uint32_t>(w) << 16) : __half2float(__ushort_as_half(w));
+}
+
+// x rounded to the 16-bit operand type.
+template <bool BF16>
+__device__ __forceinline__ float round16(float x) {
+  if constexpr (BF16) return __bfloat162float(__float2bfloat16_rn(x));
+  else return __half2float(__float2half_rn(x));
 }
 
 __device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
@@ -366,7 +377,8 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::kMinBlocks)
         if constexpr (W > 1) named_bar_sync(2 + th * KG + kg, W * 32);
         continue;
       }
-      uint32_t pf[KT][2][NTM][2];  // P^T fragments of both maps
+      constexpr int PP = Cfg::PP;
+      uint32_t pf[KT][2][NTM][2 * PP];  // P^T fragments of both maps
       float x[KT][MPW][NTR][4];    // raw scores
 #pragma unroll
       for (int j = 0; j < KT; ++j) {
@@ -520,6 +532,10 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::kMinBlocks)
               pf[j][m][n][0] = pk[j][0];
               pf[j][m][n][1] = pk[j][1];
             }
+            if constexpr (PP == 2) {
+              pf[j][m][n][PP] = movmatrix_trans(pack2<BF16>(p00 - round16<BF16>(p00), p01 - round16<BF16>(p01)));
+              pf[j][m][n][PP + 1] = movmatrix_trans(pack2<BF16>(p10 - round16<BF16>(p10), p11 - round16<BF16>(p11)));
+            }
           }
           if constexpr (W > 1) {
             const uint32_t at = xcur + ((map * Cfg::RG * NTR + rt0 + n) * 32 + lane) * 8 * KT;
@@ -592,7 +608,9 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::kMinBlocks)
 #pragma unroll
             for (int m = 0; m < 2; ++m)
 #pragma unroll
-              for (int n = 0; n < NTM; ++n) mma_op<BF16>(o[m][mtl][n], a, pf[j][m][n][0], pf[j][m][n][1]);
+              for (int n = 0; n < NTM; ++n)
+#pragma unroll
+                for (int h = 0; h < PP; ++h) mma_op<BF16>(o[m][mtl][n], a, pf[j][m][n][2 * h], pf[j][m][n][2 * h + 1]);
           }
         } else {
           // 32-dim group P32: lane reads 4 codes at dims 32 P32 + 4 g of keys

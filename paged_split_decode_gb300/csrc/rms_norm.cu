@@ -15,8 +15,10 @@
 // norm group, largest |y| per scale group) run by the group's size in vectors:
 // the whole CTA; within a warp's lanes, for 1 to 32 vectors in a power of two;
 // else through shared memory, a warp per group. Rows whose sizes or addresses
-// do not allow 16-byte vectors take a plainer kernel. Measured (fp16, residual,
-// 32768 x 4096): 153 us, 7.0 TB/s, where the plainer kernel took 867 us.
+// do not allow 16-byte vectors take a plainer kernel. Measured: 32768 x 4096,
+// fp16, residual, fp16 output 154 us (7.0 TB/s; the plainer kernel 867 us); 8192
+// x 6144, bfloat16, residual, e4m3 with a scale for every 128 values 54 us (6.6
+// TB/s; 68 us with divisions by the scale and by group sizes).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -117,9 +119,22 @@ __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
 // How a reduction over groups of `vecs` vectors runs.
 enum Reach { kReachCta, kReachLanes, kReachShared };
 struct Groups {
-  int vecs;   // vectors of a group
-  int reach;  // Reach
+  int vecs;      // vectors of a group
+  int reach;     // Reach
+  uint32_t mul;  // ceil(2^32 / vecs) (vecs > 1): i / vecs = the product's high word, as i and vecs
+                 // are at most 4096, so that i (mul vecs - 2^32) < 2^32
+  __device__ __forceinline__ int of(int i) const {
+    return vecs > 1 ? static_cast<int>(__umulhi(static_cast<uint32_t>(i), mul)) : i;
+  }
+  __device__ __forceinline__ int within(int i) const { return i - of(i) * vecs; }
 };
+
+// 1 / x, approximate (rcp.approx: at most one unit in the last place).
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 
 struct Plus {
   __device__ __forceinline__ float operator()(float a, float b) const { return a + b; }
@@ -154,26 +169,35 @@ __device__ __forceinline__ void group_reduce(float (&v)[V], int nv, const Groups
       for (int j = 0; j < V; ++j) v[j] = op(v[j], __shfl_xor_sync(0xffffffffu, v[j], o));
     }
   } else {
-    const int groups = nv / g.vecs;
+    const int groups = g.of(nv);
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       const int i = j * blockDim.x + t;
       if (i < nv) s_part[i] = v[j];
     }
     __syncthreads();
-    // a warp reads its whole group before it leaves the result in its first place
-    for (int q = warp; q < groups; q += warps) {
-      float x = 0.f;
-      for (int i = lane; i < g.vecs; i += 32) x = op(x, s_part[q * g.vecs + i]);
+    // a group's result is left in its first place: by one thread (a group of at
+    // most 32 vectors), else by a warp, which reads the group before
+    if (g.vecs <= 32) {
+      for (int q = t; q < groups; q += blockDim.x) {
+        float x = s_part[q * g.vecs];
+        for (int i = 1; i < g.vecs; ++i) x = op(x, s_part[q * g.vecs + i]);
+        s_part[q * g.vecs] = x;
+      }
+    } else {
+      for (int q = warp; q < groups; q += warps) {
+        float x = 0.f;
+        for (int i = lane; i < g.vecs; i += 32) x = op(x, s_part[q * g.vecs + i]);
 #pragma unroll
-      for (int o = 16; o >= 1; o >>= 1) x = op(x, __shfl_xor_sync(0xffffffffu, x, o));
-      if (lane == 0) s_part[q * g.vecs] = x;
+        for (int o = 16; o >= 1; o >>= 1) x = op(x, __shfl_xor_sync(0xffffffffu, x, o));
+        if (lane == 0) s_part[q * g.vecs] = x;
+      }
     }
     __syncthreads();
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       const int i = j * blockDim.x + t;
-      if (i < nv) v[j] = s_part[i / g.vecs * g.vecs];
+      if (i < nv) v[j] = s_part[g.of(i) * g.vecs];
     }
   }
 }
@@ -228,7 +252,7 @@ __global__ void __launch_bounds__(max_threads(V)) rms_norm_vec_kernel(const VecA
   for (int j = 0; j < V; ++j) {
     const int i = j * nt + t;
     const float inv = rsqrtf(ss[j] * inv_n + a.n.eps) * a.n.gain;
-    const int wi = i % a.norm.vecs;
+    const int wi = a.norm.reach == kReachCta ? min(i, nv - 1) : a.norm.within(i);
     float w[8];
     if (a.n.w_f32) {
       const float4* wp = static_cast<const float4*>(a.n.weight) + 2 * wi;
@@ -253,16 +277,17 @@ __global__ void __launch_bounds__(max_threads(V)) rms_norm_vec_kernel(const VecA
       if (i < nv) out[i] = narrow8<T>(h[j]);
     }
   } else {
-    constexpr float Q = OUT == PD_NORM_E4M3 ? 448.f : 127.f;
+    constexpr float kPerQ = 1.f / (OUT == PD_NORM_E4M3 ? 448.f : 127.f);
+    const long long scale0 = static_cast<long long>(blockIdx.x) * a.scale.of(a.chunk);
     group_reduce(m, nv, a.scale, s_part + a.chunk, s_warp[1], Most());
     uint2* out = static_cast<uint2*>(a.n.out) + base;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       const int i = j * nt + t;
       if (i >= nv) continue;
-      const float s = fmaxf(m[j] / Q, kMinScale);
-      if (i % a.scale.vecs == 0) a.n.out_scale[(base + i) / a.scale.vecs] = s;
-      const float q = 1.f / s;
+      const float s = fmaxf(m[j] * kPerQ, kMinScale);
+      if (a.scale.within(i) == 0) a.n.out_scale[scale0 + a.scale.of(i)] = s;
+      const float q = rcp(s);
 #pragma unroll
       for (int e = 0; e < 8; ++e) h[j][e] *= q;
       out[i] = make_uint2(codes4<OUT>(h[j][0], h[j][1], h[j][2], h[j][3]), codes4<OUT>(h[j][4], h[j][5], h[j][6], h[j][7]));
@@ -271,8 +296,9 @@ __global__ void __launch_bounds__(max_threads(V)) rms_norm_vec_kernel(const VecA
 }
 
 Groups groups_of(int vecs, int chunk) {
-  if (vecs == chunk) return {vecs, kReachCta};
-  return {vecs, vecs <= 32 && (vecs & (vecs - 1)) == 0 ? kReachLanes : kReachShared};
+  const bool pow2 = (vecs & (vecs - 1)) == 0;
+  const uint32_t mul = vecs > 1 ? static_cast<uint32_t>(((1ull << 32) + vecs - 1) / vecs) : 0u;
+  return {vecs, vecs == chunk ? kReachCta : pow2 && vecs <= 32 ? kReachLanes : kReachShared, mul};
 }
 
 template <class T, int OUT, int V>
@@ -292,7 +318,9 @@ pd_status launch_vec(const VecArgs& a, int threads, cudaStream_t s) {
 // Whether the vectorised path takes the call; its chunks, threads and vectors
 // per thread. Short rows are joined to chunks of about 256 vectors. With
 // fewer chunks than SMs a thread takes as few vectors as 1024 threads allow
-// (latency), else four; the widest rows take eight.
+// (latency), else four (8192 x 6144 to e4m3, residual: 54 us, with one / two /
+// three vectors 112 / 59 / 54; 32768 x 6144 without one 125 us, three / eight
+// 134 / 186); the widest rows take eight.
 bool vec_plan(const NormArgs& n, int out_kind, int sms, VecArgs* a, int* threads, int* per) {
   auto off = [](const void* p, uintptr_t mask) { return (reinterpret_cast<uintptr_t>(p) & mask) != 0; };
   const bool codes = out_kind != PD_NORM_SAME;
@@ -310,7 +338,7 @@ bool vec_plan(const NormArgs& n, int out_kind, int sms, VecArgs* a, int* threads
   while (a->chunk > max_threads(*per) * *per) *per *= 2;
   *threads = ((a->chunk + *per - 1) / *per + 31) / 32 * 32;
   a->norm = groups_of(n.norm_size / 8, a->chunk);
-  a->scale = codes ? groups_of(n.scale_size / 8, a->chunk) : Groups{1, kReachLanes};
+  a->scale = codes ? groups_of(n.scale_size / 8, a->chunk) : Groups{1, kReachLanes, 0};
   return true;
 }
 
