@@ -936,14 +936,14 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::kMinBlocks)
 // Joins the partials of every split unit, takes the difference of the two maps
 // and, with a norm, normalises the row.
 //   grid (units, row chunks, heads per tile), NT threads. A thread holds four
-//   dims of one row for MPT maps; RB rows are taken at a time with PG = NT /
-//   (RB * (D / 4) * 2 / MPT) threads per item, which share the item's pieces
-//   (pg, pg + PG, ...) and are joined in pg order, so the result does not depend
-//   on scheduling. Few pieces: both maps in a thread, whose difference is then
-//   its own; many: a map each, so that twice the threads share them. What does
-//   not come from the decode kernel (the unit's layout, lambda, the norm's
-//   weights) is read before the wait for it: the CTA is small enough to sit
-//   beside the decode's.
+//   dims of one row for both maps, so that their difference is its own; RB rows
+//   are taken at a time with PG threads per item, which share the item's pieces
+//   (pg, pg + PG, ...; NB pieces' loads in flight). Adjacent lanes take adjacent
+//   dims (lanes that take adjacent pieces instead touch a line each: B = 1, 64
+//   pieces, 12 -> 19 us). The PG states of an item are scaled by their joint
+//   maximum, which is a row's own, and added in pg order, so the result does not
+//   depend on scheduling. What does not come from the decode kernel (the unit's
+//   layout, lambda, the norm's weights) is read before the wait for it.
 constexpr int kJoinThreads = 384, kJoinThreadsMany = 1024;
 
 struct JoinState {
@@ -963,12 +963,12 @@ __device__ __forceinline__ void join_add(JoinState& s, float2 ml, float4 o) {
   s.l += w * ml.y;
   s.o.x += w * o.x; s.o.y += w * o.y; s.o.z += w * o.z; s.o.w += w * o.w;
 }
-
-template <int D, int NT, int MPT>
-__global__ void __launch_bounds__(NT, NT <= 384 ? 2 : 1) diff_combine_kernel(const DiffParams dp, int RB) {
+template <int D, int NT, int NB>
+__global__ void __launch_bounds__(NT, NT <= 384 ? 2 : 1) diff_combine_kernel(const DiffParams dp, int RB, int PG) {
   const DecodeParams& p = dp.d;
-  constexpr int S4 = D / 4, NB = MPT == 2 ? 3 : 4;
-  __shared__ JoinState s_st[MPT][NT];
+  constexpr int S4 = D / 4;
+  __shared__ float4 s_o[2][NT];
+  __shared__ float2 s_ml[2][NT / S4];  // [map][pg * RB + row]: (m, l), then (weight, joint sum)
   __shared__ float s_ss[NT / 32];
   __shared__ long long s_red[2][NT / 32];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -983,11 +983,7 @@ __global__ void __launch_bounds__(NT, NT <= 384 ? 2 : 1) diff_combine_kernel(con
   const int live = p.G * qn;
   const int chunk = (live + gridDim.y - 1) / gridDim.y;
   const int r_begin = blockIdx.y * chunk, r_end = min(live, r_begin + chunk);
-  const int rows4 = RB * S4;                   // (row, four dims) items
-  const int t = threadIdx.x, width = rows4 * (2 / MPT), PG = NT / width;
-  const int item = t % rows4, pg = t / width;  // (MPT = 1: the second half of a width is map 2)
-  const int map0 = MPT == 1 ? t % width / rows4 : 0;
-  const int j = item / S4, c4 = item % S4;
+  const int t = threadIdx.x, c4 = t % S4, pg = t / S4 / RB, j = t / S4 % RB;  // (pg >= PG: a thread without an item)
   float4 wt = make_float4(1.f, 1.f, 1.f, 1.f);
   if (dp.norm_weight != nullptr)
     wt = make_float4(norm_weight_at(dp, 4 * c4), norm_weight_at(dp, 4 * c4 + 1), norm_weight_at(dp, 4 * c4 + 2),
@@ -999,24 +995,24 @@ __global__ void __launch_bounds__(NT, NT <= 384 ? 2 : 1) diff_combine_kernel(con
   const int rbase = blockIdx.z * p.rows_head, rmap = p.rows_head / 2;
   for (int r0 = r_begin; r0 < r_end; r0 += RB) {
     const int r = r0 + j;
-    if (r0 > r_begin) lam = r < r_end ? __ldg(dp.lambda + kh * p.G + r % p.G) : 0.f;
+    const bool on = pg < PG && r < r_end;
+    if (r0 > r_begin) lam = on ? __ldg(dp.lambda + kh * p.G + r % p.G) : 0.f;
     JoinState st[2];
 #pragma unroll
     for (int m = 0; m < 2; ++m) st[m] = {-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
-    if (r < r_end && pg < PG) {
+    if (on) {
 #pragma unroll 1
       for (int k0 = pg; k0 < P; k0 += NB * PG) {
-        float2 ml[NB][MPT];
-        float4 v[NB][MPT];
+        float2 ml[NB][2];
+        float4 v[NB][2];
 #pragma unroll
         for (int i = 0; i < NB; ++i) {
           const int k = k0 + i * PG;
 #pragma unroll
-          for (int m = 0; m < MPT; ++m) {
+          for (int m = 0; m < 2; ++m) {
             ml[i][m] = make_float2(-INFINITY, 0.f);
             if (k < P) {
-              const long long row =
-                  (k == 0 ? slot0 : slot_base + static_cast<long long>(step) * k) * RP + rbase + (map0 + m) * rmap + r;
+              const long long row = (k == 0 ? slot0 : slot_base + static_cast<long long>(step) * k) * RP + rbase + m * rmap + r;
               ml[i][m] = __ldcg(reinterpret_cast<const float2*>(p.ws_ml + row * 2));
               v[i][m] = __ldcg(reinterpret_cast<const float4*>(p.ws_o + row * D) + c4);
             }
@@ -1025,27 +1021,47 @@ __global__ void __launch_bounds__(NT, NT <= 384 ? 2 : 1) diff_combine_kernel(con
 #pragma unroll
         for (int i = 0; i < NB; ++i)
 #pragma unroll
-          for (int m = 0; m < MPT; ++m) join_add(st[m], ml[i][m], v[i][m]);
+          for (int m = 0; m < 2; ++m) join_add(st[m], ml[i][m], v[i][m]);
       }
     }
-    if (PG > 1 || MPT == 1) {
+    if (PG > 1) {
       if (r0 > r_begin) __syncthreads();  // the last rows' states have been read
 #pragma unroll
-      for (int m = 0; m < MPT; ++m) s_st[m][t] = st[m];
+      for (int m = 0; m < 2; ++m) {
+        s_o[m][t] = st[m].o;
+        if (pg < PG && c4 == 0) s_ml[m][t / S4] = make_float2(st[m].m, st[m].l);
+      }
       __syncthreads();
-      if (t < rows4) {
-        st[0] = s_st[0][t];
-        st[1] = MPT == 1 ? s_st[0][rows4 + t] : s_st[MPT - 1][t];
-#pragma unroll 1
-        for (int k = 1; k < PG; ++k)
+      // a warp per (map, row): the groups' weights and the joint sum
+      const int lane = t & 31;
+      for (int i = t >> 5; i < 2 * RB; i += NT / 32) {
+        float2* ml = &s_ml[i / RB][i % RB];
+        const float2 a = lane < PG ? ml[lane * RB] : make_float2(-INFINITY, 0.f);
+        float M = a.x;
 #pragma unroll
-          for (int m = 0; m < 2; ++m) {
-            const JoinState o = MPT == 1 ? s_st[0][k * width + m * rows4 + t] : s_st[m % MPT][k * width + t];
-            join_add(st[m], make_float2(o.m, o.l), o.o);
+        for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+        const float w = a.x == -INFINITY ? 0.f : ex2(a.x - M);
+        float l = w * a.y;
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+        if (lane < PG) ml[lane * RB] = make_float2(w, l);
+      }
+      __syncthreads();
+      if (pg == 0) {
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+          for (int k = 0; k < PG; ++k) {
+            const float w = s_ml[m][k * RB + j].x;
+            const float4 a = s_o[m][k * RB * S4 + t];
+            o.x += w * a.x; o.y += w * a.y; o.z += w * a.z; o.w += w * a.w;
           }
+          st[m].o = o;
+          st[m].l = s_ml[m][j].y;
+        }
       }
     }
-    const bool on = t < rows4 && r < r_end;
     const float i1 = st[0].l > 0.f ? p.out_scale / st[0].l : 0.f, i2 = st[1].l > 0.f ? p.out_scale / st[1].l * lam : 0.f;
     float4 v = make_float4(st[0].o.x * i1 - st[1].o.x * i2, st[0].o.y * i1 - st[1].o.y * i2,
                            st[0].o.z * i1 - st[1].o.z * i2, st[0].o.w * i1 - st[1].o.w * i2);
@@ -1066,7 +1082,7 @@ __global__ void __launch_bounds__(NT, NT <= 384 ? 2 : 1) diff_combine_kernel(con
       v.z = v.z == 0.f ? 0.f : v.z * f * wt.z;
       v.w = v.w == 0.f ? 0.f : v.w * f * wt.w;
     }
-    if (on)
+    if (on && pg == 0)
       *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(p.out) +
                                 (static_cast<long long>(q0 + r / p.G) * p.Hq + kh * p.G + r % p.G) * D + 4 * c4) =
           make_uint2(pack_out(p.out_bf16 != 0, v.x, v.y), pack_out(p.out_bf16 != 0, v.z, v.w));

@@ -24,7 +24,7 @@ cudaError_t launch_diff(int D, int kv, int ntm, int grouped, const CUtensorMap& 
   }
 }
 
-cudaError_t launch_diff_combine(int D, const DiffParams& p, int n_units, int row_chunks, int rows_at_once, bool many,
+cudaError_t launch_diff_combine(int D, const DiffParams& p, int n_units, int row_chunks, int rows_at_once, int groups, bool many,
                                 cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(n_units), static_cast<unsigned>(row_chunks),
@@ -36,9 +36,9 @@ cudaError_t launch_diff_combine(int D, const DiffParams& p, int n_units, int row
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const auto kernel = D == 128 ? (many ? diff_combine_kernel<128, kJoinThreadsMany, 1> : diff_combine_kernel<128, kJoinThreads, 2>)
-                               : (many ? diff_combine_kernel<256, kJoinThreadsMany, 1> : diff_combine_kernel<256, kJoinThreads, 2>);
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p, rows_at_once);
+  const auto kernel = D == 128 ? (many ? diff_combine_kernel<128, kJoinThreadsMany, 2> : diff_combine_kernel<128, kJoinThreads, 3>)
+                               : (many ? diff_combine_kernel<256, kJoinThreadsMany, 2> : diff_combine_kernel<256, kJoinThreads, 3>);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p, rows_at_once, groups);
   if (e != cudaSuccess) return e;
   return cudaPeekAtLastError();
 }

@@ -11,7 +11,7 @@ namespace pd {
 bool diff_kernel_shape(int D, int kv, int ntm, int grouped, KernelShape* out);
 cudaError_t launch_diff(int D, int kv, int ntm, int grouped, const CUtensorMap& tk, const CUtensorMap& tv,
                         const DiffParams& p, int grid, cudaStream_t stream);
-cudaError_t launch_diff_combine(int D, const DiffParams& p, int n_units, int row_chunks, int rows_at_once, bool many,
+cudaError_t launch_diff_combine(int D, const DiffParams& p, int n_units, int row_chunks, int rows_at_once, int groups, bool many,
                                 cudaStream_t stream);
 
 bool diff_shape_f16(int D, int ntm, int grouped, KernelShape* out);

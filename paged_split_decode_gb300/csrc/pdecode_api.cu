@@ -515,18 +515,17 @@ pd_status decode_paged_diff(const void* q, const void* k_cache, const void* v_ca
   cudaError_t e = launch_diff(dims->D, dims->kv_dtype, pl.nt, pl.hg > 1 ? 1 : 0, tk, tv, p, pl.grid, s);
   if (e == cudaSuccess && pl.n_merge > 0) {
     // rows of a unit's head spread over CTAs while the grid stays within one
-    // CTA per SM (resident beside the decode grid, as the split combine's). A
-    // CTA takes as many rows at a time as leave a thread no more than about
-    // four pieces of an item (one round trip to L2).
+    // CTA per SM. A CTA takes all its rows at once where its threads suffice;
+    // what is left of them share a row's pieces. Units of many pieces (few
+    // units: SMs stand free) take the join of 1024 threads.
     const long long per_unit = pl.splits == 0 ? pl.grid / (pl.units > 0 ? pl.units : 1) + 1 : pl.splits;
     int chunks = p.d.R;
     while (chunks > 1 && pl.n_merge * chunks * pl.hg > pl.sms) chunks = (chunks + 1) / 2;
-    const int rows_cta = (p.d.R + chunks - 1) / chunks;
     const bool many = per_unit > 12;
-    const int at_once = many ? kJoinThreadsMany / (dims->D / 2) : kJoinThreads / (dims->D / 4);
-    const int rows = static_cast<int>(std::max<long long>(
-        1, std::min<long long>(rows_cta, at_once / std::max<long long>(1, (per_unit + 3) / 4))));
-    e = launch_diff_combine(dims->D, p, static_cast<int>(pl.n_merge), chunks, rows, many, s);
+    const int slots = (many ? kJoinThreadsMany : kJoinThreads) / (dims->D / 4);  // (row, piece group) places
+    const int rows = std::min((p.d.R + chunks - 1) / chunks, slots);
+    const int groups = static_cast<int>(std::min<long long>(slots / rows, per_unit));
+    e = launch_diff_combine(dims->D, p, static_cast<int>(pl.n_merge), chunks, rows, groups, many, s);
   }
   return e == cudaSuccess ? PD_OK : PD_ERR_CUDA;
 }
