@@ -180,20 +180,67 @@ def test_bad_tables_and_lengths_raise_bits(pd):
     check(got[2:3], ref[2:3], bound[2:3])
 
 
-def test_a_wait_that_runs_out_reports(pd):
+@pytest.mark.parametrize("Hq,Hkv,qlen,kv", [(8, 4, 1, "f16"), (8, 4, 1, "fp8"), (6, 2, 1, "f16"), (12, 4, 3, "bf16"),
+                                            (12, 2, 3, "int8"), (24, 4, 4, "f16"), (24, 4, 5, "fp8")])
+def test_a_wait_that_runs_out_reports(pd, Hq, Hkv, qlen, kv):
+    """Every kernel shape gives up its waits, reports, and works again."""
     from paged_split_decode_gb300 import binding
-    w = inputs.make_workload(B=2, Hq=8, Hkv=4, D=128, seq_lens=[100, 40], kv="f16", seed=43, scale=0.125)
-    lam, _ = factors(w)
+    w = inputs.make_workload(B=2, Hq=Hq, Hkv=Hkv, D=128, seq_lens=[1000, 40], qlen=qlen, kv=kv, seed=43, scale=0.125)
+    lam, weight = factors(w)
     flag = torch.zeros(1, dtype=torch.int32, device=DEV)
     binding.set_wait_limit_ns(2_000_000)
     binding.set_fault_injection(1)
     try:
-        run(pd, w, lam, flag=flag)
+        for S in (0, 1):
+            run(pd, w, lam, S, weight, flag=flag)
     finally:
         binding.set_fault_injection(0)
         binding.set_wait_limit_ns(0)
     assert int(flag.item()) == pd.DEVERR_TIMEOUT
-    parity(pd, w)
+    parity(pd, w, norm=True)
+
+
+@pytest.mark.parametrize("scale", (-0.125, 0.0, 1.5))
+@pytest.mark.parametrize("kv", ("f16", "fp8_bf16q", "int8"))
+def test_scales(pd, kv, scale):
+    """A negative factor, none, and one that makes the maps peaked (scores of
+    up to about 60: the fp32 part of the bound, 2^-13 for scores whose terms sum
+    to less than 11, grows with them)."""
+    w = inputs.make_workload(B=2, Hq=8, Hkv=4, D=128, seq_lens=[300, 37], kv=kv, seed=61, scale=scale)
+    lam, _ = factors(w)
+    got = run(pd, w, lam)
+    ref, bound = ref_diff.reference(w, lam.double().numpy())
+    check(got, ref, bound * (12.0 if scale > 1 else 1.0))
+
+
+def test_rising_scores_raise_the_reference(pd):
+    """Keys that grow along the sequence: every tile passes the running maximum,
+    by little and by much."""
+    w = inputs.make_workload(B=2, Hq=8, Hkv=4, D=128, seq_lens=[600, 91], kv="f16", seed=67, scale=0.125)
+    ramp = torch.linspace(0.0, 3.0, 600)
+    for b, L in enumerate((600, 91)):
+        for j in range(L):
+            w.k_cache[int(w.block_table[b, j // 16]), j % 16] *= ramp[j]
+    for S in (0, 1, 3):
+        lam, _ = factors(w)
+        ref, bound = ref_diff.reference(w, lam.double().numpy())
+        check(run(pd, w, lam, S), ref, 4.0 * bound)  # (rows three times as large: scores' fp32 part with them)
+
+
+def test_offsets_past_32_bits(pd):
+    """Blocks at the end of caches of about 10 GB each give what the same
+    blocks give in a small cache."""
+    w = inputs.make_workload(B=2, Hq=8, Hkv=4, D=256, seq_lens=[333, 64], kv="f16", seed=71, scale=128 ** -0.5)
+    lam, weight = factors(w)
+    want = run(pd, w, lam, 0, weight)
+    n, pool = 300_000, w.k_cache.shape[0]
+    big = [torch.empty(n, 16, 4, 256, dtype=torch.float16, device=DEV) for _ in range(2)]
+    for c, small in zip(big, (w.k_cache, w.v_cache)):
+        c[n - pool:] = small.to(DEV)
+    table = torch.where(w.block_table >= 0, w.block_table + (n - pool), w.block_table).int()
+    got = pd.decode_paged_diff(w.q.to(DEV), *big, table.to(DEV), w.seq_lens.to(DEV), lam.to(DEV), w.scale,
+                               norm_weight=weight.to(DEV))
+    assert torch.equal(got, want)
 
 
 def test_two_streams_and_two_captured_graphs(pd):
