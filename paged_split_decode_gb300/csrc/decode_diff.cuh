@@ -402,7 +402,6 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::kMinBlocks)
               ldsm_x4((km ^ ((ksl & 3) * 32)) + (ksl >> 2) * Cfg::kSlabBytes, a);
 #pragma unroll
               for (int n = 0; n < NTR; ++n) {
-                if (NTM % Cfg::RG != 0 && n == NTR - 1 && rt0 + n >= NTM) continue;
                 if (ksl & 1) mma_op<BF16>(sb[m][n], a, qf[m][ksl][n][0], qf[m][ksl][n][1]);
                 else mma_op<BF16>(sa[m][n], a, qf[m][ksl][n][0], qf[m][ksl][n][1]);
               }
@@ -430,7 +429,6 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::kMinBlocks)
                 a[3] = byte_pair_to_half2<Cfg::KV>(xb, true);
 #pragma unroll
                 for (int n = 0; n < NTR; ++n) {
-                  if (NTM % Cfg::RG != 0 && n == NTR - 1 && rt0 + n >= NTM) continue;
                   if (i & 1) mma_op<BF16>(sb[m][n], a, qf[m][ksl][n][0], qf[m][ksl][n][1]);
                   else mma_op<BF16>(sa[m][n], a, qf[m][ksl][n][0], qf[m][ksl][n][1]);
                 }
