@@ -15,8 +15,8 @@
 //
 // Latency-bound: a few bytes per sequence and 12 per token. One launch of one
 // thread-block cluster: every CTA reads all lengths and scans them (each
-// thread a run of consecutive sequences, then one block scan), which costs
-// less than a second launch; the cluster barrier then makes the in-place
+// thread a run of consecutive sequences, then one block scan of one barrier),
+// which costs less than a second launch; the cluster barrier then makes the in-place
 // forms safe (seq_lens over context_lens, the count over itself), since no
 // CTA writes before all have read. Tokens and blocks are dealt to the
 // cluster's warps in contiguous shares: a lane finds its first item's sequence
@@ -32,8 +32,6 @@
 namespace pd {
 namespace {
 
-constexpr int kTabThreads = 1024;
-constexpr int kTabWarps = kTabThreads / 32;
 constexpr int kMaxTableB = 16384;  // three ints per sequence in shared memory
 constexpr uint32_t kSatMax = 0x7fffffffu;
 
@@ -41,33 +39,37 @@ constexpr uint32_t kSatMax = 0x7fffffffu;
 // them is well defined however the lengths overflow.
 __device__ __forceinline__ uint32_t sat_add(uint32_t a, uint32_t b) { return min(a + b, kSatMax); }
 
-// Exclusive scan over the block of one value per thread; `total` gets the sum.
-__device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t (&s_warp)[kTabWarps], uint32_t& total) {
+// Exclusive scans over the block of K values per thread at once; `total` gets
+// the sums. One barrier: every warp scans the warps' sums for itself.
+template <int NT, int K>
+__device__ __forceinline__ void block_scan(uint32_t (&v)[K], uint32_t (&s_warp)[K][32], uint32_t (&total)[K]) {
+  constexpr int NW = NT / 32;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  uint32_t x = v;
+  uint32_t x[K];
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x = sat_add(x, y);
-  }
-  const uint32_t prev = __shfl_up_sync(0xffffffffu, x, 1);
-  if (lane == 31) s_warp[warp] = x;
-  __syncthreads();
-  if (warp == 0) {
-    uint32_t w = s_warp[lane];
+  for (int k = 0; k < K; ++k) {
+    x[k] = v[k];
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t y = __shfl_up_sync(0xffffffffu, x[k], o);
+      if (lane >= o) x[k] = sat_add(x[k], y);
+    }
+    if (lane == 31) s_warp[k][warp] = x[k];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    uint32_t w = lane < NW ? s_warp[k][lane] : 0u;
+#pragma unroll
+    for (int o = 1; o < NW; o <<= 1) {
       const uint32_t y = __shfl_up_sync(0xffffffffu, w, o);
       if (lane >= o) w = sat_add(w, y);
     }
-    s_warp[lane] = w;
+    total[k] = __shfl_sync(0xffffffffu, w, NW - 1);
+    const uint32_t before = __shfl_sync(0xffffffffu, w, warp > 0 ? warp - 1 : 0);
+    const uint32_t prev = __shfl_up_sync(0xffffffffu, x[k], 1);
+    v[k] = sat_add(warp > 0 ? before : 0u, lane > 0 ? prev : 0u);
   }
-  __syncthreads();
-  total = s_warp[kTabWarps - 1];
-  const uint32_t base = warp > 0 ? s_warp[warp - 1] : 0u;
-  const uint32_t r = sat_add(base, lane > 0 ? prev : 0u);
-  __syncthreads();  // s_warp free again
-  return r;
 }
 
 // The sequence whose range holds x: the largest b with pre[b] <= x, given
@@ -93,17 +95,17 @@ __device__ __forceinline__ void raise_bits(uint32_t* flag, uint32_t bits) {
 // every 32nd of its warp's: `item` is called with each k, in increasing order,
 // kBatch of them between two calls of `flush`.
 constexpr int kBatch = 8;
-template <class Item, class Flush>
+template <int NT, class Item, class Flush>
 __device__ __forceinline__ void deal(int n, int rank, int ranks, Item item, Flush flush) {
-  if (n <= ranks * kTabThreads) {  // one item a thread
-    const int k = rank * kTabThreads + static_cast<int>(threadIdx.x);
+  if (n <= ranks * NT) {  // one item a thread
+    const int k = rank * NT + static_cast<int>(threadIdx.x);
     if (k < n) {
       item(k, 0);
       flush(k, 0);
     }
     return;
   }
-  const int warps = ranks * kTabWarps, warp = rank * kTabWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const int warps = ranks * (NT / 32), warp = rank * (NT / 32) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   const int share = ((n + warps - 1) / warps + 31) / 32 * 32;
   const long long first = static_cast<long long>(warp) * share;
   const int end = static_cast<int>(min(static_cast<long long>(n), first + share));
@@ -146,18 +148,19 @@ struct TableArgs {
 };
 
 // Shared: s_start[B + 1], s_off[B + 1], s_ctx[B] (-1: the sequence is refused).
-__global__ void __launch_bounds__(kTabThreads, 1) build_tables_kernel(const TableArgs a) {
+template <int NT>
+__global__ void __launch_bounds__(NT, 1) build_tables_kernel(const TableArgs a) {
   extern __shared__ int s_dyn[];
   int* s_start = s_dyn;
   int* s_off = s_start + a.B + 1;
   int* s_ctx = s_off + a.B + 1;
-  __shared__ uint32_t s_warp[kTabWarps];
+  __shared__ uint32_t s_warp[2][32];
   __shared__ int s_taken;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int t = threadIdx.x, rank = blockIdx.x, ranks = gridDim.x;
   const long long cap = static_cast<long long>(a.max_blocks) * a.bs;
-  const int per = (a.B + kTabThreads - 1) / kTabThreads;
+  const int per = (a.B + NT - 1) / NT;
   const int b0 = min(a.B, t * per), b1 = min(a.B, b0 + per);
   uint32_t bits = 0;
   int count = *a.count_in;
@@ -179,9 +182,9 @@ __global__ void __launch_bounds__(kTabThreads, 1) build_tables_kernel(const Tabl
     qs = sat_add(qs, q > 0 ? q : 0);
     ns = sat_add(ns, need);
   }
-  uint32_t q_total, n_total;
-  uint32_t q_run = block_scan(qs, s_warp, q_total);
-  uint32_t n_run = block_scan(ns, s_warp, n_total);
+  uint32_t run[2] = {qs, ns}, total[2];
+  block_scan<NT, 2>(run, s_warp, total);
+  uint32_t q_run = run[0], n_run = run[1];
   int taken = 0;
   for (int b = b0; b < b1; ++b) {
     const uint32_t q = s_start[b], need = s_off[b];
@@ -203,14 +206,14 @@ __global__ void __launch_bounds__(kTabThreads, 1) build_tables_kernel(const Tabl
     n_run = ne;
   }
   if (t == 0) {
-    s_start[a.B] = static_cast<int>(q_total);
-    s_off[a.B] = static_cast<int>(n_total);
+    s_start[a.B] = static_cast<int>(total[0]);
+    s_off[a.B] = static_cast<int>(total[1]);
   }
   if (taken) atomicMax(&s_taken, taken);
   cluster_sync();  // (and a block barrier) every CTA has read its inputs
   taken = s_taken;
 
-  const int nt = ranks * kTabThreads, me = rank * kTabThreads + t;
+  const int nt = ranks * NT, me = rank * NT + t;
   for (int b = me; b <= a.B; b += nt) {
     a.q_start[b] = s_start[b];
     if (b < a.B) {
@@ -224,7 +227,7 @@ __global__ void __launch_bounds__(kTabThreads, 1) build_tables_kernel(const Tabl
   {
     int b = -1, blk[kBatch];
     long long at[kBatch];
-    deal(taken, rank, ranks,
+    deal<NT>(taken, rank, ranks,
          [&](int k, int j) {
            b = next_seq(s_off, a.B, k, b);
            blk[j] = a.free_blocks[count - 1 - k];
@@ -239,7 +242,7 @@ __global__ void __launch_bounds__(kTabThreads, 1) build_tables_kernel(const Tabl
   const int live = min(s_start[a.B], a.T);
   {
     int b = -1, blk[kBatch], pos[kBatch];
-    deal(a.T, rank, ranks,
+    deal<NT>(a.T, rank, ranks,
          [&](int k, int j) {
            pos[j] = -1;
            if (k >= live) return;
@@ -277,17 +280,18 @@ struct ReleaseArgs {
 };
 
 // Shared: s_off[B + 1], s_len[B] (the length to write).
-__global__ void __launch_bounds__(kTabThreads, 1) release_kernel(const ReleaseArgs a) {
+template <int NT>
+__global__ void __launch_bounds__(NT, 1) release_kernel(const ReleaseArgs a) {
   extern __shared__ int s_dyn[];
   int* s_off = s_dyn;
   int* s_len = s_off + a.B + 1;
-  __shared__ uint32_t s_warp[kTabWarps];
+  __shared__ uint32_t s_warp[1][32];
   __shared__ int s_given;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int t = threadIdx.x, rank = blockIdx.x, ranks = gridDim.x;
   const long long cap = static_cast<long long>(a.max_blocks) * a.bs;
-  const int per = (a.B + kTabThreads - 1) / kTabThreads;
+  const int per = (a.B + NT - 1) / NT;
   const int b0 = min(a.B, t * per), b1 = min(a.B, b0 + per);
   uint32_t bits = 0;
   int count = *a.count_in;
@@ -308,8 +312,9 @@ __global__ void __launch_bounds__(kTabThreads, 1) release_kernel(const ReleaseAr
     s_off[b] = n;
     ns = sat_add(ns, n);
   }
-  uint32_t n_total;
-  uint32_t n_run = block_scan(ns, s_warp, n_total);
+  uint32_t run[1] = {ns}, total[1];
+  block_scan<NT, 1>(run, s_warp, total);
+  uint32_t n_run = run[0];
   int given = 0;
   for (int b = b0; b < b1; ++b) {
     const uint32_t n = s_off[b], ne = sat_add(n_run, n);
@@ -323,15 +328,15 @@ __global__ void __launch_bounds__(kTabThreads, 1) release_kernel(const ReleaseAr
     }
     n_run = ne;
   }
-  if (t == 0) s_off[a.B] = static_cast<int>(n_total);
+  if (t == 0) s_off[a.B] = static_cast<int>(total[0]);
   if (given) atomicMax(&s_given, given);
   cluster_sync();
   given = s_given;
-  const int nt = ranks * kTabThreads, me = rank * kTabThreads + t;
+  const int nt = ranks * NT, me = rank * NT + t;
   for (int b = me; b < a.B; b += nt) a.lens_out[b] = s_len[b];
   if (me == 0) *a.count_out = count + given;
   int b = -1, blk[kBatch];
-  deal(given, rank, ranks,
+  deal<NT>(given, rank, ranks,
        [&](int k, int j) {
          b = next_seq(s_off, a.B, k, b);
          blk[j] = a.table[static_cast<long long>(b) * a.max_blocks + (k - s_off[b])];
@@ -357,25 +362,41 @@ pd_status check_table_dims(const pd_dims* d) {
 
 bool misaligned(const void* p, uintptr_t mask) { return (reinterpret_cast<uintptr_t>(p) & mask) != 0; }
 
-// One cluster of `ctas` CTAs: 1, 8 (the portable size) or, where the device runs
-// such a cluster, 16.
-template <class Kern, class Args>
-pd_status launch_cluster(Kern kernel, unsigned long long (&done)[64], unsigned long long (&done_occ)[64],
-                         int (&cache)[64][kMaxCluster + 1], int ctas, size_t smem, cudaStream_t s, const Args& args) {
+// One cluster of `ctas` CTAs of NT threads: 1, 8 (the portable size) or, where
+// the device runs such a cluster, 16.
+template <int NT, class Kern, class Args>
+pd_status launch_cluster(Kern kernel, int ctas, size_t smem, cudaStream_t s, const Args& args) {
+  static unsigned long long done[64] = {}, done_occ[64] = {};
+  static int cache[64][kMaxCluster + 1] = {};
   const int most = (3 * kMaxTableB + 2) * 4;
   if (once_per_context(done, [&] { return set_kernel_attributes(kernel, most); }) != cudaSuccess) return PD_ERR_CUDA;
   if (ctas > 8) {
     int counts[kMaxCluster + 1];
-    max_active_clusters(kernel, kTabThreads, most, done_occ, cache, counts);
+    max_active_clusters(kernel, NT, most, done_occ, cache, counts);
     if (counts[ctas] < 1) ctas = 8;
   }
-  return launch_pdl(kernel, ctas, kTabThreads, static_cast<int>(smem), s, ctas, args) == cudaSuccess ? PD_OK
-                                                                                                    : PD_ERR_CUDA;
+  return launch_pdl(kernel, ctas, NT, static_cast<int>(smem), s, ctas, args) == cudaSuccess ? PD_OK : PD_ERR_CUDA;
 }
 
-// CTAs for `items` dealt out to the threads. More than one costs a cluster launch
-// and barrier, more than eight a place for 16 CTAs at once.
-int table_ctas(long long items) { return items <= kTabThreads ? 1 : items <= 8 * kTabThreads ? 8 : 16; }
+// At most 256 sequences and items (one a thread): one CTA of 256 threads, whose
+// launch and barriers are shorter (32 sequences of one token 3.6 -> 3.2 us; with
+// several items a thread it loses: 1000 tokens 4.2 -> 6.5). Else CTAs of 1024
+// for the `items` dealt out to the threads: more than one costs a cluster launch
+// and barrier, more than eight a place for 16 CTAs (32768 tokens 7.3 -> 5.9 us,
+// 262144 released blocks 12.2 -> 8.3 against eight).
+bool few_items(int B, long long items) { return B <= 256 && items <= 256; }
+int table_ctas(long long items) { return items <= 1024 ? 1 : items <= 8 * 1024 ? 8 : 16; }
+
+template <class Args>
+pd_status launch_build(const Args& a, size_t smem, cudaStream_t s) {
+  if (few_items(a.B, a.T)) return launch_cluster<256>(build_tables_kernel<256>, 1, smem, s, a);
+  return launch_cluster<1024>(build_tables_kernel<1024>, table_ctas(a.T), smem, s, a);
+}
+template <class Args>
+pd_status launch_release(const Args& a, long long blocks, size_t smem, cudaStream_t s) {
+  if (few_items(a.B, blocks)) return launch_cluster<256>(release_kernel<256>, 1, smem, s, a);
+  return launch_cluster<1024>(release_kernel<1024>, table_ctas(blocks), smem, s, a);
+}
 
 }  // namespace
 }  // namespace pd
@@ -404,10 +425,7 @@ extern "C" pd_status build_block_tables(const int32_t* context_lens, const int32
   TableArgs a{context_lens, query_lens, block_table, free_blocks, free_count, free_count_out, seq_lens,
               query_start_loc, slot_mapping, positions, error_flag, d.B, num_tokens, d.block_size, d.num_blocks,
               d.max_blocks_per_seq};
-  static unsigned long long done[64] = {}, done_occ[64] = {};
-  static int cache[64][kMaxCluster + 1] = {};
-  return launch_cluster(build_tables_kernel, done, done_occ, cache, table_ctas(num_tokens), (3 * static_cast<size_t>(d.B) + 2) * 4,
-                        static_cast<cudaStream_t>(stream), a);
+  return launch_build(a, (3 * static_cast<size_t>(d.B) + 2) * 4, static_cast<cudaStream_t>(stream));
 }
 
 extern "C" pd_status release_blocks(const int32_t* block_table, const int32_t* seq_lens, const uint8_t* released,
@@ -426,9 +444,6 @@ extern "C" pd_status release_blocks(const int32_t* block_table, const int32_t* s
     return PD_ERR_ALIGN;
   ReleaseArgs a{block_table, seq_lens, released, free_blocks, free_count, free_count_out, seq_lens_out, error_flag,
                 d.B, d.block_size, d.num_blocks, d.max_blocks_per_seq};
-  static unsigned long long done[64] = {}, done_occ[64] = {};
-  static int cache[64][kMaxCluster + 1] = {};
   const long long blocks = static_cast<long long>(d.B) * d.max_blocks_per_seq;
-  return launch_cluster(release_kernel, done, done_occ, cache, table_ctas(blocks), (2 * static_cast<size_t>(d.B) + 1) * 4,
-                        static_cast<cudaStream_t>(stream), a);
+  return launch_release(a, blocks, (2 * static_cast<size_t>(d.B) + 1) * 4, static_cast<cudaStream_t>(stream));
 }
