@@ -52,6 +52,7 @@ bool diff_shape_of(KernelShape* out) {
   out->rows_padded = Cfg::RP;
   out->ctas_per_sm = Cfg::kMinBlocks;
   out->heads = Cfg::HG;
+  out->key_groups = Cfg::KG;
   // what a piece's end costs, in tiles: 1 us from the accumulators, 5 us where key
   // groups merge first (measured, D = 256 GQA 6:1, L = 8192, B = 8, qlen = 3, 4 /
   // 10 / 16 / 24 / 48 tiles: fp16 61.0 / 59.2 / 57.2 / 56.8 / 57.5 us, e4m3 64.0 /

@@ -161,9 +161,21 @@ pd_status make_plan(const pd_dims* d, int qlen, int num_splits, int sm_count, Pl
   if (splits == 0 && d->B > kMaxAutoB) splits = 1;  // plenty of units: one piece each
   const int ctas = sms * ks.ctas_per_sm;  // persistent grid: every resident CTA slot
   const bool automatic = splits == 0;
-  if (automatic && pl->units > 0 && pl->units <= ctas / 4) {
-    const long long cap_keys = static_cast<long long>(d->max_blocks_per_seq) * d->block_size;
-    const long long vis_keys = window > 0 ? std::min<long long>(cap_keys, window + qlen + kTileKeys) : cap_keys;
+  const long long cap_keys = static_cast<long long>(d->max_blocks_per_seq) * d->block_size;
+  const long long vis_keys = window > 0 ? std::min<long long>(cap_keys, 0ll + window + qlen + kTileKeys) : cap_keys;
+  // Short tables: whole units one per CTA walk (waves - units / ctas) * tiles more
+  // than the balanced split does and launch no join, whose launch and reads cost
+  // four steps of the key groups or more. Balanced -> whole units (B = 48): fp16 D =
+  // 256, 96 units, 1 / 4 / 8 / 16 tiles: 9.2 / 12.2 / 13.5 / 16.7 -> 6.9 / 9.3 /
+  // 12.6 / 19.3 us; e4m3 qlen = 3, 384 units, 8 / 16 tiles: 32.5 / 36.2 -> 23.6 /
+  // 29.4 us; B = 1, three key groups, 8 / 16 tiles: 8.3 / 8.4 -> 7.4 / 8.8 us. Eight
+  // steps at most: a batch with one long sequence then waits four steps longer.
+  if (automatic && diff && pl->units > 0) {
+    const long long waves = (pl->units + ctas - 1) / ctas;
+    const long long tiles = (vis_keys + kTileKeys - 1) / kTileKeys;
+    if (tiles <= 8 * ks.key_groups && tiles * (waves * ctas - pl->units) <= 4ll * ctas * ks.key_groups) splits = 1;
+  }
+  if (splits == 0 && pl->units > 0 && pl->units <= ctas / 4) {
     const long long tiles = pl->units * (vis_keys / kTileKeys + 1);
     if (tiles <= 24ll * ctas || ks.fixed_pieces)
       splits = static_cast<int>(std::max<long long>(1, (ctas * 27 / 32) / pl->units));
