@@ -2,6 +2,7 @@
 // differential decode's instantiation units (one per cache element kind).
 #pragma once
 #include "decode_diff.cuh"
+#include "decode_diff_tc.cuh"
 #include "launch.h"
 
 namespace pd {
@@ -52,7 +53,8 @@ bool diff_shape_of(KernelShape* out) {
   out->rows_padded = Cfg::RP;
   out->ctas_per_sm = Cfg::kMinBlocks;
   out->heads = Cfg::HG;
-  out->key_groups = Cfg::KG;
+  out->step_tiles = Cfg::KG;
+  out->whole_tile = 1;
   // what a piece's end costs, in tiles: 1 us from the accumulators, 5 us where key
   // groups merge first (measured, D = 256 GQA 6:1, L = 8192, B = 8, qlen = 3, 4 /
   // 10 / 16 / 24 / 48 tiles: fp16 61.0 / 59.2 / 57.2 / 56.8 / 57.5 us, e4m3 64.0 /
@@ -93,13 +95,29 @@ struct DiffShapes {
   using C3 = DiffCfgFor<D, KV, 3, 1, 4, 2, 2, 1>;
   using C4 = DiffCfgFor<D, KV, 4, 1, 4, 2, 1, 1>;
 
+  // byte caches, two or more row tiles per map, where shared memory holds it: the
+  // tensor-memory kernel
+  template <class C>
+  static constexpr bool kTc = KV == kKvFp8 || (KV == kKvInt8 && (D == 128 || C::NTM < 4));
+  template <class C>
+  static bool rows_shape(KernelShape* out) {
+    if constexpr (kTc<C>) return diff_tc_shape_of<DiffTc<D, KV, C::NTM>>(out);
+    else return diff_shape_of<C>(out);
+  }
+  template <class C>
+  static cudaError_t rows_launch(const CUtensorMap& tk, const CUtensorMap& tv, const DiffParams& p, int grid,
+                                 cudaStream_t s) {
+    if constexpr (kTc<C>) return launch_diff_tc<DiffTc<D, KV, C::NTM>>(tk, tv, p, grid, s);
+    else return diff_launch_cfg<C>(tk, tv, p, grid, s);
+  }
+
   static bool shape(int ntm, int grouped, KernelShape* out) {
     if (grouped) return ntm == 1 && diff_shape_of<C1H>(out);
     switch (ntm) {
       case 1: return diff_shape_of<C1>(out);
-      case 2: return diff_shape_of<C2>(out);
-      case 3: return diff_shape_of<C3>(out);
-      case 4: return diff_shape_of<C4>(out);
+      case 2: return rows_shape<C2>(out);
+      case 3: return rows_shape<C3>(out);
+      case 4: return rows_shape<C4>(out);
       default: return false;
     }
   }
@@ -108,9 +126,9 @@ struct DiffShapes {
     if (grouped) return ntm == 1 ? diff_launch_cfg<C1H>(tk, tv, p, grid, s) : cudaErrorInvalidValue;
     switch (ntm) {
       case 1: return diff_launch_cfg<C1>(tk, tv, p, grid, s);
-      case 2: return diff_launch_cfg<C2>(tk, tv, p, grid, s);
-      case 3: return diff_launch_cfg<C3>(tk, tv, p, grid, s);
-      case 4: return diff_launch_cfg<C4>(tk, tv, p, grid, s);
+      case 2: return rows_launch<C2>(tk, tv, p, grid, s);
+      case 3: return rows_launch<C3>(tk, tv, p, grid, s);
+      case 4: return rows_launch<C4>(tk, tv, p, grid, s);
       default: return cudaErrorInvalidValue;
     }
   }

@@ -18,7 +18,8 @@ struct KernelShape {
   int unit_cost;    // balanced split: virtual tiles charged to every unit start
   int fixed_pieces; // 1: a piece has a large fixed cost (set-up, pipeline refill, epilogue), so
                     // an automatic plan over few units takes the fixed split (one piece per CTA)
-  int key_groups = 1;  // groups of warps that walk every key_groups-th tile (the plan of short tables)
+  int whole_tile = 0;  // 1: a TMA box is a tile of all slabs (4-D map), else one slab of it
+  int step_tiles = 1;  // tiles that a CTA takes at once (the plan of short tables)
   int max_clusters[17];  // [S]: clusters of S CTAs the device runs at once (0: no cluster merge)
 };
 

@@ -71,6 +71,7 @@ struct Plan {
   long long units;  // B * Hkv / hg work units
   int rows_padded;
   int unit_cost;    // balanced split: virtual tiles per unit start
+  bool whole_tile;  // a TMA box is a tile of all slabs
   int cluster;      // > 1: the fixed split's pieces of a unit form a cluster that merges them
   int sms;          // SMs of the device the plan was made for
   size_t off_ml, off_o, bytes;  // workspace layout
@@ -156,6 +157,7 @@ pd_status make_plan(const pd_dims* d, int qlen, int num_splits, int sm_count, Pl
   pl->hg = ks.heads;
   pl->rows_padded = ks.rows_padded;
   pl->unit_cost = ks.unit_cost;
+  pl->whole_tile = ks.whole_tile != 0;
   pl->units = static_cast<long long>(d->B) * (d->Hkv / pl->hg);
   int splits = num_splits;
   if (splits == 0 && d->B > kMaxAutoB) splits = 1;  // plenty of units: one piece each
@@ -165,7 +167,7 @@ pd_status make_plan(const pd_dims* d, int qlen, int num_splits, int sm_count, Pl
   const long long vis_keys = window > 0 ? std::min<long long>(cap_keys, 0ll + window + qlen + kTileKeys) : cap_keys;
   // Short tables: whole units one per CTA walk (waves - units / ctas) * tiles more
   // than the balanced split does and launch no join, whose launch and reads cost
-  // four steps of the key groups or more. Balanced -> whole units (B = 48): fp16 D =
+  // four steps or more. Balanced -> whole units (B = 48): fp16 D =
   // 256, 96 units, 1 / 4 / 8 / 16 tiles: 9.2 / 12.2 / 13.5 / 16.7 -> 6.9 / 9.3 /
   // 12.6 / 19.3 us; e4m3 qlen = 3, 384 units, 8 / 16 tiles: 32.5 / 36.2 -> 23.6 /
   // 29.4 us; B = 1, three key groups, 8 / 16 tiles: 8.3 / 8.4 -> 7.4 / 8.8 us. Eight
@@ -173,7 +175,7 @@ pd_status make_plan(const pd_dims* d, int qlen, int num_splits, int sm_count, Pl
   if (automatic && diff && pl->units > 0) {
     const long long waves = (pl->units + ctas - 1) / ctas;
     const long long tiles = (vis_keys + kTileKeys - 1) / kTileKeys;
-    if (tiles <= 8 * ks.key_groups && tiles * (waves * ctas - pl->units) <= 4ll * ctas * ks.key_groups) splits = 1;
+    if (tiles <= 8 * ks.step_tiles && tiles * (waves * ctas - pl->units) <= 4ll * ctas * ks.step_tiles) splits = 1;
   }
   if (splits == 0 && pl->units > 0 && pl->units <= ctas / 4) {
     const long long tiles = pl->units * (vis_keys / kTileKeys + 1);
@@ -372,7 +374,7 @@ pd_status prepare_decode(const void* q, const void* k_cache, const void* v_cache
     if (reinterpret_cast<uintptr_t>(workspace) & 255u) return PD_ERR_ALIGN;
   }
 
-  if (!encode_cache_map(&tk, k_cache, dims, pl.hg, diff) || !encode_cache_map(&tv, v_cache, dims, pl.hg, diff))
+  if (!encode_cache_map(&tk, k_cache, dims, pl.hg, pl.whole_tile) || !encode_cache_map(&tv, v_cache, dims, pl.hg, pl.whole_tile))
     return PD_ERR_CUDA;
 
   const bool fp8 = byte_kind(dims->kv_dtype);  // scaled codes

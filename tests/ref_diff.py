@@ -8,11 +8,15 @@ weight is rounded to it before P.V, so map m is off by at most u A_m, A_m =
 sum_j w_j |v_j| (the oracle run on |V|). The fp32 parts: a score sums D / 2
 products, off by at most (D / 2) 2^-24 sum |q_d k_d| scale < 2^-13 for the
 N(0, 1) rows drawn here, which moves a weight by that relative amount, and
-exponentials, rescalings and sums stay below it: 2^-12 A_m together. So
+exponentials, rescalings and sums stay below it: 2^-12 A_m together. With e4m3
+caches and several query rows per head, q enters as e4m3 terms that leave at
+most 2^-17 max|q| of elements below 2^-6 max|q| (N(0, 1): fewer than a quarter
+of a half row's 64 or 128); a score then moves by less than 2^-17 5.5 32 0.8
+128^-1/2 < 2^-13 more, so 2^-11 stands for all of it there (f). So
 
-    d = (u + 2^-12) (A_1 + |lambda| A_2),   |gpu - ref| <= d + u_out |ref|
+    d = (u + f) (A_1 + |lambda| A_2),   |gpu - ref| <= d + u_out |ref|
 
-with u_out the half step of the output type. The norm gives y = o f w, f = gain
+with f = 2^-12, or 2^-11 for e4m3, and u_out the half step of the output type. The norm gives y = o f w, f = gain
 / sqrt(mean o^2 + eps); with e = rms(d) over the row, the computed row's rms
 is within e of o's, so f lies between f_lo and f_hi, its values at rms(o) + e
 and max(rms(o) - e, 0), and
@@ -69,7 +73,7 @@ def reference(w, lam, norm_weight=None, eps=1e-5, gain=1.0):
         out = out + c * _oracle(w, qm, as_np(w.v_cache))
         va = _abs_codes(w)
         bound = bound + np.abs(c) * _oracle(w, qm, va.view(np.float16) if va.dtype == np.uint16 and not w.bf16 else va)
-    bound = (u + 2.0 ** -12) * bound
+    bound = (u + 2.0 ** (-11 if w.kv_fp8 else -12)) * bound
     if norm_weight is not None:
         rms = np.sqrt(np.mean(out ** 2, axis=-1, keepdims=True))
         e = np.sqrt(np.mean(bound ** 2, axis=-1, keepdims=True))
