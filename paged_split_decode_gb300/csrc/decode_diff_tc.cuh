@@ -89,6 +89,10 @@ struct DiffTc {
   // maxima, 300 with 3.)
   static constexpr float kRaise = CODES ? 3.f : 4.f;
   static constexpr float kBias = CODES ? -kRaise : 4.f;
+  // The row state holds the threshold m + kRaise. Before the first visible key m is a
+  // number below every score, so that nothing need be told apart: the exponential
+  // of a masked score (-inf) against it is zero.
+  static constexpr float kNone = -3e38f;
   static constexpr int kUnitCost = 24;                // a piece's fixed cost in 16-key tiles (balanced split)
 
   static constexpr int kOffV = NBK * kBlkBytes;
@@ -97,7 +101,7 @@ struct DiffTc {
   static constexpr int kOffPt = kOffQ + kQSlabs * kQSlab;
   static constexpr int kOffRed = kOffPt + kPtBytes;          // float [NG][4 warps][16]
   static constexpr int kOffRow = kOffRed + NG * 4 * 16 * 4;  // row state, [NG][map][8]: score factor,
-  static constexpr int kFs = 0, kMu = kON, kAl = 2 * kON, kL = 3 * kON;  // maximum, rescale, sum;
+  static constexpr int kFs = 0, kTh = kON, kAl = 2 * kON, kL = 3 * kON;  // threshold, rescale, sum;
   static constexpr int kLo = 4 * kON, kHi = kLo + kRows, kFlag = kHi + kRows;  // [NG][8]: visible range; a flag
   static constexpr int kOffBars = (kOffRow + (kFlag + NG) * 4 + 15) / 16 * 16;
   // barriers: fullK, emptyK [NBK], fullV, emptyV [NBV], then these (kBarS2: S^T
@@ -221,7 +225,7 @@ __device__ __forceinline__ void diff_tc_softmax(const DiffParams& dp, const int*
   float* rf = reinterpret_cast<float*>(smem + T::kOffRow);
   int* ri = reinterpret_cast<int*>(smem + T::kOffRow);
   float* red = reinterpret_cast<float*>(smem + T::kOffRed) + 64 * g;  // [4 warps][16]
-  float *fs_row = rf + T::kFs + 16 * g, *mu_row = rf + T::kMu + 16 * g, *al_row = rf + T::kAl + 16 * g,
+  float *fs_row = rf + T::kFs + 16 * g, *th_row = rf + T::kTh + 16 * g, *al_row = rf + T::kAl + 16 * g,
         *l_row = rf + T::kL + 16 * g;
   const int *lo_row = ri + T::kLo + 8 * g, *hi_row = ri + T::kHi + 8 * g;
   const uint32_t fullk0 = sbase + T::kOffBars, emptyk0 = fullk0 + 8 * NBK;
@@ -369,7 +373,7 @@ __device__ __forceinline__ void diff_tc_softmax(const DiffParams& dp, const int*
       if ((part & 3) == 0) {
         const int at = 16 * (r >> 3) + 8 * (part >> 2) + (r & 7);
         rf[T::kFs + at] = r < pq.R ? p.sl2 * pow2f(-e) : 0.f;
-        rf[T::kMu + at] = -INFINITY;
+        rf[T::kTh + at] = T::kNone;
       }
       if (part == 0) {
         const int hi = r < pq.R ? pq.L - pq.qlen + r / p.G : -1;
@@ -399,7 +403,7 @@ __device__ __forceinline__ void diff_tc_softmax(const DiffParams& dp, const int*
         if (i + 1 < nblk) widen_k(b + 1);
       }
       // ---- this key's scores for the group's 8 rows of both maps
-      float x[16], mu[16];
+      float x[16], th[16];
       if (ok) ok = mbar_wait(bar(T::kBarSFull + sb), (b >> 1) & 1, p.timeout_ns);
       ok = __all_sync(0xffffffffu, ok);  // tcgen05.ld is warp-collective
       tc_fence_after();
@@ -425,9 +429,9 @@ __device__ __forceinline__ void diff_tc_softmax(const DiffParams& dp, const int*
         __syncwarp();
         if (ok && lane == 0) mbar_arrive(bar(T::kBarS2 + sb));
       }
-      load16(fs_row, mu);
+      load16(fs_row, th);
 #pragma unroll
-      for (int r = 0; r < 16; ++r) x[r] *= mu[r];
+      for (int r = 0; r < 16; ++r) x[r] *= th[r];
       if (nvalid < 128 || key0 < pc.tile_lo_all || key0 + 127 > pc.tile_hi_all) {
         const int j = key0 + key;
 #pragma unroll
@@ -435,50 +439,50 @@ __device__ __forceinline__ void diff_tc_softmax(const DiffParams& dp, const int*
           if (!(key < nvalid && j >= lo_row[r] && j <= hi_row[r])) x[r] = x[8 + r] = -INFINITY;
       }
       // ---- running maxima, raised where a block's maximum passes one by 2^kRaise
-      load16(mu_row, mu);
+      load16(th_row, th);
       bool upd = false;
 #pragma unroll
-      for (int r = 0; r < 16; ++r) upd |= x[r] > mu[r] + T::kRaise;
+      for (int r = 0; r < 16; ++r) upd |= x[r] > th[r];
       bool rescale = false;
       if (bar_red_or(bid, 128, upd)) {
 #pragma unroll
-        for (int r = 0; r < 16; ++r) mu[r] = x[r];
-        const float m = warp_transpose_reduce<true, 16>(mu, lane);
+        for (int r = 0; r < 16; ++r) th[r] = x[r];
+        const float m = warp_transpose_reduce<true, 16>(th, lane);
         if (lane < 16) red[(warp & 3) * 16 + lane] = m;
         named_bar_sync(bid, 128);
         if ((warp & 3) == 0) {
           const int l16 = lane & 15;
           const float mx = fmaxf(fmaxf(red[l16], red[16 + l16]), fmaxf(red[32 + l16], red[48 + l16]));
-          const float m0 = mu_row[l16];
-          const bool up = mx > m0 + T::kRaise;
-          const float al = !up ? 1.f : m0 == -INFINITY ? 0.f : ex2(m0 - mx);
+          const float th0 = th_row[l16];
+          const bool up = mx > th0;
+          const float al = up ? ex2(th0 - T::kRaise - mx) : 1.f;  // (0 from kNone)
           __syncwarp();
           if (lane < 16) {
-            if (up) mu_row[lane] = mx;
+            if (up) th_row[lane] = mx + T::kRaise;
             al_row[lane] = al;
           }
-          const bool any = __any_sync(0xffffffffu, al != 1.f);
+          const bool any = __any_sync(0xffffffffu, up);
           if (lane == 0) ri[T::kFlag + g] = any ? 1 : 0;
         }
         named_bar_sync(bid, 128);
-        load16(mu_row, mu);
+        load16(th_row, th);
         rescale = ri[T::kFlag + g] != 0;
       }
-      // ---- weights 2^(x - mu + kBias) rounded to fp16; the sums add the rounded ones
+      // ---- weights 2^(x - m + kBias) rounded to fp16; the sums add the rounded ones
       uint32_t pw[8];
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        const float a = ex2(x[2 * k] - (mu[2 * k] == -INFINITY ? 0.f : mu[2 * k] - T::kBias));
-        const float c = ex2(x[2 * k + 1] - (mu[2 * k + 1] == -INFINITY ? 0.f : mu[2 * k + 1] - T::kBias));
+        constexpr float kUp = T::kRaise + T::kBias;  // 0 for CODES
+        const float a = ex2(x[2 * k] - th[2 * k] + kUp), c = ex2(x[2 * k + 1] - th[2 * k + 1] + kUp);
         pw[k] = pack_half2(a, c);
         const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&pw[k]));
         x[2 * k] = f.x;
         x[2 * k + 1] = f.y;
       }
       if (rescale) {
-        load16(al_row, mu);
+        load16(al_row, th);
 #pragma unroll
-        for (int r = 0; r < 16; ++r) lp[r] = lp[r] * mu[r] + x[r];
+        for (int r = 0; r < 16; ++r) lp[r] = lp[r] * th[r] + x[r];
       } else {
 #pragma unroll
         for (int r = 0; r < 16; ++r) lp[r] += x[r];
@@ -494,7 +498,7 @@ __device__ __forceinline__ void diff_tc_softmax(const DiffParams& dp, const int*
           tmem_ld16(tl + T::kColO + T::kON * c + 16 * g, o);
           tmem_wait_ld();
 #pragma unroll
-          for (int r = 0; r < 16; ++r) o[r] *= mu[r];
+          for (int r = 0; r < 16; ++r) o[r] *= th[r];
           tmem_st16(tl + T::kColO + T::kON * c + 16 * g, o);
         }
         tmem_wait_st();
@@ -538,21 +542,24 @@ __device__ __forceinline__ void diff_tc_softmax(const DiffParams& dp, const int*
     float o[S][16];
 #pragma unroll
     for (int h = 0; h < S; ++h) {
-#pragma unroll
-      for (int r = 0; r < 16; ++r) o[h][r] = 0.f;
       if (ok) {
-#pragma unroll
-        for (int m = NTM - 1; m >= 0; --m) {
+        const uint32_t at = tl + T::kColO + T::kON * NTM * h + 16 * g;
+        tmem_ld16(at, o[h]);
+        if constexpr (CODES) {  // the terms' scales; the codes stand for 2^8 times the weights
           float y[16];
-          tmem_ld16(tl + T::kColO + T::kON * (NTM * h + m) + 16 * g, y);
+          tmem_ld16(at + T::kON, y);
           tmem_wait_ld();
 #pragma unroll
-          for (int r = 0; r < 16; ++r) o[h][r] = fmaf(o[h][r], 0x1p-4f, y[r]);
-        }
-        if constexpr (CODES) {  // (codes stand for 2^8 times the weights)
+          for (int r = 0; r < 16; ++r) o[h][r] = fmaf(y[r], 0x1p-12f, o[h][r] * 0x1p-8f);
+          tmem_ld16(at + 2 * T::kON, y);
+          tmem_wait_ld();
 #pragma unroll
-          for (int r = 0; r < 16; ++r) o[h][r] *= 0x1p-8f;
+          for (int r = 0; r < 16; ++r) o[h][r] = fmaf(y[r], 0x1p-16f, o[h][r]);
         }
+        tmem_wait_ld();
+      } else {
+#pragma unroll
+        for (int r = 0; r < 16; ++r) o[h][r] = 0.f;
       }
     }
     tc_fence_before();
@@ -617,10 +624,10 @@ __device__ __forceinline__ void diff_tc_softmax(const DiffParams& dp, const int*
         }
       }
       if (key < 16 && 8 * g + (key & 7) < pc.R) {
-        const float mu = mu_row[key];
+        const float th = th_row[key], l = l_row[key];  // (l = 0: no key was visible)
         __stcg(reinterpret_cast<float2*>(
                    p.ws_ml + (static_cast<long long>(pc.slot) * p.rows_padded + (key >> 3) * T::kRows + 8 * g + (key & 7)) * 2),
-               make_float2(mu == -INFINITY ? -INFINITY : mu - T::kBias, l_row[key]));
+               make_float2(l == 0.f ? -INFINITY : th - (T::kRaise + T::kBias), l));
       }
     }
     named_bar_sync(T::kBarAll, NST);  // the row state and red[] are rewritten by the next piece
