@@ -876,8 +876,8 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::kMinBlocks)
         for (int k = 0; k < KG; ++k) M = fmaxf(M, merge_ml[(k * Cfg::RP + row) * 2]);
 #pragma unroll
         for (int k = 0; k < KG; ++k) {
-          const float mk = merge_ml[(k * Cfg::RP + row) * 2];
-          if (mk != -INFINITY) L += ex2(mk - M) * merge_ml[(k * Cfg::RP + row) * 2 + 1];
+          const float mk = merge_ml[(k * Cfg::RP + row) * 2], lk = merge_ml[(k * Cfg::RP + row) * 2 + 1];
+          if (lk != 0.f) L += ex2(mk - M) * lk;  // (0: no key; a NaN row has m = -inf and keeps its NaN)
         }
       };
       constexpr int V4 = D / 128;  // float4 groups per lane of a row
@@ -948,9 +948,10 @@ struct JoinState {
   float m, l;
   float4 o;
 };
-// Adds a partial (m, l, O) to a state.
+// Adds a partial (m, l, O) to a state. l = 0: it saw no key. (A row of NaN scores has
+// m = -inf and a NaN l, which goes on into the sum.)
 __device__ __forceinline__ void join_add(JoinState& s, float2 ml, float4 o) {
-  if (ml.x == -INFINITY) return;
+  if (ml.y == 0.f) return;
   if (ml.x > s.m) {
     const float f = s.m == -INFINITY ? 0.f : ex2(s.m - ml.x);
     s.l *= f;

@@ -295,3 +295,68 @@ def test_a_workspace_too_small_is_refused(pd):
         run(pd, w, lam, workspace=torch.empty(256, dtype=torch.uint8, device=DEV))
     need = pd.diff_workspace_bytes(pd.dims_of(w.q, w.k_cache, w.block_table, 1), 1, 0)
     parity(pd, w, workspace=torch.empty(need, dtype=torch.uint8, device=DEV))
+
+
+# byte caches with 9 to 32 query rows per map: the tensor-memory engine (three
+# sizes of units, both head sizes), rings that wrap, pieces that start inside a
+# sequence, windows whose first block is cut
+@pytest.mark.parametrize("window", (0, 700))
+@pytest.mark.parametrize("S", (0, 1, 3, 9))
+@pytest.mark.parametrize("Hq,Hkv,D,qlen", [(12, 2, 256, 3), (12, 2, 128, 5), (8, 2, 256, 3), (8, 2, 128, 8)])
+@pytest.mark.parametrize("kv", ("fp8", "fp8_bf16q", "int8"))
+def test_many_rows_long(pd, kv, Hq, Hkv, D, qlen, S, window):
+    w = inputs.make_workload(B=3, Hq=Hq, Hkv=Hkv, D=D, seq_lens=[2600, 0, 1301], qlen=qlen, window=window, kv=kv,
+                             seed=73 + D, scale=(D // 2) ** -0.5, stale="nan")
+    parity(pd, w, S, norm=S != 3)
+
+
+@pytest.mark.parametrize("kv", ("fp8", "int8_bf16q"))
+def test_many_rows_varlen(pd, kv):
+    """Units of 24, 0, 6, 12 and 18 rows in one batch, more units than SMs."""
+    qlens = [4, 0, 1, 2, 3] * 16
+    rng = np.random.RandomState(3)
+    w = inputs.make_varlen_workload(B=80, qlens=qlens, Hq=24, Hkv=4, D=256,
+                                    seq_lens=[max(q, int(x)) for q, x in zip(qlens, rng.randint(0, 900, 80))], kv=kv,
+                                    seed=79, scale=128 ** -0.5)
+    parity(pd, w, norm=True)
+
+
+@pytest.mark.parametrize("S", (1, 3))
+@pytest.mark.parametrize("kv", ("fp8", "int8"))
+def test_many_rows_rising_scores(pd, kv, S):
+    """Keys that grow along the sequence: thresholds rise in late blocks, the
+    accumulators are rescaled. (Scores of twice the usual size: 4 bounds.)"""
+    w = inputs.make_workload(B=2, Hq=12, Hkv=2, D=256, seq_lens=[1500, 291], qlen=2, kv=kv, seed=83, scale=0.25)
+    for b, L in enumerate((1500, 291)):
+        for j in range(L):
+            row = w.k_cache[int(w.block_table[b, j // 16]), j % 16]
+            codes = row.view(torch.int8 if kv == "int8" else torch.float8_e4m3fn)
+            x = codes.float() * (j / 1500)
+            row.copy_((x.round() if kv == "int8" else x).to(codes.dtype).view(row.dtype))
+    lam, _ = factors(w)
+    ref, bound = ref_diff.reference(w, lam.double().numpy())
+    check(run(pd, w, lam, S), ref, 4.0 * bound)
+
+
+@pytest.mark.parametrize("S", (0, 1, 3))
+@pytest.mark.parametrize("kv,qlen", [("f16", 1), ("bf16", 3), ("fp8", 1), ("fp8_bf16q", 3), ("int8", 3)])
+def test_a_nan_stays_in_its_row(pd, kv, qlen, S):
+    """A NaN in one head's query row makes that row NaN and no other."""
+    w = inputs.make_workload(B=2, Hq=12, Hkv=2, D=256, seq_lens=[700, 91], qlen=qlen, kv=kv, seed=89, scale=128 ** -0.5)
+    lam, _ = factors(w)
+    want = run(pd, w, lam, S)
+    w.q[1, 7, 200] = float("nan")
+    got = run(pd, w, lam, S)
+    assert torch.isnan(got[1, 7]).all()
+    got[1, 7] = want[1, 7]
+    assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("B,L,kv,qlen", [(1, 16, "f16", 1), (48, 128, "f16", 1), (100, 60, "bf16", 3), (1, 300, "int8", 3),
+                                         (48, 200, "fp8_bf16q", 3), (80, 500, "fp8", 2), (300, 33, "fp8", 1)])
+def test_short_tables(pd, B, L, kv, qlen):
+    """Tables of few blocks, where the automatic plan leaves units whole."""
+    lens = [L if i % 7 == 0 else (i * 37) % (L + 1) for i in range(B)]
+    w = inputs.make_workload(B=B, Hq=24, Hkv=4, D=256, seq_lens=lens, qlen=qlen, kv=kv, seed=97, scale=128 ** -0.5,
+                             stale="nan")
+    parity(pd, w, norm=True)
