@@ -103,7 +103,10 @@ struct DiffTc {
   static constexpr int kOffRow = kOffRed + NG * 4 * 16 * 4;  // row state, [NG][map][8]: score factor,
   static constexpr int kFs = 0, kTh = kON, kAl = 2 * kON, kL = 3 * kON;  // threshold, rescale, sum;
   static constexpr int kLo = 4 * kON, kHi = kLo + kRows, kFlag = kHi + kRows;  // [NG][8]: visible range; a flag
-  static constexpr int kOffBars = (kOffRow + (kFlag + NG) * 4 + 15) / 16 * 16;
+  // Cluster merge: each CTA stages its partial (m, l) here, [map][row], and its
+  // partial O rows [map][row][D] at offset 0, over the K ring, idle by then.
+  static constexpr int kOffStage = (kOffRow + (kFlag + NG) * 4 + 15) / 16 * 16;
+  static constexpr int kOffBars = kOffStage + 2 * kRows * 8;
   // barriers: fullK, emptyK [NBK], fullV, emptyV [NBV], then these (kBarS2: S^T
   // read, CODES; else K widened)
   static constexpr int kBarSFull = 0, kBarS2 = 2, kBarPFull = 4, kBarPvDone = 5, kBarQFull = 6, kBarFinal = 7;
@@ -116,6 +119,7 @@ struct DiffTc {
   static_assert(kOffRow % 16 == 0, "row state read as float4");
   static_assert(kCols <= kTmemCols, "tensor-memory columns");
   static_assert(kSmemBytes <= 227 * 1024, "one CTA per SM");
+  static_assert(2 * kRows * D * 4 <= kOffV, "the staged rows fit over the K ring");
 };
 
 // Four fp16 weights in [0, 1] (two pairs) to three words of e4m3 codes, w 2^8 = t1
@@ -613,26 +617,105 @@ __device__ __forceinline__ void diff_tc_softmax(const DiffParams& dp, const int*
           dst[128 * h + key] = static_cast<uint16_t>(pack_out(p.out_bf16 != 0, o[h][r], 0.f) & 0xffffu);
       }
     } else {
+      // the partial rows: staged for a cluster merge, else the piece's slot
+      float* part = p.cluster > 1 ? reinterpret_cast<float*>(smem)
+                                  : p.ws_o + static_cast<long long>(pc.slot) * p.rows_padded * D;
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
 #pragma unroll
         for (int r = 0; r < 8; ++r) {
           if (8 * g + r >= pc.R) break;
-          float* dst = p.ws_o + (static_cast<long long>(pc.slot) * p.rows_padded + m * T::kRows + 8 * g + r) * D;
+          float* dst = part + (m * T::kRows + 8 * g + r) * D + key;
 #pragma unroll
-          for (int h = 0; h < S; ++h) __stcg(dst + 128 * h + key, o[h][8 * m + r]);
+          for (int h = 0; h < S; ++h) {
+            if (p.cluster > 1) dst[128 * h] = o[h][8 * m + r];
+            else __stcg(dst + 128 * h, o[h][8 * m + r]);
+          }
         }
       }
       if (key < 16 && 8 * g + (key & 7) < pc.R) {
+        const int row = (key >> 3) * T::kRows + 8 * g + (key & 7);
         const float th = th_row[key], l = l_row[key];  // (l = 0: no key was visible)
-        __stcg(reinterpret_cast<float2*>(
-                   p.ws_ml + (static_cast<long long>(pc.slot) * p.rows_padded + (key >> 3) * T::kRows + 8 * g + (key & 7)) * 2),
-               make_float2(l == 0.f ? -INFINITY : th - (T::kRaise + T::kBias), l));
+        const float2 ml = make_float2(l == 0.f ? -INFINITY : th - (T::kRaise + T::kBias), l);
+        if (p.cluster > 1)
+          reinterpret_cast<float2*>(smem + T::kOffStage)[row] = ml;
+        else
+          __stcg(reinterpret_cast<float2*>(p.ws_ml) + static_cast<long long>(pc.slot) * p.rows_padded + row, ml);
       }
     }
     named_bar_sync(T::kBarAll, NST);  // the row state and red[] are rewritten by the next piece
   }
   if (!ok && lane == 0) raise_error(p.error_flag, kErrTimeout);
+}
+
+// Merge of a fixed split whose pieces are the CTAs of one cluster: a warp takes a
+// row (both maps), CTA s the rows r with r % S == s, reads the S partials through
+// distributed shared memory and finishes the row as diff_combine_kernel does. A
+// CTA without a piece staged l = 0; a unit of one piece was finished by it.
+template <class T>
+__device__ __forceinline__ void diff_tc_merge(const DiffParams& dp, uint32_t sbase) {
+  const DecodeParams& p = dp.d;
+  constexpr int D = T::D, V4 = D / 128;
+  const int S = p.cluster, rank = static_cast<int>(cluster_rank()), u = blockIdx.x / S;
+  const int b = u / p.hgn, kh = u % p.hgn;
+  int L, t0, n, q0, qn;
+  seq_span(p, b, false, L, t0, n, q0, qn);
+  if (n == 0) return;
+  const int chunk = (n + S - 1) / S;
+  if (n <= chunk) return;
+  const int R = p.G * qn, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int r = rank + S * warp; r < R; r += S * (T::kThreads / 32)) {
+    float4 y[V4];
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      const int row = m * T::kRows + r;
+      float2 ml = make_float2(-INFINITY, 0.f);
+      if (lane < S) ml = ld_peer_f2(peer_smem(sbase + T::kOffStage + 8 * row, lane));
+      float M = ml.x;
+#pragma unroll
+      for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+      const float w = ml.y == 0.f ? 0.f : ex2(ml.x - M);
+      float l = w * ml.y;
+#pragma unroll
+      for (int o = 16; o >= 1; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+      const uint32_t live = __ballot_sync(0xffffffffu, ml.y != 0.f);
+      float4 acc[V4];
+#pragma unroll
+      for (int v = 0; v < V4; ++v) acc[v] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+      for (int s = 0; s < S; ++s) {
+        const float ws = __shfl_sync(0xffffffffu, w, s);
+        if (!(live >> s & 1)) continue;
+        const uint32_t at = peer_smem(sbase + row * D * 4, s);
+#pragma unroll
+        for (int v = 0; v < V4; ++v) {
+          const float4 a = ld_peer_f4(at + 16 * (32 * v + lane));
+          acc[v].x += ws * a.x; acc[v].y += ws * a.y; acc[v].z += ws * a.z; acc[v].w += ws * a.w;
+        }
+      }
+      float inv = l > 0.f ? p.out_scale / l : 0.f;
+      if (m == 1) inv *= -__ldg(dp.lambda + kh * p.G + r % p.G);
+#pragma unroll
+      for (int v = 0; v < V4; ++v) {
+        if (m == 0) y[v] = make_float4(acc[v].x * inv, acc[v].y * inv, acc[v].z * inv, acc[v].w * inv);
+        else y[v] = make_float4(fmaf(acc[v].x, inv, y[v].x), fmaf(acc[v].y, inv, y[v].y), fmaf(acc[v].z, inv, y[v].z),
+                                fmaf(acc[v].w, inv, y[v].w));
+      }
+    }
+    float f = 1.f;
+    if (dp.norm_weight != nullptr) {
+      float ss = 0.f;
+#pragma unroll
+      for (int v = 0; v < V4; ++v) ss += y[v].x * y[v].x + y[v].y * y[v].y + y[v].z * y[v].z + y[v].w * y[v].w;
+#pragma unroll
+      for (int o = 16; o >= 1; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      f = rsqrtf(ss / static_cast<float>(D) + dp.norm_eps) * dp.norm_gain;
+    }
+    uint16_t* dst = reinterpret_cast<uint16_t*>(p.out) +
+                    (static_cast<long long>(q0 + r / p.G) * p.Hq + kh * p.G + r % p.G) * D;
+#pragma unroll
+    for (int v = 0; v < V4; ++v) store_row4(dp, dst, 4 * (32 * v + lane), y[v], f);
+  }
 }
 
 template <class T>
@@ -680,6 +763,9 @@ __global__ void __launch_bounds__(T::kThreads, 1)
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
   }
+  // a CTA of a cluster that gets no piece contributes nothing to the merge
+  if (threadIdx.x < 2 * T::kRows)
+    reinterpret_cast<float2*>(smem + T::kOffStage)[threadIdx.x] = make_float2(-INFINITY, 0.f);
   // nothing above touches global memory (programmatic dependent launch)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (p.num_splits == 0 && warp == 0) balanced_prefix(p, s_pre, lane);
@@ -794,6 +880,11 @@ __global__ void __launch_bounds__(T::kThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
+  if (p.cluster > 1) {
+    cluster_sync();  // every CTA of the cluster has staged its partial
+    diff_tc_merge<T>(dp, sbase);
+    cluster_sync();  // no CTA leaves while a peer still reads its shared memory
+  }
   if (warp == T::kMmaWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, T::kTmemCols);
@@ -807,7 +898,7 @@ cudaError_t launch_diff_tc(const CUtensorMap& tk, const CUtensorMap& tv, const D
   const cudaError_t e =
       once_per_context(attr_ctx, [] { return set_kernel_attributes(decode_diff_tc_kernel<T>, T::kSmemBytes); });
   if (e != cudaSuccess) return e;
-  return launch_pdl(decode_diff_tc_kernel<T>, grid, T::kThreads, T::kSmemBytes, stream, 1, tk, tv, p);
+  return launch_pdl(decode_diff_tc_kernel<T>, grid, T::kThreads, T::kSmemBytes, stream, p.d.cluster, tk, tv, p);
 }
 
 template <class T>
@@ -821,7 +912,9 @@ bool diff_tc_shape_of(KernelShape* out) {
   out->fixed_pieces = 1;
   out->step_tiles = T::kBlkTiles;
   out->whole_tile = T::CODES ? 0 : 1;
-  for (int& c : out->max_clusters) c = 0;  // split units go through the combine
+  static unsigned long long ctx_done[64] = {};
+  static int cache[64][kMaxCluster + 1] = {};
+  max_active_clusters(decode_diff_tc_kernel<T>, T::kThreads, T::kSmemBytes, ctx_done, cache, out->max_clusters);
   return true;
 }
 
