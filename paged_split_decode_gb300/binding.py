@@ -416,7 +416,8 @@ def decode_paged_diff(q, k_cache, v_cache, block_table, seq_lens, lam, scale, wi
     tables, masks and splits as in ``decode_paged``; with ``query_start_loc``
     (int32 [B+1]) sequence b has its own count of query tokens, at most
     ``qlen``, as in ``decode_paged_varlen`` (rows outside every range are left
-    as they were; a new ``out`` is zeroed there).
+    as they were; a new ``out`` is zeroed there). A map contributes zeros to a
+    row that sees no key, or a score that is NaN or +infinity.
     """
     return (_bind or _fast()).decode_paged_diff(q, k_cache, v_cache, block_table, seq_lens, lam, scale, window, qlen,
                                                 num_splits, out, query_start_loc, norm_weight, norm_eps, norm_gain,

@@ -117,6 +117,10 @@ __device__ __forceinline__ float round16(float x) {
 
 __device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
 
+// A map's output where its sum of weights l is a positive number, else nothing: a
+// map without a visible key, or with a NaN among its scores, contributes zeros.
+__device__ __forceinline__ float map_out(float l, float o) { return l > 0.f ? o : 0.f; }
+
 __device__ __forceinline__ uint32_t pack_out(bool bf16, float lo, float hi) {
   return bf16 ? pack_bf162(lo, hi) : pack_half2(lo, hi);
 }
@@ -758,7 +762,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::kMinBlocks)
           for (int mtl = 0; mtl < MTW; ++mtl)
 #pragma unroll
             for (int e = c; e < 4; e += 2) {
-              const float v = o[0][mtl][n][e] * inv1 - o[1][mtl][n][e] * inv2;
+              const float v = map_out(l_map[0][n][c], o[0][mtl][n][e]) * inv1 - map_out(l_map[1][n][c], o[1][mtl][n][e]) * inv2;
               o[0][mtl][n][e] = v;
               s += v * v;
             }
@@ -877,7 +881,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::kMinBlocks)
 #pragma unroll
         for (int k = 0; k < KG; ++k) {
           const float mk = merge_ml[(k * Cfg::RP + row) * 2], lk = merge_ml[(k * Cfg::RP + row) * 2 + 1];
-          if (lk != 0.f) L += ex2(mk - M) * lk;  // (0: no key; a NaN row has m = -inf and keeps its NaN)
+          if (lk != 0.f) L += ex2(mk - M) * lk;  // (0: no key; a NaN goes on into the sum)
         }
       };
       constexpr int V4 = D / 128;  // float4 groups per lane of a row
@@ -909,8 +913,8 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::kMinBlocks)
           for (int v = 0; v < V4; ++v) {
             const float4 a = *(reinterpret_cast<const float4*>(merge_o + row1 * Cfg::kDP) + v * 32 + lane);
             const float4 b = *(reinterpret_cast<const float4*>(merge_o + row2 * Cfg::kDP) + v * 32 + lane);
-            y[v] = make_float4(a.x * inv1 - b.x * inv2, a.y * inv1 - b.y * inv2, a.z * inv1 - b.z * inv2,
-                               a.w * inv1 - b.w * inv2);
+            y[v] = make_float4(map_out(l1, a.x) * inv1 - map_out(l2, b.x) * inv2, map_out(l1, a.y) * inv1 - map_out(l2, b.y) * inv2,
+                               map_out(l1, a.z) * inv1 - map_out(l2, b.z) * inv2, map_out(l1, a.w) * inv1 - map_out(l2, b.w) * inv2);
             ss += y[v].x * y[v].x + y[v].y * y[v].y + y[v].z * y[v].z + y[v].w * y[v].w;
           }
           float f = 1.f;
@@ -948,8 +952,8 @@ struct JoinState {
   float m, l;
   float4 o;
 };
-// Adds a partial (m, l, O) to a state. l = 0: it saw no key. (A row of NaN scores has
-// m = -inf and a NaN l, which goes on into the sum.)
+// Adds a partial (m, l, O) to a state. l = 0: it saw no key. (A NaN score leaves a NaN
+// l, with m = -inf where there is no other, which goes on into the sum.)
 __device__ __forceinline__ void join_add(JoinState& s, float2 ml, float4 o) {
   if (ml.y == 0.f) return;
   if (ml.x > s.m) {
@@ -1062,8 +1066,10 @@ __global__ void __launch_bounds__(NT, NT <= 384 ? 2 : 1) diff_combine_kernel(con
       }
     }
     const float i1 = st[0].l > 0.f ? p.out_scale / st[0].l : 0.f, i2 = st[1].l > 0.f ? p.out_scale / st[1].l * lam : 0.f;
-    float4 v = make_float4(st[0].o.x * i1 - st[1].o.x * i2, st[0].o.y * i1 - st[1].o.y * i2,
-                           st[0].o.z * i1 - st[1].o.z * i2, st[0].o.w * i1 - st[1].o.w * i2);
+    const float l1 = st[0].l, l2 = st[1].l;
+    const float4 a = st[0].o, b2 = st[1].o;
+    float4 v = make_float4(map_out(l1, a.x) * i1 - map_out(l2, b2.x) * i2, map_out(l1, a.y) * i1 - map_out(l2, b2.y) * i2,
+                           map_out(l1, a.z) * i1 - map_out(l2, b2.z) * i2, map_out(l1, a.w) * i1 - map_out(l2, b2.w) * i2);
     if (dp.norm_weight != nullptr) {
       float ss = v.x * v.x + v.y * v.y + v.z * v.z + v.w * v.w;
 #pragma unroll

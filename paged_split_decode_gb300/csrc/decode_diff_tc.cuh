@@ -586,7 +586,7 @@ __device__ __forceinline__ void diff_tc_softmax(const DiffParams& dp, const int*
         ss[r] = 0.f;
 #pragma unroll
         for (int h = 0; h < S; ++h) {
-          o[h][r] = o[h][r] * i1 - o[h][8 + r] * i2;
+          o[h][r] = map_out(l1, o[h][r]) * i1 - map_out(l2, o[h][8 + r]) * i2;
           ss[r] += o[h][r] * o[h][r];
         }
       }
@@ -697,6 +697,7 @@ __device__ __forceinline__ void diff_tc_merge(const DiffParams& dp, uint32_t sba
       if (m == 1) inv *= -__ldg(dp.lambda + kh * p.G + r % p.G);
 #pragma unroll
       for (int v = 0; v < V4; ++v) {
+        acc[v] = make_float4(map_out(l, acc[v].x), map_out(l, acc[v].y), map_out(l, acc[v].z), map_out(l, acc[v].w));
         if (m == 0) y[v] = make_float4(acc[v].x * inv, acc[v].y * inv, acc[v].z * inv, acc[v].w * inv);
         else y[v] = make_float4(fmaf(acc[v].x, inv, y[v].x), fmaf(acc[v].y, inv, y[v].y), fmaf(acc[v].z, inv, y[v].z),
                                 fmaf(acc[v].w, inv, y[v].w));

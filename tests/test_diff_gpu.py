@@ -340,15 +340,34 @@ def test_many_rows_rising_scores(pd, kv, S):
 
 @pytest.mark.parametrize("S", (0, 1, 3))
 @pytest.mark.parametrize("kv,qlen", [("f16", 1), ("bf16", 3), ("fp8", 1), ("fp8_bf16q", 3), ("int8", 3)])
-def test_a_nan_stays_in_its_row(pd, kv, qlen, S):
-    """A NaN in one head's query row makes that row NaN and no other."""
+def test_a_nan_score_silences_its_map(pd, kv, qlen, S):
+    """A NaN in the second half of one head's query row: that row's second map
+    contributes nothing (as with lambda = 0), no other row changes. A NaN in the
+    first half too: the row is zero."""
     w = inputs.make_workload(B=2, Hq=12, Hkv=2, D=256, seq_lens=[700, 91], qlen=qlen, kv=kv, seed=89, scale=128 ** -0.5)
     lam, _ = factors(w)
-    want = run(pd, w, lam, S)
+    want, alone = run(pd, w, lam, S), run(pd, w, torch.zeros(12), S)
     w.q[1, 7, 200] = float("nan")
-    got = run(pd, w, lam, S)
-    assert torch.isnan(got[1, 7]).all()
-    got[1, 7] = want[1, 7]
+    want[1, 7] = alone[1, 7]
+    assert torch.equal(run(pd, w, lam, S), want)
+    w.q[1, 7, 20] = float("nan")
+    want[1, 7] = 0
+    assert torch.equal(run(pd, w, lam, S), want)
+
+
+@pytest.mark.parametrize("qlen", (1, 3))
+def test_nan_codes_of_visible_keys(pd, qlen):
+    """A NaN code in a K row silences the map of its half for the KV head's rows that
+    see the key, one in a V row shows in its dimension of the rows that see it."""
+    w = inputs.make_workload(B=2, Hq=12, Hkv=2, D=256, seq_lens=[700, 91], qlen=qlen, kv="fp8", seed=101, scale=128 ** -0.5)
+    lam, _ = factors(w)
+    want, alone = run(pd, w, lam), run(pd, w, torch.zeros(12))
+    w.k_cache.view(torch.uint8)[int(w.block_table[0, 5]), 3, 1, 130] = 0x7F  # second half, KV head 1
+    w.v_cache.view(torch.uint8)[int(w.block_table[1, 2]), 9, 0, 77] = 0xFF
+    got = run(pd, w, lam)
+    want[:qlen, 6:] = alone[:qlen, 6:]
+    assert torch.isnan(got[qlen:, :6, 77]).all()
+    got[qlen:, :6, 77] = want[qlen:, :6, 77]
     assert torch.equal(got, want)
 
 
