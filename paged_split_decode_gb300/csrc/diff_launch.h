@@ -57,8 +57,8 @@ bool diff_shape_of(KernelShape* out) {
   out->whole_tile = 1;
   // what a piece's end costs, in tiles: 1 us from the accumulators, 5 us where key
   // groups merge first (measured, D = 256 GQA 6:1, L = 8192, B = 8, qlen = 3, 4 /
-  // 10 / 16 / 24 / 48 tiles: fp16 61.0 / 59.2 / 57.2 / 56.8 / 57.5 us, e4m3 64.0 /
-  // 62.2 / 59.6 / 59.4 / 60.4; without key groups 4 to 12 tiles are within 1 %)
+  // 10 / 16 / 24 / 48 tiles: fp16 61.0 / 59.2 / 57.2 / 56.8 / 57.5 us; without key
+  // groups 4 to 12 tiles are within 1 %)
   out->unit_cost = Cfg::KG > 1 ? 20 : 4;
   out->fixed_pieces = 0;
   for (int& c : out->max_clusters) c = 0;  // split units go through the combine
@@ -85,7 +85,7 @@ cudaError_t diff_launch_cfg(const CUtensorMap& tk, const CUtensorMap& tv, const 
 //    CTAs per SM (two CTAs' producers: one tile's copies take 0.2 us to issue).
 //  * C2 to C4, two to four row tiles per map: four warps a head, two key groups,
 //    one CTA per SM; two tiles a step while the fragments fit (qlen = 3, e4m3, L
-//    = 8192, B = 8: 69 -> 65 us).
+//    = 8192, B = 8: 69 -> 65 us before those had the tensor-memory engine below).
 template <int D, int KV>
 struct DiffShapes {
   // row tiles per map, heads per tile, warps per head, key groups, tiles per step, CTAs per SM
@@ -96,7 +96,8 @@ struct DiffShapes {
   using C4 = DiffCfgFor<D, KV, 4, 1, 4, 2, 1, 1>;
 
   // byte caches, two or more row tiles per map, where shared memory holds it: the
-  // tensor-memory kernel
+  // tensor-memory engine (L = 8192, B = 8, qlen = 2 / 3 / 5: e4m3 45.9 / 58.7 / 76.7
+  // here, 33.3 / 35.5 / 44.7 us there, int8 51.4 / 63.4 here, 40.2 / 44.4 there)
   template <class C>
   static constexpr bool kTc = KV == kKvFp8 || (KV == kKvInt8 && (D == 128 || C::NTM < 4));
   template <class C>

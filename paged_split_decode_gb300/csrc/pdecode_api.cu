@@ -165,26 +165,39 @@ pd_status make_plan(const pd_dims* d, int qlen, int num_splits, int sm_count, Pl
   const bool automatic = splits == 0;
   const long long cap_keys = static_cast<long long>(d->max_blocks_per_seq) * d->block_size;
   const long long vis_keys = window > 0 ? std::min<long long>(cap_keys, 0ll + window + qlen + kTileKeys) : cap_keys;
-  // Short tables: whole units one per CTA walk (waves - units / ctas) * tiles more
-  // than the balanced split does and launch no join, whose launch and reads cost
-  // four steps or more. Balanced -> whole units (B = 48): fp16 D =
-  // 256, 96 units, 1 / 4 / 8 / 16 tiles: 9.2 / 12.2 / 13.5 / 16.7 -> 6.9 / 9.3 /
-  // 12.6 / 19.3 us; e4m3 qlen = 3, 384 units, 8 / 16 tiles: 32.5 / 36.2 -> 23.6 /
-  // 29.4 us; B = 1, three key groups, 8 / 16 tiles: 8.3 / 8.4 -> 7.4 / 8.8 us. Eight
-  // steps at most: a batch with one long sequence then waits four steps longer.
+  // Short tables: whole units, one per CTA, walk (waves - units / ctas) * tiles more
+  // than the balanced split does, but launch no join and end no pieces inside a
+  // unit, which costs four steps of the CTA and up to twice that where every CTA
+  // has such ends. Balanced -> whole: fp16 D = 256, 48 units, 1 / 4 / 8 tiles 9.2 /
+  // 12.2 / 13.5 -> 6.9 / 9.1 / 12.4 us; three key groups, 2 units, 8 / 16 tiles 8.3 /
+  // 8.3 -> 7.2 / 8.7; tensor-memory engine (steps of 8 tiles), 4 / 64 / 384 units, 16
+  // tiles 12.6 / 18.5 / 44.4 -> 11.3 / 11.8 / 33.3, 64 tiles 16.1 / 25.6 / 72.6 ->
+  // 19.1 / 19.6 / 59.5. Eight steps at most: a batch with one long sequence then
+  // waits four steps longer. Where pieces merge inside a cluster, as many of two steps
+  // or more as the CTAs hold are better still (4 / 32 / 64 units, 48 tiles 16.7 / 16.8
+  // / 17.1 -> 13.4 / 13.8 / 15.4).
   if (automatic && diff && pl->units > 0) {
     const long long waves = (pl->units + ctas - 1) / ctas;
     const long long tiles = (vis_keys + kTileKeys - 1) / kTileKeys;
-    if (tiles <= 8 * ks.step_tiles && tiles * (waves * ctas - pl->units) <= 4ll * ctas * ks.step_tiles) splits = 1;
+    const long long room = std::min<long long>({ctas / pl->units, tiles / (2 * ks.step_tiles), kMaxCluster});
+    if (tiles <= 8 * ks.step_tiles) {
+      if (room >= 2 && ks.max_clusters[room] >= pl->units)
+        splits = static_cast<int>(room);
+      else if (tiles * (waves * ctas - pl->units) <= 4ll * ks.step_tiles * (ctas + pl->units))
+        splits = 1;
+    }
   }
   if (splits == 0 && pl->units > 0 && pl->units <= ctas / 4) {
     const long long tiles = pl->units * (vis_keys / kTileKeys + 1);
     if (tiles <= 24ll * ctas || ks.fixed_pieces)
       splits = static_cast<int>(std::max<long long>(1, (ctas * 27 / 32) / pl->units));
     // its join reads two maps' partials: pieces of at least four tiles (B = 1, L
-    // = 4096, fp16 / e4m3: 13.9 / 13.6 -> 12.4 / 12.3 us; eight tiles 13.3 / 13.9)
-    if (diff && splits > 1)
-      splits = static_cast<int>(std::max<long long>(1, std::min<long long>(splits, (vis_keys / kTileKeys + 3) / 4)));
+    // = 4096, fp16 / e4m3: 13.9 / 13.6 -> 12.4 / 12.3 us; eight tiles 13.3 / 13.9), of
+    // two steps on the tensor-memory engine (qlen = 3, e4m3, L = 1024 / 2048: 16.1 /
+    // 15.5 -> 13.2 / 14.0)
+    const long long piece = ks.fixed_pieces ? 2 * ks.step_tiles : 4;
+    const long long most = (vis_keys / kTileKeys + piece - 1) / piece;
+    if (diff && splits > 1) splits = static_cast<int>(std::max<long long>(1, std::min<long long>(splits, most)));
   }
   pl->splits = splits;
   if (splits == 0) {
@@ -374,7 +387,8 @@ pd_status prepare_decode(const void* q, const void* k_cache, const void* v_cache
     if (reinterpret_cast<uintptr_t>(workspace) & 255u) return PD_ERR_ALIGN;
   }
 
-  if (!encode_cache_map(&tk, k_cache, dims, pl.hg, pl.whole_tile) || !encode_cache_map(&tv, v_cache, dims, pl.hg, pl.whole_tile))
+  if (!encode_cache_map(&tk, k_cache, dims, pl.hg, pl.whole_tile) ||
+      !encode_cache_map(&tv, v_cache, dims, pl.hg, pl.whole_tile))
     return PD_ERR_CUDA;
 
   const bool fp8 = byte_kind(dims->kv_dtype);  // scaled codes

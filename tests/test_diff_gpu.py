@@ -371,10 +371,12 @@ def test_nan_codes_of_visible_keys(pd, qlen):
     assert torch.equal(got, want)
 
 
-@pytest.mark.parametrize("B,L,kv,qlen", [(1, 16, "f16", 1), (48, 128, "f16", 1), (100, 60, "bf16", 3), (1, 300, "int8", 3),
+@pytest.mark.parametrize("B,L,kv,qlen", [(4, 600, "fp8", 3), (16, 900, "int8", 3), (1, 1500, "fp8_bf16q", 4),
+                                         (1, 16, "f16", 1), (48, 128, "f16", 1), (100, 60, "bf16", 3), (1, 300, "int8", 3),
                                          (48, 200, "fp8_bf16q", 3), (80, 500, "fp8", 2), (300, 33, "fp8", 1)])
 def test_short_tables(pd, B, L, kv, qlen):
-    """Tables of few blocks, where the automatic plan leaves units whole."""
+    """Tables of few blocks, where the automatic plan leaves units whole or cuts
+    them into the pieces of a cluster."""
     lens = [L if i % 7 == 0 else (i * 37) % (L + 1) for i in range(B)]
     w = inputs.make_workload(B=B, Hq=24, Hkv=4, D=256, seq_lens=lens, qlen=qlen, kv=kv, seed=97, scale=128 ** -0.5,
                              stale="nan")
