@@ -6,7 +6,7 @@
 //
 // Why compiled: a call checks up to twelve tensors (device, type, layout, size).
 // Through the interpreter and ctypes that took 8.7 us for build_block_tables on
-// the GPU's host, more than twice its kernel (3.6 us).
+// the GPU's host, more than twice its kernel (3.2 us).
 //
 // The functions take their arguments by position, in the order of the Python
 // functions that wrap them (binding.py, which documents them); None stands for

@@ -106,7 +106,7 @@ __device__ __forceinline__ void deal(int n, int rank, int ranks, Item item, Flus
     return;
   }
   const int warps = ranks * (NT / 32), warp = rank * (NT / 32) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  const int share = ((n + warps - 1) / warps + 31) / 32 * 32;
+  const int share = (n / warps + 32) / 32 * 32;
   const long long first = static_cast<long long>(warp) * share;
   const int end = static_cast<int>(min(static_cast<long long>(n), first + share));
   for (long long k0 = first + lane; k0 < end; k0 += 32 * kBatch) {

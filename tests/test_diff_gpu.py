@@ -301,11 +301,11 @@ def test_a_workspace_too_small_is_refused(pd):
 # sizes of units, both head sizes), rings that wrap, pieces that start inside a
 # sequence, windows whose first block is cut
 @pytest.mark.parametrize("window", (0, 700))
-@pytest.mark.parametrize("S", (0, 1, 3, 9))
+@pytest.mark.parametrize("S", (0, 1, 3, 9, 40))
 @pytest.mark.parametrize("Hq,Hkv,D,qlen", [(12, 2, 256, 3), (12, 2, 128, 5), (8, 2, 256, 3), (8, 2, 128, 8)])
 @pytest.mark.parametrize("kv", ("fp8", "fp8_bf16q", "int8"))
 def test_many_rows_long(pd, kv, Hq, Hkv, D, qlen, S, window):
-    w = inputs.make_workload(B=3, Hq=Hq, Hkv=Hkv, D=D, seq_lens=[2600, 0, 1301], qlen=qlen, window=window, kv=kv,
+    w = inputs.make_workload(B=4, Hq=Hq, Hkv=Hkv, D=D, seq_lens=[2600, 0, 1301, 70], qlen=qlen, window=window, kv=kv,
                              seed=73 + D, scale=(D // 2) ** -0.5, stale="nan")
     parity(pd, w, S, norm=S != 3)
 
