@@ -365,7 +365,10 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::kMinBlocks)
     // by ring position (a piece may start or end inside a step)
     const int lead = KG > 1 && KT > 1 ? static_cast<int>(q % KT) : 0;
     const uint32_t step0 = (q - lead) / KT;
-    for (int st = (kg - static_cast<int>(step0 % KG) + KG) % KG; st * KT - lead < ntiles; st += KG) {
+    // (a piece without tiles has no step, not even the one that it would start in:
+    // that one's stage is not its to give back)
+    const int last = ntiles > 0 ? ntiles + lead : 0;
+    for (int st = (kg - static_cast<int>(step0 % KG) + KG) % KG; st * KT < last; st += KG) {
       const int k0 = st * KT - lead;
       bool have[KT];
       int tile[KT];  // a step's missing tile is its other one over again, masked: no branch splits the step

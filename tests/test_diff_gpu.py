@@ -381,3 +381,16 @@ def test_short_tables(pd, B, L, kv, qlen):
     w = inputs.make_workload(B=B, Hq=24, Hkv=4, D=256, seq_lens=lens, qlen=qlen, kv=kv, seed=97, scale=128 ** -0.5,
                              stale="nan")
     parity(pd, w, norm=True)
+
+
+@pytest.mark.parametrize("S", (0, 1, 5))
+@pytest.mark.parametrize("Hq,Hkv,D,qlen", [(12, 2, 256, 2), (24, 4, 256, 3), (28, 4, 128, 3), (6, 3, 128, 1), (32, 8, 128, 1)])
+@pytest.mark.parametrize("kv", ("f16", "bf16", "fp8", "int8_bf16q"))
+def test_empty_units_between_odd_ones(pd, kv, Hq, Hkv, D, qlen, S):
+    """Units without keys between units of odd tile counts, many to a CTA: an
+    empty one takes nothing from the ring, wherever the last one left it."""
+    lens = [(qlen, 0, 17, 0, 0, 33, 40, 0, 5, 0, 90, 0)[i % 12] if i % 5 else 0 for i in range(400)]
+    w = inputs.make_workload(B=400, Hq=Hq, Hkv=Hkv, D=D, seq_lens=lens, qlen=qlen, kv=kv, seed=103 + D,
+                             scale=(D // 2) ** -0.5, stale="nan")
+    for _ in range(3):
+        parity(pd, w, S, norm=True)
