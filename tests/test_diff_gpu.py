@@ -394,3 +394,21 @@ def test_empty_units_between_odd_ones(pd, kv, Hq, Hkv, D, qlen, S):
                              scale=(D // 2) ** -0.5, stale="nan")
     for _ in range(3):
         parity(pd, w, S, norm=True)
+
+
+@pytest.mark.parametrize("seed", range(48))
+def test_drawn_calls(pd, seed):
+    """Heads, lengths, query counts, windows, splits and kinds drawn together."""
+    r = np.random.RandomState(7000 + seed)
+    pick = lambda *v: v[r.randint(len(v))]
+    D, Hkv, G, q = pick(128, 256), pick(1, 2, 3, 4, 5, 8), pick(1, 2, 3, 4, 6, 7), pick(1, 1, 2, 3, 4, 5, 8)
+    q = min(q, 32 // G)
+    B, top = pick((1, 1500), (3, 1500), (7, 400), (20, 200), (60, 100))
+    lens = [pick(0, r.randint(top + 1), r.randint(top + 1)) for _ in range(B - 1)] + [top]
+    kw = dict(B=B, Hq=G * Hkv, Hkv=Hkv, D=D, seq_lens=lens, kv=pick(*KINDS), window=pick(0, 0, 1, 9, 100), seed=seed,
+              scale=(D // 2) ** -0.5)
+    if r.randint(2):
+        w = inputs.make_varlen_workload(qlens=[r.randint(q + 1) for _ in range(B - 1)] + [q], **kw)
+    else:
+        w = inputs.make_workload(qlen=q, block_size=pick(16, 32, 48), stale="nan", **kw)
+    parity(pd, w, pick(0, 0, 1, 2, 3, 7, 16, 33), norm=bool(r.randint(2)))
