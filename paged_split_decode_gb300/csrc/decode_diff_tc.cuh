@@ -102,7 +102,8 @@ struct DiffTc {
   static constexpr int kOffRed = kOffPt + kPtBytes;          // float [NG][4 warps][16]
   static constexpr int kOffRow = kOffRed + NG * 4 * 16 * 4;  // row state, [NG][map][8]: score factor,
   static constexpr int kFs = 0, kTh = kON, kAl = 2 * kON, kL = 3 * kON;  // threshold, rescale, sum;
-  static constexpr int kLo = 4 * kON, kHi = kLo + kRows, kFlag = kHi + kRows;  // [NG][8]: visible range; a flag
+  static constexpr int kLo = 4 * kON, kHi = kLo + kRows, kRow = kHi + kRows;  // [NG][8]: visible range,
+  static constexpr int kLam = kRow + kRows, kFlag = kLam + kRows;  // output row (of Hq a token), lambda; a flag
   // Cluster merge: each CTA stages its partial (m, l) here, [map][row], and its
   // partial O rows [map][row][D] at offset 0, over the K ring, idle by then.
   static constexpr int kOffStage = (kOffRow + (kFlag + NG) * 4 + 15) / 16 * 16;
@@ -317,9 +318,8 @@ __device__ __forceinline__ void diff_tc_softmax(const DiffParams& dp, const int*
     for (int item = tid; item < T::kRows * 8; item += NST) {
       const int r = item >> 3, part = item & 7;
       constexpr int NW = D / 64;  // 8-dim pieces per item
-      const __half* qrow = nullptr;
-      if (r < pq.R)
-        qrow = p.q + (static_cast<long long>(pq.q0 + r / p.G) * p.Hq + pq.kh * p.G + r % p.G) * D;
+      const int row = (pq.q0 + r / p.G) * p.Hq + pq.kh * p.G + r % p.G;
+      const __half* qrow = r < pq.R ? p.q + static_cast<long long>(row) * D : nullptr;
       uint4 qv[NW];
       float mx = 0.f;
       auto to_f = [&](uint32_t w) { return p.out_bf16 ? pair_to_float2<true>(w) : pair_to_float2<false>(w); };
@@ -383,6 +383,8 @@ __device__ __forceinline__ void diff_tc_softmax(const DiffParams& dp, const int*
         const int hi = r < pq.R ? pq.L - pq.qlen + r / p.G : -1;
         ri[T::kHi + r] = hi;
         ri[T::kLo + r] = p.window > 0 ? max(0, hi - p.window + 1) : 0;
+        ri[T::kRow + r] = row;
+        rf[T::kLam + r] = r < pq.R ? __ldg(dp.lambda + row % p.Hq) : 0.f;
       }
     }
     fence_proxy_async_smem();
@@ -538,6 +540,10 @@ __device__ __forceinline__ void diff_tc_softmax(const DiffParams& dp, const int*
     }
     bq += nblk;
 
+    float w[S];  // the norm's weights of this thread's dims, read before the waits
+#pragma unroll
+    for (int h = 0; h < S; ++h)
+      w[h] = dp.norm_weight != nullptr && pc.npieces == 1 ? norm_weight_at(dp, 128 * h + key) : 0.f;
     // ---- the piece's end: O^T (this thread: dims key, key + 128) of the group's
     // rows of both maps, and the row sums
     if (ok) ok = mbar_wait(bar(T::kBarPvDone), (bq - 1) & 1, p.timeout_ns);
@@ -580,8 +586,7 @@ __device__ __forceinline__ void diff_tc_softmax(const DiffParams& dp, const int*
 #pragma unroll
       for (int r = 0; r < 8; ++r) {
         const float l1 = l_row[r], l2 = l_row[8 + r];
-        const int row = 8 * g + r;
-        const float lam = row < pc.R ? __ldg(dp.lambda + pc.kh * p.G + row % p.G) : 0.f;
+        const float lam = rf[T::kLam + 8 * g + r];
         const float i1 = l1 > 0.f ? p.out_scale / l1 : 0.f, i2 = l2 > 0.f ? p.out_scale / l2 * lam : 0.f;
         ss[r] = 0.f;
 #pragma unroll
@@ -594,9 +599,6 @@ __device__ __forceinline__ void diff_tc_softmax(const DiffParams& dp, const int*
         const float sum = warp_transpose_reduce<false, 8>(ss, lane);
         if (lane < 8) red[(warp & 3) * 16 + lane] = sum;
         named_bar_sync(bid, 128);
-        float w[S];
-#pragma unroll
-        for (int h = 0; h < S; ++h) w[h] = norm_weight_at(dp, 128 * h + key);
 #pragma unroll
         for (int r = 0; r < 8; ++r) {
           const float tot = (red[r] + red[16 + r]) + (red[32 + r] + red[48 + r]);
@@ -608,10 +610,8 @@ __device__ __forceinline__ void diff_tc_softmax(const DiffParams& dp, const int*
       }
 #pragma unroll
       for (int r = 0; r < 8; ++r) {
-        const int row = 8 * g + r;
-        if (row >= pc.R) break;
-        uint16_t* dst = reinterpret_cast<uint16_t*>(p.out) +
-                        (static_cast<long long>(pc.q0 + row / p.G) * p.Hq + pc.kh * p.G + row % p.G) * D;
+        if (8 * g + r >= pc.R) break;
+        uint16_t* dst = reinterpret_cast<uint16_t*>(p.out) + static_cast<long long>(ri[T::kRow + 8 * g + r]) * D;
 #pragma unroll
         for (int h = 0; h < S; ++h)
           dst[128 * h + key] = static_cast<uint16_t>(pack_out(p.out_bf16 != 0, o[h][r], 0.f) & 0xffffu);
@@ -658,13 +658,24 @@ __device__ __forceinline__ void diff_tc_merge(const DiffParams& dp, uint32_t sba
   constexpr int D = T::D, V4 = D / 128;
   const int S = p.cluster, rank = static_cast<int>(cluster_rank()), u = blockIdx.x / S;
   const int b = u / p.hgn, kh = u % p.hgn;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // what is no partial is read before the cluster's barrier
   int L, t0, n, q0, qn;
   seq_span(p, b, false, L, t0, n, q0, qn);
-  if (n == 0) return;
-  const int chunk = (n + S - 1) / S;
-  if (n <= chunk) return;
-  const int R = p.G * qn, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int r = rank + S * warp; r < R; r += S * (T::kThreads / 32)) {
+  const int R = n > (n + S - 1) / S ? p.G * qn : 0;  // (one piece or none: finished)
+  float4 wt[V4];
+  if (dp.norm_weight != nullptr) {
+#pragma unroll
+    for (int v = 0; v < V4; ++v) {
+      const int d = 4 * (32 * v + lane);
+      wt[v] = make_float4(norm_weight_at(dp, d), norm_weight_at(dp, d + 1), norm_weight_at(dp, d + 2),
+                          norm_weight_at(dp, d + 3));
+    }
+  }
+  int r = rank + S * warp;
+  float lam = r < R ? __ldg(dp.lambda + kh * p.G + r % p.G) : 0.f;
+  cluster_sync();  // every CTA of the cluster has staged its partial
+  for (; r < R; r += S * (T::kThreads / 32)) {
     float4 y[V4];
 #pragma unroll
     for (int m = 0; m < 2; ++m) {
@@ -694,7 +705,7 @@ __device__ __forceinline__ void diff_tc_merge(const DiffParams& dp, uint32_t sba
         }
       }
       float inv = l > 0.f ? p.out_scale / l : 0.f;
-      if (m == 1) inv *= -__ldg(dp.lambda + kh * p.G + r % p.G);
+      if (m == 1) inv *= -lam;
 #pragma unroll
       for (int v = 0; v < V4; ++v) {
         acc[v] = make_float4(map_out(l, acc[v].x), map_out(l, acc[v].y), map_out(l, acc[v].z), map_out(l, acc[v].w));
@@ -703,19 +714,28 @@ __device__ __forceinline__ void diff_tc_merge(const DiffParams& dp, uint32_t sba
                                 fmaf(acc[v].w, inv, y[v].w));
       }
     }
-    float f = 1.f;
     if (dp.norm_weight != nullptr) {
       float ss = 0.f;
 #pragma unroll
       for (int v = 0; v < V4; ++v) ss += y[v].x * y[v].x + y[v].y * y[v].y + y[v].z * y[v].z + y[v].w * y[v].w;
 #pragma unroll
       for (int o = 16; o >= 1; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      f = rsqrtf(ss / static_cast<float>(D) + dp.norm_eps) * dp.norm_gain;
+      const float f = rsqrtf(ss / static_cast<float>(D) + dp.norm_eps) * dp.norm_gain;
+      // (a zero row with eps = 0: rsqrt is infinite, the row stays zero)
+      auto normed = [&](float x, float w) { return x == 0.f ? 0.f : x * f * w; };
+#pragma unroll
+      for (int v = 0; v < V4; ++v)
+        y[v] = make_float4(normed(y[v].x, wt[v].x), normed(y[v].y, wt[v].y), normed(y[v].z, wt[v].z),
+                           normed(y[v].w, wt[v].w));
     }
     uint16_t* dst = reinterpret_cast<uint16_t*>(p.out) +
                     (static_cast<long long>(q0 + r / p.G) * p.Hq + kh * p.G + r % p.G) * D;
+    const bool bf = p.out_bf16 != 0;
 #pragma unroll
-    for (int v = 0; v < V4; ++v) store_row4(dp, dst, 4 * (32 * v + lane), y[v], f);
+    for (int v = 0; v < V4; ++v)
+      *reinterpret_cast<uint2*>(dst + 4 * (32 * v + lane)) =
+          make_uint2(pack_out(bf, y[v].x, y[v].y), pack_out(bf, y[v].z, y[v].w));
+    if (r + S * (T::kThreads / 32) < R) lam = __ldg(dp.lambda + kh * p.G + (r + S * (T::kThreads / 32)) % p.G);
   }
 }
 
@@ -882,7 +902,6 @@ __global__ void __launch_bounds__(T::kThreads, 1)
   tc_fence_before();
   __syncthreads();
   if (p.cluster > 1) {
-    cluster_sync();  // every CTA of the cluster has staged its partial
     diff_tc_merge<T>(dp, sbase);
     cluster_sync();  // no CTA leaves while a peer still reads its shared memory
   }
