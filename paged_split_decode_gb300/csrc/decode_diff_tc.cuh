@@ -93,7 +93,10 @@ struct DiffTc {
   // number below every score, so that nothing need be told apart: the exponential
   // of a masked score (-inf) against it is zero.
   static constexpr float kNone = -3e38f;
-  static constexpr int kUnitCost = 24;                // a piece's fixed cost in 16-key tiles (balanced split)
+  // A piece's fixed cost in 16-key tiles (balanced split; 24 / 40 / 64: e4m3, 32
+  // ragged sequences of up to 8192 keys, D = 256 72.3 / 63.2 / 64.9 us, 24 of 8 heads, D =
+  // 128 76.3 / 64.0 / 61.5; int8, 24 / 32 / 40: 78.7 / 77.0 / 78.9, 79.9 / 73.1 / 72.2).
+  static constexpr int kUnitCost = CODES ? 40 : 32;
 
   static constexpr int kOffV = NBK * kBlkBytes;
   static constexpr int kOffV16 = kOffV + NBV * kBlkBytes;
