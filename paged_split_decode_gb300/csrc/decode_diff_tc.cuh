@@ -60,8 +60,9 @@ struct DiffTc {
   static constexpr int kTerms = CODES ? 3 : 1;        // terms of a weight
   // e4m3: terms of q that stand side by side on the N side of S^T, two where the
   // tensor memory holds it (B = 8, L = 8192, qlen = 3: 16 products of one term
-  // each take 1630 cycles a block to issue, 43.2 us; 8 of two take 1040, 37.7). A third term then comes with a fourth
-  // of zeros in a second pass, added to the first.
+  // each take 1630 cycles a block to issue, 43.2 us; 8 of two take 1040, 37.7). A
+  // third term then comes with a fourth of zeros in a second pass, added to the
+  // first.
   static constexpr int kStack = CODES && 8 * kRows + kSlabs * 3 * 16 * NG <= 512 ? 2 : 1;
   static constexpr int kQTerms = !CODES ? 1 : kStack == 2 ? 4 : 3;
   static constexpr int kQTerm = kRows * 128;          // a term of q, 128 bytes of its dims: [rows][128 B]
@@ -136,7 +137,8 @@ __device__ __forceinline__ void split_weight(uint32_t a, uint32_t b, uint32_t (&
   auto codes = [](uint32_t x, uint32_t y) { return prmt(x >> 7, y >> 7, 0x6420u); };
   auto rest = [&](uint32_t x) {
     const uint32_t lead = x & 0xff80ff80u;
-    const __half2 r = __hmul2(__hsub2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&lead)), s16);
+    const __half2 r =
+        __hmul2(__hsub2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&lead)), s16);
     return *reinterpret_cast<const uint32_t*>(&r);
   };
   t[0] = codes(a, b);
