@@ -243,31 +243,34 @@ def test_offsets_past_32_bits(pd):
     assert torch.equal(got, want)
 
 
-def test_two_streams_and_two_captured_graphs(pd):
+@pytest.mark.parametrize("kv,qlen", [("f16", 1), ("fp8_bf16q", 3), ("int8", 4)])
+def test_two_streams_and_two_captured_graphs(pd, kv, qlen):
     """Calls without a workspace on two streams, and two graphs captured on
     one stream and replayed on two, do not share partials."""
-    ws = [inputs.make_workload(B=2, Hq=24, Hkv=4, D=256, seq_lens=[3000, 2000], kv="f16", seed=s, scale=128 ** -0.5)
-          for s in (47, 48)]
+    ws = [inputs.make_workload(B=2, Hq=24, Hkv=4, D=256, seq_lens=[3000, 2000], qlen=qlen, kv=kv, seed=s,
+                               scale=128 ** -0.5) for s in (47, 48)]
     lams = [factors(w)[0] for w in ws]
     want = [run(pd, w, lam).clone() for w, lam in zip(ws, lams)]
     args = []
     for w, lam in zip(ws, lams):
         k, v = caches(w)
-        args.append([w.q.to(DEV), k, v, w.block_table.to(DEV), w.seq_lens.to(DEV), lam.to(DEV), w.scale])
-    outs = [torch.empty_like(a[0]) for a in args]
+        args.append(dict(q=w.q.to(DEV), k_cache=k, v_cache=v, block_table=w.block_table.to(DEV),
+                         seq_lens=w.seq_lens.to(DEV), lam=lam.to(DEV), scale=w.scale, qlen=qlen, k_scale=w.k_scale,
+                         v_scale=w.v_scale))
+    outs = [torch.empty_like(a["q"]) for a in args]
     streams = [torch.cuda.Stream(), torch.cuda.Stream()]
     torch.cuda.synchronize()
     for _ in range(20):
         for s, a, o in zip(streams, args, outs):
             with torch.cuda.stream(s):
-                pd.decode_paged_diff(*a, out=o)
+                pd.decode_paged_diff(**a, out=o)
     torch.cuda.synchronize()
     assert all(torch.equal(o, x) for o, x in zip(outs, want))
     graphs = []
     for a, o in zip(args, outs):
         g = torch.cuda.CUDAGraph()
         with torch.cuda.graph(g, stream=streams[0]):
-            pd.decode_paged_diff(*a, out=o)
+            pd.decode_paged_diff(**a, out=o)
         graphs.append(g)
         o.zero_()
     torch.cuda.synchronize()
