@@ -5,8 +5,11 @@ under _build/, then linked into paged_split_decode_gb300/libpdecode.so (the
 CUDA runtime is linked statically; the driver's tensor-map encoder is reached
 through the runtime's entry-point query, so no -lcuda is needed). csrc/bind.cpp
 becomes _bind.so beside it, the compiled part of the Python binding, against
-the headers of the installed PyTorch. A rebuild is skipped when both are newer
-than every source and header and PyTorch is the one they were built for.
+the headers of the installed PyTorch. The library does not depend on it: where
+those headers are missing the library is built all the same, with a warning, and
+the calls that go through the compiled binding raise. Each of the two is built
+when it is older than a source or header of its own, _bind.so also when PyTorch
+is not the one it was built for.
 """
 from __future__ import annotations
 
@@ -18,6 +21,7 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -45,7 +49,11 @@ def sources():
 
 
 def _bind_for() -> str:
-    return f"torch {importlib.metadata.version('torch')} python {sys.version.split()[0]}"
+    try:
+        version = importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:
+        version = "missing"
+    return f"torch {version} python {sys.version.split()[0]}"
 
 
 def _bind_command(out: str):
@@ -57,19 +65,45 @@ def _bind_command(out: str):
             "-ltorch_cpu", "-ltorch_python", "-Xlinker", f"-rpath={lib}"]
 
 
-def _stale() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(BIND):
+def _older(target: str, deps) -> bool:
+    if not os.path.exists(target):
         return True
+    t = os.path.getmtime(target)
+    return any(os.path.getmtime(p) > t for p in [*deps, *glob.glob(os.path.join(ROOT, "include", "*.h")), __file__])
+
+
+def _stale() -> bool:
+    headers = glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh"))
+    return _older(LIB, sources() + headers)
+
+
+def _bind_stale() -> bool:
     if not os.path.exists(BIND_FOR) or open(BIND_FOR).read() != _bind_for():
         return True
-    t = min(os.path.getmtime(LIB), os.path.getmtime(BIND))
-    deps = sources() + [BIND_SRC] + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh")) \
-        + glob.glob(os.path.join(ROOT, "include", "*.h")) + [__file__]
-    return any(os.path.getmtime(p) > t for p in deps)
+    return _older(BIND, [BIND_SRC])
+
+
+def _build_bind() -> str:
+    """Build _bind.so; returns "" or what failed."""
+    tmp = BIND + f".tmp{os.getpid()}"
+    try:
+        r = subprocess.run(_bind_command(tmp), capture_output=True, text=True)
+        if r.returncode == 0:
+            os.replace(tmp, BIND)
+            with open(BIND_FOR, "w") as f:
+                f.write(_bind_for())
+            return ""
+        why = f"{r.stdout}\n{r.stderr}"
+    except (OSError, AttributeError) as e:  # no compiler, no PyTorch
+        why = repr(e)
+    if os.path.exists(BIND):
+        os.remove(BIND)  # one of other sources or another PyTorch
+    return why
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
-    if not force and not _stale():
+    lib, bind = force or _stale(), force or _bind_stale()
+    if not lib and not bind:
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     cc = nvcc()
@@ -85,25 +119,19 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
             sys.stderr.write(r.stdout + r.stderr)
         return obj
 
-    def compile_bind():
-        tmp = BIND + f".tmp{os.getpid()}"
-        r = subprocess.run(_bind_command(tmp), capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"build of {BIND_SRC} failed:\n{r.stdout}\n{r.stderr}")
-        os.replace(tmp, BIND)
-        with open(BIND_FOR, "w") as f:
-            f.write(_bind_for())
-
     with ThreadPoolExecutor(max_workers=min(16, os.cpu_count() or 1)) as ex:
-        bind = ex.submit(compile_bind)
-        objs = list(ex.map(compile_one, sources()))
-        bind.result()
-    tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [cc, *ARCH, "-shared", "-o", tmp, *objs]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, LIB)
+        bind_done = ex.submit(_build_bind) if bind else None
+        if lib:
+            objs = list(ex.map(compile_one, sources()))
+            tmp = LIB + f".tmp{os.getpid()}"
+            r = subprocess.run([cc, *ARCH, "-shared", "-o", tmp, *objs], capture_output=True, text=True)
+            if r.returncode != 0:
+                raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+            os.replace(tmp, LIB)
+        why = bind_done.result() if bind_done else ""
+    if why:
+        warnings.warn(f"build of {BIND_SRC} failed; the calls of the compiled binding will raise:\n{why}",
+                      RuntimeWarning, stacklevel=2)
     return LIB
 
 

@@ -155,3 +155,30 @@ def test_python_refusals():
         a.update(kw)
         with pytest.raises(ValueError):
             pd.decode_paged_diff(**a)
+
+
+def test_the_library_is_built_without_the_python_headers(tmp_path, monkeypatch):
+    """A compiled binding that does not build (no PyTorch or Python headers) is
+    reported and leaves the library built; the calls that need it say why."""
+    src = tmp_path / "one.cu"
+    src.write_text('extern "C" __attribute__((visibility("default"))) int answer() { return 42; }\n')
+    for name, path in (("BUILD", "_build"), ("LIB", "lib.so"), ("BIND", "_bind.so"), ("BIND_FOR", "bind.for")):
+        monkeypatch.setattr(build, name, str(tmp_path / path))
+    monkeypatch.setattr(build, "sources", lambda: [str(src)])
+    command = build._bind_command
+    monkeypatch.setattr(build, "_bind_command", lambda out: ["false"])
+    with pytest.warns(RuntimeWarning, match="bind.cpp"):
+        assert build.build() == str(tmp_path / "lib.so")
+    assert ctypes.CDLL(build.LIB).answer() == 42 and not (tmp_path / "_bind.so").exists()
+    # the next build does not compile the library again, and builds the binding once that works
+    before = (tmp_path / "lib.so").stat().st_mtime_ns
+    monkeypatch.setattr(build, "_bind_command", lambda out: ["touch", out])
+    assert build.build() == build.LIB
+    assert (tmp_path / "lib.so").stat().st_mtime_ns == before and (tmp_path / "_bind.so").exists()
+    # a binding left from other sources does not stand in for one that fails
+    (tmp_path / "bind.for").write_text("another PyTorch")
+    monkeypatch.setattr(build, "_bind_command", lambda out: ["false"])
+    with pytest.warns(RuntimeWarning):
+        build.build()
+    assert not (tmp_path / "_bind.so").exists()
+    monkeypatch.setattr(build, "_bind_command", command)
