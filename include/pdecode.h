@@ -274,9 +274,14 @@ PD_API pd_status decode_paged_diff(const void* q, const void* k_cache, const voi
  * A sequence is served whole or not at all: one with a bad length
  * (PD_DEVERR_SEQ_LEN), whose tokens pass num_tokens (PD_DEVERR_QUERY_START) or
  * for which the free list has too few blocks (PD_DEVERR_FREE_LIST; every later
- * sequence that needs a block is refused too) takes no block, its seq_lens
- * entry is 0 and its slots are -1. An id outside [0, num_blocks) among those
- * used sets PD_DEVERR_BLOCK_ID and gives slot -1. One launch on `stream`. */
+ * sequence that needs a block is refused too) takes no block and its slots are
+ * -1. Its seq_lens entry is 0 where seq_lens is a buffer of its own (a decode
+ * then writes zeros for it); where seq_lens is context_lens itself the entry
+ * stays as it was, so that the sequence keeps its blocks, can be served in a
+ * later step and released (a decode of the refused step then gives its rows
+ * the keys that it has: results to be ignored, as its slots say). An id outside
+ * [0, num_blocks) among those used sets PD_DEVERR_BLOCK_ID and gives slot -1.
+ * One launch on `stream`. */
 PD_API pd_status build_block_tables(const int32_t* context_lens, const int32_t* query_lens,
                                     int num_tokens, int32_t* block_table,
                                     const int32_t* free_blocks, const int32_t* free_count,

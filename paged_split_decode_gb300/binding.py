@@ -437,6 +437,12 @@ def build_block_tables(context_lens, query_lens, block_table, free_blocks, free_
     ``num_tokens`` entries (or those of the given ``slot_mapping``), -1 / 0
     behind the last token. ``seq_lens`` may be ``context_lens`` itself;
     ``free_count`` is updated in place unless ``free_count_out`` is given.
+
+    A sequence that cannot be served (no free block, a full row, a token buffer
+    that is too short) takes nothing, its slots are -1 and ``error_flag`` says
+    why. Its ``seq_lens`` entry is 0 in a buffer of its own; in place it keeps
+    its context, so the sequence and its blocks are there for a later step or
+    a release.
     """
     return (_bind or _fast()).build_block_tables(context_lens, query_lens, block_table, free_blocks, free_count,
                                                  block_size, num_tokens, seq_lens, query_start_loc, slot_mapping,

@@ -219,8 +219,10 @@ __global__ void __launch_bounds__(NT, 1) build_tables_kernel(const TableArgs a) 
     if (b < a.B) {
       const int c = s_ctx[b];
       // query_b = start_{b+1} - start_b (exact while the sums do not saturate,
-      // and a sequence behind a saturated sum is refused)
-      a.seq_lens[b] = c >= 0 ? c + (s_start[b + 1] - s_start[b]) : 0;
+      // and a sequence behind a saturated sum is refused). In place, a refused
+      // sequence keeps its context: nothing else knows the blocks that it holds.
+      if (c >= 0) a.seq_lens[b] = c + (s_start[b + 1] - s_start[b]);
+      else if (a.seq_lens != a.context) a.seq_lens[b] = 0;
     }
   }
   if (me == 0) *a.count_out = count - taken;
