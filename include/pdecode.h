@@ -113,8 +113,9 @@ typedef struct {
  * every partial row, then its O row); a split unit's pieces and their slots
  * follow from the sequence lengths, so nothing else is stored. Every
  * call writes what it later reads, so the buffer needs no initialisation and
- * one buffer serves any sequence of calls on one stream; calls that may run
- * at the same time must not share a workspace. Returns 0 for invalid dims. */
+ * one buffer serves any sequence of calls on one stream, from any threads (a
+ * call's launches stay together); calls that may run at the same time on the
+ * GPU must not share a workspace. Returns 0 for invalid dims. */
 PD_API size_t pd_workspace_bytes(const pd_dims* dims, int qlen, int num_splits, int sm_count);
 
 /* Number of CTAs decode_paged launches for these arguments (persistent grid),

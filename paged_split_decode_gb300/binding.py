@@ -203,8 +203,9 @@ def get_workspace(device: torch.device, nbytes: int, stream: int | None = None) 
     """A reusable workspace per (device, stream), grown on demand.
 
     Every call writes what it reads, so one buffer serves every call made on
-    one stream in turn; calls on different streams (which may overlap on the
-    GPU) get different buffers. ``stream`` is the raw cudaStream_t handle the
+    one stream in turn, whichever threads make them (a call's launches stay
+    together); calls on different streams (which may overlap on the GPU) get
+    different buffers. ``stream`` is the raw cudaStream_t handle the
     call launches on (default: torch's current stream on ``device``); the
     buffer is allocated on that stream, so torch's allocator reuses it, once
     it is outgrown, only in that stream's order."""
