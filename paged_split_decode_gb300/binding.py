@@ -391,14 +391,15 @@ def _diff_workspace(need, index, stream):
     """The workspace of a differential decode that brought none. A captured
     call keeps one of its own in the graph's pool, as graphs may be replayed at
     the same time; else the (device, stream) one of ``get_workspace``."""
-    s = torch._C._cuda_getCurrentRawStream(index) if stream is None else int(stream)
-    if not torch.cuda.is_current_stream_capturing():
-        ws = _workspaces.get(("cuda", index, s))
-        if ws is not None and ws.numel() >= need:
-            return ws
+    cur = torch._C._cuda_getCurrentRawStream(index)
+    s = cur if stream is None else int(stream)
+    if s == cur:
+        if not torch.cuda.is_current_stream_capturing():
+            ws = _workspaces.get(("cuda", index, s))
+            return ws if ws is not None and ws.numel() >= need else get_workspace(torch.device("cuda", index), need, s)
+        return torch.empty(need, dtype=torch.uint8, device=torch.device("cuda", index))
     device = torch.device("cuda", index)
-    cur = torch.cuda.current_stream(device)
-    with torch.cuda.stream(cur if s == cur.cuda_stream else torch.cuda.ExternalStream(s, device=device)):
+    with torch.cuda.stream(torch.cuda.ExternalStream(s, device=device)):  # (whether the call's stream is capturing)
         if torch.cuda.is_current_stream_capturing():
             return torch.empty(need, dtype=torch.uint8, device=device)
         return get_workspace(device, need, s)

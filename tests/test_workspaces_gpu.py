@@ -1,10 +1,11 @@
-"""Calls without a workspace of their own: two threads on one stream."""
+"""Calls without a workspace of their own: two threads on one stream, and
+captures made through a stream handle."""
 import threading
 
 import pytest
 import torch
 
-from paged_split_decode_gb300 import inputs
+from paged_split_decode_gb300 import binding, inputs
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
@@ -59,3 +60,31 @@ def test_two_threads_on_one_stream(pd, kinds):
     torch.cuda.synchronize()
     assert not failed
     assert [int(b) for b in bad] == [0, 0]
+
+
+def test_a_capture_through_a_stream_handle_has_its_own_workspace(pd):
+    """The captured stream is the call's, not the current one: the graph's
+    workspace is not the one that eager calls of that stream use."""
+    s, other = torch.cuda.Stream(), torch.cuda.Stream()
+    args = prepared("diff", 5)
+    torch.cuda.synchronize()
+    pd.decode_paged_diff(**args, stream=s.cuda_stream)  # the stream's eager workspace
+    torch.cuda.synchronize()
+    want = args["out"].clone()
+    eager = binding._workspaces[("cuda", 0, s.cuda_stream)]
+    seen = []
+    keep = binding._diff_workspace
+
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        with torch.cuda.stream(other):
+            seen.append(keep(1 << 16, 0, s.cuda_stream))
+            pd.decode_paged_diff(**args, stream=s.cuda_stream)
+        seen.append(keep(1 << 16, 0, None))
+    assert all(x.data_ptr() != eager.data_ptr() for x in seen)
+    assert keep(1 << 16, 0, s.cuda_stream).data_ptr() == eager.data_ptr()
+    args["out"].zero_()
+    torch.cuda.synchronize()
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(args["out"], want)
