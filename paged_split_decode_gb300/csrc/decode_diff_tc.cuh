@@ -381,7 +381,8 @@ __device__ __forceinline__ void diff_tc_softmax(const DiffParams& dp, const int*
       }
       if ((part & 3) == 0) {
         const int at = 16 * (r >> 3) + 8 * (part >> 2) + (r & 7);
-        rf[T::kFs + at] = r < pq.R ? p.sl2 * pow2f(-e) : 0.f;
+        // (an infinity has no e4m3 terms, and no key's score with it is a number)
+        rf[T::kFs + at] = mx == INFINITY ? NAN : r < pq.R ? p.sl2 * pow2f(-e) : 0.f;
         rf[T::kTh + at] = T::kNone;
       }
       if (part == 0) {
