@@ -23,11 +23,16 @@
 //  * e4m3: the products read the codes themselves (kind::f8f6f4), as in
 //    decode_tc8.cuh: no widening at all. q is the sum of two (bfloat16) or three
 //    (fp16) e4m3 terms, summed in the one accumulator of S^T. A weight is rounded
-//    to fp16 and cut into three e4m3 terms of 4, 4 and 3 of its bits, the second
-//    and third scaled by 2^4 and 2^8: every fp16 value in [0, 1] is the sum of its
-//    terms exactly, by shifts and subtractions alone (split_weight). The terms
-//    stand side by side on the N side of P.V, their accumulators are added with
-//    their scales at a piece's end.
+//    to fp16 and cut into three e5m2 terms, the second and third scaled by 2^4 and
+//    2^8: every fp16 value in [0, 2^15] is the sum of its terms exactly, by bit
+//    operations and subtractions alone (split_weight). The terms stand side by side
+//    on the N side of P.V, their accumulators are added with their scales at a
+//    piece's end.
+//  * Weights are 2^15 where a score reaches its row's threshold, so that fp16 keeps
+//    11 bits of them down to 2^-29 of that and the last down to 2^-39: a key of few
+//    weights does not vanish beside a peak (it is what two maps leave of each other
+//    once their peaks cancel). e4m3 terms reach 2^-22 of a peak, and in a map with one
+//    key 16 nats above 32767 others a percent of it was lost.
 //  * The row sums add the rounded weights. V rows of keys beyond the end are
 //    zeros, so that stale NaN codes never meet a zero weight.
 //  * S^T at NG = 3 also reads q rows 24 .. 31 of the operand, which belong to the
@@ -83,13 +88,12 @@ struct DiffTc {
   static constexpr int kTmemCols = kCols <= 256 ? 256 : 512;
   static constexpr uint32_t kIdescS = CODES ? idesc_e4m3(128, kSN) : idesc_f16(128, kSN, false, false);
   static constexpr uint32_t kIdescO =
-      CODES ? idesc_e4m3(128, kTerms * kON) | (3u << 15) : idesc_f16(128, kON, true, true);
+      CODES ? idesc_e4m3(128, kTerms * kON) | (1u << 10) /* B: e5m2 */ | (3u << 15) : idesc_f16(128, kON, true, true);
   // A running maximum is raised past a gap of kRaise (log2); weights are
-  // 2^(x - m + kBias): at most 1 for split_weight, at most 2^8 where they are plain
-  // fp16. (A gap of 1 raises in most of the first blocks: 830 cycles a block for the
+  // 2^(x - m + kBias), at most 2^15. (A gap of 1 raises in most of the first blocks: 830 cycles a block for the
   // maxima, 300 with 3.)
   static constexpr float kRaise = CODES ? 3.f : 4.f;
-  static constexpr float kBias = CODES ? -kRaise : 4.f;
+  static constexpr float kBias = 15.f - kRaise;
   // The row state holds the threshold m + kRaise. Before the first visible key m is a
   // number below every score, so that nothing need be told apart: the exponential
   // of a masked score (-inf) against it is zero.
@@ -127,24 +131,27 @@ struct DiffTc {
   static_assert(2 * kRows * D * 4 <= kOffV, "the staged rows fit over the K ring");
 };
 
-// Four fp16 weights in [0, 1] (two pairs) to three words of e4m3 codes, w 2^8 = t1
-// + t2 2^-4 + t3 2^-8 exactly. A value's leading four bits are its fp16 bits above
-// the seventh: shifted there they are the e4m3 code of 2^8 times it, subnormals
-// included (both types count 2^-17 there). The rest, below 2^-3 of the value,
-// moves up by 2^4 and gives its leading four; what is left are three bits.
+// Four fp16 weights in [0, 2^15] (two pairs) to three words of e5m2 codes, w = t1 +
+// t2 2^-4 + t3 2^-8 exactly. An e5m2 code is the upper byte of an fp16 value, the
+// nearest one that of the bits plus half of the lower byte's range. What it leaves of a
+// weight in [2^e, 2^(e+1)), a multiple of 2^(e-10), is at most 2^(e-3); 2^4 times that
+// is rounded in turn and leaves at most 8 multiples of 2^(e-6), which 2^4 times are an
+// e5m2 value. (Below 2^-14 the steps are those of e = -14.)
 __device__ __forceinline__ void split_weight(uint32_t a, uint32_t b, uint32_t (&t)[3]) {
   const __half2 s16 = __float2half2_rn(16.f);
-  auto codes = [](uint32_t x, uint32_t y) { return prmt(x >> 7, y >> 7, 0x6420u); };
-  auto rest = [&](uint32_t x) {
-    const uint32_t lead = x & 0xff80ff80u;
+  auto near = [](uint32_t x) { return (x + 0x00800080u) & 0xff00ff00u; };
+  auto codes = [](uint32_t x, uint32_t y) { return prmt(x, y, 0x7531u); };
+  auto rest = [&](uint32_t x, uint32_t lead) {
     const __half2 r =
         __hmul2(__hsub2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&lead)), s16);
     return *reinterpret_cast<const uint32_t*>(&r);
   };
-  t[0] = codes(a, b);
-  a = rest(a), b = rest(b);
-  t[1] = codes(a, b);
-  a = rest(a), b = rest(b);
+#pragma unroll
+  for (int m = 0; m < 2; ++m) {
+    const uint32_t na = near(a), nb = near(b);
+    t[m] = codes(na, nb);
+    a = rest(a, na), b = rest(b, nb);
+  }
   t[2] = codes(a, b);
 }
 
@@ -484,7 +491,7 @@ __device__ __forceinline__ void diff_tc_softmax(const DiffParams& dp, const int*
       uint32_t pw[8];
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        constexpr float kUp = T::kRaise + T::kBias;  // 0 for CODES
+        constexpr float kUp = T::kRaise + T::kBias;  // 15
         const float a = ex2(x[2 * k] - th[2 * k] + kUp), c = ex2(x[2 * k + 1] - th[2 * k + 1] + kUp);
         pw[k] = pack_half2(a, c);
         const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&pw[k]));
@@ -561,16 +568,16 @@ __device__ __forceinline__ void diff_tc_softmax(const DiffParams& dp, const int*
       if (ok) {
         const uint32_t at = tl + T::kColO + T::kON * NTM * h + 16 * g;
         tmem_ld16(at, o[h]);
-        if constexpr (CODES) {  // the terms' scales; the codes stand for 2^8 times the weights
+        if constexpr (CODES) {  // the terms' scales
           float y[16];
           tmem_ld16(at + T::kON, y);
           tmem_wait_ld();
 #pragma unroll
-          for (int r = 0; r < 16; ++r) o[h][r] = fmaf(y[r], 0x1p-12f, o[h][r] * 0x1p-8f);
+          for (int r = 0; r < 16; ++r) o[h][r] = fmaf(y[r], 0x1p-4f, o[h][r]);
           tmem_ld16(at + 2 * T::kON, y);
           tmem_wait_ld();
 #pragma unroll
-          for (int r = 0; r < 16; ++r) o[h][r] = fmaf(y[r], 0x1p-16f, o[h][r]);
+          for (int r = 0; r < 16; ++r) o[h][r] = fmaf(y[r], 0x1p-8f, o[h][r]);
         }
         tmem_wait_ld();
       } else {

@@ -1,4 +1,9 @@
-"""The differential decode where numbers are extreme: infinite queries and keys."""
+"""The differential decode where numbers are extreme: infinite queries and keys, and
+maps with one key far above the rest.
+
+The error bound is ref_diff.py's with the weights' rounding u as an argument:
+d = (u + f) (A_1 + |lambda| A_2), |gpu - ref| <= d + u_out |ref|."""
+import numpy as np
 import pytest
 import torch
 
@@ -16,6 +21,28 @@ def pd():
     import paged_split_decode_gb300 as pd
     pd.load()
     return pd
+
+
+def reference(w, lam, u, f, norm_weight=None, eps=1e-5, gain=1.0, extra=0.0):
+    """(out, bound) of ref_diff.reference with u, f and an absolute term d_0 = ``extra``."""
+    out, full = ref_diff.reference(w, lam)
+    own = (2.0 ** -11 if (w.kv_fp8 or w.kv_int8) else ref_diff.HALF_STEP[w.q.dtype]) + 2.0 ** (-11 if w.kv_fp8 else -12)
+    half = ref_diff.HALF_STEP[w.q.dtype]
+    d = (full - half * np.abs(out) - 2.0 ** -24) * ((u + f) / own) + extra
+    if norm_weight is not None:
+        rms = np.sqrt(np.mean(out ** 2, axis=-1, keepdims=True))
+        e = np.sqrt(np.mean(d ** 2, axis=-1, keepdims=True))
+        k, lo, hi = (gain / np.sqrt(x ** 2 + eps) for x in (rms, rms + e, np.maximum(rms - e, 0.0)))
+        d = np.abs(norm_weight) * (d * hi + np.abs(out) * np.maximum(hi - k, k - lo))
+        out = out * k * norm_weight
+    return out, d + half * np.abs(out) + 2.0 ** -24
+
+
+def check(got, ref, bound):
+    g = got.float().cpu().numpy().astype(np.float64)
+    assert np.all(np.isfinite(g))
+    excess = np.abs(g - ref) / bound
+    assert excess.max() <= 1.0, f"error {excess.max():.2f}x the bound"
 
 
 # ---------------------------------------------------------------------------
@@ -89,3 +116,79 @@ def test_an_infinite_key(pd, kv, qlen):
             err = (got[i, 6 + h].double().cpu() - o).abs()
             assert torch.all(err <= (u + 2.0 ** -12) * a + u * o.abs() + 2.0 ** -24)
 
+
+# ---------------------------------------------------------------------------
+def peaked(kv, L, qlen, G, seed, peak_value):
+    """One key near the middle with a score about 16 above all others in both maps; the
+    other keys' values have a common offset of 2.
+
+    q = (+-1 rows of a fixed sign vector) + 0.25 N(0, 1), the peak key 1.45 times
+    that vector: its score is 1.45 128 128^-1/2 (1 +- 0.02) = 16.4 +- 0.5; the
+    others' N(0, 1) rows score N(0, 1.06)."""
+    g = torch.Generator().manual_seed(seed)
+    w = inputs.make_workload(B=1, Hq=G, Hkv=1, D=256, seq_lens=[L], qlen=qlen, kv=kv, seed=seed, scale=128 ** -0.5)
+    u = torch.where(torch.rand(256, generator=g) < 0.5, -1.0, 1.0)
+    w.q = (u + 0.25 * torch.randn(w.q.shape, generator=g)).to(w.q.dtype)
+    at = L // 2 + 5
+    blk, off = int(w.block_table[0, at // 16]), at % 16
+
+    def codes(x, s):
+        if w.kv_int8:
+            return (x / s).round().clamp(-127, 127).to(torch.int8).view(torch.uint8)
+        if w.kv_fp8:
+            return (x / s).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+        return x.to(w.k_cache.dtype)
+
+    noise = torch.randn(w.v_cache.shape, generator=g)
+    if w.kv_int8 or w.kv_fp8:
+        w.v_scale = 8.0 / (127 if w.kv_int8 else 448)
+    w.v_cache = codes(2.0 + noise, w.v_scale)
+    w.k_cache[blk, off, 0] = codes(1.45 * u, w.k_scale)
+    w.v_cache[blk, off, 0] = codes(peak_value * noise[blk, off, 0], w.v_scale)
+    return w
+
+
+def weight_step(w):
+    return 2.0 ** -11 if w.kv_int8 or w.kv_fp8 else ref_diff.HALF_STEP[w.q.dtype]
+
+
+# The scores' fp32 part of f (2^-13 for scores whose terms sum to less than 11) is
+# twice that here (17.5 for the peak); the exponentials and sums stay below it as
+# there: f = 2^-12 + 2^-13, and 2^-11 + 2^-13 with e4m3 terms of q.
+def peaked_f(w):
+    return (2.0 ** -11 if w.kv_fp8 else 2.0 ** -12) + 2.0 ** -13
+
+
+@pytest.mark.parametrize("S", (0, 1, 3))
+@pytest.mark.parametrize("L", (8192, 32768))
+@pytest.mark.parametrize("G,qlen", [(6, 3), (4, 3), (6, 4)])
+@pytest.mark.parametrize("kv", ("fp8", "fp8_bf16q", "int8"))
+def test_the_tail_of_a_peaked_map(pd, kv, G, qlen, L, S):
+    """The peak's value is zero, so the output is the tail's alone: weights 2^-23 of
+    the peak's, which hold as many bits as any."""
+    w = peaked(kv, L, qlen, G, 5 + L + G, 0.0)
+    lam = torch.full((G,), 0.97)
+    ref, bound = reference(w, lam.double().numpy(), weight_step(w), peaked_f(w))
+    assert np.abs(ref).max() > 4e-5  # the tail is there
+    check(run(pd, w, lam, S), ref, bound)
+    weight = (1 + 0.1 * torch.randn(256, generator=torch.Generator().manual_seed(3))).to(w.q.dtype)
+    ref, bound = reference(w, lam.double().numpy(), weight_step(w), peaked_f(w), weight.double().numpy(), 1e-12, 0.4)
+    check(run(pd, w, lam, S, weight, norm_eps=1e-12, norm_gain=0.4), ref, bound)
+
+
+@pytest.mark.parametrize("kv", ("fp8", "int8"))
+@pytest.mark.parametrize("L", (8192, 32768))
+@pytest.mark.parametrize("qlen", (3,))
+def test_a_peak_with_a_value(pd, kv, L, qlen):
+    """The peak's own value in the output. Every key's product is added to an
+    accumulator of the peak's size, where it loses at most a last place of that
+    accumulator, 2^-23 of it: L 2^-23 |v_peak| more."""
+    w = peaked(kv, L, qlen, 6, 9 + L, 1.0)
+    lam = torch.full((6,), 0.97)
+    at = L // 2 + 5
+    v = w.v_cache[int(w.block_table[0, at // 16]), at % 16, 0]
+    if kv != "f16":
+        v = v.view(torch.int8 if kv == "int8" else torch.float8_e4m3fn)
+    v = v.double().abs().numpy() * w.v_scale
+    ref, bound = reference(w, lam.double().numpy(), weight_step(w), peaked_f(w), extra=1.97 * L * 2.0 ** -23 * v)
+    check(run(pd, w, lam), ref, bound)
