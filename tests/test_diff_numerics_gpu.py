@@ -161,8 +161,8 @@ def peaked_f(w):
 
 @pytest.mark.parametrize("S", (0, 1, 3))
 @pytest.mark.parametrize("L", (8192, 32768))
-@pytest.mark.parametrize("G,qlen", [(6, 3), (4, 3), (6, 4)])
-@pytest.mark.parametrize("kv", ("fp8", "fp8_bf16q", "int8"))
+@pytest.mark.parametrize("G,qlen", [(6, 3), (4, 3), (6, 4), (8, 4), (6, 1)])
+@pytest.mark.parametrize("kv", ("fp8", "fp8_bf16q", "int8", "f16", "bf16"))
 def test_the_tail_of_a_peaked_map(pd, kv, G, qlen, L, S):
     """The peak's value is zero, so the output is the tail's alone: weights 2^-23 of
     the peak's, which hold as many bits as any."""
@@ -176,9 +176,9 @@ def test_the_tail_of_a_peaked_map(pd, kv, G, qlen, L, S):
     check(run(pd, w, lam, S, weight, norm_eps=1e-12, norm_gain=0.4), ref, bound)
 
 
-@pytest.mark.parametrize("kv", ("fp8", "int8"))
+@pytest.mark.parametrize("kv", ("fp8", "int8", "f16"))
 @pytest.mark.parametrize("L", (8192, 32768))
-@pytest.mark.parametrize("qlen", (3,))
+@pytest.mark.parametrize("qlen", (1, 3))
 def test_a_peak_with_a_value(pd, kv, L, qlen):
     """The peak's own value in the output. Every key's product is added to an
     accumulator of the peak's size, where it loses at most a last place of that
