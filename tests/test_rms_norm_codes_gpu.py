@@ -55,3 +55,27 @@ def test_codes_are_the_rounded_quotients(pd, N, kind, top, offset):
     want = t.to(torch.float8_e4m3fn).float() if q == 448.0 else t.round()
     bad = (codes.float().cpu() != want).nonzero()
     assert bad.shape[0] == 0, f"{bad.shape[0]} codes of {3 * N} are off, first {bad[0].tolist()}"
+
+
+@pytest.mark.parametrize("kind", (torch.float8_e4m3fn, torch.int8))
+@pytest.mark.parametrize("seed", range(12))
+def test_codes_under_drawn_scales(pd, kind, seed):
+    """Scales drawn over 60 powers of two, quotients anywhere and on ties, small and subnormal codes among them."""
+    q = 448.0 if kind == torch.float8_e4m3fn else 127.0
+    rng = np.random.RandomState(100 + seed)
+    N = 4096
+    top = np.float32(rng.uniform(1, 2) * 2.0 ** rng.randint(-30, 30))
+    w = weights(N, q, top, seed)
+    some = rng.rand(N) < 0.5
+    w[some] = (top * rng.uniform(0, 1, N) * 2.0 ** -rng.uniform(0, 18, N)).astype(np.float32)[some]
+    w[rng.randint(N)] = top
+    assert w.max() == top
+    codes, scale = pd.rms_norm(torch.ones(1, N, dtype=torch.float16, device=DEV), torch.from_numpy(w).to(DEV), 0.0,
+                               out_dtype=kind)
+    torch.cuda.synchronize()
+    s = top / np.float32(q)
+    assert float(scale) == s
+    t = torch.from_numpy(w / s)
+    want = t.to(torch.float8_e4m3fn).float() if q == 448.0 else t.round()
+    bad = (codes[0].float().cpu() != want).nonzero()
+    assert bad.shape[0] == 0, f"{bad.shape[0]} codes of {N} are off, first {bad[0].tolist()}"
