@@ -86,8 +86,7 @@ struct DiffCfg {
   static constexpr int kXTiles = 2 * RG * NTR;
   static constexpr int kXP = kXTiles * 32 * 8 * KT;
   static constexpr int kXOne = kXP + kXTiles * 8 * 4 + 16;
-  static constexpr int kXEnd = kXTiles * 8 * 4 + W * NTM * 8 * 4;  // row sums; sums of squares
-  static constexpr int kXHead = 2 * kXOne + (kMerge ? 0 : kXEnd);
+  static constexpr int kXHead = 2 * kXOne;
   static constexpr int kX = W > 1 ? HG * KG * kXHead : 0;
   static constexpr int kOffMergeML = NS * kStageBytes + kMergeO;
   static constexpr int kOffX = kOffMergeML + kMergeML;
@@ -99,6 +98,9 @@ struct DiffCfg {
   static_assert(KG == 1 || NS % (KG * KT) == 0, "ring stages must be a multiple of the key groups' steps");
   static_assert(KT == 1 || KT == 2, "one or two tiles a step");
   static_assert(W == 1 || W == 4, "one or four warps per head");
+  // the straight epilogue has no exchange between a head's warps, and no barrier
+  // that keeps a fast warp's next piece out of the buffers that a slow one still reads
+  static_assert(W == 1 || kMerge, "a head's warps end a piece in the merge's barriers");
   static_assert(HG * KG <= 14, "named barriers 2.. serve the heads' warps");
 };
 
@@ -711,49 +713,23 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::kMinBlocks)
               }
             }
           }
-        if (g == 0) {  // the maxima and sums of the rows this warp scored
+        if (g == 0) {  // the maxima and sums
 #pragma unroll
-          for (int m = 0; m < MPW; ++m)
+          for (int m = 0; m < 2; ++m)
 #pragma unroll
-            for (int n = 0; n < NTR; ++n)
+            for (int n = 0; n < NTM; ++n)
 #pragma unroll
               for (int c = 0; c < 2; ++c) {
-                const int r = (rt0 + n) * 8 + 2 * t4 + c;
-                const long long prow =
-                    static_cast<long long>(pc.slot) * Cfg::RP + th * Cfg::RH + (W == 1 ? m : map) * Cfg::RM + r;
+                const int r = n * 8 + 2 * t4 + c;
+                const long long prow = static_cast<long long>(pc.slot) * Cfg::RP + th * Cfg::RH + m * Cfg::RM + r;
                 if (r < pc.R)
                   __stcg(reinterpret_cast<float2*>(p.ws_ml + prow * 2), make_float2(m_r[m][n][c], l_r[m][n][c]));
               }
         }
         continue;
       }
-      // the whole unit: row sums of both maps, the difference, the norm. The
-      // warps of a head swap sums; the buffers' last readers are a tile's
-      // barrier back, and a piece without tiles (all sums zero) swaps nothing.
-      const uint32_t xl = xch + 2 * Cfg::kXOne, xs = xl + Cfg::kXTiles * 32;
-      float l_map[2][NTM][2];
-      if constexpr (W > 1) {
-        if (g == 0) {
-#pragma unroll
-          for (int n = 0; n < NTR; ++n)
-            sts_f2(xl + (map * Cfg::RG * NTR + rt0 + n) * 32 + 8 * t4, l_r[0][n][0], l_r[0][n][1]);
-        }
-        if (pc.ntiles > 0) named_bar_sync(2 + th * KG + kg, W * 32);
-      }
-#pragma unroll
-      for (int m = 0; m < 2; ++m)
-#pragma unroll
-        for (int n = 0; n < NTM; ++n) {
-          if constexpr (W == 1) {
-            l_map[m][n][0] = l_r[m % MPW][n % NTR][0];
-            l_map[m][n][1] = l_r[m % MPW][n % NTR][1];
-          } else {
-            float2 v = make_float2(0.f, 0.f);
-            if (ntiles > 0) v = lds_f2(xl + (m * Cfg::RG * NTR + n) * 32 + 8 * t4);
-            l_map[m][n][0] = v.x;
-            l_map[m][n][1] = v.y;
-          }
-        }
+      // the whole unit: the difference of both maps, the norm (W = 1: the warp holds
+      // the rows' sums and all of V's dims)
       float ss[NTM][2];
 #pragma unroll
       for (int n = 0; n < NTM; ++n)
@@ -761,14 +737,15 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::kMinBlocks)
         for (int c = 0; c < 2; ++c) {
           const int r = n * 8 + 2 * t4 + c;
           const float lam = r < pc.R ? __ldg(dp.lambda + (pc.kh + th) * p.G + r % p.G) : 0.f;
-          const float inv1 = l_map[0][n][c] > 0.f ? p.out_scale / l_map[0][n][c] : 0.f;
-          const float inv2 = l_map[1][n][c] > 0.f ? p.out_scale / l_map[1][n][c] * lam : 0.f;
+          const float l1 = l_r[0][n][c], l2 = l_r[1][n][c];
+          const float inv1 = l1 > 0.f ? p.out_scale / l1 : 0.f;
+          const float inv2 = l2 > 0.f ? p.out_scale / l2 * lam : 0.f;
           float s = 0.f;
 #pragma unroll
           for (int mtl = 0; mtl < MTW; ++mtl)
 #pragma unroll
             for (int e = c; e < 4; e += 2) {
-              const float v = map_out(l_map[0][n][c], o[0][mtl][n][e]) * inv1 - map_out(l_map[1][n][c], o[1][mtl][n][e]) * inv2;
+              const float v = map_out(l1, o[0][mtl][n][e]) * inv1 - map_out(l2, o[1][mtl][n][e]) * inv2;
               o[0][mtl][n][e] = v;
               s += v * v;
             }
@@ -781,25 +758,6 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::kMinBlocks)
           for (int off = 4; off < 32; off <<= 1) {
             ss[n][0] += __shfl_xor_sync(0xffffffffu, ss[n][0], off);
             ss[n][1] += __shfl_xor_sync(0xffffffffu, ss[n][1], off);
-          }
-          if (W > 1 && g == 0)
-            sts_f2(xs + (w * NTM + n) * 32 + 8 * t4, ss[n][0], ss[n][1]);
-        }
-        if constexpr (W > 1) {
-          if (pc.ntiles > 0) named_bar_sync(2 + th * KG + kg, W * 32);
-#pragma unroll
-          for (int n = 0; n < NTM; ++n) {
-            float2 s = make_float2(0.f, 0.f);
-            if (pc.ntiles > 0) {
-#pragma unroll
-              for (int ww = 0; ww < W; ++ww) {
-                const float2 v = lds_f2(xs + (ww * NTM + n) * 32 + 8 * t4);
-                s.x += v.x;
-                s.y += v.y;
-              }
-            }
-            ss[n][0] = s.x;
-            ss[n][1] = s.y;
           }
         }
       }
