@@ -60,10 +60,16 @@ struct DiffCfg {
   static constexpr int kSlabBytes = HG * kHeadBytes;  // [head][key][128 B]
   static constexpr int kTileBytes = kSlabs * kSlabBytes;
   static constexpr int kStageBytes = 2 * kTileBytes;
-  // 16-bit caches, a warp per head: P is carried as the sum of two operands (the
-  // rounded value and the rounded rest), which makes the output as exact as one
-  // rounding allows
-  static constexpr int PP = W == 1 && !BYTE ? 2 : 1;
+  // 16-bit caches, up to 16 query rows per map: P is carried as the sum of two
+  // operands (the rounded value and the rounded rest), which makes the output as
+  // exact as one rounding allows (error against 64 bits, relative to its norm: fp16
+  // 2.1e-4, bfloat16 1.66e-3, as in 32 bits throughout). Elsewhere P is rounded to the
+  // operands' type once (fp16 3.2e-4, bfloat16 2.5e-3; byte caches, whose operands are
+  // fp16, 3.2e-4 under an fp16 q, 1.69e-3 under a bfloat16 one): the second products
+  // cost 2 % with two row tiles (qlen = 2, B = 8, L = 8192, D = 256: 50.0 -> 51.1 us), 26
+  // and 30 % with three and four (56.1 -> 71.0, 74.6 -> 97.1), 28 % over byte caches
+  // with one (e4m3, B = 32, L = 4096: 53.8 -> 69.8).
+  static constexpr int PP = !BYTE && NTM <= 2 ? 2 : 1;
   static constexpr int MPW = W == 1 ? 2 : 1;             // maps a warp scores
   static constexpr int RG = W == 4 ? 2 : 1;              // row groups
   static constexpr int NTR = (NTM + RG - 1) / RG;        // row tiles (per map) a warp scores
@@ -84,7 +90,8 @@ struct DiffCfg {
   // a head's exchange, double-buffered: packed P [map][row tile][lane], rescale
   // factors [map][row tile][row], a flag per warp
   static constexpr int kXTiles = 2 * RG * NTR;
-  static constexpr int kXP = kXTiles * 32 * 8 * KT;
+  static constexpr int kXPlane = kXTiles * 32 * 8 * KT;
+  static constexpr int kXP = kXPlane * PP;
   static constexpr int kXOne = kXP + kXTiles * 8 * 4 + 16;
   static constexpr int kXHead = 2 * kXOne;
   static constexpr int kX = W > 1 ? HG * KG * kXHead : 0;
@@ -527,7 +534,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::kMinBlocks)
           float nb[2];
 #pragma unroll
           for (int c = 0; c < 2; ++c) nb[c] = m_r[m][n][c] == -INFINITY ? 0.f : kUp - m_r[m][n][c];
-          uint32_t pk[KT][2];
+          uint32_t pk[KT][2 * PP];
 #pragma unroll
           for (int j = 0; j < KT; ++j) {
             const float p00 = ex2(fmaf(x[j][m][n][0], sl2r[m][n][0], nb[0]));
@@ -538,19 +545,22 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::kMinBlocks)
             l_r[m][n][1] += p01 + p11;
             pk[j][0] = movmatrix_trans(pack2<BF16>(p00, p01));
             pk[j][1] = movmatrix_trans(pack2<BF16>(p10, p11));
-            if constexpr (W == 1) {
-              pf[j][m][n][0] = pk[j][0];
-              pf[j][m][n][1] = pk[j][1];
-            }
             if constexpr (PP == 2) {
-              pf[j][m][n][PP] = movmatrix_trans(pack2<BF16>(p00 - round16<BF16>(p00), p01 - round16<BF16>(p01)));
-              pf[j][m][n][PP + 1] = movmatrix_trans(pack2<BF16>(p10 - round16<BF16>(p10), p11 - round16<BF16>(p11)));
+              pk[j][PP] = movmatrix_trans(pack2<BF16>(p00 - round16<BF16>(p00), p01 - round16<BF16>(p01)));
+              pk[j][PP + 1] = movmatrix_trans(pack2<BF16>(p10 - round16<BF16>(p10), p11 - round16<BF16>(p11)));
+            }
+            if constexpr (W == 1) {
+#pragma unroll
+              for (int i = 0; i < 2 * PP; ++i) pf[j][m][n][i] = pk[j][i];
             }
           }
           if constexpr (W > 1) {
             const uint32_t at = xcur + ((map * Cfg::RG * NTR + rt0 + n) * 32 + lane) * 8 * KT;
-            if constexpr (KT == 1) sts_v2(at, pk[0][0], pk[0][1]);
-            else sts_v4(at, pk[0][0], pk[0][1], pk[KT - 1][0], pk[KT - 1][1]);
+#pragma unroll
+            for (int h = 0; h < PP; ++h) {
+              if constexpr (KT == 1) sts_v2(at + h * Cfg::kXPlane, pk[0][2 * h], pk[0][2 * h + 1]);
+              else sts_v4(at + h * Cfg::kXPlane, pk[0][2 * h], pk[0][2 * h + 1], pk[KT - 1][2 * h], pk[KT - 1][2 * h + 1]);
+            }
           }
         }
       if constexpr (W > 1) {
@@ -562,16 +572,19 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::kMinBlocks)
 #pragma unroll
           for (int n = 0; n < NTM; ++n) {
             const uint32_t at = xcur + ((m * Cfg::RG * NTR + n) * 32 + lane) * 8 * KT;
-            if constexpr (KT == 1) {
-              const uint2 v = lds_v2(at);
-              pf[0][m][n][0] = v.x;
-              pf[0][m][n][1] = v.y;
-            } else {
-              const uint4 v = lds_v4(at);
-              pf[0][m][n][0] = v.x;
-              pf[0][m][n][1] = v.y;
-              pf[KT - 1][m][n][0] = v.z;
-              pf[KT - 1][m][n][1] = v.w;
+#pragma unroll
+            for (int h = 0; h < PP; ++h) {
+              if constexpr (KT == 1) {
+                const uint2 v = lds_v2(at + h * Cfg::kXPlane);
+                pf[0][m][n][2 * h] = v.x;
+                pf[0][m][n][2 * h + 1] = v.y;
+              } else {
+                const uint4 v = lds_v4(at + h * Cfg::kXPlane);
+                pf[0][m][n][2 * h] = v.x;
+                pf[0][m][n][2 * h + 1] = v.y;
+                pf[KT - 1][m][n][2 * h] = v.z;
+                pf[KT - 1][m][n][2 * h + 1] = v.w;
+              }
             }
           }
         if (uniform(fl.x | fl.y | fl.z | fl.w)) {

@@ -192,3 +192,33 @@ def test_a_peak_with_a_value(pd, kv, L, qlen):
     v = v.double().abs().numpy() * w.v_scale
     ref, bound = reference(w, lam.double().numpy(), weight_step(w), peaked_f(w), extra=1.97 * L * 2.0 ** -23 * v)
     check(run(pd, w, lam), ref, bound)
+
+
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("S", (0, 1, 2))
+@pytest.mark.parametrize("Hq,Hkv,D,qlen", [(24, 4, 256, 1), (32, 8, 128, 1), (6, 3, 128, 1), (12, 2, 256, 2), (8, 1, 128, 2),
+                                           (32, 8, 128, 4), (6, 3, 256, 5)])
+@pytest.mark.parametrize("kv", ("f16", "bf16"))
+def test_weights_of_two_operands(pd, kv, Hq, Hkv, D, qlen, S):
+    """Up to 16 rows per map over 16-bit caches: nothing of a weight's rounding is seen
+    where the two maps nearly cancel (lambda = 1, halves alike to 5 %), short
+    sequences, so that a single weight's error shows.
+
+    u = 2^-16 (bfloat16) or 2^-22: the rest of a rounded weight, rounded. f: scores
+    whose terms sum to less than 3 take at most D / 2 <= 128 additions of 2^-23 of
+    that, 2^-14.4; exponentials, sums over 10 keys and the last division stay below
+    2^-18: f = 2^-14."""
+    B = 40
+    lens = [qlen + 2 + i % 8 for i in range(B)]
+    w = inputs.make_workload(B=B, Hq=Hq, Hkv=Hkv, D=D, seq_lens=lens, qlen=qlen, kv=kv, seed=D + qlen,
+                             scale=(D // 2) ** -0.5)
+    h = D // 2
+    g = torch.Generator().manual_seed(77)
+    w.q = (0.2 * w.q.float()).to(w.q.dtype)
+    for x in (w.q, w.k_cache):
+        x[..., h:] = (x[..., :h].float() * (1 + 0.05 * torch.randn(x[..., :h].shape, generator=g))).to(x.dtype)
+    terms = w.q[..., :h].float().abs().view(-1, h) @ w.k_cache[..., :h].float().abs().view(-1, h).T * w.scale
+    assert float(terms.max()) < 3.0
+    u = 2.0 ** -22 if kv == "f16" else 2.0 ** -16
+    ref, bound = reference(w, np.ones(Hq), u, 2.0 ** -14)
+    check(run(pd, w, torch.ones(Hq), S), ref, bound)
