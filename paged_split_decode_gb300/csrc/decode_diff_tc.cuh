@@ -943,7 +943,7 @@ bool diff_tc_shape_of(KernelShape* out) {
   out->heads = 1;
   out->unit_cost = T::kUnitCost;
   out->fixed_pieces = 1;
-  out->step_tiles = T::kBlkTiles;
+  out->step_tiles = out->key_groups = T::kBlkTiles;
   out->whole_tile = T::CODES ? 0 : 1;
   static unsigned long long ctx_done[64] = {};
   static int cache[64][kMaxCluster + 1] = {};

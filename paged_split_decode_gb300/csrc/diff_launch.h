@@ -53,7 +53,8 @@ bool diff_shape_of(KernelShape* out) {
   out->rows_padded = Cfg::RP;
   out->ctas_per_sm = Cfg::kMinBlocks;
   out->heads = Cfg::HG;
-  out->step_tiles = Cfg::KG;
+  out->step_tiles = Cfg::KG * Cfg::KT;
+  out->key_groups = Cfg::KG;
   out->whole_tile = 1;
   // what a piece's end costs, in tiles: 1 us from the accumulators, 5 us where key
   // groups merge first (measured, D = 256 GQA 6:1, L = 8192, B = 8, qlen = 3, 4 /

@@ -20,6 +20,7 @@ struct KernelShape {
                     // an automatic plan over few units takes the fixed split (one piece per CTA)
   int whole_tile = 0;  // 1: a TMA box is a tile of all slabs (4-D map), else one slab of it
   int step_tiles = 1;  // tiles that a CTA takes at once (the plan of short tables)
+  int key_groups = 1;  // of them, tiles that different warps take (few units of short tables)
   int max_clusters[17];  // [S]: clusters of S CTAs the device runs at once (0: no cluster merge)
 };
 

@@ -185,15 +185,20 @@ pd_status make_plan(const pd_dims* d, int qlen, int num_splits, int sm_count, Pl
   // 19.1 / 19.6 / 59.5. Eight steps at most: a batch with one long sequence then
   // waits four steps longer. Where pieces merge inside a cluster, as many of two steps
   // or more as the CTAs hold are better still (4 / 32 / 64 units, 48 tiles 16.7 / 16.8
-  // / 17.1 -> 13.4 / 13.8 / 15.4).
+  // / 17.1 -> 13.4 / 13.8 / 15.4). A step is as many tiles as the CTA takes at once,
+  // two per key group where a warp takes two (D = 128, 32 x 8 heads, B = 76, 12 / 16 tiles
+  // balanced 25.9 / 28.6 -> 18.1 / 20.9, three row tiles, B = 38, 24 / 32 tiles 26.5 / 29.6
+  // -> 21.7 / 24.7); for few units, whose other plan is the fixed split below with pieces
+  // that end early, one per key group (B = 1, 12 tiles 11.8, whole 14.2).
   if (automatic && diff && pl->units > 0) {
     const long long waves = (pl->units + ctas - 1) / ctas;
     const long long tiles = (vis_keys + kTileKeys - 1) / kTileKeys;
-    const long long room = std::min<long long>({ctas / pl->units, tiles / (2 * ks.step_tiles), kMaxCluster});
-    if (tiles <= 8 * ks.step_tiles) {
+    const int step = pl->units <= ctas / 4 ? ks.key_groups : ks.step_tiles;
+    const long long room = std::min<long long>({ctas / pl->units, tiles / (2 * step), kMaxCluster});
+    if (tiles <= 8 * step) {
       if (room >= 2 && ks.max_clusters[room] >= pl->units)
         splits = static_cast<int>(room);
-      else if (tiles * (waves * ctas - pl->units) <= 4ll * ks.step_tiles * (ctas + pl->units))
+      else if (tiles * (waves * ctas - pl->units) <= 4ll * step * (ctas + pl->units))
         splits = 1;
     }
   }
