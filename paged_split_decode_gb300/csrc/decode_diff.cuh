@@ -134,14 +134,21 @@ __device__ __forceinline__ uint32_t pack_out(bool bf16, float lo, float hi) {
   return bf16 ? pack_bf162(lo, hi) : pack_half2(lo, hi);
 }
 
+// The factor of a row of D elements whose squares sum to ss. (A row of zeros with eps =
+// 0 stays zero; one with a NaN is NaN throughout, its zeros too.)
+template <int D>
+__device__ __forceinline__ float norm_factor(const DiffParams& p, float ss) {
+  const float t = ss / static_cast<float>(D) + p.norm_eps;
+  return t == 0.f ? 0.f : rsqrtf(t) * p.norm_gain;
+}
+
 // Four dims d .. d + 3 of an output row, normalised by f where there is a norm.
-// (A zero row with eps = 0: rsqrt is infinite, the row stays zero.)
 __device__ __forceinline__ void store_row4(const DiffParams& p, uint16_t* dst, int d, float4 v, float f) {
   if (p.norm_weight != nullptr) {
-    v.x = v.x == 0.f ? 0.f : v.x * f * norm_weight_at(p, d);
-    v.y = v.y == 0.f ? 0.f : v.y * f * norm_weight_at(p, d + 1);
-    v.z = v.z == 0.f ? 0.f : v.z * f * norm_weight_at(p, d + 2);
-    v.w = v.w == 0.f ? 0.f : v.w * f * norm_weight_at(p, d + 3);
+    v.x *= f * norm_weight_at(p, d);
+    v.y *= f * norm_weight_at(p, d + 1);
+    v.z *= f * norm_weight_at(p, d + 2);
+    v.w *= f * norm_weight_at(p, d + 3);
   }
   const bool bf = p.d.out_bf16 != 0;
   *reinterpret_cast<uint2*>(dst + d) = make_uint2(pack_out(bf, v.x, v.y), pack_out(bf, v.z, v.w));
@@ -780,7 +787,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::kMinBlocks)
         for (int c = 0; c < 2; ++c) {
           const int r = n * 8 + 2 * t4 + c;
           if (r >= pc.R) continue;
-          const float f = rsqrtf(ss[n][c] / static_cast<float>(D) + dp.norm_eps) * dp.norm_gain;
+          const float f = norm_factor<D>(dp, ss[n][c]);
           uint16_t* dst = reinterpret_cast<uint16_t*>(p.out) +
                           (static_cast<long long>(pc.q0 + r / p.G) * p.Hq + (pc.kh + th) * p.G + r % p.G) * D;
 #pragma unroll
@@ -788,9 +795,8 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::kMinBlocks)
             const int d0 = dim0(mtl);
             float a = o[0][mtl][n][c], b = o[0][mtl][n][2 + c];
             if (dp.norm_weight != nullptr) {
-              // (a zero row with eps = 0: rsqrt is infinite, the row stays zero)
-              a = a == 0.f ? 0.f : a * f * norm_weight_at(dp, d0);
-              b = b == 0.f ? 0.f : b * f * norm_weight_at(dp, d0 + kStep);
+              a *= f * norm_weight_at(dp, d0);
+              b *= f * norm_weight_at(dp, d0 + kStep);
             }
             const uint32_t v = pack_out(p.out_bf16 != 0, a, b);
             if constexpr (BYTE) {
@@ -898,7 +904,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::kMinBlocks)
           if (dp.norm_weight != nullptr) {
 #pragma unroll
             for (int off = 16; off >= 1; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
-            f = rsqrtf(ss / static_cast<float>(D) + dp.norm_eps) * dp.norm_gain;
+            f = norm_factor<D>(dp, ss);
           }
           uint16_t* dst = reinterpret_cast<uint16_t*>(p.out) + (static_cast<long long>(pc.q0 + r / p.G) * p.Hq + head) * D;
 #pragma unroll
@@ -1057,12 +1063,11 @@ __global__ void __launch_bounds__(NT, NT <= 384 ? 2 : 1) diff_combine_kernel(con
         __syncthreads();
         ss = s_ss[(t >> 5) & ~1] + s_ss[(t >> 5) | 1];
       }
-      const float f = rsqrtf(ss / static_cast<float>(D) + dp.norm_eps) * dp.norm_gain;
-      // (a zero row with eps = 0: rsqrt is infinite, the row stays zero)
-      v.x = v.x == 0.f ? 0.f : v.x * f * wt.x;
-      v.y = v.y == 0.f ? 0.f : v.y * f * wt.y;
-      v.z = v.z == 0.f ? 0.f : v.z * f * wt.z;
-      v.w = v.w == 0.f ? 0.f : v.w * f * wt.w;
+      const float f = norm_factor<D>(dp, ss);
+      v.x *= f * wt.x;
+      v.y *= f * wt.y;
+      v.z *= f * wt.z;
+      v.w *= f * wt.w;
     }
     if (on && pg == 0)
       *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(p.out) +

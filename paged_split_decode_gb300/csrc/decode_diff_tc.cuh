@@ -615,10 +615,9 @@ __device__ __forceinline__ void diff_tc_softmax(const DiffParams& dp, const int*
 #pragma unroll
         for (int r = 0; r < 8; ++r) {
           const float tot = (red[r] + red[16 + r]) + (red[32 + r] + red[48 + r]);
-          const float f = rsqrtf(tot / static_cast<float>(D) + dp.norm_eps) * dp.norm_gain;
-          // (a zero row with eps = 0: rsqrt is infinite, the row stays zero)
+          const float f = norm_factor<D>(dp, tot);
 #pragma unroll
-          for (int h = 0; h < S; ++h) o[h][r] = o[h][r] == 0.f ? 0.f : o[h][r] * f * w[h];
+          for (int h = 0; h < S; ++h) o[h][r] *= f * w[h];
         }
       }
 #pragma unroll
@@ -733,9 +732,8 @@ __device__ __forceinline__ void diff_tc_merge(const DiffParams& dp, uint32_t sba
       for (int v = 0; v < V4; ++v) ss += y[v].x * y[v].x + y[v].y * y[v].y + y[v].z * y[v].z + y[v].w * y[v].w;
 #pragma unroll
       for (int o = 16; o >= 1; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      const float f = rsqrtf(ss / static_cast<float>(D) + dp.norm_eps) * dp.norm_gain;
-      // (a zero row with eps = 0: rsqrt is infinite, the row stays zero)
-      auto normed = [&](float x, float w) { return x == 0.f ? 0.f : x * f * w; };
+      const float f = norm_factor<D>(dp, ss);
+      auto normed = [&](float x, float w) { return x * (f * w); };
 #pragma unroll
       for (int v = 0; v < V4; ++v)
         y[v] = make_float4(normed(y[v].x, wt[v].x), normed(y[v].y, wt[v].y), normed(y[v].z, wt[v].z),
