@@ -238,8 +238,9 @@ PD_API pd_status write_kv_cache(const void* k_new, const void* v_new, const int6
  *                   norm_weight)
  *   workspace       pd_diff_workspace_bytes(dims, qlen, num_splits, 0) bytes
  * A map contributes zeros to a row that has no visible key, or where a visible
- * score is NaN or +infinity (a NaN in that half of q or K); NaN and infinities
- * of visible V rows show in the output. Softmax weights are computed in fp32 and
+ * score is NaN or +infinity (a NaN in that half of q or K). NaN and infinities
+ * of V rows show, as NaN or infinity, in the output rows that see the key and in no other
+ * (several query tokens, windows). Softmax weights are computed in fp32 and
  * enter the product with V as two 16-bit operands over 16-bit caches with
  * Hq/Hkv*qlen <= 16, else rounded once to 16 bits (bfloat16 for bfloat16 caches,
  * fp16 for all others); every sum is fp32. Hq/Hkv*qlen must be <= 32. */

@@ -35,12 +35,15 @@
 #pragma once
 #include <cuda_bf16.h>
 
+#include <type_traits>
+
 #include "decode_kernel.cuh"
 
 namespace pd {
 
 struct DiffParams {
   DecodeParams d;
+  const void* v_cache;      // V beside its tensor map (for the rare look at single elements)
   const float* lambda;      // [Hq]
   const void* norm_weight;  // [D] or null
   int norm_f32;             // norm_weight is fp32 (else q's type)
@@ -152,6 +155,20 @@ __device__ __forceinline__ void store_row4(const DiffParams& p, uint16_t* dst, i
   }
   const bool bf = p.d.out_bf16 != 0;
   *reinterpret_cast<uint2*>(dst + d) = make_uint2(pack_out(bf, v.x, v.y), pack_out(bf, v.z, v.w));
+}
+
+// NaN and infinities in V of keys that not every row of a unit sees -- the newest
+// keys under several query tokens, those about a window's start -- would reach the
+// rows that do not see them, whose weight of zero times them is NaN. Such keys are
+// in a unit's first and last tiles only: there they are taken out of the product's
+// operand, and a piece that had one marks the outputs of the rows that see it at its
+// end.
+
+// The elements that are NaN or infinite of two 16-bit ones, as a mask.
+template <bool BF16>
+__device__ __forceinline__ uint32_t not_finite_16(uint32_t w) {
+  constexpr uint32_t kExp = BF16 ? 0x7f807f80u : 0x7c007c00u, kUlp = BF16 ? 0x00800080u : 0x04000400u;
+  return ((((w & kExp) + kUlp) & 0x80008000u) >> 15) * 0xffffu;
 }
 
 template <class Cfg>
@@ -306,6 +323,9 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::kMinBlocks)
   while (uniform(work_next(p, s_pre, it, pc))) {
     const int ntiles = uniform(pc.ntiles), first_tile = uniform(pc.first_tile), seq_len = uniform(pc.L);
     const int lo_all = uniform(pc.tile_lo_all), hi_all = uniform(pc.tile_hi_all);
+    constexpr bool kScreen = Cfg::KV != kKvInt8;
+    const int screen_hi = pc.qlen > 1 ? hi_all : 0x7fffffff;
+    uint32_t odd = 0;                        // elements that were taken out
     // ---- q fragments of the rows and maps this warp scores
     float sl2r[MPW][NTR][2];                 // score factors (log2 units), positive
     int hi_r[NTR][2];                        // last visible key of a row
@@ -384,13 +404,19 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::kMinBlocks)
     // (a piece without tiles has no step, not even the one that it would start in:
     // that one's stage is not its to give back)
     const int last = ntiles > 0 ? ntiles + lead : 0;
-    for (int st = (kg - static_cast<int>(step0 % KG) + KG) % KG; st * KT < last; st += KG) {
+    // A step is compiled twice: for tiles that every row sees whole, and for the others
+    // (EDGE: masks, values, a missing tile), so that the common one has no branch (B = 32,
+    // L = 4096, D = 256: int8 61.0 -> 57.8 us, e4m3 53.8 -> 53.2; fp16, qlen = 3, B = 8, L =
+    // 8192: 56.6 before values were looked at, 58.0 so, 62.6 in one copy). int8 caches have
+    // no values to look at, and four warps a head gain nothing there.
+    auto step = [&](const int st, auto edge_step) __attribute__((always_inline)) {
+      constexpr bool EDGE = decltype(edge_step)::value;
       const int k0 = st * KT - lead;
       bool have[KT];
       int tile[KT];  // a step's missing tile is its other one over again, masked: no branch splits the step
 #pragma unroll
       for (int j = 0; j < KT; ++j) {
-        have[j] = k0 + j >= 0 && k0 + j < ntiles;
+        have[j] = !EDGE || (k0 + j >= 0 && k0 + j < ntiles);
         if (ok && have[j])
           ok = __all_sync(0xffffffffu, mbar_wait(full0 + 8 * ((q + k0 + j) % NS), ((q + k0 + j) / NS) & 1, p.timeout_ns));
       }
@@ -398,7 +424,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::kMinBlocks)
       for (int j = 0; j < KT; ++j) tile[j] = have[j] ? k0 + j : k0 + (KT - 1 - j);
       if (!ok) {  // gave up: keep the head's barrier sequence
         if constexpr (W > 1) named_bar_sync(2 + th * KG + kg, W * 32);
-        continue;
+        return;
       }
       constexpr int PP = Cfg::PP;
       uint32_t pf[KT][2][NTM][2 * PP];  // P^T fragments of both maps
@@ -459,7 +485,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::kMinBlocks)
             }
         }
         const int key0 = (first_tile + tile[j]) * kTileKeys;
-        const bool interior = have[j] && key0 >= lo_all && key0 + kTileKeys - 1 <= hi_all;
+        const bool interior = !EDGE || (have[j] && key0 >= lo_all && key0 + kTileKeys - 1 <= hi_all);
         const int j0 = key0 + kg0, j1 = j0 + 8;
 #pragma unroll
         for (int n = 0; n < NTR; ++n) {
@@ -617,7 +643,16 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::kMinBlocks)
       for (int j = 0; j < KT; ++j) {
         const uint32_t stage = (q + tile[j]) % NS, sbase = smem0 + stage * Cfg::kStageBytes;
         const int key0 = (first_tile + tile[j]) * kTileKeys;
-        const bool tail = key0 + kTileKeys > seq_len;
+        const bool tail = EDGE && key0 + kTileKeys > seq_len;
+        const bool screen = EDGE && kScreen && (key0 < lo_all || key0 + kTileKeys - 1 > screen_hi);
+        auto screened = [&](uint32_t (&a)[4]) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t bad = not_finite_16<BF16>(a[i]);
+            odd |= bad;
+            a[i] &= ~bad;
+          }
+        };
         if constexpr (!BYTE) {
           // this warp's m-tiles: a part of a slab's four, or whole slabs
           const uint32_t va = (sbase + v_off[0] + (MTW >= 4 ? w * (MTW / 4) * Cfg::kSlabBytes : (w * MTW >> 2) * Cfg::kSlabBytes)) ^
@@ -635,6 +670,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::kMinBlocks)
             if (tail) {
               a[0] &= vm01; a[1] &= vm01; a[2] &= vm23; a[3] &= vm23;
             }
+            if (screen) screened(a);
 #pragma unroll
             for (int m = 0; m < 2; ++m)
 #pragma unroll
@@ -669,6 +705,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::kMinBlocks)
             a[1] = byte_pair_to_half2<Cfg::KV>(ab01, true);
             a[2] = byte_pair_to_half2<Cfg::KV>(cd01, false);
             a[3] = byte_pair_to_half2<Cfg::KV>(cd01, true);
+            if (screen) screened(a);
 #pragma unroll
             for (int m = 0; m < 2; ++m)
 #pragma unroll
@@ -677,6 +714,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::kMinBlocks)
             a[1] = byte_pair_to_half2<Cfg::KV>(ab23, true);
             a[2] = byte_pair_to_half2<Cfg::KV>(cd23, false);
             a[3] = byte_pair_to_half2<Cfg::KV>(cd23, true);
+            if (screen) screened(a);
 #pragma unroll
             for (int m = 0; m < 2; ++m)
 #pragma unroll
@@ -687,6 +725,13 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::kMinBlocks)
         // (a stage taken twice is given back after the second time)
         if (lane == 0 && (j == KT - 1 || (have[0] && have[KT - 1]))) mbar_arrive(empty0 + 8 * stage);
       }
+    };
+    for (int st = (kg - static_cast<int>(step0 % KG) + KG) % KG; st * KT < last; st += KG) {
+      const int key0 = (first_tile + st * KT - lead) * kTileKeys;
+      if ((W == 1 || kScreen) && st * KT >= lead && (st + 1) * KT <= last && key0 >= lo_all && key0 + KT * kTileKeys - 1 <= hi_all)
+        step(st, std::false_type());
+      else
+        step(st, std::true_type());
     }
     q += ntiles;
 
@@ -707,6 +752,39 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::kMinBlocks)
     };
     constexpr int kStep = BYTE ? 1 : 8;
     const bool direct = pc.npieces == 1;
+    if constexpr (kScreen) {
+      if (__any_sync(0xffffffffu, odd != 0u)) {
+#pragma unroll 1
+        for (int j = max(0, (p.window > 0 ? hi_all - p.window + 1 : 0)) / kTileKeys * kTileKeys; j < seq_len; ++j) {
+          const int key0 = j / kTileKeys * kTileKeys;
+          if (key0 >= lo_all && key0 + kTileKeys - 1 <= screen_hi) {  // tiles that nothing was taken out of
+            j = max(key0 + kTileKeys, screen_hi / kTileKeys * kTileKeys) - 1;
+            continue;
+          }
+          const int blk = __ldg(p.block_table + static_cast<long long>(pc.b) * p.max_blocks + j / p.block_size);
+          const long long slot = static_cast<long long>(blk >= 0 && blk < p.num_blocks ? blk : 0) * p.block_size + j % p.block_size;
+          const uint8_t* row = static_cast<const uint8_t*>(dp.v_cache) + (slot * p.Hkv + pc.kh + th) * (D * Cfg::kElem);
+#pragma unroll
+          for (int mtl = 0; mtl < MTW; ++mtl) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int d = dim0(mtl) + e * kStep;
+              const bool bad = BYTE ? (row[d] & 0x7fu) == 0x7fu
+                                    : not_finite_16<BF16>(reinterpret_cast<const uint16_t*>(row)[d]) != 0u;
+#pragma unroll
+              for (int n = 0; n < NTM; ++n)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                  const int hi = hi_all + (n * 8 + 2 * t4 + c) / p.G;
+                  const bool mark = bad && j <= hi && (p.window <= 0 || j > hi - p.window);
+                  o[0][mtl][n][2 * e + c] = mark ? NAN : o[0][mtl][n][2 * e + c];
+                  o[1][mtl][n][2 * e + c] = mark ? NAN : o[1][mtl][n][2 * e + c];
+                }
+            }
+          }
+        }
+      }
+    }
 
     if constexpr (!Cfg::kMerge) {
       // straight from the accumulators

@@ -112,9 +112,10 @@ struct DiffTc {
   static constexpr int kFs = 0, kTh = kON, kAl = 2 * kON, kL = 3 * kON;  // threshold, rescale, sum;
   static constexpr int kLo = 4 * kON, kHi = kLo + kRows, kRow = kHi + kRows;  // [NG][8]: visible range,
   static constexpr int kLam = kRow + kRows, kFlag = kLam + kRows;  // output row (of Hq a token), lambda; a flag
+  static constexpr int kOdd = kFlag + NG;  // a NaN code in V of a key that only some rows see
   // Cluster merge: each CTA stages its partial (m, l) here, [map][row], and its
   // partial O rows [map][row][D] at offset 0, over the K ring, idle by then.
-  static constexpr int kOffStage = (kOffRow + (kFlag + NG) * 4 + 15) / 16 * 16;
+  static constexpr int kOffStage = (kOffRow + (kOdd + 1) * 4 + 15) / 16 * 16;
   static constexpr int kOffBars = kOffStage + 2 * kRows * 8;
   // barriers: fullK, emptyK [NBK], fullV, emptyV [NBV], then these (kBarS2: S^T
   // read, CODES; else K widened)
@@ -327,6 +328,7 @@ __device__ __forceinline__ void diff_tc_softmax(const DiffParams& dp, const int*
   // bits), into [2^7, 2^8) for e4m3 terms (exact but where |q| is below 2^-6 of
   // the largest, fp16, 2^-9, bfloat16: there off by 2^-17 of the largest at most).
   auto q_setup = [&](const Piece& pq) {
+    if (tid == 0) ri[T::kOdd] = 0;
     for (int item = tid; item < T::kRows * 8; item += NST) {
       const int r = item >> 3, part = item & 7;
       constexpr int NW = D / 64;  // 8-dim pieces per item
@@ -408,6 +410,7 @@ __device__ __forceinline__ void diff_tc_softmax(const DiffParams& dp, const int*
     q_setup(pc);
     named_bar_sync(T::kBarAll, NST);
     if (tid == 0) mbar_arrive(bar(T::kBarQFull));
+    auto first_key = [&] { return p.window > 0 ? pc.tile_hi_all - p.window + 1 : 0; };  // that a row sees
     float lp[16];  // this key lane's share of each row's weight sum ([map][row])
 #pragma unroll
     for (int r = 0; r < 16; ++r) lp[r] = 0.f;
@@ -451,7 +454,8 @@ __device__ __forceinline__ void diff_tc_softmax(const DiffParams& dp, const int*
       load16(fs_row, th);
 #pragma unroll
       for (int r = 0; r < 16; ++r) x[r] *= th[r];
-      if (nvalid < 128 || key0 < pc.tile_lo_all || key0 + 127 > pc.tile_hi_all) {
+      const bool edge = nvalid < 128 || key0 < pc.tile_lo_all || key0 + 127 > pc.tile_hi_all;
+      if (edge) {
         const int j = key0 + key;
 #pragma unroll
         for (int r = 0; r < 8; ++r)
@@ -531,13 +535,35 @@ __device__ __forceinline__ void diff_tc_softmax(const DiffParams& dp, const int*
         for (int k = 0; k < 4; ++k) split_weight(pw[2 * k], pw[2 * k + 1], tw[k]);
 #pragma unroll
         for (int m = 0; m < 3; ++m) st_shared_v4(pt_at(m * NG + g), tw[0][m], tw[1][m], tw[2][m], tw[3][m]);
-        if (g == 0 && lim < 128) {
+        if (g == 0 && edge) {
           const int st = b % NBV;
+          const uint32_t vblk = sbase + T::kOffV + st * T::kBlkBytes;
           if (ok) ok = mbar_wait(fullv0 + 8 * st, (b / NBV) & 1, p.timeout_ns);
-          if (ok && key >= lim) {
-            const uint32_t vrow = sbase + T::kOffV + st * T::kBlkBytes + key * 128;
+          if (ok && (key >= lim || key0 + key < first_key())) {  // V rows that no query row sees
 #pragma unroll
-            for (int c = 0; c < 8 * S; ++c) st_shared_v4(vrow + (c >> 3) * T::kSlabBlk + 16 * (c & 7), 0u, 0u, 0u, 0u);
+            for (int c = 0; c < 8 * S; ++c)
+              st_shared_v4(vblk + key * 128 + (c >> 3) * T::kSlabBlk + 16 * (c & 7), 0u, 0u, 0u, 0u);
+          }
+          // NaN codes of keys that only some of the rows see (several query tokens) become
+          // zeros, lest they meet the others' zero weights; the piece's end puts them back
+          const int lo0 = max(0, first_key() - key0), lo1 = min(lim, pc.tile_lo_all - key0);
+          const int hi0 = max(max(lo0, lo1), pc.tile_hi_all + 1 - key0);
+          const int nlo = max(0, lo1 - lo0), some = nlo + max(0, lim - hi0);
+          for (int item = key; ok && item < some * 8 * S; item += 128) {
+            const int r = item / (8 * S), c = item % (8 * S);
+            const uint32_t at = vblk + (r < nlo ? lo0 + r : hi0 + r - nlo) * 128 + (c >> 3) * T::kSlabBlk + 16 * (c & 7);
+            const uint4 v = ld_shared_v4(at);
+            uint32_t w[4] = {v.x, v.y, v.z, v.w}, odd = 0;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t nan = (((w[k] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7;
+              w[k] &= ~(nan * 0xffu);
+              odd |= nan;
+            }
+            if (odd) {
+              st_shared_v4(at, w[0], w[1], w[2], w[3]);
+              ri[T::kOdd] = 1;
+            }
           }
         }
       } else {
@@ -553,6 +579,13 @@ __device__ __forceinline__ void diff_tc_softmax(const DiffParams& dp, const int*
     }
     bq += nblk;
 
+    // does the piece hold keys that only some rows see? (the same for all threads; group
+    // 0's note of a NaN among them reaches the others, who wait for its weights anyway)
+    auto some_rows = [&] {
+      return CODES && pc.qlen > 1 && (pc.first_tile * kTileKeys < pc.tile_lo_all ||
+                                      min(pc.L, (pc.first_tile + pc.ntiles) * kTileKeys) - 1 > pc.tile_hi_all);
+    };
+    if (some_rows()) named_bar_sync(T::kBarAll, NST);
     float w[S];  // the norm's weights of this thread's dims, read before the waits
 #pragma unroll
     for (int h = 0; h < S; ++h)
@@ -653,6 +686,41 @@ __device__ __forceinline__ void diff_tc_softmax(const DiffParams& dp, const int*
           reinterpret_cast<float2*>(smem + T::kOffStage)[row] = ml;
         else
           __stcg(reinterpret_cast<float2*>(p.ws_ml) + static_cast<long long>(pc.slot) * p.rows_padded + row, ml);
+      }
+    }
+    if constexpr (CODES) {
+      if (some_rows() && ri[T::kOdd] != 0) {
+        // the outputs of rows that see a NaN are NaN (under a norm the whole row): each
+        // thread writes over what it has written
+        const int key_hi = min(pc.L, (pc.first_tile + pc.ntiles) * kTileKeys);
+        float* part = p.cluster > 1 ? reinterpret_cast<float*>(smem)
+                                    : p.ws_o + static_cast<long long>(pc.slot) * p.rows_padded * D;
+#pragma unroll 1
+        for (int j = max(first_key(), pc.first_tile * kTileKeys); j < key_hi; ++j) {
+          if (j >= pc.tile_lo_all && j <= pc.tile_hi_all) {  // seen by all: in the products
+            j = pc.tile_hi_all;
+            continue;
+          }
+          const int blk = __ldg(p.block_table + static_cast<long long>(pc.b) * p.max_blocks + j / p.block_size);
+          const long long slot = static_cast<long long>(blk >= 0 && blk < p.num_blocks ? blk : 0) * p.block_size + j % p.block_size;
+          const uint8_t* v = static_cast<const uint8_t*>(dp.v_cache) + (slot * p.Hkv + pc.kh) * D;
+          bool any = false;
+#pragma unroll 1
+          for (int d = 0; d < D && dp.norm_weight != nullptr; ++d) any |= (v[d] & 0x7fu) == 0x7fu;
+#pragma unroll 1
+          for (int i = 0; i < 8 * S; ++i) {
+            const int r = i & 7, d = 128 * (i >> 3) + key;
+            const bool nan = (v[d] & 0x7fu) == 0x7fu;
+            if (8 * g + r >= pc.R || j < lo_row[r] || j > hi_row[r]) continue;
+            if (pc.npieces == 1) {
+              if ((nan || any) && (l_row[r] > 0.f || l_row[8 + r] > 0.f))
+                reinterpret_cast<uint16_t*>(p.out)[static_cast<long long>(ri[T::kRow + 8 * g + r]) * D + d] = 0x7fffu;
+            } else if (nan) {
+              part[(8 * g + r) * D + d] = NAN;
+              part[(T::kRows + 8 * g + r) * D + d] = NAN;
+            }
+          }
+        }
       }
     }
     named_bar_sync(T::kBarAll, NST);  // the row state and red[] are rewritten by the next piece

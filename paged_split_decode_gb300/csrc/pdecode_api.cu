@@ -551,6 +551,7 @@ pd_status decode_paged_diff(const void* q, const void* k_cache, const void* v_ca
                                       static_cast<int>(total), scale, window, qlen, num_splits, out, dims, workspace,
                                       workspace_bytes, error_flag, true, pl, tk, tv, p.d, ready);
   if (st != PD_OK || !ready) return st;
+  p.v_cache = v_cache;
   p.lambda = lambda;
   p.norm_weight = norm_weight;
   p.norm_f32 = norm_weight_f32 ? 1 : 0;

@@ -119,6 +119,12 @@ __device__ __forceinline__ void sts_v4(uint32_t a, uint32_t x, uint32_t y, uint3
   asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
 
+// Shared-memory writes of this thread become visible to the async
+// proxy's accesses (tensor cores' reads, copies) that are ordered after the next synchronisation.
+__device__ __forceinline__ void fence_proxy_async_smem() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
 // True in one lane (the same at every call) of a converged warp.
 __device__ __forceinline__ bool elect_one() {
   uint32_t ok;

@@ -25,11 +25,6 @@ __device__ __forceinline__ void tc_fence_before() {
 __device__ __forceinline__ void tc_fence_after() {
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 }
-// Shared-memory writes of this thread become visible to the tensor cores'
-// (async proxy) reads that are ordered after the next synchronisation.
-__device__ __forceinline__ void fence_proxy_async_smem() {
-  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-}
 
 // 32 consecutive fp32 columns of the TMEM lane (32 * (warp % 4) + lane):
 // taddr = TMEM address (lane in bits 31:16, column in 15:0) of the warp's lane 0.
