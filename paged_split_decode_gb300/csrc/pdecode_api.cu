@@ -433,7 +433,9 @@ pd_status prepare_decode(const void* q, const void* k_cache, const void* v_cache
   p.block_size = dims->block_size;
   p.num_blocks = dims->num_blocks;
   p.tiles_per_block = dims->block_size / kTileKeys;
-  p.window = window > 0 ? window : 0;
+  // a window that no sequence can fill is none (and positions less a window stay in 32 bits)
+  const long long cap_keys = static_cast<long long>(dims->max_blocks_per_seq) * dims->block_size;
+  p.window = window > 0 && window < cap_keys ? window : 0;
   p.num_splits = pl.splits;
   p.unit_cost = pl.unit_cost;
   const double ks = fp8 ? static_cast<double>(dims->k_scale) : 1.0;
