@@ -347,8 +347,8 @@ typedef struct {
  *   out_scale    8-bit outputs: fp32 [rows, N / scale_size], s = max(max |y| / Q,
  *                2^-100), Q = 448 (e4m3fn) or 127 (int8), NaN left out of the
  *                maximum
- * Otherwise no output may overlap an input or another output. One launch on
- * `stream`. */
+ * Otherwise no output may overlap an input or another output (PD_ERR_SHAPE). One
+ * launch on `stream`. */
 PD_API pd_status rms_norm(const void* x, const void* residual, const void* weight, float eps,
                           float gain, void* residual_out, void* out, float* out_scale,
                           const pd_norm_dims* dims, void* stream);

@@ -476,6 +476,24 @@ extern "C" pd_status rms_norm(const void* x, const void* residual, const void* w
   if (bad(x, 1) || bad(residual, 1) || bad(residual_out, 1) || bad(weight, d.weight_f32 ? 3 : 1) ||
       bad(out, d.out_kind == PD_NORM_SAME ? 1 : 0) || bad(out_scale, 3))
     return PD_ERR_ALIGN;
+  // outputs over inputs or each other, but for h over x or the residual and y over x or
+  // a residual that h does not replace: those a thread reads before it writes them
+  const int64_t n = d.rows * d.N, code = d.out_kind == PD_NORM_SAME ? 2 : 1;
+  const int64_t scales = d.out_kind == PD_NORM_SAME ? 0 : d.rows * (d.N / d.scale_size) * 4;
+  const int64_t weights = static_cast<int64_t>(d.norm_size) * (d.weight_f32 ? 4 : 2);
+  auto over = [](const void* a, int64_t na, const void* b, int64_t nb) {
+    const uintptr_t p = reinterpret_cast<uintptr_t>(a), q = reinterpret_cast<uintptr_t>(b);
+    return p && q && p < q + static_cast<uintptr_t>(nb) && q < p + static_cast<uintptr_t>(na);
+  };
+  const bool same = d.out_kind == PD_NORM_SAME;
+  if ((residual_out != x && over(residual_out, 2 * n, x, 2 * n)) ||
+      (residual_out != residual && over(residual_out, 2 * n, residual, 2 * n)) ||
+      over(residual_out, 2 * n, weight, weights) || over(residual_out, 2 * n, out, code * n) ||
+      over(residual_out, 2 * n, out_scale, scales) || (!(same && out == x) && over(out, code * n, x, 2 * n)) ||
+      (!(same && out == residual) && over(out, code * n, residual, 2 * n)) || over(out, code * n, weight, weights) ||
+      over(out, code * n, out_scale, scales) || over(out_scale, scales, x, 2 * n) ||
+      over(out_scale, scales, residual, 2 * n) || over(out_scale, scales, weight, weights))
+    return PD_ERR_SHAPE;
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1)

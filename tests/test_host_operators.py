@@ -182,3 +182,15 @@ def test_the_library_is_built_without_the_python_headers(tmp_path, monkeypatch):
         build.build()
     assert not (tmp_path / "_bind.so").exists()
     monkeypatch.setattr(build, "_bind_command", command)
+
+
+def test_rms_norm_refuses_overlaps(lib):
+    """Outputs over inputs or each other; what the header allows is tested where it can run."""
+    m = 1 << 20  # 4 x 256 fp16 values are 2 KiB, as codes 1 KiB; 4 scales 16 bytes
+    kw = dict(x=m, w=2 * m, out=3 * m, out_scale=4 * m)
+    for bad in (dict(res=5 * m, res_out=3 * m), dict(res=5 * m, res_out=3 * m + 2046), dict(res_out=m + 2), dict(out=m + 16),
+                dict(out=2 * m), dict(out=2 * m - 2046), dict(res=5 * m, res_out=5 * m, out=5 * m), dict(res=5 * m, out=5 * m + 64),
+                dict(res=m + 1024, res_out=m), dict(kind=1, out=m), dict(kind=2, res=5 * m, out=5 * m + 2047),
+                dict(kind=1, out_scale=m + 2044), dict(kind=1, out_scale=3 * m + 1020), dict(kind=2, out_scale=2 * m),
+                dict(kind=2, res=5 * m, out_scale=5 * m), dict(kind=1, res_out=4 * m - 2044)):
+        assert _norm(lib, **{**kw, **bad}) == 2, bad
