@@ -328,7 +328,7 @@ __device__ __forceinline__ void diff_tc_softmax(const DiffParams& dp, const int*
   // bits), into [2^7, 2^8) for e4m3 terms (exact but where |q| is below 2^-6 of
   // the largest, fp16, 2^-9, bfloat16: there off by 2^-17 of the largest at most).
   auto q_setup = [&](const Piece& pq) {
-    if (tid == 0) ri[T::kOdd] = 0;
+    if (CODES && tid == 0) ri[T::kOdd] = 0;
     for (int item = tid; item < T::kRows * 8; item += NST) {
       const int r = item >> 3, part = item & 7;
       constexpr int NW = D / 64;  // 8-dim pieces per item
