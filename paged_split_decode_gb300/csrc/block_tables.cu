@@ -385,7 +385,7 @@ pd_status launch_cluster(Kern kernel, int ctas, size_t smem, cudaStream_t s, con
 // several items a thread it loses: 1000 tokens 4.2 -> 6.5). Else CTAs of 1024
 // for the `items` dealt out to the threads: more than one costs a cluster launch
 // and barrier, more than eight a place for 16 CTAs (32768 tokens 7.3 -> 5.9 us,
-// 262144 released blocks 12.2 -> 8.3 against eight).
+// 262144 released blocks 12.2 -> 8.7 against eight; other boxes 6.5 and 9.2).
 bool few_items(int B, long long items) { return B <= 256 && items <= 256; }
 int table_ctas(long long items) { return items <= 1024 ? 1 : items <= 8 * 1024 ? 8 : 16; }
 

@@ -98,7 +98,7 @@ struct DiffShapes {
 
   // byte caches, two or more row tiles per map, where shared memory holds it: the
   // tensor-memory engine (L = 8192, B = 8, qlen = 2 / 3 / 5: e4m3 45.9 / 58.7 / 76.7
-  // here, 33.3 / 35.5 / 44.7 us there, int8 51.4 / 63.4 here, 40.2 / 44.4 there)
+  // here, 33.2 / 35.3 / 44.3 us there, int8 51.4 / 63.4 here, 40.9 / 45.4 there)
   template <class C>
   static constexpr bool kTc = KV == kKvFp8 || (KV == kKvInt8 && (D == 128 || C::NTM < 4));
   template <class C>
