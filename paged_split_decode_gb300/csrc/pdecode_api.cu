@@ -62,10 +62,24 @@ constexpr unsigned long long kTimeoutNs = 2000000000ull;  // 2 s per pipeline wa
 // which no other call's may come between: this lock, one of a few picked by the
 // workspace's address, is held around both. A thread that waits on a full launch
 // queue holds it, but no call on another workspace needs it to make room.
-std::mutex& workspace_lock(const void* workspace) {
+std::mutex& workspace_mutex(const void* workspace) {
   static std::mutex locks[61];
   return locks[(reinterpret_cast<uintptr_t>(workspace) >> 8) % 61];
 }
+class WorkspaceLock {  // (std::unique_lock's out-of-line members would be exported)
+ public:
+  WorkspaceLock(const void* workspace, bool needed) : m_(needed ? &workspace_mutex(workspace) : nullptr) {
+    if (m_) m_->lock();
+  }
+  ~WorkspaceLock() {
+    if (m_) m_->unlock();
+  }
+  WorkspaceLock(const WorkspaceLock&) = delete;
+  WorkspaceLock& operator=(const WorkspaceLock&) = delete;
+
+ private:
+  std::mutex* m_;
+};
 
 std::atomic<unsigned long long> g_wait_limit_ns{kTimeoutNs};
 std::atomic<int> g_inject{0};
@@ -463,8 +477,7 @@ pd_status decode_impl(const void* q, const void* k_cache, const void* v_cache,
                                       num_splits, out, dims, workspace, workspace_bytes, error_flag, false, pl, tk, tv,
                                       p, ready);
   if (st != PD_OK || !ready) return st;
-  std::unique_lock<std::mutex> lock;
-  if (pl.n_merge > 0) lock = std::unique_lock<std::mutex>(workspace_lock(workspace));
+  const WorkspaceLock lock(workspace, pl.n_merge > 0);
   cudaError_t e = launch_decode(dims->D, dims->kv_dtype, pl.nt, pl.hg > 1 ? 1 : 0, tk, tv, p, pl.grid,
                                 static_cast<cudaStream_t>(stream));
   if (e == cudaSuccess && pl.n_merge > 0) {
@@ -560,8 +573,7 @@ pd_status decode_paged_diff(const void* q, const void* k_cache, const void* v_ca
   p.norm_eps = norm_eps;
   p.norm_gain = norm_gain;
   auto s = static_cast<cudaStream_t>(stream);
-  std::unique_lock<std::mutex> lock;
-  if (pl.n_merge > 0) lock = std::unique_lock<std::mutex>(workspace_lock(workspace));
+  const WorkspaceLock lock(workspace, pl.n_merge > 0);
   cudaError_t e = launch_diff(dims->D, dims->kv_dtype, pl.nt, pl.hg > 1 ? 1 : 0, tk, tv, p, pl.grid, s);
   if (e == cudaSuccess && pl.n_merge > 0) {
     // rows of a unit's head spread over CTAs while the grid stays within one
