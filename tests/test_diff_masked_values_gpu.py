@@ -51,7 +51,7 @@ def check(pd, w, planted, S, norm):
 CASES = [("f16", 24, 4, 256, 3), ("f16", 8, 4, 128, 2), ("bf16", 12, 2, 128, 2), ("bf16", 6, 3, 256, 5),
          ("f16", 8, 2, 256, 8), ("bf16", 8, 1, 256, 4), ("fp8", 24, 4, 256, 3), ("fp8_bf16q", 12, 2, 128, 4),
          ("fp8", 8, 4, 128, 2), ("fp8", 4, 2, 256, 3), ("fp8", 8, 1, 128, 4), ("fp8", 12, 2, 256, 2), ("f16", 6, 2, 128, 1),
-         ("fp8", 24, 4, 256, 1)]
+         ("fp8", 24, 4, 256, 1), ("fp8", 16, 1, 256, 1), ("bf16", 24, 2, 128, 1), ("fp8", 32, 2, 128, 2)]
 
 
 @pytest.mark.parametrize("norm", (False, True))
