@@ -78,7 +78,13 @@ typedef enum {
   PD_KV_FP8_E4M3_BF16 = 4, /* e4m3fn caches as PD_KV_FP8_E4M3, q and out (and the writer's new
                               tokens) in bfloat16: each q row is scaled by a power of two into
                               fp16 exactly and the products run as for an fp16 q */
-  PD_KV_INT8_BF16 = 5  /* int8 caches as PD_KV_INT8, q and out (and new tokens) in bfloat16 */
+  PD_KV_INT8_BF16 = 5, /* int8 caches as PD_KV_INT8, q and out (and new tokens) in bfloat16 */
+  /* 4-bit caches (decode_paged_scored, write_kv_cache_fp4 and evict_kv_cache only): e2m1 codes, two
+     to a byte (the even dim in the low nibble), [num_blocks, Hkv, block_size, D / 2], with an e4m3fn
+     scale for every 16 dims, [num_blocks, Hkv, block_size, D / 16]; value = code * scale * k_scale
+     (v_scale). Heads come before keys here. */
+  PD_KV_FP4 = 6,       /* q and out fp16 */
+  PD_KV_FP4_BF16 = 7   /* q and out bfloat16 */
 } pd_kv_dtype;
 
 /* Bits written into *error_flag by the device. */
@@ -253,6 +259,114 @@ PD_API pd_status decode_paged_diff(const void* q, const void* k_cache, const voi
                                    float norm_eps, float norm_gain, void* out, const pd_dims* dims,
                                    void* workspace, size_t workspace_bytes, uint32_t* error_flag,
                                    void* stream);
+
+/* What a scored decode does beside decode_paged's arithmetic. Zeros and NULLs
+ * leave a part out.
+ *   cap             y = cap * tanh(y / cap) on every scaled score (0: none; else >= 1e-30)
+ *   alibi_slopes    device fp32 [Hq]: slope[h] * |position of the query token - position of
+ *                   the key| is taken off the (capped) score
+ *   prefix_lens     device int32 [B]: the first prefix_lens[b] keys of sequence b are visible
+ *                   to each of its query tokens, whatever the window and whether they come
+ *                   before or after the token (clamped to [0, seq_lens[b]])
+ *   k_block_scale,  4-bit caches: the scales of 16 dims, e4m3fn, 16-byte aligned
+ *   v_block_scale
+ *   lse             device fp32, one for each row of q and head ([T, Hq]): the natural
+ *                   logarithm of the sum of e^score, -inf for a row without a visible key
+ *   key_weights,    device fp32 [num_blocks, Hkv, block_size]: for every key of the call's
+ *   key_weights_out sequences, out = in + the softmax weights that its KV head's query heads
+ *                   and all query tokens give it; the keys of the call's own query tokens (the
+ *                   last qlen of a sequence) start from zero, so that a new key needs no
+ *                   clearing. May be the same buffer; entries of no key of a sequence are left
+ *                   alone. Blocks that two sequences share get the sum of one of them. */
+typedef struct {
+  float cap;
+  const float* alibi_slopes;
+  const int32_t* prefix_lens;
+  const void* k_block_scale;
+  const void* v_block_scale;
+  float* lse;
+  const float* key_weights;
+  float* key_weights_out;
+} pd_score;
+
+/* decode_paged over every cache kind, 4-bit caches among them, with capped and
+ * biased scores, a prefix that is always visible, and what the softmax knows about
+ * its rows and keys:
+ *   y[j] = scale * q . k[j];  y[j] = cap * tanh(y[j] / cap);  y[j] -= slope * |p - j|
+ *   out = softmax(y) V over the visible keys, lse = log(sum_j e^y[j])
+ * Key j < L is visible to the token at position p >= 0 when j <= p and, with a window
+ * W > 0, j > p - W, or when j < prefix_lens[b].
+ * The layouts, the writer (write_kv_cache, write_kv_cache_fp4), block_table, seq_lens,
+ * splits and errors are decode_paged's; query_start_loc, num_query_tokens and qlen as
+ * in decode_paged_diff. workspace: pd_scored_workspace_bytes(dims, qlen, num_splits,
+ * key_weights_out != NULL, 0) bytes.
+ * A row without a visible key is zeros. NaN scores, and NaN and infinities of V, show in the
+ * rows that see the key, as NaN or infinity, and in no other. Softmax weights are computed
+ * in fp32 and enter the product with V as two 16-bit operands, or rounded once to fp16 where a
+ * bfloat16 out over 8- and 4-bit caches hides it; every sum is fp32. Caches of 8-bit codes
+ * with Hq/Hkv*qlen > 8 run slower than in decode_paged. */
+PD_API size_t pd_scored_workspace_bytes(const pd_dims* dims, int qlen, int num_splits, int key_weights, int sm_count);
+PD_API pd_status decode_paged_scored(const void* q, const void* k_cache, const void* v_cache,
+                                     const int32_t* block_table, const int32_t* seq_lens,
+                                     const int32_t* query_start_loc, int num_query_tokens, float scale,
+                                     int window, int qlen, int num_splits, const pd_score* score, void* out,
+                                     const pd_dims* dims, void* workspace, size_t workspace_bytes,
+                                     uint32_t* error_flag, void* stream);
+
+/* write_kv_cache for 4-bit caches: for every 16 dims of a new row,
+ *   s = e4m3fn(max|x| / (6 * k_scale)) to the nearest, ties to even, at most 448
+ *   code = e2m1(x / (s * k_scale)) to the nearest, ties to even, at most 6 in magnitude
+ * with the quotients and s * k_scale rounded to fp32 (V: v_scale). Where s is zero the codes
+ * are zeros, with x's signs; a group with a NaN gets the scale NaN (0x7F) and zero codes.
+ *   k_new, v_new    [num_tokens, Hkv, D], fp16 (PD_KV_FP4) or bfloat16 (PD_KV_FP4_BF16), 16-byte aligned
+ *   slot_mapping    as in write_kv_cache
+ *   k_cache, v_cache, k_block_scale, v_block_scale   as PD_KV_FP4 describes, updated in
+ *                   place (codes 8-byte aligned)
+ *   dims            Hkv, D (a multiple of 16), block_size, num_blocks, kv_dtype, k_scale and v_scale
+ *                   (finite, > 0) are read */
+PD_API pd_status write_kv_cache_fp4(const void* k_new, const void* v_new, const int64_t* slot_mapping,
+                                    int num_tokens, void* k_cache, void* v_cache, void* k_block_scale,
+                                    void* v_block_scale, const pd_dims* dims, uint32_t* error_flag, void* stream);
+
+/* What evict_kv_cache keeps.
+ *   keep      keys that a sequence is left with, for each KV head; >= 1
+ *   trigger   sequences of more than this many keys are cut to keep (>= keep)
+ *   first     the first `first` keys are kept,
+ *   recent    and the last `recent` (first + recent <= keep): the rest of keep are the
+ *             keys with the largest weights, on a tie the lower index */
+typedef struct {
+  int32_t keep, trigger, first, recent;
+} pd_eviction;
+
+/* Cuts long sequences down by the attention weight that their keys have collected
+ * (decode_paged_scored's key_weights): each KV head of a sequence keeps the keys of
+ * pd_eviction and moves their K and V rows (for 4-bit caches the scales too) and weights to the
+ * sequence's first `keep` slots, in their order. A NaN weight counts as less than any number.
+ *   key_weights      fp32 [num_blocks, Hkv, block_size], moved along
+ *   block_table      int32 [B, max_blocks_per_seq]
+ *   seq_lens         int32 [B]; seq_lens_out [B] gets the new lengths (may be seq_lens itself)
+ *   block_table_out, NULL: the kept keys are moved within the sequence's own blocks. Else int32
+ *   max_blocks_out   [B, max_blocks_out]: they are copied to these blocks, none of which may hold
+ *                    keys of the call, and so are all keys of sequences that are not cut;
+ *                    max_blocks_out * block_size must hold the longer of keep and of the
+ *                    table's capacity up to trigger
+ *   free_blocks,     NULL, or (only without a block_table_out) the free list of
+ *   free_count       build_block_tables, to which the blocks that the cut sequences no longer
+ *                    need are appended, sequences in order, table entries in order; the count is
+ *                    updated in place
+ *   workspace        pd_evict_workspace_bytes(dims, evict) bytes
+ * A sequence with a bad length (PD_DEVERR_SEQ_LEN) is left alone (0 in a seq_lens_out
+ * of its own). Rows whose table entry is outside [0, num_blocks) are not moved
+ * (PD_DEVERR_BLOCK_ID); such an entry is appended as -1. Blocks that would make the free
+ * list longer than num_blocks are not appended (PD_DEVERR_FREE_LIST). Blocks must not be shared
+ * between sequences that are cut in place. Two launches on `stream`, three with a free list. */
+PD_API size_t pd_evict_workspace_bytes(const pd_dims* dims, const pd_eviction* evict);
+PD_API pd_status evict_kv_cache(void* k_cache, void* v_cache, void* k_block_scale, void* v_block_scale,
+                                float* key_weights, const int32_t* block_table, const int32_t* seq_lens,
+                                const pd_eviction* evict, const int32_t* block_table_out, int max_blocks_out,
+                                int32_t* seq_lens_out, int32_t* free_blocks, int32_t* free_count,
+                                const pd_dims* dims, void* workspace, size_t workspace_bytes,
+                                uint32_t* error_flag, void* stream);
 
 /* Block tables and slot maps of one serving step, built on the GPU from the
  * requests' lengths, for write_kv_cache and decode_paged_varlen. Sequence b

@@ -7,12 +7,14 @@ seeded synthetic workload generator. Build the library with
 """
 from .binding import (DEVERR_BLOCK_ID, DEVERR_FREE_LIST, DEVERR_QUERY_START, DEVERR_SEQ_LEN,
                       DEVERR_SLOT, DEVERR_TIMEOUT, DecodeError, build_block_tables, decode_paged,
-                      decode_paged_combine, decode_paged_diff, decode_paged_varlen,
-                      diff_workspace_bytes, dims_of, get_workspace, grid_ctas, load, make_dims,
-                      release_blocks, rms_norm, status_str, workspace_bytes, write_kv_cache)
+                      decode_paged_combine, decode_paged_diff, decode_paged_scored, decode_paged_varlen,
+                      diff_workspace_bytes, dims_of, evict_kv_cache, get_workspace, grid_ctas, load,
+                      make_dims, release_blocks, rms_norm, scored_workspace_bytes, status_str,
+                      workspace_bytes, write_kv_cache, write_kv_cache_fp4)
 
 __all__ = ["DEVERR_BLOCK_ID", "DEVERR_FREE_LIST", "DEVERR_QUERY_START", "DEVERR_SEQ_LEN",
            "DEVERR_SLOT", "DEVERR_TIMEOUT", "DecodeError", "build_block_tables", "decode_paged",
-           "decode_paged_combine", "decode_paged_diff", "decode_paged_varlen",
-           "diff_workspace_bytes", "dims_of", "get_workspace", "grid_ctas", "load", "make_dims",
-           "release_blocks", "rms_norm", "status_str", "workspace_bytes", "write_kv_cache"]
+           "decode_paged_combine", "decode_paged_diff", "decode_paged_scored", "decode_paged_varlen",
+           "diff_workspace_bytes", "dims_of", "evict_kv_cache", "get_workspace", "grid_ctas", "load",
+           "make_dims", "release_blocks", "rms_norm", "scored_workspace_bytes", "status_str",
+           "workspace_bytes", "write_kv_cache", "write_kv_cache_fp4"]

@@ -25,6 +25,8 @@ PD_KV_INT8 = 2
 PD_KV_BF16 = 3
 PD_KV_FP8_E4M3_BF16 = 4  # e4m3fn caches under a bfloat16 q and out
 PD_KV_INT8_BF16 = 5      # int8 caches under a bfloat16 q and out
+PD_KV_FP4 = 6            # e2m1 codes with e4m3fn scales of 16 dims (decode_paged_scored)
+PD_KV_FP4_BF16 = 7       # the same under a bfloat16 q and out
 _BF16_IO = (PD_KV_BF16, PD_KV_FP8_E4M3_BF16, PD_KV_INT8_BF16)
 DEVERR_BLOCK_ID = 1
 DEVERR_SEQ_LEN = 2
@@ -35,7 +37,8 @@ DEVERR_FREE_LIST = 32
 
 EXPORTS = ("decode_paged", "decode_paged_varlen", "decode_paged_combine", "decode_paged_static_scratch",
            "write_kv_cache", "decode_paged_diff", "build_block_tables", "release_blocks", "rms_norm",
-           "pd_workspace_bytes", "pd_diff_workspace_bytes", "pd_grid_ctas", "pd_status_str", "pd_set_wait_limit_ns",
+           "decode_paged_scored", "write_kv_cache_fp4", "evict_kv_cache", "pd_scored_workspace_bytes",
+           "pd_evict_workspace_bytes", "pd_workspace_bytes", "pd_diff_workspace_bytes", "pd_grid_ctas", "pd_status_str", "pd_set_wait_limit_ns",
            "pd_set_fault_injection")
 
 
@@ -51,6 +54,17 @@ class PdNormDims(ctypes.Structure):
     _fields_ = [("rows", ctypes.c_int64), ("N", ctypes.c_int32), ("norm_size", ctypes.c_int32),
                 ("scale_size", ctypes.c_int32), ("x_bf16", ctypes.c_int32),
                 ("weight_f32", ctypes.c_int32), ("out_kind", ctypes.c_int32)]
+
+
+class PdScore(ctypes.Structure):
+    _fields_ = [("cap", ctypes.c_float), ("alibi_slopes", ctypes.c_void_p), ("prefix_lens", ctypes.c_void_p),
+                ("k_block_scale", ctypes.c_void_p), ("v_block_scale", ctypes.c_void_p), ("lse", ctypes.c_void_p),
+                ("key_weights", ctypes.c_void_p), ("key_weights_out", ctypes.c_void_p)]
+
+
+class PdEviction(ctypes.Structure):
+    _fields_ = [("keep", ctypes.c_int32), ("trigger", ctypes.c_int32), ("first", ctypes.c_int32),
+                ("recent", ctypes.c_int32)]
 
 
 class DecodeError(RuntimeError):
@@ -100,6 +114,17 @@ def load():
             lib.build_block_tables.argtypes = [P, P, i, P, P, P, P, P, P, P, P, dims_p, P, P]
             lib.release_blocks.argtypes = [P, P, P, P, P, P, P, dims_p, P, P]
             lib.rms_norm.argtypes = [P, P, P, f, f, P, P, P, ctypes.POINTER(PdNormDims), P]
+            lib.decode_paged_scored.argtypes = [P, P, P, P, P, P, i, f, i, i, i, ctypes.POINTER(PdScore), P, dims_p, P,
+                                                ctypes.c_size_t, P, P]
+            lib.pd_scored_workspace_bytes.argtypes = [dims_p, i, i, i, i]
+            lib.pd_scored_workspace_bytes.restype = ctypes.c_size_t
+            lib.write_kv_cache_fp4.argtypes = [P, P, P, i, P, P, P, P, dims_p, P, P]
+            evict_p = ctypes.POINTER(PdEviction)
+            lib.evict_kv_cache.argtypes = [P, P, P, P, P, P, P, evict_p, P, i, P, P, P, dims_p, P, ctypes.c_size_t, P, P]
+            lib.pd_evict_workspace_bytes.argtypes = [dims_p, evict_p]
+            lib.pd_evict_workspace_bytes.restype = ctypes.c_size_t
+            for fn in (lib.decode_paged_scored, lib.write_kv_cache_fp4, lib.evict_kv_cache):
+                fn.restype = i
             for fn in (lib.decode_paged_diff, lib.build_block_tables, lib.release_blocks, lib.rms_norm):
                 fn.restype = i
             lib.pd_set_wait_limit_ns.argtypes = [ctypes.c_ulonglong]
@@ -194,6 +219,13 @@ def diff_workspace_bytes(dims: PdDims, qlen: int, num_splits: int, sm_count: int
     """Workspace of decode_paged_diff (two maps' partials)."""
     return int(load().pd_diff_workspace_bytes(ctypes.byref(dims), int(qlen), int(num_splits),
                                               int(sm_count)))
+
+
+def scored_workspace_bytes(dims: PdDims, qlen: int, num_splits: int, key_weights: bool = False,
+                           sm_count: int = 0) -> int:
+    """Workspace of decode_paged_scored; more with ``key_weights`` (every key's scores)."""
+    return int(load().pd_scored_workspace_bytes(ctypes.byref(dims), int(qlen), int(num_splits), int(key_weights),
+                                                int(sm_count)))
 
 
 _workspaces: dict = {}
@@ -382,13 +414,14 @@ def _fast():
             spec.loader.exec_module(mod)
             mod.init(*(ctypes.cast(fn, ctypes.c_void_p).value for fn in (
                 lib.decode_paged_diff, lib.pd_diff_workspace_bytes, lib.build_block_tables, lib.release_blocks,
-                lib.rms_norm, lib.pd_status_str)), DecodeError, _diff_workspace)
+                lib.rms_norm, lib.pd_status_str, lib.decode_paged_scored, lib.pd_scored_workspace_bytes,
+                lib.write_kv_cache_fp4, lib.evict_kv_cache, lib.pd_evict_workspace_bytes)), DecodeError, _call_workspace)
             _bind = mod
     return _bind
 
 
-def _diff_workspace(need, index, stream):
-    """The workspace of a differential decode that brought none. A captured
+def _call_workspace(need, index, stream):
+    """The workspace of a call of the compiled binding that brought none. A captured
     call keeps one of its own in the graph's pool, as graphs may be replayed at
     the same time; else the (device, stream) one of ``get_workspace``."""
     cur = torch._C._cuda_getCurrentRawStream(index)
@@ -475,3 +508,57 @@ def rms_norm(x, weight, eps=1e-5, *, residual=None, residual_out=None, gain=1.0,
     out_scale)`` for the 8-bit types."""
     return (_bind or _fast()).rms_norm(x, weight, eps, residual, residual_out, gain, norm_size, out_dtype, scale_size,
                                        out, out_scale, stream)
+
+
+def decode_paged_scored(q, k_cache, v_cache, block_table, seq_lens, scale, window=0, qlen=1, num_splits=0, out=None, *,
+                        query_start_loc=None, score_cap=0.0, alibi_slopes=None, prefix_lens=None, k_block_scale=None,
+                        v_block_scale=None, k_scale=1.0, v_scale=1.0, lse=None, key_weights=None, key_weights_out=None,
+                        workspace=None, error_flag=None, stream=None):
+    """Paged decode with capped and biased scores, prefixes, 4-bit caches, and what the softmax knows about its
+    rows and keys; returns ``out`` (q's type, [T, Hq, D]).
+
+    ``y = scale * q . k``, then ``score_cap * tanh(y / score_cap)`` (0: no cap), less ``alibi_slopes[h] * |p - j|``
+    (float32 [Hq]) for the query token at p and the key at j. The first ``prefix_lens[b]`` keys (int32 [B]) are
+    visible to every query token, beside those that causality and ``window`` leave. Caches, tables and splits as in
+    ``decode_paged``; with ``query_start_loc`` (int32 [B+1]) sequence b has its own count of query tokens, at most
+    ``qlen``, as in ``decode_paged_varlen`` (rows outside every range are left as they were; a new ``out`` is zeroed
+    there).
+
+    4-bit caches: uint8 [num_blocks, Hkv, block_size, D/2] of e2m1 codes (the even dim in the low nibble) with
+    ``k_block_scale``/``v_block_scale``, float8_e4m3fn (or uint8) [num_blocks, Hkv, block_size, D/16]; a value is code
+    * block scale * ``k_scale``.
+
+    ``lse`` (float32 [T, Hq]) gets the natural log-sum-exp of each row. ``key_weights`` (float32 [num_blocks, Hkv,
+    block_size]) collects the softmax weight that each key is given, in place unless ``key_weights_out`` is given; the
+    step's own keys, the last of each sequence, start from zero. ``evict_kv_cache`` goes by it.
+    """
+    return (_bind or _fast()).decode_paged_scored(q, k_cache, v_cache, block_table, seq_lens, scale, window, qlen,
+                                                  num_splits, out, query_start_loc, score_cap, alibi_slopes, prefix_lens,
+                                                  k_block_scale, v_block_scale, k_scale, v_scale, lse, key_weights,
+                                                  key_weights_out, workspace, error_flag, stream)
+
+
+def write_kv_cache_fp4(k_new, v_new, slot_mapping, k_cache, v_cache, k_block_scale, v_block_scale, *, k_scale=1.0,
+                       v_scale=1.0, error_flag=None, stream=None):
+    """Store new tokens' K/V rows in 4-bit paged caches, in place.
+
+    k_new/v_new: fp16 or bfloat16 [T, Hkv, D]; slot_mapping: int64 [T] (negative = padding); caches as in
+    ``decode_paged_scored``. Every 16 dims get the scale e4m3(max|x| / (6 k_scale)) and the codes nearest to
+    x / (scale k_scale)."""
+    return (_bind or _fast()).write_kv_cache_fp4(k_new, v_new, slot_mapping, k_cache, v_cache, k_block_scale,
+                                                 v_block_scale, k_scale, v_scale, error_flag, stream)
+
+
+def evict_kv_cache(k_cache, v_cache, key_weights, block_table, seq_lens, keep, *, trigger=None, first=0, recent=0,
+                   block_table_out=None, seq_lens_out=None, k_block_scale=None, v_block_scale=None, free_blocks=None,
+                   free_count=None, workspace=None, error_flag=None, stream=None):
+    """Cut sequences of more than ``trigger`` (default: ``keep``) keys down to ``keep`` for each KV head: the first
+    ``first``, the last ``recent``, and the heaviest of the rest by ``key_weights`` (float32 [num_blocks, Hkv,
+    block_size]; on a tie the lower index). Their K and V rows, block scales and weights move to the sequence's first
+    slots, in order; with ``block_table_out`` (int32 [B, columns]) they are copied to those blocks instead, as are
+    all keys of the other sequences. ``seq_lens`` is updated in place unless ``seq_lens_out`` is given; returns the
+    lengths. ``free_blocks``/``free_count`` (as in ``build_block_tables``): the blocks that sequences cut in place no
+    longer need are pushed."""
+    return (_bind or _fast()).evict_kv_cache(k_cache, v_cache, key_weights, block_table, seq_lens, keep, trigger, first,
+                                             recent, block_table_out, seq_lens_out, k_block_scale, v_block_scale,
+                                             free_blocks, free_count, workspace, error_flag, stream)

@@ -1,6 +1,7 @@
 // bind.cpp -- argument checks and marshalling of the calls that run beside
-// kernels of a few microseconds (decode_paged_diff, build_block_tables,
-// release_blocks, rms_norm), as a CPython extension over libpdecode's C ABI:
+// kernels of a few microseconds (decode_paged_diff, decode_paged_scored,
+// write_kv_cache_fp4, evict_kv_cache, build_block_tables, release_blocks,
+// rms_norm), as a CPython extension over libpdecode's C ABI:
 // tensors become device pointers, the current stream becomes the launch stream,
 // a status other than PD_OK becomes an exception. No computation happens here.
 //
@@ -41,6 +42,11 @@ decltype(&::build_block_tables) f_build;
 decltype(&::release_blocks) f_release;
 decltype(&::rms_norm) f_norm;
 decltype(&::pd_status_str) f_status;
+decltype(&::decode_paged_scored) f_scored;
+decltype(&::pd_scored_workspace_bytes) f_scored_ws;
+decltype(&::write_kv_cache_fp4) f_write4;
+decltype(&::evict_kv_cache) f_evict;
+decltype(&::pd_evict_workspace_bytes) f_evict_ws;
 PyObject* g_error = nullptr;      // DecodeError
 PyObject* g_workspace = nullptr;  // callable(need, device index, stream handle) -> tensor
 
@@ -433,14 +439,263 @@ PyObject* diff(PyObject*, PyObject* const* args, Py_ssize_t n) {
   });
 }
 
+// The caches of a call: their kind, and the sizes that follow from them. 4-bit caches are uint8
+// tensors of codes with block scales beside them, heads before keys.
+struct Caches {
+  const Tensor &k, &v;
+  const Tensor *k_scale, *v_scale;
+  ScalarType type;
+
+  Caches(const Tensor& k_, const Tensor& v_, const Tensor* ks, const Tensor* vs) : k(k_), v(v_), k_scale(ks), v_scale(vs) {
+    type = k.scalar_type();
+    if (k.dim() != 4) value_error("the caches must be [num_blocks, block_size, Hkv, D], 4-bit ones [num_blocks, Hkv, block_size, D/2]");
+    if (v.sizes() != k.sizes() || v.scalar_type() != type) value_error("v_cache must match k_cache in shape and dtype");
+    if ((k_scale != nullptr) != (v_scale != nullptr)) value_error("give both k_block_scale and v_block_scale, or neither");
+    if (!k_scale) return;
+    if (type != at::kByte) type_error("4-bit caches (those with block scales) must be uint8");
+    for (const Tensor* s : {k_scale, v_scale})
+      if (s->dim() != 4 || s->size(0) != k.size(0) || s->size(1) != k.size(1) || s->size(2) != k.size(2) ||
+          s->size(3) * 8 != k.size(3))
+        value_error("block scales must be [num_blocks, Hkv, block_size, D/16]");
+  }
+  bool fp4() const { return k_scale != nullptr; }
+  // q (or new tokens) of type qt
+  int32_t kind(ScalarType qt) const {
+    const bool bf = qt == at::kBFloat16;
+    if (fp4()) return bf ? PD_KV_FP4_BF16 : PD_KV_FP4;
+    if (type == at::kHalf) return PD_KV_F16;
+    if (type == at::kBFloat16) return PD_KV_BF16;
+    if (type == at::kByte || type == at::kFloat8_e4m3fn) return bf ? PD_KV_FP8_E4M3_BF16 : PD_KV_FP8_E4M3;
+    if (type == at::kChar) return bf ? PD_KV_INT8_BF16 : PD_KV_INT8;
+    type_error(std::string("unsupported KV cache dtype ") + c10::toString(type));
+  }
+  void fill(pd_dims& d) const {
+    d.num_blocks = extent(k.size(0), "k_cache");
+    d.Hkv = extent(k.size(fp4() ? 1 : 2), "k_cache");
+    d.block_size = extent(k.size(fp4() ? 2 : 1), "k_cache");
+    d.D = extent(k.size(3) * (fp4() ? 2 : 1), "k_cache");
+  }
+  void check_weights(const Tensor* w, const char* name) const {
+    if (w && (w->dim() != 3 || w->size(0) != k.size(0) || w->size(1) != k.size(fp4() ? 1 : 2) ||
+              w->size(2) != k.size(fp4() ? 2 : 1)))
+      value_error(std::string(name) + " must be [num_blocks, Hkv, block_size]");
+  }
+  void* scale_ptr(const Tensor* s, const char* name, int index) const {
+    return pointer(s, name, index, at::kFloat8_e4m3fn, at::kByte);
+  }
+};
+
+// The workspace that a call brought none of, from binding.py.
+Tensor own_workspace(size_t need, int index, PyObject* stream) {
+  PyObject* o = PyObject_CallFunction(g_workspace, "niO", static_cast<Py_ssize_t>(need), index, stream);
+  if (!o) throw PyFail{};
+  Tensor t;
+  if (THPVariable_Check(o)) t = THPVariable_Unpack(o);
+  Py_DECREF(o);
+  if (!t.defined()) type_error("workspace must be a tensor");
+  return t;
+}
+
+// q, k_cache, v_cache, block_table, seq_lens, scale, window, qlen, num_splits, out, query_start_loc,
+// score_cap, alibi_slopes, prefix_lens, k_block_scale, v_block_scale, k_scale, v_scale, lse, key_weights,
+// key_weights_out, workspace, error_flag, stream
+PyObject* scored(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    Args a(args, n, 24);
+    const Tensor &q = tensor(a[0], "q"), &table = tensor(a[3], "block_table"), &seq = tensor(a[4], "seq_lens");
+    const Caches c(tensor(a[1], "k_cache"), tensor(a[2], "v_cache"), tensor_or_none(a[14], "k_block_scale"),
+                   tensor_or_none(a[15], "v_block_scale"));
+    const Tensor *out = tensor_or_none(a[9], "out"), *start = tensor_or_none(a[10], "query_start_loc"),
+                 *slopes = tensor_or_none(a[12], "alibi_slopes"), *prefix = tensor_or_none(a[13], "prefix_lens"),
+                 *lse = tensor_or_none(a[18], "lse"), *weights = tensor_or_none(a[19], "key_weights"),
+                 *weights_out = tensor_or_none(a[20], "key_weights_out"), *ws = tensor_or_none(a[21], "workspace"),
+                 *flag = tensor_or_none(a[22], "error_flag");
+    pd_dims d{};
+    d.kv_dtype = c.kind(q.scalar_type());
+    const ScalarType io = d.kv_dtype == PD_KV_BF16 || d.kv_dtype == PD_KV_FP8_E4M3_BF16 ||
+                                  d.kv_dtype == PD_KV_INT8_BF16 || d.kv_dtype == PD_KV_FP4_BF16
+                              ? at::kBFloat16
+                              : at::kHalf;
+    c.fill(d);
+    if (q.dim() != 3 || table.dim() != 2) value_error("q must be [T, Hq, D], block_table [B, max_blocks]");
+    const int64_t T = q.size(0), B = table.size(0);
+    const int32_t qlen = integer(a[7], "qlen"), splits = integer(a[8], "num_splits");
+    if (q.size(2) != d.D || seq.numel() != B) value_error("q must be [T, Hq, D] with the caches' D; seq_lens [B]");
+    if (!start && T != B * qlen) value_error("q must be [B*qlen, Hq, D] with B = rows of block_table");
+    if (start && start->numel() != B + 1) value_error("query_start_loc must be [B+1]");
+    if (slopes && slopes->numel() != q.size(1)) value_error("alibi_slopes must be [Hq]");
+    if (prefix && prefix->numel() != B) value_error("prefix_lens must be [B]");
+    if (lse && lse->numel() != T * q.size(1)) value_error("lse must be [T, Hq]");
+    if (out && out->sizes() != q.sizes()) value_error("out must have q's shape");
+    if (weights_out && !weights) value_error("key_weights_out needs key_weights");
+    if (!weights_out) weights_out = weights;
+    c.check_weights(weights, "key_weights");
+    c.check_weights(weights_out, "key_weights_out");
+    d.B = extent(B, "block_table");
+    d.Hq = extent(q.size(1), "q");
+    d.max_blocks_per_seq = extent(table.size(1), "block_table");
+    d.k_scale = static_cast<float>(real(a[16]));
+    d.v_scale = static_cast<float>(real(a[17]));
+    const int32_t total = extent(T, "q");
+    const int index = gpu_of(q, "q");
+    const Launch at_stream(index, a[23]);
+    Tensor made;
+    if (!out) {  // rows outside every sequence's range are zero in a new output
+      made = at_stream.alloc([&] { return start ? at::zeros_like(q) : at::empty_like(q); });
+      out = &made;
+    }
+    Tensor ws_made;
+    if (!ws) {
+      // kept by the shapes that the plan depends on
+      using Key = std::tuple<int, int, int, int, int, int, int, int, int, int, int, bool>;
+      static std::map<Key, size_t> sizes;
+      const Key key{index, d.B, d.Hq, d.Hkv, d.D, d.block_size, d.num_blocks, d.max_blocks_per_seq, d.kv_dtype, qlen,
+                    splits, weights != nullptr};
+      auto it = sizes.find(key);
+      if (it == sizes.end()) {
+        if (sizes.size() >= 4096) sizes.clear();
+        it = sizes.emplace(key, f_scored_ws(&d, qlen, splits, weights != nullptr, 0)).first;
+      }
+      if (it->second > 0) {
+        ws_made = own_workspace(it->second, index, a[23]);
+        ws = &ws_made;
+      }
+    }
+    void *pq = pointer(&q, "q", index, io), *pk = pointer(&c.k, "k_cache", index, c.type),
+         *pv = pointer(&c.v, "v_cache", index, c.type), *po = pointer(out, "out", index, io),
+         *pws = ws ? pointer(ws, "workspace", index, ws->scalar_type()) : nullptr;
+    int32_t *pt = ints(&table, "block_table", index), *ps = ints(&seq, "seq_lens", index),
+            *pstart = ints(start, "query_start_loc", index);
+    pd_score s{};
+    s.cap = static_cast<float>(real(a[11]));
+    s.alibi_slopes = pointer<float>(slopes, "alibi_slopes", index, at::kFloat);
+    s.prefix_lens = ints(prefix, "prefix_lens", index);
+    s.k_block_scale = c.scale_ptr(c.k_scale, "k_block_scale", index);
+    s.v_block_scale = c.scale_ptr(c.v_scale, "v_block_scale", index);
+    s.lse = pointer<float>(lse, "lse", index, at::kFloat);
+    s.key_weights = pointer<float>(weights, "key_weights", index, at::kFloat);
+    s.key_weights_out = pointer<float>(weights_out, "key_weights_out", index, at::kFloat);
+    uint32_t* pflag = flag_of(flag, index);
+    const float scale = static_cast<float>(real(a[5]));
+    const int32_t window = integer(a[6], "window");
+    const size_t ws_bytes = ws ? ws->nbytes() : 0;
+    pd_status st;
+    Py_BEGIN_ALLOW_THREADS;
+    st = f_scored(pq, pk, pv, pt, ps, pstart, total, scale, window, qlen, splits, &s, po, &d, pws, ws_bytes, pflag,
+                  at_stream.stream);
+    Py_END_ALLOW_THREADS;
+    check(st, "decode_paged_scored");
+    return made.defined() ? wrap(made) : same(a[9]);
+  });
+}
+
+// k_new, v_new, slot_mapping, k_cache, v_cache, k_block_scale, v_block_scale, k_scale, v_scale, error_flag, stream
+PyObject* write_fp4(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    Args a(args, n, 11);
+    const Tensor &k = tensor(a[0], "k_new"), &v = tensor(a[1], "v_new"), &slots = tensor(a[2], "slot_mapping");
+    const Caches c(tensor(a[3], "k_cache"), tensor(a[4], "v_cache"), &tensor(a[5], "k_block_scale"),
+                   &tensor(a[6], "v_block_scale"));
+    const Tensor* flag = tensor_or_none(a[9], "error_flag");
+    const ScalarType xt = k.scalar_type();
+    if (xt != at::kHalf && xt != at::kBFloat16)
+      type_error(std::string("k_new has dtype ") + c10::toString(xt) + ", expected Half or BFloat16");
+    pd_dims d{};
+    c.fill(d);
+    d.Hq = d.Hkv;
+    d.kv_dtype = c.kind(xt);
+    if (k.dim() != 3 || k.size(0) != slots.numel() || k.size(1) != d.Hkv || k.size(2) != d.D || v.sizes() != k.sizes())
+      value_error("k_new/v_new must be [T, Hkv, D] with T = len(slot_mapping)");
+    d.k_scale = static_cast<float>(real(a[7]));
+    d.v_scale = static_cast<float>(real(a[8]));
+    const int32_t T = extent(slots.numel(), "slot_mapping");
+    const int index = gpu_of(c.k, "k_cache");
+    const Launch at_stream(index, a[10]);
+    void *pkn = pointer(&k, "k_new", index, xt), *pvn = pointer(&v, "v_new", index, xt),
+         *pk = pointer(&c.k, "k_cache", index, at::kByte), *pv = pointer(&c.v, "v_cache", index, at::kByte),
+         *pks = c.scale_ptr(c.k_scale, "k_block_scale", index), *pvs = c.scale_ptr(c.v_scale, "v_block_scale", index);
+    int64_t* pslot = pointer<int64_t>(&slots, "slot_mapping", index, at::kLong);
+    uint32_t* pflag = flag_of(flag, index);
+    pd_status st;
+    Py_BEGIN_ALLOW_THREADS;
+    st = f_write4(pkn, pvn, pslot, T, pk, pv, pks, pvs, &d, pflag, at_stream.stream);
+    Py_END_ALLOW_THREADS;
+    check(st, "write_kv_cache_fp4");
+    Py_RETURN_NONE;
+  });
+}
+
+// k_cache, v_cache, key_weights, block_table, seq_lens, keep, trigger, first, recent, block_table_out, seq_lens_out,
+// k_block_scale, v_block_scale, free_blocks, free_count, workspace, error_flag, stream
+PyObject* evict(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    Args a(args, n, 18);
+    const Caches c(tensor(a[0], "k_cache"), tensor(a[1], "v_cache"), tensor_or_none(a[11], "k_block_scale"),
+                   tensor_or_none(a[12], "v_block_scale"));
+    const Tensor &weights = tensor(a[2], "key_weights"), &table = tensor(a[3], "block_table"),
+                 &seq = tensor(a[4], "seq_lens");
+    const Tensor *table_out = tensor_or_none(a[9], "block_table_out"), *seq_out = tensor_or_none(a[10], "seq_lens_out"),
+                 *free_blocks = tensor_or_none(a[13], "free_blocks"), *count = tensor_or_none(a[14], "free_count"),
+                 *ws = tensor_or_none(a[15], "workspace"), *flag = tensor_or_none(a[16], "error_flag");
+    pd_dims d{};
+    c.fill(d);
+    d.Hq = d.Hkv;
+    d.kv_dtype = c.kind(at::kHalf);
+    c.check_weights(&weights, "key_weights");
+    if (table.dim() != 2) value_error("block_table must be [B, max_blocks]");
+    if (table_out && (table_out->dim() != 2 || table_out->size(0) != table.size(0)))
+      value_error("block_table_out must be [B, max_blocks_out]");
+    if (seq.numel() != table.size(0)) value_error("seq_lens must be [B]");
+    if (seq_out && seq_out->numel() != table.size(0)) value_error("seq_lens_out must be [B]");
+    if (free_blocks && free_blocks->numel() != d.num_blocks) value_error("free_blocks must be [num_blocks]");
+    if (count && count->numel() != 1) value_error("free_count must be [1]");
+    if (!seq_out) seq_out = &seq;
+    d.B = extent(table.size(0), "block_table");
+    d.max_blocks_per_seq = extent(table.size(1), "block_table");
+    pd_eviction e{};
+    e.keep = integer(a[5], "keep");
+    e.trigger = a[6] == Py_None ? e.keep : integer(a[6], "trigger");
+    e.first = integer(a[7], "first");
+    e.recent = integer(a[8], "recent");
+    const int index = gpu_of(c.k, "k_cache");
+    const Launch at_stream(index, a[17]);
+    Tensor ws_made;
+    if (!ws) {
+      const size_t need = f_evict_ws(&d, &e);
+      if (need > 0) {
+        ws_made = own_workspace(need, index, a[17]);
+        ws = &ws_made;
+      }
+    }
+    void *pk = pointer(&c.k, "k_cache", index, c.type), *pv = pointer(&c.v, "v_cache", index, c.type),
+         *pks = c.scale_ptr(c.k_scale, "k_block_scale", index), *pvs = c.scale_ptr(c.v_scale, "v_block_scale", index),
+         *pws = ws ? pointer(ws, "workspace", index, ws->scalar_type()) : nullptr;
+    float* pw = pointer<float>(&weights, "key_weights", index, at::kFloat);
+    int32_t *pt = ints(&table, "block_table", index), *pto = ints(table_out, "block_table_out", index),
+            *ps = ints(&seq, "seq_lens", index), *pso = ints(seq_out, "seq_lens_out", index),
+            *pf = ints(free_blocks, "free_blocks", index), *pn = ints(count, "free_count", index);
+    uint32_t* pflag = flag_of(flag, index);
+    const int32_t cols = table_out ? extent(table_out->size(1), "block_table_out") : 0;
+    const size_t ws_bytes = ws ? ws->nbytes() : 0;
+    pd_status st;
+    Py_BEGIN_ALLOW_THREADS;
+    st = f_evict(pk, pv, pks, pvs, pw, pt, ps, &e, pto, cols, pso, pf, pn, &d, pws, ws_bytes, pflag, at_stream.stream);
+    Py_END_ALLOW_THREADS;
+    check(st, "evict_kv_cache");
+    return same(a[10] == Py_None ? a[4] : a[10]);
+  });
+}
+
 // init(addresses of decode_paged_diff, pd_diff_workspace_bytes,
-// build_block_tables, release_blocks, rms_norm, pd_status_str; the error class;
-// the workspace callable)
+// build_block_tables, release_blocks, rms_norm, pd_status_str, decode_paged_scored,
+// pd_scored_workspace_bytes, write_kv_cache_fp4, evict_kv_cache, pd_evict_workspace_bytes;
+// the error class; the workspace callable)
 PyObject* init(PyObject*, PyObject* const* args, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
-    Args a(args, n, 8);
-    void* p[6];
-    for (int i = 0; i < 6; ++i) {
+    constexpr int kEntries = 11;
+    Args a(args, n, kEntries + 2);
+    void* p[kEntries];
+    for (int i = 0; i < kEntries; ++i) {
       p[i] = PyLong_AsVoidPtr(a[i]);
       if (!p[i]) {
         if (!PyErr_Occurred()) value_error("a null entry point");
@@ -453,8 +708,13 @@ PyObject* init(PyObject*, PyObject* const* args, Py_ssize_t n) {
     f_release = reinterpret_cast<decltype(f_release)>(p[3]);
     f_norm = reinterpret_cast<decltype(f_norm)>(p[4]);
     f_status = reinterpret_cast<decltype(f_status)>(p[5]);
-    Py_XSETREF(g_error, Py_NewRef(a[6]));
-    Py_XSETREF(g_workspace, Py_NewRef(a[7]));
+    f_scored = reinterpret_cast<decltype(f_scored)>(p[6]);
+    f_scored_ws = reinterpret_cast<decltype(f_scored_ws)>(p[7]);
+    f_write4 = reinterpret_cast<decltype(f_write4)>(p[8]);
+    f_evict = reinterpret_cast<decltype(f_evict)>(p[9]);
+    f_evict_ws = reinterpret_cast<decltype(f_evict_ws)>(p[10]);
+    Py_XSETREF(g_error, Py_NewRef(a[kEntries]));
+    Py_XSETREF(g_workspace, Py_NewRef(a[kEntries + 1]));
     Py_RETURN_NONE;
   });
 }
@@ -465,6 +725,9 @@ PyMethodDef methods[] = {
     {"build_block_tables", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(build_tables)), METH_FASTCALL, nullptr},
     {"release_blocks", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(release)), METH_FASTCALL, nullptr},
     {"rms_norm", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(norm)), METH_FASTCALL, nullptr},
+    {"decode_paged_scored", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(scored)), METH_FASTCALL, nullptr},
+    {"write_kv_cache_fp4", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(write_fp4)), METH_FASTCALL, nullptr},
+    {"evict_kv_cache", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(evict)), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_bind", "Argument marshalling over libpdecode.", -1, methods,
                       nullptr, nullptr, nullptr, nullptr};

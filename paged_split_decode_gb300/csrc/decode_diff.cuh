@@ -164,13 +164,6 @@ __device__ __forceinline__ void store_row4(const DiffParams& p, uint16_t* dst, i
 // operand, and a piece that had one marks the outputs of the rows that see it at its
 // end.
 
-// The elements that are NaN or infinite of two 16-bit ones, as a mask.
-template <bool BF16>
-__device__ __forceinline__ uint32_t not_finite_16(uint32_t w) {
-  constexpr uint32_t kExp = BF16 ? 0x7f807f80u : 0x7c007c00u, kUlp = BF16 ? 0x00800080u : 0x04000400u;
-  return ((((w & kExp) + kUlp) & 0x80008000u) >> 15) * 0xffffu;
-}
-
 template <class Cfg>
 __global__ void __launch_bounds__(Cfg::kThreads, Cfg::kMinBlocks)
     decode_diff_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,

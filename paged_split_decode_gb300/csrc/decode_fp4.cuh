@@ -1,0 +1,580 @@
+// decode_fp4.cuh -- paged split-K decode over 4-bit caches for sm_103a.
+//
+// The decode of decode_kernel.cuh (its units, balanced and fixed splits, partials
+// and combine; the scored decode's caps, biases and prefixes) over caches of e2m1
+// codes, two to a byte, with an e4m3 scale for every 16 values of a row and an fp32
+// scale for each cache: codes [num_blocks, Hkv, block_size, D / 2], scales
+// [num_blocks, Hkv, block_size, D / 16]. Heads before keys, so that a head's 16 keys
+// are one run of 8 D bytes of codes and one of D bytes of scales: at 4 bits a single
+// row is 64 or 128 bytes.
+//
+// 9/16 byte a value is so little that the tensor products' operands, not HBM, are
+// what the consumers wait for: a tile of 16 keys of one head (D = 256) takes 128
+// conversions e2m1 -> fp16, as many multiplications by the scales, and 32 to 48
+// mma.sync for 4.6 KB. So no warp does anything else, and none waits for another:
+//  * A unit is (sequence, KV head). Its tiles go to the CTA's warps in turn; every
+//    warp translates pages, copies, computes and keeps (m, l, O) on its own, and the
+//    warps meet only at the end of a piece. No producer warp, no barriers in the loop.
+//  * A lane copies (cp.async) the 16-byte pieces of codes that it will itself
+//    multiply, into a ring of its warp's own: [piece][lane], no bank conflicts. Only
+//    the scales, 16 bytes a key, are read across lanes.
+//  * S^T = K Q^T: row g of the A operand is key g, and since the order of the
+//    contraction is free a byte of codes converts straight to an operand register
+//    (two adjacent dims of a key); q is read in the same order.
+//  * O^T = V^T P^T: an operand register is two keys of one dim. The nibbles of two
+//    keys' words are exchanged first (four logical operations for 16 values), so that
+//    a byte again converts to a register; rows g and g + 8 of an m-tile are two
+//    adjacent dims.
+//  * A code times its scale has at most six significant bits: exact in fp16, as
+//    operands for K and V alike. The caches' fp32 scales go into the score factor and
+//    the output.
+//  * The softmax reference is raised only when a score passes it by 2^8, so that the
+//    common step has no shuffles and no rescaling.
+#pragma once
+#include "decode_kernel.cuh"
+
+namespace pd {
+
+struct Fp4Params : ScoredParams {
+  const uint8_t *k_codes, *v_codes, *k_sf, *v_sf;
+  int q_bf16;  // q and out are bfloat16: q rows are scaled into fp16 (exactly)
+};
+
+// NT: row tiles of 8 query rows that a warp computes, RG: row groups of that many
+// (warps that read the same tiles), KG: key groups, ST: steps in a warp's ring, KT:
+// tiles a step.
+template <int D_, int NT_, int RG_, int KG_, int KT_, int ST_, int MINB_, bool QB_>
+struct Fp4Cfg {
+  static constexpr int D = D_, NT = NT_, RG = RG_, KG = KG_, KT = KT_, ST = ST_, kMinBlocks = MINB_;
+  static constexpr bool QB = QB_;
+  // P as two operands unless a bfloat16 output's own rounding hides one (see decode_kernel.cuh)
+  static constexpr int PP = QB ? 1 : 2;
+  static constexpr int kWarps = KG * RG, kThreads = kWarps * 32;
+  static constexpr int kCodes = kTileKeys * D / 2, kScales = kTileKeys * D / 16;
+  static constexpr int kTile = 2 * kCodes + 2 * kScales;  // K codes, V codes, K scales, V scales
+  static constexpr int kStage = KT * kTile;
+  static constexpr int kRing = ST * kStage;               // a warp's
+  static constexpr int MT = D / 16;                       // m-tiles (pairs of dims by lane)
+  static constexpr int kPitch = 33;                       // float4 pitch of an m-tile's fragments in the merge
+  static constexpr int kMerge = NT * MT * kPitch * 16;    // a warp's (m, l, O) fragments, over its ring
+  static_assert(kMerge <= kRing, "the merge buffer lies over the ring");
+  static constexpr int RP = RG * NT * 8;
+  static constexpr int kOffQ = kWarps * kRing;            // q fragments [row group][row tile][k-step][lane] uint2
+  static constexpr bool kQSmem = NT > 1;
+  static constexpr int kQ = kQSmem ? RG * NT * MT * 32 * 8 : 0;
+  static constexpr int kOffML = kOffQ + kQ;               // [warp][NT * 8] (m, l)
+  static constexpr int kOffPre = kOffML + kWarps * NT * 8 * 8;
+  static constexpr int kSmemBytes = kOffPre + (kMaxAutoB + 1) * 4 + 12;
+};
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// The four bytes of a word of e2m1 codes as four fp16 pairs (low nibble -> low half), exact.
+__device__ __forceinline__ void e2m1x8_to_half2(uint32_t w, uint32_t (&h)[4]) {
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "mov.b32 {a, b, c, d}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(w));
+}
+__device__ __forceinline__ uint32_t hmul2_u(uint32_t a, uint32_t b) {
+  const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint16_t lds_u16(uint32_t a) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a) : "memory");
+  return v;
+}
+
+template <class Cfg>
+__global__ void __launch_bounds__(Cfg::kThreads, Cfg::kMinBlocks) decode_fp4_kernel(const Fp4Params p) {
+  constexpr int D = Cfg::D, NT = Cfg::NT, RG = Cfg::RG, KG = Cfg::KG, KT = Cfg::KT, ST = Cfg::ST, MT = Cfg::MT;
+  constexpr int PP = Cfg::PP;
+  extern __shared__ __align__(16) uint8_t smem[];
+  float2* s_ml = reinterpret_cast<float2*>(smem + Cfg::kOffML);
+  int* s_pre = reinterpret_cast<int*>(smem + Cfg::kOffPre);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rg = warp % RG, kg = warp / RG;
+  const int g = lane >> 2, t4 = lane & 3;
+
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (p.num_splits == 0 && warp == 0) balanced_prefix(p, s_pre, lane);
+  __syncthreads();
+  WorkIter it;
+  work_init(p, s_pre, it);
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  Piece pc;
+
+  const uint32_t ring = smem_u32(smem) + warp * Cfg::kRing;
+  // this lane's pieces of a tile: K bytes (key g, chunk t4) and what follows it, V bytes
+  // of the keys that its operand registers hold
+  const uint32_t k_src = D == 256 ? g * 128 + t4 * 16 : g * 64 + t4 * 16;
+  uint2* s_q = reinterpret_cast<uint2*>(smem + Cfg::kOffQ);
+
+  while (work_next(p, s_pre, it, pc)) {
+    const int kh = pc.kh;
+    // ---- copies of the warp's steps: step i is tiles (i KG + kg) KT ..
+    const int steps = (pc.ntiles - kg * KT + KG * KT - 1) / (KG * KT);  // (<= 0: none)
+    const int32_t* row = p.block_table + static_cast<long long>(pc.b) * p.max_blocks;
+    auto load_blocks = [&](int i0, int (&blk)[KT]) {  // lane: the physical blocks of step i0 + lane
+#pragma unroll
+      for (int j = 0; j < KT; ++j) {
+        const int k = ((i0 + lane) * KG + kg) * KT + j;
+        blk[j] = 0;
+        if (k < pc.ntiles) blk[j] = __ldg(row + piece_tile(p, pc, k) / p.tiles_per_block);
+      }
+    };
+    int cur[KT], nxt[KT];
+    load_blocks(0, cur);
+    load_blocks(32, nxt);
+    auto issue = [&](int i) {  // copies of step i (any i: none behind the last)
+      if (i < steps) {
+        if ((i & 31) == 0 && i > 0) {
+#pragma unroll
+          for (int j = 0; j < KT; ++j) cur[j] = nxt[j];
+          load_blocks(i + 32, nxt);
+        }
+        const uint32_t stage = ring + (i % ST) * Cfg::kStage;
+#pragma unroll
+        for (int j = 0; j < KT; ++j) {
+          const int k = (i * KG + kg) * KT + j;
+          int blk = __shfl_sync(0xffffffffu, cur[j], i & 31);
+          if (KT > 1 && k >= pc.ntiles) continue;
+          if (blk < 0 || blk >= p.num_blocks) {
+            if (lane == 0) raise_error(p.error_flag, kErrBlockId);
+            blk = 0;
+          }
+          const long long key = (static_cast<long long>(blk) * p.Hkv + kh) * p.block_size +
+                                (piece_tile(p, pc, k) % p.tiles_per_block) * kTileKeys;
+          const uint8_t* kc = p.k_codes + key * (D / 2);
+          const uint8_t* vc = p.v_codes + key * (D / 2);
+          const uint32_t dst = stage + j * Cfg::kTile;
+          if constexpr (D == 256) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {  // keys g, g + 8; chunks t4, t4 + 4
+              cp_async16(dst + q * 512 + lane * 16, kc + k_src + (q >> 1) * 1024 + (q & 1) * 64);
+              // keys 2 t4, 2 t4 + 1, 2 t4 + 8, 2 t4 + 9; chunk g
+              cp_async16(dst + Cfg::kCodes + q * 512 + lane * 16,
+                         vc + (2 * t4 + (q & 1) + (q >> 1) * 8) * 128 + g * 16);
+            }
+            cp_async16(dst + 2 * Cfg::kCodes + lane * 16,
+                       (lane < 16 ? p.k_sf : p.v_sf) + key * (D / 16) + (lane & 15) * 16);
+          } else {
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {  // keys g, g + 8; chunk t4
+              cp_async16(dst + q * 512 + lane * 16, kc + k_src + q * 512);
+              // V: 16-byte piece c of line l (two keys' rows) lies at c ^ 2 l of its line: the lanes of
+              // a read (keys 2 t4, 8-byte chunks g) meet all banks
+              const int line = q * 4 + (lane >> 3);
+              cp_async16(dst + Cfg::kCodes + line * 128 + (((lane & 7) ^ (2 * line & 7)) << 4),
+                         vc + line * 128 + (lane & 7) * 16);
+            }
+            if (lane < 16)
+              cp_async16(dst + 2 * Cfg::kCodes + lane * 16,
+                         (lane < 8 ? p.k_sf : p.v_sf) + key * (D / 16) + (lane & 7) * 16);
+          }
+        }
+      }
+      cp_async_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < ST - 1; ++i) issue(i);
+
+    // ---- q fragments, in the order that the codes' bytes give the contraction
+    uint32_t qf[Cfg::kQSmem ? 1 : NT][MT][2];
+    float sl2r[NT][2];
+    int lo_r[NT][2], hi_r[NT][2], pre_r[NT][2];
+    float m_r[NT][2], l_r[NT][2], slope_r[NT][2];
+    float o[MT][NT][4];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const int r = (rg * NT + n) * 8 + g;
+      const uint32_t* qrow = nullptr;
+      if (r < pc.R && pc.ntiles > 0) {
+        const int i = r / p.G, hl = r % p.G;
+        qrow = reinterpret_cast<const uint32_t*>(
+            p.q + (static_cast<long long>(pc.q0 + i) * p.Hq + kh * p.G + hl) * D);
+      }
+      uint32_t f[MT][2];
+#pragma unroll
+      for (int ks = 0; ks < MT; ++ks) {
+        // chunk of 32 dims (t4, then t4 + 4), four dims of it a k-step
+        const int d = D == 256 ? (ks >> 3) * 128 + 32 * t4 + (ks & 7) * 4 : 32 * t4 + ks * 4;
+        const uint2 v = qrow ? __ldg(reinterpret_cast<const uint2*>(qrow + d / 2)) : make_uint2(0u, 0u);
+        f[ks][0] = v.x;
+        f[ks][1] = v.y;
+      }
+      sl2r[n][0] = sl2r[n][1] = p.sl2;
+      if constexpr (Cfg::QB) {
+        float m = 0.f;
+#pragma unroll
+        for (int ks = 0; ks < MT; ++ks)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            m = fmaxf(m, fmaxf(fabsf(__uint_as_float(f[ks][h] << 16)), fabsf(__uint_as_float(f[ks][h] & 0xffff0000u))));
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+        const int eq = q_row_exponent(m);
+        sl2r[n][0] = p.sl2 * pow2f(-__shfl_sync(0xffffffffu, eq, 8 * t4));
+        sl2r[n][1] = p.sl2 * pow2f(-__shfl_sync(0xffffffffu, eq, 8 * t4 + 4));
+        const float up = pow2f(eq);
+#pragma unroll
+        for (int ks = 0; ks < MT; ++ks)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            f[ks][h] = pack_half2(__uint_as_float(f[ks][h] << 16) * up, __uint_as_float(f[ks][h] & 0xffff0000u) * up);
+      }
+      if constexpr (Cfg::kQSmem) {  // each key group's warps write the same
+#pragma unroll
+        for (int ks = 0; ks < MT; ++ks)
+          if (kg == 0) s_q[((rg * NT + n) * MT + ks) * 32 + lane] = make_uint2(f[ks][0], f[ks][1]);
+      } else {
+#pragma unroll
+        for (int ks = 0; ks < MT; ++ks) {
+          qf[n][ks][0] = f[ks][0];
+          qf[n][ks][1] = f[ks][1];
+        }
+      }
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int rr = (rg * NT + n) * 8 + 2 * t4 + c;
+        hi_r[n][c] = -1;
+        lo_r[n][c] = pre_r[n][c] = 0;
+        slope_r[n][c] = 0.f;
+        if (rr < pc.R) {
+          const int pos = pc.L - pc.qlen + rr / p.G;
+          hi_r[n][c] = pos;
+          lo_r[n][c] = p.window > 0 ? max(0, pos - p.window + 1) : 0;
+          pre_r[n][c] = pos >= 0 ? pc.prefix : 0;
+          if (p.slopes != nullptr) slope_r[n][c] = __ldg(p.slopes + kh * p.G + rr % p.G) * kLog2e;
+        }
+        m_r[n][c] = -INFINITY;
+        l_r[n][c] = 0.f;
+      }
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) o[mt][n][0] = o[mt][n][1] = o[mt][n][2] = o[mt][n][3] = 0.f;
+    }
+    if constexpr (Cfg::kQSmem) __syncthreads();
+
+    for (int i = 0; i < steps; ++i) {
+      cp_async_wait<ST - 2>();
+      __syncwarp();  // the step's scales are there, and every lane is done with the stage that is filled next
+      issue(i + ST - 1);
+      const uint32_t stage = ring + (i % ST) * Cfg::kStage;
+      // ---- S^T = K Q^T: 16 keys x 8 rows for each tile and row tile
+      float x[KT][NT][4];
+#pragma unroll
+      for (int j = 0; j < KT; ++j) {
+        float sa[NT][4], sb[NT][4];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sa[n][e] = sb[n][e] = 0.f;
+        const uint32_t kt = stage + j * Cfg::kTile;
+        constexpr int NC = D / 128;  // 16-byte chunks of a key that a lane holds
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+          // scales of the two groups of 16 dims of the chunk, for keys g and g + 8
+          const uint32_t sf = kt + 2 * Cfg::kCodes + g * (D / 16) + c * 8 + 2 * t4;
+          const uint32_t s0 = e4m3x2_to_half2(lds_u16(sf)), s8 = e4m3x2_to_half2(lds_u16(sf + D / 2));
+          const uint32_t s00 = prmt(s0, s0, 0x1010u), s01 = prmt(s0, s0, 0x3232u);
+          const uint32_t s80 = prmt(s8, s8, 0x1010u), s81 = prmt(s8, s8, 0x3232u);
+          const uint4 w0 = lds_v4(kt + c * 512 + lane * 16), w8 = lds_v4(kt + (NC + c) * 512 + lane * 16);
+          const uint32_t wa[4] = {w0.x, w0.y, w0.z, w0.w}, wb[4] = {w8.x, w8.y, w8.z, w8.w};
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {  // a word: 8 dims, two k-steps; words 0, 1 are the first group
+            uint32_t ha[4], hb[4];
+            e2m1x8_to_half2(wa[w], ha);
+            e2m1x8_to_half2(wb[w], hb);
+            const uint32_t f0 = w < 2 ? s00 : s01, f8 = w < 2 ? s80 : s81;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t a[4] = {hmul2_u(ha[2 * h], f0), hmul2_u(hb[2 * h], f8), hmul2_u(ha[2 * h + 1], f0),
+                                     hmul2_u(hb[2 * h + 1], f8)};
+              const int ks = c * 8 + 2 * w + h;
+#pragma unroll
+              for (int n = 0; n < NT; ++n) {
+                uint32_t b0, b1;
+                if constexpr (Cfg::kQSmem) {
+                  const uint2 b = s_q[((rg * NT + n) * MT + ks) * 32 + lane];
+                  b0 = b.x;
+                  b1 = b.y;
+                } else {
+                  b0 = qf[n][ks][0];
+                  b1 = qf[n][ks][1];
+                }
+                if (h) mma_16816(sb[n], a, b0, b1);
+                else mma_16816(sa[n], a, b0, b1);
+              }
+            }
+          }
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[j][n][e] = (sa[n][e] + sb[n][e]) * sl2r[n][e & 1];
+      }
+      // ---- caps, biases, masks
+      uint32_t see[KT][NT][2];
+      bool edge[KT];
+      int key0[KT];
+#pragma unroll
+      for (int j = 0; j < KT; ++j) {
+        const int k = (i * KG + kg) * KT + j;
+        const bool there = KT == 1 || k < pc.ntiles;
+        key0[j] = piece_tile(p, pc, k) * kTileKeys;
+        edge[j] = !((key0[j] >= pc.tile_lo_all && key0[j] + kTileKeys - 1 <= pc.tile_hi_all) ||
+                    (key0[j] + kTileKeys <= pc.prefix && pc.tile_hi_all >= 0)) || !there;
+        const int j0 = key0[j] + g;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          if (p.cap_out > 0.f) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[j][n][e] = p.cap_out * tanh_f32(x[j][n][e] * p.cap_u);
+          }
+          if (p.slopes != nullptr) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              x[j][n][e] -= slope_r[n][e & 1] * static_cast<float>(abs(j0 + (e >> 1) * 8 - hi_r[n][e & 1]));
+          }
+          if (!edge[j]) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[j][n][e] = hi_r[n][e & 1] >= 0 ? x[j][n][e] : -INFINITY;
+          } else {
+            bool v[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int jj = j0 + (e >> 1) * 8;
+              v[e] = there && ((jj >= lo_r[n][e & 1] && jj <= hi_r[n][e & 1]) || jj < pre_r[n][e & 1]);
+              x[j][n][e] = v[e] ? x[j][n][e] : -INFINITY;
+            }
+            see[j][n][0] = movmatrix_trans(pack_half2(v[0] ? 1.f : 0.f, v[1] ? 1.f : 0.f));
+            see[j][n][1] = movmatrix_trans(pack_half2(v[2] ? 1.f : 0.f, v[3] ? 1.f : 0.f));
+          }
+          if (p.scores != nullptr && there) {
+            float* dst = p.scores + ((static_cast<long long>(pc.b) * p.Hkv + kh) * p.max_blocks * p.tiles_per_block +
+                                     key0[j] / kTileKeys) * (RG * NT * 128) + (rg * NT + n) * 128;
+            __stcg(reinterpret_cast<float2*>(dst + g * 8 + 2 * t4), make_float2(x[j][n][0], x[j][n][1]));
+            __stcg(reinterpret_cast<float2*>(dst + (g + 8) * 8 + 2 * t4), make_float2(x[j][n][2], x[j][n][3]));
+          }
+        }
+      }
+      // ---- softmax: weights relative to a reference that is at most 2^8 below a score,
+      // times 2^7, so that they stay below fp16's end and its last bit is 2^-31 of the
+      // reference's weight
+      bool up = false;
+#pragma unroll
+      for (int j = 0; j < KT; ++j)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) up |= x[j][n][e] > m_r[n][e & 1] + 8.f;
+      if (__any_sync(0xffffffffu, up)) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            float mx = m_r[n][c];
+#pragma unroll
+            for (int j = 0; j < KT; ++j) mx = fmaxf(mx, fmaxf(x[j][n][c], x[j][n][c + 2]));
+#pragma unroll
+            for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+            const float al = m_r[n][c] == -INFINITY ? 1.f : ex2(m_r[n][c] - mx);  // (O and l are zero before the first)
+            m_r[n][c] = mx;
+            l_r[n][c] *= al;
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+              o[mt][n][c] *= al;
+              o[mt][n][c + 2] *= al;
+            }
+          }
+      }
+      uint32_t pb[KT][NT][2], pl[PP == 2 ? KT : 1][PP == 2 ? NT : 1][2];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const float b0 = m_r[n][0] == -INFINITY ? 0.f : m_r[n][0] - 7.f;
+        const float b1 = m_r[n][1] == -INFINITY ? 0.f : m_r[n][1] - 7.f;
+#pragma unroll
+        for (int j = 0; j < KT; ++j) {
+          const float p0 = ex2(x[j][n][0] - b0), p1 = ex2(x[j][n][1] - b1), p2 = ex2(x[j][n][2] - b0),
+                      p3 = ex2(x[j][n][3] - b1);
+          l_r[n][0] += p0 + p2;
+          l_r[n][1] += p1 + p3;
+          const uint32_t w0 = pack_half2(p0, p1), w1 = pack_half2(p2, p3);
+          pb[j][n][0] = movmatrix_trans(w0);
+          pb[j][n][1] = movmatrix_trans(w1);
+          if constexpr (PP == 2) {
+            const float2 h0 = unpack2<false>(w0), h1 = unpack2<false>(w1);
+            pl[j][n][0] = movmatrix_trans(pack_half2(p0 - h0.x, p1 - h0.y));
+            pl[j][n][1] = movmatrix_trans(pack_half2(p2 - h1.x, p3 - h1.y));
+          }
+        }
+      }
+      // ---- O^T += V^T P^T
+#pragma unroll
+      for (int j = 0; j < KT; ++j) {
+        if (KT > 1 && (i * KG + kg) * KT + j >= pc.ntiles) continue;
+        const uint32_t vt = stage + j * Cfg::kTile + Cfg::kCodes;
+        const uint32_t sf = stage + j * Cfg::kTile + 2 * Cfg::kCodes + Cfg::kScales;
+        constexpr int NG = D / 128;  // groups of 16 dims that a lane holds
+        constexpr int NWD = D / 64;  // words of a key that a lane holds
+        // scales of keys (2 t4, 2 t4 + 1) and (2 t4 + 8, 2 t4 + 9) for groups NG g ..
+        uint32_t f01[NG], f89[NG], w[4][NWD];
+        if constexpr (NG == 2) {
+          const uint32_t at = sf + 2 * t4 * 16 + 2 * g;
+          const uint32_t a = e4m3x2_to_half2(lds_u16(at)), b = e4m3x2_to_half2(lds_u16(at + 16)),
+                         c = e4m3x2_to_half2(lds_u16(at + 128)), d = e4m3x2_to_half2(lds_u16(at + 144));
+          f01[0] = prmt(a, b, 0x5410u); f01[1] = prmt(a, b, 0x7632u);
+          f89[0] = prmt(c, d, 0x5410u); f89[1] = prmt(c, d, 0x7632u);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const uint4 v = lds_v4(vt + q * 512 + lane * 16);
+            w[q][0] = v.x; w[q][1] = v.y; w[q][2] = v.z; w[q][3] = v.w;
+          }
+        } else {
+          // rows of 8 scales: a byte for this lane's group of each key
+          const uint32_t at = sf + 2 * t4 * 8 + (g & ~1);
+          const uint32_t a = lds_u16(at), b = lds_u16(at + 8), c = lds_u16(at + 64), d = lds_u16(at + 72);
+          const uint32_t sel = (g & 1) ? 0x0051u : 0x0040u;
+          f01[0] = e4m3x2_to_half2(static_cast<uint16_t>(prmt(a, b, sel)));
+          f89[0] = e4m3x2_to_half2(static_cast<uint16_t>(prmt(c, d, sel)));
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int key = 2 * t4 + (q & 1) + (q >> 1) * 8, line = key >> 1;
+            const uint2 v = lds_v2(vt + line * 128 + ((((key & 1) * 4 + (g >> 1)) ^ (2 * line & 7)) << 4) + (g & 1) * 8);
+            w[q][0] = v.x; w[q][1] = v.y;
+          }
+        }
+        // Keys at or past the sequence's end may hold any bits: a scale of NaN must not meet a
+        // weight of zero. Nor must one of a key that only some rows see: it is taken out, and a
+        // product of ones marks the outputs of the rows that see it.
+        if (edge[j]) {
+          const int k0 = key0[j] + 2 * t4;
+          const uint32_t in01 = (k0 < pc.L ? 0x0000ffffu : 0u) | (k0 + 1 < pc.L ? 0xffff0000u : 0u);
+          const uint32_t in89 = (k0 + 8 < pc.L ? 0x0000ffffu : 0u) | (k0 + 9 < pc.L ? 0xffff0000u : 0u);
+#pragma unroll
+          for (int gr = 0; gr < NG; ++gr) {
+            f01[gr] &= in01;
+            f89[gr] &= in89;
+            const uint32_t o01 = not_finite_16<false>(f01[gr]), o89 = not_finite_16<false>(f89[gr]);
+            if (__any_sync(0xffffffffu, (o01 | o89) != 0)) {
+              f01[gr] &= ~o01;
+              f89[gr] &= ~o89;
+              const uint32_t a[4] = {o01 & 0x3c003c00u, o01 & 0x3c003c00u, o89 & 0x3c003c00u, o89 & 0x3c003c00u};
+#pragma unroll
+              for (int n = 0; n < NT; ++n) {
+                float mark[4] = {0.f, 0.f, 0.f, 0.f};
+                mma_16816(mark, a, see[j][n][0], see[j][n][1]);
+#pragma unroll
+                for (int mt = 0; mt < 8; ++mt)
+#pragma unroll
+                  for (int e = 0; e < 4; ++e)
+                    if (mark[e] > 0.f) o[gr * 8 + mt][n][e] = __uint_as_float(0x7fffffffu);
+              }
+            }
+          }
+        }
+#pragma unroll
+        for (int q = 0; q < NWD; ++q) {  // a word: 8 dims, four m-tiles
+          constexpr uint32_t M = 0x0f0f0f0fu;
+          const uint32_t e01 = (w[0][q] & M) | ((w[1][q] << 4) & ~M), d01 = ((w[0][q] >> 4) & M) | (w[1][q] & ~M);
+          const uint32_t e89 = (w[2][q] & M) | ((w[3][q] << 4) & ~M), d89 = ((w[2][q] >> 4) & M) | (w[3][q] & ~M);
+          uint32_t he[4], hd[4], je[4], jd[4];
+          e2m1x8_to_half2(e01, he);
+          e2m1x8_to_half2(d01, hd);
+          e2m1x8_to_half2(e89, je);
+          e2m1x8_to_half2(d89, jd);
+          const uint32_t s01 = f01[q / 2], s89 = f89[q / 2];
+#pragma unroll
+          for (int b = 0; b < 4; ++b) {
+            const uint32_t a[4] = {hmul2_u(he[b], s01), hmul2_u(hd[b], s01), hmul2_u(je[b], s89), hmul2_u(jd[b], s89)};
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              mma_16816(o[4 * q + b][n], a, pb[j][n][0], pb[j][n][1]);
+              if constexpr (PP == 2) mma_16816(o[4 * q + b][n], a, pl[j][n][0], pl[j][n][1]);
+            }
+          }
+        }
+      }
+    }
+
+    // ---- the warps' (m, l, O) meet; m becomes what the weights are relative to
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1) l_r[n][c] += __shfl_xor_sync(0xffffffffu, l_r[n][c], off);
+        if (l_r[n][c] != l_r[n][c] && m_r[n][c] == -INFINITY) m_r[n][c] = 0.f;  // nothing but NaN: not an empty row
+        if (g == 0) s_ml[warp * NT * 8 + n * 8 + 2 * t4 + c] = make_float2(m_r[n][c] - 7.f, l_r[n][c]);
+      }
+    cp_async_wait<0>();
+    __syncwarp();  // (every lane is done with the warp's ring)
+    float4* mine = reinterpret_cast<float4*>(smem + warp * Cfg::kRing);
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+        mine[(n * MT + mt) * Cfg::kPitch + lane] = make_float4(o[mt][n][0], o[mt][n][1], o[mt][n][2], o[mt][n][3]);
+    __syncthreads();
+    // item: two dims of two rows (an accumulator fragment) of a row tile
+    const bool direct = pc.npieces == 1;
+    for (int item = threadIdx.x; item < RG * NT * MT * 32; item += Cfg::kThreads) {
+      const int mt = item % MT, ln = (item / MT) % 32, tile = item / (MT * 32);
+      const int rw = tile / NT, n = tile % NT, r0 = tile * 8 + 2 * (ln & 3);
+      if (r0 >= pc.R) continue;
+      float M[2] = {-INFINITY, -INFINITY}, L[2] = {0.f, 0.f};
+      float2 ml[KG][2];
+#pragma unroll
+      for (int k = 0; k < KG; ++k)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          ml[k][c] = s_ml[(k * RG + rw) * NT * 8 + n * 8 + 2 * (ln & 3) + c];
+          M[c] = fmaxf(M[c], ml[k][c].x);
+        }
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int k = 0; k < KG; ++k) {
+        const float4 v = reinterpret_cast<const float4*>(smem + (k * RG + rw) * Cfg::kRing)[(n * MT + mt) * Cfg::kPitch + ln];
+        const float f0 = ml[k][0].x == -INFINITY ? 0.f : ex2(ml[k][0].x - M[0]);
+        const float f1 = ml[k][1].x == -INFINITY ? 0.f : ex2(ml[k][1].x - M[1]);
+        L[0] += f0 * ml[k][0].y;
+        L[1] += f1 * ml[k][1].y;
+        acc.x += f0 * v.x; acc.y += f1 * v.y; acc.z += f0 * v.z; acc.w += f1 * v.w;
+      }
+      const int d = D / 8 * (ln >> 2) + 2 * mt;  // dims d, d + 1 of rows r0, r0 + 1
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int r = r0 + c;
+        if (r >= pc.R) break;
+        const float v0 = c ? acc.y : acc.x, v1 = c ? acc.w : acc.z;
+        if (direct) {
+          const int q = r / p.G, head = kh * p.G + r % p.G;
+          const float inv = row_factor(p, L[c]);
+          *reinterpret_cast<uint32_t*>(reinterpret_cast<uint16_t*>(p.out) +
+                                       (static_cast<long long>(pc.q0 + q) * p.Hq + head) * D + d) =
+              Cfg::QB ? pack_bf162(v0 * inv, v1 * inv) : pack_half2(v0 * inv, v1 * inv);
+          if (d == 0) store_row_sum(p, pc.b, pc.q0, q, head, M[c], L[c]);
+        } else {
+          const long long prow = static_cast<long long>(pc.slot) * Cfg::RP + r;
+          __stcg(reinterpret_cast<float2*>(p.ws_o + prow * D + d), make_float2(v0, v1));
+          if (d == 0) __stcg(reinterpret_cast<float2*>(p.ws_ml + prow * 2), make_float2(M[c], L[c]));
+        }
+      }
+    }
+    __syncthreads();  // the rings are free again
+  }
+}
+
+}  // namespace pd

@@ -57,6 +57,7 @@ constexpr unsigned long long kDrainLimitNs = 2000000000ull;
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct DecodeParams {
+  static constexpr bool kScored = false;
   const __half* q;            // [total_q, Hq, D] fp16 (bfloat16 bits for bfloat16 caches)
   __half* out;                // [total_q, Hq, D] same type as q
   const int32_t* block_table; // [B, max_blocks]
@@ -83,6 +84,19 @@ struct DecodeParams {
   int inject;                     // fault injection: 1 = the producer issues no load
   int cluster;                    // > 1: fixed split of this many pieces per unit, one CTA each, launched as
                                   // thread-block clusters that merge a unit's partials in shared memory
+};
+
+// The scored decode's: scores capped and biased, a prefix that every query token
+// sees, the rows' log-sum-exp, and the scores themselves for the keys' weights.
+struct ScoredParams : DecodeParams {
+  static constexpr bool kScored = true;
+  float cap_u;                // ln 2 / cap: a score in log2 units to tanh's argument
+  float cap_out;              // cap * log2(e); 0: no cap
+  const float* slopes;        // [Hq] or null
+  const int32_t* prefix_lens; // [B] or null
+  float* lse;                 // [total_q, Hq] or null
+  float2* row_ml;             // [B, qlen, Hq] (m in log2 units, l) or null: for the keys' weights
+  float* scores;              // [B, Hkv, tiles of a table row, row tiles, 16 keys, 8 rows] in log2 units, or null
 };
 
 // KV element kinds: fp16, one byte per element (OCP e4m3fn or int8 codes), or
@@ -121,6 +135,11 @@ template <bool BF16>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   if constexpr (BF16) return pack_bf162(lo, hi);
   else return pack_half2(lo, hi);
+}
+template <bool BF16>
+__device__ __forceinline__ float2 unpack2(uint32_t w) {
+  if constexpr (BF16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+  else return __half22float2(*reinterpret_cast<const __half2*>(&w));
 }
 template <bool BF16>
 __device__ __forceinline__ uint16_t pack1(float x) {
@@ -241,6 +260,9 @@ struct Piece {
   int qlen;            // query tokens of sequence b (0: nothing to compute or write)
   int R;               // G * qlen rows of the unit
   int q0;              // row of q / out holding the sequence's first query token
+  // scored decode: the first np of the unit's tiles are tiles 0 .. np - 1 of the sequence (a
+  // prefix that does not touch the window), the others follow unit_t0; the prefix's keys
+  int np, prefix;
 };
 
 // Query tokens of sequence b: rows [q0, q0 + qn) of q and out. With
@@ -277,9 +299,24 @@ __device__ __forceinline__ void raise_error(uint32_t* flag, uint32_t bit) {
   if (flag) atomicOr(flag, bit);
 }
 
-// The visible tiles [t0, t0 + n) of a sequence of (validated) length L whose
-// query rows are [q0, q0 + qn).
-__device__ __forceinline__ void span_of(const DecodeParams& p, int L, int qn, int& t0, int& n) {
+// Keys of sequence b's prefix, which every query token sees.
+__device__ __forceinline__ int prefix_of(const DecodeParams&, int, int) { return 0; }
+__device__ __forceinline__ int prefix_of(const ScoredParams& p, int b, int L) {
+  return p.prefix_lens == nullptr ? 0 : max(0, min(__ldg(p.prefix_lens + b), L));
+}
+
+// Tiles of a prefix that lie before the first tile of the window, tile `first`,
+// with a gap between them (0: none, or the two touch).
+__device__ __forceinline__ int prefix_tiles(int prefix, int first) {
+  const int np = (prefix + kTileKeys - 1) / kTileKeys;
+  return np < first ? np : 0;
+}
+
+// The n visible tiles of sequence b, of (validated) length L, whose query rows are
+// [q0, q0 + qn): [t0, t0 + n), the first np of them standing for tiles 0 .. np - 1
+// where a prefix lies apart from the window (prefix_tiles).
+template <class Par>
+__device__ __forceinline__ void span_of(const Par& p, int b, int L, int qn, int& t0, int& n) {
   if (L == 0 || qn == 0) { t0 = 0; n = 0; return; }
   int lo = 0;
   if (p.window > 0) {
@@ -287,12 +324,36 @@ __device__ __forceinline__ void span_of(const DecodeParams& p, int L, int qn, in
     lo = first > 0 ? first : 0;
   }
   t0 = lo / kTileKeys;
+  if constexpr (Par::kScored) {
+    if (t0 > 0) {
+      const int np = (prefix_of(p, b, L) + kTileKeys - 1) / kTileKeys;
+      t0 -= min(np, t0);
+    }
+  }
   n = (L - 1) / kTileKeys - t0 + 1;
+}
+
+// The prefix of the piece's sequence and its tiles apart from the window.
+template <class Par>
+__device__ __forceinline__ void piece_prefix(const Par& p, Piece& pc) {
+  pc.np = pc.prefix = 0;
+  if constexpr (Par::kScored) {
+    pc.prefix = prefix_of(p, pc.b, pc.L);
+    if (p.window > 0) pc.np = prefix_tiles(pc.prefix, max(0, pc.L - pc.qlen - p.window + 1) / kTileKeys);
+  }
+}
+// Tile of the sequence that the piece's tile k is.
+template <class Par>
+__device__ __forceinline__ int piece_tile(const Par&, const Piece& pc, int k) {
+  const int tile = pc.first_tile + k;
+  if constexpr (Par::kScored) return tile - pc.unit_t0 < pc.np ? tile - pc.unit_t0 : tile;
+  else return tile;
 }
 
 // Visible tile span of sequence b: tiles [t0, t0 + n), and its query rows
 // [q0, q0 + qn). Validates seq_len and the query range.
-__device__ __forceinline__ void seq_span(const DecodeParams& p, int b, bool report, int& L, int& t0,
+template <class Par>
+__device__ __forceinline__ void seq_span(const Par& p, int b, bool report, int& L, int& t0,
                                          int& n, int& q0, int& qn) {
   L = p.seq_lens[b];
   const int cap = p.max_blocks * p.block_size;
@@ -301,7 +362,7 @@ __device__ __forceinline__ void seq_span(const DecodeParams& p, int b, bool repo
     L = L < 0 ? 0 : cap;
   }
   seq_queries(p, b, report, q0, qn);
-  span_of(p, L, qn, t0, n);
+  span_of(p, b, L, qn, t0, n);
 }
 
 // Balanced mode keeps, for batches of up to kSeqCacheB sequences, each
@@ -319,7 +380,8 @@ __device__ __forceinline__ void seq_cache_put(const DecodeParams& p, int* s_pre,
     s_pre[kCacheQn + b] = qn;
   }
 }
-__device__ __forceinline__ void seq_span_cached(const DecodeParams& p, const int* s_pre, int b, int& L, int& t0,
+template <class Par>
+__device__ __forceinline__ void seq_span_cached(const Par& p, const int* s_pre, int b, int& L, int& t0,
                                                 int& n, int& q0, int& qn) {
   if (p.B > kSeqCacheB) {
     seq_span(p, b, false, L, t0, n, q0, qn);
@@ -328,7 +390,7 @@ __device__ __forceinline__ void seq_span_cached(const DecodeParams& p, const int
   L = s_pre[kCacheL + b];
   q0 = s_pre[kCacheQ0 + b];
   qn = s_pre[kCacheQn + b];
-  span_of(p, L, qn, t0, n);
+  span_of(p, b, L, qn, t0, n);
 }
 
 // Balanced mode: the visible 16-key tiles of all units, laid end to end (T of
@@ -376,7 +438,8 @@ __device__ __forceinline__ ChunkPlan make_chunk_plan(long long T, int grid) {
 // Balanced mode, warp 0: the prefix over sequences of their units' cost
 // (visible tiles plus the per-unit charge, times the head groups), s_pre[b]
 // for b = 0 .. B, and the per-sequence cache of lengths and query ranges.
-__device__ __forceinline__ void balanced_prefix(const DecodeParams& p, int* s_pre, int lane) {
+template <class Par>
+__device__ __forceinline__ void balanced_prefix(const Par& p, int* s_pre, int lane) {
   int carry = 0;
   if (lane == 0) s_pre[0] = 0;
   for (int base = 0; base < p.B; base += 32) {
@@ -434,7 +497,8 @@ __device__ __forceinline__ void work_init(const DecodeParams& p, const int* s_pr
 }
 
 // Produces the next piece; returns false when the CTA has no more work.
-__device__ __forceinline__ bool work_next(const DecodeParams& p, const int* s_pre, WorkIter& it,
+template <class Par>
+__device__ __forceinline__ bool work_next(const Par& p, const int* s_pre, WorkIter& it,
                                           Piece& pc) {
   const int C = gridDim.x;
   if (p.num_splits == 0) {
@@ -465,6 +529,7 @@ __device__ __forceinline__ bool work_next(const DecodeParams& p, const int* s_pr
       pc.first_slot_cta = cf;
       pc.unit_start = rs;
       common_range(p, L, pc);
+      piece_prefix(p, pc);
       it.g = pe;
       return true;
     }
@@ -515,9 +580,49 @@ __device__ __forceinline__ bool work_next(const DecodeParams& p, const int* s_pr
     pc.chunk = s;
     pc.first_slot_cta = 0; pc.unit_start = 0;
     common_range(p, L, pc);
+    piece_prefix(p, pc);
     return true;
   }
   return false;
+}
+
+// The factor that makes a row's output of its sum of weighted values. (Scored decode: a
+// NaN among the scores shows in the output.)
+template <class Par>
+__device__ __forceinline__ float row_factor(const Par& p, float l) {
+  if constexpr (Par::kScored) return l == 0.f ? 0.f : p.out_scale / l;
+  else return l > 0.f ? p.out_scale / l : 0.f;
+}
+
+// Scored decode: a row's log-sum-exp (natural logarithm), and its (m, l) for the keys' weights.
+__device__ __forceinline__ void store_row_sum(const DecodeParams&, int, int, int, int, float, float) {}
+__device__ __forceinline__ void store_row_sum(const ScoredParams& p, int b, int q0, int i, int head, float m, float l) {
+  if (p.lse != nullptr)
+    p.lse[static_cast<long long>(q0 + i) * p.Hq + head] = l == 0.f ? -INFINITY : m * 0.6931471805599453f + logf(l);
+  if (p.row_ml != nullptr) p.row_ml[(static_cast<long long>(b) * p.qlen + i) * p.Hq + head] = make_float2(m, l);
+}
+
+// tanh(u) to about 2^-22: its Taylor series to u^13 below 1/2 (the next term is 2^-23
+// of the sum there), 1 - 2 / (1 + e^2u) above, where that loses no digits.
+__device__ __forceinline__ float tanh_f32(float u) {
+  const float v = u * u;
+  float s = 21844.f / 6081075.f;
+  s = fmaf(s, v, -1382.f / 155925.f);
+  s = fmaf(s, v, 62.f / 2835.f);
+  s = fmaf(s, v, -17.f / 315.f);
+  s = fmaf(s, v, 2.f / 15.f);
+  s = fmaf(s, v, -1.f / 3.f);
+  s = fmaf(s * v, u, u);
+  const float e = ex2(u * (2.f * kLog2e));
+  const float t = 1.f - __fdividef(2.f, 1.f + e);
+  return v < 0.25f ? s : t;
+}
+
+// The elements that are NaN or infinite of two 16-bit ones, as a mask.
+template <bool BF16>
+__device__ __forceinline__ uint32_t not_finite_16(uint32_t w) {
+  constexpr uint32_t kExp = BF16 ? 0x7f807f80u : 0x7c007c00u, kUlp = BF16 ? 0x00800080u : 0x04000400u;
+  return ((((w & kExp) + kUlp) & 0x80008000u) >> 15) * 0xffffu;
 }
 
 // Cluster merge of a fixed split whose S pieces per unit (p.cluster = S) are
@@ -531,8 +636,8 @@ __device__ __forceinline__ bool work_next(const DecodeParams& p, const int* s_pr
 // writes them as the split combine would: M = max m, w = 2^(m - M),
 // out = sum w O / sum w l. A unit covered by one piece (or none) was written
 // by its piece.
-template <int D, int RP, int RH, int HG, int NTHREADS>
-__device__ __forceinline__ void cluster_merge_ws(const DecodeParams& p) {
+template <int D, int RP, int RH, int HG, int NTHREADS, class Par>
+__device__ __forceinline__ void cluster_merge_ws(const Par& p) {
   constexpr int Q4 = D / 4, SMAX = 16;  // the largest cluster
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
   const int S = p.cluster;
@@ -575,8 +680,9 @@ __device__ __forceinline__ void cluster_merge_ws(const DecodeParams& p) {
         acc.x += w * o[s].x; acc.y += w * o[s].y; acc.z += w * o[s].z; acc.w += w * o[s].w;
       }
     }
-    const float inv = lsum > 0.f ? p.out_scale / lsum : 0.f;
+    const float inv = row_factor(p, lsum);
     const int i = r / p.G, hl = r % p.G;
+    if (Par::kScored && c4 == 0) store_row_sum(p, b, q0, i, (kh + hh) * p.G + hl, M, lsum);
     uint32_t* dst = reinterpret_cast<uint32_t*>(reinterpret_cast<uint16_t*>(p.out) +
                     (static_cast<long long>(q0 + i) * p.Hq + (kh + hh) * p.G + hl) * D + 4 * c4);
     if (p.out_bf16) {
@@ -589,12 +695,13 @@ __device__ __forceinline__ void cluster_merge_ws(const DecodeParams& p) {
   }
 }
 
-template <class Cfg>
+template <class Cfg, class Par = DecodeParams>
 __global__ void __launch_bounds__(Cfg::kThreads, Cfg::kMinBlocks)
     decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
-                        const __grid_constant__ CUtensorMap tm_v, const DecodeParams p) {
+                        const __grid_constant__ CUtensorMap tm_v, const Par p) {
   constexpr int D = Cfg::D, KG = Cfg::KG, NS = Cfg::NS;
   constexpr bool FP8 = Cfg::FP8, BF16 = Cfg::BF16;
+  constexpr bool SC = Par::kScored;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -645,7 +752,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::kMinBlocks)
         // Validated where it is used, so the load stays in flight meanwhile.
         int blk = 0;
         if (t + lane < pc.ntiles) {
-          const int tile = pc.first_tile + t + lane;
+          const int tile = piece_tile(p, pc, t + lane);
           blk = __ldg(row + tile / p.tiles_per_block);
         }
         return blk;
@@ -672,7 +779,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::kMinBlocks)
           // lanes 0..kSlabs-1 load the K slabs, the next kSlabs lanes the V
           // slabs; one box covers 16 keys x HG heads x 128 bytes
           if (lane < 2 * Cfg::kSlabs) {
-            const int tile = pc.first_tile + t + i;
+            const int tile = piece_tile(p, pc, t + i);
             const int z = blk * p.block_size + (tile % p.tiles_per_block) * kTileKeys;
             const int sl = lane % Cfg::kSlabs;
             const bool is_v = lane >= Cfg::kSlabs;
@@ -711,6 +818,13 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::kMinBlocks)
   constexpr int KSTEPS = D / 16;
   constexpr int KSW = KSTEPS / DS;             // k-steps of this warp's part of D
   constexpr int MTW = D / 16 / DS;             // m-tiles (16 output dims) of this warp
+  // Scored: P as the sum of two operands, the rounded value and the rounded rest,
+  // where one rounding would show beside the output's own (error against 64 bits,
+  // relative to the output's norm: fp16 3.2e-4 with one, 2.1e-4 with two, bfloat16
+  // 2.5e-3 and 1.7e-3; a bfloat16 output over fp16 operands hides it).
+  constexpr int PP = SC && !Cfg::kQScale ? 2 : 1;
+  // Weights up to 2^14 where P is fp16, so that its last bit is 2^-38 of the peak's weight.
+  constexpr float kShift = SC && !BF16 ? 14.f : 0.f;
   float* xchg = reinterpret_cast<float*>(smem + Cfg::kOffXchg);
   uint32_t qf[KSW][NTW][2];
   float o[MTW][NTW][4];
@@ -817,6 +931,9 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::kMinBlocks)
       }
     }
     int lo_r[NTW][2], hi_r[NTW][2];
+    int pre_r[SC ? NTW : 1][2];          // scored: the prefix's keys, 0 for a row that sees nothing
+    float slope_r[SC ? NTW : 1][2];      // scored: slope * log2(e)
+    int pos_r[SC ? NTW : 1][2];          // scored: the row's position
     float m_r[NTW][2], l_r[NTW][2];
 #pragma unroll
     for (int n = 0; n < NTW; ++n) {
@@ -827,7 +944,16 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::kMinBlocks)
           const int pos = pc.L - pc.qlen + r / p.G;
           hi_r[n][c] = pos;
           lo_r[n][c] = (p.window > 0) ? max(0, pos - p.window + 1) : 0;
+          if constexpr (SC) {
+            pre_r[n][c] = pos >= 0 ? pc.prefix : 0;
+            pos_r[n][c] = pos;
+            slope_r[n][c] = p.slopes ? __ldg(p.slopes + (pc.kh + th) * p.G + r % p.G) * kLog2e : 0.f;
+          }
         } else {
+          if constexpr (SC) {
+            pre_r[n][c] = pos_r[n][c] = 0;
+            slope_r[n][c] = 0.f;
+          }
           hi_r[n][c] = -1;
           lo_r[n][c] = 0;
         }
@@ -856,7 +982,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::kMinBlocks)
       }
       const uint32_t kb = smem_u32(smem + stage * Cfg::kStageBytes);
       const uint32_t vb = kb + Cfg::kTileBytes;
-      const int key0 = (pc.first_tile + k) * kTileKeys;
+      const int key0 = piece_tile(p, pc, k) * kTileKeys;
 
       // S^T = K Q^T over this warp's part of D (16 keys x 8 rows per row tile)
       float sa[NTW][4], sb[NTW][4];
@@ -946,25 +1072,55 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::kMinBlocks)
       // per row tile: mask, online softmax, P^T fragments; C layout of S^T:
       // [0]=(key g,row 2t4) [1]=(key g,row 2t4+1) [2]=(key g+8,row 2t4) [3]=(key g+8,row 2t4+1)
       uint32_t pb0[NTW], pb1[NTW];
+      uint32_t pl0[PP == 2 ? NTW : 1], pl1[PP == 2 ? NTW : 1];    // the rest of P's rounding
+      uint32_t see0[SC ? NTW : 1], see1[SC ? NTW : 1];            // edge tiles: 1 where the row sees the key
       float al[NTW][2];
       bool rescale = false;
       // a tile every real row sees in full needs no per-key mask
-      const bool interior = key0 >= pc.tile_lo_all && key0 + kTileKeys - 1 <= pc.tile_hi_all;
+      const bool interior = (key0 >= pc.tile_lo_all && key0 + kTileKeys - 1 <= pc.tile_hi_all) ||
+                            (SC && key0 + kTileKeys <= pc.prefix && pc.tile_hi_all >= 0);
 #pragma unroll
       for (int n = 0; n < NTW; ++n) {
         const int j0 = key0 + g, j1 = j0 + 8;
         float x[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = sc[n][e] * sl2r[n][e & 1];
+        if constexpr (SC) {
+          if (p.cap_out > 0.f) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[e] = p.cap_out * tanh_f32(x[e] * p.cap_u);
+          }
+          if (p.slopes != nullptr) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              x[e] -= slope_r[n][e & 1] * static_cast<float>(abs((e < 2 ? j0 : j1) - pos_r[n][e & 1]));
+          }
+        }
         if (interior) {
           // padded rows (hi = -1) stay masked
-          x[0] = hi_r[n][0] >= 0 ? sc[n][0] * sl2r[n][0] : -INFINITY;
-          x[1] = hi_r[n][1] >= 0 ? sc[n][1] * sl2r[n][1] : -INFINITY;
-          x[2] = hi_r[n][0] >= 0 ? sc[n][2] * sl2r[n][0] : -INFINITY;
-          x[3] = hi_r[n][1] >= 0 ? sc[n][3] * sl2r[n][1] : -INFINITY;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[e] = hi_r[n][e & 1] >= 0 ? x[e] : -INFINITY;
         } else {
-          x[0] = (j0 >= lo_r[n][0] && j0 <= hi_r[n][0]) ? sc[n][0] * sl2r[n][0] : -INFINITY;
-          x[1] = (j0 >= lo_r[n][1] && j0 <= hi_r[n][1]) ? sc[n][1] * sl2r[n][1] : -INFINITY;
-          x[2] = (j1 >= lo_r[n][0] && j1 <= hi_r[n][0]) ? sc[n][2] * sl2r[n][0] : -INFINITY;
-          x[3] = (j1 >= lo_r[n][1] && j1 <= hi_r[n][1]) ? sc[n][3] * sl2r[n][1] : -INFINITY;
+          bool see[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int j = e < 2 ? j0 : j1;
+            see[e] = j >= lo_r[n][e & 1] && j <= hi_r[n][e & 1];
+            if constexpr (SC) see[e] = see[e] || j < pre_r[n][e & 1];
+            x[e] = see[e] ? x[e] : -INFINITY;
+          }
+          if constexpr (SC) {
+            see0[n] = movmatrix_trans(pack2<BF16>(see[0] ? 1.f : 0.f, see[1] ? 1.f : 0.f));
+            see1[n] = movmatrix_trans(pack2<BF16>(see[2] ? 1.f : 0.f, see[3] ? 1.f : 0.f));
+          }
+        }
+        if constexpr (SC) {
+          if (p.scores != nullptr && dh == 0) {  // [key][row] of this tile and row tile
+            float* dst = p.scores + ((static_cast<long long>(pc.b) * p.Hkv + pc.kh + th) * p.max_blocks *
+                                         p.tiles_per_block + key0 / kTileKeys) * (Cfg::NT * 128) + (rg * NTW + n) * 128;
+            __stcg(reinterpret_cast<float2*>(dst + g * 8 + 2 * t4), make_float2(x[0], x[1]));
+            __stcg(reinterpret_cast<float2*>(dst + (g + 8) * 8 + 2 * t4), make_float2(x[2], x[3]));
+          }
         }
         float mx0 = fmaxf(x[0], x[2]), mx1 = fmaxf(x[1], x[3]);
 #pragma unroll
@@ -973,11 +1129,11 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::kMinBlocks)
           mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, off));
         }
         const float mn0 = fmaxf(m_r[n][0], mx0), mn1 = fmaxf(m_r[n][1], mx1);
-        const float base0 = (mn0 == -INFINITY) ? 0.f : mn0;
-        const float base1 = (mn1 == -INFINITY) ? 0.f : mn1;
+        const float base0 = (mn0 == -INFINITY) ? 0.f : mn0 - kShift;
+        const float base1 = (mn1 == -INFINITY) ? 0.f : mn1 - kShift;
         // nothing accumulated yet (m = -inf): O and l are zero, keep factor 1
-        al[n][0] = (m_r[n][0] == -INFINITY) ? 1.f : ex2(m_r[n][0] - base0);
-        al[n][1] = (m_r[n][1] == -INFINITY) ? 1.f : ex2(m_r[n][1] - base1);
+        al[n][0] = (m_r[n][0] == -INFINITY) ? 1.f : ex2(m_r[n][0] - kShift - base0);
+        al[n][1] = (m_r[n][1] == -INFINITY) ? 1.f : ex2(m_r[n][1] - kShift - base1);
         const float p00 = ex2(x[0] - base0), p01 = ex2(x[1] - base1);
         const float p10 = ex2(x[2] - base0), p11 = ex2(x[3] - base1);
         m_r[n][0] = mn0;
@@ -985,8 +1141,14 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::kMinBlocks)
         l_r[n][0] = l_r[n][0] * al[n][0] + (p00 + p10);
         l_r[n][1] = l_r[n][1] * al[n][1] + (p01 + p11);
         rescale |= (al[n][0] != 1.f || al[n][1] != 1.f);
-        pb0[n] = movmatrix_trans(pack2<BF16>(p00, p01));
-        pb1[n] = movmatrix_trans(pack2<BF16>(p10, p11));
+        const uint32_t w0 = pack2<BF16>(p00, p01), w1 = pack2<BF16>(p10, p11);
+        pb0[n] = movmatrix_trans(w0);
+        pb1[n] = movmatrix_trans(w1);
+        if constexpr (PP == 2) {
+          const float2 h0 = unpack2<BF16>(w0), h1 = unpack2<BF16>(w1);
+          pl0[n] = movmatrix_trans(pack2<BF16>(p00 - h0.x, p01 - h0.y));
+          pl1[n] = movmatrix_trans(pack2<BF16>(p10 - h1.x, p11 - h1.y));
+        }
       }
       if (__any_sync(0xffffffffu, rescale)) {
 #pragma unroll
@@ -1002,6 +1164,39 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::kMinBlocks)
       // end (the unwritten tail of its last block) may hold any bits, NaN
       // included: their V is zeroed so that P = 0 there never meets 0 * NaN.
       const bool tail = key0 + kTileKeys > pc.L;
+      auto pv = [&](int mtl, uint32_t (&a)[4]) {
+        if constexpr (SC && Cfg::KV != kKvInt8) {
+          // Rows that do not see a key of this tile have a zero weight for it, which
+          // times a NaN or an infinity of its V is NaN: such elements are taken out, and
+          // a product of ones (the element's place, the rows that see the key) marks
+          // the outputs that they belong to.
+          if (!interior) {
+            uint32_t odd[4], any = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) any |= odd[i] = not_finite_16<BF16>(a[i]);
+            if (__any_sync(0xffffffffu, any != 0)) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                a[i] &= ~odd[i];
+                odd[i] &= BF16 ? 0x3f803f80u : 0x3c003c00u;
+              }
+#pragma unroll
+              for (int n = 0; n < NTW; ++n) {
+                float mark[4] = {0.f, 0.f, 0.f, 0.f};
+                mma_op<BF16>(mark, odd, see0[n], see1[n]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  if (mark[e] > 0.f) o[mtl][n][e] = __uint_as_float(0x7fffffffu);
+              }
+            }
+          }
+        }
+#pragma unroll
+        for (int n = 0; n < NTW; ++n) {
+          mma_op<BF16>(o[mtl][n], a, pb0[n], pb1[n]);
+          if constexpr (PP == 2) mma_op<BF16>(o[mtl][n], a, pl0[n], pl1[n]);
+        }
+      };
       if constexpr (!FP8) {
         const int key = (lane & 7) + (lane >> 4) * 8;
         const int srow = key * HG + th;
@@ -1022,8 +1217,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::kMinBlocks)
           if (tail) {
             a[0] &= vm01; a[1] &= vm01; a[2] &= vm23; a[3] &= vm23;
           }
-#pragma unroll
-          for (int n = 0; n < NTW; ++n) mma_op<BF16>(o[mtl][n], a, pb0[n], pb1[n]);
+          pv(mtl, a);
         }
       } else {
         // 32-dim group P32: lane reads 4 codes at dims 32*P32 + 4g .. +3 of keys
@@ -1058,14 +1252,12 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::kMinBlocks)
           a[1] = byte_pair_to_half2<Cfg::KV>(ab01, true);
           a[2] = byte_pair_to_half2<Cfg::KV>(cd01, false);
           a[3] = byte_pair_to_half2<Cfg::KV>(cd01, true);
-#pragma unroll
-          for (int n = 0; n < NTW; ++n) mma_op<BF16>(o[2 * pl][n], a, pb0[n], pb1[n]);
+          pv(2 * pl, a);
           a[0] = byte_pair_to_half2<Cfg::KV>(ab23, false);
           a[1] = byte_pair_to_half2<Cfg::KV>(ab23, true);
           a[2] = byte_pair_to_half2<Cfg::KV>(cd23, false);
           a[3] = byte_pair_to_half2<Cfg::KV>(cd23, true);
-#pragma unroll
-          for (int n = 0; n < NTW; ++n) mma_op<BF16>(o[2 * pl + 1][n], a, pb0[n], pb1[n]);
+          pv(2 * pl + 1, a);
         }
       }
       __syncwarp();
@@ -1081,6 +1273,16 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::kMinBlocks)
         l_r[n][0] += __shfl_xor_sync(0xffffffffu, l_r[n][0], off);
         l_r[n][1] += __shfl_xor_sync(0xffffffffu, l_r[n][1], off);
       }
+    if constexpr (SC) {  // what the weights are relative to
+#pragma unroll
+      for (int n = 0; n < NTW; ++n) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          if (l_r[n][c] != l_r[n][c] && m_r[n][c] == -INFINITY) m_r[n][c] = 0.f;  // nothing but NaN: not an empty row
+          m_r[n][c] -= kShift;
+        }
+      }
+    }
     const int tid = threadIdx.x;
     const bool direct = pc.npieces == 1;
     constexpr int NT = Cfg::NT, RH = NT * 8;  // partial rows per head of a unit
@@ -1170,7 +1372,8 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::kMinBlocks)
         if (direct) {
           const int i = r / p.G, hl = r % p.G;
           __half* dst = p.out + (static_cast<long long>(pc.q0 + i) * p.Hq + (pc.kh + hh) * p.G + hl) * D + dc * 8;
-          const float inv = (Ls > 0.f) ? p.out_scale / Ls : 0.f;
+          const float inv = row_factor(p, Ls);
+          if (SC && dc == 0) store_row_sum(p, pc.b, pc.q0, i, (pc.kh + hh) * p.G + hl, M, Ls);
           uint4 v;
           v.x = pack2<Cfg::QB>(v0.x * inv, v0.y * inv);
           v.y = pack2<Cfg::QB>(v0.z * inv, v0.w * inv);
@@ -1198,7 +1401,9 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::kMinBlocks)
           if (direct) {
             const int i = r / p.G, hl = r % p.G;
             __half* dst = p.out + (static_cast<long long>(pc.q0 + i) * p.Hq + (pc.kh + th) * p.G + hl) * D;
-            const float inv = (Ls > 0.f) ? p.out_scale / Ls : 0.f;
+            const float inv = row_factor(p, Ls);
+            if (SC && g == 0 && dh == 0)
+              store_row_sum(p, pc.b, pc.q0, i, (pc.kh + th) * p.G + hl, m_r[n][c], Ls);
 #pragma unroll
             for (int mtl = 0; mtl < MTW; ++mtl) {
               const int mt = dh * MTW + mtl;
@@ -1244,8 +1449,8 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::kMinBlocks)
 // over the sequences (a block-wide sum of every sequence's unit_cost-charged
 // span before b, and of all of them) and its chunk plan over the decode grid;
 // every thread of the CTA must call it. P <= 1: nothing to merge.
-template <int NW>
-__device__ __forceinline__ void unit_layout(const DecodeParams& p, int u, long long (&s_red)[2][NW], int& P,
+template <int NW, class Par>
+__device__ __forceinline__ void unit_layout(const Par& p, int u, long long (&s_red)[2][NW], int& P,
                                             long long& slot0, long long& slot_base, int& step) {
   const int b = u / p.hgn, grp = u % p.hgn;
   int L, t0, n, q0, qn;
@@ -1360,8 +1565,8 @@ __device__ __forceinline__ void merge_pieces(const DecodeParams& p, int P, long 
 //   and their slots are derived from the sequence lengths (inputs the decode
 //   kernel does not write) before the wait, so that the first global read
 //   after it is already a partial.
-template <int D, int NB, int NT>
-__global__ void __launch_bounds__(NT) split_combine_kernel(const DecodeParams p) {
+template <int D, int NB, int NT, class Par = DecodeParams>
+__global__ void __launch_bounds__(NT) split_combine_kernel(const Par p) {
   __shared__ float s_m[NT], s_l[NT];
   __shared__ float4 s_o[NT];
   __shared__ long long s_red[2][NT / 32];
@@ -1390,9 +1595,10 @@ __global__ void __launch_bounds__(NT) split_combine_kernel(const DecodeParams p)
   const int dims_cta = D / gridDim.y, slices = dims_cta / 4;
   const int items = R * slices;
   const int t = threadIdx.x;
-  auto store = [&](int r, int dim0, float L, float4 o) {
-    const float inv = (L > 0.f) ? p.out_scale / L : 0.f;
+  auto store = [&](int r, int dim0, float m, float L, float4 o) {
+    const float inv = row_factor(p, L);
     const int i = r / p.G, hl = r % p.G;
+    if (Par::kScored && dim0 == 0) store_row_sum(p, b, q0, i, kh * p.G + hl, m, L);
     __half* dst = p.out + (static_cast<long long>(q0 + i) * p.Hq + kh * p.G + hl) * D + dim0;
     uint2 o2;
     if (p.out_bf16) {
@@ -1413,7 +1619,7 @@ __global__ void __launch_bounds__(NT) split_combine_kernel(const DecodeParams p)
       float m_run = -INFINITY, l_run = 0.f;
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
       merge_pieces<D, NB>(p, P, slot0, slot_base, step, rbase, r, dim0, 0, 1, m_run, l_run, acc);
-      store(r, dim0, l_run, acc);
+      store(r, dim0, m_run, l_run, acc);
     }
     return;
   }
@@ -1444,7 +1650,7 @@ __global__ void __launch_bounds__(NT) split_combine_kernel(const DecodeParams p)
     const float4 a = s_o[g2 * items + item];
     o.x += w * a.x; o.y += w * a.y; o.z += w * a.z; o.w += w * a.w;
   }
-  store(r, dim0, L, o);
+  store(r, dim0, M, L, o);
 }
 
 }  // namespace pd

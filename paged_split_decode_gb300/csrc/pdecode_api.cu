@@ -14,6 +14,7 @@
 #include "diff_launch.h"
 #include "launch.h"
 #include "pdecode.h"
+#include "scored_launch.h"
 
 namespace pd {
 
@@ -84,6 +85,9 @@ class WorkspaceLock {  // (std::unique_lock's out-of-line members would be expor
 std::atomic<unsigned long long> g_wait_limit_ns{kTimeoutNs};
 std::atomic<int> g_inject{0};
 
+// Which decode a plan is for: their kernels' shapes differ.
+enum class Op { kPlain, kDiff, kScored };
+
 // Resolved work decomposition of one call.
 struct Plan {
   int splits;       // 0 = balanced, >= 1 fixed
@@ -98,6 +102,7 @@ struct Plan {
   bool whole_tile;  // a TMA box is a tile of all slabs
   int cluster;      // > 1: the fixed split's pieces of a unit form a cluster that merges them
   int sms;          // SMs of the device the plan was made for
+  int head_tiles;   // row tiles of a head in a partial
   size_t off_ml, off_o, bytes;  // workspace layout
 };
 
@@ -107,18 +112,22 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 bool byte_kind(int kv) {
   return kv == PD_KV_FP8_E4M3 || kv == PD_KV_INT8 || kv == PD_KV_FP8_E4M3_BF16 || kv == PD_KV_INT8_BF16;
 }
+bool fp4_kind(int kv) { return kv == PD_KV_FP4 || kv == PD_KV_FP4_BF16; }
 // q and out (and a writer's new tokens) in bfloat16.
-bool bf16_io(int kv) { return kv == PD_KV_BF16 || kv == PD_KV_FP8_E4M3_BF16 || kv == PD_KV_INT8_BF16; }
+bool bf16_io(int kv) {
+  return kv == PD_KV_BF16 || kv == PD_KV_FP8_E4M3_BF16 || kv == PD_KV_INT8_BF16 || kv == PD_KV_FP4_BF16;
+}
 
-pd_status check_dims(const pd_dims* d, int qlen) {
+pd_status check_dims(const pd_dims* d, int qlen, Op op = Op::kPlain) {
   if (!d) return PD_ERR_NULL;
   if (d->B < 0 || d->Hq < 1 || d->Hkv < 1 || d->D < 1 || d->block_size < 1 || d->num_blocks < 0 ||
       d->max_blocks_per_seq < 0 || qlen < 1)
     return PD_ERR_SHAPE;
   if (d->Hq % d->Hkv != 0) return PD_ERR_SHAPE;
-  if (d->kv_dtype != PD_KV_F16 && d->kv_dtype != PD_KV_BF16 && !byte_kind(d->kv_dtype))
+  const bool fp4 = op == Op::kScored && fp4_kind(d->kv_dtype);
+  if (d->kv_dtype != PD_KV_F16 && d->kv_dtype != PD_KV_BF16 && !byte_kind(d->kv_dtype) && !fp4)
     return PD_ERR_DTYPE;
-  if (byte_kind(d->kv_dtype) && (!std::isfinite(d->k_scale) || !std::isfinite(d->v_scale)))
+  if ((byte_kind(d->kv_dtype) || fp4) && (!std::isfinite(d->k_scale) || !std::isfinite(d->v_scale)))
     return PD_ERR_SHAPE;
   if (d->D != 128 && d->D != 256) return PD_ERR_UNSUPPORTED;
   if (d->block_size % kTileKeys != 0) return PD_ERR_UNSUPPORTED;
@@ -159,10 +168,11 @@ int device_sm_count(int sm_count) {
 // within ~2 % or the fixed one loses (B=16: +1.0 us, 2 x 2048 tiles: +0.5). The
 // workspace is sized for the balanced split in either case (the fixed split
 // needs fewer slots), so pd_workspace_bytes does not depend on the window.
-// `diff` plans the differential decode, whose kernels hold two maps' rows.
+// The differential decode's kernels hold two maps' rows.
 pd_status make_plan(const pd_dims* d, int qlen, int num_splits, int sm_count, Plan* pl, int window = 0,
-                    bool diff = false) {
-  pd_status st = check_dims(d, qlen);
+                    Op op = Op::kPlain) {
+  const bool diff = op == Op::kDiff;
+  pd_status st = check_dims(d, qlen, op);
   if (st != PD_OK) return st;
   if (num_splits < 0) return PD_ERR_SHAPE;
   const int sms = device_sm_count(sm_count);
@@ -175,11 +185,12 @@ pd_status make_plan(const pd_dims* d, int qlen, int num_splits, int sm_count, Pl
   // single-row-tile shapes whose head count is a multiple of four (the
   // instantiation chooses how many heads a tile holds: 2 or 4)
   const bool grouped = pl->nt == 1 && d->Hkv % 4 == 0;
-  const auto shape = diff ? diff_kernel_shape : kernel_shape;
+  const auto shape = diff ? diff_kernel_shape : op == Op::kScored ? scored_kernel_shape : kernel_shape;
   if (!(grouped && shape(d->D, d->kv_dtype, pl->nt, 1, &ks)) && !shape(d->D, d->kv_dtype, pl->nt, 0, &ks))
     return PD_ERR_UNSUPPORTED;
   pl->hg = ks.heads;
   pl->rows_padded = ks.rows_padded;
+  pl->head_tiles = ks.rows_padded / ks.heads / 8;
   pl->unit_cost = ks.unit_cost;
   pl->whole_tile = ks.whole_tile != 0;
   pl->units = static_cast<long long>(d->B) * (d->Hkv / pl->hg);
@@ -371,7 +382,7 @@ size_t pd_workspace_bytes(const pd_dims* dims, int qlen, int num_splits, int sm_
 
 size_t pd_diff_workspace_bytes(const pd_dims* dims, int qlen, int num_splits, int sm_count) {
   Plan pl;
-  if (make_plan(dims, qlen, num_splits, sm_count, &pl, 0, true) != PD_OK) return 0;
+  if (make_plan(dims, qlen, num_splits, sm_count, &pl, 0, Op::kDiff) != PD_OK) return 0;
   return pl.bytes;
 }
 
@@ -386,7 +397,7 @@ int pd_grid_ctas(const pd_dims* dims, int qlen, int num_splits, int sm_count) {
 namespace {
 
 // What every decode call checks and fills in: the plan, the caches' maps and
-// the kernel's parameters (`diff`: of the differential decode). `ready` is
+// the kernel's parameters. `ready` is
 // false when there is nothing to launch. q_start null means B sequences of qlen
 // query tokens each (total_q = B * qlen); otherwise sequence b owns rows
 // [q_start[b], q_start[b+1]) of q and out, at most qlen of them.
@@ -394,10 +405,10 @@ pd_status prepare_decode(const void* q, const void* k_cache, const void* v_cache
                          const int32_t* block_table, const int32_t* seq_lens, const int32_t* q_start,
                          int total_q, float scale, int window, int qlen, int num_splits, void* out,
                          const pd_dims* dims, void* workspace, size_t workspace_bytes,
-                         uint32_t* error_flag, bool diff, Plan& pl, CUtensorMap& tk, CUtensorMap& tv,
+                         uint32_t* error_flag, Op op, Plan& pl, CUtensorMap& tk, CUtensorMap& tv,
                          DecodeParams& p, bool& ready) {
   ready = false;
-  pd_status st = check_dims(dims, qlen);
+  pd_status st = check_dims(dims, qlen, op);
   if (st != PD_OK) return st;
   if (num_splits < 0 || !std::isfinite(scale)) return PD_ERR_SHAPE;
   if (total_q < 0 || static_cast<long long>(total_q) * dims->Hq > (1ll << 31) - 1)
@@ -409,18 +420,22 @@ pd_status prepare_decode(const void* q, const void* k_cache, const void* v_cache
       (reinterpret_cast<uintptr_t>(q_start) & 3u) || (reinterpret_cast<uintptr_t>(error_flag) & 3u))
     return PD_ERR_ALIGN;
   if (dims->num_blocks == 0) return PD_ERR_SHAPE;
-  st = make_plan(dims, qlen, num_splits, 0, &pl, window, diff);
+  st = make_plan(dims, qlen, num_splits, 0, &pl, window, op);
   if (st != PD_OK) return st;
   if (pl.bytes > 0) {
     if (!workspace || workspace_bytes < pl.bytes) return PD_ERR_WORKSPACE;
     if (reinterpret_cast<uintptr_t>(workspace) & 255u) return PD_ERR_ALIGN;
   }
 
-  if (!encode_cache_map(&tk, k_cache, dims, pl.hg, pl.whole_tile) ||
-      !encode_cache_map(&tv, v_cache, dims, pl.hg, pl.whole_tile))
+  const bool fp4 = fp4_kind(dims->kv_dtype);
+  if (fp4) {
+    tk = tv = CUtensorMap{};  // its kernels copy without maps
+  } else if (!encode_cache_map(&tk, k_cache, dims, pl.hg, pl.whole_tile) ||
+             !encode_cache_map(&tv, v_cache, dims, pl.hg, pl.whole_tile)) {
     return PD_ERR_CUDA;
+  }
 
-  const bool fp8 = byte_kind(dims->kv_dtype);  // scaled codes
+  const bool fp8 = byte_kind(dims->kv_dtype) || fp4;  // scaled codes
   p.q = static_cast<const __half*>(q);
   p.out = static_cast<__half*>(out);
   p.block_table = block_table;
@@ -464,6 +479,54 @@ pd_status prepare_decode(const void* q, const void* k_cache, const void* v_cache
   return PD_OK;
 }
 
+// How a split combine is launched: CTAs that a unit head's dims are spread over, pieces loaded
+// at a time, threads.
+struct CombineShape {
+  int chunks, batch, threads;
+};
+CombineShape combine_shape(const Plan& pl, int D, int R) {
+  // pieces per split unit: about grid / units + 1 (balanced) or S (fixed);
+  // many pieces -> spread a unit's dims over CTAs so threads can share pieces,
+  // but keep the combine grid within one CTA per SM: those CTAs are resident
+  // beside the decode grid and do their pre-wait work (the unit's piece
+  // layout) while it runs, where CTAs beyond that start only as decode CTAs
+  // exit and add that work to the tail (measured on GB300, D=256 GQA 6:1:
+  // B = 2 / 3 / 8 15.0 / 17.6 / 28.9 -> 13.9 / 16.7 / 28.6 us, e4m3 B = 32
+  // 54.1 -> 52.5, L = 32768 B = 2 47.2 -> 45.8, windowed B = 2 14.7 ->
+  // 13.7; D=128 (28,4) ragged 86.5 -> 87.0; B = 1 and B = 32 unchanged)
+  const long long per_unit = pl.splits == 0 ? pl.grid / (pl.units > 0 ? pl.units : 1) + 1 : pl.splits;
+  int chunks = per_unit >= 16 ? D / 8 : per_unit >= 4 ? D / 32 : 1;
+  while (chunks > 1 && pl.n_merge * chunks * pl.hg > pl.sms) chunks >>= 1;
+  // units of more than four pieces: the combine that loads eight pieces'
+  // partials at a time (one L2 round trip for up to eight), else the one
+  // of four, which needs fewer registers (measured on GB300, D=256 GQA 6:1:
+  // e4m3 B = 32 52.3 -> 50.8 us, B = 8 28.2 -> 27.9, B = 3 16.6 -> 16.4 with
+  // eight; the headline's ~3.4 pieces per unit 0.3 us slower with eight)
+  const int batch = per_unit > 4 ? 8 : 4;
+  // a CTA's items (row, 4 dims) beyond 256: the batch-8 kernel's 512-thread
+  // form gives each thread one item (e4m3 / int8 B = 32: 384 items)
+  const long long items = static_cast<long long>(R) * (D / chunks / 4);
+  const int threads = items > 256 ? 512 : 256;
+  return {chunks, batch, threads};
+}
+
+bool misaligned(const void* p, uintptr_t mask) { return (reinterpret_cast<uintptr_t>(p) & mask) != 0; }
+
+// Workspace of a scored decode that sums its keys' weights: the split partials, the rows' (m, l), and
+// the scores of every key of the table (16 keys x 8 rows for each tile and row tile).
+struct ScoredLayout {
+  size_t off_ml, off_scores, bytes;
+};
+ScoredLayout scored_layout(const pd_dims& d, const Plan& pl, int qlen) {
+  auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+  ScoredLayout l;
+  l.off_ml = up(pl.bytes);
+  l.off_scores = l.off_ml + up(static_cast<size_t>(d.B) * qlen * d.Hq * 8);
+  const size_t tiles = static_cast<size_t>(d.max_blocks_per_seq) * (d.block_size / kTileKeys);
+  l.bytes = l.off_scores + static_cast<size_t>(d.B) * d.Hkv * tiles * pl.head_tiles * 512;
+  return l;
+}
+
 pd_status decode_impl(const void* q, const void* k_cache, const void* v_cache,
                       const int32_t* block_table, const int32_t* seq_lens, const int32_t* q_start,
                       int total_q, float scale, int window, int qlen, int num_splits, void* out,
@@ -474,36 +537,15 @@ pd_status decode_impl(const void* q, const void* k_cache, const void* v_cache,
   DecodeParams p;
   bool ready;
   const pd_status st = prepare_decode(q, k_cache, v_cache, block_table, seq_lens, q_start, total_q, scale, window, qlen,
-                                      num_splits, out, dims, workspace, workspace_bytes, error_flag, false, pl, tk, tv,
-                                      p, ready);
+                                      num_splits, out, dims, workspace, workspace_bytes, error_flag, Op::kPlain, pl,
+                                      tk, tv, p, ready);
   if (st != PD_OK || !ready) return st;
   const WorkspaceLock lock(workspace, pl.n_merge > 0);
   cudaError_t e = launch_decode(dims->D, dims->kv_dtype, pl.nt, pl.hg > 1 ? 1 : 0, tk, tv, p, pl.grid,
                                 static_cast<cudaStream_t>(stream));
   if (e == cudaSuccess && pl.n_merge > 0) {
-    // pieces per split unit: about grid / units + 1 (balanced) or S (fixed);
-    // many pieces -> spread a unit's dims over CTAs so threads can share pieces,
-    // but keep the combine grid within one CTA per SM: those CTAs are resident
-    // beside the decode grid and do their pre-wait work (the unit's piece
-    // layout) while it runs, where CTAs beyond that start only as decode CTAs
-    // exit and add that work to the tail (measured on GB300, D=256 GQA 6:1:
-    // B = 2 / 3 / 8 15.0 / 17.6 / 28.9 -> 13.9 / 16.7 / 28.6 us, e4m3 B = 32
-    // 54.1 -> 52.5, L = 32768 B = 2 47.2 -> 45.8, windowed B = 2 14.7 ->
-    // 13.7; D=128 (28,4) ragged 86.5 -> 87.0; B = 1 and B = 32 unchanged)
-    const long long per_unit = pl.splits == 0 ? pl.grid / (pl.units > 0 ? pl.units : 1) + 1 : pl.splits;
-    int chunks = per_unit >= 16 ? dims->D / 8 : per_unit >= 4 ? dims->D / 32 : 1;
-    while (chunks > 1 && pl.n_merge * chunks * pl.hg > pl.sms) chunks >>= 1;
-    // units of more than four pieces: the combine that loads eight pieces'
-    // partials at a time (one L2 round trip for up to eight), else the one
-    // of four, which needs fewer registers (measured on GB300, D=256 GQA 6:1:
-    // e4m3 B = 32 52.3 -> 50.8 us, B = 8 28.2 -> 27.9, B = 3 16.6 -> 16.4 with
-    // eight; the headline's ~3.4 pieces per unit 0.3 us slower with eight)
-    const int batch = per_unit > 4 ? 8 : 4;
-    // a CTA's items (row, 4 dims) beyond 256: the batch-8 kernel's 512-thread
-    // form gives each thread one item (e4m3 / int8 B = 32: 384 items)
-    const long long items = static_cast<long long>(p.R) * (dims->D / chunks / 4);
-    const int threads = items > 256 ? 512 : 256;
-    e = launch_split_combine(dims->D, p, static_cast<int>(pl.n_merge), chunks, batch, threads,
+    const CombineShape c = combine_shape(pl, dims->D, p.R);
+    e = launch_split_combine(dims->D, p, static_cast<int>(pl.n_merge), c.chunks, c.batch, c.threads,
                              static_cast<cudaStream_t>(stream));
   }
   return e == cudaSuccess ? PD_OK : PD_ERR_CUDA;
@@ -564,7 +606,7 @@ pd_status decode_paged_diff(const void* q, const void* k_cache, const void* v_ca
   bool ready;
   const pd_status st = prepare_decode(q, k_cache, v_cache, block_table, seq_lens, query_start_loc,
                                       static_cast<int>(total), scale, window, qlen, num_splits, out, dims, workspace,
-                                      workspace_bytes, error_flag, true, pl, tk, tv, p.d, ready);
+                                      workspace_bytes, error_flag, Op::kDiff, pl, tk, tv, p.d, ready);
   if (st != PD_OK || !ready) return st;
   p.v_cache = v_cache;
   p.lambda = lambda;
@@ -588,6 +630,77 @@ pd_status decode_paged_diff(const void* q, const void* k_cache, const void* v_ca
     const int rows = std::min((p.d.R + chunks - 1) / chunks, slots);
     const int groups = static_cast<int>(std::min<long long>(slots / rows, per_unit));
     e = launch_diff_combine(dims->D, p, static_cast<int>(pl.n_merge), chunks, rows, groups, many, s);
+  }
+  return e == cudaSuccess ? PD_OK : PD_ERR_CUDA;
+}
+
+size_t pd_scored_workspace_bytes(const pd_dims* dims, int qlen, int num_splits, int key_weights, int sm_count) {
+  Plan pl;
+  if (make_plan(dims, qlen, num_splits, sm_count, &pl, 0, Op::kScored) != PD_OK) return 0;
+  return key_weights ? scored_layout(*dims, pl, qlen).bytes : pl.bytes;
+}
+
+pd_status decode_paged_scored(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_table,
+                              const int32_t* seq_lens, const int32_t* query_start_loc, int num_query_tokens, float scale,
+                              int window, int qlen, int num_splits, const pd_score* score, void* out,
+                              const pd_dims* dims, void* workspace, size_t workspace_bytes, uint32_t* error_flag,
+                              void* stream) {
+  if (!dims || !score) return PD_ERR_NULL;
+  long long total = num_query_tokens;
+  if (!query_start_loc) {
+    total = static_cast<long long>(dims->B) * (qlen > 0 ? qlen : 0);
+    if (total > (1ll << 31) - 1) return PD_ERR_UNSUPPORTED;
+  }
+  const pd_score& sc = *score;
+  const bool fp4 = fp4_kind(dims->kv_dtype), weights = sc.key_weights_out != nullptr;
+  if (!std::isfinite(sc.cap) || sc.cap < 0.f || (sc.cap > 0.f && !(sc.cap >= 1e-30f))) return PD_ERR_SHAPE;
+  if (misaligned(sc.alibi_slopes, 3) || misaligned(sc.prefix_lens, 3) || misaligned(sc.lse, 3) ||
+      misaligned(sc.key_weights, 3) || misaligned(sc.key_weights_out, 3) || misaligned(sc.k_block_scale, 15) ||
+      misaligned(sc.v_block_scale, 15))
+    return PD_ERR_ALIGN;
+  Plan pl;
+  CUtensorMap tk, tv;
+  Fp4Params p;
+  bool ready;
+  const pd_status st = prepare_decode(q, k_cache, v_cache, block_table, seq_lens, query_start_loc,
+                                      static_cast<int>(total), scale, window, qlen, num_splits, out, dims, workspace,
+                                      workspace_bytes, error_flag, Op::kScored, pl, tk, tv, p, ready);
+  if (st != PD_OK || !ready) return st;
+  if (fp4 && (!sc.k_block_scale || !sc.v_block_scale)) return PD_ERR_NULL;
+  if (weights && !sc.key_weights) return PD_ERR_NULL;
+  p.cap_u = sc.cap > 0.f ? static_cast<float>(0.6931471805599453 / sc.cap) : 0.f;
+  p.cap_out = sc.cap > 0.f ? static_cast<float>(sc.cap * 1.4426950408889634) : 0.f;
+  p.slopes = sc.alibi_slopes;
+  p.prefix_lens = sc.prefix_lens;
+  p.lse = sc.lse;
+  p.row_ml = nullptr;
+  p.scores = nullptr;
+  p.k_codes = static_cast<const uint8_t*>(k_cache);
+  p.v_codes = static_cast<const uint8_t*>(v_cache);
+  p.k_sf = static_cast<const uint8_t*>(sc.k_block_scale);
+  p.v_sf = static_cast<const uint8_t*>(sc.v_block_scale);
+  if (weights) {
+    const ScoredLayout lay = scored_layout(*dims, pl, qlen);
+    if (!workspace || workspace_bytes < lay.bytes) return PD_ERR_WORKSPACE;
+    if (misaligned(workspace, 255)) return PD_ERR_ALIGN;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    p.row_ml = reinterpret_cast<float2*>(ws + lay.off_ml);
+    p.scores = reinterpret_cast<float*>(ws + lay.off_scores);
+  }
+  auto s = static_cast<cudaStream_t>(stream);
+  const WorkspaceLock lock(workspace, pl.n_merge > 0 || weights);
+  cudaError_t e = launch_scored(dims->D, dims->kv_dtype, pl.nt, pl.hg > 1 ? 1 : 0, tk, tv, p, pl.grid, s);
+  if (e == cudaSuccess && pl.n_merge > 0) {
+    const CombineShape c = combine_shape(pl, dims->D, p.R);
+    e = launch_scored_combine(dims->D, p, static_cast<int>(pl.n_merge), c.chunks, c.batch, c.threads, s);
+  }
+  if (e == cudaSuccess && weights) {
+    KeyWeightParams kw;
+    kw.d = p;
+    kw.in = sc.key_weights;
+    kw.out = sc.key_weights_out;
+    kw.row_tiles = pl.head_tiles;
+    e = launch_key_weights(kw, pl.sms, s);
   }
   return e == cudaSuccess ? PD_OK : PD_ERR_CUDA;
 }
