@@ -31,6 +31,8 @@
 //  * The softmax reference is raised only when a score passes it by 2^8, so that the
 //    common step has no shuffles and no rescaling.
 #pragma once
+#include <type_traits>
+
 #include "decode_kernel.cuh"
 
 namespace pd {
@@ -59,9 +61,8 @@ struct Fp4Cfg {
   static constexpr int kMerge = NT * MT * kPitch * 16;    // a warp's (m, l, O) fragments, over its ring
   static_assert(kMerge <= kRing, "the merge buffer lies over the ring");
   static constexpr int RP = RG * NT * 8;
-  static constexpr int kOffQ = kWarps * kRing;            // q fragments [row group][row tile][k-step][lane] uint2
-  static constexpr bool kQSmem = NT > 1;
-  static constexpr int kQ = kQSmem ? RG * NT * MT * 32 * 8 : 0;
+  static constexpr int kOffQ = kWarps * kRing;            // q fragments
+  static constexpr int kQ = RG * NT * MT * 32 * 8;
   static constexpr int kOffML = kOffQ + kQ;               // [warp][NT * 8] (m, l)
   static constexpr int kOffPre = kOffML + kWarps * NT * 8 * 8;
   static constexpr int kSmemBytes = kOffPre + (kMaxAutoB + 1) * 4 + 12;
@@ -101,10 +102,10 @@ template <class Cfg>
 __global__ void __launch_bounds__(Cfg::kThreads, Cfg::kMinBlocks) decode_fp4_kernel(const Fp4Params p) {
   constexpr int D = Cfg::D, NT = Cfg::NT, RG = Cfg::RG, KG = Cfg::KG, KT = Cfg::KT, ST = Cfg::ST, MT = Cfg::MT;
   constexpr int PP = Cfg::PP;
-  extern __shared__ __align__(16) uint8_t smem[];
+  extern __shared__ __align__(128) uint8_t smem[];
   float2* s_ml = reinterpret_cast<float2*>(smem + Cfg::kOffML);
   int* s_pre = reinterpret_cast<int*>(smem + Cfg::kOffPre);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = warp_uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   const int rg = warp % RG, kg = warp / RG;
   const int g = lane >> 2, t4 = lane & 3;
 
@@ -117,91 +118,99 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::kMinBlocks) decode_fp4_ker
   Piece pc;
 
   const uint32_t ring = smem_u32(smem) + warp * Cfg::kRing;
-  // this lane's pieces of a tile: K bytes (key g, chunk t4) and what follows it, V bytes
-  // of the keys that its operand registers hold
-  const uint32_t k_src = D == 256 ? g * 128 + t4 * 16 : g * 64 + t4 * 16;
-  uint2* s_q = reinterpret_cast<uint2*>(smem + Cfg::kOffQ);
+  // this lane's pieces of a tile. D = 256: K chunks t4 and t4 + 4 of keys g and g + 8; V chunk g of
+  // keys 2 t4, 2 t4 + 1 and those + 8; scales of key lane % 16. D = 128: K chunk t4; V and the
+  // scales in 16-byte pieces of two keys' rows.
+  const uint8_t* k_src = p.k_codes + (D == 256 ? g * 128 + t4 * 16 : g * 64 + t4 * 16);
+  const uint8_t* v_src = p.v_codes + (D == 256 ? 2 * t4 * 128 + g * 16 : lane * 16);
+  constexpr int kSfLanes = D / 16;  // lanes that copy scales of K (as many of V)
+  const uint8_t* sf_src = (lane < kSfLanes ? p.k_sf : p.v_sf) + lane % kSfLanes * 16;
+  const uint32_t q_frags = smem_u32(smem + Cfg::kOffQ) + rg * NT * MT * 32 * 8;
 
-  while (work_next(p, s_pre, it, pc)) {
-    const int kh = pc.kh;
+  while (warp_uniform(work_next(p, s_pre, it, pc))) {
+    const int kh = pc.kh, ntiles = warp_uniform(pc.ntiles), seq_len = warp_uniform(pc.L);
+    const int lo_all = warp_uniform(pc.tile_lo_all), hi_all = warp_uniform(pc.tile_hi_all);
+    const int prefix = warp_uniform(pc.prefix);
     // ---- copies of the warp's steps: step i is tiles (i KG + kg) KT ..
-    const int steps = (pc.ntiles - kg * KT + KG * KT - 1) / (KG * KT);  // (<= 0: none)
+    const int steps = (ntiles - kg * KT + KG * KT - 1) / (KG * KT);  // (<= 0: none)
     const int32_t* row = p.block_table + static_cast<long long>(pc.b) * p.max_blocks;
     auto load_blocks = [&](int i0, int (&blk)[KT]) {  // lane: the physical blocks of step i0 + lane
 #pragma unroll
       for (int j = 0; j < KT; ++j) {
         const int k = ((i0 + lane) * KG + kg) * KT + j;
         blk[j] = 0;
-        if (k < pc.ntiles) blk[j] = __ldg(row + piece_tile(p, pc, k) / p.tiles_per_block);
+        if (k < ntiles) blk[j] = __ldg(row + piece_tile(p, pc, k) / p.tiles_per_block);
       }
     };
-    int cur[KT], nxt[KT];
-    load_blocks(0, cur);
-    load_blocks(32, nxt);
-    auto issue = [&](int i) {  // copies of step i (any i: none behind the last)
-      if (i < steps) {
-        if ((i & 31) == 0 && i > 0) {
+    int cur[KT], nxt[KT];  // lane: the tile in the caches' order, of step (i & ~31) + lane; blocks of the steps after
+    auto to_tiles = [&](int i0, const int (&blk)[KT], int (&tile)[KT]) {
 #pragma unroll
-          for (int j = 0; j < KT; ++j) cur[j] = nxt[j];
-          load_blocks(i + 32, nxt);
+      for (int j = 0; j < KT; ++j) {
+        int b = blk[j];
+        if (b < 0 || b >= p.num_blocks) {
+          raise_error(p.error_flag, kErrBlockId);
+          b = 0;
         }
-        const uint32_t stage = ring + (i % ST) * Cfg::kStage;
+        tile[j] = (b * p.Hkv + kh) * p.tiles_per_block +
+                  piece_tile(p, pc, ((i0 + lane) * KG + kg) * KT + j) % p.tiles_per_block;
+      }
+    };
+    load_blocks(0, nxt);
+    int next = 0;              // the step whose copies are next
+    uint32_t fill = ring;      // and its stage
+    auto issue = [&]() {
+      if (next < steps) {
+        if ((next & 31) == 0) {
+          to_tiles(next, nxt, cur);
+          load_blocks(next + 32, nxt);
+        }
 #pragma unroll
         for (int j = 0; j < KT; ++j) {
-          const int k = (i * KG + kg) * KT + j;
-          int blk = __shfl_sync(0xffffffffu, cur[j], i & 31);
-          if (KT > 1 && k >= pc.ntiles) continue;
-          if (blk < 0 || blk >= p.num_blocks) {
-            if (lane == 0) raise_error(p.error_flag, kErrBlockId);
-            blk = 0;
-          }
-          const long long key = (static_cast<long long>(blk) * p.Hkv + kh) * p.block_size +
-                                (piece_tile(p, pc, k) % p.tiles_per_block) * kTileKeys;
-          const uint8_t* kc = p.k_codes + key * (D / 2);
-          const uint8_t* vc = p.v_codes + key * (D / 2);
-          const uint32_t dst = stage + j * Cfg::kTile;
+          const long long tile = __shfl_sync(0xffffffffu, cur[j], next & 31);
+          if (KT > 1 && (next * KG + kg) * KT + j >= ntiles) continue;
+          const uint8_t* kc = k_src + tile * Cfg::kCodes;
+          const uint8_t* vc = v_src + tile * Cfg::kCodes;
+          const uint8_t* sf = sf_src + tile * Cfg::kScales;
+          const uint32_t dst = fill + j * Cfg::kTile + lane * 16;
           if constexpr (D == 256) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {  // keys g, g + 8; chunks t4, t4 + 4
-              cp_async16(dst + q * 512 + lane * 16, kc + k_src + (q >> 1) * 1024 + (q & 1) * 64);
-              // keys 2 t4, 2 t4 + 1, 2 t4 + 8, 2 t4 + 9; chunk g
-              cp_async16(dst + Cfg::kCodes + q * 512 + lane * 16,
-                         vc + (2 * t4 + (q & 1) + (q >> 1) * 8) * 128 + g * 16);
+            for (int q = 0; q < 4; ++q) {
+              cp_async16(dst + q * 512, kc + (q >> 1) * 1024 + (q & 1) * 64);
+              cp_async16(dst + Cfg::kCodes + q * 512, vc + (q >> 1) * 1024 + (q & 1) * 128);
             }
-            cp_async16(dst + 2 * Cfg::kCodes + lane * 16,
-                       (lane < 16 ? p.k_sf : p.v_sf) + key * (D / 16) + (lane & 15) * 16);
+            cp_async16(dst + 2 * Cfg::kCodes, sf);
           } else {
+            // V: 16-byte piece c of line l (two keys' rows) lies at c ^ 2 l of its line: the lanes of
+            // a read (keys 2 t4, 8-byte chunks g) meet all banks
+            const int line = lane >> 3;
+            const uint32_t vd = fill + j * Cfg::kTile + Cfg::kCodes + line * 128 + (((lane & 7) ^ (2 * line)) << 4);
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {  // keys g, g + 8; chunk t4
-              cp_async16(dst + q * 512 + lane * 16, kc + k_src + q * 512);
-              // V: 16-byte piece c of line l (two keys' rows) lies at c ^ 2 l of its line: the lanes of
-              // a read (keys 2 t4, 8-byte chunks g) meet all banks
-              const int line = q * 4 + (lane >> 3);
-              cp_async16(dst + Cfg::kCodes + line * 128 + (((lane & 7) ^ (2 * line & 7)) << 4),
-                         vc + line * 128 + (lane & 7) * 16);
+            for (int q = 0; q < 2; ++q) {
+              cp_async16(dst + q * 512, kc + q * 512);
+              cp_async16(vd + q * 512, vc + q * 512);
             }
-            if (lane < 16)
-              cp_async16(dst + 2 * Cfg::kCodes + lane * 16,
-                         (lane < 8 ? p.k_sf : p.v_sf) + key * (D / 16) + (lane & 7) * 16);
+            if (lane < 2 * kSfLanes) cp_async16(dst + 2 * Cfg::kCodes, sf);
           }
         }
       }
       cp_async_commit();
+      ++next;
+      fill = fill == ring + (ST - 1) * Cfg::kStage ? ring : fill + Cfg::kStage;
     };
 #pragma unroll
-    for (int i = 0; i < ST - 1; ++i) issue(i);
+    for (int i = 0; i < ST - 1; ++i) issue();
 
-    // ---- q fragments, in the order that the codes' bytes give the contraction
-    uint32_t qf[Cfg::kQSmem ? 1 : NT][MT][2];
+    // ---- q fragments, in the order that the codes' bytes give the contraction: lane's k-steps
+    // 2 i and 2 i + 1 side by side, [row group][row tile][i][lane] 16 bytes
     float sl2r[NT][2];
-    int lo_r[NT][2], hi_r[NT][2], pre_r[NT][2];
-    float m_r[NT][2], l_r[NT][2], slope_r[NT][2];
+    int hi_r[NT][2];          // last causal key of rows 2 t4, 2 t4 + 1 of a row tile (padded rows: -1)
+    float m_r[NT][2], l_r[NT][2];
     float o[MT][NT][4];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       const int r = (rg * NT + n) * 8 + g;
       const uint32_t* qrow = nullptr;
-      if (r < pc.R && pc.ntiles > 0) {
+      if (r < pc.R && ntiles > 0) {
         const int i = r / p.G, hl = r % p.G;
         qrow = reinterpret_cast<const uint32_t*>(
             p.q + (static_cast<long long>(pc.q0 + i) * p.Hq + kh * p.G + hl) * D);
@@ -235,43 +244,29 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::kMinBlocks) decode_fp4_ker
           for (int h = 0; h < 2; ++h)
             f[ks][h] = pack_half2(__uint_as_float(f[ks][h] << 16) * up, __uint_as_float(f[ks][h] & 0xffff0000u) * up);
       }
-      if constexpr (Cfg::kQSmem) {  // each key group's warps write the same
+      if (kg == 0) {  // (every key group has the same)
 #pragma unroll
-        for (int ks = 0; ks < MT; ++ks)
-          if (kg == 0) s_q[((rg * NT + n) * MT + ks) * 32 + lane] = make_uint2(f[ks][0], f[ks][1]);
-      } else {
-#pragma unroll
-        for (int ks = 0; ks < MT; ++ks) {
-          qf[n][ks][0] = f[ks][0];
-          qf[n][ks][1] = f[ks][1];
-        }
+        for (int i = 0; i < MT / 2; ++i)
+          sts_v4(q_frags + ((n * MT / 2 + i) * 32 + lane) * 16, f[2 * i][0], f[2 * i][1], f[2 * i + 1][0], f[2 * i + 1][1]);
       }
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         const int rr = (rg * NT + n) * 8 + 2 * t4 + c;
-        hi_r[n][c] = -1;
-        lo_r[n][c] = pre_r[n][c] = 0;
-        slope_r[n][c] = 0.f;
-        if (rr < pc.R) {
-          const int pos = pc.L - pc.qlen + rr / p.G;
-          hi_r[n][c] = pos;
-          lo_r[n][c] = p.window > 0 ? max(0, pos - p.window + 1) : 0;
-          pre_r[n][c] = pos >= 0 ? pc.prefix : 0;
-          if (p.slopes != nullptr) slope_r[n][c] = __ldg(p.slopes + kh * p.G + rr % p.G) * kLog2e;
-        }
+        hi_r[n][c] = rr < pc.R ? pc.L - pc.qlen + rr / p.G : -1;
         m_r[n][c] = -INFINITY;
         l_r[n][c] = 0.f;
       }
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) o[mt][n][0] = o[mt][n][1] = o[mt][n][2] = o[mt][n][3] = 0.f;
     }
-    if constexpr (Cfg::kQSmem) __syncthreads();
+    __syncthreads();
 
-    for (int i = 0; i < steps; ++i) {
-      cp_async_wait<ST - 2>();
-      __syncwarp();  // the step's scales are there, and every lane is done with the stage that is filled next
-      issue(i + ST - 1);
-      const uint32_t stage = ring + (i % ST) * Cfg::kStage;
+    uint32_t stage = ring;
+    // A step is compiled twice: for tiles that every row sees whole, and for the others (EDGE:
+    // masks, scales that are no numbers, a missing tile).
+    auto step = [&](const int i, auto edge_step) __attribute__((always_inline)) {
+      constexpr bool EDGE = decltype(edge_step)::value;
+      const int k0 = (i * KG + kg) * KT;
       // ---- S^T = K Q^T: 16 keys x 8 rows for each tile and row tile
       float x[KT][NT][4];
 #pragma unroll
@@ -298,25 +293,13 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::kMinBlocks) decode_fp4_ker
             e2m1x8_to_half2(wa[w], ha);
             e2m1x8_to_half2(wb[w], hb);
             const uint32_t f0 = w < 2 ? s00 : s01, f8 = w < 2 ? s80 : s81;
+            const uint32_t a0[4] = {hmul2_u(ha[0], f0), hmul2_u(hb[0], f8), hmul2_u(ha[1], f0), hmul2_u(hb[1], f8)};
+            const uint32_t a1[4] = {hmul2_u(ha[2], f0), hmul2_u(hb[2], f8), hmul2_u(ha[3], f0), hmul2_u(hb[3], f8)};
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const uint32_t a[4] = {hmul2_u(ha[2 * h], f0), hmul2_u(hb[2 * h], f8), hmul2_u(ha[2 * h + 1], f0),
-                                     hmul2_u(hb[2 * h + 1], f8)};
-              const int ks = c * 8 + 2 * w + h;
-#pragma unroll
-              for (int n = 0; n < NT; ++n) {
-                uint32_t b0, b1;
-                if constexpr (Cfg::kQSmem) {
-                  const uint2 b = s_q[((rg * NT + n) * MT + ks) * 32 + lane];
-                  b0 = b.x;
-                  b1 = b.y;
-                } else {
-                  b0 = qf[n][ks][0];
-                  b1 = qf[n][ks][1];
-                }
-                if (h) mma_16816(sb[n], a, b0, b1);
-                else mma_16816(sa[n], a, b0, b1);
-              }
+            for (int n = 0; n < NT; ++n) {
+              const uint4 b = lds_v4_tile(q_frags + ((n * MT / 2 + c * 4 + w) * 32 + lane) * 16);
+              mma_16816(sa[n], a0, b.x, b.y);
+              mma_16816(sb[n], a1, b.z, b.w);
             }
           }
         }
@@ -326,47 +309,45 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::kMinBlocks) decode_fp4_ker
           for (int e = 0; e < 4; ++e) x[j][n][e] = (sa[n][e] + sb[n][e]) * sl2r[n][e & 1];
       }
       // ---- caps, biases, masks
-      uint32_t see[KT][NT][2];
-      bool edge[KT];
+      bool there[KT];
       int key0[KT];
 #pragma unroll
       for (int j = 0; j < KT; ++j) {
-        const int k = (i * KG + kg) * KT + j;
-        const bool there = KT == 1 || k < pc.ntiles;
-        key0[j] = piece_tile(p, pc, k) * kTileKeys;
-        edge[j] = !((key0[j] >= pc.tile_lo_all && key0[j] + kTileKeys - 1 <= pc.tile_hi_all) ||
-                    (key0[j] + kTileKeys <= pc.prefix && pc.tile_hi_all >= 0)) || !there;
+        there[j] = !EDGE || k0 + j < ntiles;
+        key0[j] = piece_tile(p, pc, k0 + j) * kTileKeys;
         const int j0 = key0[j] + g;
+        if (p.cap_out > 0.f) {
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          if (p.cap_out > 0.f) {
+          for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int e = 0; e < 4; ++e) x[j][n][e] = p.cap_out * tanh_f32(x[j][n][e] * p.cap_u);
-          }
-          if (p.slopes != nullptr) {
+        }
+        if (p.slopes != nullptr) {
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              const int r = (rg * NT + n) * 8 + 2 * t4 + c;
+              const float slope = r < pc.R ? __ldg(p.slopes + kh * p.G + r % p.G) * kLog2e : 0.f;
+              x[j][n][c] -= slope * static_cast<float>(abs(j0 - hi_r[n][c]));
+              x[j][n][c + 2] -= slope * static_cast<float>(abs(j0 + 8 - hi_r[n][c]));
+            }
+        }
+        if constexpr (EDGE) {  // (padded rows: q = 0, never written)
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              x[j][n][e] -= slope_r[n][e & 1] * static_cast<float>(abs(j0 + (e >> 1) * 8 - hi_r[n][e & 1]));
-          }
-          if (!edge[j]) {
+              if (!there[j] || !row_sees(p, pc, (rg * NT + n) * 8 + 2 * t4 + (e & 1), j0 + (e >> 1) * 8))
+                x[j][n][e] = -INFINITY;
+        }
+        if (p.scores != nullptr && there[j]) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) x[j][n][e] = hi_r[n][e & 1] >= 0 ? x[j][n][e] : -INFINITY;
-          } else {
-            bool v[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int jj = j0 + (e >> 1) * 8;
-              v[e] = there && ((jj >= lo_r[n][e & 1] && jj <= hi_r[n][e & 1]) || jj < pre_r[n][e & 1]);
-              x[j][n][e] = v[e] ? x[j][n][e] : -INFINITY;
-            }
-            see[j][n][0] = movmatrix_trans(pack_half2(v[0] ? 1.f : 0.f, v[1] ? 1.f : 0.f));
-            see[j][n][1] = movmatrix_trans(pack_half2(v[2] ? 1.f : 0.f, v[3] ? 1.f : 0.f));
-          }
-          if (p.scores != nullptr && there) {
+          for (int n = 0; n < NT; ++n) {
             float* dst = p.scores + ((static_cast<long long>(pc.b) * p.Hkv + kh) * p.max_blocks * p.tiles_per_block +
-                                     key0[j] / kTileKeys) * (RG * NT * 128) + (rg * NT + n) * 128;
-            __stcg(reinterpret_cast<float2*>(dst + g * 8 + 2 * t4), make_float2(x[j][n][0], x[j][n][1]));
-            __stcg(reinterpret_cast<float2*>(dst + (g + 8) * 8 + 2 * t4), make_float2(x[j][n][2], x[j][n][3]));
+                                     key0[j] / kTileKeys) * (RG * NT * 128) + (rg * NT + n) * 128 + g * 8 + 2 * t4;
+            __stcg(reinterpret_cast<float2*>(dst), make_float2(x[j][n][0], x[j][n][1]));
+            __stcg(reinterpret_cast<float2*>(dst + 64), make_float2(x[j][n][2], x[j][n][3]));
           }
         }
       }
@@ -375,11 +356,13 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::kMinBlocks) decode_fp4_ker
       // reference's weight
       bool up = false;
 #pragma unroll
-      for (int j = 0; j < KT; ++j)
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) up |= x[j][n][e] > m_r[n][e & 1] + 8.f;
+        for (int c = 0; c < 2; ++c) {
+          float mx = fmaxf(x[0][n][c], x[0][n][c + 2]);
+          if constexpr (KT > 1) mx = fmaxf(mx, fmaxf(x[KT - 1][n][c], x[KT - 1][n][c + 2]));
+          up |= mx - m_r[n][c] > 8.f;  // (no key seen: m = -inf)
+        }
       if (__any_sync(0xffffffffu, up)) {
 #pragma unroll
         for (int n = 0; n < NT; ++n)
@@ -403,12 +386,12 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::kMinBlocks) decode_fp4_ker
       uint32_t pb[KT][NT][2], pl[PP == 2 ? KT : 1][PP == 2 ? NT : 1][2];
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        const float b0 = m_r[n][0] == -INFINITY ? 0.f : m_r[n][0] - 7.f;
-        const float b1 = m_r[n][1] == -INFINITY ? 0.f : m_r[n][1] - 7.f;
+        const float b0 = m_r[n][0] == -INFINITY ? 0.f : 7.f - m_r[n][0];
+        const float b1 = m_r[n][1] == -INFINITY ? 0.f : 7.f - m_r[n][1];
 #pragma unroll
         for (int j = 0; j < KT; ++j) {
-          const float p0 = ex2(x[j][n][0] - b0), p1 = ex2(x[j][n][1] - b1), p2 = ex2(x[j][n][2] - b0),
-                      p3 = ex2(x[j][n][3] - b1);
+          const float p0 = ex2(x[j][n][0] + b0), p1 = ex2(x[j][n][1] + b1), p2 = ex2(x[j][n][2] + b0),
+                      p3 = ex2(x[j][n][3] + b1);
           l_r[n][0] += p0 + p2;
           l_r[n][1] += p1 + p3;
           const uint32_t w0 = pack_half2(p0, p1), w1 = pack_half2(p2, p3);
@@ -424,7 +407,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::kMinBlocks) decode_fp4_ker
       // ---- O^T += V^T P^T
 #pragma unroll
       for (int j = 0; j < KT; ++j) {
-        if (KT > 1 && (i * KG + kg) * KT + j >= pc.ntiles) continue;
+        if (EDGE && !there[j]) continue;
         const uint32_t vt = stage + j * Cfg::kTile + Cfg::kCodes;
         const uint32_t sf = stage + j * Cfg::kTile + 2 * Cfg::kCodes + Cfg::kScales;
         constexpr int NG = D / 128;  // groups of 16 dims that a lane holds
@@ -451,18 +434,19 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::kMinBlocks) decode_fp4_ker
           f89[0] = e4m3x2_to_half2(static_cast<uint16_t>(prmt(c, d, sel)));
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            const int key = 2 * t4 + (q & 1) + (q >> 1) * 8, line = key >> 1;
-            const uint2 v = lds_v2(vt + line * 128 + ((((key & 1) * 4 + (g >> 1)) ^ (2 * line & 7)) << 4) + (g & 1) * 8);
+            // key 2 t4 + (q & 1) + 8 (q >> 1): line t4 + 4 (q >> 1)
+            const uint32_t at_v = vt + t4 * 128 + (((g >> 1) ^ (2 * t4)) << 4) + (g & 1) * 8;
+            const uint2 v = lds_v2((at_v ^ ((q & 1) * 64)) + (q >> 1) * 512);
             w[q][0] = v.x; w[q][1] = v.y;
           }
         }
         // Keys at or past the sequence's end may hold any bits: a scale of NaN must not meet a
         // weight of zero. Nor must one of a key that only some rows see: it is taken out, and a
         // product of ones marks the outputs of the rows that see it.
-        if (edge[j]) {
-          const int k0 = key0[j] + 2 * t4;
-          const uint32_t in01 = (k0 < pc.L ? 0x0000ffffu : 0u) | (k0 + 1 < pc.L ? 0xffff0000u : 0u);
-          const uint32_t in89 = (k0 + 8 < pc.L ? 0x0000ffffu : 0u) | (k0 + 9 < pc.L ? 0xffff0000u : 0u);
+        if constexpr (EDGE) {
+          const int ka = key0[j] + 2 * t4;
+          const uint32_t in01 = (ka < seq_len ? 0x0000ffffu : 0u) | (ka + 1 < seq_len ? 0xffff0000u : 0u);
+          const uint32_t in89 = (ka + 8 < seq_len ? 0x0000ffffu : 0u) | (ka + 9 < seq_len ? 0xffff0000u : 0u);
 #pragma unroll
           for (int gr = 0; gr < NG; ++gr) {
             f01[gr] &= in01;
@@ -474,8 +458,11 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::kMinBlocks) decode_fp4_ker
               const uint32_t a[4] = {o01 & 0x3c003c00u, o01 & 0x3c003c00u, o89 & 0x3c003c00u, o89 & 0x3c003c00u};
 #pragma unroll
               for (int n = 0; n < NT; ++n) {
+                const int r = (rg * NT + n) * 8 + g;
+                const uint32_t see0 = (row_sees(p, pc, r, ka) ? 0x3c00u : 0u) | (row_sees(p, pc, r, ka + 1) ? 0x3c000000u : 0u);
+                const uint32_t see1 = (row_sees(p, pc, r, ka + 8) ? 0x3c00u : 0u) | (row_sees(p, pc, r, ka + 9) ? 0x3c000000u : 0u);
                 float mark[4] = {0.f, 0.f, 0.f, 0.f};
-                mma_16816(mark, a, see[j][n][0], see[j][n][1]);
+                mma_16816(mark, a, see0, see1);
 #pragma unroll
                 for (int mt = 0; mt < 8; ++mt)
 #pragma unroll
@@ -507,6 +494,22 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::kMinBlocks) decode_fp4_ker
           }
         }
       }
+    };
+    for (int i = 0; i < steps; ++i) {
+      cp_async_wait<ST - 2>();
+      __syncwarp();  // the step's scales are there, and every lane is done with the stage that is filled next
+      issue();
+      const int k0 = (i * KG + kg) * KT;
+      bool plain = KT == 1 || k0 + KT <= ntiles;
+#pragma unroll
+      for (int j = 0; j < KT; ++j) {
+        const int key0 = piece_tile(p, pc, k0 + j) * kTileKeys;
+        plain = plain && ((key0 >= lo_all && key0 + kTileKeys - 1 <= hi_all) ||
+                          (key0 + kTileKeys <= prefix && hi_all >= 0));
+      }
+      if (plain) step(i, std::false_type());
+      else step(i, std::true_type());
+      stage = stage == ring + (ST - 1) * Cfg::kStage ? ring : stage + Cfg::kStage;
     }
 
     // ---- the warps' (m, l, O) meet; m becomes what the weights are relative to

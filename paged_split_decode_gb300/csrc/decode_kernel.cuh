@@ -586,6 +586,14 @@ __device__ __forceinline__ bool work_next(const Par& p, const int* s_pre, WorkIt
   return false;
 }
 
+__device__ __forceinline__ int warp_uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+
+// Scored decode: whether row r of a piece's head sees key j.
+__device__ __forceinline__ bool row_sees(const ScoredParams& p, const Piece& pc, int r, int j) {
+  const int pos = pc.L - pc.qlen + r / p.G;
+  return r < pc.R && pos >= 0 && j < pc.L && ((j <= pos && (p.window <= 0 || j > pos - p.window)) || j < pc.prefix);
+}
+
 // The factor that makes a row's output of its sum of weighted values. (Scored decode: a
 // NaN among the scores shows in the output.)
 template <class Par>
@@ -636,8 +644,8 @@ __device__ __forceinline__ uint32_t not_finite_16(uint32_t w) {
 // writes them as the split combine would: M = max m, w = 2^(m - M),
 // out = sum w O / sum w l. A unit covered by one piece (or none) was written
 // by its piece.
-template <int D, int RP, int RH, int HG, int NTHREADS, class Par>
-__device__ __forceinline__ void cluster_merge_ws(const Par& p) {
+template <int D, int RP, int RH, int HG, int NTHREADS>
+__device__ __forceinline__ void cluster_merge_ws(const DecodeParams& p) {
   constexpr int Q4 = D / 4, SMAX = 16;  // the largest cluster
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
   const int S = p.cluster;
@@ -680,9 +688,8 @@ __device__ __forceinline__ void cluster_merge_ws(const Par& p) {
         acc.x += w * o[s].x; acc.y += w * o[s].y; acc.z += w * o[s].z; acc.w += w * o[s].w;
       }
     }
-    const float inv = row_factor(p, lsum);
+    const float inv = lsum > 0.f ? p.out_scale / lsum : 0.f;
     const int i = r / p.G, hl = r % p.G;
-    if (Par::kScored && c4 == 0) store_row_sum(p, b, q0, i, (kh + hh) * p.G + hl, M, lsum);
     uint32_t* dst = reinterpret_cast<uint32_t*>(reinterpret_cast<uint16_t*>(p.out) +
                     (static_cast<long long>(q0 + i) * p.Hq + (kh + hh) * p.G + hl) * D + 4 * c4);
     if (p.out_bf16) {
@@ -695,13 +702,12 @@ __device__ __forceinline__ void cluster_merge_ws(const Par& p) {
   }
 }
 
-template <class Cfg, class Par = DecodeParams>
+template <class Cfg>
 __global__ void __launch_bounds__(Cfg::kThreads, Cfg::kMinBlocks)
     decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
-                        const __grid_constant__ CUtensorMap tm_v, const Par p) {
+                        const __grid_constant__ CUtensorMap tm_v, const DecodeParams p) {
   constexpr int D = Cfg::D, KG = Cfg::KG, NS = Cfg::NS;
   constexpr bool FP8 = Cfg::FP8, BF16 = Cfg::BF16;
-  constexpr bool SC = Par::kScored;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -752,7 +758,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::kMinBlocks)
         // Validated where it is used, so the load stays in flight meanwhile.
         int blk = 0;
         if (t + lane < pc.ntiles) {
-          const int tile = piece_tile(p, pc, t + lane);
+          const int tile = pc.first_tile + t + lane;
           blk = __ldg(row + tile / p.tiles_per_block);
         }
         return blk;
@@ -779,7 +785,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::kMinBlocks)
           // lanes 0..kSlabs-1 load the K slabs, the next kSlabs lanes the V
           // slabs; one box covers 16 keys x HG heads x 128 bytes
           if (lane < 2 * Cfg::kSlabs) {
-            const int tile = piece_tile(p, pc, t + i);
+            const int tile = pc.first_tile + t + i;
             const int z = blk * p.block_size + (tile % p.tiles_per_block) * kTileKeys;
             const int sl = lane % Cfg::kSlabs;
             const bool is_v = lane >= Cfg::kSlabs;
@@ -818,13 +824,6 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::kMinBlocks)
   constexpr int KSTEPS = D / 16;
   constexpr int KSW = KSTEPS / DS;             // k-steps of this warp's part of D
   constexpr int MTW = D / 16 / DS;             // m-tiles (16 output dims) of this warp
-  // Scored: P as the sum of two operands, the rounded value and the rounded rest,
-  // where one rounding would show beside the output's own (error against 64 bits,
-  // relative to the output's norm: fp16 3.2e-4 with one, 2.1e-4 with two, bfloat16
-  // 2.5e-3 and 1.7e-3; a bfloat16 output over fp16 operands hides it).
-  constexpr int PP = SC && !Cfg::kQScale ? 2 : 1;
-  // Weights up to 2^14 where P is fp16, so that its last bit is 2^-38 of the peak's weight.
-  constexpr float kShift = SC && !BF16 ? 14.f : 0.f;
   float* xchg = reinterpret_cast<float*>(smem + Cfg::kOffXchg);
   uint32_t qf[KSW][NTW][2];
   float o[MTW][NTW][4];
@@ -931,9 +930,6 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::kMinBlocks)
       }
     }
     int lo_r[NTW][2], hi_r[NTW][2];
-    int pre_r[SC ? NTW : 1][2];          // scored: the prefix's keys, 0 for a row that sees nothing
-    float slope_r[SC ? NTW : 1][2];      // scored: slope * log2(e)
-    int pos_r[SC ? NTW : 1][2];          // scored: the row's position
     float m_r[NTW][2], l_r[NTW][2];
 #pragma unroll
     for (int n = 0; n < NTW; ++n) {
@@ -944,16 +940,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::kMinBlocks)
           const int pos = pc.L - pc.qlen + r / p.G;
           hi_r[n][c] = pos;
           lo_r[n][c] = (p.window > 0) ? max(0, pos - p.window + 1) : 0;
-          if constexpr (SC) {
-            pre_r[n][c] = pos >= 0 ? pc.prefix : 0;
-            pos_r[n][c] = pos;
-            slope_r[n][c] = p.slopes ? __ldg(p.slopes + (pc.kh + th) * p.G + r % p.G) * kLog2e : 0.f;
-          }
         } else {
-          if constexpr (SC) {
-            pre_r[n][c] = pos_r[n][c] = 0;
-            slope_r[n][c] = 0.f;
-          }
           hi_r[n][c] = -1;
           lo_r[n][c] = 0;
         }
@@ -982,7 +969,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::kMinBlocks)
       }
       const uint32_t kb = smem_u32(smem + stage * Cfg::kStageBytes);
       const uint32_t vb = kb + Cfg::kTileBytes;
-      const int key0 = piece_tile(p, pc, k) * kTileKeys;
+      const int key0 = (pc.first_tile + k) * kTileKeys;
 
       // S^T = K Q^T over this warp's part of D (16 keys x 8 rows per row tile)
       float sa[NTW][4], sb[NTW][4];
@@ -1072,55 +1059,25 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::kMinBlocks)
       // per row tile: mask, online softmax, P^T fragments; C layout of S^T:
       // [0]=(key g,row 2t4) [1]=(key g,row 2t4+1) [2]=(key g+8,row 2t4) [3]=(key g+8,row 2t4+1)
       uint32_t pb0[NTW], pb1[NTW];
-      uint32_t pl0[PP == 2 ? NTW : 1], pl1[PP == 2 ? NTW : 1];    // the rest of P's rounding
-      uint32_t see0[SC ? NTW : 1], see1[SC ? NTW : 1];            // edge tiles: 1 where the row sees the key
       float al[NTW][2];
       bool rescale = false;
       // a tile every real row sees in full needs no per-key mask
-      const bool interior = (key0 >= pc.tile_lo_all && key0 + kTileKeys - 1 <= pc.tile_hi_all) ||
-                            (SC && key0 + kTileKeys <= pc.prefix && pc.tile_hi_all >= 0);
+      const bool interior = key0 >= pc.tile_lo_all && key0 + kTileKeys - 1 <= pc.tile_hi_all;
 #pragma unroll
       for (int n = 0; n < NTW; ++n) {
         const int j0 = key0 + g, j1 = j0 + 8;
         float x[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] = sc[n][e] * sl2r[n][e & 1];
-        if constexpr (SC) {
-          if (p.cap_out > 0.f) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) x[e] = p.cap_out * tanh_f32(x[e] * p.cap_u);
-          }
-          if (p.slopes != nullptr) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              x[e] -= slope_r[n][e & 1] * static_cast<float>(abs((e < 2 ? j0 : j1) - pos_r[n][e & 1]));
-          }
-        }
         if (interior) {
           // padded rows (hi = -1) stay masked
-#pragma unroll
-          for (int e = 0; e < 4; ++e) x[e] = hi_r[n][e & 1] >= 0 ? x[e] : -INFINITY;
+          x[0] = hi_r[n][0] >= 0 ? sc[n][0] * sl2r[n][0] : -INFINITY;
+          x[1] = hi_r[n][1] >= 0 ? sc[n][1] * sl2r[n][1] : -INFINITY;
+          x[2] = hi_r[n][0] >= 0 ? sc[n][2] * sl2r[n][0] : -INFINITY;
+          x[3] = hi_r[n][1] >= 0 ? sc[n][3] * sl2r[n][1] : -INFINITY;
         } else {
-          bool see[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int j = e < 2 ? j0 : j1;
-            see[e] = j >= lo_r[n][e & 1] && j <= hi_r[n][e & 1];
-            if constexpr (SC) see[e] = see[e] || j < pre_r[n][e & 1];
-            x[e] = see[e] ? x[e] : -INFINITY;
-          }
-          if constexpr (SC) {
-            see0[n] = movmatrix_trans(pack2<BF16>(see[0] ? 1.f : 0.f, see[1] ? 1.f : 0.f));
-            see1[n] = movmatrix_trans(pack2<BF16>(see[2] ? 1.f : 0.f, see[3] ? 1.f : 0.f));
-          }
-        }
-        if constexpr (SC) {
-          if (p.scores != nullptr && dh == 0) {  // [key][row] of this tile and row tile
-            float* dst = p.scores + ((static_cast<long long>(pc.b) * p.Hkv + pc.kh + th) * p.max_blocks *
-                                         p.tiles_per_block + key0 / kTileKeys) * (Cfg::NT * 128) + (rg * NTW + n) * 128;
-            __stcg(reinterpret_cast<float2*>(dst + g * 8 + 2 * t4), make_float2(x[0], x[1]));
-            __stcg(reinterpret_cast<float2*>(dst + (g + 8) * 8 + 2 * t4), make_float2(x[2], x[3]));
-          }
+          x[0] = (j0 >= lo_r[n][0] && j0 <= hi_r[n][0]) ? sc[n][0] * sl2r[n][0] : -INFINITY;
+          x[1] = (j0 >= lo_r[n][1] && j0 <= hi_r[n][1]) ? sc[n][1] * sl2r[n][1] : -INFINITY;
+          x[2] = (j1 >= lo_r[n][0] && j1 <= hi_r[n][0]) ? sc[n][2] * sl2r[n][0] : -INFINITY;
+          x[3] = (j1 >= lo_r[n][1] && j1 <= hi_r[n][1]) ? sc[n][3] * sl2r[n][1] : -INFINITY;
         }
         float mx0 = fmaxf(x[0], x[2]), mx1 = fmaxf(x[1], x[3]);
 #pragma unroll
@@ -1129,11 +1086,11 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::kMinBlocks)
           mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, off));
         }
         const float mn0 = fmaxf(m_r[n][0], mx0), mn1 = fmaxf(m_r[n][1], mx1);
-        const float base0 = (mn0 == -INFINITY) ? 0.f : mn0 - kShift;
-        const float base1 = (mn1 == -INFINITY) ? 0.f : mn1 - kShift;
+        const float base0 = (mn0 == -INFINITY) ? 0.f : mn0;
+        const float base1 = (mn1 == -INFINITY) ? 0.f : mn1;
         // nothing accumulated yet (m = -inf): O and l are zero, keep factor 1
-        al[n][0] = (m_r[n][0] == -INFINITY) ? 1.f : ex2(m_r[n][0] - kShift - base0);
-        al[n][1] = (m_r[n][1] == -INFINITY) ? 1.f : ex2(m_r[n][1] - kShift - base1);
+        al[n][0] = (m_r[n][0] == -INFINITY) ? 1.f : ex2(m_r[n][0] - base0);
+        al[n][1] = (m_r[n][1] == -INFINITY) ? 1.f : ex2(m_r[n][1] - base1);
         const float p00 = ex2(x[0] - base0), p01 = ex2(x[1] - base1);
         const float p10 = ex2(x[2] - base0), p11 = ex2(x[3] - base1);
         m_r[n][0] = mn0;
@@ -1141,14 +1098,8 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::kMinBlocks)
         l_r[n][0] = l_r[n][0] * al[n][0] + (p00 + p10);
         l_r[n][1] = l_r[n][1] * al[n][1] + (p01 + p11);
         rescale |= (al[n][0] != 1.f || al[n][1] != 1.f);
-        const uint32_t w0 = pack2<BF16>(p00, p01), w1 = pack2<BF16>(p10, p11);
-        pb0[n] = movmatrix_trans(w0);
-        pb1[n] = movmatrix_trans(w1);
-        if constexpr (PP == 2) {
-          const float2 h0 = unpack2<BF16>(w0), h1 = unpack2<BF16>(w1);
-          pl0[n] = movmatrix_trans(pack2<BF16>(p00 - h0.x, p01 - h0.y));
-          pl1[n] = movmatrix_trans(pack2<BF16>(p10 - h1.x, p11 - h1.y));
-        }
+        pb0[n] = movmatrix_trans(pack2<BF16>(p00, p01));
+        pb1[n] = movmatrix_trans(pack2<BF16>(p10, p11));
       }
       if (__any_sync(0xffffffffu, rescale)) {
 #pragma unroll
@@ -1164,39 +1115,6 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::kMinBlocks)
       // end (the unwritten tail of its last block) may hold any bits, NaN
       // included: their V is zeroed so that P = 0 there never meets 0 * NaN.
       const bool tail = key0 + kTileKeys > pc.L;
-      auto pv = [&](int mtl, uint32_t (&a)[4]) {
-        if constexpr (SC && Cfg::KV != kKvInt8) {
-          // Rows that do not see a key of this tile have a zero weight for it, which
-          // times a NaN or an infinity of its V is NaN: such elements are taken out, and
-          // a product of ones (the element's place, the rows that see the key) marks
-          // the outputs that they belong to.
-          if (!interior) {
-            uint32_t odd[4], any = 0;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) any |= odd[i] = not_finite_16<BF16>(a[i]);
-            if (__any_sync(0xffffffffu, any != 0)) {
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                a[i] &= ~odd[i];
-                odd[i] &= BF16 ? 0x3f803f80u : 0x3c003c00u;
-              }
-#pragma unroll
-              for (int n = 0; n < NTW; ++n) {
-                float mark[4] = {0.f, 0.f, 0.f, 0.f};
-                mma_op<BF16>(mark, odd, see0[n], see1[n]);
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                  if (mark[e] > 0.f) o[mtl][n][e] = __uint_as_float(0x7fffffffu);
-              }
-            }
-          }
-        }
-#pragma unroll
-        for (int n = 0; n < NTW; ++n) {
-          mma_op<BF16>(o[mtl][n], a, pb0[n], pb1[n]);
-          if constexpr (PP == 2) mma_op<BF16>(o[mtl][n], a, pl0[n], pl1[n]);
-        }
-      };
       if constexpr (!FP8) {
         const int key = (lane & 7) + (lane >> 4) * 8;
         const int srow = key * HG + th;
@@ -1217,7 +1135,8 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::kMinBlocks)
           if (tail) {
             a[0] &= vm01; a[1] &= vm01; a[2] &= vm23; a[3] &= vm23;
           }
-          pv(mtl, a);
+#pragma unroll
+          for (int n = 0; n < NTW; ++n) mma_op<BF16>(o[mtl][n], a, pb0[n], pb1[n]);
         }
       } else {
         // 32-dim group P32: lane reads 4 codes at dims 32*P32 + 4g .. +3 of keys
@@ -1252,12 +1171,14 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::kMinBlocks)
           a[1] = byte_pair_to_half2<Cfg::KV>(ab01, true);
           a[2] = byte_pair_to_half2<Cfg::KV>(cd01, false);
           a[3] = byte_pair_to_half2<Cfg::KV>(cd01, true);
-          pv(2 * pl, a);
+#pragma unroll
+          for (int n = 0; n < NTW; ++n) mma_op<BF16>(o[2 * pl][n], a, pb0[n], pb1[n]);
           a[0] = byte_pair_to_half2<Cfg::KV>(ab23, false);
           a[1] = byte_pair_to_half2<Cfg::KV>(ab23, true);
           a[2] = byte_pair_to_half2<Cfg::KV>(cd23, false);
           a[3] = byte_pair_to_half2<Cfg::KV>(cd23, true);
-          pv(2 * pl + 1, a);
+#pragma unroll
+          for (int n = 0; n < NTW; ++n) mma_op<BF16>(o[2 * pl + 1][n], a, pb0[n], pb1[n]);
         }
       }
       __syncwarp();
@@ -1273,16 +1194,6 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::kMinBlocks)
         l_r[n][0] += __shfl_xor_sync(0xffffffffu, l_r[n][0], off);
         l_r[n][1] += __shfl_xor_sync(0xffffffffu, l_r[n][1], off);
       }
-    if constexpr (SC) {  // what the weights are relative to
-#pragma unroll
-      for (int n = 0; n < NTW; ++n) {
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          if (l_r[n][c] != l_r[n][c] && m_r[n][c] == -INFINITY) m_r[n][c] = 0.f;  // nothing but NaN: not an empty row
-          m_r[n][c] -= kShift;
-        }
-      }
-    }
     const int tid = threadIdx.x;
     const bool direct = pc.npieces == 1;
     constexpr int NT = Cfg::NT, RH = NT * 8;  // partial rows per head of a unit
@@ -1372,8 +1283,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::kMinBlocks)
         if (direct) {
           const int i = r / p.G, hl = r % p.G;
           __half* dst = p.out + (static_cast<long long>(pc.q0 + i) * p.Hq + (pc.kh + hh) * p.G + hl) * D + dc * 8;
-          const float inv = row_factor(p, Ls);
-          if (SC && dc == 0) store_row_sum(p, pc.b, pc.q0, i, (pc.kh + hh) * p.G + hl, M, Ls);
+          const float inv = (Ls > 0.f) ? p.out_scale / Ls : 0.f;
           uint4 v;
           v.x = pack2<Cfg::QB>(v0.x * inv, v0.y * inv);
           v.y = pack2<Cfg::QB>(v0.z * inv, v0.w * inv);
@@ -1401,9 +1311,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::kMinBlocks)
           if (direct) {
             const int i = r / p.G, hl = r % p.G;
             __half* dst = p.out + (static_cast<long long>(pc.q0 + i) * p.Hq + (pc.kh + th) * p.G + hl) * D;
-            const float inv = row_factor(p, Ls);
-            if (SC && g == 0 && dh == 0)
-              store_row_sum(p, pc.b, pc.q0, i, (pc.kh + th) * p.G + hl, m_r[n][c], Ls);
+            const float inv = (Ls > 0.f) ? p.out_scale / Ls : 0.f;
 #pragma unroll
             for (int mtl = 0; mtl < MTW; ++mtl) {
               const int mt = dh * MTW + mtl;

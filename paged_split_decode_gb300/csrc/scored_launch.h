@@ -3,6 +3,7 @@
 // 4-bit caches' (decode_fp4.cu).
 #pragma once
 #include "decode_fp4.cuh"
+#include "decode_scored.cuh"
 #include "launch.h"
 
 namespace pd {
@@ -29,40 +30,59 @@ struct KeyWeightParams {
 };
 cudaError_t launch_key_weights(KeyWeightParams p, int sms, cudaStream_t stream);
 
+// The deepest ring (at most 32 stages, a multiple of the key groups' steps) that lets MINB CTAs share an SM.
+template <int D, int KV, int NT, int HG, int W, int KG, int KT, int MINB, int NS = 32>
+constexpr int scored_stages() {
+  constexpr int unit = KG > 1 ? KG * KT : 1;
+  if constexpr (NS <= unit || NS <= 2)
+    return unit > 2 ? unit : 2;
+  else if constexpr (NS % unit != 0)
+    return scored_stages<D, KV, NT, HG, W, KG, KT, MINB, NS - 1>();
+  else if constexpr (ScoredCfg<D, KV, NT, HG, W, KG, KT, NS, MINB>::kSmemBytes <= smem_limit(MINB))
+    return NS;
+  else
+    return scored_stages<D, KV, NT, HG, W, KG, KT, MINB, NS - 1>();
+}
+template <int D, int KV, int NT, int HG, int W, int KG, int KT, int MINB>
+using ScoredCfgFor = ScoredCfg<D, KV, NT, HG, W, KG, KT, scored_stages<D, KV, NT, HG, W, KG, KT, MINB>(), MINB>;
+
+#ifndef PD_V_C1H
+#define PD_V_C1H 4, 1, 1, 1, 1
+#endif
 template <int D, int KV>
 struct ScoredShapes {
   static constexpr bool kByte = cache_kind(KV) == kKvFp8 || cache_kind(KV) == kKvInt8;
-  // The plain decode's shapes (row tiles, key groups, CTAs per SM, parts of D, heads per tile,
-  // row groups). Byte caches with nine and more rows per KV head run here on mma.sync too.
-  using C1 = CfgFor<D, KV, 1, 2, 2>;
-  using C2 = CfgFor<D, KV, 2, 1, 2, 1, 1, 2>;
-  using C3 = CfgFor<D, KV, 3, 1, 2, 1, 1, 3>;
-  using C4 = CfgFor<D, KV, 4, 1, 2, 1, 1, 4>;
-  using C1H = CfgFor<D, KV, 1, 1, 1, (D == 256) == kByte ? 1 : 2, (D == 256 && !kByte) ? 2 : 4>;
+  // row tiles, heads per tile, warps per head, key groups, tiles per step, CTAs per SM
+  using C1H = ScoredCfgFor<D, KV, 1, PD_V_C1H>;
+  using C1 = ScoredCfgFor<D, KV, 1, 1, 1, 3, 1, 2>;
+  using C2 = ScoredCfgFor<D, KV, 2, 1, 2, 4, 1, 1>;
+  using C3 = ScoredCfgFor<D, KV, 3, 1, 4, 2, 1, 1>;
+  using C4 = ScoredCfgFor<D, KV, 4, 1, 4, 2, 1, 1>;
 
   template <class C>
   static bool shape_one(KernelShape* out) {
+    static_assert(C::kSmemBytes <= smem_limit(C::kMinBlocks), "the ring fits");
     out->threads = C::kThreads;
     out->smem_bytes = C::kSmemBytes;
     out->rows_padded = C::RP;
     out->ctas_per_sm = C::kMinBlocks;
     out->heads = C::HG;
-    out->unit_cost = 4;
+    out->step_tiles = C::KG * C::KT;
+    out->key_groups = C::KG;
+    out->whole_tile = 1;
+    out->unit_cost = C::KG > 1 ? 12 : 4;
     out->fixed_pieces = 0;
-    static unsigned long long ctx_done[64] = {};
-    static int cache[64][kMaxCluster + 1] = {};
-    max_active_clusters(decode_paged_kernel<C, ScoredParams>, C::kThreads, C::kSmemBytes, ctx_done, cache,
-                        out->max_clusters);
+    for (int& c : out->max_clusters) c = 0;  // split units go through the combine
     return true;
   }
   template <class C>
   static cudaError_t launch_one(const CUtensorMap& tk, const CUtensorMap& tv, const ScoredParams& p, int grid,
                                 cudaStream_t s) {
     static unsigned long long attr_ctx[64] = {};
-    const cudaError_t e = once_per_context(
-        attr_ctx, [] { return set_kernel_attributes(decode_paged_kernel<C, ScoredParams>, C::kSmemBytes); });
+    const cudaError_t e =
+        once_per_context(attr_ctx, [] { return set_kernel_attributes(decode_scored_kernel<C>, C::kSmemBytes); });
     if (e != cudaSuccess) return e;
-    return launch_pdl(decode_paged_kernel<C, ScoredParams>, grid, C::kThreads, C::kSmemBytes, s, p.cluster, tk, tv, p);
+    return launch_pdl(decode_scored_kernel<C>, grid, C::kThreads, C::kSmemBytes, s, 1, tk, tv, p);
   }
   static bool shape(int nt, int grouped, KernelShape* out) {
     if (grouped) return nt == 1 && shape_one<C1H>(out);
