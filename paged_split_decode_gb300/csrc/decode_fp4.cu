@@ -8,7 +8,7 @@ namespace {
 // a step, steps in the ring, CTAs per SM.
 template <int D, bool QB>
 struct Shapes {
-  using C1 = std::conditional_t<D == 256, Fp4Cfg<256, 1, 1, 8, 1, 2, 2, QB>, Fp4Cfg<128, 1, 1, 8, 2, 2, 2, QB>>;
+  using C1 = std::conditional_t<D == 256, Fp4Cfg<256, 1, 1, 4, 1, 2, 4, QB>, Fp4Cfg<128, 1, 1, 4, 1, 3, 5, QB>>;
   using C2 = std::conditional_t<D == 256, Fp4Cfg<256, 2, 1, 8, 1, 4, 1, QB>, Fp4Cfg<128, 2, 1, 6, 1, 6, 2, QB>>;
   using C4 = std::conditional_t<D == 256, Fp4Cfg<256, 2, 2, 4, 1, 4, 1, QB>, Fp4Cfg<128, 2, 2, 3, 1, 6, 2, QB>>;
 

@@ -64,7 +64,8 @@ struct Fp4Cfg {
   static constexpr int kOffQ = kWarps * kRing;            // q fragments
   static constexpr int kQ = RG * NT * MT * 32 * 8;
   static constexpr int kOffML = kOffQ + kQ;               // [warp][NT * 8] (m, l)
-  static constexpr int kOffPre = kOffML + kWarps * NT * 8 * 8;
+  static constexpr int kOffFactor = kOffML + kWarps * NT * 8 * 8;  // rows' score factors
+  static constexpr int kOffPre = kOffFactor + RP * 4;
   static constexpr int kSmemBytes = kOffPre + (kMaxAutoB + 1) * 4 + 12;
 };
 
@@ -98,12 +99,170 @@ __device__ __forceinline__ uint16_t lds_u16(uint32_t a) {
   return v;
 }
 
+// O^T += V^T P^T for a tile of 16 keys from `key0` on, whose codes lie at vt as the copies left them and whose
+// scales at sf: P operands pb[n] of NT row tiles (the query rows from row0 on), and with PP = 2 what their rounding left,
+// pl[n]. EDGE: not every row sees all of its keys.
+template <int D, int NT, int PP, bool EDGE>
+__device__ __forceinline__ void fp4_pv(const ScoredParams& p, const Piece& pc, int row0, uint32_t vt, uint32_t sf, int lane,
+                                       int key0, int seq_len, const uint32_t (&pb)[NT][2], const uint32_t (&pl)[NT][2],
+                                       float (&o)[D / 16][NT][4]) {
+  const int g = lane >> 2, t4 = lane & 3;
+  constexpr int NG = D / 128;  // groups of 16 dims that a lane holds
+  constexpr int NWD = D / 64;  // words of a key that a lane holds
+  // scales of keys (2 t4, 2 t4 + 1) and (2 t4 + 8, 2 t4 + 9) for groups NG g ..
+  uint32_t f01[NG], f89[NG], w[4][NWD];
+  if constexpr (NG == 2) {
+    const uint32_t at = sf + 2 * t4 * 16 + 2 * g;
+    const uint32_t a = e4m3x2_to_half2(lds_u16(at)), b = e4m3x2_to_half2(lds_u16(at + 16)),
+                   c = e4m3x2_to_half2(lds_u16(at + 128)), d = e4m3x2_to_half2(lds_u16(at + 144));
+    f01[0] = prmt(a, b, 0x5410u); f01[1] = prmt(a, b, 0x7632u);
+    f89[0] = prmt(c, d, 0x5410u); f89[1] = prmt(c, d, 0x7632u);
+  #pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const uint4 v = lds_v4(vt + q * 512 + lane * 16);
+      w[q][0] = v.x; w[q][1] = v.y; w[q][2] = v.z; w[q][3] = v.w;
+    }
+  } else {
+    // rows of 8 scales: a byte for this lane's group of each key
+    const uint32_t at = sf + 2 * t4 * 8 + (g & ~1);
+    const uint32_t a = lds_u16(at), b = lds_u16(at + 8), c = lds_u16(at + 64), d = lds_u16(at + 72);
+    const uint32_t sel = (g & 1) ? 0x0051u : 0x0040u;
+    f01[0] = e4m3x2_to_half2(static_cast<uint16_t>(prmt(a, b, sel)));
+    f89[0] = e4m3x2_to_half2(static_cast<uint16_t>(prmt(c, d, sel)));
+  #pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      // key 2 t4 + (q & 1) + 8 (q >> 1): line t4 + 4 (q >> 1)
+      const uint32_t at_v = vt + t4 * 128 + (((g >> 1) ^ (2 * t4)) << 4) + (g & 1) * 8;
+      const uint2 v = lds_v2((at_v ^ ((q & 1) * 64)) + (q >> 1) * 512);
+      w[q][0] = v.x; w[q][1] = v.y;
+    }
+  }
+  // Keys at or past the sequence's end may hold any bits: a scale of NaN must not meet a
+  // weight of zero. Nor must one of a key that only some rows see: it is taken out, and a
+  // product of ones marks the outputs of the rows that see it.
+  if constexpr (EDGE) {
+    const int ka = key0 + 2 * t4;
+    const uint32_t in01 = (ka < seq_len ? 0x0000ffffu : 0u) | (ka + 1 < seq_len ? 0xffff0000u : 0u);
+    const uint32_t in89 = (ka + 8 < seq_len ? 0x0000ffffu : 0u) | (ka + 9 < seq_len ? 0xffff0000u : 0u);
+  #pragma unroll
+    for (int gr = 0; gr < NG; ++gr) {
+      f01[gr] &= in01;
+      f89[gr] &= in89;
+      const uint32_t o01 = not_finite_16<false>(f01[gr]), o89 = not_finite_16<false>(f89[gr]);
+      if (__any_sync(0xffffffffu, (o01 | o89) != 0)) {
+        f01[gr] &= ~o01;
+        f89[gr] &= ~o89;
+        const uint32_t a[4] = {o01 & 0x3c003c00u, o01 & 0x3c003c00u, o89 & 0x3c003c00u, o89 & 0x3c003c00u};
+  #pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          const int r = row0 + n * 8 + g;
+          const uint32_t see0 = (row_sees(p, pc, r, ka) ? 0x3c00u : 0u) | (row_sees(p, pc, r, ka + 1) ? 0x3c000000u : 0u);
+          const uint32_t see1 = (row_sees(p, pc, r, ka + 8) ? 0x3c00u : 0u) | (row_sees(p, pc, r, ka + 9) ? 0x3c000000u : 0u);
+          float mark[4] = {0.f, 0.f, 0.f, 0.f};
+          mma_16816(mark, a, see0, see1);
+  #pragma unroll
+          for (int mt = 0; mt < 8; ++mt)
+  #pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (mark[e] > 0.f) o[gr * 8 + mt][n][e] = __uint_as_float(0x7fffffffu);
+        }
+      }
+    }
+  }
+  #pragma unroll
+  for (int q = 0; q < NWD; ++q) {  // a word: 8 dims, four m-tiles
+    constexpr uint32_t M = 0x0f0f0f0fu;
+    const uint32_t e01 = (w[0][q] & M) | ((w[1][q] << 4) & ~M), d01 = ((w[0][q] >> 4) & M) | (w[1][q] & ~M);
+    const uint32_t e89 = (w[2][q] & M) | ((w[3][q] << 4) & ~M), d89 = ((w[2][q] >> 4) & M) | (w[3][q] & ~M);
+    uint32_t he[4], hd[4], je[4], jd[4];
+    e2m1x8_to_half2(e01, he);
+    e2m1x8_to_half2(d01, hd);
+    e2m1x8_to_half2(e89, je);
+    e2m1x8_to_half2(d89, jd);
+    const uint32_t s01 = f01[q / 2], s89 = f89[q / 2];
+  #pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      const uint32_t a[4] = {hmul2_u(he[b], s01), hmul2_u(hd[b], s01), hmul2_u(je[b], s89), hmul2_u(jd[b], s89)};
+  #pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        mma_16816(o[4 * q + b][n], a, pb[n][0], pb[n][1]);
+        if constexpr (PP == 2) mma_16816(o[4 * q + b][n], a, pl[n][0], pl[n][1]);
+      }
+    }
+  }
+}
+
+// Dims d and d + 1 of row r of a piece, whose weights are relative to ml.x and add up to ml.y: the
+// unit's output, or the piece's partial.
+template <class Cfg>
+__device__ __forceinline__ void fp4_store(const ScoredParams& p, const Piece& pc, int r, int d, float v0, float v1, float2 ml,
+                                          bool direct) {
+  if (direct) {
+    const int q = r / p.G, head = pc.kh * p.G + r % p.G;
+    const float inv = row_factor(p, ml.y);
+    *reinterpret_cast<uint32_t*>(reinterpret_cast<uint16_t*>(p.out) +
+                                 (static_cast<long long>(pc.q0 + q) * p.Hq + head) * Cfg::D + d) =
+        Cfg::QB ? pack_bf162(v0 * inv, v1 * inv) : pack_half2(v0 * inv, v1 * inv);
+    if (d == 0) store_row_sum(p, pc.b, pc.q0, q, head, ml.x, ml.y);
+  } else {
+    const long long prow = static_cast<long long>(pc.slot) * Cfg::RP + r;
+    __stcg(reinterpret_cast<float2*>(p.ws_o + prow * Cfg::D + d), make_float2(v0, v1));
+    if (d == 0) __stcg(reinterpret_cast<float2*>(p.ws_ml + prow * 2), ml);
+  }
+}
+
+// The warps' accumulator fragments, (n MT + mt) kPitch + lane in each warp's ring, and (m, l) joined into the piece's
+// output or partial. Warp k RG + rw: key group k, row group rw of NT row tiles.
+template <class Cfg, int D, int NT, int RG, int KG, int THREADS>
+__device__ __forceinline__ void fp4_join(const ScoredParams& p, const Piece& pc, const uint8_t* rings, const float2* s_ml) {
+  constexpr int MT = D / 16;
+  static_assert(THREADS % (4 * MT) == 0, "a thread's fragments of a row tile are of the same two rows");
+  const bool direct = pc.npieces == 1;
+#pragma unroll 1
+  for (int tile = 0; tile < RG * NT; ++tile) {
+    const int rw = tile / NT, n = tile % NT, r0 = tile * 8 + 2 * (threadIdx.x / MT % 4);
+    if (r0 >= pc.R) continue;
+    // the key groups' factors and the rows' (m, l)
+    float f[KG][2];
+    float2 row[2];
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      float2 ml[KG];
+      float M = -INFINITY, L = 0.f;
+#pragma unroll
+      for (int k = 0; k < KG; ++k) {
+        ml[k] = s_ml[(k * RG + rw) * NT * 8 + n * 8 + 2 * (threadIdx.x / MT % 4) + c];
+        M = fmaxf(M, ml[k].x);
+      }
+#pragma unroll
+      for (int k = 0; k < KG; ++k) {
+        f[k][c] = ml[k].x == -INFINITY ? 0.f : ex2(ml[k].x - M);
+        L += f[k][c] * ml[k].y;
+      }
+      row[c] = make_float2(M, L);
+    }
+    for (int item = threadIdx.x; item < MT * 32; item += THREADS) {  // two dims of two rows: an accumulator fragment
+      const int mt = item % MT, ln = item / MT;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int k = 0; k < KG; ++k) {
+        const float4 v = reinterpret_cast<const float4*>(rings + (k * RG + rw) * Cfg::kRing)[(n * MT + mt) * Cfg::kPitch + ln];
+        acc.x += f[k][0] * v.x; acc.y += f[k][1] * v.y; acc.z += f[k][0] * v.z; acc.w += f[k][1] * v.w;
+      }
+      const int d = D / 8 * (ln >> 2) + 2 * mt;  // dims d, d + 1 of rows r0, r0 + 1
+      fp4_store<Cfg>(p, pc, r0, d, acc.x, acc.z, row[0], direct);
+      if (r0 + 1 < pc.R) fp4_store<Cfg>(p, pc, r0 + 1, d, acc.y, acc.w, row[1], direct);
+    }
+  }
+}
+
 template <class Cfg>
 __global__ void __launch_bounds__(Cfg::kThreads, Cfg::kMinBlocks) decode_fp4_kernel(const Fp4Params p) {
   constexpr int D = Cfg::D, NT = Cfg::NT, RG = Cfg::RG, KG = Cfg::KG, KT = Cfg::KT, ST = Cfg::ST, MT = Cfg::MT;
   constexpr int PP = Cfg::PP;
   extern __shared__ __align__(128) uint8_t smem[];
   float2* s_ml = reinterpret_cast<float2*>(smem + Cfg::kOffML);
+  float* s_factor = reinterpret_cast<float*>(smem + Cfg::kOffFactor);
   int* s_pre = reinterpret_cast<int*>(smem + Cfg::kOffPre);
   const int warp = warp_uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   const int rg = warp % RG, kg = warp / RG;
@@ -197,6 +356,22 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::kMinBlocks) decode_fp4_ker
       ++next;
       fill = fill == ring + (ST - 1) * Cfg::kStage ? ring : fill + Cfg::kStage;
     };
+    // q rows are loaded while the table's entries come
+    uint2 qv[NT][MT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const int r = (rg * NT + n) * 8 + g;
+      const uint32_t* qrow = nullptr;
+      if (kg == 0 && r < pc.R && ntiles > 0)
+        qrow = reinterpret_cast<const uint32_t*>(
+            p.q + (static_cast<long long>(pc.q0 + r / p.G) * p.Hq + kh * p.G + r % p.G) * D);
+#pragma unroll
+      for (int ks = 0; ks < MT; ++ks) {
+        // chunk of 32 dims (t4, then t4 + 4), four dims of it a k-step
+        const int d = D == 256 ? (ks >> 3) * 128 + 32 * t4 + (ks & 7) * 4 : 32 * t4 + ks * 4;
+        qv[n][ks] = qrow ? __ldg(reinterpret_cast<const uint2*>(qrow + d / 2)) : make_uint2(0u, 0u);
+      }
+    }
 #pragma unroll
     for (int i = 0; i < ST - 1; ++i) issue();
 
@@ -206,49 +381,35 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::kMinBlocks) decode_fp4_ker
     int hi_r[NT][2];          // last causal key of rows 2 t4, 2 t4 + 1 of a row tile (padded rows: -1)
     float m_r[NT][2], l_r[NT][2];
     float o[MT][NT][4];
+    if (kg == 0) {  // (the key groups share the row group's)
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const int r = (rg * NT + n) * 8 + g;
-      const uint32_t* qrow = nullptr;
-      if (r < pc.R && ntiles > 0) {
-        const int i = r / p.G, hl = r % p.G;
-        qrow = reinterpret_cast<const uint32_t*>(
-            p.q + (static_cast<long long>(pc.q0 + i) * p.Hq + kh * p.G + hl) * D);
-      }
-      uint32_t f[MT][2];
+      for (int n = 0; n < NT; ++n) {
+        if constexpr (Cfg::QB) {
+          float m = 0.f;
 #pragma unroll
-      for (int ks = 0; ks < MT; ++ks) {
-        // chunk of 32 dims (t4, then t4 + 4), four dims of it a k-step
-        const int d = D == 256 ? (ks >> 3) * 128 + 32 * t4 + (ks & 7) * 4 : 32 * t4 + ks * 4;
-        const uint2 v = qrow ? __ldg(reinterpret_cast<const uint2*>(qrow + d / 2)) : make_uint2(0u, 0u);
-        f[ks][0] = v.x;
-        f[ks][1] = v.y;
-      }
-      sl2r[n][0] = sl2r[n][1] = p.sl2;
-      if constexpr (Cfg::QB) {
-        float m = 0.f;
+          for (int ks = 0; ks < MT; ++ks)
+            m = fmaxf(m, fmaxf(fmaxf(fabsf(__uint_as_float(qv[n][ks].x << 16)), fabsf(__uint_as_float(qv[n][ks].x & 0xffff0000u))),
+                               fmaxf(fabsf(__uint_as_float(qv[n][ks].y << 16)), fabsf(__uint_as_float(qv[n][ks].y & 0xffff0000u)))));
+          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+          const int eq = q_row_exponent(m);
+          const float up = pow2f(eq);
+          if (t4 == 0) s_factor[(rg * NT + n) * 8 + g] = p.sl2 * pow2f(-eq);
 #pragma unroll
-        for (int ks = 0; ks < MT; ++ks)
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-            m = fmaxf(m, fmaxf(fabsf(__uint_as_float(f[ks][h] << 16)), fabsf(__uint_as_float(f[ks][h] & 0xffff0000u))));
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-        const int eq = q_row_exponent(m);
-        sl2r[n][0] = p.sl2 * pow2f(-__shfl_sync(0xffffffffu, eq, 8 * t4));
-        sl2r[n][1] = p.sl2 * pow2f(-__shfl_sync(0xffffffffu, eq, 8 * t4 + 4));
-        const float up = pow2f(eq);
-#pragma unroll
-        for (int ks = 0; ks < MT; ++ks)
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-            f[ks][h] = pack_half2(__uint_as_float(f[ks][h] << 16) * up, __uint_as_float(f[ks][h] & 0xffff0000u) * up);
-      }
-      if (kg == 0) {  // (every key group has the same)
+          for (int ks = 0; ks < MT; ++ks) {
+            uint2& v = qv[n][ks];
+            v.x = pack_half2(__uint_as_float(v.x << 16) * up, __uint_as_float(v.x & 0xffff0000u) * up);
+            v.y = pack_half2(__uint_as_float(v.y << 16) * up, __uint_as_float(v.y & 0xffff0000u) * up);
+          }
+        }
 #pragma unroll
         for (int i = 0; i < MT / 2; ++i)
-          sts_v4(q_frags + ((n * MT / 2 + i) * 32 + lane) * 16, f[2 * i][0], f[2 * i][1], f[2 * i + 1][0], f[2 * i + 1][1]);
+          sts_v4(q_frags + ((n * MT / 2 + i) * 32 + lane) * 16, qv[n][2 * i].x, qv[n][2 * i].y, qv[n][2 * i + 1].x,
+                 qv[n][2 * i + 1].y);
       }
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         const int rr = (rg * NT + n) * 8 + 2 * t4 + c;
@@ -260,6 +421,10 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::kMinBlocks) decode_fp4_ker
       for (int mt = 0; mt < MT; ++mt) o[mt][n][0] = o[mt][n][1] = o[mt][n][2] = o[mt][n][3] = 0.f;
     }
     __syncthreads();
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) sl2r[n][c] = Cfg::QB ? s_factor[(rg * NT + n) * 8 + 2 * t4 + c] : p.sl2;
 
     uint32_t stage = ring;
     // A step is compiled twice: for tiles that every row sees whole, and for the others (EDGE:
@@ -383,7 +548,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::kMinBlocks) decode_fp4_ker
             }
           }
       }
-      uint32_t pb[KT][NT][2], pl[PP == 2 ? KT : 1][PP == 2 ? NT : 1][2];
+      uint32_t pb[KT][NT][2], pl[PP == 2 ? KT : 1][NT][2] = {};
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         const float b0 = m_r[n][0] == -INFINITY ? 0.f : 7.f - m_r[n][0];
@@ -410,89 +575,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::kMinBlocks) decode_fp4_ker
         if (EDGE && !there[j]) continue;
         const uint32_t vt = stage + j * Cfg::kTile + Cfg::kCodes;
         const uint32_t sf = stage + j * Cfg::kTile + 2 * Cfg::kCodes + Cfg::kScales;
-        constexpr int NG = D / 128;  // groups of 16 dims that a lane holds
-        constexpr int NWD = D / 64;  // words of a key that a lane holds
-        // scales of keys (2 t4, 2 t4 + 1) and (2 t4 + 8, 2 t4 + 9) for groups NG g ..
-        uint32_t f01[NG], f89[NG], w[4][NWD];
-        if constexpr (NG == 2) {
-          const uint32_t at = sf + 2 * t4 * 16 + 2 * g;
-          const uint32_t a = e4m3x2_to_half2(lds_u16(at)), b = e4m3x2_to_half2(lds_u16(at + 16)),
-                         c = e4m3x2_to_half2(lds_u16(at + 128)), d = e4m3x2_to_half2(lds_u16(at + 144));
-          f01[0] = prmt(a, b, 0x5410u); f01[1] = prmt(a, b, 0x7632u);
-          f89[0] = prmt(c, d, 0x5410u); f89[1] = prmt(c, d, 0x7632u);
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const uint4 v = lds_v4(vt + q * 512 + lane * 16);
-            w[q][0] = v.x; w[q][1] = v.y; w[q][2] = v.z; w[q][3] = v.w;
-          }
-        } else {
-          // rows of 8 scales: a byte for this lane's group of each key
-          const uint32_t at = sf + 2 * t4 * 8 + (g & ~1);
-          const uint32_t a = lds_u16(at), b = lds_u16(at + 8), c = lds_u16(at + 64), d = lds_u16(at + 72);
-          const uint32_t sel = (g & 1) ? 0x0051u : 0x0040u;
-          f01[0] = e4m3x2_to_half2(static_cast<uint16_t>(prmt(a, b, sel)));
-          f89[0] = e4m3x2_to_half2(static_cast<uint16_t>(prmt(c, d, sel)));
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            // key 2 t4 + (q & 1) + 8 (q >> 1): line t4 + 4 (q >> 1)
-            const uint32_t at_v = vt + t4 * 128 + (((g >> 1) ^ (2 * t4)) << 4) + (g & 1) * 8;
-            const uint2 v = lds_v2((at_v ^ ((q & 1) * 64)) + (q >> 1) * 512);
-            w[q][0] = v.x; w[q][1] = v.y;
-          }
-        }
-        // Keys at or past the sequence's end may hold any bits: a scale of NaN must not meet a
-        // weight of zero. Nor must one of a key that only some rows see: it is taken out, and a
-        // product of ones marks the outputs of the rows that see it.
-        if constexpr (EDGE) {
-          const int ka = key0[j] + 2 * t4;
-          const uint32_t in01 = (ka < seq_len ? 0x0000ffffu : 0u) | (ka + 1 < seq_len ? 0xffff0000u : 0u);
-          const uint32_t in89 = (ka + 8 < seq_len ? 0x0000ffffu : 0u) | (ka + 9 < seq_len ? 0xffff0000u : 0u);
-#pragma unroll
-          for (int gr = 0; gr < NG; ++gr) {
-            f01[gr] &= in01;
-            f89[gr] &= in89;
-            const uint32_t o01 = not_finite_16<false>(f01[gr]), o89 = not_finite_16<false>(f89[gr]);
-            if (__any_sync(0xffffffffu, (o01 | o89) != 0)) {
-              f01[gr] &= ~o01;
-              f89[gr] &= ~o89;
-              const uint32_t a[4] = {o01 & 0x3c003c00u, o01 & 0x3c003c00u, o89 & 0x3c003c00u, o89 & 0x3c003c00u};
-#pragma unroll
-              for (int n = 0; n < NT; ++n) {
-                const int r = (rg * NT + n) * 8 + g;
-                const uint32_t see0 = (row_sees(p, pc, r, ka) ? 0x3c00u : 0u) | (row_sees(p, pc, r, ka + 1) ? 0x3c000000u : 0u);
-                const uint32_t see1 = (row_sees(p, pc, r, ka + 8) ? 0x3c00u : 0u) | (row_sees(p, pc, r, ka + 9) ? 0x3c000000u : 0u);
-                float mark[4] = {0.f, 0.f, 0.f, 0.f};
-                mma_16816(mark, a, see0, see1);
-#pragma unroll
-                for (int mt = 0; mt < 8; ++mt)
-#pragma unroll
-                  for (int e = 0; e < 4; ++e)
-                    if (mark[e] > 0.f) o[gr * 8 + mt][n][e] = __uint_as_float(0x7fffffffu);
-              }
-            }
-          }
-        }
-#pragma unroll
-        for (int q = 0; q < NWD; ++q) {  // a word: 8 dims, four m-tiles
-          constexpr uint32_t M = 0x0f0f0f0fu;
-          const uint32_t e01 = (w[0][q] & M) | ((w[1][q] << 4) & ~M), d01 = ((w[0][q] >> 4) & M) | (w[1][q] & ~M);
-          const uint32_t e89 = (w[2][q] & M) | ((w[3][q] << 4) & ~M), d89 = ((w[2][q] >> 4) & M) | (w[3][q] & ~M);
-          uint32_t he[4], hd[4], je[4], jd[4];
-          e2m1x8_to_half2(e01, he);
-          e2m1x8_to_half2(d01, hd);
-          e2m1x8_to_half2(e89, je);
-          e2m1x8_to_half2(d89, jd);
-          const uint32_t s01 = f01[q / 2], s89 = f89[q / 2];
-#pragma unroll
-          for (int b = 0; b < 4; ++b) {
-            const uint32_t a[4] = {hmul2_u(he[b], s01), hmul2_u(hd[b], s01), hmul2_u(je[b], s89), hmul2_u(jd[b], s89)};
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              mma_16816(o[4 * q + b][n], a, pb[j][n][0], pb[j][n][1]);
-              if constexpr (PP == 2) mma_16816(o[4 * q + b][n], a, pl[j][n][0], pl[j][n][1]);
-            }
-          }
-        }
+        fp4_pv<D, NT, PP, EDGE>(p, pc, rg * NT * 8, vt, sf, lane, key0[j], seq_len, pb[j], pl[PP == 2 ? j : 0], o);
       }
     };
     for (int i = 0; i < steps; ++i) {
@@ -531,51 +614,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::kMinBlocks) decode_fp4_ker
       for (int mt = 0; mt < MT; ++mt)
         mine[(n * MT + mt) * Cfg::kPitch + lane] = make_float4(o[mt][n][0], o[mt][n][1], o[mt][n][2], o[mt][n][3]);
     __syncthreads();
-    // item: two dims of two rows (an accumulator fragment) of a row tile
-    const bool direct = pc.npieces == 1;
-    for (int item = threadIdx.x; item < RG * NT * MT * 32; item += Cfg::kThreads) {
-      const int mt = item % MT, ln = (item / MT) % 32, tile = item / (MT * 32);
-      const int rw = tile / NT, n = tile % NT, r0 = tile * 8 + 2 * (ln & 3);
-      if (r0 >= pc.R) continue;
-      float M[2] = {-INFINITY, -INFINITY}, L[2] = {0.f, 0.f};
-      float2 ml[KG][2];
-#pragma unroll
-      for (int k = 0; k < KG; ++k)
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          ml[k][c] = s_ml[(k * RG + rw) * NT * 8 + n * 8 + 2 * (ln & 3) + c];
-          M[c] = fmaxf(M[c], ml[k][c].x);
-        }
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int k = 0; k < KG; ++k) {
-        const float4 v = reinterpret_cast<const float4*>(smem + (k * RG + rw) * Cfg::kRing)[(n * MT + mt) * Cfg::kPitch + ln];
-        const float f0 = ml[k][0].x == -INFINITY ? 0.f : ex2(ml[k][0].x - M[0]);
-        const float f1 = ml[k][1].x == -INFINITY ? 0.f : ex2(ml[k][1].x - M[1]);
-        L[0] += f0 * ml[k][0].y;
-        L[1] += f1 * ml[k][1].y;
-        acc.x += f0 * v.x; acc.y += f1 * v.y; acc.z += f0 * v.z; acc.w += f1 * v.w;
-      }
-      const int d = D / 8 * (ln >> 2) + 2 * mt;  // dims d, d + 1 of rows r0, r0 + 1
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const int r = r0 + c;
-        if (r >= pc.R) break;
-        const float v0 = c ? acc.y : acc.x, v1 = c ? acc.w : acc.z;
-        if (direct) {
-          const int q = r / p.G, head = kh * p.G + r % p.G;
-          const float inv = row_factor(p, L[c]);
-          *reinterpret_cast<uint32_t*>(reinterpret_cast<uint16_t*>(p.out) +
-                                       (static_cast<long long>(pc.q0 + q) * p.Hq + head) * D + d) =
-              Cfg::QB ? pack_bf162(v0 * inv, v1 * inv) : pack_half2(v0 * inv, v1 * inv);
-          if (d == 0) store_row_sum(p, pc.b, pc.q0, q, head, M[c], L[c]);
-        } else {
-          const long long prow = static_cast<long long>(pc.slot) * Cfg::RP + r;
-          __stcg(reinterpret_cast<float2*>(p.ws_o + prow * D + d), make_float2(v0, v1));
-          if (d == 0) __stcg(reinterpret_cast<float2*>(p.ws_ml + prow * 2), make_float2(M[c], L[c]));
-        }
-      }
-    }
+    fp4_join<Cfg, D, NT, RG, KG, Cfg::kThreads>(p, pc, smem, s_ml);
     __syncthreads();  // the rings are free again
   }
 }

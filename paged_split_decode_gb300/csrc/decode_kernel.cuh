@@ -430,7 +430,7 @@ __device__ __forceinline__ ChunkPlan make_chunk_plan(long long T, int grid) {
   ChunkPlan cp;
   cp.T = T;
   cp.Ce = T <= 0 ? 0 : static_cast<int>(T < grid ? T : grid);
-  cp.q = cp.Ce > 0 ? T / cp.Ce : 0;
+  cp.q = cp.Ce > 0 ? static_cast<unsigned>(T) / static_cast<unsigned>(cp.Ce) : 0;  // (T < 2^31: the host checks it)
   cp.r = cp.Ce > 0 ? static_cast<int>(T - cp.q * cp.Ce) : 0;
   return cp;
 }

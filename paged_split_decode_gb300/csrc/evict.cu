@@ -2,19 +2,22 @@
 // collected (evict_kv_cache): each KV head of a long sequence keeps its first keys, its
 // last ones and the heaviest of the rest, moved together in order.
 //
-// Launch 1, select_kernel: a CTA for each (sequence, KV head). The weights, as integers
+// Launch 1, select_kernel: a cluster of one to eight CTAs for each (sequence, KV head), as many
+// as the GPU holds (B = 1, eight heads, 32768 keys: one CTA each 38 us of the call's 47).
+// Each CTA has a run of the keys. The weights, as integers
 // that order as the numbers do, are held in shared memory (beyond its size they are
 // read again); the m-th largest is found digit by digit (8 bits, most significant first)
-// from histograms; then each warp counts what its run of keys keeps, a scan over the
-// warps gives its place, and it writes the kept keys' indices in order. Of the keys equal
-// to the m-th largest the lowest indices are kept.
+// from histograms, added up over the cluster; then each warp counts what its run of keys keeps, a scan over the
+// warps gives its place, and it writes where every kept key comes from and goes to, in
+// order. Of the keys equal to the m-th largest the lowest indices are kept. Bound by
+// latency: four loads of a thread are in flight at a time.
 //
 // Launch 2, move_kernel: rows move to slots at or below their own. In place that is safe
-// without a second buffer when a CTA takes its rows in order: it loads R rows, waits for
-// all its threads, and stores them; the next R rows' sources are at or behind the R-th
-// slot from here, and no store comes before it. So a (sequence, head, array) is split over CTAs by the
-// rows' columns only (pieces of 32 bytes, HBM's sector, or more); copies to other blocks by rows
-// as well. HBM-bound: 2 x the kept rows' bytes.
+// without a second buffer when a CTA takes its rows in order: it loads a batch of rows, waits for
+// all its threads, and stores them; the next batch's sources are at or behind its own first slot,
+// and no earlier store reaches that far. So a (sequence, head, array) is split over CTAs by the
+// rows' columns only (32 bytes, HBM's sector, or more); copies to other blocks by rows
+// as well. HBM-bound: 2 x the kept rows' bytes; a lane has four 16-byte pieces in flight.
 //
 // Launch 3, with a free list: the blocks behind the new ends are pushed.
 #include <cuda_runtime.h>
@@ -25,15 +28,31 @@
 
 #include "launch.h"
 #include "pdecode.h"
+#include "tc5.cuh"
 
 namespace pd {
 namespace {
 
 constexpr int kSelectThreads = 1024;
-constexpr int kMoveThreads = 512;
-constexpr int kMoveRows = 4;                     // rows that a thread has in flight
+constexpr int kLoads = 4;                        // a thread's loads in flight
+constexpr int kMoveThreads = 256;
 constexpr int kCachedKeys = 48 * 1024;           // weights in shared memory
 constexpr int kMaxArrays = 5;
+
+// n / d for n < 2^31 by a multiplication (Granlund and Montgomery's round-up method): with l =
+// ceil(log2 d) and m = floor(2^32 (2^l - d) / d) + 1, n / d = (mulhi(m, n) + n) >> l. (One CTA divides for
+// tens of thousands of keys: the GPU's own integer division was half of its time.)
+struct FastDiv {
+  uint32_t d, m, l;
+  explicit FastDiv(uint32_t d_ = 1) : d(d_), l(0) {
+    while ((1ull << l) < d) ++l;
+    m = static_cast<uint32_t>(((1ull << 32) * ((1ull << l) - d)) / d + 1);
+  }
+  __device__ __forceinline__ int div(int n) const {
+    return static_cast<int>((__umulhi(m, static_cast<uint32_t>(n)) + static_cast<uint32_t>(n)) >> l);
+  }
+  __device__ __forceinline__ int mod(int n) const { return n - div(n) * static_cast<int>(d); }
+};
 
 struct MoveArray {
   uint8_t* base;
@@ -49,11 +68,16 @@ struct EvictArgs {
   const float* weights;
   const int32_t *table, *table_out, *lens;
   int32_t *lens_out, *free_blocks, *free_count;
-  int32_t *kept, *old_lens;     // workspace: [B, Hkv, keep], [B] (-1: a bad length)
+  int4* moves;                  // workspace: [B, Hkv, most] (from, to) as slots, then as rows of [block, head, key]
+  int32_t* kept;                // [B, Hkv, most]: a cut sequence's kept keys
+  int32_t* old_lens;            // [B] (-1: a bad length)
   uint32_t* error_flag;
   int B, Hkv, block_size, num_blocks, max_blocks, max_blocks_out;
+  FastDiv bs;                   // block_size
   int keep, trigger, first, recent;
+  int most;                     // keys that a sequence can keep
   int in_place;
+  int cluster;                  // CTAs of a (sequence, head) in the select
 };
 
 // The weight as an integer that orders as it does, NaN below all.
@@ -63,50 +87,126 @@ __device__ __forceinline__ uint32_t order_of(float w) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
+__device__ __forceinline__ uint32_t ld_peer_u32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+
 __global__ void __launch_bounds__(kSelectThreads) select_kernel(const EvictArgs a) {
-  extern __shared__ uint32_t s_key[];            // [min(keys, kCachedKeys)]
-  __shared__ uint32_t s_hist[256], s_pick[2];
+  extern __shared__ uint32_t s_key[];            // the CTA's keys, kCachedKeys of them at most
+  __shared__ uint32_t s_hist[2][256], s_sum[256], s_pick[2];
   __shared__ int s_count[2][32];
-  const int b = blockIdx.x / a.Hkv, h = blockIdx.x % a.Hkv;
+  __shared__ uint32_t s_total[2];                // the CTA's keys above and equal to the m-th largest
+  const int C = a.cluster, rank = blockIdx.x % C, u = blockIdx.x / C;
+  const int b = u / a.Hkv, h = u % a.Hkv;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int L = __ldg(a.lens + b);
   const bool bad = L < 0 || L > a.max_blocks * a.block_size;
-  if (h == 0 && threadIdx.x == 0) {
+  if (h == 0 && rank == 0 && threadIdx.x == 0) {
     a.old_lens[b] = bad ? -1 : L;
     if (bad && a.error_flag) atomicOr(a.error_flag, PD_DEVERR_SEQ_LEN);
   }
-  if (bad || L <= a.trigger) return;
+  const bool cut = L > a.trigger;
+  if (bad || (a.in_place && !cut)) return;
   const int32_t* row = a.table + static_cast<long long>(b) * a.max_blocks;
-  const int lo = a.first, hi = L - a.recent;     // the keys that are chosen from
-  auto load = [&](int j) -> uint32_t {
-    const int blk = __ldg(row + j / a.block_size);
-    if (blk < 0 || blk >= a.num_blocks) return 0u;  // (the move reports it)
-    return order_of(__ldg(a.weights + (static_cast<long long>(blk) * a.Hkv + h) * a.block_size + j % a.block_size));
+  const int32_t* row_out = a.in_place ? row : a.table_out + static_cast<long long>(b) * a.max_blocks_out;
+  int4* out = a.moves + (static_cast<long long>(b) * a.Hkv + h) * a.most;
+  int32_t* kept = a.kept + (static_cast<long long>(b) * a.Hkv + h) * a.most;
+  // where the n kept keys come from and go to
+  const int thread = rank * kSelectThreads + threadIdx.x, threads = C * kSelectThreads;  // of the cluster
+  auto list_moves = [&](int n) {
+    for (int i0 = thread; i0 < n; i0 += threads * kLoads) {
+      int j[kLoads], from[kLoads], to[kLoads];
+#pragma unroll
+      for (int k = 0; k < kLoads; ++k) {
+        const int i = i0 + k * threads;
+        j[k] = i < n && cut ? __ldcg(kept + i) : i;
+      }
+#pragma unroll
+      for (int k = 0; k < kLoads; ++k) {
+        const int i = i0 + k * threads;
+        from[k] = i < n ? __ldg(row + a.bs.div(j[k])) : 0;
+        to[k] = i < n ? __ldg(row_out + a.bs.div(i)) : 0;
+      }
+#pragma unroll
+      for (int k = 0; k < kLoads; ++k) {
+        const int i = i0 + k * threads;
+        if (i >= n) continue;
+        int4 m = make_int4(-1, -1, -1, -1);  // (not in the cache: not moved)
+        if (from[k] >= 0 && from[k] < a.num_blocks && to[k] >= 0 && to[k] < a.num_blocks) {
+          const int of = a.bs.mod(j[k]), ot = a.bs.mod(i);
+          m = make_int4(from[k] * a.block_size + of, to[k] * a.block_size + ot, (from[k] * a.Hkv + h) * a.block_size + of,
+                        (to[k] * a.Hkv + h) * a.block_size + ot);
+        } else if (a.error_flag) {
+          atomicOr(a.error_flag, PD_DEVERR_BLOCK_ID);
+        }
+        out[i] = m;
+      }
+    }
   };
-  const int cached = min(hi - lo, kCachedKeys);
-  for (int i = threadIdx.x; i < cached; i += kSelectThreads) s_key[i] = load(lo + i);
+  if (!cut) {
+    list_moves(L);
+    return;
+  }
+  const int lo = a.first, hi = L - a.recent;     // the keys that are chosen from
+  auto weight = [&](int j, int blk) -> uint32_t {  // (a bad block counts as NaN; a move from it reports it)
+    if (blk < 0 || blk >= a.num_blocks) return 0u;
+    return order_of(__ldg(a.weights + (static_cast<long long>(blk) * a.Hkv + h) * a.block_size + a.bs.mod(j)));
+  };
+  auto load = [&](int j) -> uint32_t { return weight(j, __ldg(row + a.bs.div(j))); };
+  const int all = hi - lo, share = (all + C - 1) / C;
+  const int c0 = min(rank * share, all), n = min(c0 + share, all) - c0;  // this CTA's run: lo + c0 ..
+  const int cached = min(n, kCachedKeys);
+  for (int i0 = threadIdx.x; i0 < cached; i0 += kSelectThreads * kLoads) {
+    int blk[kLoads];
+    uint32_t u[kLoads];
+#pragma unroll
+    for (int k = 0; k < kLoads; ++k) {
+      const int i = i0 + k * kSelectThreads;
+      blk[k] = i < cached ? __ldg(row + a.bs.div(lo + c0 + i)) : -1;
+    }
+#pragma unroll
+    for (int k = 0; k < kLoads; ++k) u[k] = weight(lo + c0 + i0 + k * kSelectThreads, blk[k]);
+#pragma unroll
+    for (int k = 0; k < kLoads; ++k)
+      if (i0 + k * kSelectThreads < cached) s_key[i0 + k * kSelectThreads] = u[k];
+  }
   __syncthreads();
-  auto key = [&](int i) -> uint32_t { return i < kCachedKeys ? s_key[i] : load(lo + i); };
-  const int n = hi - lo;
-  const int m = a.keep - a.first - a.recent;     // of them are kept: m < n, as L > trigger >= keep
+  auto key = [&](int i) -> uint32_t { return i < kCachedKeys ? s_key[i] : load(lo + c0 + i); };
+  const int m = a.keep - a.first - a.recent;     // of all of them are kept: fewer than all, as L > trigger >= keep
   // the m-th largest, and how many equal to it are kept
   uint32_t pick = 0, mask = 0;
   uint32_t want = m;
+  if (threadIdx.x < 512) s_hist[threadIdx.x >> 8][threadIdx.x & 255] = 0;
+  __syncthreads();
   if (m > 0) {
     for (int shift = 24; shift >= 0; shift -= 8) {
-      if (threadIdx.x < 256) s_hist[threadIdx.x] = 0;
-      __syncthreads();
+      uint32_t* hist = s_hist[shift >> 3 & 1];
       for (int i = threadIdx.x; i < n; i += kSelectThreads) {
         const uint32_t u = key(i);
-        if ((u & mask) == pick) atomicAdd(&s_hist[(u >> shift) & 255u], 1u);
+        if ((u & mask) == pick) atomicAdd(&hist[(u >> shift) & 255u], 1u);
+      }
+      if (C > 1) {
+        cluster_sync();
+        if (threadIdx.x < 256) {
+          uint32_t c[8], sum = 0;
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            c[k] = k < C ? ld_peer_u32(peer_smem(static_cast<uint32_t>(__cvta_generic_to_shared(hist + threadIdx.x)), k)) : 0u;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) sum += c[k];
+          s_sum[threadIdx.x] = sum;
+        }
       }
       __syncthreads();
       if (warp == 0) {  // lane: eight digits, the largest ones first
+        const uint32_t* counts = C > 1 ? s_sum : hist;
         uint32_t c[8], sum = 0;
 #pragma unroll
-        for (int d = 0; d < 8; ++d) sum += c[d] = s_hist[255 - (lane * 8 + d)];
+        for (int d = 0; d < 8; ++d) sum += c[d] = counts[255 - (lane * 8 + d)];
         uint32_t above = sum;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -123,6 +223,9 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const EvictArgs 
           above += c[d];
         }
       }
+      // (the peers read this histogram; the one before, which the next pass fills, is read by nobody)
+      if (warp == 1)
+        for (int i = lane; i < 256; i += 32) s_hist[(shift >> 3 & 1) ^ 1][i] = 0;
       __syncthreads();
       pick |= s_pick[0] << shift;
       mask |= 255u << shift;
@@ -149,16 +252,27 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const EvictArgs 
     s_count[1][warp] = equal;
   }
   __syncthreads();
+  if (threadIdx.x < 2) {
+    int sum = 0;
+    for (int w = 0; w < 32; ++w) sum += s_count[threadIdx.x][w];
+    s_total[threadIdx.x] = static_cast<uint32_t>(sum);
+  }
+  if (C > 1) cluster_sync();
+  else __syncthreads();
   int before = 0, ties = 0;                      // kept keys and ties of earlier runs
+  for (int k = 0; k < rank; ++k) {
+    const uint32_t peer = peer_smem(static_cast<uint32_t>(__cvta_generic_to_shared(s_total)), k);
+    before += static_cast<int>(ld_peer_u32(peer));
+    ties += static_cast<int>(ld_peer_u32(peer + 4));
+  }
   for (int w = 0; w < warp; ++w) {
     before += s_count[0][w];
     ties += s_count[1][w];
   }
   const int quota = static_cast<int>(want);
   before += min(ties, quota);
-  int32_t* out = a.kept + (static_cast<long long>(b) * a.Hkv + h) * a.keep;
-  for (int i = threadIdx.x; i < a.first; i += kSelectThreads) out[i] = i;
-  for (int i = threadIdx.x; i < a.recent; i += kSelectThreads) out[a.keep - a.recent + i] = hi + i;
+  for (int i = thread; i < a.first; i += threads) __stcg(kept + i, i);
+  for (int i = thread; i < a.recent; i += threads) __stcg(kept + a.keep - a.recent + i, hi + i);
   if (m > 0) {
     const uint32_t below = (1u << lane) - 1u;
     for (int i0 = r0; i0 < r1; i0 += 32) {
@@ -168,62 +282,58 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const EvictArgs 
       const uint32_t tie_mask = __ballot_sync(0xffffffffu, tie);
       const bool keep = i < r1 && (u > pick || (tie && ties + __popc(tie_mask & below) < quota));
       const uint32_t keep_mask = __ballot_sync(0xffffffffu, keep);
-      if (keep) out[a.first + before + __popc(keep_mask & below)] = lo + i;
+      if (keep) __stcg(kept + a.first + before + __popc(keep_mask & below), lo + c0 + i);
       before += __popc(keep_mask);
       ties += __popc(tie_mask);
     }
   }
+  if (C > 1) cluster_sync();  // (and no peer reads this CTA's shared memory any more)
+  else __syncthreads();
+  list_moves(a.keep);
 }
 
 template <class V>
-__device__ __forceinline__ void move_rows(const EvictArgs& a, const MoveArray& arr, int b, int h, int slice, int part,
-                                          int n, bool cut) {
+__device__ __forceinline__ void move_rows(const EvictArgs& a, const MoveArray& arr, int b, int h, int slice, int part, int n) {
   const int vecs = arr.row_bytes / static_cast<int>(sizeof(V));
-  const int v0 = vecs * slice / arr.slices, v1 = vecs * (slice + 1) / arr.slices, width = v1 - v0;
+  const int v0 = vecs * slice / arr.slices, width = vecs * (slice + 1) / arr.slices - v0;
   const int rows = kMoveThreads / width;         // rows side by side (threads beyond them idle)
   const int tv = threadIdx.x % width, tr = threadIdx.x / width;
-  const int32_t* from = a.table + static_cast<long long>(b) * a.max_blocks;
-  const int32_t* to = a.in_place ? from : a.table_out + static_cast<long long>(b) * a.max_blocks_out;
-  const int32_t* kept = a.kept + (static_cast<long long>(b) * a.Hkv + h) * a.keep;
-  auto at = [&](const int32_t* table, int j, bool report) -> V* {
-    const int blk = __ldg(table + j / a.block_size), off = j % a.block_size;
-    if (blk < 0 || blk >= a.num_blocks) {
-      if (report && a.error_flag) atomicOr(a.error_flag, PD_DEVERR_BLOCK_ID);
-      return nullptr;
-    }
-    const long long row = arr.keys_first ? (static_cast<long long>(blk) * a.block_size + off) * a.Hkv + h
-                                         : (static_cast<long long>(blk) * a.Hkv + h) * a.block_size + off;
-    return reinterpret_cast<V*>(arr.base + row * arr.row_bytes) + v0 + tv;
-  };
+  const int4* moves = a.moves + (static_cast<long long>(b) * a.Hkv + h) * a.most;
   // rows of this part (one part in place: its rows are taken in order)
   const int share = (n + a.parts - 1) / a.parts, j0 = part * share, j1 = min(j0 + share, n);
-  const bool live = tr < rows;
-  for (int base = j0; base < j1; base += rows * kMoveRows) {
-    V x[kMoveRows];
-    V* dst[kMoveRows];
+  const bool keys_first = arr.keys_first != 0;
+  auto load = [&](int base, int2 (&m)[kLoads]) {  // where the thread's rows of a batch come from and go to
 #pragma unroll
-    for (int k = 0; k < kMoveRows; ++k) {
+    for (int k = 0; k < kLoads; ++k) {
       const int i = base + k * rows + tr;
-      dst[k] = nullptr;
-      if (live && i < j1) {
-        const int j = cut ? __ldg(kept + i) : i;
-        if (a.in_place && j == i) continue;
-        const V* src = at(from, j, true);
-        V* d = at(to, i, true);
-        if (src != nullptr && d != nullptr) {
-          x[k] = *src;
-          dst[k] = d;
-        }
-      }
+      m[k] = make_int2(-1, -1);
+      if (tr < rows && i < j1) m[k] = __ldg(reinterpret_cast<const int2*>(moves + i) + (keys_first ? 0 : 1));
     }
+  };
+  auto at = [&](int row) -> V* {
+    const long long r = keys_first ? static_cast<long long>(row) * a.Hkv + h : row;
+    return reinterpret_cast<V*>(arr.base + r * arr.row_bytes) + v0 + tv;
+  };
+  int2 m[kLoads], next[kLoads];
+  load(j0, m);
+  for (int base = j0; base < j1; base += rows * kLoads) {
+    V x[kLoads];
+#pragma unroll
+    for (int k = 0; k < kLoads; ++k) {
+      if (m[k].x < 0 || m[k].x == m[k].y) m[k].y = -1;  // (nothing to move)
+      if (m[k].y >= 0) x[k] = *at(m[k].x);
+    }
+    load(base + rows * kLoads, next);
     if (a.in_place) __syncthreads();
 #pragma unroll
-    for (int k = 0; k < kMoveRows; ++k)
-      if (dst[k] != nullptr) *dst[k] = x[k];
+    for (int k = 0; k < kLoads; ++k) {
+      if (m[k].y >= 0) *at(m[k].y) = x[k];
+      m[k] = next[k];
+    }
   }
 }
 
-__global__ void __launch_bounds__(kMoveThreads) move_kernel(const EvictArgs a) {
+__global__ void __launch_bounds__(kMoveThreads, 4) move_kernel(const EvictArgs a) {
   // CTA: ((sequence, head), slice of an array, part of the rows)
   const int part = blockIdx.x % a.parts, s = blockIdx.x / a.parts % a.slices, u = blockIdx.x / a.parts / a.slices;
   const int b = u / a.Hkv, h = u % a.Hkv;
@@ -240,9 +350,9 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const EvictArgs a) {
   int i = 0, slice = s;
   while (slice >= a.arrays[i].slices) slice -= a.arrays[i++].slices;
   const MoveArray arr = a.arrays[i];
-  if (arr.vec == 16) move_rows<uint4>(a, arr, b, h, slice, part, n, cut);
-  else if (arr.vec == 8) move_rows<uint2>(a, arr, b, h, slice, part, n, cut);
-  else move_rows<uint32_t>(a, arr, b, h, slice, part, n, cut);
+  if (arr.vec == 16) move_rows<uint4>(a, arr, b, h, slice, part, n);
+  else if (arr.vec == 8) move_rows<uint2>(a, arr, b, h, slice, part, n);
+  else move_rows<uint32_t>(a, arr, b, h, slice, part, n);
 }
 
 // One CTA: the blocks behind the cut sequences' new ends go to the free list.
@@ -315,18 +425,20 @@ pd_status check(const pd_dims* d, const pd_eviction* e) {
       static_cast<long long>(e->first) + e->recent > e->keep)
     return PD_ERR_SHAPE;
   if (d->D > 512 || static_cast<long long>(d->max_blocks_per_seq) * d->block_size > (1ll << 30) ||
-      static_cast<long long>(d->num_blocks) * d->block_size > 0x7fffffffll ||
+      static_cast<long long>(d->num_blocks) * d->block_size * d->Hkv > 0x7fffffffll ||
       static_cast<long long>(d->B) * d->Hkv > (1 << 22))
     return PD_ERR_UNSUPPORTED;
   return PD_OK;
 }
 
+// Keys that a sequence can be left with in the workspace's lists.
+long long most_kept(const pd_dims& d, const pd_eviction& e) {
+  return std::min<long long>(e.trigger, static_cast<long long>(d.max_blocks_per_seq) * d.block_size);
+}
 size_t workspace_of(const pd_dims& d, const pd_eviction& e, size_t* off_lens) {
-  // (a sequence that is cut has at least keep keys in its table)
-  const size_t most = std::min<size_t>(e.keep, static_cast<size_t>(d.max_blocks_per_seq) * d.block_size);
-  const size_t kept = (static_cast<size_t>(d.B) * d.Hkv * most * 4 + 255) / 256 * 256;
-  if (off_lens) *off_lens = kept;
-  return kept + static_cast<size_t>(d.B) * 4;
+  const size_t moves = (static_cast<size_t>(d.B) * d.Hkv * most_kept(d, e) * 20 + 255) / 256 * 256;
+  if (off_lens) *off_lens = moves;
+  return moves + static_cast<size_t>(d.B) * 4;
 }
 
 }  // namespace
@@ -351,8 +463,7 @@ extern "C" pd_status evict_kv_cache(void* k_cache, void* v_cache, void* k_block_
   const bool fp4 = d.kv_dtype == PD_KV_FP4 || d.kv_dtype == PD_KV_FP4_BF16;
   const long long cap = static_cast<long long>(d.max_blocks_per_seq) * d.block_size;
   if (block_table_out != nullptr &&
-      (max_blocks_out < 0 || static_cast<long long>(max_blocks_out) * d.block_size <
-                                 std::min<long long>(cap, std::max(e.keep, e.trigger))))
+      (max_blocks_out < 0 || static_cast<long long>(max_blocks_out) * d.block_size < most_kept(d, e)))
     return PD_ERR_SHAPE;
   if ((free_blocks != nullptr) != (free_count != nullptr)) return PD_ERR_NULL;
   if (free_blocks != nullptr && block_table_out != nullptr) return PD_ERR_SHAPE;
@@ -382,12 +493,15 @@ extern "C" pd_status evict_kv_cache(void* k_cache, void* v_cache, void* k_block_
   a.lens_out = seq_lens_out;
   a.free_blocks = free_blocks;
   a.free_count = free_count;
-  a.kept = static_cast<int32_t*>(workspace);
+  a.moves = static_cast<int4*>(workspace);
+  a.most = static_cast<int>(most_kept(d, e));
+  a.kept = reinterpret_cast<int32_t*>(a.moves + static_cast<size_t>(d.B) * d.Hkv * a.most);
   a.old_lens = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(workspace) + off_lens);
   a.error_flag = error_flag;
   a.B = d.B;
   a.Hkv = d.Hkv;
   a.block_size = d.block_size;
+  a.bs = FastDiv(static_cast<uint32_t>(d.block_size));
   a.num_blocks = d.num_blocks;
   a.max_blocks = d.max_blocks_per_seq;
   a.max_blocks_out = max_blocks_out;
@@ -416,8 +530,7 @@ extern "C" pd_status evict_kv_cache(void* k_cache, void* v_cache, void* k_block_
       while (units * 2 * s < 2 * sms && row / (2 * s) >= 32) s *= 2;
     }
   } else {
-    const long long rows = std::min<long long>(cap, std::max(e.keep, e.trigger));
-    while (units * a.n_arrays * a.parts < 8 * sms && rows / (2 * a.parts) >= 32) a.parts *= 2;
+    while (units * a.n_arrays * a.parts < 16 * sms && a.most / (2 * a.parts) >= 64) a.parts *= 2;
   }
   a.slices = 0;
   for (int i = 0; i < a.n_arrays; ++i) a.slices += a.arrays[i].slices;
@@ -427,8 +540,12 @@ extern "C" pd_status evict_kv_cache(void* k_cache, void* v_cache, void* k_block_
   cudaError_t err = once_per_context(attr_ctx, [] {
     return cudaFuncSetAttribute(select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kCachedKeys * 4);
   });
-  const int smem = static_cast<int>(std::min<long long>(cap, kCachedKeys)) * 4;
-  if (err == cudaSuccess) err = launch_pdl(select_kernel, static_cast<int>(units), kSelectThreads, smem, s, 1, a);
+  // as many CTAs a head as the GPU's SMs are, runs of 1024 keys and more
+  a.cluster = 1;
+  while (a.cluster < 8 && units * a.cluster * 2 <= sms && cap / (2 * a.cluster) >= 1024) a.cluster *= 2;
+  const int smem = static_cast<int>(std::min<long long>((cap + a.cluster - 1) / a.cluster, kCachedKeys)) * 4;
+  if (err == cudaSuccess)
+    err = launch_pdl(select_kernel, static_cast<int>(units * a.cluster), kSelectThreads, smem, s, a.cluster, a);
   const long long ctas = units * a.slices * a.parts;
   if (ctas > 0x7fffffffll) return PD_ERR_UNSUPPORTED;
   if (err == cudaSuccess) err = launch_pdl(move_kernel, static_cast<int>(ctas), kMoveThreads, 0, s, 1, a);

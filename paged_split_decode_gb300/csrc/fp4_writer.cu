@@ -18,6 +18,7 @@
 #include <cstdint>
 
 #include "pdecode.h"
+#include "ptx.cuh"
 
 namespace pd {
 namespace {
@@ -76,20 +77,6 @@ __device__ __forceinline__ uint32_t e4m3_code(float x) {
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(0.f), "f"(x));
   return r & 0xffu;
 }
-// Codes of eight quotients, the first in the lowest nibble.
-__device__ __forceinline__ uint32_t e2m1x8(const float (&q)[8]) {
-  uint32_t r;
-  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
-      "mov.b32 %0, {a, b, c, d};\n\t}"
-      : "=r"(r)
-      : "f"(q[0]), "f"(q[1]), "f"(q[2]), "f"(q[3]), "f"(q[4]), "f"(q[5]), "f"(q[6]), "f"(q[7]));
-  return r;
-}
-
 template <bool BF>
 __device__ __forceinline__ void quantise(const Vec32& x, float scale, bool fast, uint8_t* codes, uint8_t* sf) {
   uint32_t m2 = x.w[0] & 0x7fff7fffu;
@@ -125,8 +112,8 @@ __device__ __forceinline__ void quantise(const Vec32& x, float scale, bool fast,
     }
     const float a[8] = {q[0], q[1], q[2], q[3], q[4], q[5], q[6], q[7]};
     const float b[8] = {q[8], q[9], q[10], q[11], q[12], q[13], q[14], q[15]};
-    lo = e2m1x8(a);
-    hi = e2m1x8(b);
+    lo = float_to_e2m1x8(a);
+    hi = float_to_e2m1x8(b);
   }
   *reinterpret_cast<uint2*>(codes) = make_uint2(lo, hi);
   *sf = static_cast<uint8_t>(s);

@@ -140,6 +140,8 @@ pd_status check_dims(const pd_dims* d, int qlen, Op op = Op::kPlain) {
   if (static_cast<long long>(d->B) * d->Hkv * (cap_keys / kTileKeys + 1 + 64) > (1ll << 31) - 1)
     return PD_ERR_UNSUPPORTED;
   if (static_cast<long long>(d->num_blocks) * d->block_size > (1ll << 31) - 1) return PD_ERR_UNSUPPORTED;
+  if (fp4 && static_cast<long long>(d->num_blocks) * d->block_size * d->Hkv > (1ll << 31) - 1)
+    return PD_ERR_UNSUPPORTED;  // its rows are (key, head) pairs
   if (static_cast<long long>(d->B) * qlen * d->Hq > (1ll << 31) - 1) return PD_ERR_UNSUPPORTED;
   return PD_OK;
 }
