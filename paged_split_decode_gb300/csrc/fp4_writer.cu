@@ -23,7 +23,7 @@
 namespace pd {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 
 struct WriteArgs {
   const uint8_t *k_new, *v_new;
@@ -34,7 +34,7 @@ struct WriteArgs {
   long long num_slots;
   int groups, head_groups;  // of a token, of a head
   int Hkv, block_size;
-  float k_scale, v_scale;
+  float k_scale, v_scale, k_scale6, v_scale6, k_rcp6, v_rcp6;  // 6 scale, 1 / (6 scale)
   int aligned32;         // the new rows begin at a multiple of 32 bytes
   int fast;              // scales within [2^-100, 2^100]: the corrected quotient is exact
 };
@@ -77,45 +77,62 @@ __device__ __forceinline__ uint32_t e4m3_code(float x) {
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(0.f), "f"(x));
   return r & 0xffu;
 }
+// The group's 16 values x / d as codes: fast, or by the plain division.
+template <bool BF, bool FAST>
+__device__ __forceinline__ uint2 codes_of(const Vec32& x, float d, float r) {
+  uint32_t c[2];
+  const unsigned long long r2 = f2_pack(r, r), nd2 = f2_pack(-d, -d);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    float q[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 v = widen<BF>(x.w[4 * h + i]);
+      if constexpr (FAST) {
+        const unsigned long long xx = f2_pack(v.x, v.y), q0 = f2_mul(xx, r2), q1 = f2_fma(f2_fma(q0, nd2, xx), r2, q0);
+        q[2 * i] = f2_lo(q1);
+        q[2 * i + 1] = f2_hi(q1);
+      } else {  // (beyond 8 d nothing changes the code, and infinities would)
+        q[2 * i] = d > 0.f ? __fdiv_rn(fminf(fabsf(v.x), 8.f * d), d) : 0.f;
+        q[2 * i + 1] = d > 0.f ? __fdiv_rn(fminf(fabsf(v.y), 8.f * d), d) : 0.f;
+      }
+      // (the sign of a zero too)
+      q[2 * i] = copysignf(q[2 * i], v.x);
+      q[2 * i + 1] = copysignf(q[2 * i + 1], v.y);
+    }
+    c[h] = float_to_e2m1x8(q);
+  }
+  return make_uint2(c[0], c[1]);
+}
+
 template <bool BF>
-__device__ __forceinline__ void quantise(const Vec32& x, float scale, bool fast, uint8_t* codes, uint8_t* sf) {
+__device__ __forceinline__ void quantise(const Vec32& x, float scale, float scale6, float rcp6, bool fast, uint8_t* codes,
+                                         uint8_t* sf) {
   uint32_t m2 = x.w[0] & 0x7fff7fffu;
 #pragma unroll
   for (int i = 1; i < 8; ++i) m2 = max2_nan<BF>(m2, x.w[i] & 0x7fff7fffu);
   const float2 m = widen<BF>(m2);
   const float amax = fmaxf(m.x, m.y);
-  uint32_t s, lo = 0, hi = 0;
+  float t;  // amax / (6 scale)
+  if (fast) {
+    const float q0 = amax * rcp6;
+    t = fmaf(fmaf(-q0, scale6, amax), rcp6, q0);
+    if (amax == INFINITY) t = INFINITY;
+  } else {
+    t = __fdiv_rn(amax, scale6);
+  }
+  uint32_t s = e4m3_code(t);
+  const float d = e4m3_value(s) * scale;
+  uint2 c;
   if (m.x != m.x || m.y != m.y) {
     s = 0x7f;
+    c = make_uint2(0u, 0u);
+  } else if (fast && s != 0x7e) {  // (a scale below its end: quotients up to 7, finite values)
+    c = codes_of<BF, true>(x, d, d > 0.f ? __frcp_rn(d) : 0.f);
   } else {
-    s = e4m3_code(__fdiv_rn(amax, 6.f * scale));
-    const float d = e4m3_value(s) * scale;
-    // d = 0: quotients +-0. A scale that is at its end, and quotients beyond 6 with it: held
-    // to 8 d, which keeps the residual finite and changes no code.
-    const float r = d > 0.f ? __frcp_rn(d) : 0.f, lim = s == 0x7e ? 8.f * d : INFINITY;
-    float q[16];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float2 v = widen<BF>(x.w[i]);
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const float a = fminf(fabsf(h ? v.y : v.x), lim);
-        float t;
-        if (fast) {
-          const float q0 = a * r;
-          t = fmaf(fmaf(-q0, d, a), r, q0);
-        } else {
-          t = d > 0.f ? __fdiv_rn(a, d) : 0.f;
-        }
-        q[2 * i + h] = copysignf(t, h ? v.y : v.x);
-      }
-    }
-    const float a[8] = {q[0], q[1], q[2], q[3], q[4], q[5], q[6], q[7]};
-    const float b[8] = {q[8], q[9], q[10], q[11], q[12], q[13], q[14], q[15]};
-    lo = float_to_e2m1x8(a);
-    hi = float_to_e2m1x8(b);
+    c = codes_of<BF, false>(x, d, 0.f);
   }
-  *reinterpret_cast<uint2*>(codes) = make_uint2(lo, hi);
+  *reinterpret_cast<uint2*>(codes) = c;
   *sf = static_cast<uint8_t>(s);
 }
 
@@ -135,8 +152,8 @@ __global__ void __launch_bounds__(kThreads) write_fp4_kernel(const WriteArgs a) 
     const uint32_t s32 = static_cast<uint32_t>(slot), blk = s32 / a.block_size, off = s32 - blk * a.block_size;
     const long long row = (static_cast<long long>(blk) * a.Hkv + h) * a.block_size + off;
     const long long at = row * a.head_groups + gg;
-    quantise<BF>(k, a.k_scale, a.fast != 0, a.k_codes + at * 8, a.k_sf + at);
-    quantise<BF>(v, a.v_scale, a.fast != 0, a.v_codes + at * 8, a.v_sf + at);
+    quantise<BF>(k, a.k_scale, a.k_scale6, a.k_rcp6, a.fast != 0, a.k_codes + at * 8, a.k_sf + at);
+    quantise<BF>(v, a.v_scale, a.v_scale6, a.v_rcp6, a.fast != 0, a.v_codes + at * 8, a.v_sf + at);
   }
 }
 
@@ -170,12 +187,13 @@ extern "C" pd_status write_kv_cache_fp4(const void* k_new, const void* v_new, co
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1)
     return PD_ERR_CUDA;
   auto moderate = [](float x) { return x >= 0x1p-100f && x <= 0x1p100f; };
+  const float k6 = 6.f * d.k_scale, v6 = 6.f * d.v_scale;
   WriteArgs a{static_cast<const uint8_t*>(k_new), static_cast<const uint8_t*>(v_new), slot_mapping,
               static_cast<uint8_t*>(k_cache), static_cast<uint8_t*>(v_cache), static_cast<uint8_t*>(k_block_scale),
               static_cast<uint8_t*>(v_block_scale), error_flag, num_tokens * groups,
               static_cast<long long>(d.num_blocks) * d.block_size, static_cast<int>(groups), d.D / 16, d.Hkv,
-              d.block_size, d.k_scale, d.v_scale, !misaligned(k_new, 31) && !misaligned(v_new, 31), moderate(d.k_scale) && moderate(d.v_scale) ? 1 : 0};
-  const long long want = (a.items + kThreads - 1) / kThreads, cap = static_cast<long long>(sms) * 8;
+              d.block_size, d.k_scale, d.v_scale, k6, v6, 1.f / k6, 1.f / v6, !misaligned(k_new, 31) && !misaligned(v_new, 31), moderate(d.k_scale) && moderate(d.v_scale) ? 1 : 0};
+  const long long want = (a.items + kThreads - 1) / kThreads, cap = static_cast<long long>(sms) * 16;
   const unsigned grid = static_cast<unsigned>(want < cap ? want : cap);
   auto s = static_cast<cudaStream_t>(stream);
   if (d.kv_dtype == PD_KV_FP4_BF16) write_fp4_kernel<true><<<grid, kThreads, 0, s>>>(a);

@@ -27,6 +27,7 @@
 #include <cstdint>
 
 #include "pdecode.h"
+#include "ptx.cuh"
 
 namespace pd {
 namespace {
@@ -53,26 +54,6 @@ __device__ __forceinline__ uint32_t e4m3x2_of(float lo, float hi) {
 __device__ __forceinline__ uint32_t i8_bits(float t) {
   t = (t == t) ? fminf(fmaxf(t, -127.f), 127.f) : 0.f;
   return __float_as_uint(t + 12582912.f);
-}
-
-// Two fp32 values in one 64-bit register (low word = first), for the packed
-// f32x2 arithmetic of sm_100-class GPUs.
-__device__ __forceinline__ unsigned long long f2_pack(float lo, float hi) {
-  return static_cast<unsigned long long>(__float_as_uint(lo)) |
-         (static_cast<unsigned long long>(__float_as_uint(hi)) << 32);
-}
-__device__ __forceinline__ float f2_lo(unsigned long long v) { return __uint_as_float(static_cast<uint32_t>(v)); }
-__device__ __forceinline__ float f2_hi(unsigned long long v) { return __uint_as_float(static_cast<uint32_t>(v >> 32)); }
-__device__ __forceinline__ unsigned long long f2_mul(unsigned long long a, unsigned long long b) {
-  unsigned long long d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-__device__ __forceinline__ unsigned long long f2_fma(unsigned long long a, unsigned long long b,
-                                                     unsigned long long c) {
-  unsigned long long d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
 }
 
 // Correctly rounded quotients x / s of a pair (see the header): q0 = RN(x r),
