@@ -36,7 +36,7 @@ struct WriteArgs {
   int Hkv, block_size;
   float k_scale, v_scale, k_scale6, v_scale6, k_rcp6, v_rcp6;  // 6 scale, 1 / (6 scale)
   int aligned32;         // the new rows begin at a multiple of 32 bytes
-  int fast;              // scales within [2^-100, 2^100]: the corrected quotient is exact
+  int fast;              // scales within [2^-60, 2^60]: no residual that matters meets fp32's ends
 };
 
 struct Vec32 {
@@ -117,7 +117,7 @@ __device__ __forceinline__ void quantise(const Vec32& x, float scale, float scal
   if (fast) {
     const float q0 = amax * rcp6;
     t = fmaf(fmaf(-q0, scale6, amax), rcp6, q0);
-    if (amax == INFINITY) t = INFINITY;
+    if (!(amax < scale6 * 512.f)) t = INFINITY;  // (at its end anyway; q0 can overflow there)
   } else {
     t = __fdiv_rn(amax, scale6);
   }
@@ -186,13 +186,14 @@ extern "C" pd_status write_kv_cache_fp4(const void* k_new, const void* v_new, co
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1)
     return PD_ERR_CUDA;
-  auto moderate = [](float x) { return x >= 0x1p-100f && x <= 0x1p100f; };
+  auto moderate = [](float x) { return x >= 0x1p-60f && x <= 0x1p60f; };
   const float k6 = 6.f * d.k_scale, v6 = 6.f * d.v_scale;
   WriteArgs a{static_cast<const uint8_t*>(k_new), static_cast<const uint8_t*>(v_new), slot_mapping,
               static_cast<uint8_t*>(k_cache), static_cast<uint8_t*>(v_cache), static_cast<uint8_t*>(k_block_scale),
               static_cast<uint8_t*>(v_block_scale), error_flag, num_tokens * groups,
               static_cast<long long>(d.num_blocks) * d.block_size, static_cast<int>(groups), d.D / 16, d.Hkv,
-              d.block_size, d.k_scale, d.v_scale, k6, v6, 1.f / k6, 1.f / v6, !misaligned(k_new, 31) && !misaligned(v_new, 31), moderate(d.k_scale) && moderate(d.v_scale) ? 1 : 0};
+              d.block_size, d.k_scale, d.v_scale, k6, v6, 1.f / k6, 1.f / v6,
+              !misaligned(k_new, 31) && !misaligned(v_new, 31), moderate(d.k_scale) && moderate(d.v_scale) ? 1 : 0};
   const long long want = (a.items + kThreads - 1) / kThreads, cap = static_cast<long long>(sms) * 16;
   const unsigned grid = static_cast<unsigned>(want < cap ? want : cap);
   auto s = static_cast<cudaStream_t>(stream);
