@@ -354,6 +354,8 @@ typedef struct {
  *   free_count       build_block_tables, to which the blocks that the cut sequences no longer
  *                    need are appended, sequences in order, table entries in order; the count is
  *                    updated in place
+ *   dims             B, Hkv, D (a multiple of 16 up to 512; 4-bit caches: of 64), block_size, num_blocks,
+ *                    max_blocks_per_seq and kv_dtype are read; caches and scales 16-byte aligned
  *   workspace        pd_evict_workspace_bytes(dims, evict) bytes
  * A sequence with a bad length (PD_DEVERR_SEQ_LEN) is left alone (0 in a seq_lens_out
  * of its own). Rows whose table entry is outside [0, num_blocks) are not moved

@@ -424,7 +424,8 @@ pd_status check(const pd_dims* d, const pd_eviction* e) {
   if (e->keep < 1 || e->trigger < e->keep || e->first < 0 || e->recent < 0 ||
       static_cast<long long>(e->first) + e->recent > e->keep)
     return PD_ERR_SHAPE;
-  if (d->D > 512 || static_cast<long long>(d->max_blocks_per_seq) * d->block_size > (1ll << 30) ||
+  const bool fp4 = d->kv_dtype == PD_KV_FP4 || d->kv_dtype == PD_KV_FP4_BF16;  // (block scales move four bytes at a time)
+  if (d->D > 512 || (fp4 && d->D % 64 != 0) || static_cast<long long>(d->max_blocks_per_seq) * d->block_size > (1ll << 30) ||
       static_cast<long long>(d->num_blocks) * d->block_size * d->Hkv > 0x7fffffffll ||
       static_cast<long long>(d->B) * d->Hkv > (1 << 22))
     return PD_ERR_UNSUPPORTED;
@@ -513,14 +514,16 @@ extern "C" pd_status evict_kv_cache(void* k_cache, void* v_cache, void* k_block_
   const bool two_byte = d.kv_dtype == PD_KV_F16 || d.kv_dtype == PD_KV_BF16;
   const int row = fp4 ? d.D / 2 : two_byte ? 2 * d.D : d.D;
   auto add = [&](void* base, int bytes, bool keys_first) {
-    const int vec = bytes % 16 == 0 ? 16 : bytes % 8 == 0 ? 8 : bytes % 4 == 0 ? 4 : 0;
+    const int vec = bytes % 16 == 0 ? 16 : bytes % 8 == 0 ? 8 : 4;
     a.arrays[a.n_arrays++] = MoveArray{static_cast<uint8_t*>(base), bytes, vec, keys_first, 1};
-    return vec != 0;
   };
-  bool ok = add(k_cache, row, !fp4) && add(v_cache, row, !fp4);
-  if (fp4) ok = ok && add(k_block_scale, d.D / 16, false) && add(v_block_scale, d.D / 16, false);
-  ok = ok && add(key_weights, 4, false);
-  if (!ok) return PD_ERR_UNSUPPORTED;
+  add(k_cache, row, !fp4);
+  add(v_cache, row, !fp4);
+  if (fp4) {
+    add(k_block_scale, d.D / 16, false);
+    add(v_block_scale, d.D / 16, false);
+  }
+  add(key_weights, 4, false);
   // in place: columns of at least 32 bytes, while the CTAs are fewer than two per SM
   const long long units = static_cast<long long>(d.B) * d.Hkv;
   a.parts = 1;
@@ -544,10 +547,11 @@ extern "C" pd_status evict_kv_cache(void* k_cache, void* v_cache, void* k_block_
   a.cluster = 1;
   while (a.cluster < 8 && units * a.cluster * 2 <= sms && cap / (2 * a.cluster) >= 1024) a.cluster *= 2;
   const int smem = static_cast<int>(std::min<long long>((cap + a.cluster - 1) / a.cluster, kCachedKeys)) * 4;
-  if (err == cudaSuccess)
-    err = launch_pdl(select_kernel, static_cast<int>(units * a.cluster), kSelectThreads, smem, s, a.cluster, a);
   const long long ctas = units * a.slices * a.parts;
   if (ctas > 0x7fffffffll) return PD_ERR_UNSUPPORTED;
+  const WorkspaceLock lock(workspace, true);
+  if (err == cudaSuccess)
+    err = launch_pdl(select_kernel, static_cast<int>(units * a.cluster), kSelectThreads, smem, s, a.cluster, a);
   if (err == cudaSuccess) err = launch_pdl(move_kernel, static_cast<int>(ctas), kMoveThreads, 0, s, 1, a);
   if (err == cudaSuccess && free_blocks != nullptr) err = launch_pdl(free_tail_kernel, 1, 1024, 0, s, 1, a);
   return err == cudaSuccess ? PD_OK : PD_ERR_CUDA;

@@ -5,9 +5,32 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <mutex>
+
 #include "decode_kernel.cuh"
 
 namespace pd {
+
+// Two threads may call on one stream with one workspace (the Python calls keep one
+// per stream). The launch that fills it and those that read it are several launches,
+// which no other call's may come between: this lock, one of a few picked by the
+// workspace's address, is held around them all. A thread that waits on a full launch
+// queue holds it, but no call on another workspace needs it to make room.
+std::mutex& workspace_mutex(const void* workspace);
+class WorkspaceLock {  // (std::unique_lock's out-of-line members would be exported)
+ public:
+  WorkspaceLock(const void* workspace, bool needed) : m_(needed ? &workspace_mutex(workspace) : nullptr) {
+    if (m_) m_->lock();
+  }
+  ~WorkspaceLock() {
+    if (m_) m_->unlock();
+  }
+  WorkspaceLock(const WorkspaceLock&) = delete;
+  WorkspaceLock& operator=(const WorkspaceLock&) = delete;
+
+ private:
+  std::mutex* m_;
+};
 
 struct KernelShape {
   int threads;      // threads per CTA

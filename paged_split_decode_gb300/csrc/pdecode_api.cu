@@ -55,33 +55,14 @@ cudaError_t launch_decode(int D, int kv, int nt, int grouped, const CUtensorMap&
                          : launch_f16_d256(nt, grouped, tk, tv, p, grid, s);
 }
 
-namespace {
-
-constexpr unsigned long long kTimeoutNs = 2000000000ull;  // 2 s per pipeline wait (default)
-// Two threads may call on one stream with one workspace (the Python calls keep one
-// per stream). The decode and the join that reads its partials are two launches,
-// which no other call's may come between: this lock, one of a few picked by the
-// workspace's address, is held around both. A thread that waits on a full launch
-// queue holds it, but no call on another workspace needs it to make room.
 std::mutex& workspace_mutex(const void* workspace) {
   static std::mutex locks[61];
   return locks[(reinterpret_cast<uintptr_t>(workspace) >> 8) % 61];
 }
-class WorkspaceLock {  // (std::unique_lock's out-of-line members would be exported)
- public:
-  WorkspaceLock(const void* workspace, bool needed) : m_(needed ? &workspace_mutex(workspace) : nullptr) {
-    if (m_) m_->lock();
-  }
-  ~WorkspaceLock() {
-    if (m_) m_->unlock();
-  }
-  WorkspaceLock(const WorkspaceLock&) = delete;
-  WorkspaceLock& operator=(const WorkspaceLock&) = delete;
 
- private:
-  std::mutex* m_;
-};
+namespace {
 
+constexpr unsigned long long kTimeoutNs = 2000000000ull;  // 2 s per pipeline wait (default)
 std::atomic<unsigned long long> g_wait_limit_ns{kTimeoutNs};
 std::atomic<int> g_inject{0};
 

@@ -46,14 +46,10 @@ constexpr int scored_stages() {
 template <int D, int KV, int NT, int HG, int W, int KG, int KT, int MINB>
 using ScoredCfgFor = ScoredCfg<D, KV, NT, HG, W, KG, KT, scored_stages<D, KV, NT, HG, W, KG, KT, MINB>(), MINB>;
 
-#ifndef PD_V_C1H
-#define PD_V_C1H 4, 1, 1, 1, 1
-#endif
 template <int D, int KV>
 struct ScoredShapes {
-  static constexpr bool kByte = cache_kind(KV) == kKvFp8 || cache_kind(KV) == kKvInt8;
   // row tiles, heads per tile, warps per head, key groups, tiles per step, CTAs per SM
-  using C1H = ScoredCfgFor<D, KV, 1, PD_V_C1H>;
+  using C1H = ScoredCfgFor<D, KV, 1, 4, 1, 1, 1, 1>;
   using C1 = ScoredCfgFor<D, KV, 1, 1, 1, 3, 1, 2>;
   using C2 = ScoredCfgFor<D, KV, 2, 1, 2, 4, 1, 1>;
   using C3 = ScoredCfgFor<D, KV, 3, 1, 4, 2, 1, 1>;
