@@ -415,12 +415,12 @@ def _fast():
             mod.init(*(ctypes.cast(fn, ctypes.c_void_p).value for fn in (
                 lib.decode_paged_diff, lib.pd_diff_workspace_bytes, lib.build_block_tables, lib.release_blocks,
                 lib.rms_norm, lib.pd_status_str, lib.decode_paged_scored, lib.pd_scored_workspace_bytes,
-                lib.write_kv_cache_fp4, lib.evict_kv_cache, lib.pd_evict_workspace_bytes)), DecodeError, _call_workspace)
+                lib.write_kv_cache_fp4, lib.evict_kv_cache, lib.pd_evict_workspace_bytes)), DecodeError, _diff_workspace)
             _bind = mod
     return _bind
 
 
-def _call_workspace(need, index, stream):
+def _diff_workspace(need, index, stream):
     """The workspace of a call of the compiled binding that brought none. A captured
     call keeps one of its own in the graph's pool, as graphs may be replayed at
     the same time; else the (device, stream) one of ``get_workspace``."""

@@ -7,13 +7,12 @@
 // HBM-bound: K and V are read once. The decode's frame (decode_kernel.cuh: balanced
 // ranges of 16-key tiles, one TMA producer warp, a ring of 128B-swizzled stages,
 // bounded waits, partials and combine) with the differential decode's consumers, for one map:
-//  * W = 1, one row tile of 8 query rows per KV head: a warp serves a head alone, all
-//    of D, so that a score is capped and biased by one lane only (two warps that split
-//    D would both do it).
-//  * W = 2 or 4, as many row tiles or fewer: warp w scores row tile w over all of D, the
-//    warps swap their packed P fragments (one barrier a step), and each accumulates every
-//    row tile over 1 / W of V's dims.
-//  * KG key groups of such warps take the ring's steps in turn and merge at the end of a piece.
+//  * A warp serves one row tile of 8 query rows of one head, all of D, so that a score is
+//    capped and biased by one lane only (two warps that split D would both do it) and no warp
+//    waits for another. RG such warps read the same tile where a head has more rows. (Warps that
+//    split V's dims and exchange their packed P at a barrier a step, 18 rows over e4m3 caches,
+//    B = 8, L = 4096: 41.1 us against 34.8, fp16 caches 44.2 against 33.1.)
+//  * KG key groups of such warps take the ring's tiles in turn and merge at the end of a piece.
 // A tile is one box of a 4-D tensor map with keys before heads (no bank conflicts). The
 // softmax reference is raised only when a score passes it by 2^8: the common step has
 // no shuffles and no rescaling.
@@ -24,9 +23,9 @@
 
 namespace pd {
 
-template <int D_, int KV_, int NT_, int HG_, int W_, int KG_, int KT_, int NS_, int MINB_>
+template <int D_, int KV_, int HG_, int RG_, int KG_, int NS_, int MINB_>
 struct ScoredCfg {
-  static constexpr int D = D_, KV = cache_kind(KV_), NT = NT_, HG = HG_, W = W_, KG = KG_, KT = KT_, NS = NS_;
+  static constexpr int D = D_, KV = cache_kind(KV_), HG = HG_, RG = RG_, KG = KG_, NS = NS_;
   static constexpr int kMinBlocks = MINB_;
   static constexpr bool BYTE = KV == kKvFp8 || KV == kKvInt8;
   static constexpr bool BF16 = KV == kKvBf16;   // bfloat16 operands; byte kinds use fp16 ones
@@ -42,42 +41,32 @@ struct ScoredCfg {
   // the output's norm: fp16 3.2e-4 with one, 2.1e-4 with two, bfloat16 2.5e-3 and
   // 1.7e-3; a bfloat16 output over fp16 operands hides it).
   static constexpr int PP = QB && !BF16 ? 1 : 2;
-  static constexpr int kGroupWarps = HG * W;    // warps of a key group
+  static constexpr int kGroupWarps = HG * RG;   // warps of a key group
   static constexpr int kConsumerWarps = kGroupWarps * KG;
   static constexpr int kConsumerThreads = kConsumerWarps * 32;
   // Eight consumer warps alone on an SM take the registers that the producer's
   // warpgroup gives up (256 x 216 + 128 x 56 of the launch's 384 x 168).
   static constexpr bool kSplitRegs = kConsumerWarps == 8 && MINB_ == 1;
   static constexpr int kThreads = kConsumerThreads + (kSplitRegs ? 128 : 32);
-  static constexpr int RH = NT * 8;              // partial rows per head
+  static constexpr int RH = RG * 8;              // partial rows per head
   static constexpr int RP = HG * RH;             // per unit
-  static constexpr bool kMerge = KG > 1 || W > 1;  // the epilogue goes through shared memory
+  static constexpr bool kMerge = KG > 1;         // the epilogue goes through shared memory
   static constexpr int kDP = D + 4;              // merge row pitch (floats)
   static constexpr int kMergeO = kMerge ? RP * kDP * 4 : 0;
   static constexpr int kMergeML = kMerge ? KG * RP * 8 : 0;
-  // a head's exchange, double-buffered: packed P [operand][row tile][lane], rescale factors
-  // [row tile][row], a flag per warp
-  static constexpr int kXPlane = NT * 32 * 8 * KT;
-  static constexpr int kXP = kXPlane * PP;
-  static constexpr int kXOne = kXP + NT * 32 + 16;
-  static constexpr int kX = W > 1 ? HG * KG * 2 * kXOne : 0;
   static constexpr int kOffMergeML = NS * kStageBytes + kMergeO;
-  static constexpr int kOffX = kOffMergeML + kMergeML;
-  static constexpr int kOffBars = kOffX + kX;
+  static constexpr int kOffBars = kOffMergeML + kMergeML;
   static constexpr int kOffPre = kOffBars + 2 * NS * 8;
   static constexpr int kSmemBytes = (kOffPre + (kMaxAutoB + 1) * 4 + 15) / 16 * 16 + 1024;
-  // a stage always belongs to the same key group, which takes KT consecutive ring positions a step
-  static_assert(KG == 1 || NS % (KG * KT) == 0, "ring stages must be a multiple of the key groups' steps");
-  static_assert(KT == 1 || KT == 2, "one or two tiles a step");
-  static_assert(NT <= W && (W == 1 || W == 2 || W == 4), "a warp scores one row tile");
-  static_assert(HG * KG <= 14, "named barriers 2.. serve the heads' warps");
+  // a stage always belongs to the same key group
+  static_assert(NS % KG == 0, "ring stages must be a multiple of the key groups");
 };
 
 template <class Cfg>
 __global__ void __launch_bounds__(Cfg::kThreads, Cfg::kMinBlocks)
     decode_scored_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                          const ScoredParams p) {
-  constexpr int D = Cfg::D, NS = Cfg::NS, NT = Cfg::NT;
+  constexpr int D = Cfg::D, NS = Cfg::NS;
   constexpr bool BYTE = Cfg::BYTE, BF16 = Cfg::BF16;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -173,18 +162,16 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::kMinBlocks)
   }
 
   // -------------------------------------------------------------- consumers
-  constexpr int W = Cfg::W, KG = Cfg::KG, KT = Cfg::KT, HG = Cfg::HG, PP = Cfg::PP;
-  const int w = warp % W;                    // warp of the head: its row tile, its 1 / W of V's dims
-  const int kg = (warp / W) % KG;            // key group
-  const int th = warp / (W * KG);            // head of the tile
-  const bool scores = w < NT;                // (W > NT: a warp without a row tile)
+  constexpr int RG = Cfg::RG, KG = Cfg::KG, HG = Cfg::HG, PP = Cfg::PP;
+  const int kg = warp % KG;                  // key group
+  const int rt = (warp / KG) % RG;           // row tile
+  const int th = warp / (KG * RG);           // head of the tile
   const int g = lane >> 2, t4 = lane & 3;
   constexpr int KS = D / 16;                 // k-steps of S^T
-  constexpr int MTW = D / 16 / W;            // m-tiles of 16 output dims of this warp
+  constexpr int MT = D / 16;                 // m-tiles of 16 output dims
   float* merge_o = reinterpret_cast<float*>(smem + NS * Cfg::kStageBytes);
   float* merge_ml = reinterpret_cast<float*>(smem + Cfg::kOffMergeML);
   const uint32_t smem0 = smem_u32(smem);
-  const uint32_t xch = smem0 + Cfg::kOffX + (th * KG + kg) * 2 * Cfg::kXOne;
   // One-byte tiles: 16-byte chunk 4 s + t4 of a 64-dim super-step s. The eight lanes of a
   // shared-memory phase hold two accumulator rows of four chunks, so rows 2i and 2i + 1
   // stand for keys whose swizzle phases differ by 4; and the four keys that a V read
@@ -205,7 +192,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::kMinBlocks)
     }
   }
   uint32_t qf[KS][2];
-  float o[MTW][NT][4];
+  float o[MT][4];
   uint32_t q = 0;                            // ring position of the piece's first tile
   bool ok = true;
 
@@ -218,9 +205,9 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::kMinBlocks)
     int hi_r[2];                              // last causal key of rows 2 t4, 2 t4 + 1 (padded rows: -1)
     float m_r[2] = {-INFINITY, -INFINITY}, l_r[2] = {0.f, 0.f};
     {
-      const int r = w * 8 + g;
+      const int r = rt * 8 + g;
       const __half* qrow = nullptr;
-      if (scores && r < pc.R && pc.ntiles > 0)
+      if (r < pc.R && pc.ntiles > 0)
         qrow = p.q + (static_cast<long long>(pc.q0 + r / p.G) * p.Hq + (pc.kh + th) * p.G + r % p.G) * D;
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks) {
@@ -231,7 +218,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::kMinBlocks)
       }
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        const int rc = w * 8 + 2 * t4 + c;
+        const int rc = rt * 8 + 2 * t4 + c;
         hi_r[c] = rc < pc.R ? pc.L - pc.qlen + rc / p.G : -1;
         if (p.slopes != nullptr && rc < pc.R) slope[c] = __ldg(p.slopes + (pc.kh + th) * p.G + rc % p.G) * kLog2e;
       }
@@ -258,300 +245,199 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::kMinBlocks)
           qf[ks][h] = pack_half2(__uint_as_float(qf[ks][h] << 16) * up, __uint_as_float(qf[ks][h] & 0xffff0000u) * up);
     }
 #pragma unroll
-    for (int mt = 0; mt < MTW; ++mt)
-#pragma unroll
-      for (int n = 0; n < NT; ++n) o[mt][n][0] = o[mt][n][1] = o[mt][n][2] = o[mt][n][3] = 0.f;
+    for (int mt = 0; mt < MT; ++mt) o[mt][0] = o[mt][1] = o[mt][2] = o[mt][3] = 0.f;
 
-    // ---- this key group's steps: KT ring positions each, dealt to the groups
-    // by ring position (a piece may start or end inside a step)
-    const int lead = KG > 1 && KT > 1 ? static_cast<int>(q % KT) : 0;
-    const uint32_t step0 = (q - lead) / KT;
-    const int last = ntiles > 0 ? ntiles + lead : 0;
+    // ---- this key group's tiles, dealt to the groups by ring position
     // A step is compiled twice: for tiles that every row sees whole, and for the others
-    // (EDGE: masks, values, a missing tile), so that the common one has no branch.
+    // (EDGE: masks, values), so that the common one has no branch.
     auto step = [&](const int st, auto edge_step) __attribute__((always_inline)) {
       constexpr bool EDGE = decltype(edge_step)::value;
-      const int k0 = st * KT - lead;
-      bool have[KT];
-      int tile[KT];  // a step's missing tile is its other one over again, masked
+      const uint32_t stage = (q + st) % NS;
+      const int key0 = piece_tile(p, pc, st) * kTileKeys;
+      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(full0 + 8 * stage, ((q + st) / NS) & 1, p.timeout_ns));
+      if (!ok) return;
+      uint32_t pf[2 * PP];          // P^T fragments
+      float x[4];                   // scores (log2 units)
+      // ---- S^T: 16 keys x 8 rows
+      const uint32_t ka = smem0 + stage * Cfg::kStageBytes + k_off;
+      float sa[4] = {0.f, 0.f, 0.f, 0.f}, sb[4] = {0.f, 0.f, 0.f, 0.f};
+      if constexpr (!BYTE) {
 #pragma unroll
-      for (int j = 0; j < KT; ++j) {
-        have[j] = !EDGE || (k0 + j >= 0 && k0 + j < ntiles);
-        if (ok && have[j])
-          ok = __all_sync(0xffffffffu, mbar_wait(full0 + 8 * ((q + k0 + j) % NS), ((q + k0 + j) / NS) & 1, p.timeout_ns));
-      }
-#pragma unroll
-      for (int j = 0; j < KT; ++j) tile[j] = have[j] ? k0 + j : k0 + (KT - 1 - j);
-      if (!ok) {  // gave up: keep the head's barrier sequence
-        if constexpr (W > 1) named_bar_sync(2 + th * KG + kg, W * 32);
-        return;
-      }
-      uint32_t pf[KT][NT][2 * PP];  // P^T fragments of every row tile
-      float x[KT][4];               // this warp's scores (log2 units)
-      bool raise = false;
-      float al[2];
-      uint32_t pk[KT][2 * PP];
-      if (W == NT || scores) {
-#pragma unroll
-        for (int j = 0; j < KT; ++j) {
-          // ---- S^T: 16 keys x 8 rows
-          const uint32_t ka = smem0 + ((q + tile[j]) % NS) * Cfg::kStageBytes + k_off;
-          float sa[4] = {0.f, 0.f, 0.f, 0.f}, sb[4] = {0.f, 0.f, 0.f, 0.f};
-          if constexpr (!BYTE) {
-#pragma unroll
-            for (int ks = 0; ks < KS; ++ks) {
-              uint32_t a[4];
-              ldsm_x4((ka ^ ((ks & 3) * 32)) + (ks >> 2) * Cfg::kSlabBytes, a);
-              if (ks & 1) mma_op<BF16>(sb, a, qf[ks][0], qf[ks][1]);
-              else mma_op<BF16>(sa, a, qf[ks][0], qf[ks][1]);
-            }
-          } else {
-#pragma unroll
-            for (int sup = 0; sup < KS / 4; ++sup) {  // 64-dim super-steps: two a slab
-              const uint32_t at = (ka ^ ((sup & 1) * 64)) + (sup >> 1) * Cfg::kSlabBytes;
-              const uint4 w0 = lds_v4_tile(at), w8 = lds_v4_tile(at + 8 * 128);
-              const uint32_t wa[4] = {w0.x, w0.y, w0.z, w0.w};
-              const uint32_t wb[4] = {w8.x, w8.y, w8.z, w8.w};
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const uint32_t xa = byte_word_prep<Cfg::KV>(wa[i]), xb = byte_word_prep<Cfg::KV>(wb[i]);
-                const uint32_t a[4] = {byte_pair_to_half2<Cfg::KV>(xa, false), byte_pair_to_half2<Cfg::KV>(xb, false),
-                                       byte_pair_to_half2<Cfg::KV>(xa, true), byte_pair_to_half2<Cfg::KV>(xb, true)};
-                if (i & 1) mma_op<BF16>(sb, a, qf[sup * 4 + i][0], qf[sup * 4 + i][1]);
-                else mma_op<BF16>(sa, a, qf[sup * 4 + i][0], qf[sup * 4 + i][1]);
-              }
-            }
-          }
-          const int key0 = piece_tile(p, pc, tile[j]) * kTileKeys, j0 = key0 + kg0;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) x[j][e] = (sa[e] + sb[e]) * sl2r[e & 1];
-          if (p.cap_out > 0.f) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) x[j][e] = p.cap_out * tanh_f32(x[j][e] * p.cap_u);
-          }
-          if (p.slopes != nullptr) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              x[j][e] -= slope[e & 1] * static_cast<float>(abs(j0 + (e >> 1) * 8 - hi_r[e & 1]));
-          }
-          if constexpr (EDGE) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (!have[j] || !row_sees(p, pc, w * 8 + 2 * t4 + (e & 1), j0 + (e >> 1) * 8)) x[j][e] = -INFINITY;
-          }
-          if (p.scores != nullptr && have[j]) {  // [key][row] of this tile and row tile
-            float* dst = p.scores + ((static_cast<long long>(pc.b) * p.Hkv + pc.kh + th) * p.max_blocks *
-                                         p.tiles_per_block + key0 / kTileKeys) * (NT * 128) + w * 128 + kg0 * 8 + 2 * t4;
-            __stcg(reinterpret_cast<float2*>(dst), make_float2(x[j][0], x[j][1]));
-            __stcg(reinterpret_cast<float2*>(dst + 64), make_float2(x[j][2], x[j][3]));
-          }
+        for (int ks = 0; ks < KS; ++ks) {
+          uint32_t a[4];
+          ldsm_x4((ka ^ ((ks & 3) * 32)) + (ks >> 2) * Cfg::kSlabBytes, a);
+          if (ks & 1) mma_op<BF16>(sb, a, qf[ks][0], qf[ks][1]);
+          else mma_op<BF16>(sa, a, qf[ks][0], qf[ks][1]);
         }
-        // ---- online softmax. P = 2^(x - m + kUp) is relative to a reference m that is
-        // raised to the running maximum only when a score passes it by more than
-        // 2^kLazy: P stays at most 2^15, and 2^kUp moves fp16's last bit from 2^-24 to
-        // 2^-31 of the reference's weight.
-        constexpr float kLazy = 8.f, kUp = 15.f - kLazy;
-#pragma unroll
-        for (int j = 0; j < KT; ++j)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) raise |= x[j][e] - m_r[e & 1] > kLazy;  // (no key seen: m = -inf)
-        raise = __any_sync(0xffffffffu, raise);
-        if (raise) {
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            float mx = fmaxf(x[0][c], x[0][2 + c]);
-            if constexpr (KT > 1) mx = fmaxf(mx, fmaxf(x[KT - 1][c], x[KT - 1][2 + c]));
-#pragma unroll
-            for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-            const float old = m_r[c], mn = fmaxf(old, mx);
-            al[c] = old == -INFINITY ? 1.f : ex2(old - mn);  // (nothing accumulated yet: keep factor 1)
-            m_r[c] = mn;
-            l_r[c] *= al[c];
-          }
-          if constexpr (W == 1) {
-#pragma unroll
-            for (int mt = 0; mt < MTW; ++mt) {
-              o[mt][0][0] *= al[0]; o[mt][0][1] *= al[1];
-              o[mt][0][2] *= al[0]; o[mt][0][3] *= al[1];
-            }
-          }
-        }
-        float nb[2];
-#pragma unroll
-        for (int c = 0; c < 2; ++c) nb[c] = m_r[c] == -INFINITY ? 0.f : kUp - m_r[c];
-#pragma unroll
-        for (int j = 0; j < KT; ++j) {
-          const float p00 = ex2(x[j][0] + nb[0]), p01 = ex2(x[j][1] + nb[1]), p10 = ex2(x[j][2] + nb[0]),
-                      p11 = ex2(x[j][3] + nb[1]);
-          l_r[0] += p00 + p10;
-          l_r[1] += p01 + p11;
-          const uint32_t w0 = pack2<BF16>(p00, p01), w1 = pack2<BF16>(p10, p11);
-          pk[j][0] = movmatrix_trans(w0);
-          pk[j][1] = movmatrix_trans(w1);
-          if constexpr (PP == 2) {
-            const float2 h0 = unpack2<BF16>(w0), h1 = unpack2<BF16>(w1);
-            pk[j][2] = movmatrix_trans(pack2<BF16>(p00 - h0.x, p01 - h0.y));
-            pk[j][3] = movmatrix_trans(pack2<BF16>(p10 - h1.x, p11 - h1.y));
-          }
-        }
-      }
-      if constexpr (W == 1) {
-#pragma unroll
-        for (int j = 0; j < KT; ++j)
-#pragma unroll
-          for (int i = 0; i < 2 * PP; ++i) pf[j][0][i] = pk[j][i];
       } else {
-        const uint32_t xcur = xch + (static_cast<uint32_t>(st / KG) & 1u) * Cfg::kXOne;
-        const uint32_t xa = xcur + Cfg::kXP, flags = xa + NT * 32;
-        if (scores) {
-          const uint32_t at = xcur + (w * 32 + lane) * 8 * KT;
 #pragma unroll
-          for (int h = 0; h < PP; ++h) {
-            if constexpr (KT == 1) sts_v2(at + h * Cfg::kXPlane, pk[0][2 * h], pk[0][2 * h + 1]);
-            else sts_v4(at + h * Cfg::kXPlane, pk[0][2 * h], pk[0][2 * h + 1], pk[KT - 1][2 * h], pk[KT - 1][2 * h + 1]);
-          }
-          if (raise && g == 0) sts_f2(xa + w * 32 + 8 * t4, al[0], al[1]);
-        }
-        if (lane == 0) sts_b32(flags + 4 * w, raise ? 1u : 0u);
-        named_bar_sync(2 + th * KG + kg, W * 32);
+        for (int sup = 0; sup < KS / 4; ++sup) {  // 64-dim super-steps: two a slab
+          const uint32_t at = (ka ^ ((sup & 1) * 64)) + (sup >> 1) * Cfg::kSlabBytes;
+          const uint4 w0 = lds_v4_tile(at), w8 = lds_v4_tile(at + 8 * 128);
+          const uint32_t wa[4] = {w0.x, w0.y, w0.z, w0.w};
+          const uint32_t wb[4] = {w8.x, w8.y, w8.z, w8.w};
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int h = 0; h < PP; ++h) {
-            const uint32_t at = xcur + h * Cfg::kXPlane + (n * 32 + lane) * 8 * KT;
-            if constexpr (KT == 1) {
-              const uint2 v = lds_v2(at);
-              pf[0][n][2 * h] = v.x;
-              pf[0][n][2 * h + 1] = v.y;
-            } else {
-              const uint4 v = lds_v4(at);
-              pf[0][n][2 * h] = v.x;
-              pf[0][n][2 * h + 1] = v.y;
-              pf[KT - 1][n][2 * h] = v.z;
-              pf[KT - 1][n][2 * h + 1] = v.w;
-            }
-          }
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          uint32_t f;
-          asm volatile("ld.shared.b32 %0, [%1];" : "=r"(f) : "r"(flags + 4 * n) : "memory");
-          if (warp_uniform(f)) {
-            const float2 a2 = lds_f2(xa + n * 32 + 8 * t4);
-#pragma unroll
-            for (int mt = 0; mt < MTW; ++mt) {
-              o[mt][n][0] *= a2.x; o[mt][n][1] *= a2.y;
-              o[mt][n][2] *= a2.x; o[mt][n][3] *= a2.y;
-            }
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t xa = byte_word_prep<Cfg::KV>(wa[i]), xb = byte_word_prep<Cfg::KV>(wb[i]);
+            const uint32_t a[4] = {byte_pair_to_half2<Cfg::KV>(xa, false), byte_pair_to_half2<Cfg::KV>(xb, false),
+                                   byte_pair_to_half2<Cfg::KV>(xa, true), byte_pair_to_half2<Cfg::KV>(xb, true)};
+            if (i & 1) mma_op<BF16>(sb, a, qf[sup * 4 + i][0], qf[sup * 4 + i][1]);
+            else mma_op<BF16>(sa, a, qf[sup * 4 + i][0], qf[sup * 4 + i][1]);
           }
         }
       }
-
-      // ---- O^T += V^T P^T over this warp's dims
+      const int j0 = key0 + kg0;
 #pragma unroll
-      for (int j = 0; j < KT; ++j) {
-        const uint32_t stage = (q + tile[j]) % NS, sbase = smem0 + stage * Cfg::kStageBytes;
-        const int key0 = piece_tile(p, pc, tile[j]) * kTileKeys;
-        // V of keys at or past the sequence's end is zeroed (its bits may be anything)
-        const bool tail = EDGE && key0 + kTileKeys > seq_len;
-        auto product = [&](int mtl, uint32_t (&a)[4]) {
-          if constexpr (EDGE && Cfg::KV != kKvInt8) {
-            // Rows that do not see a key have a zero weight for it, which times a NaN or an
-            // infinity of its V is NaN: such elements are taken out, and a product of ones (the
-            // elements' places, the rows that see the key) marks the outputs that they belong to.
-            uint32_t odd[4], any = 0;
+      for (int e = 0; e < 4; ++e) x[e] = (sa[e] + sb[e]) * sl2r[e & 1];
+      if (p.cap_out > 0.f) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) any |= odd[i] = not_finite_16<BF16>(a[i]);
-            if (__any_sync(0xffffffffu, any != 0)) {
-              constexpr uint32_t kOne = BF16 ? 0x3f803f80u : 0x3c003c00u;
+        for (int e = 0; e < 4; ++e) x[e] = p.cap_out * tanh_f32(x[e] * p.cap_u);
+      }
+      if (p.slopes != nullptr) {
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                a[i] &= ~odd[i];
-                odd[i] &= kOne;
-              }
-              const int ja = key0 + key_of(2 * t4), jb = key0 + key_of(2 * t4 + 1);
+        for (int e = 0; e < 4; ++e)
+          x[e] -= slope[e & 1] * static_cast<float>(abs(j0 + (e >> 1) * 8 - hi_r[e & 1]));
+      }
+      if constexpr (EDGE) {
 #pragma unroll
-              for (int n = 0; n < NT; ++n) {
-                const int r = n * 8 + g;
-                const uint32_t see[2] = {
-                    kOne & ((row_sees(p, pc, r, ja) ? 0xffffu : 0u) | (row_sees(p, pc, r, jb) ? 0xffff0000u : 0u)),
-                    kOne & ((row_sees(p, pc, r, ja + 8) ? 0xffffu : 0u) | (row_sees(p, pc, r, jb + 8) ? 0xffff0000u : 0u))};
-                float mark[4] = {0.f, 0.f, 0.f, 0.f};
-                mma_op<BF16>(mark, odd, see[0], see[1]);
+        for (int e = 0; e < 4; ++e)
+          if (!row_sees(p, pc, rt * 8 + 2 * t4 + (e & 1), j0 + (e >> 1) * 8)) x[e] = -INFINITY;
+      }
+      if (p.scores != nullptr) {  // [key][row] of this tile and row tile
+        float* dst = p.scores + ((static_cast<long long>(pc.b) * p.Hkv + pc.kh + th) * p.max_blocks *
+                                     p.tiles_per_block + key0 / kTileKeys) * (RG * 128) + rt * 128 + kg0 * 8 + 2 * t4;
+        __stcg(reinterpret_cast<float2*>(dst), make_float2(x[0], x[1]));
+        __stcg(reinterpret_cast<float2*>(dst + 64), make_float2(x[2], x[3]));
+      }
+      // ---- online softmax. P = 2^(x - m + kUp) is relative to a reference m that is
+      // raised to the running maximum only when a score passes it by more than
+      // 2^kLazy: P stays at most 2^15, and 2^kUp moves fp16's last bit from 2^-24 to
+      // 2^-31 of the reference's weight.
+      constexpr float kLazy = 8.f, kUp = 15.f - kLazy;
+      bool raise = false;
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                  if (mark[e] > 0.f) o[mtl][n][e] = __uint_as_float(0x7fffffffu);
-              }
+      for (int e = 0; e < 4; ++e) raise |= x[e] - m_r[e & 1] > kLazy;  // (no key seen: m = -inf)
+      if (__any_sync(0xffffffffu, raise)) {
+        float al[2];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          float mx = fmaxf(x[c], x[2 + c]);
+#pragma unroll
+          for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+          const float old = m_r[c], mn = fmaxf(old, mx);
+          al[c] = old == -INFINITY ? 1.f : ex2(old - mn);  // (nothing accumulated yet: keep factor 1)
+          m_r[c] = mn;
+          l_r[c] *= al[c];
+        }
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          o[mt][0] *= al[0]; o[mt][1] *= al[1];
+          o[mt][2] *= al[0]; o[mt][3] *= al[1];
+        }
+      }
+      float nb[2];
+#pragma unroll
+      for (int c = 0; c < 2; ++c) nb[c] = m_r[c] == -INFINITY ? 0.f : kUp - m_r[c];
+      const float p00 = ex2(x[0] + nb[0]), p01 = ex2(x[1] + nb[1]), p10 = ex2(x[2] + nb[0]), p11 = ex2(x[3] + nb[1]);
+      l_r[0] += p00 + p10;
+      l_r[1] += p01 + p11;
+      const uint32_t w0 = pack2<BF16>(p00, p01), w1 = pack2<BF16>(p10, p11);
+      pf[0] = movmatrix_trans(w0);
+      pf[1] = movmatrix_trans(w1);
+      if constexpr (PP == 2) {
+        const float2 h0 = unpack2<BF16>(w0), h1 = unpack2<BF16>(w1);
+        pf[2] = movmatrix_trans(pack2<BF16>(p00 - h0.x, p01 - h0.y));
+        pf[3] = movmatrix_trans(pack2<BF16>(p10 - h1.x, p11 - h1.y));
+      }
+      // ---- O^T += V^T P^T
+      const uint32_t sbase = smem0 + stage * Cfg::kStageBytes;
+      // V of keys at or past the sequence's end is zeroed (its bits may be anything)
+      const bool tail = EDGE && key0 + kTileKeys > seq_len;
+      auto product = [&](int mtl, uint32_t (&a)[4]) {
+        if constexpr (EDGE && Cfg::KV != kKvInt8) {
+          // Rows that do not see a key have a zero weight for it, which times a NaN or an
+          // infinity of its V is NaN: such elements are taken out, and a product of ones (the
+          // elements' places, the rows that see the key) marks the outputs that they belong to.
+          uint32_t odd[4], any = 0;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) any |= odd[i] = not_finite_16<BF16>(a[i]);
+          if (__any_sync(0xffffffffu, any != 0)) {
+            constexpr uint32_t kOne = BF16 ? 0x3f803f80u : 0x3c003c00u;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              a[i] &= ~odd[i];
+              odd[i] &= kOne;
             }
+            const int ja = key0 + key_of(2 * t4), jb = key0 + key_of(2 * t4 + 1);
+            const int r = rt * 8 + g;
+            const uint32_t see[2] = {
+                kOne & ((row_sees(p, pc, r, ja) ? 0xffffu : 0u) | (row_sees(p, pc, r, jb) ? 0xffff0000u : 0u)),
+                kOne & ((row_sees(p, pc, r, ja + 8) ? 0xffffu : 0u) | (row_sees(p, pc, r, jb + 8) ? 0xffff0000u : 0u))};
+            float mark[4] = {0.f, 0.f, 0.f, 0.f};
+            mma_op<BF16>(mark, odd, see[0], see[1]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (mark[e] > 0.f) o[mtl][e] = __uint_as_float(0x7fffffffu);
           }
+        }
 #pragma unroll
-          for (int n = 0; n < NT; ++n)
+        for (int h = 0; h < PP; ++h) mma_op<BF16>(o[mtl], a, pf[2 * h], pf[2 * h + 1]);
+      };
+      if constexpr (!BYTE) {
+        const uint32_t va = sbase + v_off[0];
+        uint32_t vm01 = 0xffffffffu, vm23 = 0xffffffffu;
+        if (tail) {
+          const int kt = key0 + 2 * t4;
+          vm01 = (kt < seq_len ? 0x0000ffffu : 0u) | (kt + 1 < seq_len ? 0xffff0000u : 0u);
+          vm23 = (kt + 8 < seq_len ? 0x0000ffffu : 0u) | (kt + 9 < seq_len ? 0xffff0000u : 0u);
+        }
 #pragma unroll
-            for (int h = 0; h < PP; ++h) mma_op<BF16>(o[mtl][n], a, pf[j][n][2 * h], pf[j][n][2 * h + 1]);
-        };
-        if constexpr (!BYTE) {
-          // this warp's m-tiles: a part of a slab's four, or whole slabs
-          const uint32_t va = (sbase + v_off[0] + (MTW >= 4 ? w * (MTW / 4) : w * MTW >> 2) * Cfg::kSlabBytes) ^
-                              (MTW >= 4 ? 0 : (w * MTW & 3) * 32);
-          uint32_t vm01 = 0xffffffffu, vm23 = 0xffffffffu;
+        for (int mtl = 0; mtl < MT; ++mtl) {
+          uint32_t a[4];
+          ldsm_x4_trans((va ^ ((mtl & 3) * 32)) + (mtl >> 2) * Cfg::kSlabBytes, a);
           if (tail) {
-            const int kt = key0 + 2 * t4;
-            vm01 = (kt < seq_len ? 0x0000ffffu : 0u) | (kt + 1 < seq_len ? 0xffff0000u : 0u);
-            vm23 = (kt + 8 < seq_len ? 0x0000ffffu : 0u) | (kt + 9 < seq_len ? 0xffff0000u : 0u);
+            a[0] &= vm01; a[1] &= vm01; a[2] &= vm23; a[3] &= vm23;
           }
-#pragma unroll
-          for (int mtl = 0; mtl < MTW; ++mtl) {
-            uint32_t a[4];
-            ldsm_x4_trans((va ^ ((mtl & 3) * 32)) + (mtl >> 2) * Cfg::kSlabBytes, a);
-            if (tail) {
-              a[0] &= vm01; a[1] &= vm01; a[2] &= vm23; a[3] &= vm23;
-            }
-            product(mtl, a);
-          }
-        } else {
-          // 32-dim group P32: lane reads 4 codes at dims 32 P32 + 4 g of keys
-          // key_of(2 t4), key_of(2 t4 + 1) and those + 8; m-tile 2 P32 takes
-          // dims 4 g (row g) and 4 g + 1 (row g + 8), m-tile 2 P32 + 1 the next two
-          const int kA = key_of(2 * t4), kB = key_of(2 * t4 + 1), kC = kA + 8, kD = kB + 8;
-#pragma unroll
-          for (int pl = 0; pl < MTW / 2; ++pl) {
-            const int P32 = w * (MTW / 2) + pl;
-            const uint32_t x32 = (P32 & 3) * 32, slab = sbase + (P32 >> 2) * Cfg::kSlabBytes;
-            const uint32_t vA = slab + (v_off[0] ^ x32), vB = slab + (v_off[1] ^ x32);
-            uint32_t wA = lds_b32_tile(vA), wB = lds_b32_tile(vB);
-            uint32_t wC = lds_b32_tile(vA + 8 * 128), wD = lds_b32_tile(vB + 8 * 128);
-            if (tail) {  // code 0 is the value 0 in both byte formats
-              if (key0 + kA >= seq_len) wA = 0u;
-              if (key0 + kB >= seq_len) wB = 0u;
-              if (key0 + kC >= seq_len) wC = 0u;
-              if (key0 + kD >= seq_len) wD = 0u;
-            }
-            wA = byte_word_prep<Cfg::KV>(wA); wB = byte_word_prep<Cfg::KV>(wB);
-            wC = byte_word_prep<Cfg::KV>(wC); wD = byte_word_prep<Cfg::KV>(wD);
-            const uint32_t ab01 = prmt(wA, wB, 0x5140u), ab23 = prmt(wA, wB, 0x7362u);
-            const uint32_t cd01 = prmt(wC, wD, 0x5140u), cd23 = prmt(wC, wD, 0x7362u);
-            uint32_t a[4] = {byte_pair_to_half2<Cfg::KV>(ab01, false), byte_pair_to_half2<Cfg::KV>(ab01, true),
-                             byte_pair_to_half2<Cfg::KV>(cd01, false), byte_pair_to_half2<Cfg::KV>(cd01, true)};
-            product(2 * pl, a);
-            uint32_t b[4] = {byte_pair_to_half2<Cfg::KV>(ab23, false), byte_pair_to_half2<Cfg::KV>(ab23, true),
-                             byte_pair_to_half2<Cfg::KV>(cd23, false), byte_pair_to_half2<Cfg::KV>(cd23, true)};
-            product(2 * pl + 1, b);
-          }
+          product(mtl, a);
         }
-        __syncwarp();
-        // (a stage taken twice is given back after the second time)
-        if (lane == 0 && (j == KT - 1 || (have[0] && have[KT - 1]))) mbar_arrive(empty0 + 8 * stage);
-      }
-    };
-    for (int st = (kg - static_cast<int>(step0 % KG) + KG) % KG; st * KT < last; st += KG) {
-      bool plain = st * KT >= lead && (st + 1) * KT <= last;
+      } else {
+        // 32-dim group P32: lane reads 4 codes at dims 32 P32 + 4 g of keys
+        // key_of(2 t4), key_of(2 t4 + 1) and those + 8; m-tile 2 P32 takes
+        // dims 4 g (row g) and 4 g + 1 (row g + 8), m-tile 2 P32 + 1 the next two
+        const int kA = key_of(2 * t4), kB = key_of(2 * t4 + 1), kC = kA + 8, kD = kB + 8;
 #pragma unroll
-      for (int j = 0; j < KT; ++j) {
-        const int key0 = piece_tile(p, pc, st * KT - lead + j) * kTileKeys;
-        plain = plain && ((key0 >= lo_all && key0 + kTileKeys - 1 <= hi_all) ||
-                          (key0 + kTileKeys <= prefix && hi_all >= 0));
+        for (int P32 = 0; P32 < MT / 2; ++P32) {
+          const uint32_t x32 = (P32 & 3) * 32, slab = sbase + (P32 >> 2) * Cfg::kSlabBytes;
+          const uint32_t vA = slab + (v_off[0] ^ x32), vB = slab + (v_off[1] ^ x32);
+          uint32_t wA = lds_b32_tile(vA), wB = lds_b32_tile(vB);
+          uint32_t wC = lds_b32_tile(vA + 8 * 128), wD = lds_b32_tile(vB + 8 * 128);
+          if (tail) {  // code 0 is the value 0 in both byte formats
+            if (key0 + kA >= seq_len) wA = 0u;
+            if (key0 + kB >= seq_len) wB = 0u;
+            if (key0 + kC >= seq_len) wC = 0u;
+            if (key0 + kD >= seq_len) wD = 0u;
+          }
+          wA = byte_word_prep<Cfg::KV>(wA); wB = byte_word_prep<Cfg::KV>(wB);
+          wC = byte_word_prep<Cfg::KV>(wC); wD = byte_word_prep<Cfg::KV>(wD);
+          const uint32_t ab01 = prmt(wA, wB, 0x5140u), ab23 = prmt(wA, wB, 0x7362u);
+          const uint32_t cd01 = prmt(wC, wD, 0x5140u), cd23 = prmt(wC, wD, 0x7362u);
+          uint32_t a[4] = {byte_pair_to_half2<Cfg::KV>(ab01, false), byte_pair_to_half2<Cfg::KV>(ab01, true),
+                           byte_pair_to_half2<Cfg::KV>(cd01, false), byte_pair_to_half2<Cfg::KV>(cd01, true)};
+          product(2 * P32, a);
+          uint32_t b[4] = {byte_pair_to_half2<Cfg::KV>(ab23, false), byte_pair_to_half2<Cfg::KV>(ab23, true),
+                           byte_pair_to_half2<Cfg::KV>(cd23, false), byte_pair_to_half2<Cfg::KV>(cd23, true)};
+          product(2 * P32 + 1, b);
+        }
       }
-      if (plain) step(st, std::false_type());
-      else step(st, std::true_type());
+      __syncwarp();
+      if (lane == 0) mbar_arrive(empty0 + 8 * stage);
+    };
+    for (int st = (kg - static_cast<int>(q % KG) + KG) % KG; st < ntiles; st += KG) {
+      const int key0 = piece_tile(p, pc, st) * kTileKeys;
+      if ((key0 >= lo_all && key0 + kTileKeys - 1 <= hi_all) || (key0 + kTileKeys <= prefix && hi_all >= 0))
+        step(st, std::false_type());
+      else
+        step(st, std::true_type());
     }
     q += ntiles;
 
@@ -565,8 +451,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::kMinBlocks)
       m_r[c] -= kUp;
     }
     // output dims of accumulator registers e = 0/1 and 2/3 of m-tile mtl
-    auto dim0 = [&](int mtl) {
-      const int mt = w * MTW + mtl;
+    auto dim0 = [&](int mt) {
       return BYTE ? (mt >> 1) * 32 + 4 * g + 2 * (mt & 1) : mt * 16 + g;
     };
     constexpr int kStep = BYTE ? 1 : 8;
@@ -575,7 +460,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::kMinBlocks)
       // straight from the accumulators
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        const int r = 2 * t4 + c;
+        const int r = rt * 8 + 2 * t4 + c;
         if (r >= pc.R) continue;
         if (direct) {
           const int head = (pc.kh + th) * p.G + r % p.G;
@@ -583,9 +468,9 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::kMinBlocks)
           if (g == 0) store_row_sum(p, pc.b, pc.q0, r / p.G, head, m_r[c], l_r[c]);
           uint16_t* dst = reinterpret_cast<uint16_t*>(p.out) + (static_cast<long long>(pc.q0 + r / p.G) * p.Hq + head) * D;
 #pragma unroll
-          for (int mtl = 0; mtl < MTW; ++mtl) {
+          for (int mtl = 0; mtl < MT; ++mtl) {
             const int d0 = dim0(mtl);
-            const uint32_t v = pack2<Cfg::QB>(o[mtl][0][c] * inv, o[mtl][0][2 + c] * inv);
+            const uint32_t v = pack2<Cfg::QB>(o[mtl][c] * inv, o[mtl][2 + c] * inv);
             if constexpr (BYTE) {
               *reinterpret_cast<uint32_t*>(dst + d0) = v;
             } else {
@@ -597,13 +482,13 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::kMinBlocks)
           const long long prow = static_cast<long long>(pc.slot) * Cfg::RP + th * Cfg::RH + r;
           float* dst = p.ws_o + prow * D;
 #pragma unroll
-          for (int mtl = 0; mtl < MTW; ++mtl) {
+          for (int mtl = 0; mtl < MT; ++mtl) {
             const int d0 = dim0(mtl);
             if constexpr (BYTE) {
-              __stcg(reinterpret_cast<float2*>(dst + d0), make_float2(o[mtl][0][c], o[mtl][0][2 + c]));
+              __stcg(reinterpret_cast<float2*>(dst + d0), make_float2(o[mtl][c], o[mtl][2 + c]));
             } else {
-              __stcg(dst + d0, o[mtl][0][c]);
-              __stcg(dst + d0 + 8, o[mtl][0][2 + c]);
+              __stcg(dst + d0, o[mtl][c]);
+              __stcg(dst + d0 + 8, o[mtl][2 + c]);
             }
           }
           if (g == 0) __stcg(reinterpret_cast<float2*>(p.ws_ml + prow * 2), make_float2(m_r[c], l_r[c]));
@@ -611,8 +496,8 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::kMinBlocks)
       }
     } else {
       // ---- through shared memory: a row's key groups weighted by 2^(m - max m) and added in group order
-      if (g == 0 && scores) {
-        float* ml = merge_ml + (kg * Cfg::RP + th * Cfg::RH + w * 8 + 2 * t4) * 2;
+      if (g == 0) {
+        float* ml = merge_ml + (kg * Cfg::RP + th * Cfg::RH + rt * 8 + 2 * t4) * 2;
         ml[0] = m_r[0];
         ml[1] = l_r[0];
         ml[2] = m_r[1];
@@ -623,29 +508,27 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::kMinBlocks)
       for (int k = 0; k < KG; ++k) {
         if (kg == k) {
 #pragma unroll
-          for (int n = 0; n < NT; ++n)
+          for (int c = 0; c < 2; ++c) {
+            const int row = th * Cfg::RH + rt * 8 + 2 * t4 + c;
+            float M = -INFINITY;
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              const int row = th * Cfg::RH + n * 8 + 2 * t4 + c;
-              float M = -INFINITY;
+            for (int kk = 0; kk < KG; ++kk) M = fmaxf(M, merge_ml[(kk * Cfg::RP + row) * 2]);
+            const float mk = merge_ml[(k * Cfg::RP + row) * 2];
+            const float f = mk == -INFINITY ? 0.f : ex2(mk - M);
+            float* mo = merge_o + row * Cfg::kDP;
 #pragma unroll
-              for (int kk = 0; kk < KG; ++kk) M = fmaxf(M, merge_ml[(kk * Cfg::RP + row) * 2]);
-              const float mk = merge_ml[(k * Cfg::RP + row) * 2];
-              const float f = mk == -INFINITY ? 0.f : ex2(mk - M);
-              float* mo = merge_o + row * Cfg::kDP;
-#pragma unroll
-              for (int mtl = 0; mtl < MTW; ++mtl) {
-                const int d0 = dim0(mtl);
-                const float a = f * o[mtl][n][c], b = f * o[mtl][n][2 + c];
-                if (k == 0) {
-                  mo[d0] = a;
-                  mo[d0 + kStep] = b;
-                } else {
-                  mo[d0] += a;
-                  mo[d0 + kStep] += b;
-                }
+            for (int mtl = 0; mtl < MT; ++mtl) {
+              const int d0 = dim0(mtl);
+              const float a = f * o[mtl][c], b = f * o[mtl][2 + c];
+              if (k == 0) {
+                mo[d0] = a;
+                mo[d0 + kStep] = b;
+              } else {
+                mo[d0] += a;
+                mo[d0 + kStep] += b;
               }
             }
+          }
         }
         named_bar_sync(1, Cfg::kConsumerThreads);
       }

@@ -36,19 +36,28 @@
 //    computed, a V stage when the P.V product that reads it completes.
 //  * At the end of a piece the warps read O^T (one output dim per thread) and
 //    write fp16 rows (unit done in one piece) or the fp32 (m, l, O) partial.
+//  * For the scored decode (SC) the softmax threads cap, bias and mask their
+//    key's scores and leave them for the keys' weights; the weights are split
+//    from fp32 into terms scaled by 1, 2^4 and 2^8, which keeps 12 bits of them and
+//    holds tiny ones to 2^-22 of the largest (many keys beside a dominant one); NaN
+//    codes of V that only some rows see are taken out of the ring and marked.
 //  * Every wait is bounded; after a timeout each role stops waiting and
 //    issuing but keeps the softmax warps' named-barrier sequence, so the CTA
 //    always reaches its exit, where the tensor memory is freed.
 #pragma once
+#include <type_traits>
+
 #include "launch.h"
 #include "tc5.cuh"
 
 namespace pd {
 
-template <int D_, bool QB_ = false, int NG_ = 4>
+template <int D_, bool QB_ = false, int NG_ = 4, bool SC_ = false>
 struct Tc8 {
   static constexpr int D = D_;
   static constexpr bool QB = QB_;                   // q and out in bfloat16 (else fp16)
+  static constexpr bool SC = SC_;                   // the scored decode
+  using Params = std::conditional_t<SC, ScoredParams, DecodeParams>;
   static constexpr int NG = NG_;                    // softmax groups = 8-row tiles of a unit (1 to 4)
   static constexpr int kSlabs = D / 128;            // 128-byte slabs of one e4m3 key row
   static constexpr int kBlkTiles = 8;               // 16-key tiles per 128-key block
@@ -83,12 +92,13 @@ struct Tc8 {
   static constexpr int kOffQ = kOffV + NBV * kKBlk;
   static constexpr int kOffPt = kOffQ + kQBytes;
   static constexpr int kOffRed = kOffPt + 3 * kPtTerm;     // float [NG groups][4 warps][8 rows]
-  static constexpr int kRowWords = 7 * 32;                 // row state: 7 arrays of 32 words
+  static constexpr int kRowWords = (SC ? 9 : 7) * 32;      // row state: arrays of 32 words
   static constexpr int kOffRow = kOffRed + NG * 4 * kGroupRows * 4;
   // Cluster merge (a fixed split whose pieces are the CTAs of one cluster):
   // each CTA stages its partial (m, l) here and its partial O rows [32][D]
   // fp32 at offset 0, over the K ring, which is idle once the piece is done.
-  static constexpr int kOffStageMl = kOffRow + kRowWords * 4;  // float2 [32 rows]
+  static constexpr int kOffMark = kOffRow + kRowWords * 4;     // SC: a bit for each row and dim that meets a NaN of V
+  static constexpr int kOffStageMl = kOffMark + (SC ? kN * D / 8 : 0);  // float2 [32 rows]
   static constexpr int kOffBars = kOffStageMl + 32 * 8;
   static constexpr int kBars = 2 * NBK + 2 * NBV + 8;
   static constexpr int kOffTmem = kOffBars + kBars * 8;
@@ -135,9 +145,28 @@ __device__ __forceinline__ void split3_e4m3(uint32_t x, uint32_t& t1, uint32_t& 
   t3 = half2_to_e4m3x2(*reinterpret_cast<const uint32_t*>(&r2));
 }
 
+// Two floats in [0, 2^8] as three e4m3 code pairs, the second and third scaled by 2^4 and 2^8: their
+// sum is off by at most 2^-12 of the value, or 2^-18. (Every difference is exact in fp32.)
+__device__ __forceinline__ uint32_t floats_to_e4m3x2(float lo, float hi) {
+  uint16_t d;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+__device__ __forceinline__ void split3_e4m3_up(float lo, float hi, uint32_t (&t)[3]) {
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    t[k] = floats_to_e4m3x2(lo, hi);
+    const uint32_t h = e4m3x2_to_half2(static_cast<uint16_t>(t[k]));
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+    lo = (lo - f.x) * 16.f;
+    hi = (hi - f.y) * 16.f;
+  }
+}
+
 // Row state arrays in shared memory (32 entries each).
-// kRowCf (a per-row score offset) is used by the int8 kernel only.
-enum { kRowFsl = 0, kRowMu = 1, kRowAl = 2, kRowLo = 3, kRowHi = 4, kRowL = 5, kRowFlag = 6, kRowCf = 7 };
+// kRowCf (a per-row score offset) is used by the int8 kernel only, kRowSlope (of the
+// distance bias, in log2 units) by the scored decode.
+enum { kRowFsl = 0, kRowMu = 1, kRowAl = 2, kRowLo = 3, kRowHi = 4, kRowL = 5, kRowFlag = 6, kRowCf = 7, kRowSlope = 8 };
 // Barriers: fullK[NBK], emptyK[NBK], fullV[NBV], emptyV[NBV], then these.
 enum { kBarSFull = 0, kBarSEmpty = 2, kBarPFull = 4, kBarPvDone = 5, kBarQFull = 6, kBarFinal = 7 };
 
@@ -170,8 +199,8 @@ __device__ __forceinline__ float warp_transpose_reduce(float (&v)[N], int lane) 
 // The next piece with visible tiles for the softmax warps (thread index < NST);
 // pieces with nothing visible are finished on the spot: their rows are written
 // as zeros (such a unit is never split).
-template <class T>
-__device__ __forceinline__ bool tc_next_piece(const DecodeParams& p, const int* s_pre, WorkIter& it, Piece& out) {
+template <class T, class Par>
+__device__ __forceinline__ bool tc_next_piece(const Par& p, const int* s_pre, WorkIter& it, Piece& out) {
   constexpr int D = T::D;
   while (work_next(p, s_pre, it, out)) {
     if (out.ntiles > 0) return true;
@@ -180,6 +209,7 @@ __device__ __forceinline__ bool tc_next_piece(const DecodeParams& p, const int* 
       const int i = r / p.G, hl = r % p.G;
       *reinterpret_cast<uint4*>(p.out + (static_cast<long long>(out.q0 + i) * p.Hq + out.kh * p.G + hl) * D +
                                 dc * 8) = make_uint4(0u, 0u, 0u, 0u);
+      if (dc == 0) store_row_sum(p, out.b, out.q0, i, out.kh * p.G + hl, -INFINITY, 0.f);
     }
   }
   return false;
@@ -205,6 +235,47 @@ __device__ __forceinline__ void tc_scale_mask(float (&x)[8], const float (&fs)[8
 #pragma unroll
     for (int r = 0; r < NR; ++r)
       x[r] = (loaded && j >= ri[kRowLo * 32 + rb + r] && j <= ri[kRowHi * 32 + rb + r]) ? scaled(r) : -INFINITY;
+  }
+}
+
+// Scored decode: whether the row of state index r (its causal and window limits) sees key j.
+__device__ __forceinline__ bool tc_row_sees(const Piece& pc, const int* ri, int r, int j) {
+  const int hi = ri[kRowHi * 32 + r];
+  return (j >= ri[kRowLo * 32 + r] && j <= hi) || (j < pc.prefix && hi >= 0);
+}
+// Whether every row of the piece sees the keys j0 .. j1.
+__device__ __forceinline__ bool tc_all_see(const Piece& pc, int j0, int j1) {
+  return (j0 >= pc.tile_lo_all && j1 <= pc.tile_hi_all) || (j1 < pc.prefix && pc.tile_hi_all >= 0);
+}
+// Scored decode: the scores of key j (tile j / 16, loaded or not) as tc_scale_mask, capped and
+// biased, and left in the workspace for the keys' weights.
+template <class T>
+__device__ __forceinline__ void tc_score(const ScoredParams& p, float (&x)[8], const float (&fs)[8], int j, bool loaded,
+                                         const Piece& pc, const float* rf, const int* ri, int g) {
+  constexpr int NR = T::kGroupRows;
+  const int rb = NR * g, tile = j / kTileKeys;
+#pragma unroll
+  for (int r = 0; r < NR; ++r) x[r] *= fs[r];
+  if (p.cap_out > 0.f) {
+#pragma unroll
+    for (int r = 0; r < NR; ++r) x[r] = p.cap_out * tanh_f32(x[r] * p.cap_u);
+  }
+  if (p.slopes != nullptr) {
+#pragma unroll
+    for (int r = 0; r < NR; ++r)
+      x[r] -= rf[kRowSlope * 32 + rb + r] * static_cast<float>(abs(j - ri[kRowHi * 32 + rb + r]));
+  }
+  if (!loaded || !tc_all_see(pc, tile * kTileKeys, tile * kTileKeys + kTileKeys - 1)) {
+#pragma unroll
+    for (int r = 0; r < NR; ++r)
+      if (!loaded || !tc_row_sees(pc, ri, rb + r, j)) x[r] = -INFINITY;
+  }
+  if (p.scores != nullptr && loaded) {
+    float4* dst = reinterpret_cast<float4*>(
+        p.scores + ((static_cast<long long>(pc.b) * p.Hkv + pc.kh) * p.max_blocks * p.tiles_per_block + tile) *
+                       (T::NG * 128) + g * 128 + j % kTileKeys * 8);
+    __stcg(dst, make_float4(x[0], x[1], x[2], x[3]));
+    __stcg(dst + 1, make_float4(x[4], x[5], x[6], x[7]));
   }
 }
 
@@ -257,13 +328,25 @@ __device__ __forceinline__ bool tc_raise_max(const float (&x)[8], float (&mu)[8]
   return ri[kRowFlag * 32 + g] != 0;
 }
 
+// What the weights of row r are relative to (-inf: none; scored decode: nothing but NaN is not an empty row).
+template <class T>
+__device__ __forceinline__ float tc_row_base(const float* rf, int r) {
+  const float mu = rf[kRowMu * 32 + r];
+  if (mu != -INFINITY) return mu - T::kBias;
+  if constexpr (T::SC) {
+    const float l = rf[kRowL * 32 + r];
+    if (l != l) return 0.f;
+  }
+  return -INFINITY;
+}
+
 // End of a piece for softmax group g: the rows' weight sums (this thread's key
 // lane shares lp, reduced over the group), then the output: fp16 / bfloat16
 // rows when the unit is one piece, else the unnormalised O rows and (m, l) --
 // staged in shared memory for a cluster merge, or written to the workspace
 // slot of the piece. o[h][k] is output dim 128 h + key of row 8 g + k.
 template <class T>
-__device__ __forceinline__ void tc_write_piece(const DecodeParams& p, const Piece& pc, const float (&o)[T::kSlabs][8],
+__device__ __forceinline__ void tc_write_piece(const typename T::Params& p, const Piece& pc, const float (&o)[T::kSlabs][8],
                                                const float (&lp)[8], uint8_t* smem, float* rf, float* red, int g,
                                                int warp, int lane, int key) {
   constexpr int D = T::D, S = T::kSlabs, NR = T::kGroupRows;
@@ -288,7 +371,8 @@ __device__ __forceinline__ void tc_write_piece(const DecodeParams& p, const Piec
     if (direct) {
       const int i = r / p.G, hl = r % p.G;
       __half* dst = p.out + (static_cast<long long>(pc.q0 + i) * p.Hq + pc.kh * p.G + hl) * D;
-      const float inv = L > 0.f ? p.out_scale / L : 0.f;
+      const float inv = row_factor(p, L);
+      if (key == 0) store_row_sum(p, pc.b, pc.q0, i, pc.kh * p.G + hl, tc_row_base<T>(rf, r), L);
 #pragma unroll
       for (int h = 0; h < S; ++h)
         reinterpret_cast<uint16_t*>(dst)[128 * h + key] = pack1<T::QB>(o[h][k] * inv);
@@ -304,12 +388,48 @@ __device__ __forceinline__ void tc_write_piece(const DecodeParams& p, const Piec
   }
   if (!direct && key < NR && rb + key < pc.R) {
     const int r = rb + key;
-    const float mu = rf[kRowMu * 32 + r];
-    const float2 ml = make_float2(mu == -INFINITY ? -INFINITY : mu - T::kBias, rf[kRowL * 32 + r]);
+    const float2 ml = make_float2(tc_row_base<T>(rf, r), rf[kRowL * 32 + r]);
     if (p.cluster > 1)
       reinterpret_cast<float2*>(smem + T::kOffStageMl)[r] = ml;
     else
       __stcg(reinterpret_cast<float2*>(p.ws_ml + (static_cast<long long>(pc.slot) * p.rows_padded + r) * 2), ml);
+  }
+}
+
+// Scored decode: the row's distance slope, in log2 units; a row before the sequence's start sees nothing.
+template <class T>
+__device__ __forceinline__ void tc_row_slope(const typename T::Params& p, const Piece& pc, float* rf, int r) {
+  if constexpr (T::SC) {
+    rf[kRowSlope * 32 + r] =
+        p.slopes != nullptr && r < pc.R ? __ldg(p.slopes + pc.kh * p.G + r % p.G) * kLog2e : 0.f;
+  }
+}
+
+// Takes the NaN codes out of key j's V row in the ring (row `key` of its block) and marks the outputs of the rows that
+// see the key.
+template <class T>
+__device__ __noinline__ void take_nan_codes(const Piece& pc, const int* ri, uint32_t* mark, uint32_t vrow, int key, int j) {
+  uint32_t any = 0;
+#pragma unroll
+  for (int i = 0; i < T::kSlabs * 8; ++i) {
+    const uint4 w = lds_v4(vrow + (i >> 3) * T::kSlabBlk + (((i & 7) ^ (key & 7)) << 4));
+    any |= ((w.x & 0x7f7f7f7fu) + 0x01010101u) | ((w.y & 0x7f7f7f7fu) + 0x01010101u) |
+           ((w.z & 0x7f7f7f7fu) + 0x01010101u) | ((w.w & 0x7f7f7f7fu) + 0x01010101u);
+  }
+  if ((any & 0x80808080u) == 0) return;
+#pragma unroll 1
+  for (int i = 0; i < T::kSlabs * 32; ++i) {  // words of the row
+    const uint32_t at = vrow + (i >> 5) * T::kSlabBlk + (i & 31) * 4;
+    uint32_t w;
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w) : "r"(at) : "memory");
+    uint32_t nan = ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+    if (nan == 0) continue;
+    asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(w & ~((nan >> 7) * 255u)) : "memory");
+    const int dim0 = (i >> 5) * 128 + ((((i & 31) >> 2) ^ (key & 7)) << 4) + (i & 3) * 4;
+    uint32_t bits = 0;
+    for (; nan != 0; nan &= nan - 1) bits |= 1u << ((dim0 & 31) + (__ffs(nan) - 8) / 8);
+    for (int r = 0; r < pc.R; ++r)
+      if (tc_row_sees(pc, ri, r, j)) atomicOr(mark + r * (T::D / 32) + dim0 / 32, bits);
   }
 }
 
@@ -319,7 +439,7 @@ __device__ __forceinline__ void tc_write_piece(const DecodeParams& p, const Piec
 // with their running maxima, sums and O^T columns, so the groups never wait on
 // each other inside a block.
 template <class T>
-__device__ __forceinline__ void softmax_role(const DecodeParams& p, const int* s_pre, WorkIter& it, Piece& pc,
+__device__ __forceinline__ void softmax_role(const typename T::Params& p, const int* s_pre, WorkIter& it, Piece& pc,
                                              uint8_t* smem, uint32_t sbase, uint32_t tmem, bool& ok) {
   constexpr int D = T::D, NBK = T::NBK, NBV = T::NBV, S = T::kSlabs, NR = T::kGroupRows;
   constexpr int NST = T::kSoftThreads;
@@ -335,6 +455,7 @@ __device__ __forceinline__ void softmax_role(const DecodeParams& p, const int* s
   auto bar = [&](int i) -> uint32_t { return bx + 8 * i; };
   const uint32_t tl = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);  // this warp's TMEM lanes
   const uint32_t qs = sbase + T::kOffQ, pt = sbase + T::kOffPt;
+  uint32_t* mark = reinterpret_cast<uint32_t*>(smem + T::kOffMark);  // SC: [row][dim / 32]
   uint32_t bq = 0;
   // A piece's q terms (the B operand of S^T: K-major, 128-byte swizzle, the
   // three terms stacked on N), row score factors and visible key limits; the
@@ -410,8 +531,11 @@ __device__ __forceinline__ void softmax_role(const DecodeParams& p, const int* s
         rf[kRowMu * 32 + r] = -INFINITY;
         ri[kRowLo * 32 + r] = lo;
         ri[kRowHi * 32 + r] = hi;
+        tc_row_slope<T>(p, pq, rf, r);
       }
     }
+    if constexpr (T::SC)
+      for (int i = tid; i < T::kN * D / 32; i += NST) mark[i] = 0u;
     fence_proxy_async_smem();
   };
   auto load8 = [&](const float* src, float (&dst)[NR]) {
@@ -459,7 +583,9 @@ __device__ __forceinline__ void softmax_role(const DecodeParams& p, const int* s
       tc_fence_before();
       __syncwarp();
       if (ok && lane == 0) mbar_arrive(bar(kBarSEmpty + sb));
-      tc_scale_mask<T>(x, fs, fs, key0, nvalid, pc, ri, rb, key);
+      const int j = T::SC ? piece_tile(p, pc, T::kBlkTiles * i + (key >> 4)) * kTileKeys + (key & 15) : key0 + key;
+      if constexpr (T::SC) tc_score<T>(p, x, fs, j, key < nvalid, pc, rf, ri, g);
+      else tc_scale_mask<T>(x, fs, fs, key0, nvalid, pc, ri, rb, key);
       // ---- running maximum per row (see tc_raise_max)
       float mu[NR];
       const bool rescale = tc_raise_max<T>(x, mu, rf, ri, red, g, warp, lane);
@@ -498,7 +624,13 @@ __device__ __forceinline__ void softmax_role(const DecodeParams& p, const int* s
         uint32_t tt[3][NR / 2];
 #pragma unroll
         for (int k = 0; k < NR / 2; ++k)
-          split3_e4m3(pack_half2(x[2 * k], x[2 * k + 1]), tt[0][k], tt[1][k], tt[2][k]);
+          if constexpr (T::SC) {
+            uint32_t t[3];
+            split3_e4m3_up(x[2 * k], x[2 * k + 1], t);
+            tt[0][k] = t[0]; tt[1][k] = t[1]; tt[2][k] = t[2];
+          } else {
+            split3_e4m3(pack_half2(x[2 * k], x[2 * k + 1]), tt[0][k], tt[1][k], tt[2][k]);
+          }
         const uint32_t row = pt + (key >> 3) * 256 + (key & 7) * 32 +
                              ((((g >> 1) ^ ((key & 7) >> 2)) << 4) | ((g & 1) << 3));
 #pragma unroll
@@ -510,12 +642,17 @@ __device__ __forceinline__ void softmax_role(const DecodeParams& p, const int* s
       // ---- V rows of keys past the sequence end or not loaded (stale or
       // unwritten bytes, NaN codes included) are zeroed in the ring by the first
       // group: the P.V product reads V there, and a zero weight must not meet a NaN
-      const int lim = min(nvalid, pc.L - key0);
-      if (g == 0 && lim < 128) {
+      // (scored decode: nor must a NaN code of a key that only some rows see meet the zero weights of the others)
+      const bool dead = T::SC ? key >= nvalid || j >= pc.L : key >= min(nvalid, pc.L - key0);
+      const bool partly = T::SC && !dead && !tc_all_see(pc, j, j);
+      if (g == 0 && (T::SC ? __any_sync(0xffffffffu, dead || partly) : min(nvalid, pc.L - key0) < 128)) {
         if (ok) ok = mbar_wait(fullv0 + 8 * sv, (b / NBV) & 1, p.timeout_ns);
         ok = __all_sync(0xffffffffu, ok);
-        if (ok && key >= lim) {
-          const uint32_t vrow = sbase + T::kOffV + sv * T::kKBlk + key * 128;
+        const uint32_t vrow = sbase + T::kOffV + sv * T::kKBlk + key * 128;
+        if constexpr (T::SC) {
+          if (ok && partly) take_nan_codes<T>(pc, ri, mark, vrow, key, j);
+        }
+        if (ok && dead) {
 #pragma unroll
           for (int sl = 0; sl < S; ++sl)
 #pragma unroll
@@ -547,13 +684,22 @@ __device__ __forceinline__ void softmax_role(const DecodeParams& p, const int* s
         tmem_ld8(oc + 64, z);
         tmem_wait_ld();
 #pragma unroll
-        for (int r = 0; r < NR; ++r) o[h][r] = (o[h][r] + y[r]) + z[r];
+        for (int r = 0; r < NR; ++r)
+          o[h][r] = T::SC ? fmaf(z[r], 1.f / 256.f, fmaf(y[r], 1.f / 16.f, o[h][r])) : (o[h][r] + y[r]) + z[r];
       } else {
 #pragma unroll
         for (int r = 0; r < NR; ++r) o[h][r] = 0.f;
       }
     }
     tc_fence_before();
+    if constexpr (T::SC) {
+      named_bar_sync(T::kBarAll, NST);  // (all marks are there)
+#pragma unroll
+      for (int h = 0; h < S; ++h)
+#pragma unroll
+        for (int r = 0; r < NR; ++r)
+          if (mark[(rb + r) * (D / 32) + 4 * h + (key >> 5)] >> (key & 31) & 1u) o[h][r] = __uint_as_float(0x7fffffffu);
+    }
     tc_write_piece<T>(p, pc, o, lp, smem, rf, red, g, warp, lane, key);
     named_bar_sync(T::kBarAll, NST);  // the row state and red[] are rewritten by the next piece
   }
@@ -570,7 +716,7 @@ __device__ __forceinline__ void softmax_role(const DecodeParams& p, const int* s
 // m = -inf (weight 0; its O rows are never written and are not used). A unit
 // covered by one piece (or none) was written by its piece.
 template <class T>
-__device__ __forceinline__ void cluster_merge(const DecodeParams& p, uint32_t sbase) {
+__device__ __forceinline__ void cluster_merge(const typename T::Params& p, uint32_t sbase) {
   constexpr int D = T::D, Q4 = D / 4, SMAX = kMaxCluster;
   const int S = p.cluster;
   const int rank = static_cast<int>(cluster_rank());
@@ -610,8 +756,9 @@ __device__ __forceinline__ void cluster_merge(const DecodeParams& p, uint32_t sb
         acc.x += w * o[s].x; acc.y += w * o[s].y; acc.z += w * o[s].z; acc.w += w * o[s].w;
       }
     }
-    const float inv = lsum > 0.f ? p.out_scale / lsum : 0.f;
+    const float inv = row_factor(p, lsum);
     const int i = r / p.G, hl = r % p.G;
+    if (c4 == 0) store_row_sum(p, b, q0, i, kh * p.G + hl, M, lsum);
     uint16_t* dst = reinterpret_cast<uint16_t*>(p.out) +
                     (static_cast<long long>(q0 + i) * p.Hq + kh * p.G + hl) * D + 4 * c4;
     const uint32_t lo = pack2<T::QB>(acc.x * inv, acc.y * inv), hi = pack2<T::QB>(acc.z * inv, acc.w * inv);
@@ -627,8 +774,8 @@ __device__ __forceinline__ void cluster_merge(const DecodeParams& p, uint32_t sb
 // next group in flight. Rings and their barriers: K stages at offset 0, V
 // stages at kOffV; fullK[NBK], emptyK[NBK], fullV[NBV], emptyV[NBV] first in
 // the barrier area.
-template <class T>
-__device__ __forceinline__ void tc_producer_role(const DecodeParams& p, const int* s_pre, WorkIter& it, Piece& pc,
+template <class T, class Par>
+__device__ __forceinline__ void tc_producer_role(const Par& p, const int* s_pre, WorkIter& it, Piece& pc,
                                                  const CUtensorMap* tm_k, const CUtensorMap* tm_v, uint32_t sbase,
                                                  bool& ok) {
   constexpr int NBK = T::NBK, NBV = T::NBV;
@@ -648,7 +795,7 @@ __device__ __forceinline__ void tc_producer_role(const DecodeParams& p, const in
     const int32_t* row = p.block_table + static_cast<long long>(pc.b) * p.max_blocks;
     auto load_group = [&](int t) -> int {
       int blk = 0;
-      if (t + lane < pc.ntiles) blk = __ldg(row + (pc.first_tile + t + lane) / p.tiles_per_block);
+      if (t + lane < pc.ntiles) blk = __ldg(row + piece_tile(p, pc, t + lane) / p.tiles_per_block);
       return blk;
     };
     // block table entries 32 tiles (4 blocks) at a time, the next group in flight
@@ -680,7 +827,7 @@ __device__ __forceinline__ void tc_producer_role(const DecodeParams& p, const in
           if (!is_v) raise_error(p.error_flag, kErrBlockId);
           blk = 0;
         }
-        const int gt = pc.first_tile + t0 + j;
+        const int gt = piece_tile(p, pc, t0 + j);
         const int z = blk * p.block_size + (gt % p.tiles_per_block) * kTileKeys;
         const int sl = lane % T::kSlabs;
         tma_load_3d(ringb + st * T::kKBlk + sl * T::kSlabBlk + j * T::kTileBox, tm, fullb + 8 * st, sl * 128,
@@ -701,7 +848,7 @@ __device__ __forceinline__ void tc_producer_role(const DecodeParams& p, const in
 template <class T>
 __global__ void __launch_bounds__(T::kThreads, 1)
     decode_tc8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                      const DecodeParams p) {
+                      const typename T::Params p) {
   constexpr int D = T::D, NBK = T::NBK, NBV = T::NBV, KS = D / 32;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -850,7 +997,7 @@ __global__ void __launch_bounds__(T::kThreads, 1)
 // programmatic dependent launch and, for a cluster-merged fixed split,
 // clusters of p.cluster CTAs; sets the shared-memory opt-in once per context.
 template <class T>
-cudaError_t launch_tc8(const CUtensorMap& tk, const CUtensorMap& tv, const DecodeParams& p, int grid,
+cudaError_t launch_tc8(const CUtensorMap& tk, const CUtensorMap& tv, const typename T::Params& p, int grid,
                        cudaStream_t stream) {
   static unsigned long long attr_ctx[64] = {};
   const cudaError_t e = once_per_context(attr_ctx, [] {

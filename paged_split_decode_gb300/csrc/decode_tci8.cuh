@@ -24,6 +24,11 @@
 //    under exactly the weights the product used.
 //  * S^T [128 keys x 32 rows] = K Q^T; O^T [D x 32 rows] accumulates in tensor
 //    memory, output dims 128 h .. 128 h + 127 in columns kColO + 32 h.
+//  * For the scored decode (SC, a bfloat16 q) the softmax threads cap, bias and
+//    mask their key's scores and leave them for the keys' weights. The log-sum-exp
+//    and those weights show what the output's rounding hides: K is widened to x
+//    itself (the offset's sum leaves 1e-6 of a score), and the row sums add the
+//    weights before their rounding.
 //  * Every wait is bounded; after a timeout each role stops waiting and
 //    issuing but keeps the softmax warps' named-barrier sequence, so the CTA
 //    always reaches its exit, where the tensor memory is freed.
@@ -32,10 +37,12 @@
 
 namespace pd {
 
-template <int D_, bool QB_ = false, int NG_ = 4>
+template <int D_, bool QB_ = false, int NG_ = 4, bool SC_ = false>
 struct Tci8 {
   static constexpr int D = D_;
   static constexpr bool QB = QB_;                   // q and out in bfloat16 (else fp16)
+  static constexpr bool SC = SC_;                   // the scored decode
+  using Params = std::conditional_t<SC, ScoredParams, DecodeParams>;
   static constexpr int NG = NG_;                    // softmax groups = 8-row tiles of a unit (1 to 4)
   static constexpr int kSlabs = D / 128;            // 128-byte slabs of an int8 key row; 128-dim halves of O^T
   static constexpr int kBlkTiles = 8;               // 16-key tiles per 128-key block
@@ -72,7 +79,7 @@ struct Tci8 {
   static constexpr int kOffQ = kOffV16 + kV16Bytes;
   static constexpr int kOffPt = kOffQ + kQBytes;
   static constexpr int kOffRed = kOffPt + kPtBytes;        // float [NG groups][4 warps][8 rows]
-  static constexpr int kRowWords = 8 * 32;                 // row state: 8 arrays of 32 words
+  static constexpr int kRowWords = (SC ? 9 : 8) * 32;      // row state: arrays of 32 words
   static constexpr int kOffRow = kOffRed + NG * 4 * kGroupRows * 4;
   // Cluster merge: each CTA stages its partial (m, l) here and its partial O
   // rows [32][D] fp32 at offset 0, over the K ring, idle once the piece is done.
@@ -139,7 +146,7 @@ __device__ __forceinline__ void widen_i8x16(const uint4& w, uint32_t (&h)[8]) {
 // chunk c by group (kChunks + c) % NG, which evens out each group's share of
 // the 2 kChunks chunks of a key.
 template <class T>
-__device__ __forceinline__ void softmax_role_i8(const DecodeParams& p, const int* s_pre, WorkIter& it, Piece& pc,
+__device__ __forceinline__ void softmax_role_i8(const typename T::Params& p, const int* s_pre, WorkIter& it, Piece& pc,
                                                 uint8_t* smem, uint32_t sbase, uint32_t tmem, bool& ok) {
   constexpr int D = T::D, NBK = T::NBK, NBV = T::NBV, S = T::kSlabs, NR = T::kGroupRows, NG = T::NG;
   constexpr int NST = T::kSoftThreads, NCH = T::kChunks, PER = (NCH + NG - 1) / NG;
@@ -176,7 +183,9 @@ __device__ __forceinline__ void softmax_role_i8(const DecodeParams& p, const int
         const int c = g + NG * k;
         if (c < NCH) {  // warp-uniform
           uint32_t h[8];
-          widen_i8x16_offset(ld_shared_v4(src + (c >> 3) * T::kSlabBlk + (((c & 7) ^ swz) << 4)), h);
+          const uint4 w = ld_shared_v4(src + (c >> 3) * T::kSlabBlk + (((c & 7) ^ swz) << 4));
+          if constexpr (T::SC) widen_i8x16(w, h);
+          else widen_i8x16_offset(w, h);
           tmem_st8u(dst + 8 * c, h);
         }
       }
@@ -277,6 +286,7 @@ __device__ __forceinline__ void softmax_role_i8(const DecodeParams& p, const int
         rf[kRowMu * 32 + r] = -INFINITY;
         ri[kRowLo * 32 + r] = lo;
         ri[kRowHi * 32 + r] = hi;
+        tc_row_slope<T>(p, pq, rf, r);
       }
     }
     fence_proxy_async_smem();
@@ -321,7 +331,11 @@ __device__ __forceinline__ void softmax_role_i8(const DecodeParams& p, const int
         const float4 f = reinterpret_cast<const float4*>(rf + kRowCf * 32 + rb)[k];
         cf[4 * k] = f.x; cf[4 * k + 1] = f.y; cf[4 * k + 2] = f.z; cf[4 * k + 3] = f.w;
       }
-      tc_scale_mask<T, true>(x, fs, cf, key0, nvalid, pc, ri, rb, key);
+      if constexpr (T::SC)
+        tc_score<T>(p, x, fs, piece_tile(p, pc, T::kBlkTiles * i + (key >> 4)) * kTileKeys + (key & 15),
+                          key < nvalid, pc, rf, ri, g);
+      else
+        tc_scale_mask<T, true>(x, fs, cf, key0, nvalid, pc, ri, rb, key);
       float mu[NR];
       const bool rescale = tc_raise_max<T>(x, mu, rf, ri, red, g, warp, lane);
       // ---- weights 2^(x - mu + kBias) (<= 2^8) rounded to fp16, and the row
@@ -333,8 +347,8 @@ __device__ __forceinline__ void softmax_role_i8(const DecodeParams& p, const int
         const float c = ex2(x[2 * k + 1] - (mu[2 * k + 1] == -INFINITY ? 0.f : mu[2 * k + 1] - T::kBias));
         pw[k] = pack_half2(a, c);
         const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&pw[k]));
-        x[2 * k] = f.x;
-        x[2 * k + 1] = f.y;
+        x[2 * k] = T::SC ? a : f.x;
+        x[2 * k + 1] = T::SC ? c : f.y;
       }
       if (rescale) {
 #pragma unroll
@@ -398,7 +412,7 @@ __device__ __forceinline__ void softmax_role_i8(const DecodeParams& p, const int
 template <class T>
 __global__ void __launch_bounds__(T::kThreads, 1)
     decode_tci8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                       const DecodeParams p) {
+                       const typename T::Params p) {
   constexpr int D = T::D, NBK = T::NBK, NBV = T::NBV;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -537,7 +551,7 @@ __global__ void __launch_bounds__(T::kThreads, 1)
 // programmatic dependent launch and, for a cluster-merged fixed split,
 // clusters of p.cluster CTAs; sets the shared-memory opt-in once per context.
 template <class T>
-cudaError_t launch_tci8(const CUtensorMap& tk, const CUtensorMap& tv, const DecodeParams& p, int grid,
+cudaError_t launch_tci8(const CUtensorMap& tk, const CUtensorMap& tv, const typename T::Params& p, int grid,
                         cudaStream_t stream) {
   static unsigned long long attr_ctx[64] = {};
   const cudaError_t e = once_per_context(attr_ctx, [] {

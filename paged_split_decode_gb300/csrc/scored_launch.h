@@ -4,6 +4,7 @@
 #pragma once
 #include "decode_fp4.cuh"
 #include "decode_scored.cuh"
+#include "decode_tci8.cuh"
 #include "launch.h"
 
 namespace pd {
@@ -30,30 +31,31 @@ struct KeyWeightParams {
 };
 cudaError_t launch_key_weights(KeyWeightParams p, int sms, cudaStream_t stream);
 
-// The deepest ring (at most 32 stages, a multiple of the key groups' steps) that lets MINB CTAs share an SM.
-template <int D, int KV, int NT, int HG, int W, int KG, int KT, int MINB, int NS = 32>
+// The deepest ring (at most 32 stages, a multiple of the key groups) that lets MINB CTAs share an SM.
+template <int D, int KV, int HG, int RG, int KG, int MINB, int NS = 32>
 constexpr int scored_stages() {
-  constexpr int unit = KG > 1 ? KG * KT : 1;
-  if constexpr (NS <= unit || NS <= 2)
-    return unit > 2 ? unit : 2;
-  else if constexpr (NS % unit != 0)
-    return scored_stages<D, KV, NT, HG, W, KG, KT, MINB, NS - 1>();
-  else if constexpr (ScoredCfg<D, KV, NT, HG, W, KG, KT, NS, MINB>::kSmemBytes <= smem_limit(MINB))
+  if constexpr (NS <= KG || NS <= 2)
+    return KG > 2 ? KG : 2;
+  else if constexpr (NS % KG != 0)
+    return scored_stages<D, KV, HG, RG, KG, MINB, NS - 1>();
+  else if constexpr (ScoredCfg<D, KV, HG, RG, KG, NS, MINB>::kSmemBytes <= smem_limit(MINB))
     return NS;
   else
-    return scored_stages<D, KV, NT, HG, W, KG, KT, MINB, NS - 1>();
+    return scored_stages<D, KV, HG, RG, KG, MINB, NS - 1>();
 }
-template <int D, int KV, int NT, int HG, int W, int KG, int KT, int MINB>
-using ScoredCfgFor = ScoredCfg<D, KV, NT, HG, W, KG, KT, scored_stages<D, KV, NT, HG, W, KG, KT, MINB>(), MINB>;
+template <int D, int KV, int HG, int RG, int KG, int MINB>
+using ScoredCfgFor = ScoredCfg<D, KV, HG, RG, KG, scored_stages<D, KV, HG, RG, KG, MINB>(), MINB>;
 
 template <int D, int KV>
 struct ScoredShapes {
-  // row tiles, heads per tile, warps per head, key groups, tiles per step, CTAs per SM
-  using C1H = ScoredCfgFor<D, KV, 1, 4, 1, 1, 1, 1>;
-  using C1 = ScoredCfgFor<D, KV, 1, 1, 1, 3, 1, 2>;
-  using C2 = ScoredCfgFor<D, KV, 2, 1, 2, 4, 1, 1>;
-  using C3 = ScoredCfgFor<D, KV, 3, 1, 4, 2, 1, 1>;
-  using C4 = ScoredCfgFor<D, KV, 4, 1, 4, 2, 1, 1>;
+  // heads per tile, row tiles per head, key groups, CTAs per SM. C4, 30 rows over fp16 caches, B = 8: two key groups in
+  // one CTA 40.3 us at L = 4096 and 16.6 at 512, two CTAs of one group 46.4 and 16.1 (C2, C3 the other way round:
+  // 42.4 and 37.3 against 32.8 and 33.1).
+  using C1H = ScoredCfgFor<D, KV, 4, 1, 1, 1>;
+  using C1 = ScoredCfgFor<D, KV, 1, 1, 3, 2>;
+  using C2 = ScoredCfgFor<D, KV, 1, 2, 1, 2>;
+  using C3 = ScoredCfgFor<D, KV, 1, 3, 1, 2>;
+  using C4 = ScoredCfgFor<D, KV, 1, 4, 2, 1>;
 
   template <class C>
   static bool shape_one(KernelShape* out) {
@@ -63,7 +65,7 @@ struct ScoredShapes {
     out->rows_padded = C::RP;
     out->ctas_per_sm = C::kMinBlocks;
     out->heads = C::HG;
-    out->step_tiles = C::KG * C::KT;
+    out->step_tiles = C::KG;
     out->key_groups = C::KG;
     out->whole_tile = 1;
     out->unit_cost = C::KG > 1 ? 12 : 4;
@@ -80,8 +82,28 @@ struct ScoredShapes {
     if (e != cudaSuccess) return e;
     return launch_pdl(decode_scored_kernel<C>, grid, C::kThreads, C::kSmemBytes, s, 1, tk, tv, p);
   }
+  // Two to four row tiles over e4m3 caches, and over int8 caches under a bfloat16 q (an fp16 output wants more bits
+  // of P than the int8 kernel's products take): the kernels of tensor memory. 18 rows, B = 8, L = 4096: e4m3 20.5 us
+  // against C3's 34.8, int8 26.4 against 40.0.
+  static constexpr bool kTc = cache_kind(KV) == kKvFp8 || KV == kKvInt8Bq;
+  template <int NG>
+  using Tc = std::conditional_t<cache_kind(KV) == kKvFp8, Tc8<D, q_is_bf16(KV), NG, true>, Tci8<D, true, NG, true>>;
+  template <int NG>
+  static bool shape_tc(KernelShape* out) {
+    if constexpr (cache_kind(KV) == kKvFp8) return shape_tc8<Tc<NG>>(NG, out);
+    else return shape_tci8<Tc<NG>>(NG, out);
+  }
+  template <int NG>
+  static cudaError_t launch_tc(const CUtensorMap& tk, const CUtensorMap& tv, const ScoredParams& p, int grid, cudaStream_t s) {
+    if constexpr (cache_kind(KV) == kKvFp8) return launch_tc8<Tc<NG>>(tk, tv, p, grid, s);
+    else return launch_tci8<Tc<NG>>(tk, tv, p, grid, s);
+  }
   static bool shape(int nt, int grouped, KernelShape* out) {
     if (grouped) return nt == 1 && shape_one<C1H>(out);
+    if constexpr (kTc) {
+      if (nt > 1) return nt == 2 ? shape_tc<2>(out) : nt == 3 ? shape_tc<3>(out) : nt == 4 && shape_tc<4>(out);
+      return shape_one<C1>(out);
+    } else
     switch (nt) {
       case 1: return shape_one<C1>(out);
       case 2: return shape_one<C2>(out);
@@ -93,6 +115,13 @@ struct ScoredShapes {
   static cudaError_t launch(int nt, int grouped, const CUtensorMap& tk, const CUtensorMap& tv, const ScoredParams& p,
                             int grid, cudaStream_t s) {
     if (grouped) return nt == 1 ? launch_one<C1H>(tk, tv, p, grid, s) : cudaErrorInvalidValue;
+    if constexpr (kTc) {
+      return nt == 1   ? launch_one<C1>(tk, tv, p, grid, s)
+             : nt == 2 ? launch_tc<2>(tk, tv, p, grid, s)
+             : nt == 3 ? launch_tc<3>(tk, tv, p, grid, s)
+             : nt == 4 ? launch_tc<4>(tk, tv, p, grid, s)
+                       : cudaErrorInvalidValue;
+    } else
     switch (nt) {
       case 1: return launch_one<C1>(tk, tv, p, grid, s);
       case 2: return launch_one<C2>(tk, tv, p, grid, s);

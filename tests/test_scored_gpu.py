@@ -255,3 +255,24 @@ def test_binding_refusals(pd):
         pd.decode_paged_scored(*args, **sf, key_weights=up(w.key_weights), workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
     with pytest.raises((TypeError, ValueError, pd.DecodeError)):
         pd.decode_paged(*args)  # 4-bit caches are the scored decode's
+
+
+@pytest.mark.parametrize("q", ("f16", "bf16"))
+@pytest.mark.parametrize("kv,one", [("f16", 0.92), ("bf16", 0.92), ("fp8", 72.0), ("int8", 24.0), ("fp4", None)])
+@pytest.mark.parametrize("qlen", (1, 3))
+def test_a_dominant_key(pd, kv, one, q, qlen):
+    """One key weighs 2^15 times as much as each of 8000 others, which together count for a fifth of the output. Three-term
+    weights are held to 2^-22 of the largest, for each key: 2^-22 sum |v| beside the usual bound."""
+    w = Work(kv, 6, 1, 128, [8000], qlen=qlen, q=q, seed=15)
+    w.q = torch.ones_like(w.q)
+    at = (int(w.table[0, 0]), slice(None), 0) if kv == "fp4" else (int(w.table[0, 0]), 0)
+    w.caches[0] = torch.zeros_like(w.caches[0])
+    if kv == "fp4":
+        w.caches[0][at], w.sf[0][at] = 0x66, 40.0  # (code 4)
+        w.caches[1] &= 0x77
+    else:
+        w.caches[0][at] = torch.tensor(one).to(w.caches[0].dtype)
+        w.caches[1] = w.caches[1].float().abs().to(w.caches[1].dtype)
+    ref = list(w.reference())
+    ref[1] = ref[1] + 2.0 ** -22 * w.value(1)[w.table[0].long()].flatten(0, 1).abs().sum(0).max()
+    check(w, w.run(pd), ref)
