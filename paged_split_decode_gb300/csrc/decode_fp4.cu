@@ -4,13 +4,17 @@
 namespace pd {
 namespace {
 
-// Shapes by row tiles of 8 query rows per KV head: row tiles of a warp, row groups, key groups, tiles
-// a step, steps in the ring, CTAs per SM.
+// Shapes by row tiles of 8 query rows per KV head: row tiles of a warp, row groups, key groups, steps in the ring,
+// CTAs per SM. One row tile: four CTAs of four warps (B = 32, L = 4096: 43.1 us; one CTA of 16 warps 49.2). Three
+// tiles in one warp read and convert a tile once: D = 128, 18 rows, B = 32, L = 4096 50.6 us, two groups of two
+// 62.6 (D = 256 103 and 118; at L = 512 36.3 and 34.0); four tiles, D = 128, 58.3 and 65.8 (D = 256: their sums do
+// not fit the registers).
 template <int D, bool QB>
 struct Shapes {
-  using C1 = std::conditional_t<D == 256, Fp4Cfg<256, 1, 1, 4, 1, 2, 4, QB>, Fp4Cfg<128, 1, 1, 4, 1, 3, 5, QB>>;
-  using C2 = std::conditional_t<D == 256, Fp4Cfg<256, 2, 1, 8, 1, 4, 1, QB>, Fp4Cfg<128, 2, 1, 6, 1, 6, 2, QB>>;
-  using C4 = std::conditional_t<D == 256, Fp4Cfg<256, 2, 2, 4, 1, 4, 1, QB>, Fp4Cfg<128, 2, 2, 3, 1, 6, 2, QB>>;
+  using C1 = std::conditional_t<D == 256, Fp4Cfg<256, 1, 1, 4, 2, 4, QB>, Fp4Cfg<128, 1, 1, 4, 3, 5, QB>>;
+  using C2 = std::conditional_t<D == 256, Fp4Cfg<256, 2, 1, 8, 4, 1, QB>, Fp4Cfg<128, 2, 1, 6, 6, 2, QB>>;
+  using C3 = std::conditional_t<D == 256, Fp4Cfg<256, 3, 1, 6, 6, 1, QB>, Fp4Cfg<128, 3, 1, 6, 6, 2, QB>>;
+  using C4 = std::conditional_t<D == 256, Fp4Cfg<256, 2, 2, 4, 4, 1, QB>, Fp4Cfg<128, 4, 1, 4, 8, 2, QB>>;
 
   template <class C>
   static bool shape_one(KernelShape* out) {
@@ -34,12 +38,13 @@ struct Shapes {
     return launch_pdl(decode_fp4_kernel<C>, grid, C::kThreads, C::kSmemBytes, s, 1, p);
   }
   static bool shape(int nt, KernelShape* out) {
-    return nt == 1 ? shape_one<C1>(out) : nt == 2 ? shape_one<C2>(out) : nt <= 4 && shape_one<C4>(out);
+    return nt == 1 ? shape_one<C1>(out) : nt == 2 ? shape_one<C2>(out) : nt == 3 ? shape_one<C3>(out) : nt == 4 && shape_one<C4>(out);
   }
   static cudaError_t launch(int nt, const Fp4Params& p, int grid, cudaStream_t s) {
     return nt == 1 ? launch_one<C1>(p, grid, s)
            : nt == 2 ? launch_one<C2>(p, grid, s)
-           : nt <= 4 ? launch_one<C4>(p, grid, s)
+           : nt == 3 ? launch_one<C3>(p, grid, s)
+           : nt == 4 ? launch_one<C4>(p, grid, s)
                      : cudaErrorInvalidValue;
   }
 };

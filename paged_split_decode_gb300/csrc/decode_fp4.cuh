@@ -43,18 +43,17 @@ struct Fp4Params : ScoredParams {
 };
 
 // NT: row tiles of 8 query rows that a warp computes, RG: row groups of that many
-// (warps that read the same tiles), KG: key groups, ST: steps in a warp's ring, KT:
-// tiles a step.
-template <int D_, int NT_, int RG_, int KG_, int KT_, int ST_, int MINB_, bool QB_>
+// (warps that read the same tiles), KG: key groups, ST: tiles in a warp's ring.
+template <int D_, int NT_, int RG_, int KG_, int ST_, int MINB_, bool QB_>
 struct Fp4Cfg {
-  static constexpr int D = D_, NT = NT_, RG = RG_, KG = KG_, KT = KT_, ST = ST_, kMinBlocks = MINB_;
+  static constexpr int D = D_, NT = NT_, RG = RG_, KG = KG_, ST = ST_, kMinBlocks = MINB_;
   static constexpr bool QB = QB_;
   // P as two operands unless a bfloat16 output's own rounding hides one (see decode_kernel.cuh)
   static constexpr int PP = QB ? 1 : 2;
   static constexpr int kWarps = KG * RG, kThreads = kWarps * 32;
   static constexpr int kCodes = kTileKeys * D / 2, kScales = kTileKeys * D / 16;
   static constexpr int kTile = 2 * kCodes + 2 * kScales;  // K codes, V codes, K scales, V scales
-  static constexpr int kStage = KT * kTile;
+  static constexpr int kStage = kTile;
   static constexpr int kRing = ST * kStage;               // a warp's
   static constexpr int MT = D / 16;                       // m-tiles (pairs of dims by lane)
   static constexpr int kPitch = 33;                       // float4 pitch of an m-tile's fragments in the merge
@@ -258,7 +257,7 @@ __device__ __forceinline__ void fp4_join(const ScoredParams& p, const Piece& pc,
 
 template <class Cfg>
 __global__ void __launch_bounds__(Cfg::kThreads, Cfg::kMinBlocks) decode_fp4_kernel(const Fp4Params p) {
-  constexpr int D = Cfg::D, NT = Cfg::NT, RG = Cfg::RG, KG = Cfg::KG, KT = Cfg::KT, ST = Cfg::ST, MT = Cfg::MT;
+  constexpr int D = Cfg::D, NT = Cfg::NT, RG = Cfg::RG, KG = Cfg::KG, ST = Cfg::ST, MT = Cfg::MT;
   constexpr int PP = Cfg::PP;
   extern __shared__ __align__(128) uint8_t smem[];
   float2* s_ml = reinterpret_cast<float2*>(smem + Cfg::kOffML);
@@ -290,66 +289,52 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::kMinBlocks) decode_fp4_ker
     const int kh = pc.kh, ntiles = warp_uniform(pc.ntiles), seq_len = warp_uniform(pc.L);
     const int lo_all = warp_uniform(pc.tile_lo_all), hi_all = warp_uniform(pc.tile_hi_all);
     const int prefix = warp_uniform(pc.prefix);
-    // ---- copies of the warp's steps: step i is tiles (i KG + kg) KT ..
-    const int steps = (ntiles - kg * KT + KG * KT - 1) / (KG * KT);  // (<= 0: none)
+    // ---- copies of the warp's steps: step i is tile i KG + kg
+    const int steps = (ntiles - kg + KG - 1) / KG;  // (<= 0: none)
     const int32_t* row = p.block_table + static_cast<long long>(pc.b) * p.max_blocks;
-    auto load_blocks = [&](int i0, int (&blk)[KT]) {  // lane: the physical blocks of step i0 + lane
-#pragma unroll
-      for (int j = 0; j < KT; ++j) {
-        const int k = ((i0 + lane) * KG + kg) * KT + j;
-        blk[j] = 0;
-        if (k < ntiles) blk[j] = __ldg(row + piece_tile(p, pc, k) / p.tiles_per_block);
-      }
+    auto load_block = [&](int i0) -> int {  // lane: the physical block of step i0 + lane
+      const int k = (i0 + lane) * KG + kg;
+      return k < ntiles ? __ldg(row + piece_tile(p, pc, k) / p.tiles_per_block) : 0;
     };
-    int cur[KT], nxt[KT];  // lane: the tile in the caches' order, of step (i & ~31) + lane; blocks of the steps after
-    auto to_tiles = [&](int i0, const int (&blk)[KT], int (&tile)[KT]) {
-#pragma unroll
-      for (int j = 0; j < KT; ++j) {
-        int b = blk[j];
-        if (b < 0 || b >= p.num_blocks) {
-          raise_error(p.error_flag, kErrBlockId);
-          b = 0;
-        }
-        tile[j] = (b * p.Hkv + kh) * p.tiles_per_block +
-                  piece_tile(p, pc, ((i0 + lane) * KG + kg) * KT + j) % p.tiles_per_block;
+    int cur = 0, nxt = load_block(0);  // lane: the tile in the caches' order, of step (i & ~31) + lane; blocks of the steps after
+    auto to_tile = [&](int i0, int blk) -> int {
+      if (blk < 0 || blk >= p.num_blocks) {
+        raise_error(p.error_flag, kErrBlockId);
+        blk = 0;
       }
+      return (blk * p.Hkv + kh) * p.tiles_per_block + piece_tile(p, pc, (i0 + lane) * KG + kg) % p.tiles_per_block;
     };
-    load_blocks(0, nxt);
     int next = 0;              // the step whose copies are next
     uint32_t fill = ring;      // and its stage
     auto issue = [&]() {
       if (next < steps) {
         if ((next & 31) == 0) {
-          to_tiles(next, nxt, cur);
-          load_blocks(next + 32, nxt);
+          cur = to_tile(next, nxt);
+          nxt = load_block(next + 32);
         }
+        const long long tile = __shfl_sync(0xffffffffu, cur, next & 31);
+        const uint8_t* kc = k_src + tile * Cfg::kCodes;
+        const uint8_t* vc = v_src + tile * Cfg::kCodes;
+        const uint8_t* sf = sf_src + tile * Cfg::kScales;
+        const uint32_t dst = fill + lane * 16;
+        if constexpr (D == 256) {
 #pragma unroll
-        for (int j = 0; j < KT; ++j) {
-          const long long tile = __shfl_sync(0xffffffffu, cur[j], next & 31);
-          if (KT > 1 && (next * KG + kg) * KT + j >= ntiles) continue;
-          const uint8_t* kc = k_src + tile * Cfg::kCodes;
-          const uint8_t* vc = v_src + tile * Cfg::kCodes;
-          const uint8_t* sf = sf_src + tile * Cfg::kScales;
-          const uint32_t dst = fill + j * Cfg::kTile + lane * 16;
-          if constexpr (D == 256) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              cp_async16(dst + q * 512, kc + (q >> 1) * 1024 + (q & 1) * 64);
-              cp_async16(dst + Cfg::kCodes + q * 512, vc + (q >> 1) * 1024 + (q & 1) * 128);
-            }
-            cp_async16(dst + 2 * Cfg::kCodes, sf);
-          } else {
-            // V: 16-byte piece c of line l (two keys' rows) lies at c ^ 2 l of its line: the lanes of
-            // a read (keys 2 t4, 8-byte chunks g) meet all banks
-            const int line = lane >> 3;
-            const uint32_t vd = fill + j * Cfg::kTile + Cfg::kCodes + line * 128 + (((lane & 7) ^ (2 * line)) << 4);
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-              cp_async16(dst + q * 512, kc + q * 512);
-              cp_async16(vd + q * 512, vc + q * 512);
-            }
-            if (lane < 2 * kSfLanes) cp_async16(dst + 2 * Cfg::kCodes, sf);
+          for (int q = 0; q < 4; ++q) {
+            cp_async16(dst + q * 512, kc + (q >> 1) * 1024 + (q & 1) * 64);
+            cp_async16(dst + Cfg::kCodes + q * 512, vc + (q >> 1) * 1024 + (q & 1) * 128);
           }
+          cp_async16(dst + 2 * Cfg::kCodes, sf);
+        } else {
+          // V: 16-byte piece c of line l (two keys' rows) lies at c ^ 2 l of its line: the lanes of
+          // a read (keys 2 t4, 8-byte chunks g) meet all banks
+          const int line = lane >> 3;
+          const uint32_t vd = fill + Cfg::kCodes + line * 128 + (((lane & 7) ^ (2 * line)) << 4);
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            cp_async16(dst + q * 512, kc + q * 512);
+            cp_async16(vd + q * 512, vc + q * 512);
+          }
+          if (lane < 2 * kSfLanes) cp_async16(dst + 2 * Cfg::kCodes, sf);
         }
       }
       cp_async_commit();
@@ -428,20 +413,19 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::kMinBlocks) decode_fp4_ker
 
     uint32_t stage = ring;
     // A step is compiled twice: for tiles that every row sees whole, and for the others (EDGE:
-    // masks, scales that are no numbers, a missing tile).
+    // masks, scales that are no numbers).
     auto step = [&](const int i, auto edge_step) __attribute__((always_inline)) {
       constexpr bool EDGE = decltype(edge_step)::value;
-      const int k0 = (i * KG + kg) * KT;
-      // ---- S^T = K Q^T: 16 keys x 8 rows for each tile and row tile
-      float x[KT][NT][4];
-#pragma unroll
-      for (int j = 0; j < KT; ++j) {
+      const int key0 = piece_tile(p, pc, i * KG + kg) * kTileKeys;
+      // ---- S^T = K Q^T: 16 keys x 8 rows for each row tile
+      float x[NT][4];
+      {
         float sa[NT][4], sb[NT][4];
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int e = 0; e < 4; ++e) sa[n][e] = sb[n][e] = 0.f;
-        const uint32_t kt = stage + j * Cfg::kTile;
+        const uint32_t kt = stage;
         constexpr int NC = D / 128;  // 16-byte chunks of a key that a lane holds
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
@@ -471,49 +455,42 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::kMinBlocks) decode_fp4_ker
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) x[j][n][e] = (sa[n][e] + sb[n][e]) * sl2r[n][e & 1];
+          for (int e = 0; e < 4; ++e) x[n][e] = (sa[n][e] + sb[n][e]) * sl2r[n][e & 1];
       }
       // ---- caps, biases, masks
-      bool there[KT];
-      int key0[KT];
+      const int j0 = key0 + g;
+      if (p.cap_out > 0.f) {
 #pragma unroll
-      for (int j = 0; j < KT; ++j) {
-        there[j] = !EDGE || k0 + j < ntiles;
-        key0[j] = piece_tile(p, pc, k0 + j) * kTileKeys;
-        const int j0 = key0[j] + g;
-        if (p.cap_out > 0.f) {
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int n = 0; n < NT; ++n)
+          for (int e = 0; e < 4; ++e) x[n][e] = p.cap_out * tanh_f32(x[n][e] * p.cap_u);
+      }
+      if (p.slopes != nullptr) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) x[j][n][e] = p.cap_out * tanh_f32(x[j][n][e] * p.cap_u);
-        }
-        if (p.slopes != nullptr) {
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              const int r = (rg * NT + n) * 8 + 2 * t4 + c;
-              const float slope = r < pc.R ? __ldg(p.slopes + kh * p.G + r % p.G) * kLog2e : 0.f;
-              x[j][n][c] -= slope * static_cast<float>(abs(j0 - hi_r[n][c]));
-              x[j][n][c + 2] -= slope * static_cast<float>(abs(j0 + 8 - hi_r[n][c]));
-            }
-        }
-        if constexpr (EDGE) {  // (padded rows: q = 0, never written)
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (!there[j] || !row_sees(p, pc, (rg * NT + n) * 8 + 2 * t4 + (e & 1), j0 + (e >> 1) * 8))
-                x[j][n][e] = -INFINITY;
-        }
-        if (p.scores != nullptr && there[j]) {
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            float* dst = p.scores + ((static_cast<long long>(pc.b) * p.Hkv + kh) * p.max_blocks * p.tiles_per_block +
-                                     key0[j] / kTileKeys) * (RG * NT * 128) + (rg * NT + n) * 128 + g * 8 + 2 * t4;
-            __stcg(reinterpret_cast<float2*>(dst), make_float2(x[j][n][0], x[j][n][1]));
-            __stcg(reinterpret_cast<float2*>(dst + 64), make_float2(x[j][n][2], x[j][n][3]));
+          for (int c = 0; c < 2; ++c) {
+            const int r = (rg * NT + n) * 8 + 2 * t4 + c;
+            const float slope = r < pc.R ? __ldg(p.slopes + kh * p.G + r % p.G) * kLog2e : 0.f;
+            x[n][c] -= slope * static_cast<float>(abs(j0 - hi_r[n][c]));
+            x[n][c + 2] -= slope * static_cast<float>(abs(j0 + 8 - hi_r[n][c]));
           }
+      }
+      if constexpr (EDGE) {  // (padded rows: q = 0, never written)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (!row_sees(p, pc, (rg * NT + n) * 8 + 2 * t4 + (e & 1), j0 + (e >> 1) * 8))
+              x[n][e] = -INFINITY;
+      }
+      if (p.scores != nullptr) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          float* dst = p.scores + ((static_cast<long long>(pc.b) * p.Hkv + kh) * p.max_blocks * p.tiles_per_block +
+                                   key0 / kTileKeys) * (RG * NT * 128) + (rg * NT + n) * 128 + g * 8 + 2 * t4;
+          __stcg(reinterpret_cast<float2*>(dst), make_float2(x[n][0], x[n][1]));
+          __stcg(reinterpret_cast<float2*>(dst + 64), make_float2(x[n][2], x[n][3]));
         }
       }
       // ---- softmax: weights relative to a reference that is at most 2^8 below a score,
@@ -524,18 +501,14 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::kMinBlocks) decode_fp4_ker
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          float mx = fmaxf(x[0][n][c], x[0][n][c + 2]);
-          if constexpr (KT > 1) mx = fmaxf(mx, fmaxf(x[KT - 1][n][c], x[KT - 1][n][c + 2]));
-          up |= mx - m_r[n][c] > 8.f;  // (no key seen: m = -inf)
+          up |= fmaxf(x[n][c], x[n][c + 2]) - m_r[n][c] > 8.f;  // (no key seen: m = -inf)
         }
       if (__any_sync(0xffffffffu, up)) {
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            float mx = m_r[n][c];
-#pragma unroll
-            for (int j = 0; j < KT; ++j) mx = fmaxf(mx, fmaxf(x[j][n][c], x[j][n][c + 2]));
+            float mx = fmaxf(m_r[n][c], fmaxf(x[n][c], x[n][c + 2]));
 #pragma unroll
             for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
             const float al = m_r[n][c] == -INFINITY ? 1.f : ex2(m_r[n][c] - mx);  // (O and l are zero before the first)
@@ -548,50 +521,36 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::kMinBlocks) decode_fp4_ker
             }
           }
       }
-      uint32_t pb[KT][NT][2], pl[PP == 2 ? KT : 1][NT][2] = {};
+      uint32_t pb[NT][2], pl[NT][2] = {};
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         const float b0 = m_r[n][0] == -INFINITY ? 0.f : 7.f - m_r[n][0];
         const float b1 = m_r[n][1] == -INFINITY ? 0.f : 7.f - m_r[n][1];
-#pragma unroll
-        for (int j = 0; j < KT; ++j) {
-          const float p0 = ex2(x[j][n][0] + b0), p1 = ex2(x[j][n][1] + b1), p2 = ex2(x[j][n][2] + b0),
-                      p3 = ex2(x[j][n][3] + b1);
-          l_r[n][0] += p0 + p2;
-          l_r[n][1] += p1 + p3;
-          const uint32_t w0 = pack_half2(p0, p1), w1 = pack_half2(p2, p3);
-          pb[j][n][0] = movmatrix_trans(w0);
-          pb[j][n][1] = movmatrix_trans(w1);
-          if constexpr (PP == 2) {
-            const float2 h0 = unpack2<false>(w0), h1 = unpack2<false>(w1);
-            pl[j][n][0] = movmatrix_trans(pack_half2(p0 - h0.x, p1 - h0.y));
-            pl[j][n][1] = movmatrix_trans(pack_half2(p2 - h1.x, p3 - h1.y));
-          }
+        const float p0 = ex2(x[n][0] + b0), p1 = ex2(x[n][1] + b1), p2 = ex2(x[n][2] + b0), p3 = ex2(x[n][3] + b1);
+        l_r[n][0] += p0 + p2;
+        l_r[n][1] += p1 + p3;
+        const uint32_t w0 = pack_half2(p0, p1), w1 = pack_half2(p2, p3);
+        pb[n][0] = movmatrix_trans(w0);
+        pb[n][1] = movmatrix_trans(w1);
+        if constexpr (PP == 2) {
+          const float2 h0 = unpack2<false>(w0), h1 = unpack2<false>(w1);
+          pl[n][0] = movmatrix_trans(pack_half2(p0 - h0.x, p1 - h0.y));
+          pl[n][1] = movmatrix_trans(pack_half2(p2 - h1.x, p3 - h1.y));
         }
       }
       // ---- O^T += V^T P^T
-#pragma unroll
-      for (int j = 0; j < KT; ++j) {
-        if (EDGE && !there[j]) continue;
-        const uint32_t vt = stage + j * Cfg::kTile + Cfg::kCodes;
-        const uint32_t sf = stage + j * Cfg::kTile + 2 * Cfg::kCodes + Cfg::kScales;
-        fp4_pv<D, NT, PP, EDGE>(p, pc, rg * NT * 8, vt, sf, lane, key0[j], seq_len, pb[j], pl[PP == 2 ? j : 0], o);
-      }
+      fp4_pv<D, NT, PP, EDGE>(p, pc, rg * NT * 8, stage + Cfg::kCodes, stage + 2 * Cfg::kCodes + Cfg::kScales, lane, key0,
+                              seq_len, pb, pl, o);
     };
     for (int i = 0; i < steps; ++i) {
       cp_async_wait<ST - 2>();
       __syncwarp();  // the step's scales are there, and every lane is done with the stage that is filled next
       issue();
-      const int k0 = (i * KG + kg) * KT;
-      bool plain = KT == 1 || k0 + KT <= ntiles;
-#pragma unroll
-      for (int j = 0; j < KT; ++j) {
-        const int key0 = piece_tile(p, pc, k0 + j) * kTileKeys;
-        plain = plain && ((key0 >= lo_all && key0 + kTileKeys - 1 <= hi_all) ||
-                          (key0 + kTileKeys <= prefix && hi_all >= 0));
-      }
-      if (plain) step(i, std::false_type());
-      else step(i, std::true_type());
+      const int key0 = piece_tile(p, pc, i * KG + kg) * kTileKeys;
+      if ((key0 >= lo_all && key0 + kTileKeys - 1 <= hi_all) || (key0 + kTileKeys <= prefix && hi_all >= 0))
+        step(i, std::false_type());
+      else
+        step(i, std::true_type());
       stage = stage == ring + (ST - 1) * Cfg::kStage ? ring : stage + Cfg::kStage;
     }
 

@@ -8,9 +8,14 @@
 // tokens start from zero, keys that no row sees keep their sum.
 //
 // Bytes: 32 a key, head and row tile of eight rows, written by the decode and
-// read here mostly from L2 (B = 32, L = 4096, four heads: 17 MB), and 8 for the
-// sums; against 512 to 2048 for the key's K and V. A thread a key: its eight rows
-// are two 16-byte loads, the rows' (m, 1 / l) come from shared memory.
+// read here, and 8 for the sums; against 512 to 2048 for the key's K and V. A thread
+// takes two keys: each one's eight rows are two 16-byte loads, the rows' (m, 1 / l) come
+// from shared memory. Bound by the latency of two dependent loads: the table and the old
+// sums are read before the decode's end is waited for, and a CTA has 256 keys only, so
+// that long sequences of a ragged batch spread over the SMs (32 sequences of up to 16384
+// keys, four heads of seven rows, 4-bit: the call takes 100.1 us with CTAs of 128 threads
+// and two keys a thread, 113.0 with four, 119.6 with eight; 115.6 with one key of 256
+// threads and every load behind the wait; without this launch 86.8).
 #include <algorithm>
 
 #include "scored_launch.h"
@@ -18,7 +23,8 @@
 namespace pd {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
+constexpr int kKeys = 2;  // keys of a thread, in flight together
 
 __global__ void __launch_bounds__(kThreads) key_weights_kernel(const KeyWeightParams kp) {
   const ScoredParams& p = kp.d;
@@ -26,46 +32,74 @@ __global__ void __launch_bounds__(kThreads) key_weights_kernel(const KeyWeightPa
   const int u = blockIdx.x / kp.chunks, c = blockIdx.x % kp.chunks;  // unit, share of its keys
   const int b = u / p.Hkv, kh = u % p.Hkv;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // lengths, table and the old sums are not the decode's: they are read before its end
   int L, t0, n, q0, qn;
   seq_span(p, b, false, L, t0, n, q0, qn);
-  if (c * kThreads >= L) return;
   const int R = p.G * qn;
-  if (threadIdx.x < 32) {
-    float2 v = make_float2(0.f, 0.f);
-    if (static_cast<int>(threadIdx.x) < R) {
-      v = __ldcg(p.row_ml + (static_cast<long long>(b) * p.qlen + threadIdx.x / p.G) * p.Hq + kh * p.G + threadIdx.x % p.G);
-      v.y = v.y == 0.f ? 0.f : 1.f / v.y;
-    }
-    s_row[threadIdx.x] = v;
-  }
-  __syncthreads();
   // visible tiles: [0, np) and [first, ...)
   const int first = p.window > 0 ? max(0, L - qn - p.window + 1) / kTileKeys : 0;
   const int np = (prefix_of(p, b, L) + kTileKeys - 1) / kTileKeys;
-  const float* scores = p.scores + static_cast<long long>(u) * p.max_blocks * p.tiles_per_block * (kp.row_tiles * 128);
+  const int stride = kp.row_tiles * 128;  // floats of a tile
+  const float* scores = p.scores + static_cast<long long>(u) * p.max_blocks * p.tiles_per_block * stride;
   const int32_t* row = p.block_table + static_cast<long long>(b) * p.max_blocks;
-  for (int j = c * kThreads + threadIdx.x; j < L; j += kp.chunks * kThreads) {
-    const int blk = __ldg(row + j / p.block_size);
-    if (blk < 0 || blk >= p.num_blocks) continue;  // (the decode reported it, where it is visible)
-    const long long at = (static_cast<long long>(blk) * p.Hkv + kh) * p.block_size + j % p.block_size;
-    const float old = j < L - qn ? kp.in[at] : 0.f;
-    const int tile = j / kTileKeys;
-    float sum = 0.f;
-    if (tile < np || tile >= first) {
-      const float* src = scores + static_cast<long long>(tile) * (kp.row_tiles * 128) + (j % kTileKeys) * 8;
-      for (int r = 0; r < R; r += 8) {
-        const float4 a = __ldcg(reinterpret_cast<const float4*>(src + r * 16));
-        const float4 c = __ldcg(reinterpret_cast<const float4*>(src + r * 16 + 4));
-        const float x[8] = {a.x, a.y, a.z, a.w, c.x, c.y, c.z, c.w};
+  bool ready = false;
+  for (int j0 = c * kThreads * kKeys; j0 < L; j0 += kp.chunks * kThreads * kKeys) {
+    long long at[kKeys];
+    float old[kKeys], sum[kKeys];
+    const float* src[kKeys];  // null: no row sees the key
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float2 ml = s_row[r + e];
-          if (r + e < R && x[e] != -INFINITY) sum += ex2(x[e] - ml.x) * ml.y;
+    for (int k = 0; k < kKeys; ++k) {
+      const int j = j0 + k * kThreads + threadIdx.x;
+      const int blk = j < L ? __ldg(row + j / p.block_size) : -1;
+      // (a bad block: the decode reported it, where it is visible)
+      at[k] = blk < 0 || blk >= p.num_blocks
+                  ? -1 : (static_cast<long long>(blk) * p.Hkv + kh) * p.block_size + j % p.block_size;
+    }
+#pragma unroll
+    for (int k = 0; k < kKeys; ++k) {
+      const int j = j0 + k * kThreads + threadIdx.x, tile = j / kTileKeys;
+      old[k] = at[k] >= 0 && j < L - qn ? kp.in[at[k]] : 0.f;
+      sum[k] = 0.f;
+      src[k] = at[k] >= 0 && (tile < np || tile >= first)
+                   ? scores + static_cast<long long>(tile) * stride + (j % kTileKeys) * 8 : nullptr;
+    }
+    if (!ready) {
+      asm volatile("griddepcontrol.wait;" ::: "memory");
+      if (threadIdx.x < 32) {
+        float2 v = make_float2(0.f, 0.f);
+        if (static_cast<int>(threadIdx.x) < R) {
+          v = __ldcg(p.row_ml + (static_cast<long long>(b) * p.qlen + threadIdx.x / p.G) * p.Hq + kh * p.G +
+                     threadIdx.x % p.G);
+          v.y = v.y == 0.f ? 0.f : 1.f / v.y;
+        }
+        s_row[threadIdx.x] = v;
+      }
+    }
+    for (int r = 0; r < R; r += 8) {
+      float4 x[kKeys][2];
+#pragma unroll
+      for (int k = 0; k < kKeys; ++k)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          x[k][h] = src[k] ? __ldcg(reinterpret_cast<const float4*>(src[k] + r * 16) + h)
+                           : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+      if (!ready) __syncthreads();
+      ready = true;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float2 ml = s_row[r + e];
+        if (r + e >= R) break;
+#pragma unroll
+        for (int k = 0; k < kKeys; ++k) {
+          const float4 v = x[k][e >> 2];
+          const float y = (e & 3) == 0 ? v.x : (e & 3) == 1 ? v.y : (e & 3) == 2 ? v.z : v.w;
+          if (y != -INFINITY) sum[k] += ex2(y - ml.x) * ml.y;
         }
       }
     }
-    kp.out[at] = old + sum;
+#pragma unroll
+    for (int k = 0; k < kKeys; ++k)
+      if (at[k] >= 0) kp.out[at[k]] = old[k] + sum[k];
   }
 }
 
@@ -76,7 +110,7 @@ cudaError_t launch_key_weights(KeyWeightParams p, int sms, cudaStream_t stream) 
   const long long units = static_cast<long long>(p.d.B) * p.d.Hkv;
   const long long keys = static_cast<long long>(p.d.max_blocks) * p.d.block_size;
   const long long most = std::max<long long>(1, 64ll * sms / units);
-  p.chunks = static_cast<int>(std::max<long long>(1, std::min((keys + kThreads - 1) / kThreads, most)));
+  p.chunks = static_cast<int>(std::max<long long>(1, std::min((keys + kThreads * kKeys - 1) / (kThreads * kKeys), most)));
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(units * p.chunks));
   cfg.blockDim = dim3(kThreads);
