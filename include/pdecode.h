@@ -262,7 +262,7 @@ PD_API pd_status decode_paged_diff(const void* q, const void* k_cache, const voi
 
 /* What a scored decode does beside decode_paged's arithmetic. Zeros and NULLs
  * leave a part out.
- *   cap             y = cap * tanh(y / cap) on every scaled score (0: none; else >= 1e-30)
+ *   cap             y = cap * tanh(y / cap) on every scaled score (0: none; else 1e-30 .. 1e30)
  *   alibi_slopes    device fp32 [Hq]: slope[h] * |position of the query token - position of
  *                   the key| is taken off the (capped) score
  *   prefix_lens     device int32 [B]: the first prefix_lens[b] keys of sequence b are visible
@@ -302,8 +302,9 @@ typedef struct {
  * key_weights_out != NULL, 0) bytes.
  * A row without a visible key is zeros. NaN scores, and NaN and infinities of V, show in the
  * rows that see the key, as NaN or infinity, and in no other. Softmax weights are computed
- * in fp32 and enter the product with V as two 16-bit operands, or rounded once to fp16 where a
- * bfloat16 out over 8- and 4-bit caches hides it; every sum is fp32. Caches of 8-bit codes
+ * in fp32 and enter the product with V as two 16-bit operands, as three e4m3 ones (e4m3
+ * caches, more than 8 rows per KV head: 12 bits), or rounded once to fp16 where a bfloat16
+ * out over 8- and 4-bit caches hides it; every sum is fp32. int8 caches under an fp16 q
  * with Hq/Hkv*qlen > 8 run slower than in decode_paged. */
 PD_API size_t pd_scored_workspace_bytes(const pd_dims* dims, int qlen, int num_splits, int key_weights, int sm_count);
 PD_API pd_status decode_paged_scored(const void* q, const void* k_cache, const void* v_cache,

@@ -636,7 +636,7 @@ pd_status decode_paged_scored(const void* q, const void* k_cache, const void* v_
   }
   const pd_score& sc = *score;
   const bool fp4 = fp4_kind(dims->kv_dtype), weights = sc.key_weights_out != nullptr;
-  if (!std::isfinite(sc.cap) || sc.cap < 0.f || (sc.cap > 0.f && !(sc.cap >= 1e-30f))) return PD_ERR_SHAPE;
+  if (!(sc.cap == 0.f || (sc.cap >= 1e-30f && sc.cap <= 1e30f))) return PD_ERR_SHAPE;
   if (misaligned(sc.alibi_slopes, 3) || misaligned(sc.prefix_lens, 3) || misaligned(sc.lse, 3) ||
       misaligned(sc.key_weights, 3) || misaligned(sc.key_weights_out, 3) || misaligned(sc.k_block_scale, 15) ||
       misaligned(sc.v_block_scale, 15))

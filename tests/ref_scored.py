@@ -3,8 +3,11 @@ kernels.
 
 Bound per output element. A row's weights w_j (summing to one) meet the product with V as two 16-bit operands, which
 leave u = 2^-20 (fp16: a rest below half an fp16 step of half an fp16 step, with one binade to spare) or 2^-15
-(bfloat16) of each, or as one fp16 operand, 2^-11, where the output is bfloat16 over 8- and 4-bit caches. Tiny weights
-are held to 2^-31 of the largest, of at most 2^11 keys here: 2^-20 of the sum, inside f. The fp32 parts move a weight
+(bfloat16) of each, or as one fp16 operand, 2^-11, where the output is bfloat16 over 8- and 4-bit caches. Over e4m3
+caches with more than 8 rows per KV head they are three e4m3 operands: three nearest roundings to 4 bits leave 2^-4 each,
+2^-12 in all (beside a bfloat16 output less than the 2^-11 that it is given), and the last one's smallest step, 2^-9
+times 2^-8, half of which is 2^-18 beside a largest weight of 2^4 or more: 2^-22, of either sign, so that 2^12 keys
+add up to 2^-16. Elsewhere tiny weights are held to 2^-31 of the largest, of at most 2^11 keys here: 2^-20 of the sum, inside f. The fp32 parts move a weight
 by a relative amount f: a score is a sum of D products, off by at most D 2^-24 sum |q_d k_d| scale, for the N(0, 1)
 rows drawn here (D = 256, sum |q_d k_d| < 300, scale 1 / 16) 2^-12; tanh to 2^-21 of itself, times a cap of at most 50:
 2^-15; a bias of up to 2^10 nats to 2^-14; f = 2^-11 stands for all of it. So with A = sum_j w_j |v_j|
@@ -86,7 +89,8 @@ class Work:
     def u(self):
         if self.qt == torch.bfloat16:
             return 2.0 ** -15 if self.kv == "bf16" else 2.0 ** -11
-        return 2.0 ** -20
+        three = self.kv == "fp8" and self.Hq // self.Hkv * self.qlen > 8
+        return 2.0 ** -12 if three else 2.0 ** -20
 
     def reference(self):
         """out, its bound, lse, its bound, key weights, their bound; rows of no sequence are None-like NaN."""

@@ -59,7 +59,7 @@ def test_scored_refusals(lib, kind):
     for name in ("alibi_slopes", "prefix_lens", "lse", "key_weights", "key_weights_out"):
         assert _scored(lib, d, **{name: 18}, **sf) == ALIGN
     assert _scored(lib, d, k_block_scale=24, v_block_scale=16) == ALIGN
-    for cap in (-1.0, math.nan, math.inf, 1e-38):
+    for cap in (-1.0, math.nan, math.inf, 1e-38, 3e38):
         assert _scored(lib, d, cap=cap, **sf) == SHAPE
     assert _scored(lib, d, splits=-1, **sf) == SHAPE
     assert _scored(lib, d, qlen=0, **sf) == SHAPE
