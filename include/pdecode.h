@@ -303,7 +303,7 @@ typedef struct {
  * A row without a visible key is zeros. NaN scores, and NaN and infinities of V, show in the
  * rows that see the key, as NaN or infinity, and in no other. Softmax weights are computed
  * in fp32 and enter the product with V as two 16-bit operands, as three e4m3 ones (e4m3
- * caches, more than 8 rows per KV head: 12 bits), or rounded once to fp16 where a bfloat16
+ * caches, more than 8 rows per KV head: 12 bits, and none below 2^-22 of a row's largest), or rounded once to fp16 where a bfloat16
  * out over 8- and 4-bit caches hides it; every sum is fp32. int8 caches under an fp16 q
  * with Hq/Hkv*qlen > 8 run slower than in decode_paged. */
 PD_API size_t pd_scored_workspace_bytes(const pd_dims* dims, int qlen, int num_splits, int key_weights, int sm_count);

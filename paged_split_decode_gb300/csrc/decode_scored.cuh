@@ -4,7 +4,8 @@
 //
 //   y = c q . k;  y = cap tanh(y / cap);  y -= slope_h |p - j|;  out = softmax(y) V
 //
-// HBM-bound: K and V are read once. The decode's frame (decode_kernel.cuh: balanced
+// HBM-bound: K and V are read once (fp16, 24 x 4 heads, D = 256, B = 32, L = 4096, capped: 85.4 us, 0.94 of the
+// copy rate; 32 ragged sequences, D = 128, biased: 0.92 to 1.05). The decode's frame (decode_kernel.cuh: balanced
 // ranges of 16-key tiles, one TMA producer warp, a ring of 128B-swizzled stages,
 // bounded waits, partials and combine) with the differential decode's consumers, for one map:
 //  * A warp serves one row tile of 8 query rows of one head, all of D, so that a score is
