@@ -5,13 +5,15 @@ namespace pd {
 namespace {
 
 // Shapes by row tiles of 8 query rows per KV head: row tiles of a warp, row groups, key groups, steps in the ring,
-// CTAs per SM. One row tile: four CTAs of four warps (B = 32, L = 4096: 43.1 us; one CTA of 16 warps 49.2). Three
+// CTAs per SM. One row tile, L = 4096, B = 1 / 8 / 32: D = 256, two CTAs of six warps 10.1 / 17.8 / 42.5 us, four of
+// four 11.2 / 18.6 / 42.9 (128 registers), two of eight 10.6 / 18.8 / 44.0, one of 16 50.4 at B = 32; D = 128, four of
+// four 9.8 / 12.3 / 28.7, five 10.6 / 13.6 / 31.0, two of eight 9.1 / 13.0 / 26.6 (at L = 1024 15.8 against 12.7). Three
 // tiles in one warp read and convert a tile once: D = 128, 18 rows, B = 32, L = 4096 50.6 us, two groups of two
 // 62.6 (D = 256 103 and 118; at L = 512 36.3 and 34.0); four tiles, D = 128, 58.3 and 65.8 (D = 256: their sums do
 // not fit the registers).
 template <int D, bool QB>
 struct Shapes {
-  using C1 = std::conditional_t<D == 256, Fp4Cfg<256, 1, 1, 4, 2, 4, QB>, Fp4Cfg<128, 1, 1, 4, 3, 5, QB>>;
+  using C1 = std::conditional_t<D == 256, Fp4Cfg<256, 1, 1, 6, 2, 2, QB>, Fp4Cfg<128, 1, 1, 4, 3, 4, QB>>;
   using C2 = std::conditional_t<D == 256, Fp4Cfg<256, 2, 1, 8, 4, 1, QB>, Fp4Cfg<128, 2, 1, 6, 6, 2, QB>>;
   using C3 = std::conditional_t<D == 256, Fp4Cfg<256, 3, 1, 6, 6, 1, QB>, Fp4Cfg<128, 3, 1, 6, 6, 2, QB>>;
   using C4 = std::conditional_t<D == 256, Fp4Cfg<256, 2, 2, 4, 4, 1, QB>, Fp4Cfg<128, 4, 1, 4, 8, 2, QB>>;

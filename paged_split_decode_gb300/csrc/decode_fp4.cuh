@@ -12,7 +12,7 @@
 // what the consumers wait for: a tile of 16 keys of one head (D = 256) takes 128
 // conversions e2m1 -> fp16, as many multiplications by the scales, and 32 to 48
 // mma.sync for 4.6 KB: 640 instructions of a warp in all, 240 cycles of an SM where HBM
-// would take 200 (24 x 4 heads, B = 32, L = 4096: 43.4 us, of which 8 lie around the loop; L = 16384
+// would take 200 (24 x 4 heads, B = 32, L = 4096: 43.3 us, of which 8 lie around the loop; L = 16384
 // 125 us, 0.72 of the copy rate). So no warp does anything else, and none waits for another:
 //  * A unit is (sequence, KV head). Its tiles go to the CTA's warps in turn; every
 //    warp translates pages, copies, computes and keeps (m, l, O) on its own, and the
@@ -22,8 +22,7 @@
 //    the scales, 16 bytes a key, are read across lanes.
 //  * S^T = K Q^T: row g of the A operand is key g, and since the order of the
 //    contraction is free a byte of codes converts straight to an operand register
-//    (two adjacent dims of a key); q lies in shared memory in the same order (its 64
-//    registers a lane bought a fourth CTA an SM: 49 -> 43 us).
+//    (two adjacent dims of a key); q lies in shared memory in the same order.
 //  * O^T = V^T P^T: an operand register is two keys of one dim. The nibbles of two
 //    keys' words are exchanged first (four logical operations for 16 values), so that
 //    a byte again converts to a register; rows g and g + 8 of an m-tile are two
