@@ -217,9 +217,10 @@ pd_status make_plan(const pd_dims* d, int qlen, int num_splits, int sm_count, Pl
     // the differential decode's join reads two maps' partials: pieces of at least four tiles (B = 1, L
     // = 4096, fp16 / e4m3: 13.9 / 13.6 -> 12.4 / 12.3 us; eight tiles 13.3 / 13.9), of
     // two steps on the tensor-memory engine (qlen = 3, e4m3, L = 1024 / 2048: 16.1 /
-    // 15.5 -> 13.2 / 14.0). The scored decode's (B = 1, L = 4096, 24 x 4 heads, D = 256 11.2 -> 10.1 us,
-    // 8 x 1 heads, D = 128 11.0 -> 8.8; L = 1024 8.8 -> 9.3 and 8.6 -> 8.3)
-    const long long piece = ks.fixed_pieces ? 2 * ks.step_tiles : 4;
+    // 15.5 -> 13.2 / 14.0). The scored decode's too (B = 1, L = 4096, 24 x 4 heads, D = 256 11.2 -> 10.1 us,
+    // 8 x 1 heads, D = 128 11.0 -> 8.8; L = 1024 8.8 -> 9.3 and 8.6 -> 8.3), there of a block of eight
+    // (qlen = 3, e4m3, L = 1024 14.9 -> 12.4, 8 x 1 heads, D = 128, L = 4096 15.8 -> 11.2; two blocks 12.3 and 12.2)
+    const long long piece = !ks.fixed_pieces ? 4 : diff ? 2 * ks.step_tiles : 8;
     const long long most = (vis_keys / kTileKeys + piece - 1) / piece;
     if (op != Op::kPlain && splits > 1) splits = static_cast<int>(std::max<long long>(1, std::min<long long>(splits, most)));
   }
