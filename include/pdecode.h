@@ -277,7 +277,8 @@ PD_API pd_status decode_paged_diff(const void* q, const void* k_cache, const voi
  *                   and all query tokens give it; the keys of the call's own query tokens (the
  *                   last qlen of a sequence) start from zero, so that a new key needs no
  *                   clearing. May be the same buffer; entries of no key of a sequence are left
- *                   alone. Blocks that two sequences share get the sum of one of them. */
+ *                   alone, and everything is by a call without query tokens. Entries of blocks that
+ *                   two sequences share get some of their sums (unspecified which). */
 typedef struct {
   float cap;
   const float* alibi_slopes;
@@ -356,7 +357,8 @@ typedef struct {
  *                    need are appended, sequences in order, table entries in order; the count is
  *                    updated in place
  *   dims             B, Hkv, D (a multiple of 16 up to 512; 4-bit caches: of 64), block_size, num_blocks,
- *                    max_blocks_per_seq and kv_dtype are read; caches and scales 16-byte aligned
+ *                    max_blocks_per_seq and kv_dtype are read (at most 2^31 - 1 slots times Hkv, 2^30 keys a table
+ *                    row); caches and scales 16-byte aligned
  *   workspace        pd_evict_workspace_bytes(dims, evict) bytes
  * A sequence with a bad length (PD_DEVERR_SEQ_LEN) is left alone (0 in a seq_lens_out
  * of its own). Rows whose table entry is outside [0, num_blocks) are not moved

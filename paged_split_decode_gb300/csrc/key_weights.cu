@@ -101,6 +101,8 @@ __global__ void __launch_bounds__(kThreads) key_weights_kernel(const KeyWeightPa
     for (int k = 0; k < kKeys; ++k)
       if (at[k] >= 0) kp.out[at[k]] = old[k] + sum[k];
   }
+  // (CTAs without keys leave at once; one must stay, so that this grid does not end before the decode)
+  if (blockIdx.x == 0 && !ready) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 }  // namespace
