@@ -197,7 +197,7 @@ extern "C" pd_status write_kv_cache_fp4(const void* k_new, const void* v_new, co
               static_cast<long long>(d.num_blocks) * d.block_size, static_cast<int>(groups), d.D / 16, d.Hkv,
               d.block_size, d.k_scale, d.v_scale, k6, v6, 1.f / k6, 1.f / v6,
               !misaligned(k_new, 31) && !misaligned(v_new, 31), moderate(d.k_scale) && moderate(d.v_scale) ? 1 : 0};
-  const long long want = (a.items + kThreads - 1) / kThreads, cap = static_cast<long long>(sms) * 16;
+  const long long want = (a.items + kThreads - 1) / kThreads, cap = static_cast<long long>(sms) * 64;
   const unsigned grid = static_cast<unsigned>(want < cap ? want : cap);
   auto s = static_cast<cudaStream_t>(stream);
   if (d.kv_dtype == PD_KV_FP4_BF16) write_fp4_kernel<true><<<grid, kThreads, 0, s>>>(a);
