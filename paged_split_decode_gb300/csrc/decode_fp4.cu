@@ -26,7 +26,10 @@ struct Shapes {
     out->rows_padded = C::RP;
     out->ctas_per_sm = C::kMinBlocks;
     out->heads = 1;
-    out->unit_cost = 16;
+    // a piece's start and end, in tiles (one row tile, 32 ragged sequences of up to 16384 keys: D = 128 8 heads 16 / 32 /
+    // 48 tiles 74.0 / 60.5 / 65.1 us, D = 256 4 heads 16 / 24 / 40 72.8 / 61.2 / 62.3; 32 x 8192 keys 65.6 / 68.5 / 72.5
+    // and 67.4 / 66.9 / 68.4; two row tiles, D = 256 8 / 16 / 24 122 / 114 / 102)
+    out->unit_cost = D == 128 && C::NT * C::RG == 1 ? 32 : 24;
     out->fixed_pieces = 0;
     for (int& c : out->max_clusters) c = 0;  // split units go through the combine
     return true;

@@ -68,7 +68,9 @@ struct ScoredShapes {
     out->step_tiles = C::KG;
     out->key_groups = C::KG;
     out->whole_tile = 1;
-    out->unit_cost = C::KG > 1 ? 12 : 4;
+    // (key groups, 14 x 2 heads, D = 128, fp16, 128 ragged sequences of up to 1024 keys: 12 / 24 tiles 25.3 / 22.0 us, 32 of
+    // up to 16384 44.7 / 43.5; four heads a tile 4 / 8 51.6 / 49.5 and 143.9 / 144.9, whole 4096 keys 88.4 / 89.1)
+    out->unit_cost = C::KG > 1 ? 24 : 4;
     out->fixed_pieces = 0;
     for (int& c : out->max_clusters) c = 0;  // split units go through the combine
     return true;
