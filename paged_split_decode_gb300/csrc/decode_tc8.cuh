@@ -37,9 +37,10 @@
 //  * At the end of a piece the warps read O^T (one output dim per thread) and
 //    write fp16 rows (unit done in one piece) or the fp32 (m, l, O) partial.
 //  * For the scored decode (SC) the softmax threads cap, bias and mask their
-//    key's scores and leave them for the keys' weights; the weights are split
-//    from fp32 into terms scaled by 1, 2^4 and 2^8, which keeps 12 bits of them and
-//    holds tiny ones to 2^-22 of the largest (many keys beside a dominant one); NaN
+//    key's scores and leave them for the keys' weights; q and the weights are split
+//    from fp32 into terms scaled by 1, 2^4 and 2^8, which keeps q exact far below its
+//    row's largest (unscaled terms leave 1e-6 of a log-sum-exp of few keys), 12 bits of
+//    the weights, and tiny ones to 2^-22 of the largest (many keys beside a dominant one); NaN
 //    codes of V that only some rows see are taken out of the ring and marked.
 //  * Every wait is bounded; after a timeout each role stops waiting and
 //    issuing but keeps the softmax warps' named-barrier sequence, so the CTA
@@ -145,7 +146,7 @@ __device__ __forceinline__ void split3_e4m3(uint32_t x, uint32_t& t1, uint32_t& 
   t3 = half2_to_e4m3x2(*reinterpret_cast<const uint32_t*>(&r2));
 }
 
-// Two floats in [0, 2^8] as three e4m3 code pairs, the second and third scaled by 2^4 and 2^8: their
+// Two floats of at most 2^8 as three e4m3 code pairs, the second and third scaled by 2^4 and 2^8: their
 // sum is off by at most 2^-12 of the value, or 2^-18. (Every difference is exact in fp32.)
 __device__ __forceinline__ uint32_t floats_to_e4m3x2(float lo, float hi) {
   uint16_t d;
@@ -508,8 +509,13 @@ __device__ __forceinline__ void softmax_role(const typename T::Params& p, const 
             uint32_t a[3], b[3];
             const float2 fa = pair_to_float2<T::QB>(w[k]);
             const float2 fb = pair_to_float2<T::QB>(w[k + 1]);
-            split3_e4m3(pack_half2(fa.x * up, fa.y * up), a[0], a[1], a[2]);
-            split3_e4m3(pack_half2(fb.x * up, fb.y * up), b[0], b[1], b[2]);
+            if constexpr (T::SC) {
+              split3_e4m3_up(fa.x * up, fa.y * up, a);
+              split3_e4m3_up(fb.x * up, fb.y * up, b);
+            } else {
+              split3_e4m3(pack_half2(fa.x * up, fa.y * up), a[0], a[1], a[2]);
+              split3_e4m3(pack_half2(fb.x * up, fb.y * up), b[0], b[1], b[2]);
+            }
 #pragma unroll
             for (int t = 0; t < 3; ++t) tw[t][2 * hh + k / 2] = a[t] | (b[t] << 16);
           }
@@ -575,7 +581,8 @@ __device__ __forceinline__ void softmax_role(const typename T::Params& p, const 
         tmem_ld8(sc + 64, z);
         tmem_wait_ld();
 #pragma unroll
-        for (int r = 0; r < NR; ++r) x[r] = (x[r] + y[r]) + z[r];
+        for (int r = 0; r < NR; ++r)
+          x[r] = T::SC ? fmaf(z[r], 1.f / 256.f, fmaf(y[r], 1.f / 16.f, x[r])) : (x[r] + y[r]) + z[r];
       } else {
 #pragma unroll
         for (int r = 0; r < NR; ++r) x[r] = 0.f;

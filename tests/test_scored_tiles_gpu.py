@@ -143,3 +143,23 @@ def test_4bit_writer_past_4gib(pd):
         assert torch.equal(c[-25:].cpu(), want_c) and torch.equal(s[-25:].cpu(), want_s)
     del caches, sfs
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("kv,q", [("fp8", "f16"), ("fp8", "bf16"), ("int8", "bf16"), ("f16", "f16")])
+def test_log_sum_exp_of_few_keys(pd, kv, q):
+    """Products of q with codes are exact, their sums fp32's: a row of one or two keys has its log-sum-exp to D 2^-24 of
+    sum |q k| scale (D = 256, each product at most 2^-24 of the sum so far off), and a few roundings of itself."""
+    w = Work(kv, 24, 4, 256, [1, 2] * 20, qlen=3, q=q, seed=18)
+    lse = w.run(pd)[1].double().cpu()
+    want = w.reference()[2]
+    K = w.value(0)
+    for b, L in enumerate(w.lens.tolist()):
+        for t in range(3 - L, 3):
+            n = t - (3 - L) + 1  # keys that the token sees
+            at = w.table[b, 0].long()
+            for h in range(4):
+                mag = (w.q[b * 3 + t, h * 6:(h + 1) * 6].double().abs() @ K[at, :n, h].abs().T).max(-1).values * w.scale
+                err = (lse[b * 3 + t, h * 6:(h + 1) * 6] - want[b * 3 + t, h * 6:(h + 1) * 6]).abs()
+                assert bool((err <= 256 * 2.0 ** -24 * mag + 2.0 ** -21 * (want[b * 3 + t, h * 6:(h + 1) * 6].abs() + 1)).all())
+    rel = float((lse - want)[torch.isfinite(want)].norm() / want[torch.isfinite(want)].norm())
+    assert rel <= 1e-6  # (and as a whole: random roundings add as a root of their number, 16 2^-24 of a score)
