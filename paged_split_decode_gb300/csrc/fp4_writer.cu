@@ -10,10 +10,10 @@
 // 32 bytes in, 9 out for a group. A thread takes a group of K and the
 // same of V: its values stay in its registers, and the group's maximum needs no
 // exchange between lanes. Each is one 32-byte load (two of 16 where the rows are not
-// aligned to it). Quotients go two to an instruction (32768 tokens, 4 heads, D = 256: 35 to
-// 37 us, 0.70 of the copy rate; one by one 37.6; CTAs of 256 threads 37.4). What is left: the ALU
-// pipe at 57 %, and a token's scales are 16 bytes of a sector in each head, written back
-// with what lies beside them.
+// aligned to it). Quotients go two to an instruction (32768 tokens, 4 heads, D = 256: 35.1 to
+// 36.7 us, 0.7 of the copy rate; one by one 37.6; 16 CTAs an SM instead of 64 36.7; the next
+// group's loads before this one's quotients 37.2). What is left: a token's scales are 16 bytes of a
+// sector in each head, written back with what lies beside them.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
