@@ -21,6 +21,10 @@
 // as well. HBM-bound: 2 x the kept rows' bytes; a lane has four 16-byte pieces in flight.
 //
 // Launch 3, with a free list: the blocks behind the new ends are pushed.
+//
+// A launch's CTAs may be resident while the one before it still writes (programmatic dependent
+// launch), so what another launch may have written (the weights, the table, the lists) is read from L2
+// (__ldcg) behind the wait: the read-only path wants data that no one writes while the grid is resident.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -104,7 +108,7 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const EvictArgs 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int L = __ldg(a.lens + b);
+  const int L = __ldcg(a.lens + b);
   const bool bad = L < 0 || L > a.max_blocks * a.block_size;
   if (h == 0 && rank == 0 && threadIdx.x == 0) {
     a.old_lens[b] = bad ? -1 : L;
@@ -129,8 +133,8 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const EvictArgs 
 #pragma unroll
       for (int k = 0; k < kLoads; ++k) {
         const int i = i0 + k * threads;
-        from[k] = i < n ? __ldg(row + a.bs.div(j[k])) : 0;
-        to[k] = i < n ? __ldg(row_out + a.bs.div(i)) : 0;
+        from[k] = i < n ? __ldcg(row + a.bs.div(j[k])) : 0;
+        to[k] = i < n ? __ldcg(row_out + a.bs.div(i)) : 0;
       }
 #pragma unroll
       for (int k = 0; k < kLoads; ++k) {
@@ -155,9 +159,9 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const EvictArgs 
   const int lo = a.first, hi = L - a.recent;     // the keys that are chosen from
   auto weight = [&](int j, int blk) -> uint32_t {  // (a bad block counts as NaN; a move from it reports it)
     if (blk < 0 || blk >= a.num_blocks) return 0u;
-    return order_of(__ldg(a.weights + (static_cast<long long>(blk) * a.Hkv + h) * a.block_size + a.bs.mod(j)));
+    return order_of(__ldcg(a.weights + (static_cast<long long>(blk) * a.Hkv + h) * a.block_size + a.bs.mod(j)));
   };
-  auto load = [&](int j) -> uint32_t { return weight(j, __ldg(row + a.bs.div(j))); };
+  auto load = [&](int j) -> uint32_t { return weight(j, __ldcg(row + a.bs.div(j))); };
   const int all = hi - lo, share = (all + C - 1) / C;
   const int c0 = min(rank * share, all), n = min(c0 + share, all) - c0;  // this CTA's run: lo + c0 ..
   const int cached = min(n, kCachedKeys);
@@ -167,7 +171,7 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const EvictArgs 
 #pragma unroll
     for (int k = 0; k < kLoads; ++k) {
       const int i = i0 + k * kSelectThreads;
-      blk[k] = i < cached ? __ldg(row + a.bs.div(lo + c0 + i)) : -1;
+      blk[k] = i < cached ? __ldcg(row + a.bs.div(lo + c0 + i)) : -1;
     }
 #pragma unroll
     for (int k = 0; k < kLoads; ++k) u[k] = weight(lo + c0 + i0 + k * kSelectThreads, blk[k]);
@@ -308,7 +312,7 @@ __device__ __forceinline__ void move_rows(const EvictArgs& a, const MoveArray& a
     for (int k = 0; k < kLoads; ++k) {
       const int i = base + k * rows + tr;
       m[k] = make_int2(-1, -1);
-      if (tr < rows && i < j1) m[k] = __ldg(reinterpret_cast<const int2*>(moves + i) + (keys_first ? 0 : 1));
+      if (tr < rows && i < j1) m[k] = __ldcg(reinterpret_cast<const int2*>(moves + i) + (keys_first ? 0 : 1));
     }
   };
   auto at = [&](int row) -> V* {
@@ -398,7 +402,7 @@ __global__ void __launch_bounds__(1024) free_tail_kernel(const EvictArgs a) {
       const int32_t* row = a.table + static_cast<long long>(b0 + i) * a.max_blocks + held;
       for (int k = lane; k < s_n[i]; k += 32) {
         const long long at = s_off[i] + k;
-        int blk = __ldg(row + k);
+        int blk = __ldcg(row + k);
         if (blk < 0 || blk >= a.num_blocks) {
           if (a.error_flag) atomicOr(a.error_flag, PD_DEVERR_BLOCK_ID);
           blk = -1;
