@@ -85,9 +85,9 @@ struct EvictArgs {
   int cluster;                  // CTAs of a (sequence, head) in the select
 };
 
-// The weight as an integer that orders as it does, NaN below all.
+// The weight as an integer that orders as it does, NaN below all; zeros of either sign are equal.
 __device__ __forceinline__ uint32_t order_of(float w) {
-  const uint32_t u = __float_as_uint(w);
+  const uint32_t u = __float_as_uint(w == 0.f ? 0.f : w);
   if (w != w) return 0u;
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
