@@ -510,9 +510,11 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::kMinBlocks) decode_fp4_ker
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            float mx = fmaxf(m_r[n][c], fmaxf(x[n][c], x[n][c + 2]));
+            float mx = fmaxf(x[n][c], x[n][c + 2]);
 #pragma unroll
             for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+            // (each row goes by its own scores: its bits do not depend on the tiles' other rows)
+            mx = mx - m_r[n][c] > 8.f ? mx : m_r[n][c];
             const float al = m_r[n][c] == -INFINITY ? 1.f : ex2(m_r[n][c] - mx);  // (O and l are zero before the first)
             m_r[n][c] = mx;
             l_r[n][c] *= al;

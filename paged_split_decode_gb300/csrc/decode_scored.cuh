@@ -325,7 +325,8 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::kMinBlocks)
           float mx = fmaxf(x[c], x[2 + c]);
 #pragma unroll
           for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-          const float old = m_r[c], mn = fmaxf(old, mx);
+          // (each row goes by its own scores: its bits do not depend on the tile's other rows)
+          const float old = m_r[c], mn = mx - old > kLazy ? mx : old;
           al[c] = old == -INFINITY ? 1.f : ex2(old - mn);  // (nothing accumulated yet: keep factor 1)
           m_r[c] = mn;
           l_r[c] *= al[c];
