@@ -329,16 +329,12 @@ __device__ __forceinline__ bool tc_raise_max(const float (&x)[8], float (&mu)[8]
   return ri[kRowFlag * 32 + g] != 0;
 }
 
-// What the weights of row r are relative to (-inf: none; scored decode: nothing but NaN is not an empty row).
+// What the weights of row r are relative to (-inf: none; a row of nothing but NaN scores is not an empty one,
+// which a merge would leave out).
 template <class T>
 __device__ __forceinline__ float tc_row_base(const float* rf, int r) {
-  const float mu = rf[kRowMu * 32 + r];
-  if (mu != -INFINITY) return mu - T::kBias;
-  if constexpr (T::SC) {
-    const float l = rf[kRowL * 32 + r];
-    if (l != l) return 0.f;
-  }
-  return -INFINITY;
+  const float mu = rf[kRowMu * 32 + r], l = rf[kRowL * 32 + r];
+  return mu != -INFINITY ? mu - T::kBias : l != l ? 0.f : -INFINITY;
 }
 
 // End of a piece for softmax group g: the rows' weight sums (this thread's key
