@@ -493,6 +493,28 @@ __device__ __forceinline__ void softmax_role(const typename T::Params& p, const 
       const int e = mx > 0.f ? max(-126, min(126, 134 - static_cast<int>((__float_as_uint(mx) >> 23) & 255u)))
                              : 0;
       const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+      // e4m3 terms have no infinity. A row with one infinite element has scores of that element's products
+      // alone, infinite or (a zero of K) NaN: the others become zeros, so that the terms' sum is a multiple of
+      // that product, and the row's factor is infinite. Several infinities cancel as a rule: a factor of NaN.
+      const bool inf_row = mx == INFINITY;
+      int infs = 0;
+      if (__any_sync(0xffffffffu, inf_row)) {
+#pragma unroll
+        for (int c = 0; c < NCH; ++c)
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh) {
+            uint32_t v[4] = {qv[c][hh].x, qv[c][hh].y, qv[c][hh].z, qv[c][hh].w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float2 f = pair_to_float2<T::QB>(v[k]);
+              infs += (fabsf(f.x) == INFINITY) + (fabsf(f.y) == INFINITY);
+              if (inf_row) v[k] &= (fabsf(f.x) < INFINITY ? 0u : 0xffffu) | (fabsf(f.y) < INFINITY ? 0u : 0xffff0000u);
+            }
+            qv[c][hh] = make_uint4(v[0], v[1], v[2], v[3]);
+          }
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) infs += __shfl_xor_sync(0xffffffffu, infs, o);
+      }
 #pragma unroll
       for (int c = 0; c < NCH; ++c) {
         const int d0 = part * (D / 8) + 16 * c;
@@ -529,7 +551,9 @@ __device__ __forceinline__ void softmax_role(const typename T::Params& p, const 
           hi = pq.L - pq.qlen + r / p.G;
           lo = p.window > 0 ? max(0, hi - p.window + 1) : 0;
         }
-        rf[kRowFsl * 32 + r] = r < pq.R ? p.sl2 * __uint_as_float(static_cast<uint32_t>(127 - e) << 23) : 0.f;
+        const float down = !inf_row ? __uint_as_float(static_cast<uint32_t>(127 - e) << 23)
+                                    : infs == 1 ? INFINITY : __uint_as_float(0x7fffffffu);
+        rf[kRowFsl * 32 + r] = r < pq.R ? p.sl2 * down : 0.f;
         rf[kRowMu * 32 + r] = -INFINITY;
         ri[kRowLo * 32 + r] = lo;
         ri[kRowHi * 32 + r] = hi;
