@@ -94,6 +94,7 @@ struct ScoredParams : DecodeParams {
   float cap_out;              // cap * log2(e); 0: no cap
   const float* slopes;        // [Hq] or null
   const int32_t* prefix_lens; // [B] or null
+  int least_tiles;            // tiles of a fixed split's piece at least (but the unit's last)
   float* lse;                 // [total_q, Hq] or null
   float2* row_ml;             // [B, qlen, Hq] (m in log2 units, l) or null: for the keys' weights
   float* scores;              // [B, Hkv, tiles of a table row, row tiles, 16 keys, 8 rows] in log2 units, or null
@@ -461,6 +462,14 @@ __device__ __forceinline__ void balanced_prefix(const Par& p, int* s_pre, int la
   }
 }
 
+// Fixed split: tiles of a piece of a unit of n tiles.
+template <class Par>
+__device__ __forceinline__ int fixed_chunk(const Par& p, int n, int S) {
+  const int chunk = (n + S - 1) / S;
+  if constexpr (Par::kScored) return max(chunk, p.least_tiles);
+  else return chunk;
+}
+
 struct WorkIter {
   ChunkPlan cp;
   long long g, g_end, chunk_start;
@@ -561,7 +570,7 @@ __device__ __forceinline__ bool work_next(const Par& p, const int* s_pre, WorkIt
     int L, t0, n, q0, qn;
     seq_span(p, b, s == 0 && kh == 0, L, t0, n, q0, qn);
     pc.qlen = qn; pc.R = p.G * qn; pc.q0 = q0;
-    const int chunk = (n + S - 1) / S;
+    const int chunk = fixed_chunk(p, n, S);
     const int c0 = s * chunk;
     const int c1 = (c0 + chunk < n) ? c0 + chunk : n;
     if (n == 0) {
@@ -1365,7 +1374,7 @@ __device__ __forceinline__ void unit_layout(const Par& p, int u, long long (&s_r
   seq_span(p, b, false, L, t0, n, q0, qn);
   if (p.num_splits > 0) {
     const int S = p.num_splits;
-    const int chunk = (n + S - 1) / S;
+    const int chunk = fixed_chunk(p, n, S);
     P = n > 0 ? (n + chunk - 1) / chunk : 0;
     slot0 = slot_base = static_cast<long long>(u) * S;
     step = 1;

@@ -752,7 +752,7 @@ __device__ __forceinline__ void cluster_merge(const typename T::Params& p, uint3
   int L, t0, n, q0, qn;
   seq_span(p, b, false, L, t0, n, q0, qn);
   if (n == 0) return;
-  const int chunk = (n + S - 1) / S;
+  const int chunk = fixed_chunk(p, n, S);
   if ((n + chunk - 1) / chunk <= 1) return;
   const int R = p.G * qn;
   uint32_t peer[SMAX];  // each peer's shared memory base in the cluster window

@@ -84,6 +84,7 @@ struct Plan {
   int cluster;      // > 1: the fixed split's pieces of a unit form a cluster that merges them
   int sms;          // SMs of the device the plan was made for
   int head_tiles;   // row tiles of a head in a partial
+  int least;        // scored decode: tiles of a fixed split's piece at least
   size_t off_ml, off_o, bytes;  // workspace layout
 };
 
@@ -151,9 +152,15 @@ int device_sm_count(int sm_count) {
 // within ~2 % or the fixed one loses (B=16: +1.0 us, 2 x 2048 tiles: +0.5). The
 // workspace is sized for the balanced split in either case (the fixed split
 // needs fewer slots), so pd_workspace_bytes does not depend on the window.
-// The differential decode's kernels hold two maps' rows.
+// The differential decode's kernels hold two maps' rows. How many keys `prefixes` add to a
+// window is known on the device alone: few units are then split into as many pieces as
+// the table's capacity could need, and the device makes pieces of Plan::least tiles or more of
+// the keys that there are. (24 x 4 heads, D = 256, B = 1, L = 8192; planned by the window alone -> so:
+// window 16, prefix 8000, fp16 / 4-bit / e4m3 with qlen = 3 343 / 91 / 84 -> 12.4 / 11.6 / 15.4 us; window
+// 256, prefix 4, a table of 131072 keys 11.3 / 8.4 / 12.0 -> 11.7 / 9.1 / 13.5; window 4096, prefix 128,
+// 4-bit, B = 4 13.9 both ways.)
 pd_status make_plan(const pd_dims* d, int qlen, int num_splits, int sm_count, Plan* pl, int window = 0,
-                    Op op = Op::kPlain) {
+                    Op op = Op::kPlain, bool prefixes = false) {
   const bool diff = op == Op::kDiff;
   pd_status st = check_dims(d, qlen, op);
   if (st != PD_OK) return st;
@@ -182,7 +189,7 @@ pd_status make_plan(const pd_dims* d, int qlen, int num_splits, int sm_count, Pl
   const int ctas = sms * ks.ctas_per_sm;  // persistent grid: every resident CTA slot
   const bool automatic = splits == 0;
   const long long cap_keys = static_cast<long long>(d->max_blocks_per_seq) * d->block_size;
-  const long long vis_keys = window > 0 ? std::min<long long>(cap_keys, 0ll + window + qlen + kTileKeys) : cap_keys;
+  const long long vis_keys = window > 0 && !prefixes ? std::min<long long>(cap_keys, 0ll + window + qlen + kTileKeys) : cap_keys;
   // Short tables: whole units, one per CTA, walk (waves - units / ctas) * tiles more
   // than the balanced split does, but launch no join and end no pieces inside a
   // unit, which costs four steps of the CTA and up to twice that where every CTA
@@ -210,9 +217,10 @@ pd_status make_plan(const pd_dims* d, int qlen, int num_splits, int sm_count, Pl
         splits = 1;
     }
   }
+  pl->least = 1;
   if (splits == 0 && pl->units > 0 && pl->units <= ctas / 4) {
     const long long tiles = pl->units * (vis_keys / kTileKeys + 1);
-    if (tiles <= 24ll * ctas || ks.fixed_pieces)
+    if (tiles <= 24ll * ctas || ks.fixed_pieces || prefixes)
       splits = static_cast<int>(std::max<long long>(1, (ctas * 27 / 32) / pl->units));
     // the differential decode's join reads two maps' partials: pieces of at least four tiles (B = 1, L
     // = 4096, fp16 / e4m3: 13.9 / 13.6 -> 12.4 / 12.3 us; eight tiles 13.3 / 13.9), of
@@ -223,6 +231,7 @@ pd_status make_plan(const pd_dims* d, int qlen, int num_splits, int sm_count, Pl
     const long long piece = !ks.fixed_pieces ? 4 : diff ? 2 * ks.step_tiles : 8;
     const long long most = (vis_keys / kTileKeys + piece - 1) / piece;
     if (op != Op::kPlain && splits > 1) splits = static_cast<int>(std::max<long long>(1, std::min<long long>(splits, most)));
+    if (prefixes) pl->least = static_cast<int>(piece);
   }
   pl->splits = splits;
   if (splits == 0) {
@@ -383,14 +392,14 @@ namespace {
 
 // What every decode call checks and fills in: the plan, the caches' maps and
 // the kernel's parameters. `ready` is
-// false when there is nothing to launch. q_start null means B sequences of qlen
+// false when there is nothing to launch. prefixes: keys beside the window's may be visible. q_start null means B sequences of qlen
 // query tokens each (total_q = B * qlen); otherwise sequence b owns rows
 // [q_start[b], q_start[b+1]) of q and out, at most qlen of them.
 pd_status prepare_decode(const void* q, const void* k_cache, const void* v_cache,
                          const int32_t* block_table, const int32_t* seq_lens, const int32_t* q_start,
                          int total_q, float scale, int window, int qlen, int num_splits, void* out,
                          const pd_dims* dims, void* workspace, size_t workspace_bytes,
-                         uint32_t* error_flag, Op op, Plan& pl, CUtensorMap& tk, CUtensorMap& tv,
+                         uint32_t* error_flag, Op op, bool prefixes, Plan& pl, CUtensorMap& tk, CUtensorMap& tv,
                          DecodeParams& p, bool& ready) {
   ready = false;
   pd_status st = check_dims(dims, qlen, op);
@@ -405,7 +414,7 @@ pd_status prepare_decode(const void* q, const void* k_cache, const void* v_cache
       (reinterpret_cast<uintptr_t>(q_start) & 3u) || (reinterpret_cast<uintptr_t>(error_flag) & 3u))
     return PD_ERR_ALIGN;
   if (dims->num_blocks == 0) return PD_ERR_SHAPE;
-  st = make_plan(dims, qlen, num_splits, 0, &pl, window, op);
+  st = make_plan(dims, qlen, num_splits, 0, &pl, window, op, prefixes);
   if (st != PD_OK) return st;
   if (pl.bytes > 0) {
     if (!workspace || workspace_bytes < pl.bytes) return PD_ERR_WORKSPACE;
@@ -522,8 +531,8 @@ pd_status decode_impl(const void* q, const void* k_cache, const void* v_cache,
   DecodeParams p;
   bool ready;
   const pd_status st = prepare_decode(q, k_cache, v_cache, block_table, seq_lens, q_start, total_q, scale, window, qlen,
-                                      num_splits, out, dims, workspace, workspace_bytes, error_flag, Op::kPlain, pl,
-                                      tk, tv, p, ready);
+                                      num_splits, out, dims, workspace, workspace_bytes, error_flag, Op::kPlain,
+                                      false, pl, tk, tv, p, ready);
   if (st != PD_OK || !ready) return st;
   const WorkspaceLock lock(workspace, pl.n_merge > 0);
   cudaError_t e = launch_decode(dims->D, dims->kv_dtype, pl.nt, pl.hg > 1 ? 1 : 0, tk, tv, p, pl.grid,
@@ -591,7 +600,7 @@ pd_status decode_paged_diff(const void* q, const void* k_cache, const void* v_ca
   bool ready;
   const pd_status st = prepare_decode(q, k_cache, v_cache, block_table, seq_lens, query_start_loc,
                                       static_cast<int>(total), scale, window, qlen, num_splits, out, dims, workspace,
-                                      workspace_bytes, error_flag, Op::kDiff, pl, tk, tv, p.d, ready);
+                                      workspace_bytes, error_flag, Op::kDiff, false, pl, tk, tv, p.d, ready);
   if (st != PD_OK || !ready) return st;
   p.v_cache = v_cache;
   p.lambda = lambda;
@@ -649,7 +658,8 @@ pd_status decode_paged_scored(const void* q, const void* k_cache, const void* v_
   bool ready;
   const pd_status st = prepare_decode(q, k_cache, v_cache, block_table, seq_lens, query_start_loc,
                                       static_cast<int>(total), scale, window, qlen, num_splits, out, dims, workspace,
-                                      workspace_bytes, error_flag, Op::kScored, pl, tk, tv, p, ready);
+                                      workspace_bytes, error_flag, Op::kScored, sc.prefix_lens != nullptr, pl, tk, tv, p,
+                                      ready);
   if (st != PD_OK || !ready) return st;
   if (fp4 && (!sc.k_block_scale || !sc.v_block_scale)) return PD_ERR_NULL;
   if (weights && !sc.key_weights) return PD_ERR_NULL;
@@ -657,6 +667,7 @@ pd_status decode_paged_scored(const void* q, const void* k_cache, const void* v_
   p.cap_out = sc.cap > 0.f ? static_cast<float>(sc.cap * 1.4426950408889634) : 0.f;
   p.slopes = sc.alibi_slopes;
   p.prefix_lens = sc.prefix_lens;
+  p.least_tiles = pl.least;
   p.lse = sc.lse;
   p.row_ml = nullptr;
   p.scores = nullptr;
