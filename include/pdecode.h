@@ -276,7 +276,9 @@ PD_API pd_status decode_paged_diff(const void* q, const void* k_cache, const voi
  *   key_weights_out sequences, out = in + the softmax weights that its KV head's query heads
  *                   and all query tokens give it; the keys of the call's own query tokens (the
  *                   last qlen of a sequence) start from zero, so that a new key needs no
- *                   clearing. May be the same buffer; entries of no key of a sequence are left
+ *                   clearing. Keys that come in otherwise (a prompt through the writer alone) start
+ *                   from what their slots hold, in blocks of a free list the sums of
+ *                   their last owner: set those to zero first. May be the same buffer; entries of no key of a sequence are left
  *                   alone, and everything is by a call without query tokens. Entries of blocks that
  *                   two sequences share get some of their sums (unspecified which). */
 typedef struct {
@@ -300,8 +302,11 @@ typedef struct {
  * The layouts, the writer (write_kv_cache, write_kv_cache_fp4), block_table, seq_lens,
  * splits and errors are decode_paged's; query_start_loc, num_query_tokens and qlen as
  * in decode_paged_diff. workspace: pd_scored_workspace_bytes(dims, qlen, num_splits,
- * key_weights_out != NULL, 0) bytes.
- * A row without a visible key is zeros. NaN scores, and NaN and infinities of V, show in the
+ * key_weights_out != NULL, 0) bytes; with key weights they hold 32 bytes for each key that the
+ * tables have room for, KV head and eight of its rows (64 sequences, 8 KV heads of at most eight
+ * rows, 131072 keys a table row: 2.1 GB).
+ * A row without a visible key is zeros, and so is one whose visible scores are all -infinity; the
+ * log-sum-exp is -inf. NaN scores, and NaN and infinities of V, show in the
  * rows that see the key, as NaN or infinity, and in no other. Softmax weights are computed
  * in fp32 and enter the product with V as two 16-bit operands, as three e4m3 ones (e4m3
  * caches, more than 8 rows per KV head: 12 bits, and none below 2^-22 of a row's largest), or rounded once to fp16 where a bfloat16
@@ -318,7 +323,8 @@ PD_API pd_status decode_paged_scored(const void* q, const void* k_cache, const v
 /* write_kv_cache for 4-bit caches: for every 16 dims of a new row,
  *   s = e4m3fn(max|x| / (6 * k_scale)) to the nearest, ties to even, at most 448
  *   code = e2m1(x / (s * k_scale)) to the nearest, ties to even, at most 6 in magnitude
- * with the quotients and s * k_scale rounded to fp32 (V: v_scale). Where s is zero the codes
+ * with 6 * k_scale, the quotients and s * k_scale rounded to fp32 (V: v_scale; above
+ * 5.6e37 the first is infinite, and all is zero). Where s is zero the codes
  * are zeros, with x's signs; a group with a NaN gets the scale NaN (0x7F) and zero codes.
  *   k_new, v_new    [num_tokens, Hkv, D], fp16 (PD_KV_FP4) or bfloat16 (PD_KV_FP4_BF16), 16-byte aligned
  *   slot_mapping    as in write_kv_cache
@@ -344,6 +350,9 @@ typedef struct {
  * (decode_paged_scored's key_weights): each KV head of a sequence keeps the keys of
  * pd_eviction and moves their K and V rows (for 4-bit caches the scales too) and weights to the
  * sequence's first `keep` slots, in their order. A NaN weight counts as less than any number.
+ * From then on a key's place is its rank among the keys that its head kept, so that heads differ:
+ * windows, prefixes, distance biases and build_block_tables' positions of later calls count ranks,
+ * not the tokens' original positions (K rows keep what they were rotated by).
  *   key_weights      fp32 [num_blocks, Hkv, block_size], moved along
  *   block_table      int32 [B, max_blocks_per_seq]
  *   seq_lens         int32 [B]; seq_lens_out [B] gets the new lengths (may be seq_lens itself)
@@ -363,8 +372,8 @@ typedef struct {
  * A sequence with a bad length (PD_DEVERR_SEQ_LEN) is left alone (0 in a seq_lens_out
  * of its own). Rows whose table entry is outside [0, num_blocks) are not moved
  * (PD_DEVERR_BLOCK_ID); such an entry is appended as -1. Blocks that would make the free
- * list longer than num_blocks are not appended (PD_DEVERR_FREE_LIST). Blocks must not be shared
- * between sequences that are cut in place. Two launches on `stream`, three with a free list. */
+ * list longer than num_blocks are not appended (PD_DEVERR_FREE_LIST). A block of a
+ * sequence that is cut in place must not belong to any other sequence, cut or not. Two launches on `stream`, three with a free list. */
 PD_API size_t pd_evict_workspace_bytes(const pd_dims* dims, const pd_eviction* evict);
 PD_API pd_status evict_kv_cache(void* k_cache, void* v_cache, void* k_block_scale, void* v_block_scale,
                                 float* key_weights, const int32_t* block_table, const int32_t* seq_lens,

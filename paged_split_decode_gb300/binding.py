@@ -530,7 +530,10 @@ def decode_paged_scored(q, k_cache, v_cache, block_table, seq_lens, scale, windo
 
     ``lse`` (float32 [T, Hq]) gets the natural log-sum-exp of each row. ``key_weights`` (float32 [num_blocks, Hkv,
     block_size]) collects the softmax weight that each key is given, in place unless ``key_weights_out`` is given; the
-    step's own keys, the last of each sequence, start from zero. ``evict_kv_cache`` goes by it.
+    step's own keys, the last of each sequence, start from zero. Keys that a writer alone brought (a prompt) start from
+    what their slots hold: set them to zero first. ``evict_kv_cache`` goes by it. With key weights the workspace takes
+    32 bytes for each key that ``block_table`` has room for, KV head and eight of its rows; a call without ``workspace``
+    keeps one for each stream, a captured call one of its own.
     """
     return (_bind or _fast()).decode_paged_scored(q, k_cache, v_cache, block_table, seq_lens, scale, window, qlen,
                                                   num_splits, out, query_start_loc, score_cap, alibi_slopes, prefix_lens,
@@ -555,10 +558,11 @@ def evict_kv_cache(k_cache, v_cache, key_weights, block_table, seq_lens, keep, *
     """Cut sequences of more than ``trigger`` (default: ``keep``) keys down to ``keep`` for each KV head: the first
     ``first``, the last ``recent``, and the heaviest of the rest by ``key_weights`` (float32 [num_blocks, Hkv,
     block_size]; on a tie the lower index). Their K and V rows, block scales and weights move to the sequence's first
-    slots, in order; with ``block_table_out`` (int32 [B, columns]) they are copied to those blocks instead, as are
+    slots, in order, and count by their rank there in later calls (windows, prefixes, distances, positions), which may
+    differ from head to head; with ``block_table_out`` (int32 [B, columns]) they are copied to those blocks instead, as are
     all keys of the other sequences. ``seq_lens`` is updated in place unless ``seq_lens_out`` is given; returns the
     lengths. ``free_blocks``/``free_count`` (as in ``build_block_tables``): the blocks that sequences cut in place no
-    longer need are pushed."""
+    longer need are pushed. A block of a sequence that is cut in place must not belong to another sequence."""
     return (_bind or _fast()).evict_kv_cache(k_cache, v_cache, key_weights, block_table, seq_lens, keep, trigger, first,
                                              recent, block_table_out, seq_lens_out, k_block_scale, v_block_scale,
                                              free_blocks, free_count, workspace, error_flag, stream)
