@@ -41,7 +41,6 @@ namespace pd {
 
 struct Fp4Params : ScoredParams {
   const uint8_t *k_codes, *v_codes, *k_sf, *v_sf;
-  int q_bf16;  // q and out are bfloat16: q rows are scaled into fp16 (exactly)
 };
 
 // NT: row tiles of 8 query rows that a warp computes, RG: row groups of that many
