@@ -13,7 +13,7 @@
 // from shared memory. Bound by the latency of two dependent loads: the table and the old
 // sums are read before the decode's end is waited for, and a CTA has 256 keys only, so
 // that long sequences of a ragged batch spread over the SMs (32 sequences of up to 16384
-// keys, four heads of seven rows, 4-bit: the call takes 100.1 us with CTAs of 128 threads
+// keys, eight heads of four rows, 4-bit: the call takes 100.1 us with CTAs of 128 threads
 // and two keys a thread, 113.0 with four, 119.6 with eight; 115.6 with one key of 256
 // threads and every load behind the wait; without this launch 86.8).
 #include <algorithm>
