@@ -153,11 +153,11 @@ int device_sm_count(int sm_count) {
 // workspace is sized for the balanced split in either case (the fixed split
 // needs fewer slots), so pd_workspace_bytes does not depend on the window.
 // The differential decode's kernels hold two maps' rows. How many keys `prefixes` add to a
-// window is known on the device alone: few units are then split into as many pieces as
+// window is known on the device alone: a fixed split then has as many pieces as
 // the table's capacity could need, and the device makes pieces of Plan::least tiles or more of
 // the keys that there are. (24 x 4 heads, D = 256, B = 1, L = 8192; planned by the window alone -> so:
 // window 16, prefix 8000, fp16 / 4-bit / e4m3 with qlen = 3 343 / 91 / 84 -> 12.4 / 11.6 / 15.4 us; window
-// 256, prefix 4, a table of 131072 keys 11.3 / 8.4 / 12.0 -> 11.7 / 9.1 / 13.5; window 4096, prefix 128,
+// 256, prefix 4, a table of 131072 keys 11.1 / 8.3 / 12.1 -> 11.7 / 9.0 / 13.5; window 4096, prefix 128,
 // 4-bit, B = 4 13.9 both ways.)
 pd_status make_plan(const pd_dims* d, int qlen, int num_splits, int sm_count, Plan* pl, int window = 0,
                     Op op = Op::kPlain, bool prefixes = false) {
@@ -189,7 +189,7 @@ pd_status make_plan(const pd_dims* d, int qlen, int num_splits, int sm_count, Pl
   const int ctas = sms * ks.ctas_per_sm;  // persistent grid: every resident CTA slot
   const bool automatic = splits == 0;
   const long long cap_keys = static_cast<long long>(d->max_blocks_per_seq) * d->block_size;
-  const long long vis_keys = window > 0 && !prefixes ? std::min<long long>(cap_keys, 0ll + window + qlen + kTileKeys) : cap_keys;
+  const long long vis_keys = window > 0 ? std::min<long long>(cap_keys, 0ll + window + qlen + kTileKeys) : cap_keys;
   // Short tables: whole units, one per CTA, walk (waves - units / ctas) * tiles more
   // than the balanced split does, but launch no join and end no pieces inside a
   // unit, which costs four steps of the CTA and up to twice that where every CTA
@@ -220,7 +220,7 @@ pd_status make_plan(const pd_dims* d, int qlen, int num_splits, int sm_count, Pl
   pl->least = 1;
   if (splits == 0 && pl->units > 0 && pl->units <= ctas / 4) {
     const long long tiles = pl->units * (vis_keys / kTileKeys + 1);
-    if (tiles <= 24ll * ctas || ks.fixed_pieces || prefixes)
+    if (tiles <= 24ll * ctas || ks.fixed_pieces)
       splits = static_cast<int>(std::max<long long>(1, (ctas * 27 / 32) / pl->units));
     // the differential decode's join reads two maps' partials: pieces of at least four tiles (B = 1, L
     // = 4096, fp16 / e4m3: 13.9 / 13.6 -> 12.4 / 12.3 us; eight tiles 13.3 / 13.9), of
@@ -229,9 +229,9 @@ pd_status make_plan(const pd_dims* d, int qlen, int num_splits, int sm_count, Pl
     // 8 x 1 heads, D = 128 11.0 -> 8.8; L = 1024 8.8 -> 9.3 and 8.6 -> 8.3), there of a block of eight
     // (qlen = 3, e4m3, L = 1024 14.9 -> 12.4, 8 x 1 heads, D = 128, L = 4096 15.8 -> 11.2; two blocks 12.3 and 12.2)
     const long long piece = !ks.fixed_pieces ? 4 : diff ? 2 * ks.step_tiles : 8;
-    const long long most = (vis_keys / kTileKeys + piece - 1) / piece;
+    const long long most = ((prefixes ? cap_keys : vis_keys) / kTileKeys + piece - 1) / piece;
     if (op != Op::kPlain && splits > 1) splits = static_cast<int>(std::max<long long>(1, std::min<long long>(splits, most)));
-    if (prefixes) pl->least = static_cast<int>(piece);
+    if (prefixes && vis_keys < cap_keys) pl->least = static_cast<int>(piece);
   }
   pl->splits = splits;
   if (splits == 0) {
